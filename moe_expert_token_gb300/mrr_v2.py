@@ -139,6 +139,21 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.mrr_v2_run_noalloc.restype = I32
     lib.mrr_v2_run_noalloc.argtypes = [P, I32, I64, I64, P, I32, I64, I64, P, I32, I64, P,
                                        P, P, P, P, P, I64, I64, I32, P]
+    lib.moe_mx_quantize_run.restype = I32
+    lib.moe_mx_quantize_run.argtypes = [P, I32, I64, I64, I64, P, P, P]
+    lib.moe_mx_dequantize_run.restype = I32
+    lib.moe_mx_dequantize_run.argtypes = [P, P, I64, I64, I32, P, I64, P]
+    lib.moe_mx_grouped_workspace.restype = ctypes.c_size_t
+    lib.moe_mx_grouped_workspace.argtypes = [I64]
+    lib.moe_mx_grouped_run.restype = I32
+    lib.moe_mx_grouped_run.argtypes = [P, P, I64, I64, P, I32, I64, I64, P, P, I64, I32, P, P, I32, P, P,
+                                       ctypes.c_size_t, P]
+    lib.moe_few_token_layer_workspace.restype = ctypes.c_size_t
+    lib.moe_few_token_layer_workspace.argtypes = [I64, I64, I64, I64, I64]
+    lib.moe_few_token_layer_run.restype = I32
+    lib.moe_few_token_layer_run.argtypes = [P, I32, I64, I64, P, I64, P, P, P, P, P, I32, I64, I64, I64, I64,
+                                            ctypes.c_float, ctypes.c_float, I64, I64, P, P, P, P,
+                                            ctypes.c_size_t, P]
     if path == _build.LIB_PATH:
         _lib = lib
     return lib
