@@ -1,0 +1,11 @@
+// Instances of the layer's kernel for x in bf16 (they compile beside the other type's).
+#include "moe_layer_kernel.cuh"
+
+namespace moe_layer {
+
+cudaError_t launch_bf16(const Params &p, bool mx, int grid, size_t smem, cudaStream_t s)
+{
+    return launch_dt<MOE_BF16>(p, mx, grid, smem, s);
+}
+
+}  // namespace moe_layer
