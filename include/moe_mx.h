@@ -71,8 +71,9 @@ size_t moe_mx_grouped_workspace(int64_t E);
  *                   MRR_ERR_COUNT_SUM (the counts do not sum to A), MRR_ERR_TIMEOUT; the outputs
  *                   are then unspecified
  * Host errors: MRR_ERR_DTYPE, MRR_ERR_ATTR (expert_num_type, gated not 0 or 1), MRR_ERR_SHAPE (A
- * < 0 or above INT32_MAX, E outside 1 .. 4096, K < 32 or not a multiple of 32 or above 2^20, N
- * outside 1 .. 2^20, an MXFP4 out with N not a multiple of 32), MRR_ERR_NULL, MRR_ERR_ALIGN (codes
+ * < 0 or above 2^31 - 257, E outside 1 .. 4096, K < 32 or not a multiple of 32 or above 2^20, N
+ * outside 1 .. 2^20, more than 2^31 - 513 weight rows in all, an MXFP4 out with N not a multiple of
+ * 32), MRR_ERR_NULL, MRR_ERR_ALIGN (codes
  * or w_codes not 16-byte aligned, scales or w_scales not 2-byte aligned, another pointer not
  * aligned to its type), MRR_ERR_WORKSPACE, MRR_ERR_CUDA.
  */

@@ -1,146 +1,528 @@
-// The experts' product on expert-major MXFP4 rows (include/moe_mx.h).
+// The experts' product on expert-major MXFP4 rows (include/moe_mx.h), for GB300 (sm_103a).
 //
 // y[r, n] = sum_k x[r, k] w[e(r), n, k]; gated: silu(y_gate) * y_up; times row_weight.
+//
+// Both operands stay in 4 bits up to the tensor cores: tcgen05.mma kind::mxf4 multiplies e2m1 codes
+// and applies the e8m0 scales of 32-element blocks itself, with float32 sums in tensor memory.
+//
+//  * Weights are the 128-row operand and token rows the columns, so an expert with few rows pads
+//    16 columns and not 128 rows, and a lane of the result holds one output feature: 32 lanes are
+//    one 32-block of an MXFP4 result, and a gate and its up value meet in the same lane.
+//  * A tile is two 128-row weight tiles (gated: the gate rows and their up rows; else neighbours)
+//    by up to 192 token rows of one expert, K in steps of 256 (128 bytes a row).  An expert's rows
+//    are split evenly over its tiles, in multiples of 16.
+//  * One persistent block an SM.  Warp 0 issues the tiled bulk copies of codes, warp 1 the matrix
+//    instructions, warps 12-15 bring the scales (8 bytes a row and step, which the tensor cores
+//    want in an order of their own), warps 4-11 turn finished sums into results while the next
+//    tile's stages are being filled.
+//  * Neighbouring blocks work on the token tiles of the same weights, which so come from HBM once.
+//
+// Every wait is bounded: one that lasts two seconds sets a flag, all roles leave, copies in flight
+// are waited for, tensor memory is freed, and mrr_v2_read_status reports MRR_ERR_TIMEOUT.
+#include <cuda.h>
+
 #include "mx.cuh"
+#include "tc.cuh"
 #include "ws_layout.h"
 
 using namespace moe_mx;
 
 namespace {
 
-constexpr int kTile = 64, kStep = 32, kThreads = 256;
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kThreads = 512;
+constexpr int kEpilogueWarp = 4, kEpilogueWarps = 8, kScaleWarp = 12;
+constexpr int kRowTile = 128;            // weight rows of one matrix instruction
+constexpr int kStepBytes = 128;          // bytes of a row in a stage: 256 elements
+constexpr int kBoxRows = 32;             // token rows of one copy
+constexpr int kMaxStages = 8;
+constexpr int kColumns = 512;            // all of tensor memory
+constexpr int kMaxExperts = 4096;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct Params {
-    const uint8_t *codes, *scales;
-    int64_t A, K;
+    const uint8_t *scales, *w_scales;
+    int A, K, E, N, counts_i64, counts_prefix, gated, out_dt;
     const void *counts;
-    int counts_i64, counts_prefix, E;
-    const uint8_t *w_codes, *w_scales;
-    int64_t N;
     const float *row_weight;
     void *out;
-    int out_dt;
     uint8_t *out_scales;
     uint32_t *status;
+    int tokens;        // most token rows of a tile (64 or 192)
+    int stages, sums;  // ring stages; sets of sums in tensor memory (1 or 2)
+    int wide, w_wide;  // scale rows are 8-byte aligned
+    int sm_stage, sm_tables;
 };
 
-__device__ __forceinline__ int64_t count_at(const Params &p, int e)
+struct Tile {
+    int expert, feature, row, rows, columns;   // columns: rows rounded up to 16
+};
+
+__host__ __device__ constexpr int groups_of(int tokens) { return (tokens + 127) / 128; }
+__host__ __device__ constexpr int stage_bytes(int tokens)
 {
-    return p.counts_i64 ? __ldg(static_cast<const long long *>(p.counts) + e)
-                        : (int64_t)__ldg(static_cast<const int *>(p.counts) + e);
+    return 2 * kRowTile * kStepBytes + tokens * kStepBytes + 2048 + 1024 * groups_of(tokens);
 }
 
-// one tile of 64 rows of one expert by 64 outputs, 4 x 4 of them a thread, from decoded 32-blocks
-template <bool kGated>
-__global__ void __launch_bounds__(kThreads) grouped_simple(Params p)
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages], sums_full[2], sums_empty[2], drained;
+    long long scan_rows[kThreads / 32];
+    int scan_tiles[kThreads / 32];
+    uint32_t tmem;
+    int abort, bad;
+};
+
+__device__ __forceinline__ bool wait(Shared *sh, uint64_t *bar, uint32_t parity)
 {
-    constexpr int kMats = kGated ? 2 : 1;
-    __shared__ float sx[kTile][kStep + 1], sw[kMats][kTile][kStep + 1], sy[kTile][kTile + 1];
-    __shared__ int64_t s_row0, s_end;
-    __shared__ int s_expert;
-    if (threadIdx.x == 0) {
-        int64_t at = 0, tile = blockIdx.x;
-        int bad = 0;
-        s_expert = -1;
-        for (int e = 0; e < p.E; ++e) {
-            const int64_t c = p.counts_prefix ? count_at(p, e) - at : count_at(p, e);
-            if (c < 0 || c > p.A - at) {
-                bad = c < 0 ? mrr_ws::kFlagNonPos : mrr_ws::kFlagSum;
-                break;
+    if (mrr::mbar_try_wait(mrr::smem_addr(bar), parity))
+        return true;
+    const uint64_t t0 = mrr::global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mrr::mbar_try_wait(mrr::smem_addr(bar), parity))
+            return true;
+        if (it % 64 == 0) {
+            if (*reinterpret_cast<volatile int *>(&sh->abort))
+                return false;
+            if (mrr::global_timer_ns() - t0 > kWaitLimitNs) {
+                *reinterpret_cast<volatile int *>(&sh->abort) = 1;
+                return false;
             }
-            const int64_t tiles = (c + kTile - 1) / kTile;
-            if (s_expert < 0 && tile < tiles) {
-                s_expert = e;
-                s_row0 = at + tile * kTile;
-                s_end = at + c;
-            }
-            tile -= tiles;
-            at += c;
-        }
-        if (!bad && at != p.A)
-            bad = mrr_ws::kFlagSum;
-        if (bad)
-            s_expert = -1;
-        if (blockIdx.x == 0 && blockIdx.y == 0) {
-            p.status[0] = bad;
-            p.status[1] = 0;
         }
     }
+}
+
+// Row and tile prefixes of the experts, into tables[0 .. E] and tables[E + 1 .. 2 E + 1]; flags of bad
+// counts.  Every thread sums a run of experts, then the runs are scanned over the block.
+__device__ int scan_counts(const Params &p, Shared *sh, int *tables)
+{
+    const int per = (p.E + kThreads - 1) / kThreads, lo = min(p.E, (int)threadIdx.x * per), hi = min(p.E, lo + per);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    auto at = [&](int e) {
+        return p.counts_i64 ? (long long)__ldg(static_cast<const long long *>(p.counts) + e)
+                            : (long long)__ldg(static_cast<const int *>(p.counts) + e);
+    };
+    if (threadIdx.x == 0)
+        sh->bad = 0;
     __syncthreads();
-    if (s_expert < 0)
-        return;
-    const int64_t row0 = s_row0, end = s_end, n0 = (int64_t)blockIdx.y * kTile, srow = scale_row_bytes(p.K);
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    float acc[kMats][4][4] = {};
-    for (int64_t k0 = 0; k0 < p.K; k0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * (1 + kMats) * 4; i += kThreads) {   // 8 elements each
-            const int r = i / 4, part = i % 4, m = r / kTile - 1, rr = r % kTile;
-            const uint8_t *q = p.codes, *s = p.scales;
-            int64_t row = row0 + rr;
-            bool in = row < end;
-            if (m >= 0) {
-                q = p.w_codes, s = p.w_scales;
-                in = n0 + rr < p.N;
-                row = ((int64_t)s_expert * kMats + m) * p.N + n0 + rr;
-            }
-            float v[8] = {};
-            if (in) {
-                decode8(__ldg(reinterpret_cast<const uint32_t *>(q + row * (p.K / 2) + k0 / 2) + part), v);
-                const float f = e8m0_value(__ldg(s + row * srow + k0 / 32));
-                for (int j = 0; j < 8; ++j)
-                    v[j] *= f;
-            }
-            float *d = m < 0 ? &sx[rr][part * 8] : &sw[m < 0 ? 0 : m][rr][part * 8];
-            for (int j = 0; j < 8; ++j)
-                d[j] = v[j];
+    long long rows = 0;
+    int tiles = 0, bad = 0;
+    for (int e = lo; e < hi; ++e) {
+        const long long v = at(e), c = p.counts_prefix && e > 0 ? v - at(e - 1) : v;
+        if (c < 0 || (p.counts_prefix && v < 0))
+            bad |= mrr_ws::kFlagNonPos;
+        else if (c > p.A || v > p.A)
+            bad |= mrr_ws::kFlagSum;
+        else {
+            rows += c;
+            tiles += (int)((c + p.tokens - 1) / p.tokens);
         }
-        __syncthreads();
-        for (int k = 0; k < kStep; ++k)
-            for (int m = 0; m < kMats; ++m)
-                for (int a = 0; a < 4; ++a)
-                    for (int b = 0; b < 4; ++b)
-                        acc[m][a][b] = fmaf(sx[ty + 16 * a][k], sw[m][tx + 16 * b][k], acc[m][a][b]);
-        __syncthreads();
     }
-    for (int a = 0; a < 4; ++a)
-        for (int b = 0; b < 4; ++b) {
-            const int64_t row = row0 + ty + 16 * a, n = n0 + tx + 16 * b;
-            float y = acc[0][a][b];
-            if (kGated)
-                y = y / (1.f + expf(-y)) * acc[kMats - 1][a][b];
-            if (p.row_weight && row < end)
-                y *= p.row_weight[row];
-            sy[ty + 16 * a][tx + 16 * b] = y;
-            if (row < end && n < p.N) {
-                if (p.out_dt == MOE_F32)
-                    store1<MOE_F32>(p.out, row * p.N + n, y);
-                else if (p.out_dt == MOE_BF16)
-                    store1<MOE_BF16>(p.out, row * p.N + n, y);
-                else if (p.out_dt == MOE_F16)
-                    store1<MOE_F16>(p.out, row * p.N + n, y);
-            }
-        }
-    if (p.out_dt != MOE_MXFP4)
-        return;
+    // a run's rows are at most 8 A < 2^34: cap them, a sum above A is refused below
+    int r = (int)min(rows, (long long)p.A + 1 > 0x7fffffffll ? 0x7fffffffll : (long long)p.A + 1), t = tiles;
+    if (rows > p.A)
+        bad |= mrr_ws::kFlagSum;
+    if (bad)
+        atomicOr(&sh->bad, bad);
     __syncthreads();
-    for (int i = threadIdx.x; i < kTile * 2; i += kThreads) {   // one 32-block each; N is a multiple of 32
-        const int r = i / 2, h = i % 2;
-        const int64_t row = row0 + r, n = n0 + 32 * h;
-        if (row >= end || n >= p.N)
-            continue;
-        uint32_t m = 0u;
-        for (int j = 0; j < 32; ++j)
-            m = max(m, __float_as_uint(sy[r][32 * h + j]) & 0x7fffffffu);
-        const uint32_t sb = scale_byte(m);
-        const float f = inverse_scale(sb);
-        uint8_t *q = static_cast<uint8_t *>(p.out) + row * (p.N / 2) + n / 2;
-        for (int j = 0; j < 16; ++j)
-            q[j] = (uint8_t)encode2(sy[r][32 * h + 2 * j] * f, sy[r][32 * h + 2 * j + 1] * f);
+    if (sh->bad)   // no sum is formed of counts that do not fit
+        return sh->bad & mrr_ws::kFlagNonPos ? mrr_ws::kFlagNonPos : mrr_ws::kFlagSum;
+    // the sum over the block may pass 2^31 where single runs do not: scan in 64 bits
+    long long rs = r;
+    int ts = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long a = __shfl_up_sync(kFull, rs, o);
+        const int b = __shfl_up_sync(kFull, ts, o);
+        if (lane >= o) {
+            rs += a;
+            ts += b;
+        }
+    }
+    if (lane == 31) {
+        sh->scan_rows[warp] = rs;
+        sh->scan_tiles[warp] = ts;
+    }
+    __syncthreads();
+    long long row0 = rs - r, total = 0;
+    int tile0 = ts - t;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) {
+            row0 += sh->scan_rows[w];
+            tile0 += sh->scan_tiles[w];
+        }
+        total += sh->scan_rows[w];
+    }
+    if (total != p.A)
+        return mrr_ws::kFlagSum;
+    for (int e = lo; e < hi; ++e) {
+        tables[e] = (int)row0;
+        tables[p.E + 1 + e] = tile0;
+        const int c = (int)(p.counts_prefix && e > 0 ? at(e) - at(e - 1) : at(e));
+        row0 += c;
+        tile0 += (c + p.tokens - 1) / p.tokens;
+    }
+    if (hi == p.E && lo < hi) {
+        tables[p.E] = (int)row0;
+        tables[2 * p.E + 1] = tile0;
+    }
+    __syncthreads();
+    return 0;
+}
+
+__device__ __forceinline__ Tile tile_at(const Params &p, const int *tables, int features, long long index)
+{
+    const int *rows = tables, *tiles = tables + p.E + 1;
+    int lo = 0, hi = p.E - 1;   // the last expert whose first tile is at or before index (one that has tiles)
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if ((long long)tiles[mid] * features <= index)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int n = tiles[lo + 1] - tiles[lo], count = rows[lo + 1] - rows[lo];
+    const int q = (int)(index - (long long)tiles[lo] * features), f = q / n, i = q - f * n;
+    const int share = (((count + n - 1) / n) + 15) & ~15;
+    Tile t;
+    t.expert = lo;
+    t.feature = f * (p.gated ? kRowTile : 2 * kRowTile);
+    t.row = rows[lo] + i * share;
+    t.rows = min(share, count - i * share);
+    t.columns = (t.rows + 15) & ~15;
+    return t;
+}
+
+// scale bytes of 8 blocks of row `row` from block b0; blocks at or past `blocks` read 0 (their codes
+// are zeros, and a scale of 2^-127 keeps them so)
+__device__ __forceinline__ uint2 scales8(const uint8_t *s, int64_t row, int64_t row_bytes, int b0, int blocks, bool wide)
+{
+    const uint8_t *at = s + row * row_bytes + b0;
+    uint2 v = make_uint2(0, 0);
+    if (wide) {
+        v = __ldg(reinterpret_cast<const uint2 *>(at));
+    } else {
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)   // pairs are whole: a row holds ceil(K / 64) of them
+            h[i] = b0 + 2 * i < blocks ? __ldg(reinterpret_cast<const uint16_t *>(at) + i) : 0u;
+        v = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    }
+    const int left = blocks - b0;
+    if (left < 8) {
+        v.x &= left >= 4 ? kFull : (1u << (8 * left)) - 1u;
+        v.y &= left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u;
+    }
+    return v;
+}
+
+// silu(g) u
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + expf(-g)) * u; }
+
+__device__ __forceinline__ void store_value(const Params &p, int64_t at, float v)
+{
+    if (p.out_dt == MOE_BF16)
+        store1<MOE_BF16>(p.out, at, v);
+    else if (p.out_dt == MOE_F16)
+        store1<MOE_F16>(p.out, at, v);
+    else
+        store1<MOE_F32>(p.out, at, v);
+}
+
+// one result of each lane, 32 features of a row from n (n + lane), as an MXFP4 block
+__device__ __forceinline__ void store_block(const Params &p, int64_t row, int n, int lane, float v)
+{
+    const uint32_t s = scale_byte(__reduce_max_sync(kFull, __float_as_uint(v) & 0x7fffffffu));
+    v *= inverse_scale(s);
+    const uint32_t two = encode2(v, __shfl_down_sync(kFull, v, 1));   // of lanes 2 i, 2 i + 1
+    if (lane % 2 == 0)
+        static_cast<uint8_t *>(p.out)[row * (p.N / 2) + (n + lane) / 2] = (uint8_t)two;
+    if (lane == 0) {
         uint8_t *so = p.out_scales + row * scale_row_bytes(p.N) + n / 32;
-        so[0] = (uint8_t)sb;
+        so[0] = (uint8_t)s;
         if (n / 32 % 2 == 0 && n + 32 >= p.N)
             so[1] = 127;
     }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap x_map,
+                   const __grid_constant__ CUtensorMap w_map)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Shared *sh = reinterpret_cast<Shared *>(smem);
+    int *tables = reinterpret_cast<int *>(smem + p.sm_tables);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    const int bad = scan_counts(p, sh, tables);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.status[0] = (uint32_t)bad;
+        p.status[1] = 0;
+    }
+    if (bad)
+        return;
+    const int mats = p.gated ? 2 : 1;
+    const int features = (p.N + (p.gated ? kRowTile : 2 * kRowTile) - 1) / (p.gated ? kRowTile : 2 * kRowTile);
+    const long long total = (long long)tables[2 * p.E + 1] * features;
+    if ((long long)blockIdx.x >= total)
+        return;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mrr::mbar_init(mrr::smem_addr(&sh->full[s]), 1 + 4);   // the copies' thread, four scale warps
+            mrr::mbar_init(mrr::smem_addr(&sh->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mrr::mbar_init(mrr::smem_addr(&sh->sums_full[b]), 1);
+            mrr::mbar_init(mrr::smem_addr(&sh->sums_empty[b]), kEpilogueWarps);
+        }
+        mrr::mbar_init(mrr::smem_addr(&sh->drained), 1);
+        sh->abort = 0;
+        mrr::mbar_init_fence();
+        tc::prefetch_map(&x_map);
+        tc::prefetch_map(&w_map);
+    }
+    if (warp == 1)
+        tc::alloc(mrr::smem_addr(&sh->tmem), kColumns);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&sh->tmem);
+
+    const int steps = (p.K + 255) / 256, groups = groups_of(p.tokens);
+    const uint32_t stage0 = mrr::smem_addr(smem) + p.sm_stage;
+    const uint32_t stage_size = stage_bytes(p.tokens);
+    const uint32_t off_x = 2 * kRowTile * kStepBytes, off_sfa = off_x + p.tokens * kStepBytes, off_sfb = off_sfa + 2048;
+    auto next_stage = [&](int &stage, uint32_t &parity) {
+        if (++stage == p.stages) {
+            stage = 0;
+            parity ^= 1u;
+        }
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {   // codes
+            int stage = 0;
+            uint32_t parity = 1u, issued = 0u;
+            bool ok = true;
+            for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
+                const Tile t = tile_at(p, tables, features, i);
+                const int w_row = t.expert * mats * p.N + t.feature, second = p.gated ? p.N : kRowTile;
+                const int boxes = (t.columns + kBoxRows - 1) / kBoxRows;
+                for (int k = 0; k < steps; ++k) {
+                    if (!(ok = wait(sh, &sh->empty[stage], parity)))
+                        break;
+                    const uint32_t at = stage0 + stage * stage_size, bar = mrr::smem_addr(&sh->full[stage]);
+                    mrr::mbar_arrive_expect_tx(bar, 2 * kRowTile * kStepBytes + boxes * kBoxRows * kStepBytes);
+                    tc::load_box(at, &w_map, k * kStepBytes, w_row, bar);
+                    tc::load_box(at + kRowTile * kStepBytes, &w_map, k * kStepBytes, w_row + second, bar);
+                    for (int b = 0; b < boxes; ++b)
+                        tc::load_box(at + off_x + b * kBoxRows * kStepBytes, &x_map, k * kStepBytes, t.row + b * kBoxRows,
+                                     bar);
+                    issued |= 1u << stage;
+                    next_stage(stage, parity);
+                }
+            }
+            if (!ok) {   // leave no copy in flight: give each stage's a moment to land
+                for (int s = 0; s < p.stages; ++s)
+                    if (issued >> s & 1u)
+                        for (int b = 0; b < 2; ++b)
+                            mrr::mbar_wait_bounded(mrr::smem_addr(&sh->full[s]), b, 1000000ull);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {   // matrix instructions
+            int stage = 0, set = 0;
+            uint32_t parity = 0u, set_parity = 1u;
+            bool ok = true;
+            const uint32_t scale_columns = 16 + 8 * groups, scales0 = tmem + p.sums * 2 * p.tokens;
+            for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
+                const Tile t = tile_at(p, tables, features, i);
+                if (!(ok = wait(sh, &sh->sums_empty[set], set_parity)))
+                    break;
+                tc::fence_after();
+                const uint32_t d = tmem + set * 2 * p.tokens;
+                const uint32_t instr[2] = {tc::mxf4_instr(t.columns, 0), tc::mxf4_instr(t.columns, 1)};
+                for (int k = 0; k < steps; ++k) {
+                    if (!(ok = wait(sh, &sh->full[stage], parity)))
+                        break;
+                    tc::fence_after();
+                    const uint32_t at = stage0 + stage * stage_size;
+                    const uint32_t sfa = scales0 + stage * scale_columns, sfb = sfa + 16;
+                    // atoms of 128 rows by 4 blocks: weights [tile][half], tokens [half][group]
+                    for (int a = 0; a < 4; ++a)
+                        tc::copy_scales(sfa + 4 * a, tc::desc_rows16(at + off_sfa + a * 512));
+                    for (int a = 0; a < 2 * groups; ++a)
+                        tc::copy_scales(sfb + 4 * a, tc::desc_rows16(at + off_sfb + a * 512));
+                    const uint64_t w0 = tc::desc_swizzle128(at), w1 = tc::desc_swizzle128(at + kRowTile * kStepBytes);
+                    const uint64_t x = tc::desc_swizzle128(at + off_x);
+                    const int parts = min(4, (p.K - k * 256 + 63) / 64);
+                    for (int j = 0; j < parts; ++j) {   // 64 elements: 32 bytes further along the rows
+                        const uint32_t half = j / 2;
+                        tc::mma_mxf4(d, w0 + 2 * j, x + 2 * j, instr[j % 2], sfa + 4 * half, sfb + 4 * groups * half,
+                                     k > 0 || j > 0);
+                        tc::mma_mxf4(d + p.tokens, w1 + 2 * j, x + 2 * j, instr[j % 2], sfa + 8 + 4 * half,
+                                     sfb + 4 * groups * half, k > 0 || j > 0);
+                    }
+                    tc::commit(mrr::smem_addr(&sh->empty[stage]));
+                    next_stage(stage, parity);
+                }
+                if (ok)
+                    tc::commit(mrr::smem_addr(&sh->sums_full[set]));
+                if (++set == p.sums) {
+                    set = 0;
+                    set_parity ^= 1u;
+                }
+            }
+            if (!ok) {   // tensor memory is freed only after what was issued is done
+                tc::commit(mrr::smem_addr(&sh->drained));
+                mrr::mbar_wait_bounded(mrr::smem_addr(&sh->drained), 0, 100000000ull);
+            }
+        }
+    } else if (warp >= kScaleWarp) {   // scales
+        const int r = threadIdx.x - 32 * kScaleWarp;
+        const int blocks = p.K / 32;
+        const int64_t row_bytes = scale_row_bytes(p.K), w_rows = (int64_t)p.E * mats * p.N;
+        const int second = p.gated ? p.N : kRowTile;
+        // two steps are loaded ahead of the one being stored
+        long long ahead = blockIdx.x;
+        int ahead_k = 0;
+        Tile t = tile_at(p, tables, features, ahead);
+        auto load = [&](uint2 (&v)[4]) {
+            if (ahead >= total)
+                return;
+            const int b0 = ahead_k * 8;
+            const int64_t w_row = (int64_t)t.expert * mats * p.N + t.feature + r;
+            v[0] = w_row < w_rows ? scales8(p.w_scales, w_row, row_bytes, b0, blocks, p.w_wide) : make_uint2(0, 0);
+            v[1] = w_row + second < w_rows ? scales8(p.w_scales, w_row + second, row_bytes, b0, blocks, p.w_wide)
+                                           : make_uint2(0, 0);
+            v[2] = r < t.rows ? scales8(p.scales, (int64_t)t.row + r, row_bytes, b0, blocks, p.wide) : make_uint2(0, 0);
+            v[3] = r + 128 < t.rows ? scales8(p.scales, (int64_t)t.row + r + 128, row_bytes, b0, blocks, p.wide)
+                                    : make_uint2(0, 0);
+            if (++ahead_k == steps) {
+                ahead_k = 0;
+                ahead += gridDim.x;
+                if (ahead < total)
+                    t = tile_at(p, tables, features, ahead);
+            }
+        };
+        uint2 v0[4] = {}, v1[4] = {}, v2[4] = {};
+        load(v0);
+        load(v1);
+        int stage = 0;
+        uint32_t parity = 1u;
+        const long long mine = (total - blockIdx.x + gridDim.x - 1) / gridDim.x * steps;
+        const uint32_t to = (r % 32) * 16 + (r / 32) * 4;   // a row's place in an atom
+        for (long long i = 0; i < mine; ++i) {
+            load(v2);
+            if (!wait(sh, &sh->empty[stage], parity))
+                break;
+            const uint32_t at = stage0 + stage * stage_size;
+            auto put = [&](uint32_t a, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); };
+            put(at + off_sfa + to, v0[0].x);
+            put(at + off_sfa + 512 + to, v0[0].y);
+            put(at + off_sfa + 1024 + to, v0[1].x);
+            put(at + off_sfa + 1536 + to, v0[1].y);
+            put(at + off_sfb + to, v0[2].x);
+            put(at + off_sfb + 512 * groups + to, v0[2].y);
+            if (groups == 2) {
+                put(at + off_sfb + 512 + to, v0[3].x);
+                put(at + off_sfb + 1536 + to, v0[3].y);
+            }
+            tc::fence_to_async();
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(mrr::smem_addr(&sh->full[stage]));
+            next_stage(stage, parity);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v0[j] = v1[j];
+                v1[j] = v2[j];
+            }
+        }
+    } else if (warp >= kEpilogueWarp) {
+        const int quarter = warp % 4, part = (warp - kEpilogueWarp) / 4;   // lanes; every other 16 columns
+        int set = 0;
+        uint32_t parity = 0u;
+        for (long long i = blockIdx.x; i < total; i += gridDim.x) {
+            const Tile t = tile_at(p, tables, features, i);
+            if (!wait(sh, &sh->sums_full[set], parity))
+                break;
+            tc::fence_after();
+            const int n0 = t.feature + 32 * quarter, n = n0 + lane;
+            const uint32_t d = tmem + set * 2 * p.tokens + ((uint32_t)(32 * quarter) << 16);
+            for (int c = 16 * part; c < t.columns; c += 32) {
+                uint32_t a[16], b[16];
+                tc::load16(d + c, a);
+                tc::load16(d + p.tokens + c, b);
+                tc::load_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    if (c + j >= t.rows)
+                        break;
+                    const int64_t row = t.row + c + j;
+                    const float w = p.row_weight ? __ldg(p.row_weight + row) : 1.f;
+                    const float u = __uint_as_float(a[j]), v = __uint_as_float(b[j]);
+                    if (p.gated) {
+                        const float y = swiglu(u, v) * w;
+                        if (p.out_dt == MOE_MXFP4) {
+                            if (n0 < p.N)
+                                store_block(p, row, n0, lane, y);
+                        } else if (n < p.N) {
+                            store_value(p, row * p.N + n, y);
+                        }
+                    } else if (p.out_dt == MOE_MXFP4) {
+                        if (n0 < p.N)
+                            store_block(p, row, n0, lane, u * w);
+                        if (n0 + kRowTile < p.N)
+                            store_block(p, row, n0 + kRowTile, lane, v * w);
+                    } else {
+                        if (n < p.N)
+                            store_value(p, row * p.N + n, u * w);
+                        if (n + kRowTile < p.N)
+                            store_value(p, row * p.N + n + kRowTile, v * w);
+                    }
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(mrr::smem_addr(&sh->sums_empty[set]));
+            if (++set == p.sums) {
+                set = 0;
+                parity ^= 1u;
+            }
+        }
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (threadIdx.x == 0 && sh->abort)
+        atomicOr(p.status, mrr_ws::kFlagTimeout);
+    if (warp == 1)
+        tc::dealloc(tmem, kColumns);
+}
+
+// a 2-D map of `rows` rows of row_bytes bytes, boxes of 128 bytes by box_rows, 128-byte swizzle
+bool make_map(CUtensorMap *map, const uint8_t *base, int64_t rows, int64_t row_bytes, int box_rows)
+{
+    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {kStepBytes, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dims, strides, box, one,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -161,8 +543,8 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
         return MRR_ERR_DTYPE;
     if ((expert_num_type != 0 && expert_num_type != 1) || (gated != 0 && gated != 1))
         return MRR_ERR_ATTR;
-    if (A < 0 || A > INT32_MAX || E < 1 || E > 4096 || K < 32 || K % 32 || K > (1 << 20) || N < 1 || N > (1 << 20) ||
-        (out_dt == MOE_MXFP4 && N % 32))
+    if (A < 0 || A > INT32_MAX - 256 || E < 1 || E > kMaxExperts || K < 32 || K % 32 || K > (1 << 20) || N < 1 ||
+        N > (1 << 20) || E * N * (gated ? 2 : 1) > INT32_MAX - 512 || (out_dt == MOE_MXFP4 && N % 32))
         return MRR_ERR_SHAPE;
     if (!expert_num || !w_codes || !w_scales || (A > 0 && (!codes || !scales || !out)) ||
         (out_dt == MOE_MXFP4 && A > 0 && !out_scales))
@@ -173,16 +555,48 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
         return MRR_ERR_ALIGN;
     if (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < moe_mx_grouped_workspace(E))
         return MRR_ERR_WORKSPACE;
-    Params p{codes, scales, A, K, expert_num, expert_num_is_i64, expert_num_type == 0, (int)E, w_codes, w_scales, N,
-             row_weight, out, (int)out_dt, out_scales, static_cast<uint32_t *>(workspace)};
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t tiles = A / kTile + E;   // at least as many as the experts' tiles
-    const dim3 grid((unsigned)tiles, (unsigned)((N + kTile - 1) / kTile));
-    if (gated)
-        grouped_simple<true><<<grid, kThreads, 0, s>>>(p);
-    else
-        grouped_simple<false><<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? MRR_OK : MRR_ERR_CUDA;
+    int device = -1, sms = 0, smem_max = 0;
+    if (cudaGetDevice(&device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, device) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MRR_ERR_CUDA;
+    }
+    Params p{};
+    p.scales = scales, p.w_scales = w_scales;
+    p.A = (int)A, p.K = (int)K, p.E = (int)E, p.N = (int)N;
+    p.counts_i64 = expert_num_is_i64, p.counts_prefix = expert_num_type == 0, p.gated = gated, p.out_dt = (int)out_dt;
+    p.counts = expert_num, p.row_weight = row_weight, p.out = out, p.out_scales = out_scales;
+    p.status = static_cast<uint32_t *>(workspace);
+    // Few rows an expert: narrow tiles, more stages, two sets of sums.  Else as wide as tensor memory
+    // allows beside the scales (2 x 192 columns): a wide tile re-reads its weights less often.
+    p.tokens = A <= 64 * E ? 64 : 192;
+    p.sums = p.tokens <= 64 ? 2 : 1;
+    p.wide = (uintptr_t)scales % 8 == 0 && scale_row_bytes(K) % 8 == 0;
+    p.w_wide = (uintptr_t)w_scales % 8 == 0 && scale_row_bytes(K) % 8 == 0;
+    p.sm_tables = (int)mrr_ws::round_up(sizeof(Shared), 16);
+    p.sm_stage = (int)mrr_ws::round_up(p.sm_tables + 8 * (E + 1), 1024);
+    const int columns_left = (kColumns - p.sums * 2 * p.tokens) / (16 + 8 * groups_of(p.tokens));
+    int stages = (smem_max - p.sm_stage) / stage_bytes(p.tokens);
+    stages = stages < columns_left ? stages : columns_left;
+    p.stages = stages < kMaxStages ? stages : kMaxStages;
+    if (p.stages < 2)
+        return MRR_ERR_CUDA;
+    CUtensorMap x_map, w_map;
+    if (!make_map(&w_map, w_codes, E * N * (gated ? 2 : 1), K / 2, kRowTile) ||
+        !make_map(&x_map, A ? codes : w_codes, A ? A : 1, K / 2, kBoxRows))
+        return MRR_ERR_CUDA;
+    const size_t smem = (size_t)p.sm_stage + (size_t)p.stages * stage_bytes(p.tokens);
+    cudaError_t err = cudaFuncSetAttribute(grouped_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err == cudaSuccess) {
+        grouped_kernel<<<sms, kThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p, x_map, w_map);
+        err = cudaGetLastError();
+    }
+    if (err != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MRR_ERR_CUDA;
+    }
+    return MRR_OK;
 }
 
 }  // extern "C"
