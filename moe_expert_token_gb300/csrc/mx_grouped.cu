@@ -12,9 +12,12 @@
 //    by up to 192 token rows of one expert, K in steps of 256 (128 bytes a row).  An expert's rows
 //    are split evenly over its tiles, in multiples of 16.
 //  * One persistent block an SM.  Warp 0 issues the tiled bulk copies of codes, warp 1 the matrix
-//    instructions, warps 12-15 bring the scales (8 bytes a row and step, which the tensor cores
-//    want in an order of their own), warps 4-11 turn finished sums into results while the next
-//    tile's stages are being filled.
+//    instructions, warps 12-15 bring the scales, warps 4-11 turn finished sums into results while
+//    the next tile's stages are being filled.
+//  * Scales go from global memory through shared memory, where they change order, into tensor memory
+//    by the scale warps' own stores.  The tensor pipe's copy instruction would do the last leg, but
+//    it holds up the matrix instructions behind it: 8 copies a step took 92 of 266 us at 16384
+//    rows, 32 experts, 7168x2048 gated.
 //  * Neighbouring blocks work on the token tiles of the same weights, which so come from HBM once.
 //
 // Every wait is bounded: one that lasts two seconds sets a flag, all roles leave, copies in flight
@@ -51,7 +54,7 @@ struct Params {
     int tokens;        // most token rows of a tile (64 or 192)
     int stages, sums;  // ring stages; sets of sums in tensor memory (1 or 2)
     int wide, w_wide;  // scale rows are 8-byte aligned
-    int sm_stage, sm_tables;
+    int sm_stage, sm_tables, sm_scales;
 };
 
 struct Tile {
@@ -61,7 +64,7 @@ struct Tile {
 __host__ __device__ constexpr int groups_of(int tokens) { return (tokens + 127) / 128; }
 __host__ __device__ constexpr int stage_bytes(int tokens)
 {
-    return 2 * kRowTile * kStepBytes + tokens * kStepBytes + 2048 + 1024 * groups_of(tokens);
+    return 2 * kRowTile * kStepBytes + tokens * kStepBytes;
 }
 
 struct Shared {
@@ -74,16 +77,17 @@ struct Shared {
 
 __device__ __forceinline__ bool wait(Shared *sh, uint64_t *bar, uint32_t parity)
 {
-    if (mrr::mbar_try_wait(mrr::smem_addr(bar), parity))
-        return true;
-    const uint64_t t0 = mrr::global_timer_ns();
+    uint64_t t0 = 0;   // the timer is slow to read: not before a wait has become a long one
     for (uint32_t it = 1;; ++it) {
         if (mrr::mbar_try_wait(mrr::smem_addr(bar), parity))
             return true;
-        if (it % 64 == 0) {
+        if (it % 1024 == 0) {
             if (*reinterpret_cast<volatile int *>(&sh->abort))
                 return false;
-            if (mrr::global_timer_ns() - t0 > kWaitLimitNs) {
+            const uint64_t now = mrr::global_timer_ns();
+            if (t0 == 0)
+                t0 = now;
+            else if (now - t0 > kWaitLimitNs) {
                 *reinterpret_cast<volatile int *>(&sh->abort) = 1;
                 return false;
             }
@@ -215,35 +219,58 @@ __device__ __forceinline__ uint2 scales8(const uint8_t *s, int64_t row, int64_t 
     return v;
 }
 
+// true for every thread of the scale warps if `failed` is for any of them
+__device__ __forceinline__ bool any_scale_warp(bool failed)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "barrier.cta.red.or.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)failed)
+                 : "memory");
+    return r != 0u;
+}
+
 // silu(g) u
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + expf(-g)) * u; }
 
-__device__ __forceinline__ void store_value(const Params &p, int64_t at, float v)
+// Results of 16 columns (token rows row .. row + rows - 1) of one output feature a lane: n0 + lane.
+template <int kOut>
+__device__ __forceinline__ void store16(const Params &p, int64_t row, int rows, int n0, int lane, const float (&y)[16])
 {
-    if (p.out_dt == MOE_BF16)
-        store1<MOE_BF16>(p.out, at, v);
-    else if (p.out_dt == MOE_F16)
-        store1<MOE_F16>(p.out, at, v);
-    else
-        store1<MOE_F32>(p.out, at, v);
-}
-
-// one result of each lane, 32 features of a row from n (n + lane), as an MXFP4 block
-__device__ __forceinline__ void store_block(const Params &p, int64_t row, int n, int lane, float v)
-{
-    const uint32_t s = scale_byte(__reduce_max_sync(kFull, __float_as_uint(v) & 0x7fffffffu));
-    v *= inverse_scale(s);
-    const uint32_t two = encode2(v, __shfl_down_sync(kFull, v, 1));   // of lanes 2 i, 2 i + 1
-    if (lane % 2 == 0)
-        static_cast<uint8_t *>(p.out)[row * (p.N / 2) + (n + lane) / 2] = (uint8_t)two;
-    if (lane == 0) {
-        uint8_t *so = p.out_scales + row * scale_row_bytes(p.N) + n / 32;
-        so[0] = (uint8_t)s;
-        if (n / 32 % 2 == 0 && n + 32 >= p.N)
-            so[1] = 127;
+    const int n = n0 + lane;
+    if constexpr (kOut == MOE_MXFP4) {   // 32 lanes are one block; N is a multiple of 32
+        if (n0 >= p.N)
+            return;
+        uint8_t *q = static_cast<uint8_t *>(p.out) + row * (p.N / 2) + n / 2;
+        uint8_t *so = p.out_scales + row * scale_row_bytes(p.N) + n0 / 32;
+        const bool pad = n0 / 32 % 2 == 0 && n0 + 32 >= p.N;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const uint32_t s = scale_byte(__reduce_max_sync(kFull, __float_as_uint(y[j]) & 0x7fffffffu));
+            const float v = y[j] * inverse_scale(s);
+            const uint32_t two = encode2(v, __shfl_down_sync(kFull, v, 1));   // of lanes 2 i, 2 i + 1
+            if (j < rows) {
+                if (lane % 2 == 0)
+                    q[(int64_t)j * (p.N / 2)] = (uint8_t)two;
+                if (lane == 0) {
+                    so[j * scale_row_bytes(p.N)] = (uint8_t)s;
+                    if (pad)
+                        so[j * scale_row_bytes(p.N) + 1] = 127;
+                }
+            }
+        }
+    } else {
+        if (n >= p.N)
+            return;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (j < rows)
+                store1<kOut>(p.out, (row + j) * p.N + n, y[j]);
     }
 }
 
+template <bool kGated, int kOut>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap x_map,
                    const __grid_constant__ CUtensorMap w_map)
@@ -260,8 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (bad)
         return;
-    const int mats = p.gated ? 2 : 1;
-    const int features = (p.N + (p.gated ? kRowTile : 2 * kRowTile) - 1) / (p.gated ? kRowTile : 2 * kRowTile);
+    constexpr int mats = kGated ? 2 : 1, kFeatures = kGated ? kRowTile : 2 * kRowTile;
+    const int features = (p.N + kFeatures - 1) / kFeatures;
     const long long total = (long long)tables[2 * p.E + 1] * features;
     if ((long long)blockIdx.x >= total)
         return;
@@ -291,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int steps = (p.K + 255) / 256, groups = groups_of(p.tokens);
     const uint32_t stage0 = mrr::smem_addr(smem) + p.sm_stage;
     const uint32_t stage_size = stage_bytes(p.tokens);
-    const uint32_t off_x = 2 * kRowTile * kStepBytes, off_sfa = off_x + p.tokens * kStepBytes, off_sfb = off_sfa + 2048;
+    const uint32_t off_x = 2 * kRowTile * kStepBytes;
     auto next_stage = [&](int &stage, uint32_t &parity) {
         if (++stage == p.stages) {
             stage = 0;
@@ -306,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
                 const Tile t = tile_at(p, tables, features, i);
-                const int w_row = t.expert * mats * p.N + t.feature, second = p.gated ? p.N : kRowTile;
+                const int w_row = t.expert * mats * p.N + t.feature, second = kGated ? p.N : kRowTile;
                 const int boxes = (t.columns + kBoxRows - 1) / kBoxRows;
                 for (int k = 0; k < steps; ++k) {
                     if (!(ok = wait(sh, &sh->empty[stage], parity)))
@@ -348,11 +375,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::fence_after();
                     const uint32_t at = stage0 + stage * stage_size;
                     const uint32_t sfa = scales0 + stage * scale_columns, sfb = sfa + 16;
-                    // atoms of 128 rows by 4 blocks: weights [tile][half], tokens [half][group]
-                    for (int a = 0; a < 4; ++a)
-                        tc::copy_scales(sfa + 4 * a, tc::desc_rows16(at + off_sfa + a * 512));
-                    for (int a = 0; a < 2 * groups; ++a)
-                        tc::copy_scales(sfb + 4 * a, tc::desc_rows16(at + off_sfb + a * 512));
                     const uint64_t w0 = tc::desc_swizzle128(at), w1 = tc::desc_swizzle128(at + kRowTile * kStepBytes);
                     const uint64_t x = tc::desc_swizzle128(at + off_x);
                     const int parts = min(4, (p.K - k * 256 + 63) / 64);
@@ -382,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = threadIdx.x - 32 * kScaleWarp;
         const int blocks = p.K / 32;
         const int64_t row_bytes = scale_row_bytes(p.K), w_rows = (int64_t)p.E * mats * p.N;
-        const int second = p.gated ? p.N : kRowTile;
+        const int second = kGated ? p.N : kRowTile;
         // two steps are loaded ahead of the one being stored
         long long ahead = blockIdx.x;
         int ahead_k = 0;
@@ -411,24 +433,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         int stage = 0;
         uint32_t parity = 1u;
         const long long mine = (total - blockIdx.x + gridDim.x - 1) / gridDim.x * steps;
-        const uint32_t to = (r % 32) * 16 + (r / 32) * 4;   // a row's place in an atom
+        // An atom is 128 rows by 4 blocks: row q's bytes are word q / 32 of 16-byte line q % 32, and in
+        // tensor memory column q / 32 of lane q % 32, in each of the four lane quarters.  Atoms in
+        // order: weights [tile][half of the step], tokens [half][group of 128 rows].
+        const uint32_t buffers = mrr::smem_addr(smem) + p.sm_scales, buffer_size = 2048 + 1024 * groups;
+        const uint32_t to = (r % 32) * 16 + (r / 32) * 4;
+        const uint32_t scale_columns = 16 + 8 * groups;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + p.sums * 2 * p.tokens;
         for (long long i = 0; i < mine; ++i) {
             load(v2);
-            if (!wait(sh, &sh->empty[stage], parity))
-                break;
-            const uint32_t at = stage0 + stage * stage_size;
+            const uint32_t at = buffers + (i & 1) * buffer_size;
             auto put = [&](uint32_t a, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); };
-            put(at + off_sfa + to, v0[0].x);
-            put(at + off_sfa + 512 + to, v0[0].y);
-            put(at + off_sfa + 1024 + to, v0[1].x);
-            put(at + off_sfa + 1536 + to, v0[1].y);
-            put(at + off_sfb + to, v0[2].x);
-            put(at + off_sfb + 512 * groups + to, v0[2].y);
+            put(at + to, v0[0].x);
+            put(at + 512 + to, v0[0].y);
+            put(at + 1024 + to, v0[1].x);
+            put(at + 1536 + to, v0[1].y);
+            put(at + 2048 + to, v0[2].x);
+            put(at + 2048 + 512 * groups + to, v0[2].y);
             if (groups == 2) {
-                put(at + off_sfb + 512 + to, v0[3].x);
-                put(at + off_sfb + 1536 + to, v0[3].y);
+                put(at + 2048 + 512 + to, v0[3].x);
+                put(at + 2048 + 1536 + to, v0[3].y);
             }
-            tc::fence_to_async();
+            // the other buffer is free again once all four warps are here
+            if (any_scale_warp(!wait(sh, &sh->empty[stage], parity)))
+                break;
+            tc::fence_after();
+            const uint32_t columns = lanes + stage * scale_columns;
+#pragma unroll
+            for (int a = 0; a < 8; ++a)
+                if (a < 4 + 2 * groups) {
+                    uint32_t v[4];
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                 : "r"(at + a * 512 + lane * 16)
+                                 : "memory");
+                    tc::store4(columns + 4 * a, v);
+                }
+            tc::store_wait();
+            tc::fence_before();
             __syncwarp();
             if (lane == 0)
                 tc::mbar_arrive(mrr::smem_addr(&sh->full[stage]));
@@ -448,40 +490,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait(sh, &sh->sums_full[set], parity))
                 break;
             tc::fence_after();
-            const int n0 = t.feature + 32 * quarter, n = n0 + lane;
+            const int n0 = t.feature + 32 * quarter;
             const uint32_t d = tmem + set * 2 * p.tokens + ((uint32_t)(32 * quarter) << 16);
             for (int c = 16 * part; c < t.columns; c += 32) {
                 uint32_t a[16], b[16];
                 tc::load16(d + c, a);
                 tc::load16(d + p.tokens + c, b);
                 tc::load_wait();
+                const int64_t row = t.row + c;
+                const int rows = min(16, t.rows - c);
+                float y[16], z[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    if (c + j >= t.rows)
-                        break;
-                    const int64_t row = t.row + c + j;
-                    const float w = p.row_weight ? __ldg(p.row_weight + row) : 1.f;
-                    const float u = __uint_as_float(a[j]), v = __uint_as_float(b[j]);
-                    if (p.gated) {
-                        const float y = swiglu(u, v) * w;
-                        if (p.out_dt == MOE_MXFP4) {
-                            if (n0 < p.N)
-                                store_block(p, row, n0, lane, y);
-                        } else if (n < p.N) {
-                            store_value(p, row * p.N + n, y);
-                        }
-                    } else if (p.out_dt == MOE_MXFP4) {
-                        if (n0 < p.N)
-                            store_block(p, row, n0, lane, u * w);
-                        if (n0 + kRowTile < p.N)
-                            store_block(p, row, n0 + kRowTile, lane, v * w);
-                    } else {
-                        if (n < p.N)
-                            store_value(p, row * p.N + n, u * w);
-                        if (n + kRowTile < p.N)
-                            store_value(p, row * p.N + n + kRowTile, v * w);
+                    y[j] = __uint_as_float(a[j]);
+                    z[j] = __uint_as_float(b[j]);
+                    if (kGated)
+                        y[j] = swiglu(y[j], z[j]);
+                }
+                if (p.row_weight) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float w = j < rows ? __ldg(p.row_weight + row + j) : 0.f;
+                        y[j] *= w;
+                        z[j] *= w;
                     }
                 }
+                store16<kOut>(p, row, rows, n0, lane, y);
+                if (!kGated)
+                    store16<kOut>(p, row, rows, n0 + kRowTile, lane, z);
             }
             tc::fence_before();
             __syncwarp();
@@ -523,6 +559,17 @@ bool make_map(CUtensorMap *map, const uint8_t *base, int64_t rows, int64_t row_b
     return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dims, strides, box, one,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kGated, int kOut>
+cudaError_t launch(const Params &p, const CUtensorMap &x_map, const CUtensorMap &w_map, int grid, size_t smem, cudaStream_t s)
+{
+    auto kernel = grouped_kernel<kGated, kOut>;
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess)
+        return err;
+    kernel<<<grid, kThreads, smem, s>>>(p, x_map, w_map);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -575,7 +622,8 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
     p.wide = (uintptr_t)scales % 8 == 0 && scale_row_bytes(K) % 8 == 0;
     p.w_wide = (uintptr_t)w_scales % 8 == 0 && scale_row_bytes(K) % 8 == 0;
     p.sm_tables = (int)mrr_ws::round_up(sizeof(Shared), 16);
-    p.sm_stage = (int)mrr_ws::round_up(p.sm_tables + 8 * (E + 1), 1024);
+    p.sm_scales = (int)mrr_ws::round_up(p.sm_tables + 8 * (E + 1), 16);
+    p.sm_stage = (int)mrr_ws::round_up(p.sm_scales + 2 * (2048 + 1024 * groups_of(p.tokens)), 1024);
     const int columns_left = (kColumns - p.sums * 2 * p.tokens) / (16 + 8 * groups_of(p.tokens));
     int stages = (smem_max - p.sm_stage) / stage_bytes(p.tokens);
     stages = stages < columns_left ? stages : columns_left;
@@ -587,11 +635,16 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
         !make_map(&x_map, A ? codes : w_codes, A ? A : 1, K / 2, kBoxRows))
         return MRR_ERR_CUDA;
     const size_t smem = (size_t)p.sm_stage + (size_t)p.stages * stage_bytes(p.tokens);
-    cudaError_t err = cudaFuncSetAttribute(grouped_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err == cudaSuccess) {
-        grouped_kernel<<<sms, kThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(p, x_map, w_map);
-        err = cudaGetLastError();
-    }
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t err;
+    if (out_dt == MOE_BF16)
+        err = gated ? launch<true, MOE_BF16>(p, x_map, w_map, sms, smem, st) : launch<false, MOE_BF16>(p, x_map, w_map, sms, smem, st);
+    else if (out_dt == MOE_F16)
+        err = gated ? launch<true, MOE_F16>(p, x_map, w_map, sms, smem, st) : launch<false, MOE_F16>(p, x_map, w_map, sms, smem, st);
+    else if (out_dt == MOE_F32)
+        err = gated ? launch<true, MOE_F32>(p, x_map, w_map, sms, smem, st) : launch<false, MOE_F32>(p, x_map, w_map, sms, smem, st);
+    else
+        err = gated ? launch<true, MOE_MXFP4>(p, x_map, w_map, sms, smem, st) : launch<false, MOE_MXFP4>(p, x_map, w_map, sms, smem, st);
     if (err != cudaSuccess) {
         (void)cudaGetLastError();
         return MRR_ERR_CUDA;

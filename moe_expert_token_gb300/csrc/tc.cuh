@@ -38,7 +38,17 @@ __device__ __forceinline__ void load16(uint32_t tmem, uint32_t (&v)[16])
 
 __device__ __forceinline__ void load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// arrive on `bar` once every earlier matrix instruction and copy of this thread is complete
+// 4 columns of this warp's 32 lanes
+__device__ __forceinline__ void store4(uint32_t tmem, const uint32_t (&v)[4])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tmem), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+
+__device__ __forceinline__ void store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// arrive on `bar` once every earlier matrix instruction of this thread is complete
 __device__ __forceinline__ void commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -53,19 +63,7 @@ __device__ __forceinline__ uint64_t desc_swizzle128(uint32_t smem)
            (uint64_t)2 << 61;
 }
 
-// 16-byte rows one after the other, no swizzle (scale factors)
-__device__ __forceinline__ uint64_t desc_rows16(uint32_t smem)
-{
-    return (uint64_t)((smem >> 4) & 0x3fffu) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
-}
-
 // ---------------------------------------------------------------- block-scaled matrix instructions
-
-// 32 rows of 16 bytes to 4 columns of lanes 0..31, repeated in the other three lane quarters
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc)
-{
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-}
 
 // Instruction descriptor for e2m1 x e2m1 with e8m0 scales, 128 rows, n columns, K = 64: `pair` (0 or
 // 1) picks which two of the four scale bytes in a column apply.
@@ -103,7 +101,5 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-
-__device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 }  // namespace tc
