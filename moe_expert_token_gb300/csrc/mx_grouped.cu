@@ -53,7 +53,8 @@ struct Params {
     uint32_t *status;
     int tokens;        // most token rows of a tile (64 or 192)
     int stages, sums;  // ring stages; sets of sums in tensor memory (1 or 2)
-    int wide, w_wide;  // scale rows are 8-byte aligned
+    int align, w_align;    // of scale rows: 16, 8 or 2 bytes
+    int out_wide;          // 16-bit rows can be written 8 bytes, MXFP4 rows 4 bytes at a time
     int sm_stage, sm_tables, sm_scales;
 };
 
@@ -196,27 +197,39 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *tables, int 
     return t;
 }
 
-// scale bytes of 8 blocks of row `row` from block b0; blocks at or past `blocks` read 0 (their codes
-// are zeros, and a scale of 2^-127 keeps them so)
-__device__ __forceinline__ uint2 scales8(const uint8_t *s, int64_t row, int64_t row_bytes, int b0, int blocks, bool wide)
+// Scale bytes of 32 blocks of row `row` from block b0, four steps' worth: a whole 32-byte sector
+// where rows are aligned to one (8 bytes a step would be fetched four times over).  align: 16, 8 or 2,
+// what rows and base are aligned to.  Blocks at or past `blocks` read 0: their codes are zeros, and a
+// scale of 2^-127 keeps them so.
+__device__ __forceinline__ void scales32(uint32_t (&v)[8], const uint8_t *s, int64_t row, int64_t row_bytes, int b0,
+                                         int blocks, int align)
 {
     const uint8_t *at = s + row * row_bytes + b0;
-    uint2 v = make_uint2(0, 0);
-    if (wide) {
-        v = __ldg(reinterpret_cast<const uint2 *>(at));
-    } else {
-        uint32_t h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)   // pairs are whole: a row holds ceil(K / 64) of them
-            h[i] = b0 + 2 * i < blocks ? __ldg(reinterpret_cast<const uint16_t *>(at) + i) : 0u;
-        v = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-    }
     const int left = blocks - b0;
-    if (left < 8) {
-        v.x &= left >= 4 ? kFull : (1u << (8 * left)) - 1u;
-        v.y &= left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u;
+    if (align == 16) {   // b0 is a multiple of 32 and rows of 16 bytes: what is loaded lies inside the row
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 q = 16 * i < left ? __ldg(reinterpret_cast<const uint4 *>(at) + i) : make_uint4(0, 0, 0, 0);
+            v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
+        }
+    } else if (align == 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint2 q = 8 * i < left ? __ldg(reinterpret_cast<const uint2 *>(at) + i) : make_uint2(0, 0);
+            v[2 * i] = q.x, v[2 * i + 1] = q.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {   // pairs are whole: a row holds ceil(K / 64) of them
+            const uint32_t lo = 4 * i < left ? __ldg(reinterpret_cast<const uint16_t *>(at) + 2 * i) : 0u;
+            const uint32_t hi = 4 * i + 2 < left ? __ldg(reinterpret_cast<const uint16_t *>(at) + 2 * i + 1) : 0u;
+            v[i] = lo | hi << 16;
+        }
     }
-    return v;
+    if (left < 32)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] &= left >= 4 * i + 4 ? kFull : left > 4 * i ? (1u << (8 * (left - 4 * i))) - 1u : 0u;
 }
 
 // true for every thread of the scale warps if `failed` is for any of them
@@ -234,7 +247,18 @@ __device__ __forceinline__ bool any_scale_warp(bool failed)
 // silu(g) u
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + expf(-g)) * u; }
 
+// Lanes l and l ^ o swap so that each keeps one of two token rows with both lanes' features: the lane
+// with bit o clear keeps `a` and gets the other's a, the other keeps `b` and gets b.
+__device__ __forceinline__ void trade(uint32_t a, uint32_t b, int o, int lane, uint32_t &mine, uint32_t &theirs)
+{
+    const bool high = lane & o;
+    theirs = __shfl_xor_sync(kFull, high ? a : b, o);
+    mine = high ? b : a;
+}
+
 // Results of 16 columns (token rows row .. row + rows - 1) of one output feature a lane: n0 + lane.
+// A warp's row is 32 features: lanes first trade rows for features, so that a store instruction
+// writes 4 rows of 8-byte pieces (16-bit results) or 8 rows of 4-byte pieces (codes).
 template <int kOut>
 __device__ __forceinline__ void store16(const Params &p, int64_t row, int rows, int n0, int lane, const float (&y)[16])
 {
@@ -242,23 +266,62 @@ __device__ __forceinline__ void store16(const Params &p, int64_t row, int rows, 
     if constexpr (kOut == MOE_MXFP4) {   // 32 lanes are one block; N is a multiple of 32
         if (n0 >= p.N)
             return;
-        uint8_t *q = static_cast<uint8_t *>(p.out) + row * (p.N / 2) + n / 2;
-        uint8_t *so = p.out_scales + row * scale_row_bytes(p.N) + n0 / 32;
-        const bool pad = n0 / 32 % 2 == 0 && n0 + 32 >= p.N;
+        uint32_t scale = 0u, v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             const uint32_t s = scale_byte(__reduce_max_sync(kFull, __float_as_uint(y[j]) & 0x7fffffffu));
-            const float v = y[j] * inverse_scale(s);
-            const uint32_t two = encode2(v, __shfl_down_sync(kFull, v, 1));   // of lanes 2 i, 2 i + 1
-            if (j < rows) {
-                if (lane % 2 == 0)
-                    q[(int64_t)j * (p.N / 2)] = (uint8_t)two;
-                if (lane == 0) {
-                    so[j * scale_row_bytes(p.N)] = (uint8_t)s;
-                    if (pad)
-                        so[j * scale_row_bytes(p.N) + 1] = 127;
+            v[j] = __float_as_uint(y[j] * inverse_scale(s));
+            scale = lane == j ? s : scale;
+        }
+        const int64_t srow = scale_row_bytes(p.N);
+        if (lane < rows) {
+            uint8_t *so = p.out_scales + (row + lane) * srow + n0 / 32;
+            so[0] = (uint8_t)scale;
+            if (n0 / 32 % 2 == 0 && n0 + 32 >= p.N)
+                so[1] = 127;
+        }
+        uint32_t b[8], s[4], w[2], mine, theirs;   // 2, 4 and 8 features of one row
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {   // row 2 j + bit 0 of the lane
+            trade(v[2 * j], v[2 * j + 1], 1, lane, mine, theirs);
+            const float a = __uint_as_float(mine), c = __uint_as_float(theirs);
+            b[j] = lane & 1 ? encode2(c, a) : encode2(a, c);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {   // row 4 j + the lane's low two bits
+            trade(b[2 * j], b[2 * j + 1], 2, lane, mine, theirs);
+            s[j] = lane & 2 ? theirs | mine << 8 : mine | theirs << 8;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {   // row 8 j + the lane's low three bits
+            trade(s[2 * j], s[2 * j + 1], 4, lane, mine, theirs);
+            w[j] = lane & 4 ? theirs | mine << 16 : mine | theirs << 16;
+            const int i = 8 * j + lane % 8;
+            uint8_t *q = static_cast<uint8_t *>(p.out) + (row + i) * (p.N / 2) + n0 / 2 + lane / 8 * 4;
+            if (i < rows) {
+                if (p.out_wide) {
+                    *reinterpret_cast<uint32_t *>(q) = w[j];
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        q[c] = (uint8_t)(w[j] >> (8 * c));
                 }
             }
+        }
+    } else if (kOut != MOE_F32 && p.out_wide) {   // N is a multiple of 4
+        uint32_t b[8], mine, theirs;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {   // row 2 j + bit 0 of the lane, 2 features
+            trade(__float_as_uint(y[2 * j]), __float_as_uint(y[2 * j + 1]), 1, lane, mine, theirs);
+            const float a = __uint_as_float(mine), c = __uint_as_float(theirs);
+            b[j] = lane & 1 ? pack2<kOut>(c, a) : pack2<kOut>(a, c);
+        }
+        uint16_t *q = static_cast<uint16_t *>(p.out) + (row + lane % 4) * p.N + n0 + lane / 4 * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {   // row 4 j + the lane's low two bits, 4 features
+            trade(b[2 * j], b[2 * j + 1], 2, lane, mine, theirs);
+            if (4 * j + lane % 4 < rows && n0 + lane / 4 * 4 < p.N)
+                *reinterpret_cast<uint2 *>(q + 4 * j * (int64_t)p.N) = lane & 2 ? make_uint2(theirs, mine) : make_uint2(mine, theirs);
         }
     } else {
         if (n >= p.N)
@@ -405,34 +468,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int blocks = p.K / 32;
         const int64_t row_bytes = scale_row_bytes(p.K), w_rows = (int64_t)p.E * mats * p.N;
         const int second = kGated ? p.N : kRowTile;
-        // two steps are loaded ahead of the one being stored
+        // the next four steps' bytes are loaded while these four are stored
         long long ahead = blockIdx.x;
         int ahead_k = 0;
         Tile t = tile_at(p, tables, features, ahead);
-        auto load = [&](uint2 (&v)[4]) {
+        auto load = [&](uint32_t (&v)[4][8]) {
             if (ahead >= total)
                 return;
             const int b0 = ahead_k * 8;
             const int64_t w_row = (int64_t)t.expert * mats * p.N + t.feature + r;
-            v[0] = w_row < w_rows ? scales8(p.w_scales, w_row, row_bytes, b0, blocks, p.w_wide) : make_uint2(0, 0);
-            v[1] = w_row + second < w_rows ? scales8(p.w_scales, w_row + second, row_bytes, b0, blocks, p.w_wide)
-                                           : make_uint2(0, 0);
-            v[2] = r < t.rows ? scales8(p.scales, (int64_t)t.row + r, row_bytes, b0, blocks, p.wide) : make_uint2(0, 0);
-            v[3] = r + 128 < t.rows ? scales8(p.scales, (int64_t)t.row + r + 128, row_bytes, b0, blocks, p.wide)
-                                    : make_uint2(0, 0);
-            if (++ahead_k == steps) {
+            const int64_t row[4] = {w_row, w_row + second, (int64_t)t.row + r, (int64_t)t.row + r + 128};
+            const bool in[4] = {w_row < w_rows, w_row + second < w_rows, r < t.rows, r + 128 < t.rows};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (in[q])
+                    scales32(v[q], q < 2 ? p.w_scales : p.scales, row[q], row_bytes, b0, blocks, q < 2 ? p.w_align : p.align);
+                else
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[q][i] = 0u;
+            }
+            ahead_k += 4;
+            if (ahead_k >= steps) {
                 ahead_k = 0;
                 ahead += gridDim.x;
                 if (ahead < total)
                     t = tile_at(p, tables, features, ahead);
             }
         };
-        uint2 v0[4] = {}, v1[4] = {}, v2[4] = {};
-        load(v0);
-        load(v1);
+        uint32_t now[4][8] = {}, next[4][8] = {};
+        load(next);
         int stage = 0;
-        uint32_t parity = 1u;
-        const long long mine = (total - blockIdx.x + gridDim.x - 1) / gridDim.x * steps;
+        uint32_t parity = 1u, buffer = 0u;
         // An atom is 128 rows by 4 blocks: row q's bytes are word q / 32 of 16-byte line q % 32, and in
         // tensor memory column q / 32 of lane q % 32, in each of the four lane quarters.  Atoms in
         // order: weights [tile][half of the step], tokens [half][group of 128 rows].
@@ -440,45 +507,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t to = (r % 32) * 16 + (r / 32) * 4;
         const uint32_t scale_columns = 16 + 8 * groups;
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + p.sums * 2 * p.tokens;
-        for (long long i = 0; i < mine; ++i) {
-            load(v2);
-            const uint32_t at = buffers + (i & 1) * buffer_size;
-            auto put = [&](uint32_t a, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); };
-            put(at + to, v0[0].x);
-            put(at + 512 + to, v0[0].y);
-            put(at + 1024 + to, v0[1].x);
-            put(at + 1536 + to, v0[1].y);
-            put(at + 2048 + to, v0[2].x);
-            put(at + 2048 + 512 * groups + to, v0[2].y);
-            if (groups == 2) {
-                put(at + 2048 + 512 + to, v0[3].x);
-                put(at + 2048 + 1536 + to, v0[3].y);
-            }
-            // the other buffer is free again once all four warps are here
-            if (any_scale_warp(!wait(sh, &sh->empty[stage], parity)))
-                break;
-            tc::fence_after();
-            const uint32_t columns = lanes + stage * scale_columns;
+        bool ok = true;
+        for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
+            for (int k = 0; ok && k < steps; k += 4) {
 #pragma unroll
-            for (int a = 0; a < 8; ++a)
-                if (a < 4 + 2 * groups) {
-                    uint32_t v[4];
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                                 : "r"(at + a * 512 + lane * 16)
-                                 : "memory");
-                    tc::store4(columns + 4 * a, v);
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        now[q][j] = next[q][j];
+                load(next);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (k + u >= steps)
+                        break;
+                    const uint32_t at = buffers + buffer * buffer_size;
+                    buffer ^= 1u;
+                    auto put = [&](uint32_t a, uint32_t v) {
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + a + to), "r"(v) : "memory");
+                    };
+                    put(0, now[0][2 * u]);
+                    put(512, now[0][2 * u + 1]);
+                    put(1024, now[1][2 * u]);
+                    put(1536, now[1][2 * u + 1]);
+                    put(2048, now[2][2 * u]);
+                    put(2048 + 512 * groups, now[2][2 * u + 1]);
+                    if (groups == 2) {
+                        put(2048 + 512, now[3][2 * u]);
+                        put(2048 + 1536, now[3][2 * u + 1]);
+                    }
+                    // the other buffer is free again once all four warps are here
+                    if (any_scale_warp(!wait(sh, &sh->empty[stage], parity))) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const uint32_t columns = lanes + stage * scale_columns;
+#pragma unroll
+                    for (int a = 0; a < 8; ++a)
+                        if (a < 4 + 2 * groups) {
+                            uint32_t v[4];
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                         : "r"(at + a * 512 + lane * 16)
+                                         : "memory");
+                            tc::store4(columns + 4 * a, v);
+                        }
+                    tc::store_wait();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(mrr::smem_addr(&sh->full[stage]));
+                    next_stage(stage, parity);
                 }
-            tc::store_wait();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0)
-                tc::mbar_arrive(mrr::smem_addr(&sh->full[stage]));
-            next_stage(stage, parity);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v0[j] = v1[j];
-                v1[j] = v2[j];
             }
         }
     } else if (warp >= kEpilogueWarp) {
@@ -619,8 +699,13 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
     // allows beside the scales (2 x 192 columns): a wide tile re-reads its weights less often.
     p.tokens = A <= 64 * E ? 64 : 192;
     p.sums = p.tokens <= 64 ? 2 : 1;
-    p.wide = (uintptr_t)scales % 8 == 0 && scale_row_bytes(K) % 8 == 0;
-    p.w_wide = (uintptr_t)w_scales % 8 == 0 && scale_row_bytes(K) % 8 == 0;
+    auto aligned = [K](const void *s) {
+        const uint64_t both = (uintptr_t)s | (uint64_t)scale_row_bytes(K);
+        return both % 16 == 0 ? 16 : both % 8 == 0 ? 8 : 2;
+    };
+    p.align = aligned(scales);
+    p.w_align = aligned(w_scales);
+    p.out_wide = out_dt == MOE_MXFP4 ? (uintptr_t)out % 4 == 0 : (uintptr_t)out % 8 == 0 && N % 4 == 0;
     p.sm_tables = (int)mrr_ws::round_up(sizeof(Shared), 16);
     p.sm_scales = (int)mrr_ws::round_up(p.sm_tables + 8 * (E + 1), 16);
     p.sm_stage = (int)mrr_ws::round_up(p.sm_scales + 2 * (2048 + 1024 * groups_of(p.tokens)), 1024);
