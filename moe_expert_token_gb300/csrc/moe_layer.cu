@@ -15,11 +15,10 @@ bool sizes_ok(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
            E <= MRR_GATE_MAX_EXPERTS && k >= 1 && k <= 64 && k <= E;
 }
 
-constexpr int kMaxParts = 16;    // most shares of H the logits are split into
 constexpr int kMaxGrid = 512;    // words of a flag set
 
 struct Layout {
-    size_t flags, part, xh, x_scale, h_max, h, bytes;
+    size_t flags, part, xh, route_expert, route_weight, x_scale, h_max, h, bytes;
     int Hp, Ip;
 };
 
@@ -34,9 +33,11 @@ Layout layout(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
     Layout l;
     l.Hp = (int)mrr_ws::round_up(H, 32);   // the products read whole groups of 32
     l.Ip = (int)mrr_ws::round_up(I, 16);   // and h is written 16 rows at a time
-    l.flags = take(2 * kMaxGrid * 8);
+    l.flags = take(3 * kMaxGrid * 8);
     l.part = take(kMaxParts * T * E * 4);
     l.xh = take(T * l.Hp * 2);
+    l.route_expert = take(T * k * 4);
+    l.route_weight = take(T * k * 4);
     l.x_scale = take(T * 4);
     l.h_max = take(T * 4);
     l.h = take(T * k * l.Ip * 4);
@@ -118,6 +119,8 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     p.tag = fresh_tag();
     p.part = reinterpret_cast<float *>(ws + l.part);
     p.xh = reinterpret_cast<uint16_t *>(ws + l.xh);
+    p.route_expert = reinterpret_cast<int *>(ws + l.route_expert);
+    p.route_weight = reinterpret_cast<float *>(ws + l.route_weight);
     p.x_scale = reinterpret_cast<float *>(ws + l.x_scale);
     p.h_max = reinterpret_cast<uint32_t *>(ws + l.h_max);
     p.h = ws + l.h;
@@ -137,7 +140,7 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     // shared memory: the rings (before them, the routing's scratch), the joins, the routing
     const int64_t n = T * k, active = n < E ? n : E;
     int64_t at = (int64_t)kWarps * kStages * stage_bytes(mx);
-    const int64_t scratch = kWarps * E * 4 + E * 2;
+    const int64_t scratch = kWarps * E * 4 > 2 * (E + n) ? kWarps * E * 4 : 2 * (E + n);
     at = at > scratch ? at : scratch;
     auto take = [&at](int64_t bytes) {
         const int64_t off = at;

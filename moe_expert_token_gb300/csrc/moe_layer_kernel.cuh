@@ -44,6 +44,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStages = 4;
 constexpr int kUpRow = 128, kDownRow = 256;      // bytes of a row in a stage: 32 rows x 128, 16 rows x 256
+constexpr int kMaxParts = 16;                    // most shares of H the logits are split into
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct Params {
@@ -56,10 +57,12 @@ struct Params {
     int *expert_idx;
     // workspace
     uint32_t *status;
-    unsigned long long *flags;    // [2][grid], see grid_wait
+    unsigned long long *flags;    // [3][grid], see grid_wait
     unsigned long long tag;
     float *part;                  // [kparts][T][E]
     uint16_t *xh;                 // [T][Hp]: x's rows as the products take them
+    int *route_expert;            // [T][k], with more than 8 tokens
+    float *route_weight;
     float *x_scale;               // [T]: what undoes their scaling
     uint32_t *h_max;              // [T]: float bits of the largest |h| of the token
     void *h;                      // [T k][Ip]
@@ -76,12 +79,12 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                                     uint32_t b1)
 {
     if (DT == MOE_BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                      "{%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                      "{%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -147,10 +150,10 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t (&d)[4])
 //
 // Block b writes the call's tag into its own word of `set` and waits until every block has.  The
 // words need no initial value: tags are 64 random-looking bits, different for each call.  For a
-// launch replayed from a graph, with the same tag: each block clears its word of set 1 before it
-// arrives at set 0, and its word of set 0 once it is through set 1, so no word holds the tag
-// before its block arrives.  The launch is cooperative (all blocks run at once); a wait that lasts
-// kWaitLimitNs all the same gives up and returns false.
+// launch replayed from a graph, with the same tag: each block clears its words of sets 1 and 2
+// before it arrives at set 0, and its word of set 0 once it is through set 1 (then all are through
+// set 0), so no word holds the tag before its block arrives.  The launch is cooperative (all blocks
+// run at once); a wait that lasts kWaitLimitNs all the same gives up and returns false.
 __device__ __forceinline__ bool grid_wait(const Params &p, int set, int *s_ok)
 {
     unsigned long long *f = p.flags + (size_t)set * gridDim.x;
@@ -210,9 +213,13 @@ __device__ void route(const Params &p, int t, uint32_t *key, uint16_t *expert, f
     const float *z = p.part + (int64_t)t * E;
     float mx = -INFINITY, sum = 0.f;
     for (int e = lane; e < E; e += 32) {
-        float v = 0.f;
-        for (int q = 0; q < p.kparts; ++q)
-            v += z[q * plane + e];
+        float part[kMaxParts], v = 0.f;   // all loads at once
+#pragma unroll
+        for (int q = 0; q < kMaxParts; ++q)
+            part[q] = q < p.kparts ? __ldcg(z + q * plane + e) : 0.f;
+#pragma unroll
+        for (int q = 0; q < kMaxParts; ++q)
+            v += part[q];
         key[e] = __float_as_uint(v);
         mx = fmaxf(mx, v);
     }
@@ -314,10 +321,14 @@ __device__ void route(const Params &p, int t, uint32_t *key, uint16_t *expert, f
 
 // ---------------------------------------------------------------- one warp's weight stream
 
-// What comes next in a warp's stream: first its units of the up items of this block, then those of
-// its down items.
+// Where a warp's stream of weight stages stands: first its units of this block's up items, then
+// those of its down items.  A unit is one stage: 32 rows x 128 bytes, or 16 rows x 256 bytes.
 struct Cursor {
-    int phase, item, unit;   // phase 2: the stream is over
+    int phase;                 // 0: up, 1: down, 2: over
+    int item, expert, chunk;   // expert: index among the active ones; chunk: along K
+    const uint8_t *src;        // this lane's first 16-byte piece of chunk 0
+    const uint8_t *scale_src;  // and its 8 scale bytes
+    uint32_t rows;             // bit j: the row of its piece j exists; bit 8: that of its scales
 };
 
 template <int DT, int WDT, int NT>
@@ -334,6 +345,7 @@ struct Layer {
     uint32_t ring;               // this warp's stages
     int warp, lane, g, t;
     int nact, up_items, up_units, up_tiles, down_items, down_units, down_chunks;
+    int64_t up_row, down_row;    // bytes of a weight row
     const uint16_t *act, *start, *cols;
 
     __device__ Layer(const Params &p_, uint8_t *sm) : p(p_), smem(sm)
@@ -357,59 +369,120 @@ struct Layer {
         down_items = (p.H + 15) / 16;
         down_chunks = (p.I + kDownK - 1) / kDownK;
         down_units = nact * down_chunks;
+        up_row = kMx ? p.H / 2 : 2 * (int64_t)p.H;
+        down_row = kMx ? p.I / 2 : 2 * (int64_t)p.I;
     }
 
-    // step to the first unit at or after c that exists
-    __device__ __forceinline__ void settle(Cursor &c) const
+    // point the cursor at the rows of its item and expert
+    __device__ __forceinline__ void aim(Cursor &c) const
     {
         if (c.phase == 0) {
-            if (c.item < up_items && c.unit >= up_units) {
-                c.unit = warp;
-                c.item = c.unit < up_units ? c.item + gridDim.x : up_items;
-            }
-            if (c.item >= up_items)
-                c = {1, (int)blockIdx.x, warp};
-        }
-        if (c.phase == 1) {
-            if (c.item < down_items && c.unit >= down_units) {
-                c.unit = warp;
-                c.item = c.unit < down_units ? c.item + gridDim.x : down_items;
-            }
-            if (c.item >= down_items)
-                c.phase = 2;
+            const int i0 = (c.item - c.expert * up_tiles) * 16, left = p.I - i0;
+            const int64_t row0 = (int64_t)act[c.expert] * 2 * p.I + i0;
+            c.src = static_cast<const uint8_t *>(p.w13) + (row0 + lane / 8) * up_row + lane % 8 * 16;
+            if (kMx)
+                c.scale_src = p.w13_s + (row0 + lane % 16 + (lane >= 16 ? p.I : 0)) * scale_row_bytes(p.H);
+            c.rows = lane % 16 < left ? 256u : 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                c.rows |= (4 * j + lane / 8) % 16 < left ? 1u << j : 0u;
+        } else if (c.phase == 1) {
+            const int n0 = c.item * 16, left = p.H - n0;
+            const int64_t row0 = (int64_t)act[c.expert] * p.H + n0;
+            c.src = static_cast<const uint8_t *>(p.w2) + (row0 + lane / 16) * down_row + lane % 16 * 16;
+            if (kMx)
+                c.scale_src = p.w2_s + (row0 + lane / 2) * scale_row_bytes(p.I) + lane % 2 * 8;
+            c.rows = lane / 2 < left ? 256u : 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                c.rows |= 2 * j + lane / 16 < left ? 1u << j : 0u;
         }
     }
 
-    // start the copies of unit c into stage `slot`: kRows rows of kRow bytes, 16-byte pieces
-    // exchanged inside a row so that the reads below meet no bank twice
-    template <int kRows, int kRow>
-    __device__ __forceinline__ void fill(int slot, const void *w, const uint8_t *s, int64_t row0, int64_t second, int valid,
-                                         int K, int chunk, bool wide, bool s_wide) const
+    __device__ __forceinline__ Cursor first_unit() const
     {
-        constexpr int kPieces = kRow / 16;
-        const int64_t row_bytes = kMx ? K / 2 : 2 * (int64_t)K;
-        const int c = lane % kPieces;
-        const int64_t off = (int64_t)chunk * kRow + c * 16;
+        Cursor c;
+        c.phase = 0;
+        c.item = blockIdx.x;
+        c.chunk = warp;
+        if (c.item >= up_items || warp >= up_units)
+            first_down(c);
+        else
+            c.expert = c.item / up_tiles;
+        aim(c);
+        return c;
+    }
+
+    __device__ __forceinline__ void first_down(Cursor &c) const
+    {
+        c.item = blockIdx.x;
+        c.phase = c.item < down_items && warp < down_units ? 1 : 2;
+        c.expert = warp / down_chunks;
+        c.chunk = warp - c.expert * down_chunks;
+    }
+
+    __device__ __forceinline__ void advance(Cursor &c) const
+    {
+        c.chunk += kWarps;
+        if (c.phase == 0) {
+            if (c.chunk < up_units)
+                return;
+            c.chunk = warp;
+            c.item += gridDim.x;
+            if (c.item >= up_items)
+                first_down(c);
+            else
+                c.expert = c.item / up_tiles;
+            aim(c);
+        } else if (c.phase == 1) {
+            if (c.chunk < down_chunks)
+                return;
+            do {
+                c.chunk -= down_chunks;
+                ++c.expert;
+            } while (c.chunk >= down_chunks);
+            if (c.expert >= nact) {
+                c.item += gridDim.x;
+                if (c.item >= down_items)
+                    c.phase = 2;
+                c.expert = warp / down_chunks;
+                c.chunk = warp - c.expert * down_chunks;
+            }
+            aim(c);
+        }
+    }
+
+    // start the copies of the cursor's unit into stage `slot`, 16-byte pieces exchanged inside a row
+    // so that the reads in multiply() meet no bank twice
+    template <bool kUp>
+    __device__ __forceinline__ void fill(int slot, const Cursor &c) const
+    {
+        constexpr int kRow = kUp ? kUpRow : kDownRow, kPieces = kRow / 16, kStep = 32 / kPieces;
+        const bool wide = kUp ? p.w13_wide : p.w2_wide, s_wide = kUp ? p.s13_wide : p.s2_wide;
+        const uint8_t *none = static_cast<const uint8_t *>(kUp ? p.w13 : p.w2);
+        const int64_t row_bytes = kUp ? up_row : down_row, at = (int64_t)c.chunk * kRow;
+        const int piece = lane % kPieces;
+        const int64_t left = row_bytes - at - piece * 16;   // bytes of the row from this lane's piece on
         const uint32_t base = ring + slot * kStage;
+        const uint32_t rows = left > 0 ? c.rows : 0u;
+        const uint8_t *src = c.src + at;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int r = j * (32 / kPieces) + lane / kPieces;
-            const bool ok = (r & 15) < valid && off < row_bytes;
-            const int64_t row = row0 + (r & 15) + (kRows == 32 && r >= 16 ? second : 0);
-            const uint32_t dst = base + r * kRow + ((kMx ? c ^ (r & 7) : c ^ ((r & 1) << 2)) << 4);
-            const uint8_t *src = static_cast<const uint8_t *>(w) + row * row_bytes + off;
+            const int r = j * kStep + lane / kPieces;
+            const uint32_t dst = base + r * kRow + ((kMx ? piece ^ (r & 7) : piece ^ ((r & 1) << 2)) << 4);
+            const bool ok = rows >> j & 1u;
             if (wide) {
-                copy16(dst, ok ? src : static_cast<const uint8_t *>(w), ok);
+                copy16(dst, ok ? src : none, ok);
             } else {
                 uint32_t v[4] = {0u, 0u, 0u, 0u};
                 if (ok) {
                     if (kMx) {
                         for (int b = 0; b < 16; ++b)
-                            if (off + b < row_bytes)
+                            if (b < left)
                                 v[b / 4] |= (uint32_t)__ldg(src + b) << (8 * (b % 4));
                     } else {
                         for (int b = 0; b < 8; ++b)
-                            if (off + 2 * b < row_bytes)
+                            if (2 * b < left)
                                 v[b / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(src) + b) << (16 * (b % 2));
                     }
                 }
@@ -417,23 +490,24 @@ struct Layer {
                              "r"(v[3])
                              : "memory");
             }
+            src += kStep * row_bytes;
+            if (kUp && j == 3)   // from the 16 gate rows to the up rows
+                src += (p.I - 16) * row_bytes;
         }
         if (kMx) {   // 8 scale bytes a lane: row lane (32 rows of 8), or row lane / 2 (16 rows of 16)
-            constexpr int kLanes = 32 / kRows;
-            const int r = lane / kLanes;
-            const int64_t srow = scale_row_bytes(K), soff = (int64_t)chunk * (8 * kLanes) + (lane % kLanes) * 8;
-            const bool ok = (r & 15) < valid && soff < srow;
-            const int64_t row = row0 + (r & 15) + (kRows == 32 && r >= 16 ? second : 0);
+            const int64_t s_at = (int64_t)c.chunk * (kUp ? 8 : 16);
+            const int64_t s_left = scale_row_bytes(kUp ? p.H : p.I) - s_at - (kUp ? 0 : lane % 2 * 8);
+            const bool ok = s_left > 0 && c.rows >> 8;
             const uint32_t dst = base + 4096 + lane * 8;
-            const uint8_t *src = s + row * srow + soff;
+            const uint8_t *s = c.scale_src + s_at;
             if (s_wide) {
-                copy8(dst, ok ? src : s, ok);
+                copy8(dst, ok ? s : none, ok);
             } else {
                 uint32_t v[2] = {0u, 0u};
                 if (ok)
                     for (int b = 0; b < 8; ++b)
-                        if (soff + b < srow)
-                            v[b / 4] |= (uint32_t)__ldg(src + b) << (8 * (b % 4));
+                        if (b < s_left)
+                            v[b / 4] |= (uint32_t)__ldg(s + b) << (8 * (b % 4));
                 asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(v[0]), "r"(v[1]) : "memory");
             }
         }
@@ -441,64 +515,49 @@ struct Layer {
 
     __device__ __forceinline__ void issue(Cursor &c, int slot) const
     {
-        if (c.phase == 0) {
-            const int ai = c.item / up_tiles, i0 = (c.item - ai * up_tiles) * 16;
-            fill<32, kUpRow>(slot, p.w13, p.w13_s, (int64_t)act[ai] * 2 * p.I + i0, p.I, min(16, p.I - i0), p.H, c.unit,
-                             p.w13_wide, p.s13_wide);
-        } else if (c.phase == 1) {
-            const int ai = c.unit / down_chunks, n0 = c.item * 16;
-            fill<16, kDownRow>(slot, p.w2, p.w2_s, (int64_t)act[ai] * p.H + n0, 0, min(16, p.H - n0), p.I,
-                               c.unit - ai * down_chunks, p.w2_wide, p.s2_wide);
-        }
+        if (c.phase == 0)
+            fill<true>(slot, c);
+        else if (c.phase == 1)
+            fill<false>(slot, c);
         copy_commit();
-        if (c.phase < 2) {
-            c.unit += kWarps;
-            settle(c);
-        }
+        if (c.phase < 2)
+            advance(c);
     }
 
-    __device__ __forceinline__ uint4 lds16(uint32_t at) const
+    template <typename V>
+    __device__ __forceinline__ V stage_word(int slot, int at) const
     {
-        uint4 v;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-        return v;
+        return *reinterpret_cast<const V *>(smem + (warp * kStages + slot) * kStage + at);
     }
 
-    __device__ __forceinline__ uint32_t lds4(uint32_t at) const
-    {
-        uint32_t v;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
-        return v;
-    }
+    // Token operands of kGroups groups of 32 k for kCols column tiles: this lane's 8 elements of each.
+    static constexpr int kCols = NT == 1 ? 1 : 2;
+    template <int kGroups>
+    struct Tokens {
+        uint4 v[kCols][kGroups];
+    };
+    static constexpr int kUpGroups = kMx ? 8 : 2;      // of one stage
+    static constexpr int kDownGroups = kMx ? 8 : 4;    // of a stage, or (kMx) of half of one
+    static constexpr int kDownHalves = kMx ? 2 : 1;
 
-    __device__ __forceinline__ uint2 lds8(uint32_t at) const
+    // The products of groups q0 .. q0 + kGroups - 1 (k0: the first one's k) of a stage: kTiles 16-row
+    // tiles against column tiles j0 .. j0 + kCols - 1, of which nt exist in all.
+    template <int kTiles, int kRow, int kGroups, int kAcc>
+    __device__ __forceinline__ void multiply(int slot, int q0, int k0, int K, int j0, int nt, const Tokens<kGroups> &b,
+                                             float (&acc)[kTiles][kAcc][4]) const
     {
-        uint2 v;
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
-        return v;
-    }
-
-    // The products of one stage: kTiles 16-row tiles against nt column tiles, groups of 32 k.
-    // column(j, k): the 8 elements k .. k + 7 of this lane's column in tile j, packed.
-    template <int kTiles, int kRow, typename Column>
-    __device__ __forceinline__ void multiply(int slot, int K, int chunk, int nt, float (&acc)[kTiles][NT][4],
-                                             Column column) const
-    {
-        constexpr int kGroups = kMx ? kRow / 16 : kRow / 64;
-        const uint32_t base = ring + slot * kStage;
-        const int k0 = chunk * kGroups * 32;
-        uint2 sc[kMx ? kTiles : 1][2];   // scale bytes of rows g and g + 8, 8 groups at a time
+        uint2 sc[kMx ? kTiles : 1][2];   // scale bytes of rows g and g + 8
+        if (kMx)
 #pragma unroll
-        for (int q = 0; q < kGroups; ++q) {
-            const int k = k0 + 32 * q;
-            if (k >= K)
+            for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    sc[m][r] = stage_word<uint2>(slot, 4096 + (16 * m + 8 * r + g) * (kRow / 16) + q0);
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            if (k0 + 32 * i >= K)
                 break;
-            if (kMx && q % 8 == 0)
-#pragma unroll
-                for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        sc[m][r] = lds8(base + 4096 + (16 * m + 8 * r + g) * (kRow / 16) + q);
+            const int q = q0 + i;
             uint32_t a[kTiles][2][4];
 #pragma unroll
             for (int m = 0; m < kTiles; ++m)
@@ -506,36 +565,55 @@ struct Layer {
                 for (int r = 0; r < 2; ++r) {
                     const int row = 16 * m + 8 * r + g;
                     if (kMx) {
-                        codes_to_half(lds4(base + row * kRow + ((q ^ (row & 7)) << 4) + 4 * t), a[m][r]);
+                        codes_to_half(stage_word<uint32_t>(slot, row * kRow + ((q ^ (row & 7)) << 4) + 4 * t), a[m][r]);
                     } else {
-                        const uint4 v = lds16(base + row * kRow + (((4 * q + t) ^ ((row & 1) << 2)) << 4));
+                        const uint4 v = stage_word<uint4>(slot, row * kRow + (((4 * q + t) ^ ((row & 1) << 2)) << 4));
                         a[m][r][0] = v.x, a[m][r][1] = v.y, a[m][r][2] = v.z, a[m][r][3] = v.w;
                     }
                 }
+            float s[kTiles][2];
+            if (kMx)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                if (j >= nt)
+                for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        s[m][r] = e8m0_value((i < 4 ? sc[m][r].x : sc[m][r].y) >> (8 * (i % 4)) & 255u);
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) {
+                if (j0 + j >= nt)
                     break;
-                const uint4 b = column(j, k + 8 * t);
+                const uint4 x = b.v[j][i];
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m) {
+                    float(&to)[4] = acc[m][j0 + j];
                     if (kMx) {
                         float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma<MDT>(d, a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], b.x, b.y);
-                        mma<MDT>(d, a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], b.z, b.w);
-                        const float s0 = e8m0_value((q % 8 < 4 ? sc[m][0].x : sc[m][0].y) >> (8 * (q % 4)) & 255u);
-                        const float s1 = e8m0_value((q % 8 < 4 ? sc[m][1].x : sc[m][1].y) >> (8 * (q % 4)) & 255u);
-                        acc[m][j][0] = fmaf(s0, d[0], acc[m][j][0]);
-                        acc[m][j][1] = fmaf(s0, d[1], acc[m][j][1]);
-                        acc[m][j][2] = fmaf(s1, d[2], acc[m][j][2]);
-                        acc[m][j][3] = fmaf(s1, d[3], acc[m][j][3]);
+                        mma<MDT>(d, a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], x.x, x.y);
+                        mma<MDT>(d, a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], x.z, x.w);
+                        to[0] = fmaf(s[m][0], d[0], to[0]);
+                        to[1] = fmaf(s[m][0], d[1], to[1]);
+                        to[2] = fmaf(s[m][1], d[2], to[2]);
+                        to[3] = fmaf(s[m][1], d[3], to[3]);
                     } else {
-                        mma<MDT>(acc[m][j], a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], b.x, b.y);
-                        mma<MDT>(acc[m][j], a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], b.z, b.w);
+                        mma<MDT>(to, a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], x.x, x.y);
+                        mma<MDT>(to, a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], x.z, x.w);
                     }
                 }
             }
         }
+    }
+
+    // fetch token operands from k0 on; column(j, k): the 8 elements k .. k + 7 of this lane's column of tile j
+    template <int kGroups, typename Column>
+    __device__ __forceinline__ void fetch(Tokens<kGroups> &b, int j0, int nt, int k0, int K, Column column) const
+    {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+            if (j0 + j < nt)
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i)
+                    if (k0 + 32 * i < K)
+                        b.v[j][i] = column(j0 + j, k0 + 32 * i + 8 * t);
     }
 
     // assignment of column c of active expert ai, or -1.  Up to 8 tokens: column = token.
@@ -676,38 +754,74 @@ struct Layer {
 
     // ------------------------------------------------------------ between the waits: who goes where
 
-    // expert and weight of every assignment, the active experts in order, and their columns
-    __device__ int routing()
+    // Expert and weight of every assignment.  Up to 8 tokens every block finds them for itself, a
+    // token a warp; with more, each token is one block's, and the blocks wait for one another.
+    __device__ bool assign(uint16_t *expert, float *weight, int *s_ok)
     {
-        uint16_t *expert = reinterpret_cast<uint16_t *>(smem + p.sm_expert);
-        float *weight = reinterpret_cast<float *>(smem + p.sm_weight);
-        uint16_t *act_ = reinterpret_cast<uint16_t *>(smem + p.sm_act);
-        uint16_t *start_ = reinterpret_cast<uint16_t *>(smem + p.sm_start);
-        uint16_t *cols_ = reinterpret_cast<uint16_t *>(smem + p.sm_cols);
-        int *s_nact = reinterpret_cast<int *>(smem + p.sm_count);
         uint32_t *key = reinterpret_cast<uint32_t *>(smem) + warp * p.E;   // the ring is not in use yet
-        uint16_t *count = reinterpret_cast<uint16_t *>(smem + kWarps * p.E * 4);
-        for (int tok = warp; tok < p.T; tok += kWarps) {
-            __syncwarp();
-            route<DT>(p, tok, key, expert + tok * p.k, weight + tok * p.k);
+        if (NT == 1) {
+            if (warp < p.T)
+                route<DT>(p, warp, key, expert + warp * p.k, weight + warp * p.k);
+            __syncthreads();
+        } else {
+            for (int tok = blockIdx.x; tok < p.T; tok += gridDim.x) {
+                if (warp == 0) {
+                    route<DT>(p, tok, key, expert, weight);
+                    for (int i = lane; i < p.k; i += 32) {
+                        p.route_expert[tok * p.k + i] = expert[i];
+                        p.route_weight[tok * p.k + i] = weight[i];
+                    }
+                }
+                __syncthreads();
+            }
+            if (!grid_wait(p, 1, s_ok))
+                return false;
+            for (int a = threadIdx.x; a < p.T * p.k; a += kThreads) {
+                expert[a] = (uint16_t)__ldcg(p.route_expert + a);
+                weight[a] = __ldcg(p.route_weight + a);
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        const int n = p.T * p.k;
         if (blockIdx.x == 0)
-            for (int a = threadIdx.x; a < n; a += kThreads) {
+            for (int a = threadIdx.x; a < p.T * p.k; a += kThreads) {
                 if (p.topk_weight)
                     p.topk_weight[a] = weight[a];
                 if (p.expert_idx)
                     p.expert_idx[a] = expert[a];
             }
-        for (int e = threadIdx.x; e < p.E; e += kThreads) {
-            int c = 0;
-            for (int a = 0; a < n; ++a)
-                c += expert[a] == e;
-            count[e] = (uint16_t)c;
-        }
+        return true;
+    }
+
+    // the active experts in order, and their columns; returns how many
+    __device__ int columns(const uint16_t *expert)
+    {
+        uint16_t *act_ = reinterpret_cast<uint16_t *>(smem + p.sm_act);
+        uint16_t *start_ = reinterpret_cast<uint16_t *>(smem + p.sm_start);
+        uint16_t *cols_ = reinterpret_cast<uint16_t *>(smem + p.sm_cols);
+        int *s_nact = reinterpret_cast<int *>(smem + p.sm_count);
+        // in the ring, which is not in use yet: assignments of each expert, then its place among the
+        // active ones; an assignment's place among its expert's
+        uint16_t *count = reinterpret_cast<uint16_t *>(smem), *place = count + p.E;
+        const int n = p.T * p.k;
+        for (int e = threadIdx.x; e < p.E; e += kThreads)
+            count[e] = 0;
+        if (NT == 1)
+            for (int i = threadIdx.x; i < min(n, p.E) * 8; i += kThreads)
+                cols_[i] = 0xffffu;
         __syncthreads();
         if (warp == 0) {
+            for (int a0 = 0; a0 < n; a0 += 32) {   // in order: an expert's columns are in token order
+                const int a = a0 + lane, e = a < n ? expert[a] : -1;
+                const uint32_t same = __match_any_sync(kFull, e);
+                const int rank = __popc(same & ((1u << lane) - 1u));
+                if (a < n) {
+                    place[a] = (uint16_t)(count[e] + rank);
+                    __syncwarp(__activemask());
+                    if (rank == 0)
+                        count[e] = (uint16_t)(count[e] + __popc(same));
+                }
+                __syncwarp();
+            }
             int active = 0, at = 0;
             for (int e0 = 0; e0 < p.E; e0 += 32) {
                 const int e = e0 + lane, c = e < p.E ? count[e] : 0;
@@ -722,6 +836,7 @@ struct Layer {
                     const int i = active + __popc(some & ((1u << lane) - 1u));
                     act_[i] = (uint16_t)e;
                     start_[i] = (uint16_t)(at + before - c);
+                    count[e] = (uint16_t)i;
                 }
                 at += __shfl_sync(kFull, before, 31);
                 active += __popc(some);
@@ -732,23 +847,15 @@ struct Layer {
             }
         }
         __syncthreads();
-        const int active = *s_nact;
-        for (int i = threadIdx.x; i < active; i += kThreads) {
-            const int e = act_[i];
-            int at = start_[i];
+        for (int a = threadIdx.x; a < n; a += kThreads) {
+            const int i = count[expert[a]];
             if (NT == 1)
-                for (int c = 0; c < 8; ++c)
-                    cols_[i * 8 + c] = 0xffffu;
-            for (int a = 0; a < n; ++a)
-                if (expert[a] == e) {
-                    if (NT == 1)
-                        cols_[i * 8 + a / p.k] = (uint16_t)a;
-                    else
-                        cols_[at++] = (uint16_t)a;
-                }
+                cols_[i * 8 + a / p.k] = (uint16_t)a;
+            else
+                cols_[start_[i] + place[a]] = (uint16_t)a;
         }
         __syncthreads();
-        return active;
+        return *s_nact;
     }
 
     // ------------------------------------------------------------ the two products
@@ -756,8 +863,8 @@ struct Layer {
     __device__ void run()
     {
         int *s_ok = reinterpret_cast<int *>(smem + p.sm_count) + 1;
-        if (threadIdx.x == 0)
-            p.flags[gridDim.x + blockIdx.x] = 0;
+        if (threadIdx.x < 2)
+            p.flags[(1 + threadIdx.x) * gridDim.x + blockIdx.x] = 0;
         if (blockIdx.x == 0 && threadIdx.x < 2)
             p.status[threadIdx.x] = 0;
         for (int tok = gridDim.x - 1 - blockIdx.x; tok < p.T; tok += gridDim.x)
@@ -769,11 +876,16 @@ struct Layer {
                 atomicOr(p.status, mrr_ws::kFlagTimeout);
             return;
         }
-        sizes(routing());
-        const float *weight = reinterpret_cast<const float *>(smem + p.sm_weight);
+        float *weight = reinterpret_cast<float *>(smem + p.sm_weight);
+        uint16_t *expert = reinterpret_cast<uint16_t *>(smem + p.sm_expert);
+        if (!assign(expert, weight, s_ok)) {
+            if (threadIdx.x == 0)
+                atomicOr(p.status, mrr_ws::kFlagTimeout);
+            return;
+        }
+        sizes(columns(expert));
 
-        Cursor next = {0, (int)blockIdx.x, warp};
-        settle(next);
+        Cursor next = first_unit();
         int slot = 0, fill_slot = 0;
         auto issue_next = [&]() {
             issue(next, fill_slot);
@@ -800,11 +912,25 @@ struct Layer {
                 const int a = j < nt ? column_of(ai, 8 * j + g) : -1;
                 row[j] = a < 0 ? nullptr : p.xh + (int64_t)(a / p.k) * p.Hp;
             }
+            auto column = [&](int j, int k) {
+                return row[j] ? *reinterpret_cast<const uint4 *>(row[j] + k) : make_uint4(0, 0, 0, 0);
+            };
             float acc[2][NT][4] = {};
-            for (int u = warp; u < up_units; u += kWarps)
-                multiply<2, kUpRow>(take(), p.H, u, nt, acc, [&](int j, int k) {
-                    return row[j] ? *reinterpret_cast<const uint4 *>(row[j] + k) : make_uint4(0, 0, 0, 0);
-                });
+            Tokens<kUpGroups> ahead;   // the next unit's, fetched while this one's are multiplied
+            fetch(ahead, 0, nt, warp * kUpK, p.H, column);
+            for (int u = warp; u < up_units; u += kWarps) {
+                const int at = take();
+                Tokens<kUpGroups> b = ahead;
+                fetch(ahead, 0, nt, (u + kWarps) * kUpK, p.H, column);
+#pragma unroll
+                for (int j = 0; j < NT; j += kCols) {
+                    if (j >= nt)
+                        break;
+                    if (j > 0)
+                        fetch(b, j, nt, u * kUpK, p.H, column);
+                    multiply<2, kUpRow>(at, 0, u * kUpK, p.H, j, nt, b, acc);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 if (j >= nt)
@@ -833,7 +959,7 @@ struct Layer {
                 buf ^= 1;
             }
         }
-        if (!grid_wait(p, 1, s_ok)) {
+        if (!grid_wait(p, 2, s_ok)) {
             copy_wait<0>();
             if (threadIdx.x == 0)
                 atomicOr(p.status, mrr_ws::kFlagTimeout);
@@ -847,11 +973,31 @@ struct Layer {
         if (NT == 1) {
             const float scale = g < p.T ? h_scale(g).x : 1.f;
             for (int item = blockIdx.x; item < down_items; item += gridDim.x) {
-                float acc[1][NT][4] = {};
+                float acc[1][1][4] = {};
+                int e = warp / down_chunks, chunk = warp - e * down_chunks;   // of `ahead`
+                int a = e < nact ? column_of(e, g) : -1;
+                auto column = [&](int, int k) { return h8(a, k, scale); };
+                Tokens<kDownGroups> ahead;
+                fetch(ahead, 0, e < nact, chunk * kDownK, p.I, column);
                 for (int u = warp; u < down_units; u += kWarps) {
-                    const int ai = u / down_chunks, a = column_of(ai, g);
-                    multiply<1, kDownRow>(take(), p.I, u - ai * down_chunks, 1, acc,
-                                          [&](int, int k) { return h8(a, k, scale); });
+                    const int at = take(), k0 = chunk * kDownK;
+                    Tokens<kDownGroups> b = ahead;
+                    if (kDownHalves == 2) {
+                        fetch(ahead, 0, 1, k0 + kDownK / 2, p.I, column);
+                        multiply<1, kDownRow>(at, 0, k0, p.I, 0, 1, b, acc);
+                        b = ahead;
+                    }
+                    chunk += kWarps;
+                    if (chunk >= down_chunks) {
+                        do {
+                            chunk -= down_chunks;
+                            ++e;
+                        } while (chunk >= down_chunks);
+                        a = e < nact ? column_of(e, g) : -1;
+                    }
+                    fetch(ahead, 0, e < nact, chunk * kDownK, p.I, column);
+                    multiply<1, kDownRow>(at, kDownHalves == 2 ? kDownGroups : 0, k0 + (kDownHalves - 1) * (kDownK / 2),
+                                          p.I, 0, 1, b, acc);
                 }
                 put(red(buf), 0, acc[0][0]);
                 __syncthreads();
@@ -870,18 +1016,47 @@ struct Layer {
                 for (int i = lane; i < p.T * kPitch; i += 32)
                     mine[i] = 0.f;
                 __syncwarp();
-                for (int u = warp; u < down_units; u += kWarps) {
-                    const int ai = u / down_chunks, nt = tiles_of(ai);
-                    int a[NT];
-                    float scale[NT];
+                int e = warp / down_chunks, chunk = warp - e * down_chunks;   // of `ahead`
+                int a[NT];
+                float scale[NT];
+                auto enter = [&]() {   // the columns of expert e
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        a[j] = j < nt ? column_of(ai, 8 * j + g) : -1;
+                        a[j] = e < nact && j < tiles_of(e) ? column_of(e, 8 * j + g) : -1;
                         scale[j] = kScaled && a[j] >= 0 ? h_scale(a[j] / p.k).x : 1.f;
                     }
+                };
+                auto column = [&](int j, int k) { return h8(a[j], k, scale[j]); };
+                enter();
+                Tokens<kDownGroups> ahead;
+                fetch(ahead, 0, e < nact ? tiles_of(e) : 0, chunk * kDownK, p.I, column);
+                for (int u = warp; u < down_units; u += kWarps) {
+                    const int at = take(), k0 = chunk * kDownK, nt = tiles_of(e), ai = e;
                     float acc[1][NT][4] = {};
-                    multiply<1, kDownRow>(take(), p.I, u - ai * down_chunks, nt, acc,
-                                          [&](int j, int k) { return h8(a[j], k, scale[j]); });
+                    Tokens<kDownGroups> b = ahead;
+#pragma unroll
+                    for (int half = 0; half < kDownHalves; ++half) {
+                        const int kh = k0 + half * (kDownK / 2);
+                        if (half > 0)
+                            fetch(b, 0, nt, kh, p.I, column);
+#pragma unroll
+                        for (int j = 0; j < NT; j += kCols) {
+                            if (j >= nt)
+                                break;
+                            if (j > 0)
+                                fetch(b, j, nt, kh, p.I, column);
+                            multiply<1, kDownRow>(at, half * kDownGroups, kh, p.I, j, nt, b, acc);
+                        }
+                    }
+                    chunk += kWarps;
+                    if (chunk >= down_chunks) {
+                        do {
+                            chunk -= down_chunks;
+                            ++e;
+                        } while (chunk >= down_chunks);
+                        enter();
+                    }
+                    fetch(ahead, 0, e < nact ? tiles_of(e) : 0, chunk * kDownK, p.I, column);
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         if (j >= nt)
@@ -890,9 +1065,9 @@ struct Layer {
                         for (int c = 0; c < 2; ++c) {
                             const int q = column_of(ai, 8 * j + 2 * t + c);
                             if (q >= 0) {
-                                float *at = mine + (q / p.k) * kPitch + g;
-                                at[0] += acc[0][j][c];
-                                at[8] += acc[0][j][2 + c];
+                                float *to = mine + (q / p.k) * kPitch + g;
+                                to[0] += acc[0][j][c];
+                                to[8] += acc[0][j][2 + c];
                             }
                         }
                     }
