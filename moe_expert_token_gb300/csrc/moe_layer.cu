@@ -18,7 +18,7 @@ bool sizes_ok(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
 constexpr int kMaxGrid = 512;    // words of a flag set
 
 struct Layout {
-    size_t flags, part, xh, route_expert, route_weight, x_scale, h_max, h, bytes;
+    size_t flags, part, xh, route_expert, route_weight, x_scale, h_max, h, h_field, bytes;
     int Hp, Ip;
 };
 
@@ -40,7 +40,8 @@ Layout layout(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
     l.route_weight = take(T * k * 4);
     l.x_scale = take(T * 4);
     l.h_max = take(T * 4);
-    l.h = take(T * k * l.Ip * 4);
+    l.h = take(T * k * l.Ip * 2);
+    l.h_field = take(T * k * (l.Ip / 16));
     l.bytes = at;
     return l;
 }
@@ -123,7 +124,8 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     p.route_weight = reinterpret_cast<float *>(ws + l.route_weight);
     p.x_scale = reinterpret_cast<float *>(ws + l.x_scale);
     p.h_max = reinterpret_cast<uint32_t *>(ws + l.h_max);
-    p.h = ws + l.h;
+    p.h = reinterpret_cast<uint16_t *>(ws + l.h);
+    p.h_field = ws + l.h_field;
     p.Hp = l.Hp, p.Ip = l.Ip;
     // the router's 16-expert tiles, split over H until the blocks have one each
     const int64_t tiles = (E + 15) / 16, chunks = (H + 127) / 128;
@@ -140,7 +142,8 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     // shared memory: the rings (before them, the routing's scratch), the joins, the routing
     const int64_t n = T * k, active = n < E ? n : E;
     int64_t at = (int64_t)kWarps * kStages * stage_bytes(mx);
-    const int64_t scratch = kWarps * E * 4 > 2 * (E + n) ? kWarps * E * 4 : 2 * (E + n);
+    const int64_t keys = ((T > 8 ? 1 : T) * 2 * E + E) * 4, places = 2 * (E + n);
+    const int64_t scratch = keys > places ? keys : places;
     at = at > scratch ? at : scratch;
     auto take = [&at](int64_t bytes) {
         const int64_t off = at;
@@ -154,6 +157,7 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     p.sm_act = take(active * 2);
     p.sm_start = take((active + 1) * 2);
     p.sm_cols = take(T > 8 ? n * 2 : active * 16);
+    p.sm_tokens = T > 8 ? take(n) : 0;
     p.sm_count = take(16);
     if (at > smem_max)
         return MRR_ERR_CUDA;

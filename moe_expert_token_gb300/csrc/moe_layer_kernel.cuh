@@ -65,11 +65,12 @@ struct Params {
     float *route_weight;
     float *x_scale;               // [T]: what undoes their scaling
     uint32_t *h_max;              // [T]: float bits of the largest |h| of the token
-    void *h;                      // [T k][Ip]
+    uint16_t *h;                  // [T k][Ip]
+    uint8_t *h_field;             // [T k][Ip / 16]: exponent of the power of two each tile of h carries (float16)
     int Hp, Ip, kparts;
     int x_wide, wr_wide, w13_wide, w2_wide, s13_wide, s2_wide;   // 16-byte (scales: 8-byte) copies possible
     // dynamic shared memory, byte offsets
-    int sm_red, sm_y, sm_expert, sm_weight, sm_act, sm_start, sm_cols, sm_count;
+    int sm_red, sm_y, sm_expert, sm_weight, sm_act, sm_start, sm_cols, sm_tokens, sm_count;
 };
 
 __host__ __device__ constexpr int stage_bytes(bool mx) { return 4096 + (mx ? 256 : 0); }
@@ -109,16 +110,15 @@ __device__ __forceinline__ void copy_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// the power of two that takes the float with bits `amax` into [2^14, 2^15), so that it and all
-// smaller ones fit float16 (1 where amax is 0, infinite or NaN), and its inverse
-__device__ __forceinline__ float2 f16_scale(uint32_t amax)
+// The power of two that takes the float with bits `amax` into [2^14, 2^15), so that it and all
+// smaller ones fit float16: its exponent field.  1 for an infinite or NaN amax; the largest for 0.
+__device__ __forceinline__ uint32_t f16_scale_field(uint32_t amax)
 {
     const int field = (int)(amax >> 23);
-    if (amax == 0u || field == 255)
-        return make_float2(1.f, 1.f);
-    const int f = min(268 - field, 253);   // field <= 254: f >= 14
-    return make_float2(__uint_as_float((uint32_t)f << 23), __uint_as_float((uint32_t)(254 - f) << 23));
+    return field == 255 ? 127u : (uint32_t)min(268 - field, 253);   // field <= 254: at least 14
 }
+
+__device__ __forceinline__ float field_value(uint32_t field) { return __uint_as_float(field << 23); }
 
 // eight 16-bit elements at row * K + k as they are; elements past K read 0
 __device__ __forceinline__ uint4 load8_raw(const void *p, int64_t row, int K, int k, bool wide)
@@ -135,15 +135,27 @@ __device__ __forceinline__ uint4 load8_raw(const void *p, int64_t row, int K, in
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Eight codes to eight float16 values 2^14 times too small, as pairs (0, 4), (1, 5), (2, 6), (3, 7):
-// a code's magnitude bits e e m are float16's low exponent bits and mantissa head (0.5 becomes a
-// subnormal), so two codes 16 bits apart take four operations.
+// Eight codes to eight float16 values, in order.  The conversion instruction does two at a time: 37
+// words a nanosecond on an SM, where shifts and masks did 14 and a stream at full rate needs 12.
 __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t (&d)[4])
 {
-    d[0] = ((w << 12) & 0x80008000u) | ((w << 9) & 0x0e000e00u);
-    d[1] = ((w << 8) & 0x80008000u) | ((w << 5) & 0x0e000e00u);
-    d[2] = ((w << 4) & 0x80008000u) | ((w << 1) & 0x0e000e00u);
-    d[3] = (w & 0x80008000u) | ((w >> 3) & 0x0e000e00u);
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(w));
+}
+
+// whether any byte of w is 0 or 255
+__device__ __forceinline__ bool special_bytes(uint32_t w)
+{
+    return (((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u;
+}
+
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, __half2 b)
+{
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&a), b);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 // ---------------------------------------------------------------- the grid-wide wait
@@ -203,28 +215,50 @@ __device__ __forceinline__ float key_value(uint32_t key)
     return __uint_as_float(key ^ ((uint32_t)((int32_t)~key >> 31) | 0x80000000u));
 }
 
-// The formulas of mrr_gating.h for token t; key: this warp's E words of shared memory.  Whatever the
-// logits hold, the k experts are different and in range.
-template <int DT>
-__device__ void route(const Params &p, int t, uint32_t *key, uint16_t *expert, float *weight)
+// The `count` largest of n keys, ties to the lower index, by one warp: pick(i, index, key) is called
+// by every lane.  A key taken is set to 0; the other keys are above 0 and at least `count`.
+template <typename Pick>
+__device__ __forceinline__ void pick_largest(uint32_t *key, int n, int count, Pick pick)
+{
+    const int lane = threadIdx.x % 32;
+    uint32_t best = 0u;
+    int at = lane;
+    auto scan = [&]() {   // the best of this lane's
+        best = 0u;
+#pragma unroll 4
+        for (int e = lane; e < n; e += 32)
+            if (key[e] > best) {
+                best = key[e];
+                at = e;
+            }
+    };
+    scan();
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+        const uint32_t top = __reduce_max_sync(kFull, best);
+        const uint32_t e = __reduce_min_sync(kFull, best == top && best ? (uint32_t)at : 0xffffffffu);
+        pick(i, (int)e, top);
+        if ((int)(e % 32) == lane) {
+            key[e] = 0u;
+            scan();
+        }
+    }
+    __syncwarp();
+}
+
+// The formulas of mrr_gating.h for one token by one warp: key holds its E logits (as float bits), with
+// room for as many words behind them.  Whatever the logits hold, the k experts are different and in
+// range.
+static __device__ __noinline__ void route(const Params &p, uint32_t *key, const float *bias, uint16_t *expert, float *weight)
 {
     const int lane = threadIdx.x % 32, E = p.E;
-    const int64_t plane = (int64_t)p.T * E;
-    const float *z = p.part + (int64_t)t * E;
-    float mx = -INFINITY, sum = 0.f;
-    for (int e = lane; e < E; e += 32) {
-        float part[kMaxParts], v = 0.f;   // all loads at once
-#pragma unroll
-        for (int q = 0; q < kMaxParts; ++q)
-            part[q] = q < p.kparts ? __ldcg(z + q * plane + e) : 0.f;
-#pragma unroll
-        for (int q = 0; q < kMaxParts; ++q)
-            v += part[q];
-        key[e] = __float_as_uint(v);
-        mx = fmaxf(mx, v);
-    }
+    float sum = 0.f;
     if (p.norm_type == 0) {
+        float mx = -INFINITY;
+        for (int e = lane; e < E; e += 32)
+            mx = fmaxf(mx, __uint_as_float(key[e]));
         mx = key_value(__reduce_max_sync(kFull, order_key(mx)));
+#pragma unroll 2
         for (int e = lane; e < E; e += 32) {
             const float v = expf(__uint_as_float(key[e]) - mx);
             key[e] = __float_as_uint(v);
@@ -232,6 +266,7 @@ __device__ void route(const Params &p, int t, uint32_t *key, uint16_t *expert, f
         }
         sum = warp_sum(sum);
     }
+#pragma unroll 2
     for (int e = lane; e < E; e += 32) {
         float v = __uint_as_float(key[e]);
         if (p.norm_type == 0)
@@ -240,83 +275,43 @@ __device__ void route(const Params &p, int t, uint32_t *key, uint16_t *expert, f
             v = 1.f / (1.f + expf(-v));
         else
             v = v > 20.f ? v + log1pf(expf(-v)) : log1pf(expf(v));
-        key[e] = order_key(p.bias ? v + load1<DT>(p.bias, e) : v);
+        key[e] = order_key(bias ? v + bias[e] : v);
     }
     __syncwarp();
-    const int size = E / p.group_count;
     if (p.k_group < p.group_count) {
-        // group scores; the groups are ranked over the lanes that hold them (32 at a time)
-        uint32_t mine[MRR_GATE_MAX_EXPERTS / 32];   // key of group 32 i + lane
-        const int rounds = (p.group_count + 31) / 32;
-        for (int r = 0; r < rounds; ++r)
-            mine[r] = 0u;
-        for (int g = 0; g < p.group_count; ++g) {
-            uint32_t a = 0u, b = 0u;   // this lane's two best of the group
-            for (int e = g * size + lane; e < (g + 1) * size; e += 32) {
-                const uint32_t v = key[e];
+        uint32_t *group = key + E;
+        const int size = E / p.group_count;
+        for (int g = lane; g < p.group_count; g += 32) {
+            uint32_t a = 0u, b = 0u;   // the two best of the group
+            int e = lane % size;       // neighbouring lanes start at different banks
+#pragma unroll 4
+            for (int i = 0; i < size; ++i) {
+                const uint32_t v = key[g * size + e];
                 b = max(b, min(a, v));
                 a = max(a, v);
+                e = e + 1 == size ? 0 : e + 1;
             }
-            const uint32_t top = __reduce_max_sync(kFull, a);
-            float s = key_value(top);
-            if (p.select_mode == 1) {
-                const bool first = __ffs(__ballot_sync(kFull, a == top)) - 1 == lane;
-                s += key_value(__reduce_max_sync(kFull, first ? b : a));
-            }
-            if (g % 32 == lane)
-                mine[g / 32] = order_key(s);
+            group[g] = p.select_mode == 1 ? order_key(key_value(a) + key_value(b)) : a;
         }
-        uint32_t kept[MRR_GATE_MAX_EXPERTS / 32];   // bit: group 32 i + lane is kept
-        for (int r = 0; r < rounds; ++r)
-            kept[r] = 0u;
-        for (int i = 0; i < p.k_group; ++i) {
-            uint32_t best = 0u;
-            int at = 0;
-            for (int r = 0; r < rounds; ++r)
-                if (mine[r] > best) {
-                    best = mine[r];
-                    at = r;
-                }
-            const uint32_t top = __reduce_max_sync(kFull, best);
-            const uint32_t g = __reduce_min_sync(kFull, best == top && best ? (uint32_t)(32 * at + lane) : 0xffffffffu);
-            if ((int)(g % 32) == lane) {
-                mine[g / 32] = 0u;
-                kept[g / 32] = 1u;
-            }
-        }
-        for (int g = 0; g < p.group_count; ++g)
-            if (!(__ballot_sync(kFull, kept[g / 32]) >> (g % 32) & 1u))
-                for (int e = g * size + lane; e < (g + 1) * size; e += 32)
-                    key[e] = 0u;
+        __syncwarp();
+        pick_largest(group, p.group_count, p.k_group, [](int, int, uint32_t) {});
+        for (int e = lane; e < E; e += 32)
+            if (group[e / size])   // not picked
+                key[e] = 0u;
         __syncwarp();
     }
     float total = 0.f;
-    uint32_t best = 0u;
-    int at = 0;
-    auto scan = [&]() {
-        best = 0u;
-        for (int e = lane; e < E; e += 32)
-            if (key[e] > best) {
-                best = key[e];
-                at = e;
-            }
-    };
-    scan();
-    for (int i = 0; i < p.k; ++i) {
-        const uint32_t top = __reduce_max_sync(kFull, best);
-        const uint32_t e = __reduce_min_sync(kFull, best == top && best ? (uint32_t)at : 0xffffffffu);
-        const float s = key_value(top);
-        total += s;
-        if ((int)(e % 32) == lane) {
+    pick_largest(key, E, p.k, [&](int i, int e, uint32_t top) {
+        const float v = key_value(top);
+        total += v;
+        if (lane == 0) {
             expert[i] = (uint16_t)e;
-            weight[i] = s;
-            key[e] = 0u;
-            scan();
+            weight[i] = v;
         }
-    }
-    __syncwarp();
+    });
     for (int i = lane; i < p.k; i += 32)
         weight[i] = weight[i] / (total + p.eps) * p.rsf;
+    __syncwarp();
 }
 
 // ---------------------------------------------------------------- one warp's weight stream
@@ -326,6 +321,7 @@ __device__ void route(const Params &p, int t, uint32_t *key, uint16_t *expert, f
 struct Cursor {
     int phase;                 // 0: up, 1: down, 2: over
     int item, expert, chunk;   // expert: index among the active ones; chunk: along K
+    int part, last;            // down: the share of the expert's K that this warp is in; its end
     const uint8_t *src;        // this lane's first 16-byte piece of chunk 0
     const uint8_t *scale_src;  // and its 8 scale bytes
     uint32_t rows;             // bit j: the row of its piece j exists; bit 8: that of its scales
@@ -344,9 +340,10 @@ struct Layer {
     uint8_t *smem;
     uint32_t ring;               // this warp's stages
     int warp, lane, g, t;
-    int nact, up_items, up_units, up_tiles, down_items, down_units, down_chunks;
+    int nact, up_items, up_units, up_tiles, down_items, down_chunks, down_parts;
     int64_t up_row, down_row;    // bytes of a weight row
     const uint16_t *act, *start, *cols;
+    const uint8_t *tokens;       // of the columns (NT > 1)
 
     __device__ Layer(const Params &p_, uint8_t *sm) : p(p_), smem(sm)
     {
@@ -358,6 +355,7 @@ struct Layer {
         act = reinterpret_cast<const uint16_t *>(sm + p.sm_act);
         start = reinterpret_cast<const uint16_t *>(sm + p.sm_start);
         cols = reinterpret_cast<const uint16_t *>(sm + p.sm_cols);
+        tokens = sm + p.sm_tokens;
     }
 
     __device__ void sizes(int active)
@@ -368,7 +366,9 @@ struct Layer {
         up_units = (p.H + kUpK - 1) / kUpK;
         down_items = (p.H + 15) / 16;
         down_chunks = (p.I + kDownK - 1) / kDownK;
-        down_units = nact * down_chunks;
+        // an expert's K is cut into shares, taken by the warps in turn: single chunks, or (where a
+        // change of expert costs something) as few as give every warp four or more
+        down_parts = NT == 1 ? down_chunks : min(down_chunks, (4 * kWarps + nact - 1) / nact);
         up_row = kMx ? p.H / 2 : 2 * (int64_t)p.H;
         down_row = kMx ? p.I / 2 : 2 * (int64_t)p.I;
     }
@@ -399,6 +399,34 @@ struct Layer {
         }
     }
 
+    // the chunk after c's in the down product, within its item; false if there is none
+    __device__ __forceinline__ bool next_chunk(Cursor &c) const
+    {
+        if (++c.chunk < c.last)
+            return true;
+        c.part += kWarps;
+        return enter_part(c);
+    }
+
+    __device__ __forceinline__ bool first_chunk(Cursor &c) const
+    {
+        c.part = warp;
+        c.expert = 0;
+        return enter_part(c);
+    }
+
+    __device__ __forceinline__ bool enter_part(Cursor &c) const
+    {
+        while (c.part >= down_parts) {
+            c.part -= down_parts;
+            if (++c.expert >= nact)
+                return false;
+        }
+        c.chunk = NT == 1 ? c.part : c.part * down_chunks / down_parts;
+        c.last = NT == 1 ? c.part + 1 : (c.part + 1) * down_chunks / down_parts;
+        return true;
+    }
+
     __device__ __forceinline__ Cursor first_unit() const
     {
         Cursor c;
@@ -416,15 +444,13 @@ struct Layer {
     __device__ __forceinline__ void first_down(Cursor &c) const
     {
         c.item = blockIdx.x;
-        c.phase = c.item < down_items && warp < down_units ? 1 : 2;
-        c.expert = warp / down_chunks;
-        c.chunk = warp - c.expert * down_chunks;
+        c.phase = c.item < down_items && first_chunk(c) ? 1 : 2;
     }
 
     __device__ __forceinline__ void advance(Cursor &c) const
     {
-        c.chunk += kWarps;
         if (c.phase == 0) {
+            c.chunk += kWarps;
             if (c.chunk < up_units)
                 return;
             c.chunk = warp;
@@ -433,23 +459,17 @@ struct Layer {
                 first_down(c);
             else
                 c.expert = c.item / up_tiles;
-            aim(c);
-        } else if (c.phase == 1) {
-            if (c.chunk < down_chunks)
-                return;
-            do {
-                c.chunk -= down_chunks;
-                ++c.expert;
-            } while (c.chunk >= down_chunks);
-            if (c.expert >= nact) {
+        } else {
+            const int e = c.expert;
+            if (next_chunk(c)) {
+                if (c.expert == e)
+                    return;
+            } else {
                 c.item += gridDim.x;
-                if (c.item >= down_items)
-                    c.phase = 2;
-                c.expert = warp / down_chunks;
-                c.chunk = warp - c.expert * down_chunks;
+                c.phase = c.item < down_items && first_chunk(c) ? 1 : 2;
             }
-            aim(c);
         }
+        aim(c);
     }
 
     // start the copies of the cursor's unit into stage `slot`, 16-byte pieces exchanged inside a row
@@ -536,29 +556,23 @@ struct Layer {
     struct Tokens {
         uint4 v[kCols][kGroups];
     };
-    static constexpr int kUpGroups = kMx ? 8 : 2;      // of one stage
-    static constexpr int kDownGroups = kMx ? 8 : 4;    // of a stage, or (kMx) of half of one
-    static constexpr int kDownHalves = kMx ? 2 : 1;
+    // a stage is worked off in batches of kGroups groups
+    static constexpr int kUpGroups = kMx ? 4 : 2, kUpBatches = kMx ? 2 : 1;
+    static constexpr int kDownGroups = 4, kDownBatches = kMx ? 4 : 1;
 
-    // The products of groups q0 .. q0 + kGroups - 1 (k0: the first one's k) of a stage: kTiles 16-row
-    // tiles against column tiles j0 .. j0 + kCols - 1, of which nt exist in all.
-    template <int kTiles, int kRow, int kGroups, int kAcc>
-    __device__ __forceinline__ void multiply(int slot, int q0, int k0, int K, int j0, int nt, const Tokens<kGroups> &b,
-                                             float (&acc)[kTiles][kAcc][4]) const
+    // The products of groups q0 .. q0 + kGroups - 1 of a stage: kTiles 16-row tiles against column tiles
+    // j0 .. j0 + kN - 1.  kWhole: all groups lie before K, and (kMx) no scale is 0 or NaN.
+    template <bool kWhole, int kN, int kTiles, int kRow, int kGroups>
+    __device__ __forceinline__ void multiply_groups(int slot, int q0, int left, int j0, const Tokens<kGroups> &b,
+                                                    const uint32_t (&sc)[2][2], float (&acc)[2][NT][4]) const
     {
-        uint2 sc[kMx ? kTiles : 1][2];   // scale bytes of rows g and g + 8
-        if (kMx)
-#pragma unroll
-            for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    sc[m][r] = stage_word<uint2>(slot, 4096 + (16 * m + 8 * r + g) * (kRow / 16) + q0);
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            if (k0 + 32 * i >= K)
+            if (!kWhole && 32 * i >= left)
                 break;
             const int q = q0 + i;
             uint32_t a[kTiles][2][4];
+            float s[2][2];
 #pragma unroll
             for (int m = 0; m < kTiles; ++m)
 #pragma unroll
@@ -566,26 +580,21 @@ struct Layer {
                     const int row = 16 * m + 8 * r + g;
                     if (kMx) {
                         codes_to_half(stage_word<uint32_t>(slot, row * kRow + ((q ^ (row & 7)) << 4) + 4 * t), a[m][r]);
+                        // byte i of sc, as a float's exponent
+                        s[m][r] = kWhole ? __uint_as_float((i < 3 ? sc[m][r] << (23 - 8 * i) : sc[m][r] >> 1) & 0x7f800000u)
+                                         : e8m0_value(sc[m][r] >> (8 * i) & 255u);
                     } else {
                         const uint4 v = stage_word<uint4>(slot, row * kRow + (((4 * q + t) ^ ((row & 1) << 2)) << 4));
                         a[m][r][0] = v.x, a[m][r][1] = v.y, a[m][r][2] = v.z, a[m][r][3] = v.w;
                     }
                 }
-            float s[kTiles][2];
-            if (kMx)
 #pragma unroll
-                for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        s[m][r] = e8m0_value((i < 4 ? sc[m][r].x : sc[m][r].y) >> (8 * (i % 4)) & 255u);
-#pragma unroll
-            for (int j = 0; j < kCols; ++j) {
-                if (j0 + j >= nt)
-                    break;
+            for (int j = 0; j < kN; ++j) {
                 const uint4 x = b.v[j][i];
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m) {
-                    float(&to)[4] = acc[m][j0 + j];
+                    // one row tile: two chains of sums, so that an instruction waits for the last but one
+                    float(&to)[4] = acc[kTiles == 2 ? m : i % 2][j0 + j];
                     if (kMx) {
                         float d[4] = {0.f, 0.f, 0.f, 0.f};
                         mma<MDT>(d, a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], x.x, x.y);
@@ -603,6 +612,37 @@ struct Layer {
         }
     }
 
+    // column tiles j0 .. of nt, at most kCols of them; left: elements of K from the first group on
+    template <int kTiles, int kRow, int kGroups>
+    __device__ __forceinline__ void multiply(int slot, int q0, int left, int j0, int nt, const Tokens<kGroups> &b,
+                                             float (&acc)[2][NT][4]) const
+    {
+        bool whole = left >= 32 * kGroups;
+        uint32_t sc[2][2] = {};   // 4 scale bytes of rows g and g + 8
+        if (kMx) {
+            bool odd = false;
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    sc[m][r] = stage_word<uint32_t>(slot, 4096 + (16 * m + 8 * r + g) * (kRow / 16) + q0);
+                    odd |= special_bytes(sc[m][r]);
+                }
+            whole = whole && !__any_sync(kFull, odd);
+        }
+        if (kCols == 1 || j0 + 1 >= nt) {
+            if (whole)
+                multiply_groups<true, 1, kTiles, kRow, kGroups>(slot, q0, left, j0, b, sc, acc);
+            else
+                multiply_groups<false, 1, kTiles, kRow, kGroups>(slot, q0, left, j0, b, sc, acc);
+        } else {
+            if (whole)
+                multiply_groups<true, kCols, kTiles, kRow, kGroups>(slot, q0, left, j0, b, sc, acc);
+            else
+                multiply_groups<false, kCols, kTiles, kRow, kGroups>(slot, q0, left, j0, b, sc, acc);
+        }
+    }
+
     // fetch token operands from k0 on; column(j, k): the 8 elements k .. k + 7 of this lane's column of tile j
     template <int kGroups, typename Column>
     __device__ __forceinline__ void fetch(Tokens<kGroups> &b, int j0, int nt, int k0, int K, Column column) const
@@ -615,6 +655,9 @@ struct Layer {
                     if (k0 + 32 * i < K)
                         b.v[j][i] = column(j0 + j, k0 + 32 * i + 8 * t);
     }
+
+    // token of column c of active expert ai, which exists
+    __device__ __forceinline__ int token_of(int ai, int c) const { return NT == 1 ? c : (int)tokens[start[ai] + c]; }
 
     // assignment of column c of active expert ai, or -1.  Up to 8 tokens: column = token.
     __device__ __forceinline__ int column_of(int ai, int c) const
@@ -632,20 +675,21 @@ struct Layer {
         return NT == 1 ? 1 : ((int)start[ai + 1] - (int)start[ai] + 7) / 8;
     }
 
-    // eight elements of h's row a as the matrix instructions take them
-    __device__ __forceinline__ uint4 h8(int a, int k, float scale) const
+    // Eight elements of h's row a as the matrix instructions take them.  With float16 a 16-element tile
+    // has its own power of two, and `field` is the exponent of the one that the token's sums carry.
+    __device__ __forceinline__ uint4 h8(int a, int k, uint32_t field) const
     {
-        if (a < 0 || k >= p.Ip)
-            return make_uint4(0, 0, 0, 0);
-        if (!kScaled)
-            return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.h) + (int64_t)a * p.Ip + k);
-        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p.h) + (int64_t)a * p.Ip + k);
-        const float4 u = q[0], v = q[1];
-        if (kMx)   // the order of codes_to_half
-            return make_uint4(pack2<MDT>(u.x * scale, v.x * scale), pack2<MDT>(u.y * scale, v.y * scale),
-                              pack2<MDT>(u.z * scale, v.z * scale), pack2<MDT>(u.w * scale, v.w * scale));
-        return make_uint4(pack2<MDT>(u.x * scale, u.y * scale), pack2<MDT>(u.z * scale, u.w * scale),
-                          pack2<MDT>(v.x * scale, v.y * scale), pack2<MDT>(v.z * scale, v.w * scale));
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (a >= 0 && k < p.Ip) {
+            v = *reinterpret_cast<const uint4 *>(p.h + (int64_t)a * p.Ip + k);
+            if (kScaled) {
+                const uint32_t tile = p.h_field[(int64_t)a * (p.Ip / 16) + k / 16];
+                // token's over tile's: at most 1; below 2^-24 nothing is left of the tile
+                const __half2 r = __float2half2_rn(field_value(127u - min(tile - field, 126u)));
+                v = make_uint4(half2_mul(v.x, r), half2_mul(v.y, r), half2_mul(v.z, r), half2_mul(v.w, r));
+            }
+        }
+        return v;
     }
 
     __device__ __forceinline__ float *red(int buf) const
@@ -672,7 +716,7 @@ struct Layer {
 
     // ------------------------------------------------------------ before the first wait
 
-    // x's row t as the products take it: 16-bit, zeros past H, scaled (kMx) and in their order
+    // x's row t as the products take it: 16-bit, zeros past H, scaled (kMx)
     __device__ void prepare_row(int tok)
     {
         uint32_t *s_max = reinterpret_cast<uint32_t *>(smem + p.sm_red);
@@ -688,10 +732,10 @@ struct Layer {
             if (lane == 0)
                 atomicMax(s_max, m);
             __syncthreads();
-            const float2 s = f16_scale(*s_max);
-            scale = s.x;
+            const uint32_t field = f16_scale_field(*s_max);
+            scale = field_value(field);
             if (threadIdx.x == 0)
-                p.x_scale[tok] = s.y * 0x1p14f;   // and the codes' 2^14
+                p.x_scale[tok] = field_value(254u - field);
             __syncthreads();
         } else if (threadIdx.x == 0) {
             p.x_scale[tok] = 1.f;
@@ -702,8 +746,8 @@ struct Layer {
             uint4 v = load8_raw(p.x, tok, p.H, 8 * c, p.x_wide);
             if (kMx) {
                 const float2 a = unpack2<DT>(v.x), b = unpack2<DT>(v.y), d = unpack2<DT>(v.z), e = unpack2<DT>(v.w);
-                v = make_uint4(pack2<MDT>(a.x * scale, d.x * scale), pack2<MDT>(a.y * scale, d.y * scale),
-                               pack2<MDT>(b.x * scale, e.x * scale), pack2<MDT>(b.y * scale, e.y * scale));
+                v = make_uint4(pack2<MDT>(a.x * scale, a.y * scale), pack2<MDT>(b.x * scale, b.y * scale),
+                               pack2<MDT>(d.x * scale, d.y * scale), pack2<MDT>(e.x * scale, e.y * scale));
             }
             reinterpret_cast<uint4 *>(p.xh + (int64_t)tok * p.Hp)[c] = v;
         }
@@ -754,19 +798,47 @@ struct Layer {
 
     // ------------------------------------------------------------ between the waits: who goes where
 
+    // the sums of the logits' parts for tokens tok .. tok + n - 1, into key (2 E words a token), and
+    // the bias behind them, by the whole block
+    __device__ void logits(int tok, int n, uint32_t *key, float *bias)
+    {
+        const int64_t plane = (int64_t)p.T * p.E;
+        if (p.bias)
+            for (int e = threadIdx.x; e < p.E; e += kThreads)
+                bias[e] = load1<DT>(p.bias, e);
+#pragma unroll 1
+        for (int i = threadIdx.x; i < n * p.E; i += kThreads) {
+            const int t_ = i / p.E, e = i - t_ * p.E;
+            const float *z = p.part + (int64_t)(tok + t_) * p.E + e;
+            float part[kMaxParts], v = 0.f;   // all loads at once
+#pragma unroll
+            for (int q = 0; q < kMaxParts; ++q)
+                part[q] = q < p.kparts ? __ldcg(z + q * plane) : 0.f;
+#pragma unroll
+            for (int q = 0; q < kMaxParts; ++q)
+                v += part[q];
+            key[t_ * 2 * p.E + e] = __float_as_uint(v);
+        }
+        __syncthreads();
+    }
+
     // Expert and weight of every assignment.  Up to 8 tokens every block finds them for itself, a
     // token a warp; with more, each token is one block's, and the blocks wait for one another.
     __device__ bool assign(uint16_t *expert, float *weight, int *s_ok)
     {
-        uint32_t *key = reinterpret_cast<uint32_t *>(smem) + warp * p.E;   // the ring is not in use yet
+        uint32_t *key = reinterpret_cast<uint32_t *>(smem);   // the ring is not in use yet
+        float *bias = reinterpret_cast<float *>(key + (NT == 1 ? p.T : 1) * 2 * p.E);
+        const float *use_bias = p.bias ? bias : nullptr;
         if (NT == 1) {
+            logits(0, p.T, key, bias);
             if (warp < p.T)
-                route<DT>(p, warp, key, expert + warp * p.k, weight + warp * p.k);
+                route(p, key + warp * 2 * p.E, use_bias, expert + warp * p.k, weight + warp * p.k);
             __syncthreads();
         } else {
             for (int tok = blockIdx.x; tok < p.T; tok += gridDim.x) {
+                logits(tok, 1, key, bias);
                 if (warp == 0) {
-                    route<DT>(p, tok, key, expert, weight);
+                    route(p, key, use_bias, expert, weight);
                     for (int i = lane; i < p.k; i += 32) {
                         p.route_expert[tok * p.k + i] = expert[i];
                         p.route_weight[tok * p.k + i] = weight[i];
@@ -798,6 +870,7 @@ struct Layer {
         uint16_t *act_ = reinterpret_cast<uint16_t *>(smem + p.sm_act);
         uint16_t *start_ = reinterpret_cast<uint16_t *>(smem + p.sm_start);
         uint16_t *cols_ = reinterpret_cast<uint16_t *>(smem + p.sm_cols);
+        uint8_t *tokens_ = smem + p.sm_tokens;
         int *s_nact = reinterpret_cast<int *>(smem + p.sm_count);
         // in the ring, which is not in use yet: assignments of each expert, then its place among the
         // active ones; an assignment's place among its expert's
@@ -848,11 +921,10 @@ struct Layer {
         }
         __syncthreads();
         for (int a = threadIdx.x; a < n; a += kThreads) {
-            const int i = count[expert[a]];
-            if (NT == 1)
-                cols_[i * 8 + a / p.k] = (uint16_t)a;
-            else
-                cols_[start_[i] + place[a]] = (uint16_t)a;
+            const int i = count[expert[a]], tok = a / p.k, c = NT == 1 ? i * 8 + tok : start_[i] + place[a];
+            cols_[c] = (uint16_t)a;
+            if (NT > 1)
+                tokens_[c] = (uint8_t)tok;
         }
         __syncthreads();
         return *s_nact;
@@ -908,27 +980,32 @@ struct Layer {
             const int ai = item / up_tiles, i0 = (item - ai * up_tiles) * 16, nt = tiles_of(ai);
             const uint16_t *row[NT];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int a = j < nt ? column_of(ai, 8 * j + g) : -1;
-                row[j] = a < 0 ? nullptr : p.xh + (int64_t)(a / p.k) * p.Hp;
-            }
+            for (int j = 0; j < NT; ++j)
+                row[j] = j < nt && column_of(ai, 8 * j + g) >= 0 ? p.xh + (int64_t)token_of(ai, 8 * j + g) * p.Hp : nullptr;
             auto column = [&](int j, int k) {
-                return row[j] ? *reinterpret_cast<const uint4 *>(row[j] + k) : make_uint4(0, 0, 0, 0);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row[j])
+                    v = *reinterpret_cast<const uint4 *>(row[j] + k);
+                return v;
             };
             float acc[2][NT][4] = {};
-            Tokens<kUpGroups> ahead;   // the next unit's, fetched while this one's are multiplied
+            Tokens<kUpGroups> ahead;   // the next batch's, fetched while this one's are multiplied
             fetch(ahead, 0, nt, warp * kUpK, p.H, column);
             for (int u = warp; u < up_units; u += kWarps) {
                 const int at = take();
-                Tokens<kUpGroups> b = ahead;
-                fetch(ahead, 0, nt, (u + kWarps) * kUpK, p.H, column);
 #pragma unroll
-                for (int j = 0; j < NT; j += kCols) {
-                    if (j >= nt)
-                        break;
-                    if (j > 0)
-                        fetch(b, j, nt, u * kUpK, p.H, column);
-                    multiply<2, kUpRow>(at, 0, u * kUpK, p.H, j, nt, b, acc);
+                for (int h = 0; h < kUpBatches; ++h) {
+                    const int k0 = u * kUpK + h * kUpGroups * 32;
+                    Tokens<kUpGroups> b = ahead;
+                    fetch(ahead, 0, nt, h + 1 < kUpBatches ? k0 + kUpGroups * 32 : (u + kWarps) * kUpK, p.H, column);
+#pragma unroll
+                    for (int j = 0; j < NT; j += kCols) {
+                        if (j >= nt)
+                            break;
+                        if (j > 0)
+                            fetch(b, j, nt, k0, p.H, column);
+                        multiply<2, kUpRow>(at, h * kUpGroups, p.H - k0, j, nt, b, acc);
+                    }
                 }
             }
 #pragma unroll
@@ -941,19 +1018,21 @@ struct Layer {
                 if (threadIdx.x < 128) {
                     const int r = threadIdx.x % 16, c = threadIdx.x / 16, a = column_of(ai, 8 * j + c);
                     if (a >= 0) {
-                        const int tok = a / p.k;
+                        const int tok = token_of(ai, 8 * j + c);
                         const float s = kMx ? p.x_scale[tok] : 1.f;
                         const float gate = gather(red(buf), 0, r, c) * s, upv = gather(red(buf), 1, r, c) * s;
-                        const float h = gate / (1.f + expf(-gate)) * upv * weight[a];
+                        float h = gate / (1.f + expf(-gate)) * upv * weight[a];
                         if (kScaled) {
-                            static_cast<float *>(p.h)[(int64_t)a * p.Ip + i0 + r] = h;
                             const uint32_t half = 0xffffu << (threadIdx.x & 16);
                             const uint32_t m = __reduce_max_sync(half, __float_as_uint(h) & 0x7fffffffu);
-                            if (r == 0)
+                            const uint32_t field = f16_scale_field(m);
+                            h *= field_value(field);
+                            if (r == 0) {
+                                p.h_field[(int64_t)a * (p.Ip / 16) + i0 / 16] = (uint8_t)field;
                                 atomicMax(p.h_max + tok, m);
-                        } else {
-                            store1<MOE_BF16>(p.h, (int64_t)a * p.Ip + i0 + r, h);
+                            }
                         }
+                        store1<MDT>(p.h, (int64_t)a * p.Ip + i0 + r, h);
                     }
                 }
                 buf ^= 1;
@@ -968,44 +1047,46 @@ struct Layer {
         if (threadIdx.x == 0)
             p.flags[blockIdx.x] = 0;
 
-        // what the matrix instructions' sums are multiplied by for token tok, and h before them
-        auto h_scale = [&](int tok) { return kScaled ? f16_scale(__ldcg(p.h_max + tok)) : make_float2(1.f, 1.f); };
+        // the exponent of the power of two that token tok's sums carry (float16)
+        auto field_of = [&](int tok) { return kScaled ? f16_scale_field(__ldcg(p.h_max + tok)) : 127u; };
         if (NT == 1) {
-            const float scale = g < p.T ? h_scale(g).x : 1.f;
+            const uint32_t field = g < p.T ? field_of(g) : 127u;
             for (int item = blockIdx.x; item < down_items; item += gridDim.x) {
-                float acc[1][1][4] = {};
-                int e = warp / down_chunks, chunk = warp - e * down_chunks;   // of `ahead`
-                int a = e < nact ? column_of(e, g) : -1;
-                auto column = [&](int, int k) { return h8(a, k, scale); };
+                float acc[2][NT][4] = {};
+                Cursor w;   // where `ahead` comes from
+                bool some = first_chunk(w);
+                int a = some ? column_of(w.expert, g) : -1;
+                auto column = [&](int, int k) { return h8(a, k, field); };
                 Tokens<kDownGroups> ahead;
-                fetch(ahead, 0, e < nact, chunk * kDownK, p.I, column);
-                for (int u = warp; u < down_units; u += kWarps) {
-                    const int at = take(), k0 = chunk * kDownK;
-                    Tokens<kDownGroups> b = ahead;
-                    if (kDownHalves == 2) {
-                        fetch(ahead, 0, 1, k0 + kDownK / 2, p.I, column);
-                        multiply<1, kDownRow>(at, 0, k0, p.I, 0, 1, b, acc);
-                        b = ahead;
+                fetch(ahead, 0, some, w.chunk * kDownK, p.I, column);
+                while (some) {
+                    const int at = take(), k0 = w.chunk * kDownK;
+#pragma unroll
+                    for (int h = 0; h < kDownBatches; ++h) {
+                        const int kb = k0 + h * kDownGroups * 32;
+                        Tokens<kDownGroups> b = ahead;
+                        if (h + 1 < kDownBatches) {
+                            fetch(ahead, 0, 1, kb + kDownGroups * 32, p.I, column);
+                        } else {
+                            const int e = w.expert;
+                            some = next_chunk(w);
+                            if (some && w.expert != e)
+                                a = column_of(w.expert, g);
+                            fetch(ahead, 0, some, w.chunk * kDownK, p.I, column);
+                        }
+                        multiply<1, kDownRow>(at, h * kDownGroups, p.I - kb, 0, 1, b, acc);
                     }
-                    chunk += kWarps;
-                    if (chunk >= down_chunks) {
-                        do {
-                            chunk -= down_chunks;
-                            ++e;
-                        } while (chunk >= down_chunks);
-                        a = e < nact ? column_of(e, g) : -1;
-                    }
-                    fetch(ahead, 0, e < nact, chunk * kDownK, p.I, column);
-                    multiply<1, kDownRow>(at, kDownHalves == 2 ? kDownGroups : 0, k0 + (kDownHalves - 1) * (kDownK / 2),
-                                          p.I, 0, 1, b, acc);
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[0][0][i] += acc[1][0][i];
                 put(red(buf), 0, acc[0][0]);
                 __syncthreads();
                 if (threadIdx.x < 128) {
                     const int r = threadIdx.x % 16, tok = threadIdx.x / 16, n = item * 16 + r;
                     if (tok < p.T && n < p.H)
                         store1<DT>(p.y, (int64_t)tok * p.H + n,
-                                   gather(red(buf), 0, r, tok) * h_scale(tok).y * (kMx ? 0x1p14f : 1.f));
+                                   gather(red(buf), 0, r, tok) * field_value(254u - field_of(tok)));
                 }
                 buf ^= 1;
             }
@@ -1016,61 +1097,63 @@ struct Layer {
                 for (int i = lane; i < p.T * kPitch; i += 32)
                     mine[i] = 0.f;
                 __syncwarp();
-                int e = warp / down_chunks, chunk = warp - e * down_chunks;   // of `ahead`
+                Cursor w;
+                bool some = first_chunk(w);
                 int a[NT];
-                float scale[NT];
-                auto enter = [&]() {   // the columns of expert e
+                uint32_t field[NT];
+                auto enter = [&]() {   // the columns of expert w.expert
+                    const int nt = some ? tiles_of(w.expert) : 0;
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        a[j] = e < nact && j < tiles_of(e) ? column_of(e, 8 * j + g) : -1;
-                        scale[j] = kScaled && a[j] >= 0 ? h_scale(a[j] / p.k).x : 1.f;
+                        a[j] = j < nt ? column_of(w.expert, 8 * j + g) : -1;
+                        field[j] = kScaled && a[j] >= 0 ? field_of(token_of(w.expert, 8 * j + g)) : 127u;
                     }
+                    return nt;
                 };
-                auto column = [&](int j, int k) { return h8(a[j], k, scale[j]); };
-                enter();
+                auto column = [&](int j, int k) { return h8(a[j], k, field[j]); };
+                int nt = enter();
                 Tokens<kDownGroups> ahead;
-                fetch(ahead, 0, e < nact ? tiles_of(e) : 0, chunk * kDownK, p.I, column);
-                for (int u = warp; u < down_units; u += kWarps) {
-                    const int at = take(), k0 = chunk * kDownK, nt = tiles_of(e), ai = e;
-                    float acc[1][NT][4] = {};
-                    Tokens<kDownGroups> b = ahead;
+                fetch(ahead, 0, nt, w.chunk * kDownK, p.I, column);
+                while (some) {   // one share of an expert's K
+                    const int ai = w.expert, tiles = nt;
+                    float acc[2][NT][4] = {};
+                    for (bool more = true; more; ++w.chunk) {
+                        const int at = take(), k0 = w.chunk * kDownK;
+                        more = w.chunk + 1 < w.last;
 #pragma unroll
-                    for (int half = 0; half < kDownHalves; ++half) {
-                        const int kh = k0 + half * (kDownK / 2);
-                        if (half > 0)
-                            fetch(b, 0, nt, kh, p.I, column);
+                        for (int h = 0; h < kDownBatches; ++h) {
+                            const int kb = k0 + h * kDownGroups * 32;
+                            Tokens<kDownGroups> b = ahead;
+                            if (h + 1 < kDownBatches || more)   // a chunk is kDownBatches batches long
+                                fetch(ahead, 0, tiles, kb + kDownGroups * 32, p.I, column);
 #pragma unroll
-                        for (int j = 0; j < NT; j += kCols) {
-                            if (j >= nt)
-                                break;
-                            if (j > 0)
-                                fetch(b, j, nt, kh, p.I, column);
-                            multiply<1, kDownRow>(at, half * kDownGroups, kh, p.I, j, nt, b, acc);
-                        }
-                    }
-                    chunk += kWarps;
-                    if (chunk >= down_chunks) {
-                        do {
-                            chunk -= down_chunks;
-                            ++e;
-                        } while (chunk >= down_chunks);
-                        enter();
-                    }
-                    fetch(ahead, 0, e < nact ? tiles_of(e) : 0, chunk * kDownK, p.I, column);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        if (j >= nt)
-                            break;
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int q = column_of(ai, 8 * j + 2 * t + c);
-                            if (q >= 0) {
-                                float *to = mine + (q / p.k) * kPitch + g;
-                                to[0] += acc[0][j][c];
-                                to[8] += acc[0][j][2 + c];
+                            for (int j = 0; j < NT; j += kCols) {
+                                if (j >= tiles)
+                                    break;
+                                if (j > 0)
+                                    fetch(b, j, tiles, kb, p.I, column);
+                                multiply<1, kDownRow>(at, h * kDownGroups, p.I - kb, j, tiles, b, acc);
                             }
                         }
                     }
+                    w.part += kWarps;
+                    some = enter_part(w);
+                    nt = enter();
+                    fetch(ahead, 0, nt, w.chunk * kDownK, p.I, column);
+                    const int first = start[ai], count = start[ai + 1] - first;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        if (j >= tiles)
+                            break;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if (8 * j + 2 * t + c < count) {
+                                float *to = mine + tokens[first + 8 * j + 2 * t + c] * kPitch + g;
+                                to[0] += acc[0][j][c] + acc[1][j][c];
+                                to[8] += acc[0][j][2 + c] + acc[1][j][2 + c];
+                            }
+                    }
+                    __syncwarp();   // the next share's columns are other lanes'
                 }
                 __syncthreads();
                 const float *all = reinterpret_cast<const float *>(smem + p.sm_y);
@@ -1080,9 +1163,9 @@ struct Layer {
                         continue;
                     float v = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w)
-                        v += all[(w * p.T + tok) * kPitch + r];
-                    store1<DT>(p.y, (int64_t)tok * p.H + n, v * h_scale(tok).y * (kMx ? 0x1p14f : 1.f));
+                    for (int q = 0; q < kWarps; ++q)
+                        v += all[(q * p.T + tok) * kPitch + r];
+                    store1<DT>(p.y, (int64_t)tok * p.H + n, v * field_value(254u - field_of(tok)));
                 }
                 __syncthreads();
             }
