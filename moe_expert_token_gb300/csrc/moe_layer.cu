@@ -137,11 +137,15 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     p.wr_wide = wide(w_router, 2 * H, 16);
     p.w13_wide = wide(w13, mx ? H / 2 : 2 * H, 16);
     p.w2_wide = wide(w2, mx ? I / 2 : 2 * I, 16);
+    if (p.w13_wide && p.w2_wide &&
+        (!tc::make_map(&p.w13_map, w13, E * 2 * I, mx ? H / 2 : 2 * H, 16) ||
+         !tc::make_map(&p.w2_map, w2, E * H, mx ? I / 2 : 2 * I, 16)))
+        return MRR_ERR_CUDA;
     p.s13_wide = mx && wide(w13_scales, scale_row_bytes(H), 8);
     p.s2_wide = mx && wide(w2_scales, scale_row_bytes(I), 8);
     // shared memory: the rings (before them, the routing's scratch), the joins, the routing
     const int64_t n = T * k, active = n < E ? n : E;
-    int64_t at = (int64_t)kWarps * kStages * stage_bytes(mx);
+    int64_t at = (int64_t)kWarps * kStages * kStageBytes;
     const int64_t keys = ((T > 8 ? 1 : T) * 2 * E + E) * 4, places = 2 * (E + n);
     const int64_t scratch = keys > places ? keys : places;
     at = at > scratch ? at : scratch;
@@ -150,6 +154,8 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
         at += mrr_ws::round_up(bytes, 16);
         return (int)off;
     };
+    p.sm_scales = mx ? take(kWarps * kStages * kStageScales) : 0;
+    p.sm_bar = take(kWarps * kStages * 8);
     p.sm_red = take(2 * kWarps * 256 * 4);
     p.sm_y = T > 8 ? take(kWarps * T * 17 * 4) : 0;
     p.sm_expert = take(n * 2);

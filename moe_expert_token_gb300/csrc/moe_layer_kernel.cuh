@@ -12,9 +12,10 @@
 //    sums).  A tile of 8 columns costs no more for one token than for eight, and the tensor pipe
 //    is idle most of the time: the rate that matters is that of the loads.
 //  * Each warp streams its own share of the K axis through a private ring of kStages 4 KB stages in
-//    shared memory, filled with 16-byte asynchronous copies and waited for by that warp alone.
-//    The ring runs on across items, and from the up product into the down product: the down
-//    weights of the first items are in flight while the grid waits for h.
+//    shared memory.  A stage is two slabs of 16 rows x 128 bytes, each one tiled bulk copy issued by
+//    one lane (thread copies of 16 bytes, with their addresses, were most of the instructions that
+//    a stage cost).  The ring runs on across items, and from the up product into the down product:
+//    the down weights of the first items are in flight while the grid waits for h.
 //  * A lane's 16-byte piece of a row feeds two matrix instructions: the order of k inside a group of
 //    32 is free as long as both operands share it, so lane (g, t) holds elements 8t .. 8t+7.
 //  * The grid waits twice: for the logits, and for h.  Between them every block computes the
@@ -34,6 +35,7 @@
 #include "mrr_gating.h"
 #include "mx.cuh"
 #include "ptx.cuh"
+#include "tc.cuh"
 #include "ws_layout.h"
 
 namespace moe_layer {
@@ -43,7 +45,7 @@ using namespace moe_mx;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStages = 4;
-constexpr int kUpRow = 128, kDownRow = 256;      // bytes of a row in a stage: 32 rows x 128, 16 rows x 256
+constexpr int kSlab = 2048;                      // 16 rows x 128 bytes
 constexpr int kMaxParts = 16;                    // most shares of H the logits are split into
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -68,12 +70,15 @@ struct Params {
     uint16_t *h;                  // [T k][Ip]
     uint8_t *h_field;             // [T k][Ip / 16]: exponent of the power of two each tile of h carries (float16)
     int Hp, Ip, kparts;
-    int x_wide, wr_wide, w13_wide, w2_wide, s13_wide, s2_wide;   // 16-byte (scales: 8-byte) copies possible
+    int x_wide, wr_wide;              // 16-byte loads possible
+    int w13_wide, w2_wide;            // rows are 16-byte aligned: tiled copies possible
+    int s13_wide, s2_wide;            // scale rows are 8-byte aligned
+    CUtensorMap w13_map, w2_map;      // rows of bytes, boxes of 128 bytes x 16 rows, 128-byte swizzle
     // dynamic shared memory, byte offsets
-    int sm_red, sm_y, sm_expert, sm_weight, sm_act, sm_start, sm_cols, sm_tokens, sm_count;
+    int sm_scales, sm_bar, sm_red, sm_y, sm_expert, sm_weight, sm_act, sm_start, sm_cols, sm_tokens, sm_count;
 };
 
-__host__ __device__ constexpr int stage_bytes(bool mx) { return 4096 + (mx ? 256 : 0); }
+constexpr int kStageBytes = 2 * kSlab, kStageScales = 256;
 
 template <int DT>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -91,23 +96,16 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// asynchronous copies of 16 or 8 bytes; with ok false the destination is zeroed and src not read
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-
+// an asynchronous copy of 8 bytes; with ok false the destination is zeroed and src not read
 __device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool ok)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
 }
 
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int N>
-__device__ __forceinline__ void copy_wait()
+// this thread arrives on `bar` once its copies so far have landed
+__device__ __forceinline__ void copies_arrive(uint32_t bar)
 {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // The power of two that takes the float with bits `amax` into [2^14, 2^15), so that it and all
@@ -119,6 +117,17 @@ __device__ __forceinline__ uint32_t f16_scale_field(uint32_t amax)
 }
 
 __device__ __forceinline__ float field_value(uint32_t field) { return __uint_as_float(field << 23); }
+
+// mma with nothing to add to
+template <int DT>
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
+{
+    static_assert(DT == MOE_F16, "");
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 
 // eight 16-bit elements at row * K + k as they are; elements past K read 0
 __device__ __forceinline__ uint4 load8_raw(const void *p, int64_t row, int K, int k, bool wide)
@@ -317,31 +326,33 @@ static __device__ __noinline__ void route(const Params &p, uint32_t *key, const 
 // ---------------------------------------------------------------- one warp's weight stream
 
 // Where a warp's stream of weight stages stands: first its units of this block's up items, then
-// those of its down items.  A unit is one stage: 32 rows x 128 bytes, or 16 rows x 256 bytes.
+// those of its down items.  A unit is one stage: 16 gate rows and their 16 up rows x 128 bytes, or 16
+// rows x 256 bytes.
 struct Cursor {
     int phase;                 // 0: up, 1: down, 2: over
     int item, expert, chunk;   // expert: index among the active ones; chunk: along K
     int part, last;            // down: the share of the expert's K that this warp is in; its end
-    const uint8_t *src;        // this lane's first 16-byte piece of chunk 0
-    const uint8_t *scale_src;  // and its 8 scale bytes
-    uint32_t rows;             // bit j: the row of its piece j exists; bit 8: that of its scales
+    int row;                   // first weight row
+    const uint8_t *scale_src;  // this lane's 8 scale bytes of chunk 0; null if there is no such row
 };
 
-template <int DT, int WDT, int NT>
+template <int DT, int WDT, int NT, bool kWide>
 struct Layer {
     static constexpr bool kMx = WDT == MOE_MXFP4;
     static constexpr int MDT = kMx ? MOE_F16 : DT;            // the matrix instructions' type
-    static constexpr bool kScaled = MDT == MOE_F16;           // h is float32 in memory, scaled when packed
-    static constexpr int kStage = stage_bytes(kMx);
-    static constexpr int kPerByte2 = kMx ? 4 : 1;             // elements in two bytes
-    static constexpr int kUpK = kUpRow / 2 * kPerByte2, kDownK = kDownRow / 2 * kPerByte2;
+    static constexpr bool kScaled = MDT == MOE_F16;           // h carries a power of two for each tile
+    static constexpr int kStage = kStageBytes;
+    static constexpr int kSlabK = kMx ? 256 : 64;             // elements of K in 128 bytes
+    static constexpr int kUpK = kSlabK, kDownK = 2 * kSlabK;  // and in a stage
 
     const Params &p;
     uint8_t *smem;
-    uint32_t ring;               // this warp's stages
     int warp, lane, g, t;
+    int row;                     // of a slab's rows 0 .. 7, the one this lane's operands come from
+    int lane_at;                 // where in a slab they are
+    uint32_t bars;               // this warp's barriers, one a stage
+    bool dead;                   // a wait has given up: results do not matter any more
     int nact, up_items, up_units, up_tiles, down_items, down_chunks, down_parts;
-    int64_t up_row, down_row;    // bytes of a weight row
     const uint16_t *act, *start, *cols;
     const uint8_t *tokens;       // of the columns (NT > 1)
 
@@ -351,11 +362,25 @@ struct Layer {
         lane = threadIdx.x % 32;
         g = lane / 4;
         t = lane % 4;
-        ring = mrr::smem_addr(sm) + warp * kStages * kStage;
+        // The copies' swizzle puts 16-byte piece c of row r at c ^ (r % 8).  16-bit weights: lanes g and
+        // g + 1 of a 128-byte read take rows 4 apart, and so the two halves of the banks.
+        row = g >> 1 | (g & 1) << 2;
+        lane_at = kMx ? row * 128 + row * 16 + 4 * t : row * 128 + ((t ^ row) << 4);
+        bars = mrr::smem_addr(sm + p.sm_bar) + warp * kStages * 8;
+        dead = false;
         act = reinterpret_cast<const uint16_t *>(sm + p.sm_act);
         start = reinterpret_cast<const uint16_t *>(sm + p.sm_start);
         cols = reinterpret_cast<const uint16_t *>(sm + p.sm_cols);
         tokens = sm + p.sm_tokens;
+        if (threadIdx.x < kWarps * kStages)   // the copies' bytes, and (scales) every lane's copy
+            mrr::mbar_init(mrr::smem_addr(sm + p.sm_bar) + threadIdx.x * 8, kMx ? 33 : 1);
+        mrr::mbar_init_fence();
+    }
+
+    __device__ __forceinline__ uint8_t *stage(int slot) const { return smem + (warp * kStages + slot) * kStage; }
+    __device__ __forceinline__ uint8_t *scales(int slot) const
+    {
+        return smem + p.sm_scales + (warp * kStages + slot) * kStageScales;
     }
 
     __device__ void sizes(int active)
@@ -369,33 +394,22 @@ struct Layer {
         // an expert's K is cut into shares, taken by the warps in turn: single chunks, or (where a
         // change of expert costs something) as few as give every warp four or more
         down_parts = NT == 1 ? down_chunks : min(down_chunks, (4 * kWarps + nact - 1) / nact);
-        up_row = kMx ? p.H / 2 : 2 * (int64_t)p.H;
-        down_row = kMx ? p.I / 2 : 2 * (int64_t)p.I;
     }
 
     // point the cursor at the rows of its item and expert
     __device__ __forceinline__ void aim(Cursor &c) const
     {
+        const int r = lane % 16;
         if (c.phase == 0) {
-            const int i0 = (c.item - c.expert * up_tiles) * 16, left = p.I - i0;
-            const int64_t row0 = (int64_t)act[c.expert] * 2 * p.I + i0;
-            c.src = static_cast<const uint8_t *>(p.w13) + (row0 + lane / 8) * up_row + lane % 8 * 16;
+            const int i0 = (c.item - c.expert * up_tiles) * 16;
+            c.row = act[c.expert] * 2 * p.I + i0;
             if (kMx)
-                c.scale_src = p.w13_s + (row0 + lane % 16 + (lane >= 16 ? p.I : 0)) * scale_row_bytes(p.H);
-            c.rows = lane % 16 < left ? 256u : 0u;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                c.rows |= (4 * j + lane / 8) % 16 < left ? 1u << j : 0u;
+                c.scale_src = i0 + r < p.I ? p.w13_s + (int64_t)(c.row + r + lane / 16 * p.I) * scale_row_bytes(p.H) : nullptr;
         } else if (c.phase == 1) {
-            const int n0 = c.item * 16, left = p.H - n0;
-            const int64_t row0 = (int64_t)act[c.expert] * p.H + n0;
-            c.src = static_cast<const uint8_t *>(p.w2) + (row0 + lane / 16) * down_row + lane % 16 * 16;
+            const int n0 = c.item * 16;
+            c.row = act[c.expert] * p.H + n0;
             if (kMx)
-                c.scale_src = p.w2_s + (row0 + lane / 2) * scale_row_bytes(p.I) + lane % 2 * 8;
-            c.rows = lane / 2 < left ? 256u : 0u;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                c.rows |= 2 * j + lane / 16 < left ? 1u << j : 0u;
+                c.scale_src = n0 + r < p.H ? p.w2_s + (int64_t)(c.row + r) * scale_row_bytes(p.I) + lane / 16 * 8 : nullptr;
         }
     }
 
@@ -472,63 +486,63 @@ struct Layer {
         aim(c);
     }
 
-    // start the copies of the cursor's unit into stage `slot`, 16-byte pieces exchanged inside a row
-    // so that the reads in multiply() meet no bank twice
+    // bytes b0 .. b0 + n - 1 of a row of `bytes` bytes, loaded one element at a time; past its end 0
+    template <int n>
+    __device__ __forceinline__ void load_narrow(uint32_t (&v)[n / 4], const uint8_t *row, int64_t b0, int64_t bytes) const
+    {
+#pragma unroll
+        for (int i = 0; i < n / 4; ++i)
+            v[i] = 0u;
+        for (int b = 0; b < n; b += kMx ? 1 : 2)
+            if (b0 + b < bytes)
+                v[b / 4] |= (kMx ? (uint32_t)__ldg(row + b0 + b)
+                                 : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row + b0 + b)))
+                            << (8 * (b % 4));
+    }
+
+    // start bringing the cursor's unit into stage `slot`: slab 0 holds the gate rows or the chunk's first
+    // 128 bytes, slab 1 the up rows or the other 128 bytes
     template <bool kUp>
     __device__ __forceinline__ void fill(int slot, const Cursor &c) const
     {
-        constexpr int kRow = kUp ? kUpRow : kDownRow, kPieces = kRow / 16, kStep = 32 / kPieces;
-        const bool wide = kUp ? p.w13_wide : p.w2_wide, s_wide = kUp ? p.s13_wide : p.s2_wide;
-        const uint8_t *none = static_cast<const uint8_t *>(kUp ? p.w13 : p.w2);
-        const int64_t row_bytes = kUp ? up_row : down_row, at = (int64_t)c.chunk * kRow;
-        const int piece = lane % kPieces;
-        const int64_t left = row_bytes - at - piece * 16;   // bytes of the row from this lane's piece on
-        const uint32_t base = ring + slot * kStage;
-        const uint32_t rows = left > 0 ? c.rows : 0u;
-        const uint8_t *src = c.src + at;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int r = j * kStep + lane / kPieces;
-            const uint32_t dst = base + r * kRow + ((kMx ? piece ^ (r & 7) : piece ^ ((r & 1) << 2)) << 4);
-            const bool ok = rows >> j & 1u;
-            if (wide) {
-                copy16(dst, ok ? src : none, ok);
-            } else {
-                uint32_t v[4] = {0u, 0u, 0u, 0u};
-                if (ok) {
-                    if (kMx) {
-                        for (int b = 0; b < 16; ++b)
-                            if (b < left)
-                                v[b / 4] |= (uint32_t)__ldg(src + b) << (8 * (b % 4));
-                    } else {
-                        for (int b = 0; b < 8; ++b)
-                            if (2 * b < left)
-                                v[b / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(src) + b) << (16 * (b % 2));
-                    }
-                }
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                             "r"(v[3])
-                             : "memory");
+        const uint32_t to = mrr::smem_addr(stage(slot)), bar = bars + 8 * slot;
+        if (kWide) {
+            if (lane == 0) {
+                mrr::mbar_arrive_expect_tx(bar, 2 * kSlab);
+                const CUtensorMap *map = kUp ? &p.w13_map : &p.w2_map;
+                tc::load_box(to, map, c.chunk * (kUp ? 128 : 256), c.row, bar);
+                tc::load_box(to + kSlab, map, c.chunk * (kUp ? 128 : 256) + (kUp ? 0 : 128), c.row + (kUp ? p.I : 0), bar);
             }
-            src += kStep * row_bytes;
-            if (kUp && j == 3)   // from the 16 gate rows to the up rows
-                src += (p.I - 16) * row_bytes;
+        } else {   // rows that no 16-byte access fits: element by element, laid out as the copies would
+            const int n = (kUp ? p.I : p.H) - (kUp ? c.row - act[c.expert] * 2 * p.I : c.row - act[c.expert] * p.H);
+            const int K = kUp ? p.H : p.I;
+            const int64_t bytes = kMx ? K / 2 : 2 * (int64_t)K;
+#pragma unroll 1
+            for (int i = lane; i < 256; i += 32) {
+                const int slab = i / 128, r = i / 8 % 16, piece = i % 8;
+                uint32_t v[4] = {0u, 0u, 0u, 0u};
+                if (r < n)
+                    load_narrow<16>(v, static_cast<const uint8_t *>(kUp ? p.w13 : p.w2) + (int64_t)(c.row + r + (kUp ? slab * p.I : 0)) * bytes,
+                                    (int64_t)c.chunk * (kUp ? 128 : 256) + (kUp ? 0 : slab * 128) + piece * 16, bytes);
+                *reinterpret_cast<uint4 *>(stage(slot) + slab * kSlab + r * 128 + ((piece ^ (r & 7)) << 4)) =
+                    make_uint4(v[0], v[1], v[2], v[3]);
+            }
         }
-        if (kMx) {   // 8 scale bytes a lane: row lane (32 rows of 8), or row lane / 2 (16 rows of 16)
-            const int64_t s_at = (int64_t)c.chunk * (kUp ? 8 : 16);
-            const int64_t s_left = scale_row_bytes(kUp ? p.H : p.I) - s_at - (kUp ? 0 : lane % 2 * 8);
-            const bool ok = s_left > 0 && c.rows >> 8;
-            const uint32_t dst = base + 4096 + lane * 8;
-            const uint8_t *s = c.scale_src + s_at;
-            if (s_wide) {
-                copy8(dst, ok ? s : none, ok);
+        if (kMx) {   // 8 scale bytes a lane: [slab][row]
+            const int64_t at = (int64_t)c.chunk * (kUp ? 8 : 16), left = scale_row_bytes(kUp ? p.H : p.I) - at - (kUp ? 0 : lane / 16 * 8);
+            const bool ok = c.scale_src && left > 0;
+            if (kWide && (kUp ? p.s13_wide : p.s2_wide)) {
+                copy8(mrr::smem_addr(scales(slot)) + lane * 8, ok ? c.scale_src + at : p.w13_s, ok);
+                copies_arrive(bar);
             } else {
                 uint32_t v[2] = {0u, 0u};
                 if (ok)
                     for (int b = 0; b < 8; ++b)
-                        if (b < s_left)
-                            v[b / 4] |= (uint32_t)__ldg(s + b) << (8 * (b % 4));
-                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(v[0]), "r"(v[1]) : "memory");
+                        if (b < left)
+                            v[b / 4] |= (uint32_t)__ldg(c.scale_src + at + b) << (8 * (b % 4));
+                *reinterpret_cast<uint2 *>(scales(slot) + lane * 8) = make_uint2(v[0], v[1]);
+                if (kWide)
+                    tc::mbar_arrive(bar);
             }
         }
     }
@@ -539,15 +553,28 @@ struct Layer {
             fill<true>(slot, c);
         else if (c.phase == 1)
             fill<false>(slot, c);
-        copy_commit();
         if (c.phase < 2)
             advance(c);
     }
 
-    template <typename V>
-    __device__ __forceinline__ V stage_word(int slot, int at) const
+    // the stage's copies have landed
+    __device__ __forceinline__ void landed(int slot, uint32_t parity)
     {
-        return *reinterpret_cast<const V *>(smem + (warp * kStages + slot) * kStage + at);
+        if (kWide && !dead) {
+            uint64_t t0 = 0;   // the timer is slow to read: not before a wait has become a long one
+            for (uint32_t it = 1; !mrr::mbar_try_wait(bars + 8 * slot, parity); ++it)
+                if (it % 1024 == 0) {
+                    const uint64_t now = mrr::global_timer_ns();
+                    if (t0 == 0)
+                        t0 = now;
+                    else if (now - t0 > kWaitLimitNs) {
+                        dead = true;
+                        break;
+                    }
+                }
+            dead = __any_sync(kFull, dead);
+        }
+        __syncwarp();
     }
 
     // Token operands of kGroups groups of 32 k for kCols column tiles: this lane's 8 elements of each.
@@ -557,34 +584,38 @@ struct Layer {
         uint4 v[kCols][kGroups];
     };
     // a stage is worked off in batches of kGroups groups
+    static constexpr int kSlabGroups = kSlabK / 32;
     static constexpr int kUpGroups = kMx ? 4 : 2, kUpBatches = kMx ? 2 : 1;
     static constexpr int kDownGroups = 4, kDownBatches = kMx ? 4 : 1;
 
-    // The products of groups q0 .. q0 + kGroups - 1 of a stage: kTiles 16-row tiles against column tiles
-    // j0 .. j0 + kN - 1.  kWhole: all groups lie before K, and (kMx) no scale is 0 or NaN.
-    template <bool kWhole, int kN, int kTiles, int kRow, int kGroups>
+    // The products of groups q0 .. q0 + kGroups - 1 of a stage: two row tiles, one a slab (kUp), or one
+    // whose K runs on from slab to slab, against column tiles j0 .. j0 + kN - 1.  kWhole: all groups lie
+    // before K, and (kMx) no scale is 0 or NaN.
+    template <bool kWhole, int kN, bool kUp, int kGroups>
     __device__ __forceinline__ void multiply_groups(int slot, int q0, int left, int j0, const Tokens<kGroups> &b,
                                                     const uint32_t (&sc)[2][2], float (&acc)[2][NT][4]) const
     {
+        constexpr int kTiles = kUp ? 2 : 1;
+        const int stage_at = (warp * kStages + slot) * kStage + lane_at;   // a multiple of 1024, and lane_at
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             if (!kWhole && 32 * i >= left)
                 break;
-            const int q = q0 + i;
+            const int q = (q0 + i) % kSlabGroups, slab = kUp ? 0 : (q0 + i) / kSlabGroups;
+            const uint8_t *from = smem + (stage_at ^ (kMx ? q << 4 : q << 6)) + slab * kSlab;
             uint32_t a[kTiles][2][4];
             float s[2][2];
 #pragma unroll
             for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int row = 16 * m + 8 * r + g;
+                for (int r = 0; r < 2; ++r) {   // slab rows `row` and `row` + 8
                     if (kMx) {
-                        codes_to_half(stage_word<uint32_t>(slot, row * kRow + ((q ^ (row & 7)) << 4) + 4 * t), a[m][r]);
+                        codes_to_half(*reinterpret_cast<const uint32_t *>(from + m * kSlab + r * 1024), a[m][r]);
                         // byte i of sc, as a float's exponent
                         s[m][r] = kWhole ? __uint_as_float((i < 3 ? sc[m][r] << (23 - 8 * i) : sc[m][r] >> 1) & 0x7f800000u)
                                          : e8m0_value(sc[m][r] >> (8 * i) & 255u);
                     } else {
-                        const uint4 v = stage_word<uint4>(slot, row * kRow + (((4 * q + t) ^ ((row & 1) << 2)) << 4));
+                        const uint4 v = *reinterpret_cast<const uint4 *>(from + m * kSlab + r * 1024);
                         a[m][r][0] = v.x, a[m][r][1] = v.y, a[m][r][2] = v.z, a[m][r][3] = v.w;
                     }
                 }
@@ -594,10 +625,10 @@ struct Layer {
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m) {
                     // one row tile: two chains of sums, so that an instruction waits for the last but one
-                    float(&to)[4] = acc[kTiles == 2 ? m : i % 2][j0 + j];
-                    if (kMx) {
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma<MDT>(d, a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], x.x, x.y);
+                    float(&to)[4] = acc[kUp ? m : i % 2][j0 + j];
+                    if constexpr (kMx) {
+                        float d[4];
+                        mma_first<MDT>(d, a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], x.x, x.y);
                         mma<MDT>(d, a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], x.z, x.w);
                         to[0] = fmaf(s[m][0], d[0], to[0]);
                         to[1] = fmaf(s[m][0], d[1], to[1]);
@@ -613,33 +644,34 @@ struct Layer {
     }
 
     // column tiles j0 .. of nt, at most kCols of them; left: elements of K from the first group on
-    template <int kTiles, int kRow, int kGroups>
+    template <bool kUp, int kGroups>
     __device__ __forceinline__ void multiply(int slot, int q0, int left, int j0, int nt, const Tokens<kGroups> &b,
                                              float (&acc)[2][NT][4]) const
     {
         bool whole = left >= 32 * kGroups;
-        uint32_t sc[2][2] = {};   // 4 scale bytes of rows g and g + 8
+        uint32_t sc[2][2] = {};   // 4 scale bytes of rows `row` and `row` + 8
         if (kMx) {
+            const uint8_t *from = scales(slot) + row * 8 + (kUp ? q0 : q0 / 8 * 128 + q0 % 8);
             bool odd = false;
 #pragma unroll
-            for (int m = 0; m < kTiles; ++m)
+            for (int m = 0; m < (kUp ? 2 : 1); ++m)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    sc[m][r] = stage_word<uint32_t>(slot, 4096 + (16 * m + 8 * r + g) * (kRow / 16) + q0);
+                    sc[m][r] = *reinterpret_cast<const uint32_t *>(from + m * 128 + r * 64);
                     odd |= special_bytes(sc[m][r]);
                 }
             whole = whole && !__any_sync(kFull, odd);
         }
         if (kCols == 1 || j0 + 1 >= nt) {
             if (whole)
-                multiply_groups<true, 1, kTiles, kRow, kGroups>(slot, q0, left, j0, b, sc, acc);
+                multiply_groups<true, 1, kUp, kGroups>(slot, q0, left, j0, b, sc, acc);
             else
-                multiply_groups<false, 1, kTiles, kRow, kGroups>(slot, q0, left, j0, b, sc, acc);
+                multiply_groups<false, 1, kUp, kGroups>(slot, q0, left, j0, b, sc, acc);
         } else {
             if (whole)
-                multiply_groups<true, kCols, kTiles, kRow, kGroups>(slot, q0, left, j0, b, sc, acc);
+                multiply_groups<true, kCols, kUp, kGroups>(slot, q0, left, j0, b, sc, acc);
             else
-                multiply_groups<false, kCols, kTiles, kRow, kGroups>(slot, q0, left, j0, b, sc, acc);
+                multiply_groups<false, kCols, kUp, kGroups>(slot, q0, left, j0, b, sc, acc);
         }
     }
 
@@ -698,9 +730,9 @@ struct Layer {
     }
 
     // this warp's 16 x 8 partial sums into red[.][warp][tile][row][column]
-    __device__ __forceinline__ void put(float *r, int tile, const float (&d)[4]) const
+    __device__ __forceinline__ void put(float *r, int tile, const float (&d)[4], int row_) const
     {
-        float *at = r + (warp * 2 + tile) * 128 + g * 8 + 2 * t;
+        float *at = r + (warp * 2 + tile) * 128 + row_ * 8 + 2 * t;
         *reinterpret_cast<float2 *>(at) = make_float2(d[0], d[1]);
         *reinterpret_cast<float2 *>(at + 64) = make_float2(d[2], d[3]);
     }
@@ -785,7 +817,7 @@ struct Layer {
         for (int j = 0; j < NT; ++j) {
             if (8 * j >= p.T)
                 break;
-            put(red(j % 2), 0, acc[j]);
+            put(red(j % 2), 0, acc[j], g);
             __syncthreads();
             if (threadIdx.x < 128) {
                 const int row = threadIdx.x % 16, col = threadIdx.x / 16, tok = 8 * j + col;
@@ -957,20 +989,33 @@ struct Layer {
         }
         sizes(columns(expert));
 
+        tc::fence_to_async();   // the rings were scratch memory so far
+        __syncthreads();
         Cursor next = first_unit();
-        int slot = 0, fill_slot = 0;
+        int slot = 0, fill_slot = 0, filled = 0;
+        uint32_t parity = 0u;
         auto issue_next = [&]() {
+            filled += next.phase < 2;
             issue(next, fill_slot);
             fill_slot = fill_slot + 1 == kStages ? 0 : fill_slot + 1;
         };
         // take the next stage: its copies have landed, and every lane is done with the one before
         auto take = [&]() {
-            copy_wait<kStages - 2>();
-            __syncwarp();
+            landed(slot, parity);
             issue_next();
+            --filled;
             const int s = slot;
             slot = slot + 1 == kStages ? 0 : slot + 1;
+            parity ^= slot == 0;
             return s;
+        };
+        // before leaving early: wait for what is in flight
+        auto drain = [&]() {
+            for (; filled > 0; --filled) {
+                landed(slot, parity);
+                slot = slot + 1 == kStages ? 0 : slot + 1;
+                parity ^= slot == 0;
+            }
         };
         for (int s = 0; s < kStages - 1; ++s)
             issue_next();
@@ -978,14 +1023,14 @@ struct Layer {
         int buf = 0;
         for (int item = blockIdx.x; item < up_items; item += gridDim.x) {
             const int ai = item / up_tiles, i0 = (item - ai * up_tiles) * 16, nt = tiles_of(ai);
-            const uint16_t *row[NT];
+            const uint16_t *x_row[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                row[j] = j < nt && column_of(ai, 8 * j + g) >= 0 ? p.xh + (int64_t)token_of(ai, 8 * j + g) * p.Hp : nullptr;
+                x_row[j] = j < nt && column_of(ai, 8 * j + g) >= 0 ? p.xh + (int64_t)token_of(ai, 8 * j + g) * p.Hp : nullptr;
             auto column = [&](int j, int k) {
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (row[j])
-                    v = *reinterpret_cast<const uint4 *>(row[j] + k);
+                if (x_row[j])
+                    v = *reinterpret_cast<const uint4 *>(x_row[j] + k);
                 return v;
             };
             float acc[2][NT][4] = {};
@@ -1004,7 +1049,7 @@ struct Layer {
                             break;
                         if (j > 0)
                             fetch(b, j, nt, k0, p.H, column);
-                        multiply<2, kUpRow>(at, h * kUpGroups, p.H - k0, j, nt, b, acc);
+                        multiply<true>(at, h * kUpGroups, p.H - k0, j, nt, b, acc);
                     }
                 }
             }
@@ -1012,8 +1057,8 @@ struct Layer {
             for (int j = 0; j < NT; ++j) {
                 if (j >= nt)
                     break;
-                put(red(buf), 0, acc[0][j]);
-                put(red(buf), 1, acc[1][j]);
+                put(red(buf), 0, acc[0][j], row);
+                put(red(buf), 1, acc[1][j], row);
                 __syncthreads();
                 if (threadIdx.x < 128) {
                     const int r = threadIdx.x % 16, c = threadIdx.x / 16, a = column_of(ai, 8 * j + c);
@@ -1021,7 +1066,8 @@ struct Layer {
                         const int tok = token_of(ai, 8 * j + c);
                         const float s = kMx ? p.x_scale[tok] : 1.f;
                         const float gate = gather(red(buf), 0, r, c) * s, upv = gather(red(buf), 1, r, c) * s;
-                        float h = gate / (1.f + expf(-gate)) * upv * weight[a];
+                        // rows past I: what the copy brought there is another row's
+                        float h = i0 + r < p.I ? gate / (1.f + expf(-gate)) * upv * weight[a] : 0.f;
                         if (kScaled) {
                             const uint32_t half = 0xffffu << (threadIdx.x & 16);
                             const uint32_t m = __reduce_max_sync(half, __float_as_uint(h) & 0x7fffffffu);
@@ -1039,7 +1085,7 @@ struct Layer {
             }
         }
         if (!grid_wait(p, 2, s_ok)) {
-            copy_wait<0>();
+            drain();
             if (threadIdx.x == 0)
                 atomicOr(p.status, mrr_ws::kFlagTimeout);
             return;
@@ -1074,13 +1120,13 @@ struct Layer {
                                 a = column_of(w.expert, g);
                             fetch(ahead, 0, some, w.chunk * kDownK, p.I, column);
                         }
-                        multiply<1, kDownRow>(at, h * kDownGroups, p.I - kb, 0, 1, b, acc);
+                        multiply<false>(at, h * kDownGroups, p.I - kb, 0, 1, b, acc);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     acc[0][0][i] += acc[1][0][i];
-                put(red(buf), 0, acc[0][0]);
+                put(red(buf), 0, acc[0][0], row);
                 __syncthreads();
                 if (threadIdx.x < 128) {
                     const int r = threadIdx.x % 16, tok = threadIdx.x / 16, n = item * 16 + r;
@@ -1132,7 +1178,7 @@ struct Layer {
                                     break;
                                 if (j > 0)
                                     fetch(b, j, tiles, kb, p.I, column);
-                                multiply<1, kDownRow>(at, h * kDownGroups, p.I - kb, j, tiles, b, acc);
+                                multiply<false>(at, h * kDownGroups, p.I - kb, j, tiles, b, acc);
                             }
                         }
                     }
@@ -1148,7 +1194,7 @@ struct Layer {
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
                             if (8 * j + 2 * t + c < count) {
-                                float *to = mine + tokens[first + 8 * j + 2 * t + c] * kPitch + g;
+                                float *to = mine + tokens[first + 8 * j + 2 * t + c] * kPitch + row;
                                 to[0] += acc[0][j][c] + acc[1][j][c];
                                 to[8] += acc[0][j][2 + c] + acc[1][j][2 + c];
                             }
@@ -1170,21 +1216,22 @@ struct Layer {
                 __syncthreads();
             }
         }
-        copy_wait<0>();
+        if (dead && lane == 0)   // every unit was waited for, or given up
+            atomicOr(p.status, mrr_ws::kFlagTimeout);
     }
 };
 
-template <int DT, int WDT, int NT>
+template <int DT, int WDT, int NT, bool kWide>
 __global__ void __launch_bounds__(kThreads, 1) layer_kernel(const __grid_constant__ Params p)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
-    Layer<DT, WDT, NT>(p, smem).run();
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Layer<DT, WDT, NT, kWide>(p, smem).run();
 }
 
 template <int DT, int WDT, int NT>
 cudaError_t launch_one(const Params &p, int grid, size_t smem, cudaStream_t s)
 {
-    auto kernel = layer_kernel<DT, WDT, NT>;
+    auto kernel = p.w13_wide && p.w2_wide ? layer_kernel<DT, WDT, NT, true> : layer_kernel<DT, WDT, NT, false>;
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess)
         return err;

@@ -619,28 +619,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::dealloc(tmem, kColumns);
 }
 
-// a 2-D map of `rows` rows of row_bytes bytes, boxes of 128 bytes by box_rows, 128-byte swizzle
-bool make_map(CUtensorMap *map, const uint8_t *base, int64_t rows, int64_t row_bytes, int box_rows)
-{
-    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static const Encode encode = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<Encode>(f);
-    }();
-    const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
-    const cuuint32_t box[2] = {kStepBytes, (cuuint32_t)box_rows}, one[2] = {1, 1};
-    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dims, strides, box, one,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool kGated, int kOut>
 cudaError_t launch(const Params &p, const CUtensorMap &x_map, const CUtensorMap &w_map, int grid, size_t smem, cudaStream_t s)
 {
@@ -716,8 +694,8 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
     if (p.stages < 2)
         return MRR_ERR_CUDA;
     CUtensorMap x_map, w_map;
-    if (!make_map(&w_map, w_codes, E * N * (gated ? 2 : 1), K / 2, kRowTile) ||
-        !make_map(&x_map, A ? codes : w_codes, A ? A : 1, K / 2, kBoxRows))
+    if (!tc::make_map(&w_map, w_codes, E * N * (gated ? 2 : 1), K / 2, kRowTile) ||
+        !tc::make_map(&x_map, A ? codes : w_codes, A ? A : 1, K / 2, kBoxRows))
         return MRR_ERR_CUDA;
     const size_t smem = (size_t)p.sm_stage + (size_t)p.stages * stage_bytes(p.tokens);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
