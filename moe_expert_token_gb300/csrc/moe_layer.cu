@@ -31,8 +31,8 @@ Layout layout(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
         return off;
     };
     Layout l;
-    l.Hp = (int)mrr_ws::round_up(H, 32);   // the products read whole groups of 32
-    l.Ip = (int)mrr_ws::round_up(I, 16);   // and h is written 16 rows at a time
+    l.Hp = (int)mrr_ws::round_up(H, 256);   // the products read whole stages, of up to 256 elements
+    l.Ip = (int)mrr_ws::round_up(I, 512);   // of x and 512 of h
     l.flags = take(3 * kMaxGrid * 8);
     l.part = take(kMaxParts * T * E * 4);
     l.xh = take(T * l.Hp * 2);

@@ -577,32 +577,69 @@ struct Layer {
         __syncwarp();
     }
 
-    // Token operands of kGroups groups of 32 k for kCols column tiles: this lane's 8 elements of each.
-    static constexpr int kCols = NT == 1 ? 1 : 2;
+    // Token operands of one stage, kGroups groups of 32 k, for kCols column tiles: this lane's 8 elements
+    // of each.  Every register is loaded with the next stage's value as soon as it has been used, so
+    // that a stage's time hides the loads.
+    static constexpr int kCols = NT == 1 || kMx ? 1 : 2;
+    static constexpr int kSlabGroups = kSlabK / 32, kUpGroups = kUpK / 32, kDownGroups = kDownK / 32;
     template <int kGroups>
     struct Tokens {
         uint4 v[kCols][kGroups];
+        uint32_t tile[kCols][kGroups];   // exponents of the tiles' powers of two (h in float16)
     };
-    // a stage is worked off in batches of kGroups groups
-    static constexpr int kSlabGroups = kSlabK / 32;
-    static constexpr int kUpGroups = kMx ? 4 : 2, kUpBatches = kMx ? 2 : 1;
-    static constexpr int kDownGroups = 4, kDownBatches = kMx ? 4 : 1;
+    // Where a column's operands come from, this lane's part: null pointers for a column that is not there.
+    struct Column {
+        const uint16_t *v = nullptr;
+        const uint8_t *tile = nullptr;
+        uint32_t field = 127u;           // exponent of the power of two that the token's sums carry
+    };
 
-    // The products of groups q0 .. q0 + kGroups - 1 of a stage: two row tiles, one a slab (kUp), or one
-    // whose K runs on from slab to slab, against column tiles j0 .. j0 + kN - 1.  kWhole: all groups lie
-    // before K, and (kMx) no scale is 0 or NaN.
-    template <bool kWhole, int kN, bool kUp, int kGroups>
-    __device__ __forceinline__ void multiply_groups(int slot, int q0, int left, int j0, const Tokens<kGroups> &b,
-                                                    const uint32_t (&sc)[2][2], float (&acc)[2][NT][4]) const
+    template <bool kUp, int kGroups>
+    __device__ __forceinline__ void load(Tokens<kGroups> &b, int j, int i, const Column &c, int k0) const
     {
-        constexpr int kTiles = kUp ? 2 : 1;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (c.v)
+            v = *reinterpret_cast<const uint4 *>(c.v + k0 + 32 * i);
+        b.v[j][i] = v;
+        if (!kUp && kScaled) {
+            uint32_t f = 253u;
+            if (c.v)
+                f = c.tile[k0 / 16 + 2 * i];
+            b.tile[j][i] = f;
+        }
+    }
+
+    template <bool kUp, int kGroups>
+    __device__ __forceinline__ void load_all(Tokens<kGroups> &b, const Column (&c)[kCols], int k0) const
+    {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+                load<kUp>(b, j, i, c[j], k0);
+    }
+
+    // The products of a stage: two row tiles, one a slab (kUp), or one whose K runs on from slab to slab,
+    // against column tiles j0 .. j0 + kN - 1.  kNext: their operands are b, which is loaded anew from
+    // `next` at k1; else they are loaded here from `now` at k1, four groups at a time, into b's first.
+    // kExact: a scale is 0 or NaN (kMx).  Past K both operands are zeros.
+    template <bool kUp, bool kExact, int kN, bool kNext, int kGroups, int kHeld>
+    __device__ __forceinline__ void multiply_as(int slot, int j0, Tokens<kHeld> &b, const Column (&now)[kCols],
+                                                const Column (&next)[kCols], int k1, const uint32_t (&sc)[2][2][4],
+                                                float (&acc)[2][NT][4]) const
+    {
+        constexpr int kTiles = kUp ? 2 : 1, kBatch = kGroups < 4 ? kGroups : 4;
         const int stage_at = (warp * kStages + slot) * kStage + lane_at;   // a multiple of 1024, and lane_at
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            if (!kWhole && 32 * i >= left)
-                break;
-            const int q = (q0 + i) % kSlabGroups, slab = kUp ? 0 : (q0 + i) / kSlabGroups;
+            const int q = i % kSlabGroups, slab = kUp ? 0 : i / kSlabGroups;
             const uint8_t *from = smem + (stage_at ^ (kMx ? q << 4 : q << 6)) + slab * kSlab;
+            if (!kNext && i % kBatch == 0)
+#pragma unroll
+                for (int j = 0; j < kN; ++j)
+#pragma unroll
+                    for (int h = 0; h < kBatch; ++h)
+                        load<kUp>(b, j, h, now[j], k1 + 32 * i);
             uint32_t a[kTiles][2][4];
             float s[2][2];
 #pragma unroll
@@ -611,9 +648,9 @@ struct Layer {
                 for (int r = 0; r < 2; ++r) {   // slab rows `row` and `row` + 8
                     if (kMx) {
                         codes_to_half(*reinterpret_cast<const uint32_t *>(from + m * kSlab + r * 1024), a[m][r]);
-                        // byte i of sc, as a float's exponent
-                        s[m][r] = kWhole ? __uint_as_float((i < 3 ? sc[m][r] << (23 - 8 * i) : sc[m][r] >> 1) & 0x7f800000u)
-                                         : e8m0_value(sc[m][r] >> (8 * i) & 255u);
+                        const uint32_t w = sc[m][r][i / 4], at = i % 4;   // byte `at`, as a float's exponent
+                        s[m][r] = kExact ? e8m0_value(w >> (8 * at) & 255u)
+                                         : __uint_as_float((at < 3 ? w << (23 - 8 * at) : w >> 1) & 0x7f800000u);
                     } else {
                         const uint4 v = *reinterpret_cast<const uint4 *>(from + m * kSlab + r * 1024);
                         a[m][r][0] = v.x, a[m][r][1] = v.y, a[m][r][2] = v.z, a[m][r][3] = v.w;
@@ -621,7 +658,12 @@ struct Layer {
                 }
 #pragma unroll
             for (int j = 0; j < kN; ++j) {
-                const uint4 x = b.v[j][i];
+                const int at = kNext ? i : i % kBatch;
+                uint4 x = b.v[j][at];
+                if (!kUp && kScaled) {   // the token's power of two over the tile's: at most 1
+                    const __half2 f = __float2half2_rn(field_value(127u - min(b.tile[j][at] - now[j].field, 126u)));
+                    x = make_uint4(half2_mul(x.x, f), half2_mul(x.y, f), half2_mul(x.z, f), half2_mul(x.w, f));
+                }
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m) {
                     // one row tile: two chains of sums, so that an instruction waits for the last but one
@@ -640,52 +682,60 @@ struct Layer {
                     }
                 }
             }
+            if (kNext)
+#pragma unroll
+                for (int j = 0; j < kCols; ++j)
+                    load<kUp>(b, j, i, next[j], k1);
         }
     }
 
-    // column tiles j0 .. of nt, at most kCols of them; left: elements of K from the first group on
-    template <bool kUp, int kGroups>
-    __device__ __forceinline__ void multiply(int slot, int q0, int left, int j0, int nt, const Tokens<kGroups> &b,
-                                             float (&acc)[2][NT][4]) const
+    template <bool kUp, int kN, bool kNext, int kGroups, int kHeld>
+    __device__ __forceinline__ void multiply(int slot, int j0, Tokens<kHeld> &b, const Column (&now)[kCols],
+                                             const Column (&next)[kCols], int k1, float (&acc)[2][NT][4]) const
     {
-        bool whole = left >= 32 * kGroups;
-        uint32_t sc[2][2] = {};   // 4 scale bytes of rows `row` and `row` + 8
-        if (kMx) {
-            const uint8_t *from = scales(slot) + row * 8 + (kUp ? q0 : q0 / 8 * 128 + q0 % 8);
+        uint32_t sc[2][2][4];   // scale bytes of rows `row` and `row` + 8
+        if constexpr (kMx) {
             bool odd = false;
 #pragma unroll
             for (int m = 0; m < (kUp ? 2 : 1); ++m)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    sc[m][r] = *reinterpret_cast<const uint32_t *>(from + m * 128 + r * 64);
-                    odd |= special_bytes(sc[m][r]);
-                }
-            whole = whole && !__any_sync(kFull, odd);
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int h = 0; h < (kUp ? 1 : 2); ++h) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(scales(slot) + (kUp ? m : h) * 128 + r * 64 + row * 8);
+                        sc[m][r][2 * h] = v.x, sc[m][r][2 * h + 1] = v.y;
+                        odd |= special_bytes(v.x) || special_bytes(v.y);
+                    }
+            if (__any_sync(kFull, odd)) {
+                multiply_as<kUp, true, kN, kNext, kGroups>(slot, j0, b, now, next, k1, sc, acc);
+                return;
+            }
         }
-        if (kCols == 1 || j0 + 1 >= nt) {
-            if (whole)
-                multiply_groups<true, 1, kUp, kGroups>(slot, q0, left, j0, b, sc, acc);
-            else
-                multiply_groups<false, 1, kUp, kGroups>(slot, q0, left, j0, b, sc, acc);
-        } else {
-            if (whole)
-                multiply_groups<true, kCols, kUp, kGroups>(slot, q0, left, j0, b, sc, acc);
-            else
-                multiply_groups<false, kCols, kUp, kGroups>(slot, q0, left, j0, b, sc, acc);
-        }
+        multiply_as<kUp, false, kN, kNext, kGroups>(slot, j0, b, now, next, k1, sc, acc);
     }
 
-    // fetch token operands from k0 on; column(j, k): the 8 elements k .. k + 7 of this lane's column of tile j
-    template <int kGroups, typename Column>
-    __device__ __forceinline__ void fetch(Tokens<kGroups> &b, int j0, int nt, int k0, int K, Column column) const
+    // All nt column tiles of a stage: the first kCols, whose operands are b, and (rarely) more, whose
+    // operands are loaded here from column(tile) at k0.
+    template <bool kUp, int kGroups, typename Of>
+    __device__ __forceinline__ void multiply_all(int slot, int nt, Tokens<kGroups> &b, const Column (&now)[kCols],
+                                                 const Column (&next)[kCols], int k0, int k1, float (&acc)[2][NT][4],
+                                                 Of column) const
     {
+        if (kCols == 1 || nt == 1)
+            multiply<kUp, 1, true, kGroups>(slot, 0, b, now, next, k1, acc);
+        else
+            multiply<kUp, kCols, true, kGroups>(slot, 0, b, now, next, k1, acc);
 #pragma unroll
-        for (int j = 0; j < kCols; ++j)
-            if (j0 + j < nt)
-#pragma unroll
-                for (int i = 0; i < kGroups; ++i)
-                    if (k0 + 32 * i < K)
-                        b.v[j][i] = column(j0 + j, k0 + 32 * i + 8 * t);
+        for (int j = kCols; j < NT; j += kCols) {
+            if (j >= nt)
+                break;
+            Column more[kCols];
+            for (int c = 0; c < kCols; ++c)
+                if (j + c < nt)
+                    more[c] = column(j + c);
+            Tokens<kGroups < 4 ? kGroups : 4> x;
+            multiply<kUp, kCols, false, kGroups>(slot, j, x, more, more, k0, acc);
+        }
     }
 
     // token of column c of active expert ai, which exists
@@ -707,21 +757,31 @@ struct Layer {
         return NT == 1 ? 1 : ((int)start[ai + 1] - (int)start[ai] + 7) / 8;
     }
 
-    // Eight elements of h's row a as the matrix instructions take them.  With float16 a 16-element tile
-    // has its own power of two, and `field` is the exponent of the one that the token's sums carry.
-    __device__ __forceinline__ uint4 h8(int a, int k, uint32_t field) const
+    // column c (of this lane) of active expert ai: its row of x, and of h
+    __device__ __forceinline__ Column x_column(int ai, int tile) const
     {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (a >= 0 && k < p.Ip) {
-            v = *reinterpret_cast<const uint4 *>(p.h + (int64_t)a * p.Ip + k);
-            if (kScaled) {
-                const uint32_t tile = p.h_field[(int64_t)a * (p.Ip / 16) + k / 16];
-                // token's over tile's: at most 1; below 2^-24 nothing is left of the tile
-                const __half2 r = __float2half2_rn(field_value(127u - min(tile - field, 126u)));
-                v = make_uint4(half2_mul(v.x, r), half2_mul(v.y, r), half2_mul(v.z, r), half2_mul(v.w, r));
-            }
+        Column c;
+        if (column_of(ai, 8 * tile + g) >= 0)
+            c.v = p.xh + (int64_t)token_of(ai, 8 * tile + g) * p.Hp + 8 * t;
+        return c;
+    }
+
+    __device__ __forceinline__ Column h_column(int ai, int tile) const
+    {
+        Column c;
+        const int a = column_of(ai, 8 * tile + g);
+        if (a >= 0) {
+            c.v = p.h + (int64_t)a * p.Ip + 8 * t;
+            c.tile = p.h_field + (int64_t)a * (p.Ip / 16) + t / 2;
+            c.field = field_of(token_of(ai, 8 * tile + g));
         }
-        return v;
+        return c;
+    }
+
+    // the exponent of the power of two that token tok's down sums carry (float16)
+    __device__ __forceinline__ uint32_t field_of(int tok) const
+    {
+        return kScaled ? f16_scale_field(__ldcg(p.h_max + tok)) : 127u;
     }
 
     __device__ __forceinline__ float *red(int buf) const
@@ -748,7 +808,7 @@ struct Layer {
 
     // ------------------------------------------------------------ before the first wait
 
-    // x's row t as the products take it: 16-bit, zeros past H, scaled (kMx)
+    // x's row t as the products take it: 16-bit, zeros past H, scaled (kMx); and the ends of its h rows
     __device__ void prepare_row(int tok)
     {
         uint32_t *s_max = reinterpret_cast<uint32_t *>(smem + p.sm_red);
@@ -774,6 +834,13 @@ struct Layer {
         }
         if (threadIdx.x == 0)
             p.h_max[tok] = 0u;
+        const int end = (p.I + 15) / 16 * 16, pad = p.Ip - end;
+        for (int i = threadIdx.x; i < p.k * pad; i += kThreads) {
+            const int64_t a = (int64_t)tok * p.k + i / pad;
+            p.h[a * p.Ip + end + i % pad] = 0;
+            if (i % pad % 16 == 0)
+                p.h_field[a * (p.Ip / 16) + (end + i % pad) / 16] = 253;
+        }
         for (int c = threadIdx.x; c < p.Hp / 8; c += kThreads) {
             uint4 v = load8_raw(p.x, tok, p.H, 8 * c, p.x_wide);
             if (kMx) {
@@ -1021,37 +1088,29 @@ struct Layer {
             issue_next();
 
         int buf = 0;
+        auto x_columns = [&](Column (&c)[kCols], int ai) {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+                c[j] = j < tiles_of(ai) ? x_column(ai, j) : Column();
+        };
+        Column col[kCols], next_col[kCols];
+        Tokens<kUpGroups> ahead;   // the next unit's operands
+        if ((int)blockIdx.x < up_items && warp < up_units) {
+            x_columns(next_col, blockIdx.x / up_tiles);
+            load_all<true>(ahead, next_col, warp * kUpK);
+        }
         for (int item = blockIdx.x; item < up_items; item += gridDim.x) {
             const int ai = item / up_tiles, i0 = (item - ai * up_tiles) * 16, nt = tiles_of(ai);
-            const uint16_t *x_row[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                x_row[j] = j < nt && column_of(ai, 8 * j + g) >= 0 ? p.xh + (int64_t)token_of(ai, 8 * j + g) * p.Hp : nullptr;
-            auto column = [&](int j, int k) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (x_row[j])
-                    v = *reinterpret_cast<const uint4 *>(x_row[j] + k);
-                return v;
-            };
             float acc[2][NT][4] = {};
-            Tokens<kUpGroups> ahead;   // the next batch's, fetched while this one's are multiplied
-            fetch(ahead, 0, nt, warp * kUpK, p.H, column);
             for (int u = warp; u < up_units; u += kWarps) {
                 const int at = take();
-#pragma unroll
-                for (int h = 0; h < kUpBatches; ++h) {
-                    const int k0 = u * kUpK + h * kUpGroups * 32;
-                    Tokens<kUpGroups> b = ahead;
-                    fetch(ahead, 0, nt, h + 1 < kUpBatches ? k0 + kUpGroups * 32 : (u + kWarps) * kUpK, p.H, column);
-#pragma unroll
-                    for (int j = 0; j < NT; j += kCols) {
-                        if (j >= nt)
-                            break;
-                        if (j > 0)
-                            fetch(b, j, nt, k0, p.H, column);
-                        multiply<true>(at, h * kUpGroups, p.H - k0, j, nt, b, acc);
-                    }
+                int k1 = (u + kWarps) * kUpK;
+                if (u + kWarps >= up_units) {   // then comes the next item's first unit
+                    k1 = warp * kUpK;
+                    if (item + (int)gridDim.x < up_items)
+                        x_columns(next_col, (item + gridDim.x) / up_tiles);
                 }
+                multiply_all<true>(at, nt, ahead, col, next_col, u * kUpK, k1, acc, [&](int j) { return x_column(ai, j); });
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -1093,35 +1152,36 @@ struct Layer {
         if (threadIdx.x == 0)
             p.flags[blockIdx.x] = 0;
 
-        // the exponent of the power of two that token tok's sums carry (float16)
-        auto field_of = [&](int tok) { return kScaled ? f16_scale_field(__ldcg(p.h_max + tok)) : 127u; };
         if (NT == 1) {
             const uint32_t field = g < p.T ? field_of(g) : 127u;
+            Cursor w;   // where the operands in `b` come from
+            bool some = (int)blockIdx.x < down_items && first_chunk(w);
+            Column c[kCols], c1[kCols];
+            Tokens<kDownGroups> b;
+            auto enter = [&](Column &to) {
+                to = Column();
+                const int a = column_of(w.expert, g);
+                if (a >= 0) {
+                    to.v = p.h + (int64_t)a * p.Ip + 8 * t;
+                    to.tile = p.h_field + (int64_t)a * (p.Ip / 16) + t / 2;
+                }
+                to.field = field;
+            };
+            if (some) {
+                enter(c1[0]);
+                load_all<false>(b, c1, w.chunk * kDownK);
+            }
+            c[0].field = field;   // all that is still asked of the column whose operands are there
             for (int item = blockIdx.x; item < down_items; item += gridDim.x) {
                 float acc[2][NT][4] = {};
-                Cursor w;   // where `ahead` comes from
-                bool some = first_chunk(w);
-                int a = some ? column_of(w.expert, g) : -1;
-                auto column = [&](int, int k) { return h8(a, k, field); };
-                Tokens<kDownGroups> ahead;
-                fetch(ahead, 0, some, w.chunk * kDownK, p.I, column);
-                while (some) {
-                    const int at = take(), k0 = w.chunk * kDownK;
-#pragma unroll
-                    for (int h = 0; h < kDownBatches; ++h) {
-                        const int kb = k0 + h * kDownGroups * 32;
-                        Tokens<kDownGroups> b = ahead;
-                        if (h + 1 < kDownBatches) {
-                            fetch(ahead, 0, 1, kb + kDownGroups * 32, p.I, column);
-                        } else {
-                            const int e = w.expert;
-                            some = next_chunk(w);
-                            if (some && w.expert != e)
-                                a = column_of(w.expert, g);
-                            fetch(ahead, 0, some, w.chunk * kDownK, p.I, column);
-                        }
-                        multiply<false>(at, h * kDownGroups, p.I - kb, 0, 1, b, acc);
-                    }
+                for (bool more = some; more;) {
+                    const int at = take(), e = w.expert;
+                    more = next_chunk(w);
+                    if (!more)   // the next item starts over
+                        first_chunk(w);
+                    if (w.expert != e)
+                        enter(c1[0]);
+                    multiply_all<false>(at, 1, b, c, c1, 0, w.chunk * kDownK, acc, [&](int) { return Column(); });
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -1145,47 +1205,33 @@ struct Layer {
                 __syncwarp();
                 Cursor w;
                 bool some = first_chunk(w);
-                int a[NT];
-                uint32_t field[NT];
+                Column c[kCols], c1[kCols];
+                Tokens<kDownGroups> b;
                 auto enter = [&]() {   // the columns of expert w.expert
-                    const int nt = some ? tiles_of(w.expert) : 0;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        a[j] = j < nt ? column_of(w.expert, 8 * j + g) : -1;
-                        field[j] = kScaled && a[j] >= 0 ? field_of(token_of(w.expert, 8 * j + g)) : 127u;
-                    }
-                    return nt;
+                    for (int j = 0; j < kCols; ++j)
+                        c1[j] = some && j < tiles_of(w.expert) ? h_column(w.expert, j) : Column();
                 };
-                auto column = [&](int j, int k) { return h8(a[j], k, field[j]); };
-                int nt = enter();
-                Tokens<kDownGroups> ahead;
-                fetch(ahead, 0, nt, w.chunk * kDownK, p.I, column);
+                enter();
+                if (some)
+                    load_all<false>(b, c1, w.chunk * kDownK);
                 while (some) {   // one share of an expert's K
-                    const int ai = w.expert, tiles = nt;
+                    const int ai = w.expert, tiles = tiles_of(ai);
                     float acc[2][NT][4] = {};
-                    for (bool more = true; more; ++w.chunk) {
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j)
+                        c[j] = c1[j];
+                    for (bool more = true; more;) {
                         const int at = take(), k0 = w.chunk * kDownK;
-                        more = w.chunk + 1 < w.last;
-#pragma unroll
-                        for (int h = 0; h < kDownBatches; ++h) {
-                            const int kb = k0 + h * kDownGroups * 32;
-                            Tokens<kDownGroups> b = ahead;
-                            if (h + 1 < kDownBatches || more)   // a chunk is kDownBatches batches long
-                                fetch(ahead, 0, tiles, kb + kDownGroups * 32, p.I, column);
-#pragma unroll
-                            for (int j = 0; j < NT; j += kCols) {
-                                if (j >= tiles)
-                                    break;
-                                if (j > 0)
-                                    fetch(b, j, tiles, kb, p.I, column);
-                                multiply<false>(at, h * kDownGroups, p.I - kb, j, tiles, b, acc);
-                            }
+                        more = ++w.chunk < w.last;
+                        if (!more) {
+                            w.part += kWarps;
+                            some = enter_part(w);
+                            enter();
                         }
+                        multiply_all<false>(at, tiles, b, c, c1, k0, w.chunk * kDownK, acc,
+                                            [&](int j) { return h_column(ai, j); });
                     }
-                    w.part += kWarps;
-                    some = enter_part(w);
-                    nt = enter();
-                    fetch(ahead, 0, nt, w.chunk * kDownK, p.I, column);
                     const int first = start[ai], count = start[ai + 1] - first;
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
