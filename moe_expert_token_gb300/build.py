@@ -21,7 +21,8 @@ SOURCES = [os.path.join(CSRC, f) for f in ("gating_f16.cu", "gating_bf16.cu", "g
                                             "moe_layer.cu", "moe_layer_bf16.cu", "moe_layer_f16.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "gating_kernel.cuh"),
                   os.path.join(CSRC, "ws_layout.h"), os.path.join(CSRC, "mrr_shape.h"),
-                  os.path.join(CSRC, "mx.cuh"), os.path.join(CSRC, "tc.cuh"), os.path.join(CSRC, "moe_layer_kernel.cuh"), os.path.join(INCLUDE, "moe_mx.h"),
+                  os.path.join(CSRC, "mx.cuh"), os.path.join(CSRC, "tc.cuh"),
+                  os.path.join(CSRC, "device_info.h"), os.path.join(CSRC, "moe_layer_kernel.cuh"), os.path.join(INCLUDE, "moe_mx.h"),
                   os.path.join(INCLUDE, "moe_layer.h"),
                   os.path.join(INCLUDE, "mrr_v2.h"), os.path.join(INCLUDE, "mrr_gating.h")]
 LIB_DIR = os.path.join(PKG, "lib")

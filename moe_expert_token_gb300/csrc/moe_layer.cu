@@ -100,14 +100,12 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
         }
         return MRR_OK;
     }
-    int device = -1, sms = 0, smem_max = 0;
-    if (cudaGetDevice(&device) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
-        cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, device) != cudaSuccess) {
+    mrr_device::Info info;
+    if (!mrr_device::current(info)) {
         (void)cudaGetLastError();
         return MRR_ERR_CUDA;
     }
-    const int grid = sms < kMaxGrid ? sms : kMaxGrid;
+    const int grid = info.sms < kMaxGrid ? info.sms : kMaxGrid;
     Params p{};
     p.x = x, p.wr = w_router, p.bias = bias, p.w13 = w13, p.w2 = w2, p.w13_s = w13_scales, p.w2_s = w2_scales;
     p.T = (int)T, p.H = (int)H, p.E = (int)E, p.I = (int)I, p.k = (int)k;
@@ -165,9 +163,9 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     p.sm_cols = take(T > 8 ? n * 2 : active * 16);
     p.sm_tokens = T > 8 ? take(n) : 0;
     p.sm_count = take(16);
-    if (at > smem_max)
+    if (at > info.smem_max)
         return MRR_ERR_CUDA;
-    const cudaError_t err = dt == MOE_BF16 ? launch_bf16(p, mx, grid, (size_t)at, s) : launch_f16(p, mx, grid, (size_t)at, s);
+    const cudaError_t err = dt == MOE_BF16 ? launch_bf16(p, mx, info, grid, (size_t)at, s) : launch_f16(p, mx, info, grid, (size_t)at, s);
     if (err != cudaSuccess) {
         (void)cudaGetLastError();
         return MRR_ERR_CUDA;

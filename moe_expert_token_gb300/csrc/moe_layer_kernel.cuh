@@ -31,6 +31,7 @@
 
 #include <math.h>
 
+#include "device_info.h"
 #include "moe_layer.h"
 #include "mrr_gating.h"
 #include "mx.cuh"
@@ -181,7 +182,6 @@ __device__ __forceinline__ bool grid_wait(const Params &p, int set, int *s_ok)
     __syncthreads();
     if (threadIdx.x == 0) {
         *s_ok = 1;
-        __threadfence();
         asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(f + blockIdx.x), "l"(p.tag) : "memory");
     }
     __syncthreads();
@@ -189,7 +189,7 @@ __device__ __forceinline__ bool grid_wait(const Params &p, int set, int *s_ok)
         const uint64_t t0 = mrr::global_timer_ns();
         for (uint32_t it = 1;; ++it) {
             unsigned long long v;
-            asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(f + i) : "memory");
+            asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(f + i) : "memory");
             if (v == p.tag)
                 break;
             if (it % 64 == 0 && mrr::global_timer_ns() - t0 > kWaitLimitNs) {
@@ -198,6 +198,7 @@ __device__ __forceinline__ bool grid_wait(const Params &p, int set, int *s_ok)
             }
         }
     }
+    asm volatile("fence.acq_rel.gpu;" ::: "memory");
     __syncthreads();
     return *s_ok != 0;
 }
@@ -1275,10 +1276,12 @@ __global__ void __launch_bounds__(kThreads, 1) layer_kernel(const __grid_constan
 }
 
 template <int DT, int WDT, int NT>
-cudaError_t launch_one(const Params &p, int grid, size_t smem, cudaStream_t s)
+cudaError_t launch_one(const Params &p, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s)
 {
-    auto kernel = p.w13_wide && p.w2_wide ? layer_kernel<DT, WDT, NT, true> : layer_kernel<DT, WDT, NT, false>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> allowed[2];
+    const bool wide = p.w13_wide && p.w2_wide;
+    auto kernel = wide ? layer_kernel<DT, WDT, NT, true> : layer_kernel<DT, WDT, NT, false>;
+    const cudaError_t err = mrr_device::allow_smem(kernel, info, allowed[wide]);
     if (err != cudaSuccess)
         return err;
     void *args[] = {const_cast<Params *>(&p)};
@@ -1286,14 +1289,14 @@ cudaError_t launch_one(const Params &p, int grid, size_t smem, cudaStream_t s)
 }
 
 template <int DT>
-cudaError_t launch_dt(const Params &p, bool mx, int grid, size_t smem, cudaStream_t s)
+cudaError_t launch_dt(const Params &p, bool mx, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s)
 {
     if (p.T <= 8)
-        return mx ? launch_one<DT, MOE_MXFP4, 1>(p, grid, smem, s) : launch_one<DT, DT, 1>(p, grid, smem, s);
-    return mx ? launch_one<DT, MOE_MXFP4, 8>(p, grid, smem, s) : launch_one<DT, DT, 8>(p, grid, smem, s);
+        return mx ? launch_one<DT, MOE_MXFP4, 1>(p, info, grid, smem, s) : launch_one<DT, DT, 1>(p, info, grid, smem, s);
+    return mx ? launch_one<DT, MOE_MXFP4, 8>(p, info, grid, smem, s) : launch_one<DT, DT, 8>(p, info, grid, smem, s);
 }
 
-cudaError_t launch_bf16(const Params &p, bool mx, int grid, size_t smem, cudaStream_t s);
-cudaError_t launch_f16(const Params &p, bool mx, int grid, size_t smem, cudaStream_t s);
+cudaError_t launch_bf16(const Params &p, bool mx, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s);
+cudaError_t launch_f16(const Params &p, bool mx, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s);
 
 }  // namespace moe_layer

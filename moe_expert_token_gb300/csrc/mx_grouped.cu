@@ -24,6 +24,7 @@
 // are waited for, tensor memory is freed, and mrr_v2_read_status reports MRR_ERR_TIMEOUT.
 #include <cuda.h>
 
+#include "device_info.h"
 #include "mx.cuh"
 #include "tc.cuh"
 #include "ws_layout.h"
@@ -620,13 +621,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kGated, int kOut>
-cudaError_t launch(const Params &p, const CUtensorMap &x_map, const CUtensorMap &w_map, int grid, size_t smem, cudaStream_t s)
+cudaError_t launch(const Params &p, const CUtensorMap &x_map, const CUtensorMap &w_map, const mrr_device::Info &info, size_t smem,
+                   cudaStream_t s)
 {
+    static std::atomic<uint64_t> allowed;
     auto kernel = grouped_kernel<kGated, kOut>;
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t err = mrr_device::allow_smem(kernel, info, allowed);
     if (err != cudaSuccess)
         return err;
-    kernel<<<grid, kThreads, smem, s>>>(p, x_map, w_map);
+    kernel<<<info.sms, kThreads, smem, s>>>(p, x_map, w_map);
     return cudaGetLastError();
 }
 
@@ -660,10 +663,8 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
         return MRR_ERR_ALIGN;
     if (!workspace || (uintptr_t)workspace % 256 || workspace_bytes < moe_mx_grouped_workspace(E))
         return MRR_ERR_WORKSPACE;
-    int device = -1, sms = 0, smem_max = 0;
-    if (cudaGetDevice(&device) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
-        cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, device) != cudaSuccess) {
+    mrr_device::Info info;
+    if (!mrr_device::current(info)) {
         (void)cudaGetLastError();
         return MRR_ERR_CUDA;
     }
@@ -688,7 +689,7 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
     p.sm_scales = (int)mrr_ws::round_up(p.sm_tables + 8 * (E + 1), 16);
     p.sm_stage = (int)mrr_ws::round_up(p.sm_scales + 2 * (2048 + 1024 * groups_of(p.tokens)), 1024);
     const int columns_left = (kColumns - p.sums * 2 * p.tokens) / (16 + 8 * groups_of(p.tokens));
-    int stages = (smem_max - p.sm_stage) / stage_bytes(p.tokens);
+    int stages = (info.smem_max - p.sm_stage) / stage_bytes(p.tokens);
     stages = stages < columns_left ? stages : columns_left;
     p.stages = stages < kMaxStages ? stages : kMaxStages;
     if (p.stages < 2)
@@ -701,13 +702,13 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t err;
     if (out_dt == MOE_BF16)
-        err = gated ? launch<true, MOE_BF16>(p, x_map, w_map, sms, smem, st) : launch<false, MOE_BF16>(p, x_map, w_map, sms, smem, st);
+        err = gated ? launch<true, MOE_BF16>(p, x_map, w_map, info, smem, st) : launch<false, MOE_BF16>(p, x_map, w_map, info, smem, st);
     else if (out_dt == MOE_F16)
-        err = gated ? launch<true, MOE_F16>(p, x_map, w_map, sms, smem, st) : launch<false, MOE_F16>(p, x_map, w_map, sms, smem, st);
+        err = gated ? launch<true, MOE_F16>(p, x_map, w_map, info, smem, st) : launch<false, MOE_F16>(p, x_map, w_map, info, smem, st);
     else if (out_dt == MOE_F32)
-        err = gated ? launch<true, MOE_F32>(p, x_map, w_map, sms, smem, st) : launch<false, MOE_F32>(p, x_map, w_map, sms, smem, st);
+        err = gated ? launch<true, MOE_F32>(p, x_map, w_map, info, smem, st) : launch<false, MOE_F32>(p, x_map, w_map, info, smem, st);
     else
-        err = gated ? launch<true, MOE_MXFP4>(p, x_map, w_map, sms, smem, st) : launch<false, MOE_MXFP4>(p, x_map, w_map, sms, smem, st);
+        err = gated ? launch<true, MOE_MXFP4>(p, x_map, w_map, info, smem, st) : launch<false, MOE_MXFP4>(p, x_map, w_map, info, smem, st);
     if (err != cudaSuccess) {
         (void)cudaGetLastError();
         return MRR_ERR_CUDA;

@@ -52,54 +52,59 @@ def moe_few_token_layer_run(x, dt, T, H, w_router, E, bias, w13, w13_scales, w2,
 
 # ---------------------------------------------------------------------------- torch-level calls
 
-_codes = None
+# A decode step makes a few of these calls for each layer, on kernels of a few microseconds: what a
+# call does on the host counts.  So torch and the library are looked up once, and each call reads a
+# tensor's properties once.
+torch = None
+_lib = None
+_raw_stream = None     # a device's current stream as an integer, without a Stream object around it
+_CODES = {}
 
 
-def _dtype_codes():
-    global _codes
-    if _codes is None:
-        import torch
+def _load():
+    """The library, with torch imported beside it."""
+    global torch, _lib, _raw_stream
+    if _lib is None:
+        import torch as torch_
 
-        _codes = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
-    return _codes
+        torch = torch_
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _CODES.update({torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32})
+        _lib = _m.load_library()
+    return _lib
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _launch(dev, stream, call):
-    """Run ``call(stream value)`` with ``dev`` current, on ``stream`` or dev's current stream."""
-    import torch
-
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+def _run(function, name, args, dev, stream, workspace=None, check_status=False):
+    """Call ``function(*args, stream)`` with ``dev`` current, on ``stream`` or dev's current stream."""
+    handle = _raw_stream(dev.index) if stream is None else stream.cuda_stream
     if dev.index == torch.cuda.current_device():
-        return call(stream.cuda_stream)
-    with torch.cuda.device(dev):
-        return call(stream.cuda_stream)
-
-
-def _finish(st, where, workspace, dev, stream, check_status):
+        st = function(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = function(*args, handle)
     if st != MRR_OK:
-        raise MrrError(st, where)
+        raise MrrError(st, name)
     if check_status:
-        st = _launch(dev, stream, lambda s: _m.mrr_v2_read_status(workspace.data_ptr(), workspace.numel(), s))
+        with torch.cuda.device(dev):
+            st = _m.mrr_v2_read_status(workspace.data_ptr(), workspace.numel(), handle)
         if st != MRR_OK:
             raise MrrError(st, "device")
 
 
 def _check_mx(codes, scales, name):
     """Contiguous codes [..., K/2] and scales [..., ceil(K/64), 2] of one device; returns K."""
-    import torch
-
-    fp4 = getattr(torch, "float4_e2m1fn_x2", None)
-    if codes.dtype != torch.uint8 and (fp4 is None or codes.dtype != fp4):
+    if codes.dtype != torch.uint8 and codes.dtype != getattr(torch, "float4_e2m1fn_x2", None):
         raise TypeError(f"{name} must be packed float4_e2m1 bytes (uint8)")
     if scales is None or scales.element_size() != 1:
         raise TypeError(f"{name}'s scales must be e8m0 bytes")
-    K = 2 * codes.shape[-1]
-    if tuple(scales.shape) != tuple(codes.shape[:-1]) + ((K + 63) // 64, 2):
+    shape = codes.shape
+    K = 2 * shape[-1]
+    if scales.shape != (*shape[:-1], (K + 63) // 64, 2):
         raise ValueError(f"{name}'s scales must be [..., ceil(K/64), 2] for codes [..., K/2]")
     if not codes.is_cuda or scales.device != codes.device or not codes.is_contiguous() or not scales.is_contiguous():
         raise ValueError(f"{name} and its scales must be contiguous CUDA tensors of one device")
@@ -111,45 +116,43 @@ def moe_mx_quantize(x, *, stream=None):
     without gaps except that a 2-D x may have any row stride.  Returns (codes [..., K/2] uint8,
     scales [..., ceil(K/64), 2] uint8): the float4_e2m1 rows and e8m0 scales moe_re_routing takes.
     """
-    import torch
-
-    if not x.is_cuda or x.dim() < 1:
+    lib = _lib or _load()
+    shape = x.shape
+    if not x.is_cuda or not shape:
         raise ValueError("x must be a CUDA tensor of at least one dimension")
-    if x.dtype not in _dtype_codes():
+    code = _CODES.get(x.dtype)
+    if code is None:
         raise TypeError("x must be float16, bfloat16 or float32")
-    K = x.shape[-1]
+    K = stride = shape[-1]
     if K < 2 or K % 2:
         raise ValueError("x's last dimension must be even")
-    stride = K
     if not x.is_contiguous():
-        if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < K:
+        if len(shape) != 2 or x.stride(1) != 1 or x.stride(0) < K:
             raise ValueError("x must be contiguous, or 2-D with contiguous rows")
         stride = x.stride(0)
-    lead, dev = x.shape[:-1], x.device
-    codes = torch.empty(*lead, K // 2, dtype=torch.uint8, device=dev)
-    scales = torch.empty(*lead, (K + 63) // 64, 2, dtype=torch.uint8, device=dev)
-    st = _launch(dev, stream, lambda s: moe_mx_quantize_run(x.data_ptr(), _dtype_codes()[x.dtype], x.numel() // K, K,
-                                                            stride, codes.data_ptr(), scales.data_ptr(), s))
-    _finish(st, "moe_mx_quantize_run", None, dev, stream, False)
+    lead, dev = shape[:-1], x.device
+    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((*lead, (K + 63) // 64, 2), dtype=torch.uint8, device=dev)
+    _run(lib.moe_mx_quantize_run, "moe_mx_quantize_run",
+         (x.data_ptr(), code, x.numel() // K, K, stride, codes.data_ptr(), scales.data_ptr()), dev, stream)
     return codes, scales
 
 
 def moe_mx_dequantize(codes, scales, dtype=None, *, stream=None):
     """The values [..., K] of MXFP4 codes [..., K/2] and scales [..., ceil(K/64), 2], in ``dtype``
     (float16, bfloat16, the default, or float32)."""
-    import torch
-
+    lib = _lib or _load()
     dtype = torch.bfloat16 if dtype is None else dtype
-    if dtype not in _dtype_codes():
+    code = _CODES.get(dtype)
+    if code is None:
         raise TypeError("dtype must be float16, bfloat16 or float32")
     K = _check_mx(codes, scales, "codes")
     if K < 2:
         raise ValueError("codes' rows are empty")
     dev = codes.device
-    x = torch.empty(*codes.shape[:-1], K, dtype=dtype, device=dev)
-    st = _launch(dev, stream, lambda s: moe_mx_dequantize_run(codes.data_ptr(), scales.data_ptr(), x.numel() // K, K,
-                                                              _dtype_codes()[dtype], x.data_ptr(), K, s))
-    _finish(st, "moe_mx_dequantize_run", None, dev, stream, False)
+    x = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=dev)
+    _run(lib.moe_mx_dequantize_run, "moe_mx_dequantize_run",
+         (codes.data_ptr(), scales.data_ptr(), x.numel() // K, K, code, x.data_ptr(), K), dev, stream)
     return x
 
 
@@ -168,15 +171,14 @@ def moe_mx_grouped_matmul(tokens, scales, expert_token_num, weight, weight_scale
     for out_dtype "mxfp4" the pair (codes, scales).  Sums are float32 throughout.
     ``check_status=True`` synchronises and raises on counts that do not sum to A.
     """
-    import torch
-
+    lib = _lib or _load()
     K = _check_mx(tokens, scales, "tokens")
     if tokens.dim() != 2 or weight.dim() != 3:
         raise ValueError("tokens must be 2-D and weight 3-D")
     if _check_mx(weight, weight_scales, "weight") != K:
         raise ValueError("tokens and weight differ in K")
     A, dev, c = tokens.shape[0], tokens.device, expert_token_num
-    E, N = weight.shape[0], weight.shape[1]
+    E, N, _ = weight.shape
     if gated:
         if N % 2:
             raise ValueError("a gated weight has as many gate rows as up rows")
@@ -193,21 +195,20 @@ def moe_mx_grouped_matmul(tokens, scales, expert_token_num, weight, weight_scale
         if N % 32:
             raise ValueError("an mxfp4 result needs a multiple of 32 columns")
         code = MOE_MXFP4
-        out = torch.empty(A, N // 2, dtype=torch.uint8, device=dev)
-        out_scales = torch.empty(A, (N + 63) // 64, 2, dtype=torch.uint8, device=dev)
+        out = torch.empty((A, N // 2), dtype=torch.uint8, device=dev)
+        out_scales = torch.empty((A, (N + 63) // 64, 2), dtype=torch.uint8, device=dev)
     else:
         out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-        if out_dtype not in _dtype_codes():
+        code = _CODES.get(out_dtype)
+        if code is None:
             raise TypeError("out_dtype must be float16, bfloat16, float32 or 'mxfp4'")
-        code = _dtype_codes()[out_dtype]
-        out = torch.empty(A, N, dtype=out_dtype, device=dev)
+        out = torch.empty((A, N), dtype=out_dtype, device=dev)
     if workspace is None:
-        workspace = torch.empty(moe_mx_grouped_workspace(E), dtype=torch.uint8, device=dev)
-    st = _launch(dev, stream, lambda s: moe_mx_grouped_run(
-        tokens.data_ptr(), scales.data_ptr(), A, K, c.data_ptr(), c.dtype == torch.int64, expert_token_num_type, E,
-        weight.data_ptr(), weight_scales.data_ptr(), N, gated, _ptr(row_weight), out.data_ptr(), code,
-        _ptr(out_scales), workspace.data_ptr(), workspace.numel(), s))
-    _finish(st, "moe_mx_grouped_run", workspace, dev, stream, check_status)
+        workspace = torch.empty(lib.moe_mx_grouped_workspace(E), dtype=torch.uint8, device=dev)
+    _run(lib.moe_mx_grouped_run, "moe_mx_grouped_run",
+         (tokens.data_ptr(), scales.data_ptr(), A, K, c.data_ptr(), int(c.dtype == torch.int64), expert_token_num_type,
+          E, weight.data_ptr(), weight_scales.data_ptr(), N, int(gated), _ptr(row_weight), out.data_ptr(), code,
+          _ptr(out_scales), workspace.data_ptr(), workspace.numel()), dev, stream, workspace, check_status)
     return out if out_scales is None else (out, out_scales)
 
 
@@ -225,31 +226,27 @@ def moe_few_token_layer(x, w_router, w13, w2, k: int, *, bias=None, w13_scales=N
     Returns y [T, H] in x's dtype, or with ``return_routing`` (y, weights [T, k] float32, experts
     [T, k] int32).
     """
-    import torch
-
+    lib = _lib or _load()
     if not x.is_cuda or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D CUDA tensor")
-    if x.dtype not in (torch.float16, torch.bfloat16):
+    dtype, dev = x.dtype, x.device
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
         raise TypeError("x must be float16 or bfloat16")
+    dt = w_dt = _CODES[dtype]
     T, H = x.shape
-    dev, dt = x.device, _dtype_codes()[x.dtype]
     if w_router.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
         raise ValueError("w_router must be 2-D, w13 and w2 3-D")
-    E = w_router.shape[0]
-    mx = w13_scales is not None or w2_scales is not None
-    if mx:
+    E, I = w_router.shape[0], w2.shape[2]
+    if w13_scales is not None or w2_scales is not None:
         if _check_mx(w13, w13_scales, "w13") != H:
             raise ValueError("w13 must be [E, 2 I, H/2]")
         I = _check_mx(w2, w2_scales, "w2")
         w_dt = MOE_MXFP4
-    else:
-        I, w_dt = w2.shape[-1], dt
-        if w13.dtype != x.dtype or w2.dtype != x.dtype or w13.shape[-1] != H:
-            raise ValueError("w13 must be [E, 2 I, H] and w2 [E, H, I], in x's dtype")
-    if w_router.dtype != x.dtype or w_router.shape[1] != H or tuple(w13.shape[:2]) != (E, 2 * I) \
-            or tuple(w2.shape[:2]) != (E, H):
+    elif w13.dtype is not dtype or w2.dtype is not dtype or w13.shape[2] != H:
+        raise ValueError("w13 must be [E, 2 I, H] and w2 [E, H, I], in x's dtype")
+    if w_router.dtype is not dtype or w_router.shape[1] != H or w13.shape[:2] != (E, 2 * I) or w2.shape[:2] != (E, H):
         raise ValueError("w_router must be [E, H] in x's dtype, w13 [E, 2 I, H] and w2 [E, H, I]")
-    if bias is not None and (bias.dtype != x.dtype or bias.shape != (E,) or not bias.is_contiguous()
+    if bias is not None and (bias.dtype is not dtype or bias.shape != (E,) or not bias.is_contiguous()
                              or bias.device != dev):
         raise ValueError("bias must be contiguous [E] in x's dtype on x's device")
     for w in (w_router, w13, w2):
@@ -258,13 +255,13 @@ def moe_few_token_layer(x, w_router, w13, w2, k: int, *, bias=None, w13_scales=N
     y = torch.empty_like(x)
     weight = idx = None
     if return_routing:
-        weight = torch.empty(T, k, dtype=torch.float32, device=dev)
-        idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+        weight = torch.empty((T, k), dtype=torch.float32, device=dev)
+        idx = torch.empty((T, k), dtype=torch.int32, device=dev)
     if workspace is None:
-        workspace = torch.empty(moe_few_token_layer_workspace(T, H, E, I, k), dtype=torch.uint8, device=dev)
-    st = _launch(dev, stream, lambda s: moe_few_token_layer_run(
-        x.data_ptr(), dt, T, H, w_router.data_ptr(), E, _ptr(bias), w13.data_ptr(), _ptr(w13_scales), w2.data_ptr(),
-        _ptr(w2_scales), w_dt, I, k, k_group, group_count, routed_scaling_factor, eps, group_select_mode, norm_type,
-        y.data_ptr(), _ptr(weight), _ptr(idx), workspace.data_ptr(), workspace.numel(), s))
-    _finish(st, "moe_few_token_layer_run", workspace, dev, stream, check_status)
+        workspace = torch.empty(lib.moe_few_token_layer_workspace(T, H, E, I, k), dtype=torch.uint8, device=dev)
+    _run(lib.moe_few_token_layer_run, "moe_few_token_layer_run",
+         (x.data_ptr(), dt, T, H, w_router.data_ptr(), E, _ptr(bias), w13.data_ptr(), _ptr(w13_scales), w2.data_ptr(),
+          _ptr(w2_scales), w_dt, I, k, k_group, group_count, routed_scaling_factor, eps, group_select_mode, norm_type,
+          y.data_ptr(), _ptr(weight), _ptr(idx), workspace.data_ptr(), workspace.numel()), dev, stream, workspace,
+         check_status)
     return (y, weight, idx) if return_routing else y
