@@ -15,10 +15,10 @@ bool sizes_ok(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
            E <= MRR_GATE_MAX_EXPERTS && k >= 1 && k <= 64 && k <= E;
 }
 
-constexpr int kMaxGrid = 512;    // words of a flag set
+constexpr int kMaxGrid = 512;    // words of the first grid-wide wait
 
 struct Layout {
-    size_t flags, part, xh, route_expert, route_weight, x_scale, h_max, h, h_field, bytes;
+    size_t waits, part, xh, route_expert, route_weight, x_scale, h_max, h, h_field, bytes;
     int Hp, Ip;
 };
 
@@ -33,7 +33,7 @@ Layout layout(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
     Layout l;
     l.Hp = (int)mrr_ws::round_up(H, 256);   // the products read whole stages, of up to 256 elements
     l.Ip = (int)mrr_ws::round_up(I, 512);   // of x and 512 of h
-    l.flags = take(3 * kMaxGrid * 8);
+    l.waits = take(sizeof(Waits) + kMaxGrid * 8);
     l.part = take(kMaxParts * T * E * 4);
     l.xh = take(T * l.Hp * 2);
     l.route_expert = take(T * k * 4);
@@ -114,7 +114,7 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     p.rsf = routed_scaling_factor, p.eps = eps;
     p.y = y, p.topk_weight = topk_weight, p.expert_idx = expert_idx;
     p.status = reinterpret_cast<uint32_t *>(ws);
-    p.flags = reinterpret_cast<unsigned long long *>(ws + l.flags);
+    p.waits = reinterpret_cast<Waits *>(ws + l.waits);
     p.tag = fresh_tag();
     p.part = reinterpret_cast<float *>(ws + l.part);
     p.xh = reinterpret_cast<uint16_t *>(ws + l.xh);

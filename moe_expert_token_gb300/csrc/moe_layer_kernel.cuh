@@ -60,7 +60,7 @@ struct Params {
     int *expert_idx;
     // workspace
     uint32_t *status;
-    unsigned long long *flags;    // [3][grid], see grid_wait
+    struct Waits *waits;          // see grid_wait
     unsigned long long tag;
     float *part;                  // [kparts][T][E]
     uint16_t *xh;                 // [T][Hp]: x's rows as the products take them
@@ -168,37 +168,76 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, __half2 b)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// ---------------------------------------------------------------- the grid-wide wait
+// ---------------------------------------------------------------- the grid-wide waits
 //
-// Block b writes the call's tag into its own word of `set` and waits until every block has.  The
-// words need no initial value: tags are 64 random-looking bits, different for each call.  For a
-// launch replayed from a graph, with the same tag: each block clears its words of sets 1 and 2
-// before it arrives at set 0, and its word of set 0 once it is through set 1 (then all are through
-// set 0), so no word holds the tag before its block arrives.  The launch is cooperative (all blocks
-// run at once); a wait that lasts kWaitLimitNs all the same gives up and returns false.
-__device__ __forceinline__ bool grid_wait(const Params &p, int set, int *s_ok)
+// The launch is cooperative: all blocks run at once.  The workspace comes uninitialised, so the first
+// wait goes by words that need no initial value: block b writes the call's tag (64 random-looking
+// bits, different for each call) into its own, block 0 reads them all and then writes the tag into
+// the word that the others read.  The later waits count arrivals in words that block 0 cleared before
+// the first.  One thread a block reads one word: 152 blocks that each read 152 words held one another
+// up for microseconds.  For a launch replayed from a graph, with the same tag, each block clears its
+// word, and block 0 the common one, after the last wait, when all are through the first.  A wait that
+// lasts kWaitLimitNs all the same gives up and returns false.
+struct Waits {
+    unsigned long long go, arrived[2];
+    unsigned long long block[];
+};
+
+template <typename Done>
+__device__ __forceinline__ bool poll(const unsigned long long *word, Done done)
 {
-    unsigned long long *f = p.flags + (size_t)set * gridDim.x;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        *s_ok = 1;
-        asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(f + blockIdx.x), "l"(p.tag) : "memory");
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < (int)gridDim.x; i += kThreads) {
-        const uint64_t t0 = mrr::global_timer_ns();
-        for (uint32_t it = 1;; ++it) {
-            unsigned long long v;
-            asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(f + i) : "memory");
-            if (v == p.tag)
-                break;
-            if (it % 64 == 0 && mrr::global_timer_ns() - t0 > kWaitLimitNs) {
-                *s_ok = 0;
-                break;
-            }
+    uint64_t t0 = 0;   // the timer is slow to read: not before a wait has become a long one
+    for (uint32_t it = 1;; ++it) {
+        unsigned long long v;
+        asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(word) : "memory");
+        if (done(v))
+            return true;
+        if (it % 256 == 0) {
+            const uint64_t now = mrr::global_timer_ns();
+            if (t0 == 0)
+                t0 = now;
+            else if (now - t0 > kWaitLimitNs)
+                return false;
         }
     }
-    asm volatile("fence.acq_rel.gpu;" ::: "memory");
+}
+
+__device__ __forceinline__ void publish(unsigned long long *word, unsigned long long v)
+{
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(word), "l"(v) : "memory");
+}
+
+// which: 0, or 1 and 2 for the counted ones
+__device__ __forceinline__ bool grid_wait(const Params &p, int which, int *s_ok)
+{
+    Waits *w = p.waits;
+    auto is_tag = [&](unsigned long long v) { return v == p.tag; };
+    bool ok = true;
+    if (threadIdx.x == 0)
+        *s_ok = 1;
+    __syncthreads();
+    if (which > 0) {
+        if (threadIdx.x == 0) {
+            asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(&w->arrived[which - 1]) : "memory");
+            ok = poll(&w->arrived[which - 1], [](unsigned long long v) { return v >= gridDim.x; });
+        }
+    } else if (blockIdx.x > 0) {
+        if (threadIdx.x == 0) {
+            publish(&w->block[blockIdx.x], p.tag);
+            ok = poll(&w->go, is_tag);
+        }
+    } else {
+        for (int i = threadIdx.x; i < (int)gridDim.x; i += kThreads)
+            if (i > 0)
+                ok = ok && poll(&w->block[i], is_tag);
+        if (!ok)
+            *s_ok = 0;
+        __syncthreads();
+        if (threadIdx.x == 0 && *s_ok)
+            publish(&w->go, p.tag);
+    }
+    if (!ok)
+        *s_ok = 0;
     __syncthreads();
     return *s_ok != 0;
 }
@@ -1035,10 +1074,10 @@ struct Layer {
     __device__ void run()
     {
         int *s_ok = reinterpret_cast<int *>(smem + p.sm_count) + 1;
-        if (threadIdx.x < 2)
-            p.flags[(1 + threadIdx.x) * gridDim.x + blockIdx.x] = 0;
-        if (blockIdx.x == 0 && threadIdx.x < 2)
+        if (blockIdx.x == 0 && threadIdx.x < 2) {
+            p.waits->arrived[threadIdx.x] = 0;
             p.status[threadIdx.x] = 0;
+        }
         for (int tok = gridDim.x - 1 - blockIdx.x; tok < p.T; tok += gridDim.x)
             prepare_row(tok);
         for (int item = blockIdx.x; item < (p.E + 15) / 16 * p.kparts; item += gridDim.x)
@@ -1151,7 +1190,7 @@ struct Layer {
             return;
         }
         if (threadIdx.x == 0)
-            p.flags[blockIdx.x] = 0;
+            (blockIdx.x == 0 ? p.waits->go : p.waits->block[blockIdx.x]) = 0;
 
         if (NT == 1) {
             const uint32_t field = g < p.T ? field_of(g) : 127u;
