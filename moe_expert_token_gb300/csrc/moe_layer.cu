@@ -143,7 +143,8 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     p.s2_wide = mx && wide(w2_scales, scale_row_bytes(I), 8);
     // shared memory: the rings (before them, the routing's scratch), the joins, the routing
     const int64_t n = T * k, active = n < E ? n : E;
-    int64_t at = (int64_t)kWarps * kStages * kStageBytes;
+    const int nt = T > 8 ? 8 : 1, warps = warps_of(mx, nt), stages = stages_of(mx, nt);
+    int64_t at = (int64_t)warps * stages * kStageBytes;
     const int64_t keys = ((T > 8 ? 1 : T) * 2 * E + E) * 4, places = 2 * (E + n);
     const int64_t scratch = keys > places ? keys : places;
     at = at > scratch ? at : scratch;
@@ -152,10 +153,10 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
         at += mrr_ws::round_up(bytes, 16);
         return (int)off;
     };
-    p.sm_scales = mx ? take(kWarps * kStages * kStageScales) : 0;
-    p.sm_bar = take(kWarps * kStages * 8);
-    p.sm_red = take(2 * kWarps * 256 * 4);
-    p.sm_y = T > 8 ? take(kWarps * T * 17 * 4) : 0;
+    p.sm_scales = mx ? take(warps * stages * kStageScales) : 0;
+    p.sm_bar = take(warps * stages * 8);
+    p.sm_red = take(2 * warps * 256 * 4);
+    p.sm_y = T > 8 ? take(warps * T * 17 * 4) : 0;
     p.sm_expert = take(n * 2);
     p.sm_weight = take(n * 4);
     p.sm_act = take(active * 2);

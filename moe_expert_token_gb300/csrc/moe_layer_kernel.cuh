@@ -44,8 +44,11 @@ namespace moe_layer {
 using namespace moe_mx;
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kStages = 4;
+// Warps of a block and stages of a warp's ring.  Unpacking 4-bit weights is bound by how many
+// instructions are ready, so up to 8 tokens MXFP4 has 12 warps (as many as registers allow) with
+// shorter rings; the 16-bit types stream at the memory's rate with 8.
+__host__ __device__ constexpr int warps_of(bool mx, int nt) { return mx && nt == 1 ? 12 : 8; }
+__host__ __device__ constexpr int stages_of(bool mx, int nt) { return mx && nt == 1 ? 3 : 4; }
 constexpr int kSlab = 2048;                      // 16 rows x 128 bytes
 constexpr int kMaxParts = 16;                    // most shares of H the logits are split into
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -156,10 +159,18 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t (&d)[4])
         : "r"(w));
 }
 
-// whether any byte of w is 0 or 255
-__device__ __forceinline__ bool special_bytes(uint32_t w)
+// the four scales of w's bytes, exactly (0: 2^-127, 255: NaN)
+__device__ __forceinline__ void scales_to_float(uint32_t w, float (&s)[4])
 {
-    return (((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u;
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %0, a;\n\tcvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+    s[0] = __uint_as_float(lo << 16);
+    s[1] = __uint_as_float(lo & 0xffff0000u);
+    s[2] = __uint_as_float(hi << 16);
+    s[3] = __uint_as_float(hi & 0xffff0000u);
 }
 
 __device__ __forceinline__ uint32_t half2_mul(uint32_t a, __half2 b)
@@ -208,6 +219,7 @@ __device__ __forceinline__ void publish(unsigned long long *word, unsigned long 
 }
 
 // which: 0, or 1 and 2 for the counted ones
+template <int kThreads>
 __device__ __forceinline__ bool grid_wait(const Params &p, int which, int *s_ok)
 {
     Waits *w = p.waits;
@@ -379,6 +391,7 @@ struct Cursor {
 template <int DT, int WDT, int NT, bool kWide>
 struct Layer {
     static constexpr bool kMx = WDT == MOE_MXFP4;
+    static constexpr int kWarps = warps_of(kMx, NT), kThreads = 32 * kWarps, kStages = stages_of(kMx, NT);
     static constexpr int MDT = kMx ? MOE_F16 : DT;            // the matrix instructions' type
     static constexpr bool kScaled = MDT == MOE_F16;           // h carries a power of two for each tile
     static constexpr int kStage = kStageBytes;
@@ -617,11 +630,13 @@ struct Layer {
         __syncwarp();
     }
 
-    // Token operands of one stage, kGroups groups of 32 k, for kCols column tiles: this lane's 8 elements
-    // of each.  Every register is loaded with the next stage's value as soon as it has been used, so
-    // that a stage's time hides the loads.
+    // Token operands of one step (a stage, or half of one), kGroups groups of 32 k, for kCols column tiles: this lane's 8 elements
+    // of each.  Every register is loaded with the next step's value as soon as it has been used, so
+    // that a step's time hides the loads.
     static constexpr int kCols = NT == 1 || kMx ? 1 : 2;
-    static constexpr int kSlabGroups = kSlabK / 32, kUpGroups = kUpK / 32, kDownGroups = kDownK / 32;
+    static constexpr int kSlabGroups = kSlabK / 32, kUpGroups = kUpK / 32;
+    // MXFP4's down stages are 16 groups long: worked off a slab at a time, to hold half the operands
+    static constexpr int kDownSteps = kMx ? 2 : 1, kDownGroups = kDownK / 32 / kDownSteps;
     template <int kGroups>
     struct Tokens {
         uint4 v[kCols][kGroups];
@@ -659,20 +674,27 @@ struct Layer {
                 load<kUp>(b, j, i, c[j], k0);
     }
 
-    // The products of a stage: two row tiles, one a slab (kUp), or one whose K runs on from slab to slab,
-    // against column tiles j0 .. j0 + kN - 1.  kNext: their operands are b, which is loaded anew from
-    // `next` at k1; else they are loaded here from `now` at k1, four groups at a time, into b's first.
-    // kExact: a scale is 0 or NaN (kMx).  Past K both operands are zeros.
-    template <bool kUp, bool kExact, int kN, bool kNext, int kGroups, int kHeld>
-    __device__ __forceinline__ void multiply_as(int slot, int j0, Tokens<kHeld> &b, const Column (&now)[kCols],
-                                                const Column (&next)[kCols], int k1, const uint32_t (&sc)[2][2][4],
-                                                float (&acc)[2][NT][4]) const
+    // The products of a step: two row tiles, one a slab (kUp), or one whose K runs on from slab to slab,
+    // from slab0, against column tiles j0 .. j0 + kN - 1.  kNext: their operands are b, which is loaded
+    // anew from `next` at k1; else they are loaded here from `now` at k1, four groups at a time.
+    // Past K both operands are zeros.
+    template <bool kUp, int kN, bool kNext, int kGroups, int kHeld>
+    __device__ __forceinline__ void multiply(int slot, int slab0, int j0, Tokens<kHeld> &b, const Column (&now)[kCols],
+                                             const Column (&next)[kCols], int k1, float (&acc)[2][NT][4]) const
     {
         constexpr int kTiles = kUp ? 2 : 1, kBatch = kGroups < 4 ? kGroups : 4;
         const int stage_at = (warp * kStages + slot) * kStage + lane_at;   // a multiple of 1024, and lane_at
+        uint2 sc[2][2];   // 8 scale bytes of rows `row` and `row` + 8
+        if constexpr (kMx)
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    sc[m][r] = *reinterpret_cast<const uint2 *>(scales(slot) + (kUp ? m : slab0) * 128 + r * 64 + row * 8);
+        float s[2][2][4];
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            const int q = i % kSlabGroups, slab = kUp ? 0 : i / kSlabGroups;
+            const int q = i % kSlabGroups, slab = kUp ? 0 : slab0 + i / kSlabGroups;
             const uint8_t *from = smem + (stage_at ^ (kMx ? q << 4 : q << 6)) + slab * kSlab;
             if (!kNext && i % kBatch == 0)
 #pragma unroll
@@ -681,16 +703,14 @@ struct Layer {
                     for (int h = 0; h < kBatch; ++h)
                         load<kUp>(b, j, h, now[j], k1 + 32 * i);
             uint32_t a[kTiles][2][4];
-            float s[2][2];
 #pragma unroll
             for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {   // slab rows `row` and `row` + 8
-                    if (kMx) {
+                    if constexpr (kMx) {
                         codes_to_half(*reinterpret_cast<const uint32_t *>(from + m * kSlab + r * 1024), a[m][r]);
-                        const uint32_t w = sc[m][r][i / 4], at = i % 4;   // byte `at`, as a float's exponent
-                        s[m][r] = kExact ? e8m0_value(w >> (8 * at) & 255u)
-                                         : __uint_as_float((at < 3 ? w << (23 - 8 * at) : w >> 1) & 0x7f800000u);
+                        if (i % 4 == 0)
+                            scales_to_float(i < 4 ? sc[m][r].x : sc[m][r].y, s[m][r]);
                     } else {
                         const uint4 v = *reinterpret_cast<const uint4 *>(from + m * kSlab + r * 1024);
                         a[m][r][0] = v.x, a[m][r][1] = v.y, a[m][r][2] = v.z, a[m][r][3] = v.w;
@@ -712,10 +732,10 @@ struct Layer {
                         float d[4];
                         mma_first<MDT>(d, a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], x.x, x.y);
                         mma<MDT>(d, a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], x.z, x.w);
-                        to[0] = fmaf(s[m][0], d[0], to[0]);
-                        to[1] = fmaf(s[m][0], d[1], to[1]);
-                        to[2] = fmaf(s[m][1], d[2], to[2]);
-                        to[3] = fmaf(s[m][1], d[3], to[3]);
+                        to[0] = fmaf(s[m][0][i % 4], d[0], to[0]);
+                        to[1] = fmaf(s[m][0][i % 4], d[1], to[1]);
+                        to[2] = fmaf(s[m][1][i % 4], d[2], to[2]);
+                        to[3] = fmaf(s[m][1][i % 4], d[3], to[3]);
                     } else {
                         mma<MDT>(to, a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], x.x, x.y);
                         mma<MDT>(to, a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], x.z, x.w);
@@ -729,42 +749,17 @@ struct Layer {
         }
     }
 
-    template <bool kUp, int kN, bool kNext, int kGroups, int kHeld>
-    __device__ __forceinline__ void multiply(int slot, int j0, Tokens<kHeld> &b, const Column (&now)[kCols],
-                                             const Column (&next)[kCols], int k1, float (&acc)[2][NT][4]) const
-    {
-        uint32_t sc[2][2][4];   // scale bytes of rows `row` and `row` + 8
-        if constexpr (kMx) {
-            bool odd = false;
-#pragma unroll
-            for (int m = 0; m < (kUp ? 2 : 1); ++m)
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int h = 0; h < (kUp ? 1 : 2); ++h) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(scales(slot) + (kUp ? m : h) * 128 + r * 64 + row * 8);
-                        sc[m][r][2 * h] = v.x, sc[m][r][2 * h + 1] = v.y;
-                        odd |= special_bytes(v.x) || special_bytes(v.y);
-                    }
-            if (__any_sync(kFull, odd)) {
-                multiply_as<kUp, true, kN, kNext, kGroups>(slot, j0, b, now, next, k1, sc, acc);
-                return;
-            }
-        }
-        multiply_as<kUp, false, kN, kNext, kGroups>(slot, j0, b, now, next, k1, sc, acc);
-    }
-
-    // All nt column tiles of a stage: the first kCols, whose operands are b, and (rarely) more, whose
+    // All nt column tiles of a step: the first kCols, whose operands are b, and (rarely) more, whose
     // operands are loaded here from column(tile) at k0.
     template <bool kUp, int kGroups, typename Of>
-    __device__ __forceinline__ void multiply_all(int slot, int nt, Tokens<kGroups> &b, const Column (&now)[kCols],
-                                                 const Column (&next)[kCols], int k0, int k1, float (&acc)[2][NT][4],
-                                                 Of column) const
+    __device__ __forceinline__ void multiply_all(int slot, int slab0, int nt, Tokens<kGroups> &b,
+                                                 const Column (&now)[kCols], const Column (&next)[kCols], int k0, int k1,
+                                                 float (&acc)[2][NT][4], Of column) const
     {
         if (kCols == 1 || nt == 1)
-            multiply<kUp, 1, true, kGroups>(slot, 0, b, now, next, k1, acc);
+            multiply<kUp, 1, true, kGroups>(slot, slab0, 0, b, now, next, k1, acc);
         else
-            multiply<kUp, kCols, true, kGroups>(slot, 0, b, now, next, k1, acc);
+            multiply<kUp, kCols, true, kGroups>(slot, slab0, 0, b, now, next, k1, acc);
 #pragma unroll
         for (int j = kCols; j < NT; j += kCols) {
             if (j >= nt)
@@ -774,7 +769,7 @@ struct Layer {
                 if (j + c < nt)
                     more[c] = column(j + c);
             Tokens<kGroups < 4 ? kGroups : 4> x;
-            multiply<kUp, kCols, false, kGroups>(slot, j, x, more, more, k0, acc);
+            multiply<kUp, kCols, false, kGroups>(slot, slab0, j, x, more, more, k0, acc);
         }
     }
 
@@ -985,7 +980,7 @@ struct Layer {
                 }
                 __syncthreads();
             }
-            if (!grid_wait(p, 1, s_ok))
+            if (!grid_wait<kThreads>(p, 1, s_ok))
                 return false;
             for (int a = threadIdx.x; a < p.T * p.k; a += kThreads) {
                 expert[a] = (uint16_t)__ldcg(p.route_expert + a);
@@ -1082,7 +1077,7 @@ struct Layer {
             prepare_row(tok);
         for (int item = blockIdx.x; item < (p.E + 15) / 16 * p.kparts; item += gridDim.x)
             router_item(item);
-        if (!grid_wait(p, 0, s_ok)) {
+        if (!grid_wait<kThreads>(p, 0, s_ok)) {
             if (threadIdx.x == 0)
                 atomicOr(p.status, mrr_ws::kFlagTimeout);
             return;
@@ -1150,7 +1145,7 @@ struct Layer {
                     if (item + (int)gridDim.x < up_items)
                         x_columns(next_col, (item + gridDim.x) / up_tiles);
                 }
-                multiply_all<true>(at, nt, ahead, col, next_col, u * kUpK, k1, acc, [&](int j) { return x_column(ai, j); });
+                multiply_all<true>(at, 0, nt, ahead, col, next_col, u * kUpK, k1, acc, [&](int j) { return x_column(ai, j); });
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -1183,7 +1178,7 @@ struct Layer {
                 buf ^= 1;
             }
         }
-        if (!grid_wait(p, 2, s_ok)) {
+        if (!grid_wait<kThreads>(p, 2, s_ok)) {
             drain();
             if (threadIdx.x == 0)
                 atomicOr(p.status, mrr_ws::kFlagTimeout);
@@ -1216,12 +1211,16 @@ struct Layer {
                 float acc[2][NT][4] = {};
                 for (bool more = some; more;) {
                     const int at = take(), e = w.expert;
+                    if (kDownSteps == 2)
+                        multiply_all<false>(at, 0, 1, b, c, c1, 0, w.chunk * kDownK + kDownK / 2, acc,
+                                            [&](int) { return Column(); });
                     more = next_chunk(w);
                     if (!more)   // the next item starts over
                         first_chunk(w);
                     if (w.expert != e)
                         enter(c1[0]);
-                    multiply_all<false>(at, 1, b, c, c1, 0, w.chunk * kDownK, acc, [&](int) { return Column(); });
+                    multiply_all<false>(at, kDownSteps - 1, 1, b, c, c1, 0, w.chunk * kDownK, acc,
+                                        [&](int) { return Column(); });
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -1263,14 +1262,17 @@ struct Layer {
                         c[j] = c1[j];
                     for (bool more = true; more;) {
                         const int at = take(), k0 = w.chunk * kDownK;
+                        auto column = [&](int j) { return h_column(ai, j); };
+                        if (kDownSteps == 2)
+                            multiply_all<false>(at, 0, tiles, b, c, c1, k0, k0 + kDownK / 2, acc, column);
                         more = ++w.chunk < w.last;
                         if (!more) {
                             w.part += kWarps;
                             some = enter_part(w);
                             enter();
                         }
-                        multiply_all<false>(at, tiles, b, c, c1, k0, w.chunk * kDownK, acc,
-                                            [&](int j) { return h_column(ai, j); });
+                        multiply_all<false>(at, kDownSteps - 1, tiles, b, c, c1, k0 + (kDownSteps - 1) * (kDownK / 2),
+                                            w.chunk * kDownK, acc, column);
                     }
                     const int first = start[ai], count = start[ai + 1] - first;
 #pragma unroll
@@ -1308,7 +1310,7 @@ struct Layer {
 };
 
 template <int DT, int WDT, int NT, bool kWide>
-__global__ void __launch_bounds__(kThreads, 1) layer_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(32 * warps_of(WDT == MOE_MXFP4, NT), 1) layer_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     Layer<DT, WDT, NT, kWide>(p, smem).run();
@@ -1324,7 +1326,7 @@ cudaError_t launch_one(const Params &p, const mrr_device::Info &info, int grid, 
     if (err != cudaSuccess)
         return err;
     void *args[] = {const_cast<Params *>(&p)};
-    return cudaLaunchCooperativeKernel(reinterpret_cast<void *>(kernel), dim3(grid), dim3(kThreads), args, smem, s);
+    return cudaLaunchCooperativeKernel(reinterpret_cast<void *>(kernel), dim3(grid), dim3(32 * warps_of(WDT == MOE_MXFP4, NT)), args, smem, s);
 }
 
 template <int DT>
