@@ -141,13 +141,15 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
         return MRR_ERR_CUDA;
     p.s13_wide = mx && wide(w13_scales, scale_row_bytes(H), 8);
     p.s2_wide = mx && wide(w2_scales, scale_row_bytes(I), 8);
-    // shared memory: the rings (before them, the routing's scratch), the joins, the routing
-    const int64_t n = T * k, active = n < E ? n : E;
-    const int nt = T > 8 ? 8 : 1, warps = warps_of(mx, nt), stages = stages_of(mx, nt);
+    // shared memory: the rings (before them, the routing's scratch), the joins, who goes where
+    // active experts, counted as often as they are streamed
+    const int64_t n = T * k, active = (n < E ? n : E) + (T > 8 ? n / (8 * tiles_for(mx, true)) : 0);
+    const int warps = warps_of(mx), stages = stages_of(mx);
     int64_t at = (int64_t)warps * stages * kStageBytes;
     const int64_t keys = ((T > 8 ? 1 : T) * 2 * E + E) * 4, places = 2 * (E + n);
-    const int64_t scratch = keys > places ? keys : places;
-    at = at > scratch ? at : scratch;
+    p.sm_scratch = (int)mrr_ws::round_up(2 * n, 16);
+    const int64_t scratch = p.sm_scratch + (keys > places ? keys : places);
+    at = at > scratch ? mrr_ws::round_up(at, 16) : mrr_ws::round_up(scratch, 16);
     auto take = [&at](int64_t bytes) {
         const int64_t off = at;
         at += mrr_ws::round_up(bytes, 16);
@@ -155,10 +157,9 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     };
     p.sm_scales = mx ? take(warps * stages * kStageScales) : 0;
     p.sm_bar = take(warps * stages * 8);
-    p.sm_red = take(2 * warps * 256 * 4);
-    p.sm_y = T > 8 ? take(warps * T * 17 * 4) : 0;
-    p.sm_expert = take(n * 2);
-    p.sm_weight = take(n * 4);
+    const int64_t joins = 2 * warps * 256 * 4, sums = T > 8 ? warps * T * 17 * 4 : 0;   // of up and down: not at once
+    p.sm_red = take(joins > sums ? joins : sums);
+    p.sm_weight = take((T > 8 ? k : n) * 4);
     p.sm_act = take(active * 2);
     p.sm_start = take((active + 1) * 2);
     p.sm_cols = take(T > 8 ? n * 2 : active * 16);

@@ -44,11 +44,17 @@ namespace moe_layer {
 using namespace moe_mx;
 
 constexpr uint32_t kFull = 0xffffffffu;
+// Tiles of 8 columns that an expert's weights are multiplied with at a time.  With up to 8 tokens there
+// is one, and its columns are the tokens; with more, the columns are the tokens that chose the expert,
+// in up to 4 tiles, or one for MXFP4, whose unpacking needs the registers.  An expert with more tokens
+// than that is streamed once for each tileful (the second time from L2: both run at about the same
+// time).
+__host__ __device__ constexpr int tiles_for(bool mx, bool many) { return many && !mx ? 4 : 1; }
 // Warps of a block and stages of a warp's ring.  Unpacking 4-bit weights is bound by how many
-// instructions are ready, so up to 8 tokens MXFP4 has 12 warps (as many as registers allow) with
-// shorter rings; the 16-bit types stream at the memory's rate with 8.
-__host__ __device__ constexpr int warps_of(bool mx, int nt) { return mx && nt == 1 ? 12 : 8; }
-__host__ __device__ constexpr int stages_of(bool mx, int nt) { return mx && nt == 1 ? 3 : 4; }
+// instructions are ready, so MXFP4 has 12 warps (as many as registers allow) with shorter rings; the
+// 16-bit types stream at the memory's rate with 8.
+__host__ __device__ constexpr int warps_of(bool mx) { return mx ? 12 : 8; }
+__host__ __device__ constexpr int stages_of(bool mx) { return mx ? 3 : 4; }
 constexpr int kSlab = 2048;                      // 16 rows x 128 bytes
 constexpr int kMaxParts = 16;                    // most shares of H the logits are split into
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -79,7 +85,7 @@ struct Params {
     int s13_wide, s2_wide;            // scale rows are 8-byte aligned
     CUtensorMap w13_map, w2_map;      // rows of bytes, boxes of 128 bytes x 16 rows, 128-byte swizzle
     // dynamic shared memory, byte offsets
-    int sm_scales, sm_bar, sm_red, sm_y, sm_expert, sm_weight, sm_act, sm_start, sm_cols, sm_tokens, sm_count;
+    int sm_scales, sm_bar, sm_red, sm_scratch, sm_weight, sm_act, sm_start, sm_cols, sm_tokens, sm_count;
 };
 
 constexpr int kStageBytes = 2 * kSlab, kStageScales = 256;
@@ -388,10 +394,11 @@ struct Cursor {
     const uint8_t *scale_src;  // this lane's 8 scale bytes of chunk 0; null if there is no such row
 };
 
-template <int DT, int WDT, int NT, bool kWide>
+template <int DT, int WDT, bool kMany, bool kWide>   // kMany: more than 8 tokens
 struct Layer {
     static constexpr bool kMx = WDT == MOE_MXFP4;
-    static constexpr int kWarps = warps_of(kMx, NT), kThreads = 32 * kWarps, kStages = stages_of(kMx, NT);
+    static constexpr int NT = tiles_for(kMx, kMany);
+    static constexpr int kWarps = warps_of(kMx), kThreads = 32 * kWarps, kStages = stages_of(kMx);
     static constexpr int MDT = kMx ? MOE_F16 : DT;            // the matrix instructions' type
     static constexpr bool kScaled = MDT == MOE_F16;           // h carries a power of two for each tile
     static constexpr int kStage = kStageBytes;
@@ -407,7 +414,7 @@ struct Layer {
     bool dead;                   // a wait has given up: results do not matter any more
     int nact, up_items, up_units, up_tiles, down_items, down_chunks, down_parts;
     const uint16_t *act, *start, *cols;
-    const uint8_t *tokens;       // of the columns (NT > 1)
+    const uint8_t *tokens;       // of the columns (kMany)
 
     __device__ Layer(const Params &p_, uint8_t *sm) : p(p_), smem(sm)
     {
@@ -446,7 +453,7 @@ struct Layer {
         down_chunks = (p.I + kDownK - 1) / kDownK;
         // an expert's K is cut into shares, taken by the warps in turn: single chunks, or (where a
         // change of expert costs something) as few as give every warp four or more
-        down_parts = NT == 1 ? down_chunks : min(down_chunks, (4 * kWarps + nact - 1) / nact);
+        down_parts = !kMany ? down_chunks : min(down_chunks, (4 * kWarps + nact - 1) / nact);
     }
 
     // point the cursor at the rows of its item and expert
@@ -489,8 +496,8 @@ struct Layer {
             if (++c.expert >= nact)
                 return false;
         }
-        c.chunk = NT == 1 ? c.part : c.part * down_chunks / down_parts;
-        c.last = NT == 1 ? c.part + 1 : (c.part + 1) * down_chunks / down_parts;
+        c.chunk = !kMany ? c.part : c.part * down_chunks / down_parts;
+        c.last = !kMany ? c.part + 1 : (c.part + 1) * down_chunks / down_parts;
         return true;
     }
 
@@ -633,7 +640,7 @@ struct Layer {
     // Token operands of one step (a stage, or half of one), kGroups groups of 32 k, for kCols column tiles: this lane's 8 elements
     // of each.  Every register is loaded with the next step's value as soon as it has been used, so
     // that a step's time hides the loads.
-    static constexpr int kCols = NT == 1 || kMx ? 1 : 2;
+    static constexpr int kCols = NT == 1 ? 1 : 2;
     static constexpr int kSlabGroups = kSlabK / 32, kUpGroups = kUpK / 32;
     // MXFP4's down stages are 16 groups long: worked off a slab at a time, to hold half the operands
     static constexpr int kDownSteps = kMx ? 2 : 1, kDownGroups = kDownK / 32 / kDownSteps;
@@ -774,12 +781,12 @@ struct Layer {
     }
 
     // token of column c of active expert ai, which exists
-    __device__ __forceinline__ int token_of(int ai, int c) const { return NT == 1 ? c : (int)tokens[start[ai] + c]; }
+    __device__ __forceinline__ int token_of(int ai, int c) const { return !kMany ? c : (int)tokens[start[ai] + c]; }
 
     // assignment of column c of active expert ai, or -1.  Up to 8 tokens: column = token.
     __device__ __forceinline__ int column_of(int ai, int c) const
     {
-        if (NT == 1) {
+        if (!kMany) {
             const uint16_t a = cols[ai * 8 + c];
             return a == 0xffffu ? -1 : (int)a;
         }
@@ -789,7 +796,7 @@ struct Layer {
 
     __device__ __forceinline__ int tiles_of(int ai) const
     {
-        return NT == 1 ? 1 : ((int)start[ai + 1] - (int)start[ai] + 7) / 8;
+        return !kMany ? 1 : ((int)start[ai + 1] - (int)start[ai] + 7) / 8;
     }
 
     // column c (of this lane) of active expert ai: its row of x, and of h
@@ -893,7 +900,8 @@ struct Layer {
         const int et = item / p.kparts, part = item - et * p.kparts, chunks = (p.H + 127) / 128;
         const int lo = (int)((int64_t)chunks * part / p.kparts), hi = (int)((int64_t)chunks * (part + 1) / p.kparts);
         const int e0 = et * 16;
-        float acc[NT][4] = {};
+        constexpr int kTokenTiles = !kMany ? 1 : MOE_LAYER_MAX_TOKENS / 8;
+        float acc[kTokenTiles][4] = {};
         for (int c = lo + warp; c < hi; c += kWarps) {
             uint4 a[2][4];
 #pragma unroll
@@ -903,7 +911,7 @@ struct Layer {
                     a[r][q] = e0 + 8 * r + g < p.E ? load8_raw(p.wr, e0 + 8 * r + g, p.H, c * 128 + 32 * q + 8 * t, p.wr_wide)
                                                    : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
+            for (int j = 0; j < kTokenTiles; ++j) {
                 if (8 * j >= p.T)
                     break;
 #pragma unroll
@@ -916,7 +924,7 @@ struct Layer {
             }
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        for (int j = 0; j < kTokenTiles; ++j) {
             if (8 * j >= p.T)
                 break;
             put(red(j % 2), 0, acc[j], g);
@@ -960,10 +968,10 @@ struct Layer {
     // token a warp; with more, each token is one block's, and the blocks wait for one another.
     __device__ bool assign(uint16_t *expert, float *weight, int *s_ok)
     {
-        uint32_t *key = reinterpret_cast<uint32_t *>(smem);   // the ring is not in use yet
-        float *bias = reinterpret_cast<float *>(key + (NT == 1 ? p.T : 1) * 2 * p.E);
+        uint32_t *key = reinterpret_cast<uint32_t *>(smem + p.sm_scratch);   // the ring is not in use yet
+        float *bias = reinterpret_cast<float *>(key + (!kMany ? p.T : 1) * 2 * p.E);
         const float *use_bias = p.bias ? bias : nullptr;
-        if (NT == 1) {
+        if (!kMany) {
             logits(0, p.T, key, bias);
             if (warp < p.T)
                 route(p, key + warp * 2 * p.E, use_bias, expert + warp * p.k, weight + warp * p.k);
@@ -982,23 +990,22 @@ struct Layer {
             }
             if (!grid_wait<kThreads>(p, 1, s_ok))
                 return false;
-            for (int a = threadIdx.x; a < p.T * p.k; a += kThreads) {
+            for (int a = threadIdx.x; a < p.T * p.k; a += kThreads)
                 expert[a] = (uint16_t)__ldcg(p.route_expert + a);
-                weight[a] = __ldcg(p.route_weight + a);
-            }
             __syncthreads();
         }
         if (blockIdx.x == 0)
             for (int a = threadIdx.x; a < p.T * p.k; a += kThreads) {
                 if (p.topk_weight)
-                    p.topk_weight[a] = weight[a];
+                    p.topk_weight[a] = !kMany ? weight[a] : __ldcg(p.route_weight + a);
                 if (p.expert_idx)
                     p.expert_idx[a] = expert[a];
             }
         return true;
     }
 
-    // the active experts in order, and their columns; returns how many
+    // the active experts in order (one of more than 8 NT tokens several times, each time with as many),
+    // and their columns; returns how many
     __device__ int columns(const uint16_t *expert)
     {
         uint16_t *act_ = reinterpret_cast<uint16_t *>(smem + p.sm_act);
@@ -1008,11 +1015,11 @@ struct Layer {
         int *s_nact = reinterpret_cast<int *>(smem + p.sm_count);
         // in the ring, which is not in use yet: assignments of each expert, then its place among the
         // active ones; an assignment's place among its expert's
-        uint16_t *count = reinterpret_cast<uint16_t *>(smem), *place = count + p.E;
+        uint16_t *count = reinterpret_cast<uint16_t *>(smem + p.sm_scratch), *place = count + p.E;
         const int n = p.T * p.k;
         for (int e = threadIdx.x; e < p.E; e += kThreads)
             count[e] = 0;
-        if (NT == 1)
+        if (!kMany)
             for (int i = threadIdx.x; i < min(n, p.E) * 8; i += kThreads)
                 cols_[i] = 0xffffu;
         __syncthreads();
@@ -1031,22 +1038,24 @@ struct Layer {
             }
             int active = 0, at = 0;
             for (int e0 = 0; e0 < p.E; e0 += 32) {
-                const int e = e0 + lane, c = e < p.E ? count[e] : 0;
-                const uint32_t some = __ballot_sync(kFull, c > 0);
-                int before = c;
+                const int e = e0 + lane, c = e < p.E ? count[e] : 0, times = (c + 8 * NT - 1) / (8 * NT);
+                int both = c << 16 | times, before = both;   // two sums in one word: at most 4096 of each
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int v = __shfl_up_sync(kFull, before, o);
                     before += lane >= o ? v : 0;
                 }
-                if (c > 0) {
-                    const int i = active + __popc(some & ((1u << lane) - 1u));
-                    act_[i] = (uint16_t)e;
-                    start_[i] = (uint16_t)(at + before - c);
-                    count[e] = (uint16_t)i;
+                const int all = __shfl_sync(kFull, before, 31);
+                before -= both;
+                const int first = active + (before & 0xffff);
+                for (int i = 0; i < times; ++i) {
+                    act_[first + i] = (uint16_t)e;
+                    start_[first + i] = (uint16_t)(at + (before >> 16) + i * 8 * NT);
                 }
-                at += __shfl_sync(kFull, before, 31);
-                active += __popc(some);
+                if (c > 0)
+                    count[e] = (uint16_t)first;
+                at += all >> 16;
+                active += all & 0xffff;
             }
             if (lane == 0) {
                 start_[active] = (uint16_t)at;
@@ -1055,9 +1064,9 @@ struct Layer {
         }
         __syncthreads();
         for (int a = threadIdx.x; a < n; a += kThreads) {
-            const int i = count[expert[a]], tok = a / p.k, c = NT == 1 ? i * 8 + tok : start_[i] + place[a];
+            const int i = count[expert[a]], tok = a / p.k, c = !kMany ? i * 8 + tok : start_[i] + place[a];
             cols_[c] = (uint16_t)a;
-            if (NT > 1)
+            if (kMany)
                 tokens_[c] = (uint8_t)tok;
         }
         __syncthreads();
@@ -1083,7 +1092,7 @@ struct Layer {
             return;
         }
         float *weight = reinterpret_cast<float *>(smem + p.sm_weight);
-        uint16_t *expert = reinterpret_cast<uint16_t *>(smem + p.sm_expert);
+        uint16_t *expert = reinterpret_cast<uint16_t *>(smem);   // needed until the ring is
         if (!assign(expert, weight, s_ok)) {
             if (threadIdx.x == 0)
                 atomicOr(p.status, mrr_ws::kFlagTimeout);
@@ -1161,7 +1170,7 @@ struct Layer {
                         const float s = kMx ? p.x_scale[tok] : 1.f;
                         const float gate = gather(red(buf), 0, r, c) * s, upv = gather(red(buf), 1, r, c) * s;
                         // rows past I: what the copy brought there is another row's
-                        float h = i0 + r < p.I ? gate / (1.f + expf(-gate)) * upv * weight[a] : 0.f;
+                        float h = i0 + r < p.I ? gate / (1.f + expf(-gate)) * upv * (!kMany ? weight[a] : __ldcg(p.route_weight + a)) : 0.f;
                         if (kScaled) {
                             const uint32_t half = 0xffffu << (threadIdx.x & 16);
                             const uint32_t m = __reduce_max_sync(half, __float_as_uint(h) & 0x7fffffffu);
@@ -1187,7 +1196,7 @@ struct Layer {
         if (threadIdx.x == 0)
             (blockIdx.x == 0 ? p.waits->go : p.waits->block[blockIdx.x]) = 0;
 
-        if (NT == 1) {
+        if (!kMany) {
             const uint32_t field = g < p.T ? field_of(g) : 127u;
             Cursor w;   // where the operands in `b` come from
             bool some = (int)blockIdx.x < down_items && first_chunk(w);
@@ -1237,7 +1246,7 @@ struct Layer {
             }
         } else {
             constexpr int kPitch = 17;   // [token][16 rows and a pad]
-            float *mine = reinterpret_cast<float *>(smem + p.sm_y) + warp * p.T * kPitch;
+            float *mine = reinterpret_cast<float *>(smem + p.sm_red) + warp * p.T * kPitch;
             for (int item = blockIdx.x; item < down_items; item += gridDim.x) {
                 for (int i = lane; i < p.T * kPitch; i += 32)
                     mine[i] = 0.f;
@@ -1290,7 +1299,7 @@ struct Layer {
                     __syncwarp();   // the next share's columns are other lanes'
                 }
                 __syncthreads();
-                const float *all = reinterpret_cast<const float *>(smem + p.sm_y);
+                const float *all = reinterpret_cast<const float *>(smem + p.sm_red);
                 for (int i = threadIdx.x; i < 16 * p.T; i += kThreads) {
                     const int r = i % 16, tok = i / 16, n = item * 16 + r;
                     if (n >= p.H)
@@ -1309,32 +1318,32 @@ struct Layer {
     }
 };
 
-template <int DT, int WDT, int NT, bool kWide>
-__global__ void __launch_bounds__(32 * warps_of(WDT == MOE_MXFP4, NT), 1) layer_kernel(const __grid_constant__ Params p)
+template <int DT, int WDT, bool kMany, bool kWide>
+__global__ void __launch_bounds__(32 * warps_of(WDT == MOE_MXFP4), 1) layer_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    Layer<DT, WDT, NT, kWide>(p, smem).run();
+    Layer<DT, WDT, kMany, kWide>(p, smem).run();
 }
 
-template <int DT, int WDT, int NT>
+template <int DT, int WDT, bool kMany>
 cudaError_t launch_one(const Params &p, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s)
 {
     static std::atomic<uint64_t> allowed[2];
     const bool wide = p.w13_wide && p.w2_wide;
-    auto kernel = wide ? layer_kernel<DT, WDT, NT, true> : layer_kernel<DT, WDT, NT, false>;
+    auto kernel = wide ? layer_kernel<DT, WDT, kMany, true> : layer_kernel<DT, WDT, kMany, false>;
     const cudaError_t err = mrr_device::allow_smem(kernel, info, allowed[wide]);
     if (err != cudaSuccess)
         return err;
     void *args[] = {const_cast<Params *>(&p)};
-    return cudaLaunchCooperativeKernel(reinterpret_cast<void *>(kernel), dim3(grid), dim3(32 * warps_of(WDT == MOE_MXFP4, NT)), args, smem, s);
+    return cudaLaunchCooperativeKernel(reinterpret_cast<void *>(kernel), dim3(grid), dim3(32 * warps_of(WDT == MOE_MXFP4)), args, smem, s);
 }
 
 template <int DT>
 cudaError_t launch_dt(const Params &p, bool mx, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s)
 {
     if (p.T <= 8)
-        return mx ? launch_one<DT, MOE_MXFP4, 1>(p, info, grid, smem, s) : launch_one<DT, DT, 1>(p, info, grid, smem, s);
-    return mx ? launch_one<DT, MOE_MXFP4, 8>(p, info, grid, smem, s) : launch_one<DT, DT, 8>(p, info, grid, smem, s);
+        return mx ? launch_one<DT, MOE_MXFP4, false>(p, info, grid, smem, s) : launch_one<DT, DT, false>(p, info, grid, smem, s);
+    return mx ? launch_one<DT, MOE_MXFP4, true>(p, info, grid, smem, s) : launch_one<DT, DT, true>(p, info, grid, smem, s);
 }
 
 cudaError_t launch_bf16(const Params &p, bool mx, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s);
