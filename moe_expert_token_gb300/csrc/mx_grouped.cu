@@ -38,7 +38,7 @@ constexpr int kThreads = 512;
 constexpr int kEpilogueWarp = 4, kEpilogueWarps = 8, kScaleWarp = 12;
 constexpr int kRowTile = 128;            // weight rows of one matrix instruction
 constexpr int kStepBytes = 128;          // bytes of a row in a stage: 256 elements
-constexpr int kBoxRows = 32;             // token rows of one copy
+__host__ __device__ constexpr int box_rows(int i) { return i < 2 ? 32 << i : 64 * i; }   // token rows of a copy: 32, 64, 128, 192
 constexpr int kMaxStages = 8;
 constexpr int kColumns = 512;            // all of tensor memory
 constexpr int kMaxExperts = 4096;
@@ -57,6 +57,10 @@ struct Params {
     int align, w_align;    // of scale rows: 16, 8 or 2 bytes
     int out_wide;          // 16-bit rows can be written 8 bytes, MXFP4 rows 4 bytes at a time
     int sm_stage, sm_tables, sm_scales;
+};
+
+struct Maps {
+    CUtensorMap w, x[4];   // x: boxes of box_rows(i) rows
 };
 
 struct Tile {
@@ -336,8 +340,7 @@ __device__ __forceinline__ void store16(const Params &p, int64_t row, int rows, 
 
 template <bool kGated, int kOut>
 __global__ void __launch_bounds__(kThreads, 1)
-    grouped_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap x_map,
-                   const __grid_constant__ CUtensorMap w_map)
+    grouped_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     Shared *sh = reinterpret_cast<Shared *>(smem);
@@ -369,8 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mrr::mbar_init(mrr::smem_addr(&sh->drained), 1);
         sh->abort = 0;
         mrr::mbar_init_fence();
-        tc::prefetch_map(&x_map);
-        tc::prefetch_map(&w_map);
+        tc::prefetch_map(&maps.w);
+        for (const CUtensorMap &m : maps.x)
+            tc::prefetch_map(&m);
     }
     if (warp == 1)
         tc::alloc(mrr::smem_addr(&sh->tmem), kColumns);
@@ -390,59 +394,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     };
 
-    if (warp == 0) {
-        if (lane == 0) {   // codes
-            int stage = 0;
-            uint32_t parity = 1u, issued = 0u;
-            bool ok = true;
-            for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
-                const Tile t = tile_at(p, tables, features, i);
-                const int w_row = t.expert * mats * p.N + t.feature, second = kGated ? p.N : kRowTile;
-                const int boxes = (t.columns + kBoxRows - 1) / kBoxRows;
-                for (int k = 0; k < steps; ++k) {
-                    if (!(ok = wait(sh, &sh->empty[stage], parity)))
-                        break;
-                    const uint32_t at = stage0 + stage * stage_size, bar = mrr::smem_addr(&sh->full[stage]);
-                    mrr::mbar_arrive_expect_tx(bar, 2 * kRowTile * kStepBytes + boxes * kBoxRows * kStepBytes);
-                    tc::load_box(at, &w_map, k * kStepBytes, w_row, bar);
-                    tc::load_box(at + kRowTile * kStepBytes, &w_map, k * kStepBytes, w_row + second, bar);
-                    for (int b = 0; b < boxes; ++b)
-                        tc::load_box(at + off_x + b * kBoxRows * kStepBytes, &x_map, k * kStepBytes, t.row + b * kBoxRows,
-                                     bar);
-                    issued |= 1u << stage;
-                    next_stage(stage, parity);
+    // Warps 0 and 1 run their loops as whole warps, one lane issuing: so the compiler keeps what an
+    // instruction takes in uniform registers.  As one thread's code each matrix instruction cost 84
+    // cycles to issue, as many as it runs.
+    if (warp == 0) {   // codes
+        const bool leader = tc::elect();
+        int stage = 0;
+        uint32_t parity = 1u, issued = 0u;
+        bool ok = true;
+        for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
+            const Tile t = tile_at(p, tables, features, i);
+            const int w_row = tc::uniform(t.expert * mats * p.N + t.feature), x_row = tc::uniform(t.row);
+            const int second = kGated ? p.N : kRowTile;
+            // one copy for all token rows: the smallest box that holds them
+            const int box = tc::uniform(t.columns <= 32 ? 0 : t.columns <= 64 ? 1 : t.columns <= 128 ? 2 : 3);
+            const CUtensorMap *x_map = &maps.x[box];
+            const uint32_t bytes = (2 * kRowTile + box_rows(box)) * kStepBytes;
+            for (int k = 0; k < steps; ++k) {
+                if (!(ok = wait(sh, &sh->empty[stage], parity)))
+                    break;
+                const uint32_t at = stage0 + stage * stage_size, bar = mrr::smem_addr(&sh->full[stage]);
+                if (leader) {
+                    mrr::mbar_arrive_expect_tx(bar, bytes);
+                    tc::load_box(at, &maps.w, k * kStepBytes, w_row, bar);
+                    tc::load_box(at + kRowTile * kStepBytes, &maps.w, k * kStepBytes, w_row + second, bar);
+                    tc::load_box(at + off_x, x_map, k * kStepBytes, x_row, bar);
                 }
-            }
-            if (!ok) {   // leave no copy in flight: give each stage's a moment to land
-                for (int s = 0; s < p.stages; ++s)
-                    if (issued >> s & 1u)
-                        for (int b = 0; b < 2; ++b)
-                            mrr::mbar_wait_bounded(mrr::smem_addr(&sh->full[s]), b, 1000000ull);
+                __syncwarp();
+                issued |= 1u << stage;
+                next_stage(stage, parity);
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0) {   // matrix instructions
-            int stage = 0, set = 0;
-            uint32_t parity = 0u, set_parity = 1u;
-            bool ok = true;
-            const uint32_t scale_columns = 16 + 8 * groups, scales0 = tmem + p.sums * 2 * p.tokens;
-            for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
-                const Tile t = tile_at(p, tables, features, i);
-                if (!(ok = wait(sh, &sh->sums_empty[set], set_parity)))
+        if (!ok && lane == 0) {   // leave no copy in flight: give each stage's a moment to land
+            for (int s = 0; s < p.stages; ++s)
+                if (issued >> s & 1u)
+                    for (int b = 0; b < 2; ++b)
+                        mrr::mbar_wait_bounded(mrr::smem_addr(&sh->full[s]), b, 1000000ull);
+        }
+    } else if (warp == 1) {   // matrix instructions
+        const bool leader = tc::elect();
+        int stage = 0, set = 0;
+        uint32_t parity = 0u, set_parity = 1u;
+        bool ok = true;
+        const uint32_t scale_columns = 16 + 8 * groups, scales0 = tmem + p.sums * 2 * p.tokens;
+        for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
+            const Tile t = tile_at(p, tables, features, i);
+            if (!(ok = wait(sh, &sh->sums_empty[set], set_parity)))
+                break;
+            tc::fence_after();
+            const uint32_t d = tmem + set * 2 * p.tokens;
+            const uint32_t columns = tc::uniform(t.columns);
+            const uint32_t instr[2] = {tc::mxf4_instr(columns, 0), tc::mxf4_instr(columns, 1)};
+            for (int k = 0; k < steps; ++k) {
+                if (!(ok = wait(sh, &sh->full[stage], parity)))
                     break;
                 tc::fence_after();
-                const uint32_t d = tmem + set * 2 * p.tokens;
-                const uint32_t instr[2] = {tc::mxf4_instr(t.columns, 0), tc::mxf4_instr(t.columns, 1)};
-                for (int k = 0; k < steps; ++k) {
-                    if (!(ok = wait(sh, &sh->full[stage], parity)))
-                        break;
-                    tc::fence_after();
-                    const uint32_t at = stage0 + stage * stage_size;
-                    const uint32_t sfa = scales0 + stage * scale_columns, sfb = sfa + 16;
-                    const uint64_t w0 = tc::desc_swizzle128(at), w1 = tc::desc_swizzle128(at + kRowTile * kStepBytes);
-                    const uint64_t x = tc::desc_swizzle128(at + off_x);
-                    const int parts = min(4, (p.K - k * 256 + 63) / 64);
-                    for (int j = 0; j < parts; ++j) {   // 64 elements: 32 bytes further along the rows
+                const uint32_t at = stage0 + stage * stage_size;
+                const uint32_t sfa = scales0 + stage * scale_columns, sfb = sfa + 16;
+                const uint64_t w0 = tc::desc_swizzle128(at), w1 = tc::desc_swizzle128(at + kRowTile * kStepBytes);
+                const uint64_t x = tc::desc_swizzle128(at + off_x);
+                if (leader) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {   // 64 elements (past K: zeros): 32 bytes further along the rows
                         const uint32_t half = j / 2;
                         tc::mma_mxf4(d, w0 + 2 * j, x + 2 * j, instr[j % 2], sfa + 4 * half, sfb + 4 * groups * half,
                                      k > 0 || j > 0);
@@ -450,19 +463,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      sfb + 4 * groups * half, k > 0 || j > 0);
                     }
                     tc::commit(mrr::smem_addr(&sh->empty[stage]));
-                    next_stage(stage, parity);
+                    if (k + 1 == steps)
+                        tc::commit(mrr::smem_addr(&sh->sums_full[set]));
                 }
-                if (ok)
-                    tc::commit(mrr::smem_addr(&sh->sums_full[set]));
-                if (++set == p.sums) {
-                    set = 0;
-                    set_parity ^= 1u;
-                }
+                __syncwarp();
+                next_stage(stage, parity);
             }
-            if (!ok) {   // tensor memory is freed only after what was issued is done
-                tc::commit(mrr::smem_addr(&sh->drained));
-                mrr::mbar_wait_bounded(mrr::smem_addr(&sh->drained), 0, 100000000ull);
+            if (++set == p.sums) {
+                set = 0;
+                set_parity ^= 1u;
             }
+        }
+        if (!ok && leader) {   // tensor memory is freed only after what was issued is done
+            tc::commit(mrr::smem_addr(&sh->drained));
+            mrr::mbar_wait_bounded(mrr::smem_addr(&sh->drained), 0, 100000000ull);
         }
     } else if (warp >= kScaleWarp) {   // scales
         const int r = threadIdx.x - 32 * kScaleWarp;
@@ -621,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kGated, int kOut>
-cudaError_t launch(const Params &p, const CUtensorMap &x_map, const CUtensorMap &w_map, const mrr_device::Info &info, size_t smem,
+cudaError_t launch(const Params &p, const Maps &maps, const mrr_device::Info &info, size_t smem,
                    cudaStream_t s)
 {
     static std::atomic<uint64_t> allowed;
@@ -629,7 +643,7 @@ cudaError_t launch(const Params &p, const CUtensorMap &x_map, const CUtensorMap 
     const cudaError_t err = mrr_device::allow_smem(kernel, info, allowed);
     if (err != cudaSuccess)
         return err;
-    kernel<<<info.sms, kThreads, smem, s>>>(p, x_map, w_map);
+    kernel<<<info.sms, kThreads, smem, s>>>(p, maps);
     return cudaGetLastError();
 }
 
@@ -694,21 +708,23 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
     p.stages = stages < kMaxStages ? stages : kMaxStages;
     if (p.stages < 2)
         return MRR_ERR_CUDA;
-    CUtensorMap x_map, w_map;
-    if (!tc::make_map(&w_map, w_codes, E * N * (gated ? 2 : 1), K / 2, kRowTile) ||
-        !tc::make_map(&x_map, A ? codes : w_codes, A ? A : 1, K / 2, kBoxRows))
+    Maps maps;
+    bool made = tc::make_map(&maps.w, w_codes, E * N * (gated ? 2 : 1), K / 2, kRowTile);
+    for (int i = 0; i < 4; ++i)
+        made = made && tc::make_map(&maps.x[i], A ? codes : w_codes, A ? A : 1, K / 2, box_rows(i));
+    if (!made)
         return MRR_ERR_CUDA;
     const size_t smem = (size_t)p.sm_stage + (size_t)p.stages * stage_bytes(p.tokens);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t err;
     if (out_dt == MOE_BF16)
-        err = gated ? launch<true, MOE_BF16>(p, x_map, w_map, info, smem, st) : launch<false, MOE_BF16>(p, x_map, w_map, info, smem, st);
+        err = gated ? launch<true, MOE_BF16>(p, maps, info, smem, st) : launch<false, MOE_BF16>(p, maps, info, smem, st);
     else if (out_dt == MOE_F16)
-        err = gated ? launch<true, MOE_F16>(p, x_map, w_map, info, smem, st) : launch<false, MOE_F16>(p, x_map, w_map, info, smem, st);
+        err = gated ? launch<true, MOE_F16>(p, maps, info, smem, st) : launch<false, MOE_F16>(p, maps, info, smem, st);
     else if (out_dt == MOE_F32)
-        err = gated ? launch<true, MOE_F32>(p, x_map, w_map, info, smem, st) : launch<false, MOE_F32>(p, x_map, w_map, info, smem, st);
+        err = gated ? launch<true, MOE_F32>(p, maps, info, smem, st) : launch<false, MOE_F32>(p, maps, info, smem, st);
     else
-        err = gated ? launch<true, MOE_MXFP4>(p, x_map, w_map, info, smem, st) : launch<false, MOE_MXFP4>(p, x_map, w_map, info, smem, st);
+        err = gated ? launch<true, MOE_MXFP4>(p, maps, info, smem, st) : launch<false, MOE_MXFP4>(p, maps, info, smem, st);
     if (err != cudaSuccess) {
         (void)cudaGetLastError();
         return MRR_ERR_CUDA;

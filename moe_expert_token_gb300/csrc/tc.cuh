@@ -10,6 +10,17 @@
 
 namespace tc {
 
+// true in one lane of a converged warp, always the same
+__device__ __forceinline__ bool elect()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0u;
+}
+
+// a value that is the same in all lanes, made known as such
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // ---------------------------------------------------------------- tensor memory
 
 __device__ __forceinline__ void alloc(uint32_t smem_result, uint32_t columns)
