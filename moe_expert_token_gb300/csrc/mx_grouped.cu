@@ -42,6 +42,7 @@ __host__ __device__ constexpr int box_rows(int i) { return i < 2 ? 32 << i : 64 
 constexpr int kMaxStages = 8;
 constexpr int kColumns = 512;            // all of tensor memory
 constexpr int kMaxExperts = 4096;
+constexpr int kSingleRows = 32;          // up to so many rows an expert on average: single weight tiles
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct Params {
@@ -68,9 +69,9 @@ struct Tile {
 };
 
 __host__ __device__ constexpr int groups_of(int tokens) { return (tokens + 127) / 128; }
-__host__ __device__ constexpr int stage_bytes(int tokens)
+__host__ __device__ constexpr int stage_bytes(int halves, int tokens)
 {
-    return 2 * kRowTile * kStepBytes + tokens * kStepBytes;
+    return (halves * kRowTile + tokens) * kStepBytes;
 }
 
 struct Shared {
@@ -179,7 +180,8 @@ __device__ int scan_counts(const Params &p, Shared *sh, int *tables)
     return 0;
 }
 
-__device__ __forceinline__ Tile tile_at(const Params &p, const int *tables, int features, long long index)
+// tile `index` of an expert's rows by `width` output features
+__device__ __forceinline__ Tile tile_at(const Params &p, const int *tables, int features, int width, long long index)
 {
     const int *rows = tables, *tiles = tables + p.E + 1;
     int lo = 0, hi = p.E - 1;   // the last expert whose first tile is at or before index (one that has tiles)
@@ -195,7 +197,7 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *tables, int 
     const int share = (((count + n - 1) / n) + 15) & ~15;
     Tile t;
     t.expert = lo;
-    t.feature = f * (p.gated ? kRowTile : 2 * kRowTile);
+    t.feature = f * width;
     t.row = rows[lo] + i * share;
     t.rows = min(share, count - i * share);
     t.columns = (t.rows + 15) & ~15;
@@ -237,14 +239,14 @@ __device__ __forceinline__ void scales32(uint32_t (&v)[8], const uint8_t *s, int
             v[i] &= left >= 4 * i + 4 ? kFull : left > 4 * i ? (1u << (8 * (left - 4 * i))) - 1u : 0u;
 }
 
-// true for every thread of the scale warps if `failed` is for any of them
-__device__ __forceinline__ bool any_scale_warp(bool failed)
+// named barrier `id` of `threads` threads: true for all of them if `failed` is for any
+__device__ __forceinline__ bool any_of(int id, int threads, bool failed)
 {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-                 "barrier.cta.red.or.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 "barrier.cta.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(r)
-                 : "r"((uint32_t)failed)
+                 : "r"((uint32_t)failed), "r"(id), "r"(threads)
                  : "memory");
     return r != 0u;
 }
@@ -338,7 +340,9 @@ __device__ __forceinline__ void store16(const Params &p, int64_t row, int rows, 
     }
 }
 
-template <bool kGated, int kOut>
+// kTiles: 128-row weight tiles of a tile of results.  2: the gate rows and their up rows, or neighbours.
+// 1: 64 gate rows and their 64 up rows, or 128 rows.
+template <bool kGated, int kOut, int kTiles>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps)
 {
@@ -354,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (bad)
         return;
-    constexpr int mats = kGated ? 2 : 1, kFeatures = kGated ? kRowTile : 2 * kRowTile;
+    constexpr int mats = kGated ? 2 : 1, kFeatures = kTiles * kRowTile / mats;
+    constexpr bool kMixed = kGated && kTiles == 1;   // gate and up rows in one tile
     const int features = (p.N + kFeatures - 1) / kFeatures;
     const long long total = (long long)tables[2 * p.E + 1] * features;
     if ((long long)blockIdx.x >= total)
@@ -385,8 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int steps = (p.K + 255) / 256, groups = groups_of(p.tokens);
     const uint32_t stage0 = mrr::smem_addr(smem) + p.sm_stage;
-    const uint32_t stage_size = stage_bytes(p.tokens);
-    const uint32_t off_x = 2 * kRowTile * kStepBytes;
+    const uint32_t stage_size = stage_bytes(kTiles, p.tokens);
+    const uint32_t scale_columns = 8 * kTiles + 8 * groups, sums_columns = kTiles * p.tokens;
+    const uint32_t off_x = kTiles * kRowTile * kStepBytes;
     auto next_stage = [&](int &stage, uint32_t &parity) {
         if (++stage == p.stages) {
             stage = 0;
@@ -403,13 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t parity = 1u, issued = 0u;
         bool ok = true;
         for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
-            const Tile t = tile_at(p, tables, features, i);
+            const Tile t = tile_at(p, tables, features, kFeatures, i);
             const int w_row = tc::uniform(t.expert * mats * p.N + t.feature), x_row = tc::uniform(t.row);
             const int second = kGated ? p.N : kRowTile;
             // one copy for all token rows: the smallest box that holds them
             const int box = tc::uniform(t.columns <= 32 ? 0 : t.columns <= 64 ? 1 : t.columns <= 128 ? 2 : 3);
             const CUtensorMap *x_map = &maps.x[box];
-            const uint32_t bytes = (2 * kRowTile + box_rows(box)) * kStepBytes;
+            const uint32_t bytes = (kTiles * kRowTile + box_rows(box)) * kStepBytes;
             for (int k = 0; k < steps; ++k) {
                 if (!(ok = wait(sh, &sh->empty[stage], parity)))
                     break;
@@ -417,7 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (leader) {
                     mrr::mbar_arrive_expect_tx(bar, bytes);
                     tc::load_box(at, &maps.w, k * kStepBytes, w_row, bar);
-                    tc::load_box(at + kRowTile * kStepBytes, &maps.w, k * kStepBytes, w_row + second, bar);
+                    if (kTiles == 2 || kMixed)
+                        tc::load_box(at + (kMixed ? kRowTile / 2 : kRowTile) * kStepBytes, &maps.w, k * kStepBytes,
+                                     w_row + second, bar);
                     tc::load_box(at + off_x, x_map, k * kStepBytes, x_row, bar);
                 }
                 __syncwarp();
@@ -436,13 +444,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         int stage = 0, set = 0;
         uint32_t parity = 0u, set_parity = 1u;
         bool ok = true;
-        const uint32_t scale_columns = 16 + 8 * groups, scales0 = tmem + p.sums * 2 * p.tokens;
+        const uint32_t scales0 = tmem + p.sums * sums_columns;
         for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
-            const Tile t = tile_at(p, tables, features, i);
+            const Tile t = tile_at(p, tables, features, kFeatures, i);
             if (!(ok = wait(sh, &sh->sums_empty[set], set_parity)))
                 break;
             tc::fence_after();
-            const uint32_t d = tmem + set * 2 * p.tokens;
+            const uint32_t d = tmem + set * sums_columns;
             const uint32_t columns = tc::uniform(t.columns);
             const uint32_t instr[2] = {tc::mxf4_instr(columns, 0), tc::mxf4_instr(columns, 1)};
             for (int k = 0; k < steps; ++k) {
@@ -450,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 tc::fence_after();
                 const uint32_t at = stage0 + stage * stage_size;
-                const uint32_t sfa = scales0 + stage * scale_columns, sfb = sfa + 16;
+                const uint32_t sfa = scales0 + stage * scale_columns, sfb = sfa + 8 * kTiles;
                 const uint64_t w0 = tc::desc_swizzle128(at), w1 = tc::desc_swizzle128(at + kRowTile * kStepBytes);
                 const uint64_t x = tc::desc_swizzle128(at + off_x);
                 if (leader) {
@@ -459,8 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t half = j / 2;
                         tc::mma_mxf4(d, w0 + 2 * j, x + 2 * j, instr[j % 2], sfa + 4 * half, sfb + 4 * groups * half,
                                      k > 0 || j > 0);
-                        tc::mma_mxf4(d + p.tokens, w1 + 2 * j, x + 2 * j, instr[j % 2], sfa + 8 + 4 * half,
-                                     sfb + 4 * groups * half, k > 0 || j > 0);
+                        if (kTiles == 2)
+                            tc::mma_mxf4(d + p.tokens, w1 + 2 * j, x + 2 * j, instr[j % 2], sfa + 8 + 4 * half,
+                                         sfb + 4 * groups * half, k > 0 || j > 0);
                     }
                     tc::commit(mrr::smem_addr(&sh->empty[stage]));
                     if (k + 1 == steps)
@@ -486,14 +495,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the next four steps' bytes are loaded while these four are stored
         long long ahead = blockIdx.x;
         int ahead_k = 0;
-        Tile t = tile_at(p, tables, features, ahead);
+        Tile t = tile_at(p, tables, features, kFeatures, ahead);
         auto load = [&](uint32_t (&v)[4][8]) {
             if (ahead >= total)
                 return;
             const int b0 = ahead_k * 8;
-            const int64_t w_row = (int64_t)t.expert * mats * p.N + t.feature + r;
+            int64_t w_row = (int64_t)t.expert * mats * p.N + t.feature + r;
+            if (kMixed && r >= kRowTile / 2)
+                w_row += p.N - kRowTile / 2;
             const int64_t row[4] = {w_row, w_row + second, (int64_t)t.row + r, (int64_t)t.row + r + 128};
-            const bool in[4] = {w_row < w_rows, w_row + second < w_rows, r < t.rows, r + 128 < t.rows};
+            const bool in[4] = {w_row < w_rows, kTiles == 2 && w_row + second < w_rows, r < t.rows, r + 128 < t.rows};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if (in[q])
@@ -508,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ahead_k = 0;
                 ahead += gridDim.x;
                 if (ahead < total)
-                    t = tile_at(p, tables, features, ahead);
+                    t = tile_at(p, tables, features, kFeatures, ahead);
             }
         };
         uint32_t now[4][8] = {}, next[4][8] = {};
@@ -518,10 +529,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // An atom is 128 rows by 4 blocks: row q's bytes are word q / 32 of 16-byte line q % 32, and in
         // tensor memory column q / 32 of lane q % 32, in each of the four lane quarters.  Atoms in
         // order: weights [tile][half of the step], tokens [half][group of 128 rows].
-        const uint32_t buffers = mrr::smem_addr(smem) + p.sm_scales, buffer_size = 2048 + 1024 * groups;
+        constexpr uint32_t kTokenAtoms = kTiles * 1024;   // where the tokens' atoms begin
+        const uint32_t buffers = mrr::smem_addr(smem) + p.sm_scales, buffer_size = kTokenAtoms + 1024 * groups;
         const uint32_t to = (r % 32) * 16 + (r / 32) * 4;
-        const uint32_t scale_columns = 16 + 8 * groups;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + p.sums * 2 * p.tokens;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + p.sums * sums_columns;
         bool ok = true;
         for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
             for (int k = 0; ok && k < steps; k += 4) {
@@ -542,16 +553,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     put(0, now[0][2 * u]);
                     put(512, now[0][2 * u + 1]);
-                    put(1024, now[1][2 * u]);
-                    put(1536, now[1][2 * u + 1]);
-                    put(2048, now[2][2 * u]);
-                    put(2048 + 512 * groups, now[2][2 * u + 1]);
+                    if (kTiles == 2) {
+                        put(1024, now[1][2 * u]);
+                        put(1536, now[1][2 * u + 1]);
+                    }
+                    put(kTokenAtoms, now[2][2 * u]);
+                    put(kTokenAtoms + 512 * groups, now[2][2 * u + 1]);
                     if (groups == 2) {
-                        put(2048 + 512, now[3][2 * u]);
-                        put(2048 + 1536, now[3][2 * u + 1]);
+                        put(kTokenAtoms + 512, now[3][2 * u]);
+                        put(kTokenAtoms + 1536, now[3][2 * u + 1]);
                     }
                     // the other buffer is free again once all four warps are here
-                    if (any_scale_warp(!wait(sh, &sh->empty[stage], parity))) {
+                    if (any_of(1, 128, !wait(sh, &sh->empty[stage], parity))) {
                         ok = false;
                         break;
                     }
@@ -559,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t columns = lanes + stage * scale_columns;
 #pragma unroll
                     for (int a = 0; a < 8; ++a)
-                        if (a < 4 + 2 * groups) {
+                        if (a < 2 * kTiles + 2 * groups) {
                             uint32_t v[4];
                             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
@@ -581,43 +594,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         int set = 0;
         uint32_t parity = 0u;
         for (long long i = blockIdx.x; i < total; i += gridDim.x) {
-            const Tile t = tile_at(p, tables, features, i);
-            if (!wait(sh, &sh->sums_full[set], parity))
+            const Tile t = tile_at(p, tables, features, kFeatures, i);
+            const bool failed = !wait(sh, &sh->sums_full[set], parity);
+            // kMixed: lane quarters 0 and 1 hold gate values, 2 and 3 the up values of the same features,
+            // which change hands through shared memory; the two warps leave together
+            const int pair = 2 + 2 * part + quarter % 2;
+            if (kMixed ? any_of(pair, 64, failed) : failed)
                 break;
             tc::fence_after();
-            const int n0 = t.feature + 32 * quarter;
-            const uint32_t d = tmem + set * 2 * p.tokens + ((uint32_t)(32 * quarter) << 16);
-            for (int c = 16 * part; c < t.columns; c += 32) {
+            const int n0 = t.feature + 32 * (kMixed ? quarter % 2 : quarter);
+            const uint32_t d = tmem + set * sums_columns + ((uint32_t)(32 * quarter) << 16);
+            float *ups = reinterpret_cast<float *>(smem + p.sm_scales + 2 * (kTiles * 1024 + 1024 * groups)) +
+                         (2 * part + quarter % 2) * 512 + lane;
+            auto release = [&]() {   // the sums have been read
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(mrr::smem_addr(&sh->sums_empty[set]));
+            };
+            // the results of columns c .. c + 15, z those of the second tile
+            auto results = [&](int c, int rows, float (&y)[16], float (&z)[16]) {
                 uint32_t a[16], b[16];
                 tc::load16(d + c, a);
-                tc::load16(d + p.tokens + c, b);
+                if (kTiles == 2)
+                    tc::load16(d + p.tokens + c, b);
                 tc::load_wait();
-                const int64_t row = t.row + c;
-                const int rows = min(16, t.rows - c);
-                float y[16], z[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     y[j] = __uint_as_float(a[j]);
-                    z[j] = __uint_as_float(b[j]);
-                    if (kGated)
-                        y[j] = swiglu(y[j], z[j]);
+                    if (kTiles == 2)
+                        z[j] = __uint_as_float(b[j]);
                 }
+                if (kMixed) {
+                    if (quarter >= 2)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            ups[32 * j] = y[j];
+                    any_of(pair, 64, false);
+                    if (quarter < 2)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            z[j] = ups[32 * j];
+                    any_of(pair, 64, false);   // read: the next columns may come
+                }
+                if (kGated)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        y[j] = swiglu(y[j], z[j]);
                 if (p.row_weight) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float w = j < rows ? __ldg(p.row_weight + row + j) : 0.f;
+                        const float w = j < rows ? __ldg(p.row_weight + t.row + c + j) : 0.f;
                         y[j] *= w;
                         z[j] *= w;
                     }
                 }
-                store16<kOut>(p, row, rows, n0, lane, y);
-                if (!kGated)
-                    store16<kOut>(p, row, rows, n0 + kRowTile, lane, z);
+            };
+            for (int c = 16 * part; c < t.columns; c += 32) {
+                const int rows = min(16, t.rows - c);
+                float y[16], z[16];
+                results(c, rows, y, z);
+                if (!kMixed || quarter < 2)
+                    store16<kOut>(p, t.row + c, rows, n0, lane, y);
+                if (!kGated && kTiles == 2)
+                    store16<kOut>(p, t.row + c, rows, n0 + kRowTile, lane, z);
             }
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0)
-                tc::mbar_arrive(mrr::smem_addr(&sh->sums_empty[set]));
+            release();
             if (++set == p.sums) {
                 set = 0;
                 parity ^= 1u;
@@ -634,17 +676,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::dealloc(tmem, kColumns);
 }
 
-template <bool kGated, int kOut>
-cudaError_t launch(const Params &p, const Maps &maps, const mrr_device::Info &info, size_t smem,
+template <bool kGated, int kOut, int kTiles>
+cudaError_t launch_tiles(const Params &p, const Maps &maps, const mrr_device::Info &info, size_t smem,
                    cudaStream_t s)
 {
     static std::atomic<uint64_t> allowed;
-    auto kernel = grouped_kernel<kGated, kOut>;
+    auto kernel = grouped_kernel<kGated, kOut, kTiles>;
     const cudaError_t err = mrr_device::allow_smem(kernel, info, allowed);
     if (err != cudaSuccess)
         return err;
     kernel<<<info.sms, kThreads, smem, s>>>(p, maps);
     return cudaGetLastError();
+}
+
+template <bool kGated, int kOut>
+cudaError_t launch(const Params &p, int tiles, const Maps &maps, const mrr_device::Info &info, size_t smem, cudaStream_t s)
+{
+    return tiles == 2 ? launch_tiles<kGated, kOut, 2>(p, maps, info, smem, s)
+                      : launch_tiles<kGated, kOut, 1>(p, maps, info, smem, s);
 }
 
 }  // namespace
@@ -691,6 +740,9 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
     // Few rows an expert: narrow tiles, more stages, two sets of sums.  Else as wide as tensor memory
     // allows beside the scales (2 x 192 columns): a wide tile re-reads its weights less often.
     p.tokens = A <= 64 * E ? 64 : 192;
+    // Very few: one 128-row weight tile a block instead of two, so that the blocks' shares come out
+    // more even.
+    const int tiles = A <= kSingleRows * E ? 1 : 2;
     p.sums = p.tokens <= 64 ? 2 : 1;
     auto aligned = [K](const void *s) {
         const uint64_t both = (uintptr_t)s | (uint64_t)scale_row_bytes(K);
@@ -701,30 +753,32 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
     p.out_wide = out_dt == MOE_MXFP4 ? (uintptr_t)out % 4 == 0 : (uintptr_t)out % 8 == 0 && N % 4 == 0;
     p.sm_tables = (int)mrr_ws::round_up(sizeof(Shared), 16);
     p.sm_scales = (int)mrr_ws::round_up(p.sm_tables + 8 * (E + 1), 16);
-    p.sm_stage = (int)mrr_ws::round_up(p.sm_scales + 2 * (2048 + 1024 * groups_of(p.tokens)), 1024);
-    const int columns_left = (kColumns - p.sums * 2 * p.tokens) / (16 + 8 * groups_of(p.tokens));
-    int stages = (info.smem_max - p.sm_stage) / stage_bytes(p.tokens);
+    p.sm_stage = (int)mrr_ws::round_up(p.sm_scales + 2 * (tiles * 1024 + 1024 * groups_of(p.tokens)) +
+                                       (gated && tiles == 1 ? 4 * 2048 : 0), 1024);
+    const int columns_left = (kColumns - p.sums * tiles * p.tokens) / (8 * tiles + 8 * groups_of(p.tokens));
+    int stages = (info.smem_max - p.sm_stage) / stage_bytes(tiles, p.tokens);
     stages = stages < columns_left ? stages : columns_left;
     p.stages = stages < kMaxStages ? stages : kMaxStages;
     if (p.stages < 2)
         return MRR_ERR_CUDA;
     Maps maps;
-    bool made = tc::make_map(&maps.w, w_codes, E * N * (gated ? 2 : 1), K / 2, kRowTile);
+    bool made = tc::make_map(&maps.w, w_codes, E * N * (gated ? 2 : 1), K / 2,
+                             gated && tiles == 1 ? kRowTile / 2 : kRowTile);
     for (int i = 0; i < 4; ++i)
         made = made && tc::make_map(&maps.x[i], A ? codes : w_codes, A ? A : 1, K / 2, box_rows(i));
     if (!made)
         return MRR_ERR_CUDA;
-    const size_t smem = (size_t)p.sm_stage + (size_t)p.stages * stage_bytes(p.tokens);
+    const size_t smem = (size_t)p.sm_stage + (size_t)p.stages * stage_bytes(tiles, p.tokens);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t err;
     if (out_dt == MOE_BF16)
-        err = gated ? launch<true, MOE_BF16>(p, maps, info, smem, st) : launch<false, MOE_BF16>(p, maps, info, smem, st);
+        err = gated ? launch<true, MOE_BF16>(p, tiles, maps, info, smem, st) : launch<false, MOE_BF16>(p, tiles, maps, info, smem, st);
     else if (out_dt == MOE_F16)
-        err = gated ? launch<true, MOE_F16>(p, maps, info, smem, st) : launch<false, MOE_F16>(p, maps, info, smem, st);
+        err = gated ? launch<true, MOE_F16>(p, tiles, maps, info, smem, st) : launch<false, MOE_F16>(p, tiles, maps, info, smem, st);
     else if (out_dt == MOE_F32)
-        err = gated ? launch<true, MOE_F32>(p, maps, info, smem, st) : launch<false, MOE_F32>(p, maps, info, smem, st);
+        err = gated ? launch<true, MOE_F32>(p, tiles, maps, info, smem, st) : launch<false, MOE_F32>(p, tiles, maps, info, smem, st);
     else
-        err = gated ? launch<true, MOE_MXFP4>(p, maps, info, smem, st) : launch<false, MOE_MXFP4>(p, maps, info, smem, st);
+        err = gated ? launch<true, MOE_MXFP4>(p, tiles, maps, info, smem, st) : launch<false, MOE_MXFP4>(p, tiles, maps, info, smem, st);
     if (err != cudaSuccess) {
         (void)cudaGetLastError();
         return MRR_ERR_CUDA;
