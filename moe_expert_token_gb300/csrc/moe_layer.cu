@@ -15,6 +15,7 @@ bool sizes_ok(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
            E <= MRR_GATE_MAX_EXPERTS && k >= 1 && k <= 64 && k <= E;
 }
 
+constexpr int kPairTokens = 4;   // up to so many tokens h is held in two parts
 constexpr int kMaxGrid = 512;    // words of the first grid-wide wait
 
 struct Layout {
@@ -40,7 +41,7 @@ Layout layout(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
     l.route_weight = take(T * k * 4);
     l.x_scale = take(T * 4);
     l.h_max = take(T * 4);
-    l.h = take(T * k * l.Ip * 2);
+    l.h = take((T <= kPairTokens ? 2 : 1) * T * k * l.Ip * 2);
     l.h_field = take(T * k * (l.Ip / 16));
     l.bytes = at;
     return l;
@@ -123,6 +124,8 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     p.x_scale = reinterpret_cast<float *>(ws + l.x_scale);
     p.h_max = reinterpret_cast<uint32_t *>(ws + l.h_max);
     p.h = reinterpret_cast<uint16_t *>(ws + l.h);
+    p.h_plane = T * k * l.Ip;
+    p.pairs = T <= kPairTokens;
     p.h_field = ws + l.h_field;
     p.Hp = l.Hp, p.Ip = l.Ip;
     // the router's 16-expert tiles, split over H until the blocks have one each

@@ -77,7 +77,13 @@ struct Params {
     float *route_weight;
     float *x_scale;               // [T]: what undoes their scaling
     uint32_t *h_max;              // [T]: float bits of the largest |h| of the token
-    uint16_t *h;                  // [T k][Ip]
+    // h in 16 bits.  Up to 4 tokens (pairs) it is the sum of two parts: the down product has 8 columns
+    // anyway, and the four that the tokens leave take the second parts, so that y is rounded once, at
+    // its end.  With more tokens a second part would cost what it reads (8 % of a layer for 48 tokens,
+    // 17 % for 7), and h is rounded once: y's error is then 1.4 times that of its own rounding.
+    uint16_t *h;                  // [1 or 2][T k][Ip]
+    int64_t h_plane;              // elements from the first parts to the second
+    int pairs;
     uint8_t *h_field;             // [T k][Ip / 16]: exponent of the power of two each tile of h carries (float16)
     int Hp, Ip, kparts;
     int x_wide, wr_wide;              // 16-byte loads possible
@@ -124,6 +130,14 @@ __device__ __forceinline__ uint32_t f16_scale_field(uint32_t amax)
 {
     const int field = (int)(amax >> 23);
     return field == 255 ? 127u : (uint32_t)min(268 - field, 253);   // field <= 254: at least 14
+}
+
+// v rounded to 16 bits (an infinity or NaN: 0, so that v less this is v)
+template <int DT>
+__device__ __forceinline__ float value_of(float v)
+{
+    const float r = DT == MOE_BF16 ? __bfloat162float(__float2bfloat16_rn(v)) : __half2float(__float2half_rn(v));
+    return fabsf(r) <= 3.4e38f ? r : 0.f;
 }
 
 __device__ __forceinline__ float field_value(uint32_t field) { return __uint_as_float(field << 23); }
@@ -880,6 +894,8 @@ struct Layer {
         for (int i = threadIdx.x; i < p.k * pad; i += kThreads) {
             const int64_t a = (int64_t)tok * p.k + i / pad;
             p.h[a * p.Ip + end + i % pad] = 0;
+            if (p.pairs)
+                p.h[p.h_plane + a * p.Ip + end + i % pad] = 0;
             if (i % pad % 16 == 0)
                 p.h_field[a * (p.Ip / 16) + (end + i % pad) / 16] = 253;
         }
@@ -1181,7 +1197,10 @@ struct Layer {
                                 atomicMax(p.h_max + tok, m);
                             }
                         }
-                        store1<MDT>(p.h, (int64_t)a * p.Ip + i0 + r, h);
+                        const int64_t to = (int64_t)a * p.Ip + i0 + r;
+                        store1<MDT>(p.h, to, h);
+                        if (!kMany && p.pairs)
+                            store1<MDT>(p.h, p.h_plane + to, h - value_of<MDT>(h));
                     }
                 }
                 buf ^= 1;
@@ -1197,16 +1216,18 @@ struct Layer {
             (blockIdx.x == 0 ? p.waits->go : p.waits->block[blockIdx.x]) = 0;
 
         if (!kMany) {
-            const uint32_t field = g < p.T ? field_of(g) : 127u;
+            const int token = p.pairs ? g % 4 : g;
+            const uint32_t field = token < p.T ? field_of(token) : 127u;
             Cursor w;   // where the operands in `b` come from
             bool some = (int)blockIdx.x < down_items && first_chunk(w);
             Column c[kCols], c1[kCols];
             Tokens<kDownGroups> b;
+            // up to 4 tokens: columns 4 .. 7 are the second parts of h
             auto enter = [&](Column &to) {
                 to = Column();
-                const int a = column_of(w.expert, g);
+                const int a = column_of(w.expert, p.pairs ? g % 4 : g);
                 if (a >= 0) {
-                    to.v = p.h + (int64_t)a * p.Ip + 8 * t;
+                    to.v = p.h + (p.pairs && g >= 4 ? p.h_plane : 0) + (int64_t)a * p.Ip + 8 * t;
                     to.tile = p.h_field + (int64_t)a * (p.Ip / 16) + t / 2;
                 }
                 to.field = field;
@@ -1238,9 +1259,12 @@ struct Layer {
                 __syncthreads();
                 if (threadIdx.x < 128) {
                     const int r = threadIdx.x % 16, tok = threadIdx.x / 16, n = item * 16 + r;
-                    if (tok < p.T && n < p.H)
-                        store1<DT>(p.y, (int64_t)tok * p.H + n,
-                                   gather(red(buf), 0, r, tok) * field_value(254u - field_of(tok)));
+                    if (tok < p.T && n < p.H) {
+                        float v = gather(red(buf), 0, r, tok);
+                        if (p.pairs)
+                            v += gather(red(buf), 0, r, tok + 4);
+                        store1<DT>(p.y, (int64_t)tok * p.H + n, v * field_value(254u - field_of(tok)));
+                    }
                 }
                 buf ^= 1;
             }

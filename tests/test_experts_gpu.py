@@ -3,7 +3,8 @@
 MXFP4 codes, scales and values must be equal.  Products are held to the oracle's bound on float32
 sums (see ``oracle.experts.sum_error``) plus the result's own rounding: a unit roundoff of 2^-8 for
 bfloat16, 2^-11 for float16, 2^-24 for float32, and half of the least subnormal.  In the layer, h
-is rounded once to 16 bits on the way, with the same unit roundoffs; tokens whose experts a change
+is rounded once to 16 bits on the way, with the same unit roundoffs, or with up to 4 tokens goes on as
+the sum of two 16-bit parts, with their squares (twice that allowed for); tokens whose experts a change
 of the logits within their float32 error would change are left out (few are).
 """
 import numpy as np
@@ -17,6 +18,7 @@ from oracle import experts as ox
 pytestmark = pytest.mark.gpu
 
 UNIT = {"float16": 2.0 ** -11, "bfloat16": 2.0 ** -8, "float32": 2.0 ** -24}
+H_UNIT = {"float16": 2.0 ** -21, "bfloat16": 2.0 ** -15}
 LEAST = {"float16": 2.0 ** -25, "bfloat16": 2.0 ** -134, "float32": 2.0 ** -150}
 
 
@@ -327,7 +329,7 @@ def layer_case(seed, T, E, k, H, I, dt="bfloat16", *, mx=False, bias=False, edit
     # a logit error d moves a score, and the sum of scores, by a factor of at most 1 + d (+ float32 rounding)
     werr = 3 * logit_error + 1e-5
     assert np.all(np.abs(w - rw)[sure] <= (werr[:, None] * np.abs(rw) + 1e-9)[sure])
-    unit = UNIT["float16" if mx else dt]
+    unit = (H_UNIT if T <= 4 else UNIT)["float16" if mx else dt]
     ref, bound = ox.layer(xv, rw, ridx, werr, v13, v2, unit)
     close(y[torch.from_numpy(sure)], ref[sure], bound[sure], dt)
     return y, ok
@@ -416,7 +418,7 @@ def test_layer_unaligned_views():
     y = moe.moe_few_token_layer(x, wr, w13, w2, k, check_status=True)
     z = moe.moe_few_token_layer(x.clone(), wr.clone(), w13.clone(), w2.clone(), k, check_status=True)
     rw, ridx, sure, le = ox.routing(down(x), down(wr), k)
-    ref, bound = ox.layer(down(x), rw, ridx, 3 * le + 1e-5, down(w13), down(w2), UNIT["bfloat16"])
+    ref, bound = ox.layer(down(x), rw, ridx, 3 * le + 1e-5, down(w13), down(w2), H_UNIT["bfloat16"])
     assert sure.all()
     close(y, ref, bound, "bfloat16")
     close(z, ref, bound, "bfloat16")
@@ -461,7 +463,7 @@ def test_layer_offsets_past_32_bits():
     y = moe.moe_few_token_layer(x, wr, w13, w2, k, bias=bias, norm_type=1, check_status=True)
     rw = np.tile(np.array([3.5, 1.5]) / 5.0, (T, 1))
     ref, bound = ox.layer(down(x), rw, np.tile([0, 1], (T, 1)), np.full(T, 1e-6), down(w13[[E - 1, 1]]),
-                          down(w2[[E - 1, 1]]), UNIT["bfloat16"])
+                          down(w2[[E - 1, 1]]), H_UNIT["bfloat16"])
     close(y, ref, bound, "bfloat16")
 
 
