@@ -8,9 +8,9 @@
  *   h[t, e, i]   = silu(sum_h x[t, h] w13[e, i, h]) * sum_h x[t, h] w13[e, I + i, h]
  *   y[t, n]      = sum over token t's experts of weight * sum_i h[t, e, i] w2[e, n, i]
  *
- * Sums are held in float32.  h is rounded once to 16 bits between the two products: to x's type,
- * scaled by a power of two for each token and expert where that type is float16 (see
- * csrc/moe_layer.cu), and y once to x's type.
+ * Sums are held in float32.  y is rounded once to x's type.  Between the two products weight * h goes
+ * on in 16 bits (x's type, float16 for MXFP4 weights; float16 with a power of two for each 16
+ * elements): as the sum of two such values with up to 4 tokens, rounded once with more.
  *
  * Conventions are those of mrr_v2.h.
  */

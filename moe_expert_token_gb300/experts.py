@@ -5,6 +5,7 @@ integer device addresses) and the torch-level calls on top of it.
 ``moe_mx_quantize`` makes the packed float4_e2m1 rows and e8m0 scales that ``moe_re_routing`` moves;
 ``moe_mx_grouped_matmul`` takes what it returns, with its expert_token_num;
 ``moe_few_token_layer`` runs router, top-k, experts and the weighted sum of a decode step at once.
+A call given a ``stream`` runs and allocates there; its results are that stream's.
 Every step runs in the CUDA library; there is no other code path.
 """
 from __future__ import annotations
@@ -79,9 +80,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _run(function, name, args, dev, stream, workspace=None, check_status=False):
-    """Call ``function(*args, stream)`` with ``dev`` current, on ``stream`` or dev's current stream."""
-    handle = _raw_stream(dev.index) if stream is None else stream.cuda_stream
+def _on(stream, call, *args, **kw):
+    """``call`` with ``stream`` current: what it allocates belongs to that stream too."""
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
+
+
+def _run(function, name, args, dev, workspace=None, check_status=False):
+    """Call ``function(*args, stream)`` on dev's current stream, with ``dev`` current."""
+    handle = _raw_stream(dev.index)
     if dev.index == torch.cuda.current_device():
         st = function(*args, handle)
     else:
@@ -117,6 +124,8 @@ def moe_mx_quantize(x, *, stream=None):
     scales [..., ceil(K/64), 2] uint8): the float4_e2m1 rows and e8m0 scales moe_re_routing takes.
     """
     lib = _lib or _load()
+    if stream is not None:
+        return _on(stream, moe_mx_quantize, x)
     shape = x.shape
     if not x.is_cuda or not shape:
         raise ValueError("x must be a CUDA tensor of at least one dimension")
@@ -134,7 +143,7 @@ def moe_mx_quantize(x, *, stream=None):
     codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
     scales = torch.empty((*lead, (K + 63) // 64, 2), dtype=torch.uint8, device=dev)
     _run(lib.moe_mx_quantize_run, "moe_mx_quantize_run",
-         (x.data_ptr(), code, x.numel() // K, K, stride, codes.data_ptr(), scales.data_ptr()), dev, stream)
+         (x.data_ptr(), code, x.numel() // K, K, stride, codes.data_ptr(), scales.data_ptr()), dev)
     return codes, scales
 
 
@@ -142,6 +151,8 @@ def moe_mx_dequantize(codes, scales, dtype=None, *, stream=None):
     """The values [..., K] of MXFP4 codes [..., K/2] and scales [..., ceil(K/64), 2], in ``dtype``
     (float16, bfloat16, the default, or float32)."""
     lib = _lib or _load()
+    if stream is not None:
+        return _on(stream, moe_mx_dequantize, codes, scales, dtype)
     dtype = torch.bfloat16 if dtype is None else dtype
     code = _CODES.get(dtype)
     if code is None:
@@ -152,7 +163,7 @@ def moe_mx_dequantize(codes, scales, dtype=None, *, stream=None):
     dev = codes.device
     x = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=dev)
     _run(lib.moe_mx_dequantize_run, "moe_mx_dequantize_run",
-         (codes.data_ptr(), scales.data_ptr(), x.numel() // K, K, code, x.data_ptr(), K), dev, stream)
+         (codes.data_ptr(), scales.data_ptr(), x.numel() // K, K, code, x.data_ptr(), K), dev)
     return x
 
 
@@ -172,6 +183,10 @@ def moe_mx_grouped_matmul(tokens, scales, expert_token_num, weight, weight_scale
     ``check_status=True`` synchronises and raises on counts that do not sum to A.
     """
     lib = _lib or _load()
+    if stream is not None:
+        return _on(stream, moe_mx_grouped_matmul, tokens, scales, expert_token_num, weight, weight_scales, gated=gated,
+                   out_dtype=out_dtype, row_weight=row_weight, expert_token_num_type=expert_token_num_type,
+                   workspace=workspace, check_status=check_status)
     K = _check_mx(tokens, scales, "tokens")
     if tokens.dim() != 2 or weight.dim() != 3:
         raise ValueError("tokens must be 2-D and weight 3-D")
@@ -208,7 +223,7 @@ def moe_mx_grouped_matmul(tokens, scales, expert_token_num, weight, weight_scale
     _run(lib.moe_mx_grouped_run, "moe_mx_grouped_run",
          (tokens.data_ptr(), scales.data_ptr(), A, K, c.data_ptr(), int(c.dtype == torch.int64), expert_token_num_type,
           E, weight.data_ptr(), weight_scales.data_ptr(), N, int(gated), _ptr(row_weight), out.data_ptr(), code,
-          _ptr(out_scales), workspace.data_ptr(), workspace.numel()), dev, stream, workspace, check_status)
+          _ptr(out_scales), workspace.data_ptr(), workspace.numel()), dev, workspace, check_status)
     return out if out_scales is None else (out, out_scales)
 
 
@@ -227,6 +242,11 @@ def moe_few_token_layer(x, w_router, w13, w2, k: int, *, bias=None, w13_scales=N
     [T, k] int32).
     """
     lib = _lib or _load()
+    if stream is not None:
+        return _on(stream, moe_few_token_layer, x, w_router, w13, w2, k, bias=bias, w13_scales=w13_scales,
+                   w2_scales=w2_scales, k_group=k_group, group_count=group_count,
+                   routed_scaling_factor=routed_scaling_factor, eps=eps, group_select_mode=group_select_mode,
+                   norm_type=norm_type, return_routing=return_routing, workspace=workspace, check_status=check_status)
     if not x.is_cuda or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D CUDA tensor")
     dtype, dev = x.dtype, x.device
@@ -262,6 +282,5 @@ def moe_few_token_layer(x, w_router, w13, w2, k: int, *, bias=None, w13_scales=N
     _run(lib.moe_few_token_layer_run, "moe_few_token_layer_run",
          (x.data_ptr(), dt, T, H, w_router.data_ptr(), E, _ptr(bias), w13.data_ptr(), _ptr(w13_scales), w2.data_ptr(),
           _ptr(w2_scales), w_dt, I, k, k_group, group_count, routed_scaling_factor, eps, group_select_mode, norm_type,
-          y.data_ptr(), _ptr(weight), _ptr(idx), workspace.data_ptr(), workspace.numel()), dev, stream, workspace,
-         check_status)
+          y.data_ptr(), _ptr(weight), _ptr(idx), workspace.data_ptr(), workspace.numel()), dev, workspace, check_status)
     return (y, weight, idx) if return_routing else y

@@ -363,6 +363,30 @@ def test_layer_edges(E, k, H, I, mx):
     layer_case(E + H + 1, 1, E, k, H, I, "float16", mx=mx, norm_type=1)
 
 
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T,E,k,H,I", [(64, 1024, 64, 64, 32), (8, 1024, 64, 64, 32), (64, 64, 64, 96, 40)])
+def test_layer_most_assignments(T, E, k, H, I, mx):
+    """The largest tables: every size of the routing at its limit, against the oracle on the GPU's routing."""
+    import torch
+
+    rng = np.random.default_rng(T + E)
+    bf = lambda a: torch.from_numpy(a).to(torch.bfloat16).cuda()  # noqa: E731
+    x, wr = bf(rng.standard_normal((T, H))), bf(rng.standard_normal((E, H)) * H ** -0.5)
+    if mx:
+        (w13, s13, v13), (w2, s2, v2) = weights(rng, E, 2 * I, H), weights(rng, E, H, I)
+        w13, s13, w2, s2 = (up(a) for a in (w13, s13, w2, s2))
+    else:
+        w13, w2, s13, s2 = bf(rng.standard_normal((E, 2 * I, H)) * H ** -0.5), bf(rng.standard_normal((E, H, I)) * I ** -0.5), None, None
+        v13, v2 = down(w13), down(w2)
+    y, w, idx = moe.moe_few_token_layer(x, wr, w13, w2, k, w13_scales=s13, w2_scales=s2, norm_type=1,
+                                        return_routing=True, check_status=True)
+    idx, w = idx.cpu().numpy(), down(w)
+    assert idx.min() >= 0 and idx.max() < E and all(len(set(r)) == k for r in idx)
+    assert np.all(np.abs(w.sum(axis=1) - 1) < 1e-5) and np.all(np.diff(w, axis=1) <= 0)
+    ref, bound = ox.layer(down(x), w, idx, np.full(T, 1e-6), v13, v2, UNIT["float16" if mx else "bfloat16"])
+    close(y, ref, bound, "bfloat16")
+
+
 def test_layer_all_tokens_choose_the_same_experts():
     """A bias that decides the choice: one pair of experts takes all 64 tokens."""
     import torch
@@ -530,5 +554,45 @@ def test_given_stream_is_used():
         x.fill_(3.0)
     q, s = moe.moe_mx_quantize(x, stream=side)
     v = moe.moe_mx_dequantize(q, s, stream=side)
+    num = torch.tensor([64], dtype=torch.int32, device="cuda")
+    y = moe.moe_mx_grouped_matmul(q, s, num, q[None], s[None], out_dtype=torch.float32, stream=side, check_status=True)
     side.synchronize()
-    assert bool((v == 3.0).all())
+    assert bool((v == 3.0).all()) and bool((y == 9.0 * 4096).all())
+
+
+# ----------------------------------------------------------------------------- together
+
+def test_example_block_end_to_end():
+    """examples/moe_block.py: prefill (routing, quantisation, re-routing, products, inverse, sum) against
+    the same steps in the oracle, given the GPU's own routing.  Each row's y is rounded to bfloat16 (2^-9
+    of it at most, 2^-10 root mean square) and the sum once more; a float32 difference that moves a code
+    of h is as rare as 2^-20 of them: the whole within 2^-8.  Decode on the same weights differs from it
+    by the activations' quantisation only: two roundings to MXFP4 of about 10 % each, at random."""
+    import importlib.util
+    import os
+
+    import torch
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_block.py")
+    spec = importlib.util.spec_from_file_location("moe_block", path)
+    block = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(block)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    T, E, H, I, k = 256, 8, 256, 128, 4
+    w = block.weights(E, H, I, gen)
+    x = torch.randn(T, H, generator=gen, device="cuda").bfloat16()
+    y = block.prefill(x, w, k, ranks=2)
+
+    weight, expert, _ = moe.moe_gating_top_k(x @ w["router"].t(), k, bias=w["bias"], **block.ROUTING)
+    weight, expert = down(weight), expert.cpu().numpy()
+    xv = ox.mx_values(*ox.mx_quantize(down(x)))
+    v13 = ox.mx_values(w["w13"].cpu().numpy(), w["s13"].cpu().numpy())
+    v2 = ox.mx_values(w["w2"].cpu().numpy(), w["s2"].cpu().numpy())
+    ref = np.zeros((T, H))
+    for e in range(E):
+        t, j = np.nonzero(expert == e)
+        h = ox.mx_values(*ox.mx_quantize(ox.gated(xv[t], v13[e], I)[0]))
+        ref[t] += (h @ v2[e].T) * weight[t, j][:, None]
+    assert np.linalg.norm(down(y) - ref) <= 2.0 ** -8 * np.linalg.norm(ref)
+    z = block.decode(x[:8].contiguous(), w, k)
+    assert np.linalg.norm(down(z) - ref[:8]) <= 0.3 * np.linalg.norm(ref[:8])
