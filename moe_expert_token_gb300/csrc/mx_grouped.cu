@@ -42,6 +42,7 @@ __host__ __device__ constexpr int box_rows(int i) { return i < 2 ? 32 << i : 64 
 constexpr int kMaxStages = 8;
 constexpr int kColumns = 512;            // all of tensor memory
 constexpr int kMaxExperts = 4096;
+constexpr int kTurnPitch = 36;           // floats: 16-byte reads of rows and 4-byte writes of columns, no bank twice
 constexpr int kSingleRows = 32;          // up to so many rows an expert on average: single weight tiles
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -55,9 +56,9 @@ struct Params {
     uint32_t *status;
     int tokens;        // most token rows of a tile (64 or 192)
     int stages, sums;  // ring stages; sets of sums in tensor memory (1 or 2)
-    int align, w_align;    // of scale rows: 16, 8 or 2 bytes
-    int out_wide;          // 16-bit rows can be written 8 bytes, MXFP4 rows 4 bytes at a time
-    int sm_stage, sm_tables, sm_scales;
+    int align, w_align;    // of scale rows: 32, 16, 8 or 2 bytes
+    int out_wide;          // 16-bit and MXFP4 rows can be written so many bytes at a time: 32, 8, or 0 (less)
+    int sm_stage, sm_tables, sm_scales, sm_turn;
 };
 
 struct Maps {
@@ -205,15 +206,19 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const int *tables, int 
 }
 
 // Scale bytes of 32 blocks of row `row` from block b0, four steps' worth: a whole 32-byte sector
-// where rows are aligned to one (8 bytes a step would be fetched four times over).  align: 16, 8 or 2,
-// what rows and base are aligned to.  Blocks at or past `blocks` read 0: their codes are zeros, and a
+// where rows are aligned to one (8 bytes a step would be fetched four times over).  align: 32, 16, 8
+// or 2, what rows and base are aligned to.  Blocks at or past `blocks` read 0: their codes are zeros, and a
 // scale of 2^-127 keeps them so.
 __device__ __forceinline__ void scales32(uint32_t (&v)[8], const uint8_t *s, int64_t row, int64_t row_bytes, int b0,
                                          int blocks, int align)
 {
     const uint8_t *at = s + row * row_bytes + b0;
     const int left = blocks - b0;
-    if (align == 16) {   // b0 is a multiple of 32 and rows of 16 bytes: what is loaded lies inside the row
+    if (align == 32 && left > 0) {   // b0 is a multiple of 32 and rows of 16 or 32 bytes: what is loaded lies inside the row
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "l"(at));
+    } else if (align >= 16) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint4 q = 16 * i < left ? __ldg(reinterpret_cast<const uint4 *>(at) + i) : make_uint4(0, 0, 0, 0);
@@ -268,81 +273,85 @@ __device__ __forceinline__ float swiglu(float g, float u)
     }
 }
 
-// Lanes l and l ^ o swap so that each keeps one of two token rows with both lanes' features: the lane
-// with bit o clear keeps `a` and gets the other's a, the other keeps `b` and gets b.
-__device__ __forceinline__ void trade(uint32_t a, uint32_t b, int o, int lane, uint32_t &mine, uint32_t &theirs)
+// 16 columns of a feature a lane to 16 features of a column for each two lanes, through the warp's
+// 16 x kTurnPitch floats of shared memory
+__device__ __forceinline__ void turn_over(float *turn, int lane, const float (&y)[16], float (&v)[16])
 {
-    const bool high = lane & o;
-    theirs = __shfl_xor_sync(kFull, high ? a : b, o);
-    mine = high ? b : a;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        turn[j * kTurnPitch + lane] = y[j];
+    __syncwarp();
+    const float4 *from = reinterpret_cast<const float4 *>(turn + lane / 2 * kTurnPitch + lane % 2 * 16);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float4 f = from[c];
+        v[4 * c] = f.x, v[4 * c + 1] = f.y, v[4 * c + 2] = f.z, v[4 * c + 3] = f.w;
+    }
+    __syncwarp();
 }
 
 // Results of 16 columns (token rows row .. row + rows - 1) of one output feature a lane: n0 + lane.
-// A warp's row is 32 features: lanes first trade rows for features, so that a store instruction
-// writes 4 rows of 8-byte pieces (16-bit results) or 8 rows of 4-byte pieces (codes).
+// They are turned over first, so that a lane stores 32 bytes of a row (16-bit results) or 8 (codes), and a
+// block's maximum and scale are found by two lanes and not by 32.
 template <int kOut>
-__device__ __forceinline__ void store16(const Params &p, int64_t row, int rows, int n0, int lane, const float (&y)[16])
+__device__ __forceinline__ void store16(const Params &p, int64_t row, int rows, int n0, int lane, float *turn,
+                                        const float (&y)[16])
 {
     const int n = n0 + lane;
     if constexpr (kOut == MOE_MXFP4) {   // 32 lanes are one block; N is a multiple of 32
         if (n0 >= p.N)
             return;
-        uint32_t scale = 0u, v[16];
+        float v[16];
+        turn_over(turn, lane, y, v);
+        uint32_t m = 0u;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const uint32_t s = scale_byte(__reduce_max_sync(kFull, __float_as_uint(y[j]) & 0x7fffffffu));
-            v[j] = __float_as_uint(y[j] * inverse_scale(s));
-            scale = lane == j ? s : scale;
-        }
-        const int64_t srow = scale_row_bytes(p.N);
-        if (lane < rows) {
-            uint8_t *so = p.out_scales + (row + lane) * srow + n0 / 32;
-            so[0] = (uint8_t)scale;
-            if (n0 / 32 % 2 == 0 && n0 + 32 >= p.N)
-                so[1] = 127;
-        }
-        uint32_t b[8], s[4], w[2], mine, theirs;   // 2, 4 and 8 features of one row
+        for (int j = 0; j < 16; ++j)
+            m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+        m = max(m, __shfl_xor_sync(kFull, m, 1));
+        const uint32_t s = scale_byte(m);
+        const float r = inverse_scale(s);
+        float lo[8], hi[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {   // row 2 j + bit 0 of the lane
-            trade(v[2 * j], v[2 * j + 1], 1, lane, mine, theirs);
-            const float a = __uint_as_float(mine), c = __uint_as_float(theirs);
-            b[j] = lane & 1 ? encode2(c, a) : encode2(a, c);
-        }
+        for (int j = 0; j < 8; ++j)
+            lo[j] = v[j] * r, hi[j] = v[8 + j] * r;
+        const uint32_t w[2] = {encode8(lo), encode8(hi)};
+        const int i = lane / 2;
+        if (i < rows) {
+            uint8_t *q = static_cast<uint8_t *>(p.out) + (row + i) * (p.N / 2) + n0 / 2 + lane % 2 * 8;
+            if (p.out_wide) {
+                *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+            } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {   // row 4 j + the lane's low two bits
-            trade(b[2 * j], b[2 * j + 1], 2, lane, mine, theirs);
-            s[j] = lane & 2 ? theirs | mine << 8 : mine | theirs << 8;
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {   // row 8 j + the lane's low three bits
-            trade(s[2 * j], s[2 * j + 1], 4, lane, mine, theirs);
-            w[j] = lane & 4 ? theirs | mine << 16 : mine | theirs << 16;
-            const int i = 8 * j + lane % 8;
-            uint8_t *q = static_cast<uint8_t *>(p.out) + (row + i) * (p.N / 2) + n0 / 2 + lane / 8 * 4;
-            if (i < rows) {
-                if (p.out_wide) {
-                    *reinterpret_cast<uint32_t *>(q) = w[j];
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        q[c] = (uint8_t)(w[j] >> (8 * c));
-                }
+                for (int c = 0; c < 8; ++c)
+                    q[c] = (uint8_t)(w[c / 4] >> (8 * (c % 4)));
+            }
+            if (lane % 2 == 0) {
+                uint8_t *so = p.out_scales + (row + i) * scale_row_bytes(p.N) + n0 / 32;
+                so[0] = (uint8_t)s;
+                if (n0 / 32 % 2 == 0 && n0 + 32 >= p.N)
+                    so[1] = 127;
             }
         }
     } else if (kOut != MOE_F32 && p.out_wide) {   // N is a multiple of 4
-        uint32_t b[8], mine, theirs;
+        float v[16];
+        turn_over(turn, lane, y, v);
+        uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {   // row 2 j + bit 0 of the lane, 2 features
-            trade(__float_as_uint(y[2 * j]), __float_as_uint(y[2 * j + 1]), 1, lane, mine, theirs);
-            const float a = __uint_as_float(mine), c = __uint_as_float(theirs);
-            b[j] = lane & 1 ? pack2<kOut>(c, a) : pack2<kOut>(a, c);
-        }
-        uint16_t *q = static_cast<uint16_t *>(p.out) + (row + lane % 4) * p.N + n0 + lane / 4 * 4;
+        for (int j = 0; j < 8; ++j)
+            w[j] = pack2<kOut>(v[2 * j], v[2 * j + 1]);
+        const int f = n0 + lane % 2 * 16;   // this lane's first feature
+        uint16_t *q = static_cast<uint16_t *>(p.out) + (row + lane / 2) * p.N + f;
+        if (lane / 2 < rows && f < p.N) {
+            if (p.out_wide == 32) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "r"(w[0]), "r"(w[1]),
+                             "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                             : "memory");
+            } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {   // row 4 j + the lane's low two bits, 4 features
-            trade(b[2 * j], b[2 * j + 1], 2, lane, mine, theirs);
-            if (4 * j + lane % 4 < rows && n0 + lane / 4 * 4 < p.N)
-                *reinterpret_cast<uint2 *>(q + 4 * j * (int64_t)p.N) = lane & 2 ? make_uint2(theirs, mine) : make_uint2(mine, theirs);
+                for (int j = 0; j < 4; ++j)
+                    if (f + 4 * j < p.N)
+                        reinterpret_cast<uint2 *>(q)[j] = make_uint2(w[2 * j], w[2 * j + 1]);
+            }
         }
     } else {
         if (n >= p.N)
@@ -605,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kEpilogueWarp) {
         const int quarter = warp % 4, part = (warp - kEpilogueWarp) / 4;   // lanes; every other 16 columns
+        float *turn = reinterpret_cast<float *>(smem + p.sm_turn) + (warp - kEpilogueWarp) * 16 * kTurnPitch;
         int set = 0;
         uint32_t parity = 0u;
         for (long long i = blockIdx.x; i < total; i += gridDim.x) {
@@ -669,9 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float y[16], z[16];
                 results(c, rows, y, z);
                 if (!kMixed || quarter < 2)
-                    store16<kOut>(p, t.row + c, rows, n0, lane, y);
+                    store16<kOut>(p, t.row + c, rows, n0, lane, turn, y);
                 if (!kGated && kTiles == 2)
-                    store16<kOut>(p, t.row + c, rows, n0 + kRowTile, lane, z);
+                    store16<kOut>(p, t.row + c, rows, n0 + kRowTile, lane, turn, z);
             }
             release();
             if (++set == p.sums) {
@@ -760,15 +770,19 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
     p.sums = p.tokens <= 64 ? 2 : 1;
     auto aligned = [K](const void *s) {
         const uint64_t both = (uintptr_t)s | (uint64_t)scale_row_bytes(K);
-        return both % 16 == 0 ? 16 : both % 8 == 0 ? 8 : 2;
+        return both % 32 == 0 ? 32 : both % 16 == 0 ? 16 : both % 8 == 0 ? 8 : 2;
     };
     p.align = aligned(scales);
     p.w_align = aligned(w_scales);
-    p.out_wide = out_dt == MOE_MXFP4 ? (uintptr_t)out % 4 == 0 : (uintptr_t)out % 8 == 0 && N % 4 == 0;
+    if (out_dt == MOE_MXFP4)
+        p.out_wide = (uintptr_t)out % 8 == 0 ? 8 : 0;
+    else
+        p.out_wide = (uintptr_t)out % 32 == 0 && N % 16 == 0 ? 32 : (uintptr_t)out % 8 == 0 && N % 4 == 0 ? 8 : 0;
     p.sm_tables = (int)mrr_ws::round_up(sizeof(Shared), 16);
     p.sm_scales = (int)mrr_ws::round_up(p.sm_tables + 8 * (E + 1), 16);
-    p.sm_stage = (int)mrr_ws::round_up(p.sm_scales + 2 * (tiles * 1024 + 1024 * groups_of(p.tokens)) +
-                                       (gated && tiles == 1 ? 4 * 2048 : 0), 1024);
+    p.sm_turn = p.sm_scales + 2 * (tiles * 1024 + 1024 * groups_of(p.tokens)) + (gated && tiles == 1 ? 4 * 2048 : 0);
+    p.sm_stage = (int)mrr_ws::round_up(
+        p.sm_turn + (out_dt != MOE_F32 ? kEpilogueWarps * 16 * kTurnPitch * 4 : 0), 1024);
     const int columns_left = (kColumns - p.sums * tiles * p.tokens) / (8 * tiles + 8 * groups_of(p.tokens));
     int stages = (info.smem_max - p.sm_stage) / stage_bytes(tiles, p.tokens);
     stages = stages < columns_left ? stages : columns_left;
