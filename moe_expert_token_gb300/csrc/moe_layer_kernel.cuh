@@ -52,10 +52,14 @@ constexpr uint32_t kFull = 0xffffffffu;
 __host__ __device__ constexpr int tiles_for(bool mx, bool many) { return many && !mx ? 4 : 1; }
 // Warps of a block and stages of a warp's ring.  Unpacking 4-bit weights is bound by how many
 // instructions are ready, so MXFP4 has 12 warps (as many as registers allow) with shorter rings; the
-// 16-bit types stream at the memory's rate with 8.
-__host__ __device__ constexpr int warps_of(bool mx) { return mx ? 12 : 8; }
-__host__ __device__ constexpr int stages_of(bool mx) { return mx ? 3 : 4; }
-constexpr int kSlab = 2048;                      // 16 rows x 128 bytes
+// 16-bit types stream at the memory's rate with 8, and rows that tiled copies cannot take (narrow) have
+// longer stages, which leave no room for 12.
+__host__ __device__ constexpr int warps_of(bool mx, bool wide) { return mx && wide ? 12 : 8; }
+__host__ __device__ constexpr int stages_of(bool mx, bool wide) { return mx && wide ? 3 : 4; }
+// Bytes of a stage's row, and of a stage: two slabs of 16 rows.  Narrow rows come as 33 aligned words and
+// are shifted into place when they are read; a row of 36 keeps 16-byte reads off one another's banks.
+__host__ __device__ constexpr int pitch_of(bool wide) { return wide ? 128 : 144; }
+__host__ __device__ constexpr int stage_of(bool wide) { return 2 * 16 * pitch_of(wide); }
 constexpr int kMaxParts = 16;                    // most shares of H the logits are split into
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
@@ -94,7 +98,7 @@ struct Params {
     int sm_scales, sm_bar, sm_red, sm_scratch, sm_weight, sm_act, sm_start, sm_cols, sm_tokens, sm_count;
 };
 
-constexpr int kStageBytes = 2 * kSlab, kStageScales = 256;
+constexpr int kStageScales = 256;
 
 template <int DT>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -116,6 +120,17 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 __device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool ok)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+}
+
+// of 4 bytes
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// the first `bytes` of them are read, the rest zeros
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 // this thread arrives on `bar` once its copies so far have landed
@@ -412,10 +427,10 @@ template <int DT, int WDT, bool kMany, bool kWide>   // kMany: more than 8 token
 struct Layer {
     static constexpr bool kMx = WDT == MOE_MXFP4;
     static constexpr int NT = tiles_for(kMx, kMany);
-    static constexpr int kWarps = warps_of(kMx), kThreads = 32 * kWarps, kStages = stages_of(kMx);
+    static constexpr int kWarps = warps_of(kMx, kWide), kThreads = 32 * kWarps, kStages = stages_of(kMx, kWide);
     static constexpr int MDT = kMx ? MOE_F16 : DT;            // the matrix instructions' type
     static constexpr bool kScaled = MDT == MOE_F16;           // h carries a power of two for each tile
-    static constexpr int kStage = kStageBytes;
+    static constexpr int kPitch = pitch_of(kWide), kSlab = 16 * kPitch, kStage = stage_of(kWide);
     static constexpr int kSlabK = kMx ? 256 : 64;             // elements of K in 128 bytes
     static constexpr int kUpK = kSlabK, kDownK = 2 * kSlabK;  // and in a stage
 
@@ -426,6 +441,8 @@ struct Layer {
     int lane_at;                 // where in a slab they are
     uint32_t bars;               // this warp's barriers, one a stage
     bool dead;                   // a wait has given up: results do not matter any more
+    uint32_t held[2];            // scale bytes on their way through registers, for stage held_slot (-1: none)
+    int held_slot;
     int nact, up_items, up_units, up_tiles, down_items, down_chunks, down_parts;
     const uint16_t *act, *start, *cols;
     const uint8_t *tokens;       // of the columns (kMany)
@@ -439,15 +456,19 @@ struct Layer {
         // The copies' swizzle puts 16-byte piece c of row r at c ^ (r % 8).  16-bit weights: lanes g and
         // g + 1 of a 128-byte read take rows 4 apart, and so the two halves of the banks.
         row = g >> 1 | (g & 1) << 2;
-        lane_at = kMx ? row * 128 + row * 16 + 4 * t : row * 128 + ((t ^ row) << 4);
+        if (kWide)
+            lane_at = kMx ? row * 128 + row * 16 + 4 * t : row * 128 + ((t ^ row) << 4);
+        else
+            lane_at = row * kPitch + t * (kMx ? 4 : 16);
         bars = mrr::smem_addr(sm + p.sm_bar) + warp * kStages * 8;
         dead = false;
+        held_slot = -1;
         act = reinterpret_cast<const uint16_t *>(sm + p.sm_act);
         start = reinterpret_cast<const uint16_t *>(sm + p.sm_start);
         cols = reinterpret_cast<const uint16_t *>(sm + p.sm_cols);
         tokens = sm + p.sm_tokens;
-        if (threadIdx.x < kWarps * kStages)   // the copies' bytes, and (scales) every lane's copy
-            mrr::mbar_init(mrr::smem_addr(sm + p.sm_bar) + threadIdx.x * 8, kMx ? 33 : 1);
+        if (threadIdx.x < kWarps * kStages)   // the tiled copies, or every lane's, and (scales) every lane's
+            mrr::mbar_init(mrr::smem_addr(sm + p.sm_bar) + threadIdx.x * 8, (kWide ? 1 : 32) + (kMx ? 32 : 0));
         mrr::mbar_init_fence();
     }
 
@@ -560,24 +581,10 @@ struct Layer {
         aim(c);
     }
 
-    // bytes b0 .. b0 + n - 1 of a row of `bytes` bytes, loaded one element at a time; past its end 0
-    template <int n>
-    __device__ __forceinline__ void load_narrow(uint32_t (&v)[n / 4], const uint8_t *row, int64_t b0, int64_t bytes) const
-    {
-#pragma unroll
-        for (int i = 0; i < n / 4; ++i)
-            v[i] = 0u;
-        for (int b = 0; b < n; b += kMx ? 1 : 2)
-            if (b0 + b < bytes)
-                v[b / 4] |= (kMx ? (uint32_t)__ldg(row + b0 + b)
-                                 : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row + b0 + b)))
-                            << (8 * (b % 4));
-    }
-
     // start bringing the cursor's unit into stage `slot`: slab 0 holds the gate rows or the chunk's first
     // 128 bytes, slab 1 the up rows or the other 128 bytes
     template <bool kUp>
-    __device__ __forceinline__ void fill(int slot, const Cursor &c) const
+    __device__ __forceinline__ void fill(int slot, const Cursor &c)
     {
         const uint32_t to = mrr::smem_addr(stage(slot)), bar = bars + 8 * slot;
         if (kWide) {
@@ -587,42 +594,101 @@ struct Layer {
                 tc::load_box(to, map, c.chunk * (kUp ? 128 : 256), c.row, bar);
                 tc::load_box(to + kSlab, map, c.chunk * (kUp ? 128 : 256) + (kUp ? 0 : 128), c.row + (kUp ? p.I : 0), bar);
             }
-        } else {   // rows that no 16-byte access fits: element by element, laid out as the copies would
-            const int n = (kUp ? p.I : p.H) - (kUp ? c.row - act[c.expert] * 2 * p.I : c.row - act[c.expert] * p.H);
+        } else {
+            // Rows that no 16-byte access fits: the 33 aligned words that hold 128 bytes of each, a lane a
+            // word, cut off at the row's end; the 33rd words last, a lane a row.  Bound by these copies'
+            // instructions, 33 where a tiled copy takes one: 7 tokens, 60 experts of 2055 x 1399 in float16
+            // 197 us (2056 x 1400: 100); element loads at the time of issue took 655.
             const int K = kUp ? p.H : p.I;
             const int64_t bytes = kMx ? K / 2 : 2 * (int64_t)K;
+            const uint8_t *all = static_cast<const uint8_t *>(kUp ? p.w13 : p.w2);
+            const int n = (kUp ? p.I : p.H) - (kUp ? (c.item - c.expert * up_tiles) * 16 : c.item * 16);
+            auto word = [&](int i, int w) {   // word w of stage row i
+                const int slab = i / 16, r = i % 16;
+                const int64_t begin = (int64_t)c.chunk * (kUp ? 128 : 256) + (kUp ? 0 : slab * 128);
+                const uint8_t *row0 = all + (int64_t)(c.row + r + (kUp ? slab * p.I : 0)) * bytes;
+                const uint8_t *from = reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(row0 + begin) & ~(uintptr_t)3) + 4 * w;
+                const int64_t left = r < n ? row0 + bytes - from : 0;
+                const uint32_t dst = to + i * kPitch + 4 * w;
+                if (from >= all)
+                    copy4(dst, left > 0 ? from : reinterpret_cast<const uint8_t *>(p.status), left < 0 ? 0 : left > 4 ? 4 : (int)left);
+                else {   // the first word of a tensor that does not begin on one
+                    uint32_t v = 0u;
+                    for (int b = 0; b < 4; ++b)
+                        if (from + b >= all && b < left)
+                            v |= (uint32_t)__ldg(from + b) << (8 * b);
+                    *reinterpret_cast<uint32_t *>(stage(slot) + i * kPitch + 4 * w) = v;
+                }
+            };
+            const int64_t first = (int64_t)c.chunk * (kUp ? 128 : 256);
+            const uintptr_t at = reinterpret_cast<uintptr_t>(all + (int64_t)c.row * bytes + first);
+            if ((at & ~(uintptr_t)3) < reinterpret_cast<uintptr_t>(all)) {
 #pragma unroll 1
-            for (int i = lane; i < 256; i += 32) {
-                const int slab = i / 128, r = i / 8 % 16, piece = i % 8;
-                uint32_t v[4] = {0u, 0u, 0u, 0u};
-                if (r < n)
-                    load_narrow<16>(v, static_cast<const uint8_t *>(kUp ? p.w13 : p.w2) + (int64_t)(c.row + r + (kUp ? slab * p.I : 0)) * bytes,
-                                    (int64_t)c.chunk * (kUp ? 128 : 256) + (kUp ? 0 : slab * 128) + piece * 16, bytes);
-                *reinterpret_cast<uint4 *>(stage(slot) + slab * kSlab + r * 128 + ((piece ^ (r & 7)) << 4)) =
-                    make_uint4(v[0], v[1], v[2], v[3]);
+                for (int i = 0; i < 32; ++i)
+                    word(i, lane);
+            } else {
+                const bool whole = n >= 16 && first + (kUp ? 128 : 256) <= bytes;   // nothing to cut off
+#pragma unroll
+                for (int slab = 0; slab < 2; ++slab) {
+                    const uintptr_t at_slab = at + (kUp ? slab * p.I * bytes : slab * 128);
+                    const uint8_t *from = reinterpret_cast<const uint8_t *>(at_slab & ~(uintptr_t)3) + 4 * lane;
+                    const uint32_t dst = to + slab * kSlab + 4 * lane;
+                    uint32_t off = at_slab & 3;
+                    if (whole) {
+#pragma unroll
+                        for (int r = 0; r < 16; ++r, off += (uint32_t)bytes)
+                            copy4(dst + r * kPitch, from + (off & ~3u));
+                    } else {
+                        const int left = (int)(bytes - first) - (kUp ? 0 : slab * 128) - 4 * lane;
+#pragma unroll 4
+                        for (int r = 0; r < 16; ++r, off += (uint32_t)bytes) {
+                            const int some = r < n ? min(max(left + (int)(off & 3u), 0), 4) : 0;
+                            copy4(dst + r * kPitch, some ? from + (off & ~3u) : reinterpret_cast<const uint8_t *>(p.status), some);
+                        }
+                    }
+                }
             }
+            word(lane, 32);
+            copies_arrive(bar);
         }
         if (kMx) {   // 8 scale bytes a lane: [slab][row]
             const int64_t at = (int64_t)c.chunk * (kUp ? 8 : 16), left = scale_row_bytes(kUp ? p.H : p.I) - at - (kUp ? 0 : lane / 16 * 8);
             const bool ok = c.scale_src && left > 0;
-            if (kWide && (kUp ? p.s13_wide : p.s2_wide)) {
+            if (kUp ? p.s13_wide : p.s2_wide) {
                 copy8(mrr::smem_addr(scales(slot)) + lane * 8, ok ? c.scale_src + at : p.w13_s, ok);
                 copies_arrive(bar);
-            } else {
-                uint32_t v[2] = {0u, 0u};
+            } else {   // two bytes at a time, put into the stage at the next issue: they have come by then
+                held[0] = held[1] = 0u;
+                held_slot = slot;
                 if (ok)
-                    for (int b = 0; b < 8; ++b)
+#pragma unroll
+                    for (int b = 0; b < 8; b += 2)
                         if (b < left)
-                            v[b / 4] |= (uint32_t)__ldg(c.scale_src + at + b) << (8 * (b % 4));
-                *reinterpret_cast<uint2 *>(scales(slot) + lane * 8) = make_uint2(v[0], v[1]);
-                if (kWide)
-                    tc::mbar_arrive(bar);
+                            held[b / 4] |= load_pair(c.scale_src + at + b) << (8 * (b % 4));
             }
         }
     }
 
-    __device__ __forceinline__ void issue(Cursor &c, int slot) const
+    // two bytes at any address
+    __device__ __forceinline__ uint32_t load_pair(const uint8_t *p_) const
     {
+        if (reinterpret_cast<uintptr_t>(p_) % 2 == 0)
+            return __ldg(reinterpret_cast<const uint16_t *>(p_));
+        return (uint32_t)__ldg(p_) | (uint32_t)__ldg(p_ + 1) << 8;
+    }
+
+    __device__ __forceinline__ void put_held()
+    {
+        if (kMx && held_slot >= 0) {
+            *reinterpret_cast<uint2 *>(scales(held_slot) + lane * 8) = make_uint2(held[0], held[1]);
+            tc::mbar_arrive(bars + 8 * held_slot);
+            held_slot = -1;
+        }
+    }
+
+    __device__ __forceinline__ void issue(Cursor &c, int slot)
+    {
+        put_held();
         if (c.phase == 0)
             fill<true>(slot, c);
         else if (c.phase == 1)
@@ -634,7 +700,7 @@ struct Layer {
     // the stage's copies have landed
     __device__ __forceinline__ void landed(int slot, uint32_t parity)
     {
-        if (kWide && !dead) {
+        if (!dead) {
             uint64_t t0 = 0;   // the timer is slow to read: not before a wait has become a long one
             for (uint32_t it = 1; !mrr::mbar_try_wait(bars + 8 * slot, parity); ++it)
                 if (it % 1024 == 0) {
@@ -649,6 +715,22 @@ struct Layer {
             dead = __any_sync(kFull, dead);
         }
         __syncwarp();
+    }
+
+    // Narrow rows: by how many bits what this lane reads of the unit's slabs (rows `row` and `row` + 8, and
+    // the same of the up rows) lies past an aligned word.
+    uint32_t shift[2][2];
+
+    __device__ __forceinline__ void place_rows(const void *w, int row0, int K, int second)
+    {
+        if (kWide)
+            return;
+        const uint32_t bytes = kMx ? K / 2 : 2 * K, base = (uint32_t)reinterpret_cast<uintptr_t>(w);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                shift[m][r] = ((base + (uint32_t)(row0 + row + 8 * r + m * second) * bytes) & 3u) * 8u;
     }
 
     // Token operands of one step (a stage, or half of one), kGroups groups of 32 k, for kCols column tiles: this lane's 8 elements
@@ -704,7 +786,7 @@ struct Layer {
                                              const Column (&next)[kCols], int k1, float (&acc)[2][NT][4]) const
     {
         constexpr int kTiles = kUp ? 2 : 1, kBatch = kGroups < 4 ? kGroups : 4;
-        const int stage_at = (warp * kStages + slot) * kStage + lane_at;   // a multiple of 1024, and lane_at
+        const int stage_at = (warp * kStages + slot) * kStage + lane_at;   // kWide: a multiple of 1024, and lane_at
         uint2 sc[2][2];   // 8 scale bytes of rows `row` and `row` + 8
         if constexpr (kMx)
 #pragma unroll
@@ -716,7 +798,8 @@ struct Layer {
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int q = i % kSlabGroups, slab = kUp ? 0 : slab0 + i / kSlabGroups;
-            const uint8_t *from = smem + (stage_at ^ (kMx ? q << 4 : q << 6)) + slab * kSlab;
+            const uint8_t *from = kWide ? smem + (stage_at ^ (kMx ? q << 4 : q << 6)) + slab * kSlab
+                                        : smem + stage_at + (kMx ? q << 4 : q << 6) + slab * kSlab;
             if (!kNext && i % kBatch == 0)
 #pragma unroll
                 for (int j = 0; j < kN; ++j)
@@ -728,12 +811,21 @@ struct Layer {
             for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {   // slab rows `row` and `row` + 8
+                    const uint8_t *piece = from + m * kSlab + r * 8 * kPitch;
                     if constexpr (kMx) {
-                        codes_to_half(*reinterpret_cast<const uint32_t *>(from + m * kSlab + r * 1024), a[m][r]);
+                        uint32_t w = *reinterpret_cast<const uint32_t *>(piece);
+                        if (!kWide)
+                            w = __funnelshift_r(w, *reinterpret_cast<const uint32_t *>(piece + 4), shift[m][r]);
+                        codes_to_half(w, a[m][r]);
                         if (i % 4 == 0)
                             scales_to_float(i < 4 ? sc[m][r].x : sc[m][r].y, s[m][r]);
                     } else {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(from + m * kSlab + r * 1024);
+                        uint4 v = *reinterpret_cast<const uint4 *>(piece);
+                        if (!kWide) {
+                            const uint32_t w = *reinterpret_cast<const uint32_t *>(piece + 16);
+                            v.x = __funnelshift_r(v.x, v.y, shift[m][r]), v.y = __funnelshift_r(v.y, v.z, shift[m][r]);
+                            v.z = __funnelshift_r(v.z, v.w, shift[m][r]), v.w = __funnelshift_r(v.w, w, shift[m][r]);
+                        }
                         a[m][r][0] = v.x, a[m][r][1] = v.y, a[m][r][2] = v.z, a[m][r][3] = v.w;
                     }
                 }
@@ -1138,6 +1230,7 @@ struct Layer {
         };
         // before leaving early: wait for what is in flight
         auto drain = [&]() {
+            put_held();
             for (; filled > 0; --filled) {
                 landed(slot, parity);
                 slot = slot + 1 == kStages ? 0 : slot + 1;
@@ -1161,6 +1254,7 @@ struct Layer {
         }
         for (int item = blockIdx.x; item < up_items; item += gridDim.x) {
             const int ai = item / up_tiles, i0 = (item - ai * up_tiles) * 16, nt = tiles_of(ai);
+            place_rows(p.w13, act[ai] * 2 * p.I + i0, p.H, p.I);
             float acc[2][NT][4] = {};
             for (int u = warp; u < up_units; u += kWarps) {
                 const int at = take();
@@ -1241,6 +1335,7 @@ struct Layer {
                 float acc[2][NT][4] = {};
                 for (bool more = some; more;) {
                     const int at = take(), e = w.expert;
+                    place_rows(p.w2, act[e] * p.H + item * 16, p.I, 0);
                     if (kDownSteps == 2)
                         multiply_all<false>(at, 0, 1, b, c, c1, 0, w.chunk * kDownK + kDownK / 2, acc,
                                             [&](int) { return Column(); });
@@ -1269,10 +1364,10 @@ struct Layer {
                 buf ^= 1;
             }
         } else {
-            constexpr int kPitch = 17;   // [token][16 rows and a pad]
-            float *mine = reinterpret_cast<float *>(smem + p.sm_red) + warp * p.T * kPitch;
+            constexpr int kSumPitch = 17;   // [token][16 rows and a pad]
+            float *mine = reinterpret_cast<float *>(smem + p.sm_red) + warp * p.T * kSumPitch;
             for (int item = blockIdx.x; item < down_items; item += gridDim.x) {
-                for (int i = lane; i < p.T * kPitch; i += 32)
+                for (int i = lane; i < p.T * kSumPitch; i += 32)
                     mine[i] = 0.f;
                 __syncwarp();
                 Cursor w;
@@ -1289,6 +1384,7 @@ struct Layer {
                     load_all<false>(b, c1, w.chunk * kDownK);
                 while (some) {   // one share of an expert's K
                     const int ai = w.expert, tiles = tiles_of(ai);
+                    place_rows(p.w2, act[ai] * p.H + item * 16, p.I, 0);
                     float acc[2][NT][4] = {};
 #pragma unroll
                     for (int j = 0; j < kCols; ++j)
@@ -1315,7 +1411,7 @@ struct Layer {
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
                             if (8 * j + 2 * t + c < count) {
-                                float *to = mine + tokens[first + 8 * j + 2 * t + c] * kPitch + row;
+                                float *to = mine + tokens[first + 8 * j + 2 * t + c] * kSumPitch + row;
                                 to[0] += acc[0][j][c] + acc[1][j][c];
                                 to[8] += acc[0][j][2 + c] + acc[1][j][2 + c];
                             }
@@ -1331,7 +1427,7 @@ struct Layer {
                     float v = 0.f;
 #pragma unroll
                     for (int q = 0; q < kWarps; ++q)
-                        v += all[(q * p.T + tok) * kPitch + r];
+                        v += all[(q * p.T + tok) * kSumPitch + r];
                     store1<DT>(p.y, (int64_t)tok * p.H + n, v * field_value(254u - field_of(tok)));
                 }
                 __syncthreads();
@@ -1343,7 +1439,7 @@ struct Layer {
 };
 
 template <int DT, int WDT, bool kMany, bool kWide>
-__global__ void __launch_bounds__(32 * warps_of(WDT == MOE_MXFP4), 1) layer_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(32 * warps_of(WDT == MOE_MXFP4, kWide), 1) layer_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     Layer<DT, WDT, kMany, kWide>(p, smem).run();
@@ -1359,7 +1455,7 @@ cudaError_t launch_one(const Params &p, const mrr_device::Info &info, int grid, 
     if (err != cudaSuccess)
         return err;
     void *args[] = {const_cast<Params *>(&p)};
-    return cudaLaunchCooperativeKernel(reinterpret_cast<void *>(kernel), dim3(grid), dim3(32 * warps_of(WDT == MOE_MXFP4)), args, smem, s);
+    return cudaLaunchCooperativeKernel(reinterpret_cast<void *>(kernel), dim3(grid), dim3(32 * warps_of(WDT == MOE_MXFP4, wide)), args, smem, s);
 }
 
 template <int DT>

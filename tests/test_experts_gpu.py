@@ -448,6 +448,45 @@ def test_layer_unaligned_views():
     close(z, ref, bound, "bfloat16")
 
 
+@pytest.mark.parametrize("T", [2, 20])
+@pytest.mark.parametrize("H,I", [(334, 202), (648, 130), (1026, 516)])
+@pytest.mark.parametrize("off", [0, 1, 2, 3])
+@pytest.mark.parametrize("mx", [False, True])
+def test_layer_rows_of_any_alignment(T, H, I, off, mx):
+    """Rows that begin at any byte and end inside a word, with NaN right before and behind the experts
+    that are chosen: nothing of a neighbour's row, expert or scales may reach them."""
+    import torch
+
+    rng = np.random.default_rng(H + off)
+    E, k = 6, 2
+    bf = lambda a: torch.from_numpy(a).to(torch.bfloat16)  # noqa: E731
+
+    def view(a, n):   # the tensor, n elements past the start of an allocation
+        flat = torch.zeros(a.numel() + n, dtype=a.dtype, device="cuda")
+        flat[n:] = a.reshape(-1).cuda()
+        return flat[n:].view(a.shape)
+    x, wr = bf(rng.standard_normal((T, H))).cuda(), torch.zeros(E, H, dtype=torch.bfloat16, device="cuda")
+    bias = bf(np.array([0.0, 1.0, 0.0, 0.0, 3.0, 0.0])).cuda()
+    if mx:
+        (w13, s13, v13), (w2, s2, v2) = weights(rng, E, 2 * I, H), weights(rng, E, H, I)
+        for e in (0, 2, 3, 5):
+            s13[e], s2[e] = 255, 255
+        w13, s13, w2, s2 = (view(torch.from_numpy(a), off) for a in (w13, s13, w2, s2))
+    else:
+        w13, w2 = bf(rng.standard_normal((E, 2 * I, H)) * H ** -0.5), bf(rng.standard_normal((E, H, I)) * I ** -0.5)
+        v13, v2 = down(w13), down(w2)
+        for e in (0, 2, 3, 5):
+            w13[e], w2[e] = float("nan"), float("nan")
+        w13, w2, s13, s2 = view(w13, off), view(w2, off), None, None
+    y, w, idx = moe.moe_few_token_layer(x, wr, w13, w2, k, bias=bias, w13_scales=s13, w2_scales=s2, norm_type=1,
+                                        return_routing=True, check_status=True)
+    assert idx.cpu().tolist() == [[4, 1]] * T
+    rw = np.tile(np.array([3.5, 1.5]) / 5.0, (T, 1))
+    ref, bound = ox.layer(down(x), rw, idx.cpu().numpy(), np.full(T, 1e-6), v13, v2,
+                          (H_UNIT if T <= 4 else UNIT)["float16" if mx else "bfloat16"])
+    close(y, ref, bound, "bfloat16")
+
+
 def test_layer_no_tokens_and_refusals():
     import torch
 
