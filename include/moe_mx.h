@@ -38,7 +38,8 @@ typedef enum moe_dtype {
  *   code, magnitudes above 6 to 6.  A block of zeros gets scale byte 0; a block that holds a NaN
  *   or an infinity gets scale byte 255 (its codes are unspecified).
  * Errors: MRR_ERR_DTYPE (dt not F16, BF16, F32), MRR_ERR_SHAPE (rows < 0, K < 2, K odd or above
- * 2^30, more than 2^31 - 1 runs of 512 elements in all, row_stride < K or above 2^31), MRR_ERR_NULL, MRR_ERR_ALIGN (x not aligned to its type), MRR_ERR_CUDA.
+ * 2^30, more than 2^31 - 1 runs of 512 elements in all, row_stride < K or above 2^31),
+ * MRR_ERR_NULL, MRR_ERR_ALIGN (x not aligned to its type), MRR_ERR_CUDA.
  */
 mrr_status moe_mx_quantize_run(const void *x, moe_dtype dt, int64_t rows, int64_t K, int64_t row_stride,
                                uint8_t *codes, uint8_t *scales, mrr_stream_t stream);

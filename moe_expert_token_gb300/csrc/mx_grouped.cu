@@ -8,9 +8,9 @@
 //  * Weights are the 128-row operand and token rows the columns, so an expert with few rows pads
 //    16 columns and not 128 rows, and a lane of the result holds one output feature: 32 lanes are
 //    one 32-block of an MXFP4 result, and a gate and its up value meet in the same lane.
-//  * A tile is two 128-row weight tiles (gated: the gate rows and their up rows; else neighbours)
-//    by up to 192 token rows of one expert, K in steps of 256 (128 bytes a row).  An expert's rows
-//    are split evenly over its tiles, in multiples of 16.
+//  * A tile is two 128-row weight tiles (gated: the gate rows and their up rows; else neighbours), or
+//    one where that fills the blocks more evenly, by up to 192 token rows of one expert, K in steps
+//    of 256 (128 bytes a row).  An expert's rows are split evenly over its tiles, in multiples of 16.
 //  * One persistent block an SM.  Warp 0 issues the tiled bulk copies of codes, warp 1 the matrix
 //    instructions, warps 12-15 bring the scales, warps 4-11 turn finished sums into results while
 //    the next tile's stages are being filled.
@@ -43,7 +43,7 @@ constexpr int kMaxStages = 8;
 constexpr int kColumns = 512;            // all of tensor memory
 constexpr int kMaxExperts = 4096;
 constexpr int kTurnPitch = 36;           // floats: 16-byte reads of rows and 4-byte writes of columns, no bank twice
-constexpr int kSingleRows = 32;          // up to so many rows an expert on average: single weight tiles
+constexpr int kFewRows = 24;             // so many rows an expert, on average, or fewer: weights' bytes are what counts
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct Params {
@@ -761,12 +761,24 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
     p.counts_i64 = expert_num_is_i64, p.counts_prefix = expert_num_type == 0, p.gated = gated, p.out_dt = (int)out_dt;
     p.counts = expert_num, p.row_weight = row_weight, p.out = out, p.out_scales = out_scales;
     p.status = static_cast<uint32_t *>(workspace);
-    // Few rows an expert: narrow tiles, more stages, two sets of sums.  Else as wide as tensor memory
-    // allows beside the scales (2 x 192 columns): a wide tile re-reads its weights less often.
-    p.tokens = A <= 64 * E ? 64 : 192;
-    // Very few: one 128-row weight tile a block instead of two, so that the blocks' shares come out
-    // more even.
-    const int tiles = A <= kSingleRows * E ? 1 : 2;
+    // Tiles of 256 weight rows by up to 192 token rows re-read either operand least, and fill tensor
+    // memory beside the scales.  Tiles of 128 weight rows cost more than half as much each, but there are
+    // twice as many: taken where that fills the last round of blocks so much better that it pays.
+    // rounds() estimates how many tiles a block gets (the counts are on the device): an expert with
+    // rows has one token tile up to 96 rows on average, then half a tile more than its rows fill.
+    //  * Up to 24 rows an expert a tile's time is its weights', half of it for 128 rows.  32 experts of
+    //    7168 x 2048, gated, 512 rows: 83 us (7 rounds) against 86 (4); 16 experts, 385 rows: 51 (4)
+    //    against 45 (2).  Tiles of 64 token rows then leave room for more stages and two sets of sums,
+    //    so that a tile's results are written under the next one: 82.8 us against 85.5 with 192.
+    //  * Above, 128 weight rows cost some two thirds of 256.  8 experts of 7168 x 1024, gated, 1024
+    //    rows: 22 us (1 round) against 25 (1); 3072 rows: 49 (3) against 42 (2).
+    const int mats = gated ? 2 : 1;
+    const bool few = A <= kFewRows * E;
+    const int64_t token_tiles = A <= 96 * E ? (A < E ? A : E) : A / 192 + E / 2;
+    auto rounds = [&](int rows) { return ((N * mats + rows - 1) / rows * token_tiles + info.sms - 1) / info.sms; };
+    const int tiles = few ? (rounds(kRowTile) < 2 * rounds(2 * kRowTile) ? 1 : 2)
+                          : (2 * rounds(kRowTile) < 3 * rounds(2 * kRowTile) ? 1 : 2);
+    p.tokens = few && tiles == 1 ? 64 : 192;
     p.sums = p.tokens <= 64 ? 2 : 1;
     auto aligned = [K](const void *s) {
         const uint64_t both = (uintptr_t)s | (uint64_t)scale_row_bytes(K);

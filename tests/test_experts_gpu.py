@@ -218,6 +218,16 @@ def test_grouped_more_rows(counts, K, N, gate):
     close(got, ref, bound, "bfloat16")
 
 
+@pytest.mark.parametrize("counts", [[10] * 64, [70, 250, 3, 0, 128] * 12, [0] * 200 + [25] * 100], ids=["few", "many", "empty"])
+@pytest.mark.parametrize("K,N", [(96, 512), (544, 480)])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+def test_grouped_more_experts(counts, K, N, gate, dt):
+    """Enough tiles for every block of the GPU, with few rows each and with many."""
+    got, ref, bound = grouped_case(6, counts, K, N, gate=gate, out=dt, weighted=not gate)
+    close(got, ref, bound, dt)
+
+
 @pytest.mark.parametrize("counts,K,N", [([5, 0, 40], 256, 64), ([130, 200], 512, 160), ([1], 64, 32), ([16] * 9, 96, 96)])
 @pytest.mark.parametrize("gate", [False, True])
 def test_grouped_mxfp4_result(counts, K, N, gate):
@@ -230,6 +240,15 @@ def test_grouped_mxfp4_result(counts, K, N, gate):
     if N % 64:
         assert np.all(s.cpu().numpy()[:, -1, 1] == 127)
     assert np.mean(q.cpu().numpy() != rq) < 0.01 and np.mean(s.cpu().numpy() != rs) < 0.01
+    v = ox.mx_values(q.cpu().numpy(), s.cpu().numpy())
+    top = np.abs(ref).reshape(len(ref), -1, 32).max(-1).repeat(32, 1)
+    assert np.all(np.abs(v - ref) <= top / 4 + bound)    # saturation: 8 - 6 of at most 8
+
+
+@pytest.mark.parametrize("counts", [[10] * 64, [70, 250, 3, 0, 128] * 12], ids=["few", "many"])
+@pytest.mark.parametrize("gate", [False, True])
+def test_grouped_mxfp4_result_more_experts(counts, gate):
+    (q, s), ref, bound = grouped_case(12, counts, 160, 512, gate=gate, out="mxfp4")
     v = ox.mx_values(q.cpu().numpy(), s.cpu().numpy())
     top = np.abs(ref).reshape(len(ref), -1, 32).max(-1).repeat(32, 1)
     assert np.all(np.abs(v - ref) <= top / 4 + bound)    # saturation: 8 - 6 of at most 8
