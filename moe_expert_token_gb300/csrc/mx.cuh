@@ -51,18 +51,6 @@ __device__ __forceinline__ uint32_t encode8(const float (&v)[8])
     return r;
 }
 
-__device__ __forceinline__ uint32_t encode2(float lo, float hi)
-{
-    uint32_t r;
-    asm("{\n\t.reg .b8 b0, z;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-        "cvt.u8.u32 z, 0;\n\t"
-        "mov.b32 %0, {b0, z, z, z};\n\t}"
-        : "=r"(r)
-        : "f"(lo), "f"(hi));
-    return r;
-}
-
 // The value of a code (its low four bits): magnitude bits e e m over a bias of 1 are a float's
 // exponent and mantissa head; as a float with those bits the value is 2^-126 times too small
 // (0.5 is then subnormal), which the product puts right exactly.

@@ -2,7 +2,8 @@
 //
 // A block of 32 elements shares the scale 2^X, X = floor(log2 max|x|) - 2, and an element becomes
 // the e2m1 value nearest to x / 2^X.  Both directions read and write each byte once and compute
-// a handful of operations on it, so HBM bounds them.
+// a handful of operations on it, so HBM bounds them: 16384 x 7168 in bfloat16, 297 MB, take 45.1 us
+// (6.6 TB/s) one way and 47.2 us (6.3 TB/s) the other.
 //
 // Layout of the work: a thread owns 8 consecutive elements (one 16-byte load of 16-bit values, one
 // 4-byte store of codes), four neighbouring lanes a block, whose maximum takes two shuffles.
@@ -30,6 +31,39 @@ struct Chunk {
         for (int h = 0; h < (DT == MOE_F32 ? 2 : 1); ++h) {
             const uint4 q = __ldg(p + h);
             w[4 * h] = q.x, w[4 * h + 1] = q.y, w[4 * h + 2] = q.z, w[4 * h + 3] = q.w;
+        }
+    }
+
+    // elements i .. i + n - 1 (n up to 8) from an address aligned to W bytes, zeros for the others
+    template <int W>
+    __device__ __forceinline__ void load(const void *x, int64_t i, int n)
+    {
+        constexpr int kWords = DT == MOE_F32 ? 8 : 4;
+        const uint8_t *p = static_cast<const uint8_t *>(x) + i * (DT == MOE_F32 ? 4 : 2);
+        if (W >= 4 && n == 8) {
+#pragma unroll
+            for (int h = 0; h < kWords; h += W / 4)
+                if constexpr (W == 16) {
+                    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p + 4 * h));
+                    w[h] = q.x, w[h + 1] = q.y, w[h + 2] = q.z, w[h + 3] = q.w;
+                } else if constexpr (W == 8) {
+                    const uint2 q = __ldg(reinterpret_cast<const uint2 *>(p + 4 * h));
+                    w[h] = q.x, w[h + 1] = q.y;
+                } else {
+                    w[h] = __ldg(reinterpret_cast<const uint32_t *>(p + 4 * h));
+                }
+        } else {
+#pragma unroll
+            for (int h = 0; h < kWords; ++h) {
+                w[h] = 0u;
+                if constexpr (DT == MOE_F32) {
+                    if (h < n)
+                        w[h] = __ldg(reinterpret_cast<const uint32_t *>(p) + h);
+                } else if (2 * h < n) {   // n is even
+                    const uint16_t *e = reinterpret_cast<const uint16_t *>(p) + 2 * h;
+                    w[h] = __ldg(e) | (uint32_t)__ldg(e + 1) << 16;
+                }
+            }
         }
     }
 
@@ -63,7 +97,7 @@ struct Chunk {
 
 // Rows without gaps (stride K), K a multiple of 64, x and codes aligned for wide accesses: codes
 // and scales are then flat arrays too.  A thread takes `kQuantizeChunks` chunks of 8, a block's width
-// apart, all loaded before the first is used.
+// apart, all loaded before the first is used (1, 2 or 8 chunks were slower).
 constexpr int kQuantizeChunks = 4;
 
 template <int DT>
@@ -129,87 +163,137 @@ __global__ void __launch_bounds__(kThreads) dequantize_flat(const void *codes, c
     }
 }
 
-// two neighbouring elements, and back; pair: the address is aligned to both
+// Any even K, any stride and alignment (of x's rows to W bytes, of the codes' to `align`): as above, a lane
+// has 8 elements of each chunk, but a warp stays in one row, of which it has run_of() elements, 2 KB.
+// It is bound by instructions more than by HBM, so indices inside a row have 32 bits: 16384 x 7152 in
+// bfloat16 takes 57 us (5.2 TB/s); with 64-bit indices 62, and 1 KB a warp 69.
 template <int DT>
-__device__ __forceinline__ float2 load2(const void *x, int64_t i, bool pair)
-{
-    if (pair && DT == MOE_F32)
-        return __ldg(reinterpret_cast<const float2 *>(static_cast<const float *>(x) + i));
-    if (pair)
-        return unpack2<DT>(__ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(x) + i)));
-    return make_float2(load1<DT>(x, i), load1<DT>(x, i + 1));
-}
+__host__ __device__ constexpr int run_of() { return DT == MOE_F32 ? 512 : 1024; }
 
-template <int DT>
-__device__ __forceinline__ void store2(void *x, int64_t i, float a, float b, bool pair)
+// n / 2 bytes of codes (n elements, 8 or fewer; to load: kMost), at an address aligned to `align` bytes
+__device__ __forceinline__ void store_codes(uint8_t *to, uint32_t w, int n, int align)
 {
-    if (pair && DT == MOE_F32) {
-        *reinterpret_cast<float2 *>(static_cast<float *>(x) + i) = make_float2(a, b);
-    } else if (pair) {
-        *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(x) + i) = pack2<DT>(a, b);
+    if (n == 8 && align == 4) {
+        *reinterpret_cast<uint32_t *>(to) = w;
+    } else if (n == 8 && align == 2) {
+        reinterpret_cast<uint16_t *>(to)[0] = (uint16_t)w;
+        reinterpret_cast<uint16_t *>(to)[1] = (uint16_t)(w >> 16);
     } else {
-        store1<DT>(x, i, a);
-        store1<DT>(x, i + 1, b);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            if (2 * b < n)
+                to[b] = (uint8_t)(w >> (8 * b));
     }
 }
 
-// Any even K, any stride and alignment: a lane has two elements of a block pair (64 elements), a warp
-// kPairs of them in a row, all loaded before the first is used.
-constexpr int kPairs = 8;
+template <int kMost>
+__device__ __forceinline__ uint32_t load_codes(const uint8_t *from, int n, int align)
+{
+    if (n == kMost && align >= kMost / 2)
+        return kMost == 8 ? __ldg(reinterpret_cast<const uint32_t *>(from)) : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(from));
+    if (n == kMost && align == 2)
+        return __ldg(reinterpret_cast<const uint16_t *>(from)) | (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(from) + 1) << 16;
+    uint32_t w = 0u;
+#pragma unroll
+    for (int b = 0; b < kMost / 2; ++b)
+        if (2 * b < n)
+            w |= (uint32_t)__ldg(from + b) << (8 * b);
+    return w;
+}
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) quantize_any(const void *x, int64_t K, int64_t stride, int64_t runs,
-                                                         int64_t units, bool pair, uint8_t *codes, uint8_t *scales)
+template <int DT, int W>
+__global__ void __launch_bounds__(kThreads) quantize_any(const void *x, int K, int64_t stride, uint32_t runs,
+                                                         uint32_t units, int align, uint8_t *codes, uint8_t *scales)
 {
     const int lane = threadIdx.x % 32;
-    const int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32, pairs = (K + 63) / 64;
+    const uint32_t u = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
     if (u >= units)
         return;
-    const int64_t row = u / runs, p0 = (u - row * runs) * kPairs, k0 = p0 * 64 + 2 * lane;
-    float2 v[kPairs];
+    const int64_t row = u / runs;
+    const int first = (int)(u % runs) * run_of<DT>(), blocks = (K + 63) / 64 * 2;
+    constexpr int kChunks = run_of<DT>() / 256;
+    codes += row * (K / 2);
+    scales += row * blocks;
+    Chunk<DT> q[kChunks];
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i)   // K is even: both elements or none
-        v[i] = k0 + 64 * i < K ? load2<DT>(x, row * stride + k0 + 64 * i, pair) : make_float2(0.f, 0.f);
+    for (int i = 0; i < kChunks; ++i) {
+        const int k = first + 256 * i + 8 * lane;
+        q[i].template load<W>(x, row * stride + k, max(0, min(8, K - k)));
+    }
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-        if (p0 + i >= pairs)
-            break;
-        const bool in = k0 + 64 * i < K;
-        uint32_t m = max(__float_as_uint(v[i].x) & 0x7fffffffu, __float_as_uint(v[i].y) & 0x7fffffffu);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-            m = max(m, __shfl_xor_sync(kFull, m, o));
+    for (int i = 0; i < kChunks; ++i) {
+        const int k = first + 256 * i + 8 * lane;
+        uint32_t m = q[i].largest();
+        m = max(m, __shfl_xor_sync(kFull, m, 1));
+        m = max(m, __shfl_xor_sync(kFull, m, 2));
         const uint32_t s = scale_byte(m);
-        const float r = inverse_scale(s);
-        if (in)
-            codes[row * (K / 2) + k0 / 2 + 32 * i] = (uint8_t)encode2(v[i].x * r, v[i].y * r);
-        if (lane % 16 == 0)
-            scales[(row * pairs + p0 + i) * 2 + lane / 16] = (uint8_t)(in ? s : 127u);   // a second block past K: 127
+        float v[8];
+        q[i].scaled(inverse_scale(s), v);
+        const uint32_t w = encode8(v);
+        if (k < K)
+            store_codes(codes + k / 2, w, min(8, K - k), align);
+        if (lane % 4 == 0 && k / kBlock < blocks)   // a second block past K: 127
+            scales[k / kBlock] = (uint8_t)(k < K ? s : 127u);
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) dequantize_any(const uint8_t *codes, const uint8_t *scales, int64_t K,
-                                                           int64_t stride, int64_t runs, int64_t units, bool pair, void *x)
+template <int DT, int W>
+__global__ void __launch_bounds__(kThreads) dequantize_any(const uint8_t *codes, const uint8_t *scales, int K,
+                                                           int64_t stride, uint32_t runs, uint32_t units, int align, void *x)
 {
     const int lane = threadIdx.x % 32;
-    const int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32, pairs = (K + 63) / 64;
+    const uint32_t u = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
     if (u >= units)
         return;
-    const int64_t row = u / runs, p0 = (u - row * runs) * kPairs, k0 = p0 * 64 + 2 * lane;
-    uint32_t q[kPairs], s[kPairs];
+    const int64_t row = u / runs;
+    const int first = (int)(u % runs) * run_of<DT>(), blocks = (K + 63) / 64 * 2;
+    constexpr int kEach = DT == MOE_F32 ? 4 : 8, kChunks = 4;   // 16 bytes of x, as above
+    static_assert(kChunks * 32 * kEach == run_of<DT>(), "");
+    codes += row * (K / 2);
+    scales += row * blocks;
+    uint32_t q[kChunks], s[kChunks];
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i)
-        if (k0 + 64 * i < K) {
-            q[i] = __ldg(codes + row * (K / 2) + k0 / 2 + 32 * i);
-            s[i] = __ldg(scales + (row * pairs + p0 + i) * 2 + lane / 16);
+    for (int i = 0; i < kChunks; ++i) {
+        const int k = first + kEach * (32 * i + lane);
+        if (k < K) {
+            q[i] = load_codes<kEach>(codes + k / 2, min(kEach, K - k), align);
+            s[i] = __ldg(scales + k / kBlock);
         }
+    }
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i)
-        if (k0 + 64 * i < K) {
-            const float f = e8m0_value(s[i]);
-            store2<DT>(x, row * stride + k0 + 64 * i, decode1(q[i]) * f, decode1(q[i] >> 4) * f, pair);
+    for (int i = 0; i < kChunks; ++i) {
+        const int k = first + kEach * (32 * i + lane);
+        if (k >= K)
+            break;
+        const float f = e8m0_value(s[i]);
+        float v[kEach];
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+            v[j] = decode1(q[i] >> (4 * j)) * f;
+        if (W >= 4 && K - k >= kEach) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if constexpr (DT == MOE_F32)
+                    w[j] = __float_as_uint(v[j]);
+                else
+                    w[j] = pack2<DT>(v[2 * j], v[2 * j + 1]);
+            uint8_t *to = static_cast<uint8_t *>(x) + (row * stride + k) * (DT == MOE_F32 ? 4 : 2);
+#pragma unroll
+            for (int j = 0; j < 4; j += W / 4)
+                if constexpr (W == 16)
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                else if constexpr (W == 8)
+                    *reinterpret_cast<uint2 *>(to + 4 * j) = make_uint2(w[j], w[j + 1]);
+                else
+                    *reinterpret_cast<uint32_t *>(to + 4 * j) = w[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < kEach; ++j)
+                if (j < K - k)
+                    store1<DT>(x, row * stride + k + j, v[j]);
         }
+    }
 }
 
 mrr_status check(const void *x, moe_dtype dt, int64_t rows, int64_t K, int64_t stride, const void *codes,
@@ -236,15 +320,18 @@ bool flat(const void *x, int64_t K, int64_t stride, const void *codes)
 
 // the general kernels' launch
 struct Shape {
-    int64_t runs, units;   // runs of kPairs block pairs in a row, and in all rows
+    uint32_t runs, units;   // of `run` elements in a row, and in all rows
     unsigned grid;
-    bool pair;             // two elements can be loaded and stored at once
-    Shape(const void *x, int64_t rows, int64_t K, int64_t stride, int dt)
+    int width, align;      // bytes that x's rows and the codes' rows are aligned to: 16, 8, 4 or 2; 4, 2 or 1
+    Shape(const void *x, int64_t rows, int64_t K, int64_t stride, int size, const void *codes, int run)
     {
-        runs = ((K + 63) / 64 + kPairs - 1) / kPairs;
-        units = rows * runs;
-        grid = (unsigned)((units + kThreads / 32 - 1) / (kThreads / 32));
-        pair = stride % 2 == 0 && (uintptr_t)x % (dt == MOE_F32 ? 8 : 4) == 0;
+        runs = (uint32_t)((K + run - 1) / run);
+        units = (uint32_t)rows * runs;   // check() has seen to it that they are below 2^31
+        grid = (units + kThreads / 32 - 1) / (kThreads / 32);
+        const uint64_t both = (uintptr_t)x | (uint64_t)(stride * size);
+        width = both % 16 == 0 ? 16 : both % 8 == 0 ? 8 : both % 4 == 0 ? 4 : 2;
+        const uint64_t either = (uintptr_t)codes | (uint64_t)(K / 2);
+        align = either % 4 == 0 ? 4 : either % 2 == 0 ? 2 : 1;
     }
 };
 
@@ -258,8 +345,11 @@ void launch_quantize(const void *x, int64_t rows, int64_t K, int64_t stride, uin
             x, chunks, reinterpret_cast<uint32_t *>(codes), scales);
         return;
     }
-    const Shape s(x, rows, K, stride, DT);
-    quantize_any<DT><<<s.grid, kThreads, 0, st>>>(x, K, stride, s.runs, s.units, s.pair, codes, scales);
+    const Shape s(x, rows, K, stride, DT == MOE_F32 ? 4 : 2, codes, run_of<DT>());
+    auto kernel = s.width == 16  ? quantize_any<DT, 16>
+                  : s.width == 8 ? quantize_any<DT, 8>
+                  : s.width == 4 || DT == MOE_F32 ? quantize_any<DT, 4> : quantize_any<DT, DT == MOE_F32 ? 4 : 2>;
+    kernel<<<s.grid, kThreads, 0, st>>>(x, (int)K, stride, s.runs, s.units, s.align, codes, scales);
 }
 
 template <int DT>
@@ -271,8 +361,11 @@ void launch_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows
         dequantize_flat<DT><<<(unsigned)((chunks + per - 1) / per), kThreads, 0, st>>>(codes, scales, chunks, x);
         return;
     }
-    const Shape s(x, rows, K, stride, DT);
-    dequantize_any<DT><<<s.grid, kThreads, 0, st>>>(codes, scales, K, stride, s.runs, s.units, s.pair, x);
+    const Shape s(x, rows, K, stride, DT == MOE_F32 ? 4 : 2, codes, run_of<DT>());
+    auto kernel = s.width == 16  ? dequantize_any<DT, 16>
+                  : s.width == 8 ? dequantize_any<DT, 8>
+                  : s.width == 4 || DT == MOE_F32 ? dequantize_any<DT, 4> : dequantize_any<DT, DT == MOE_F32 ? 4 : 2>;
+    kernel<<<s.grid, kThreads, 0, st>>>(codes, scales, (int)K, stride, s.runs, s.units, s.align, x);
 }
 
 }  // namespace
