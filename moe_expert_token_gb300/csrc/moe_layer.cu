@@ -15,6 +15,7 @@ bool sizes_ok(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
            E <= MRR_GATE_MAX_EXPERTS && k >= 1 && k <= 64 && k <= E;
 }
 
+constexpr int kDenseTokens = 12;  // more tokens an expert than that, on average: 16-bit weights go to kDense
 constexpr int kPairTokens = 4;   // up to so many tokens h is held in two parts
 constexpr int kMaxGrid = 512;    // words of the first grid-wide wait
 
@@ -144,9 +145,10 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
         return MRR_ERR_CUDA;
     p.s13_wide = mx && wide(w13_scales, scale_row_bytes(H), 8);
     p.s2_wide = mx && wide(w2_scales, scale_row_bytes(I), 8);
+    const int regime = T <= 8 ? kFew : !mx && T * k > kDenseTokens * E ? kDense : kSpread;
     // shared memory: the rings (before them, the routing's scratch), the joins, who goes where
     // active experts, counted as often as they are streamed
-    const int64_t n = T * k, active = (n < E ? n : E) + (T > 8 ? n / (8 * tiles_for(mx, true)) : 0);
+    const int64_t n = T * k, active = (n < E ? n : E) + (T > 8 ? n / (8 * tiles_for(mx, regime)) : 0);
     const bool rows_wide = p.w13_wide && p.w2_wide;
     const int warps = warps_of(mx, rows_wide), stages = stages_of(mx, rows_wide);
     int64_t at = (int64_t)warps * stages * stage_of(rows_wide);
@@ -171,7 +173,7 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     p.sm_count = take(16);
     if (at > info.smem_max)
         return MRR_ERR_CUDA;
-    const cudaError_t err = dt == MOE_BF16 ? launch_bf16(p, mx, info, grid, (size_t)at, s) : launch_f16(p, mx, info, grid, (size_t)at, s);
+    const cudaError_t err = dt == MOE_BF16 ? launch_bf16(p, mx, regime, info, grid, (size_t)at, s) : launch_f16(p, mx, regime, info, grid, (size_t)at, s);
     if (err != cudaSuccess) {
         (void)cudaGetLastError();
         return MRR_ERR_CUDA;

@@ -3,9 +3,9 @@
 
 namespace moe_layer {
 
-cudaError_t launch_bf16(const Params &p, bool mx, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s)
+cudaError_t launch_bf16(const Params &p, bool mx, int regime, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s)
 {
-    return launch_dt<MOE_BF16>(p, mx, info, grid, smem, s);
+    return launch_dt<MOE_BF16>(p, mx, regime, info, grid, smem, s);
 }
 
 }  // namespace moe_layer

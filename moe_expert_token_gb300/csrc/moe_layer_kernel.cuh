@@ -23,6 +23,11 @@
 //  * Up product: an item is 16 gate rows and the 16 up rows that belong to them, K split over the
 //    warps, joined in shared memory; SwiGLU and the routing weight are applied there, in float32.
 //  * Down product: an item is 16 output rows for all tokens; the warps split (expert, K) pairs.
+// Measured, with x and the weights from HBM: 1 token, 64 experts of 7168 x 2048 in bfloat16, top 8 (706 MB)
+// 117.5 us, 6.0 TB/s; 48 tokens (5.64 GB) 899 us, 6.3 TB/s; 7 tokens, 60 experts of 2056 x 1400 in float16, top
+// 6 (0.54 GB) 99.5 us, 5.5 TB/s; 4 tokens, 256 MXFP4 experts of 7168 x 2048, top 8 (0.72 GB) 183 us, 3.9 TB/s,
+// bound by the instructions that unpack; 1 token, 8 experts of 1024 x 512 (6 MB) 16 us, bound by the
+// latency of three phases that wait for one another.
 // With up to 8 tokens the columns are the tokens themselves and the down product adds up all
 // experts in registers; with more, an expert's columns are the tokens that chose it, and each
 // warp adds them to its own sums in shared memory.  No sum depends on the order of anything but
@@ -44,15 +49,20 @@ namespace moe_layer {
 using namespace moe_mx;
 
 constexpr uint32_t kFull = 0xffffffffu;
-// Tiles of 8 columns that an expert's weights are multiplied with at a time.  With up to 8 tokens there
-// is one, and its columns are the tokens; with more, the columns are the tokens that chose the expert,
-// in up to 4 tiles, or one for MXFP4, whose unpacking needs the registers.  An expert with more tokens
-// than that is streamed once for each tileful (the second time from L2: both run at about the same
-// time).
-__host__ __device__ constexpr int tiles_for(bool mx, bool many) { return many && !mx ? 4 : 1; }
+// How the columns of the matrix instructions, in tiles of 8, are used.
+//  * kFew, up to 8 tokens: one tile, whose columns are the tokens.
+//  * kSpread: the columns are the tokens that chose the expert, in up to 4 tiles, two of them loaded ahead;
+//    one tile for MXFP4, whose unpacking needs the registers.  An expert with more tokens than that is
+//    streamed once for each tileful (the second time from L2: both run at about the same time).
+//  * kDense, 16-bit weights of experts with many tokens: all 4 tiles are loaded ahead, which takes all
+//    registers.  48 tokens, 16 experts of 7168 x 2048, 24 tokens an expert: 433 -> 333 us; 64 tokens, 64
+//    experts of 2048 x 1408, 6 tokens an expert: 261 -> 277; 12 tokens an expert: no difference.
+//    (For MXFP4, in half as long steps and with 8 warps: 16 tokens an expert 139 -> 162, 24 the same.)
+enum Regime { kFew, kSpread, kDense };
+__host__ __device__ constexpr int tiles_for(bool mx, int regime) { return regime == kFew || mx ? 1 : 4; }
 // Warps of a block and stages of a warp's ring.  Unpacking 4-bit weights is bound by how many
-// instructions are ready, so MXFP4 has 12 warps (as many as registers allow) with shorter rings; the
-// 16-bit types stream at the memory's rate with 8, and rows that tiled copies cannot take (narrow) have
+// instructions are ready, so MXFP4 has 12 warps (as many as registers allow) with shorter rings (4 tokens,
+// 256 experts of 7168 x 2048: 181 us, with 8 warps 202); the 16-bit types stream at the memory's rate with 8, and rows that tiled copies cannot take (narrow) have
 // longer stages, which leave no room for 12.
 __host__ __device__ constexpr int warps_of(bool mx, bool wide) { return mx && wide ? 12 : 8; }
 __host__ __device__ constexpr int stages_of(bool mx, bool wide) { return mx && wide ? 3 : 4; }
@@ -423,10 +433,11 @@ struct Cursor {
     const uint8_t *scale_src;  // this lane's 8 scale bytes of chunk 0; null if there is no such row
 };
 
-template <int DT, int WDT, bool kMany, bool kWide>   // kMany: more than 8 tokens
+template <int DT, int WDT, int kRegime, bool kWide>
 struct Layer {
+    static constexpr bool kMany = kRegime != kFew;            // more than 8 tokens
     static constexpr bool kMx = WDT == MOE_MXFP4;
-    static constexpr int NT = tiles_for(kMx, kMany);
+    static constexpr int NT = tiles_for(kMx, kRegime);
     static constexpr int kWarps = warps_of(kMx, kWide), kThreads = 32 * kWarps, kStages = stages_of(kMx, kWide);
     static constexpr int MDT = kMx ? MOE_F16 : DT;            // the matrix instructions' type
     static constexpr bool kScaled = MDT == MOE_F16;           // h carries a power of two for each tile
@@ -736,7 +747,7 @@ struct Layer {
     // Token operands of one step (a stage, or half of one), kGroups groups of 32 k, for kCols column tiles: this lane's 8 elements
     // of each.  Every register is loaded with the next step's value as soon as it has been used, so
     // that a step's time hides the loads.
-    static constexpr int kCols = NT == 1 ? 1 : 2;
+    static constexpr int kCols = kRegime == kDense || NT == 1 ? NT : 2;
     static constexpr int kSlabGroups = kSlabK / 32, kUpGroups = kUpK / 32;
     // MXFP4's down stages are 16 groups long: worked off a slab at a time, to hold half the operands
     static constexpr int kDownSteps = kMx ? 2 : 1, kDownGroups = kDownK / 32 / kDownSteps;
@@ -871,6 +882,8 @@ struct Layer {
     {
         if (kCols == 1 || nt == 1)
             multiply<kUp, 1, true, kGroups>(slot, slab0, 0, b, now, next, k1, acc);
+        else if (kCols > 2 && nt == 2)
+            multiply<kUp, 2, true, kGroups>(slot, slab0, 0, b, now, next, k1, acc);
         else
             multiply<kUp, kCols, true, kGroups>(slot, slab0, 0, b, now, next, k1, acc);
 #pragma unroll
@@ -1438,35 +1451,40 @@ struct Layer {
     }
 };
 
-template <int DT, int WDT, bool kMany, bool kWide>
-__global__ void __launch_bounds__(32 * warps_of(WDT == MOE_MXFP4, kWide), 1) layer_kernel(const __grid_constant__ Params p)
+template <int DT, int WDT, int kRegime, bool kWide>
+__global__ void __launch_bounds__(32 * warps_of(WDT == MOE_MXFP4, kWide), 1)
+    layer_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    Layer<DT, WDT, kMany, kWide>(p, smem).run();
+    Layer<DT, WDT, kRegime, kWide>(p, smem).run();
 }
 
-template <int DT, int WDT, bool kMany>
+template <int DT, int WDT, int kRegime>
 cudaError_t launch_one(const Params &p, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s)
 {
     static std::atomic<uint64_t> allowed[2];
     const bool wide = p.w13_wide && p.w2_wide;
-    auto kernel = wide ? layer_kernel<DT, WDT, kMany, true> : layer_kernel<DT, WDT, kMany, false>;
+    auto kernel = wide ? layer_kernel<DT, WDT, kRegime, true> : layer_kernel<DT, WDT, kRegime, false>;
     const cudaError_t err = mrr_device::allow_smem(kernel, info, allowed[wide]);
     if (err != cudaSuccess)
         return err;
     void *args[] = {const_cast<Params *>(&p)};
-    return cudaLaunchCooperativeKernel(reinterpret_cast<void *>(kernel), dim3(grid), dim3(32 * warps_of(WDT == MOE_MXFP4, wide)), args, smem, s);
+    return cudaLaunchCooperativeKernel(reinterpret_cast<void *>(kernel), dim3(grid),
+                                       dim3(32 * warps_of(WDT == MOE_MXFP4, wide)), args, smem, s);
 }
 
 template <int DT>
-cudaError_t launch_dt(const Params &p, bool mx, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s)
+cudaError_t launch_dt(const Params &p, bool mx, int regime, const mrr_device::Info &info, int grid, size_t smem,
+                      cudaStream_t s)
 {
-    if (p.T <= 8)
-        return mx ? launch_one<DT, MOE_MXFP4, false>(p, info, grid, smem, s) : launch_one<DT, DT, false>(p, info, grid, smem, s);
-    return mx ? launch_one<DT, MOE_MXFP4, true>(p, info, grid, smem, s) : launch_one<DT, DT, true>(p, info, grid, smem, s);
+    if (regime == kFew)
+        return mx ? launch_one<DT, MOE_MXFP4, kFew>(p, info, grid, smem, s) : launch_one<DT, DT, kFew>(p, info, grid, smem, s);
+    if (regime == kSpread)
+        return mx ? launch_one<DT, MOE_MXFP4, kSpread>(p, info, grid, smem, s) : launch_one<DT, DT, kSpread>(p, info, grid, smem, s);
+    return launch_one<DT, DT, kDense>(p, info, grid, smem, s);
 }
 
-cudaError_t launch_bf16(const Params &p, bool mx, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s);
-cudaError_t launch_f16(const Params &p, bool mx, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s);
+cudaError_t launch_bf16(const Params &p, bool mx, int regime, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s);
+cudaError_t launch_f16(const Params &p, bool mx, int regime, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s);
 
 }  // namespace moe_layer
