@@ -150,7 +150,7 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     // active experts, counted as often as they are streamed
     const int64_t n = T * k, active = (n < E ? n : E) + (T > 8 ? n / (8 * tiles_for(mx, regime)) : 0);
     const bool rows_wide = p.w13_wide && p.w2_wide;
-    const int warps = warps_of(mx, rows_wide), stages = stages_of(mx, rows_wide);
+    const int warps = warps_of(mx, rows_wide, regime), stages = stages_of(mx, rows_wide, regime);
     int64_t at = (int64_t)warps * stages * stage_of(rows_wide);
     const int64_t keys = ((T > 8 ? 1 : T) * 2 * E + E) * 4, places = 2 * (E + n);
     p.sm_scratch = (int)mrr_ws::round_up(2 * n, 16);

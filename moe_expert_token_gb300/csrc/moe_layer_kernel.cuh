@@ -62,12 +62,16 @@ enum Regime { kFew, kSpread, kDense };
 __host__ __device__ constexpr int tiles_for(bool mx, int regime) { return regime == kFew || mx ? 1 : 4; }
 // Warps of a block and stages of a warp's ring.  Unpacking 4-bit weights is bound by how many
 // instructions are ready, so MXFP4 has 12 warps (as many as registers allow) with shorter rings (4 tokens,
-// 256 experts of 7168 x 2048: 181 us, with 8 warps 202); the 16-bit types stream at the memory's rate with 8, and rows that tiled copies cannot take (narrow) have
-// longer stages, which leave no room for 12.
-__host__ __device__ constexpr int warps_of(bool mx, bool wide) { return mx && wide ? 12 : 8; }
-__host__ __device__ constexpr int stages_of(bool mx, bool wide) { return mx && wide ? 3 : 4; }
-// Bytes of a stage's row, and of a stage: two slabs of 16 rows.  Narrow rows come as 33 aligned words and
-// are shifted into place when they are read; a row of 36 keeps 16-byte reads off one another's banks.
+// 256 experts of 7168 x 2048: 181 us, with 8 warps 202); the 16-bit types stream at the memory's rate with 8.
+// Rows that tiled copies cannot take (narrow) cost instructions too, and have 12 where registers and
+// memory allow (7 tokens, 60 experts of 2055 x 1399: 152 us, with 8 warps 177).
+__host__ __device__ constexpr int warps_of(bool mx, bool wide, int regime)
+{
+    return wide ? (mx ? 12 : 8) : regime == kFew ? 12 : 8;
+}
+__host__ __device__ constexpr int stages_of(bool mx, bool wide, int regime) { return warps_of(mx, wide, regime) == 12 ? 3 : 4; }
+// Bytes of a stage's row, and of a stage: two slabs of 16 rows.  Narrow rows come as nine aligned 16-byte
+// pieces and are shifted into place when they are read.
 __host__ __device__ constexpr int pitch_of(bool wide) { return wide ? 128 : 144; }
 __host__ __device__ constexpr int stage_of(bool wide) { return 2 * 16 * pitch_of(wide); }
 constexpr int kMaxParts = 16;                    // most shares of H the logits are split into
@@ -132,15 +136,16 @@ __device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool ok)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
 }
 
-// of 4 bytes
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src)
+// of 16 bytes
+__device__ __forceinline__ void copy16(uint32_t dst, uintptr_t src)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+
 // the first `bytes` of them are read, the rest zeros
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes)
+__device__ __forceinline__ void copy16(uint32_t dst, uintptr_t src, int bytes)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 // this thread arrives on `bar` once its copies so far have landed
@@ -438,7 +443,8 @@ struct Layer {
     static constexpr bool kMany = kRegime != kFew;            // more than 8 tokens
     static constexpr bool kMx = WDT == MOE_MXFP4;
     static constexpr int NT = tiles_for(kMx, kRegime);
-    static constexpr int kWarps = warps_of(kMx, kWide), kThreads = 32 * kWarps, kStages = stages_of(kMx, kWide);
+    static constexpr int kWarps = warps_of(kMx, kWide, kRegime), kThreads = 32 * kWarps;
+    static constexpr int kStages = stages_of(kMx, kWide, kRegime);
     static constexpr int MDT = kMx ? MOE_F16 : DT;            // the matrix instructions' type
     static constexpr bool kScaled = MDT == MOE_F16;           // h carries a power of two for each tile
     static constexpr int kPitch = pitch_of(kWide), kSlab = 16 * kPitch, kStage = stage_of(kWide);
@@ -606,60 +612,58 @@ struct Layer {
                 tc::load_box(to + kSlab, map, c.chunk * (kUp ? 128 : 256) + (kUp ? 0 : 128), c.row + (kUp ? p.I : 0), bar);
             }
         } else {
-            // Rows that no 16-byte access fits: the 33 aligned words that hold 128 bytes of each, a lane a
-            // word, cut off at the row's end; the 33rd words last, a lane a row.  Bound by these copies'
-            // instructions, 33 where a tiled copy takes one: 7 tokens, 60 experts of 2055 x 1399 in float16
-            // 197 us (2056 x 1400: 100); element loads at the time of issue took 655.
+            // Rows that begin at any byte: the nine aligned 16-byte pieces that hold 128 bytes of each, cut off
+            // at the row's end.  Lanes take 8 pieces of 4 rows at a time, the ninth of all 32 rows last.  Bound by
+            // the instructions of copies and shifts: 7 tokens, 60 experts of 2055 x 1399 in float16 take
+            // 152 us (2056 x 1400: 97); by 33 aligned words a row 197, by loads of single elements 655.
             const int K = kUp ? p.H : p.I;
             const int64_t bytes = kMx ? K / 2 : 2 * (int64_t)K;
-            const uint8_t *all = static_cast<const uint8_t *>(kUp ? p.w13 : p.w2);
+            const uintptr_t all = reinterpret_cast<uintptr_t>(kUp ? p.w13 : p.w2);
             const int n = (kUp ? p.I : p.H) - (kUp ? (c.item - c.expert * up_tiles) * 16 : c.item * 16);
-            auto word = [&](int i, int w) {   // word w of stage row i
-                const int slab = i / 16, r = i % 16;
-                const int64_t begin = (int64_t)c.chunk * (kUp ? 128 : 256) + (kUp ? 0 : slab * 128);
-                const uint8_t *row0 = all + (int64_t)(c.row + r + (kUp ? slab * p.I : 0)) * bytes;
-                const uint8_t *from = reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(row0 + begin) & ~(uintptr_t)3) + 4 * w;
-                const int64_t left = r < n ? row0 + bytes - from : 0;
-                const uint32_t dst = to + i * kPitch + 4 * w;
-                if (from >= all)
-                    copy4(dst, left > 0 ? from : reinterpret_cast<const uint8_t *>(p.status), left < 0 ? 0 : left > 4 ? 4 : (int)left);
-                else {   // the first word of a tensor that does not begin on one
+            const int64_t first = (int64_t)c.chunk * (kUp ? 128 : 256);
+            const uintptr_t at = all + (int64_t)c.row * bytes + first;   // slab 0's first row
+            const uintptr_t at1 = at + (kUp ? p.I * bytes : 128);        // slab 1's
+            if ((at & ~(uintptr_t)15) < all) {
+                // the tensor's first piece holds bytes that are not the tensor's: byte by byte
+#pragma unroll 1
+                for (int i = lane; i < 32 * kPitch / 4; i += 32) {
+                    const int r = i / (kPitch / 4) % 16;
+                    const uintptr_t row_at = (i / (kPitch / 4) < 16 ? at : at1) + r * bytes;
+                    const uintptr_t from = (row_at & ~(uintptr_t)15) + i % (kPitch / 4) * 4;
+                    const uintptr_t end = row_at - first - (!kUp && i / (kPitch / 4) >= 16 ? 128 : 0) + bytes;
                     uint32_t v = 0u;
                     for (int b = 0; b < 4; ++b)
-                        if (from + b >= all && b < left)
-                            v |= (uint32_t)__ldg(from + b) << (8 * b);
-                    *reinterpret_cast<uint32_t *>(stage(slot) + i * kPitch + 4 * w) = v;
+                        if (r < n && from + b >= all && from + b < end)
+                            v |= (uint32_t)__ldg(reinterpret_cast<const uint8_t *>(from + b)) << (8 * b);
+                    reinterpret_cast<uint32_t *>(stage(slot))[i] = v;
                 }
-            };
-            const int64_t first = (int64_t)c.chunk * (kUp ? 128 : 256);
-            const uintptr_t at = reinterpret_cast<uintptr_t>(all + (int64_t)c.row * bytes + first);
-            if ((at & ~(uintptr_t)3) < reinterpret_cast<uintptr_t>(all)) {
-#pragma unroll 1
-                for (int i = 0; i < 32; ++i)
-                    word(i, lane);
             } else {
                 const bool whole = n >= 16 && first + (kUp ? 128 : 256) <= bytes;   // nothing to cut off
 #pragma unroll
                 for (int slab = 0; slab < 2; ++slab) {
-                    const uintptr_t at_slab = at + (kUp ? slab * p.I * bytes : slab * 128);
-                    const uint8_t *from = reinterpret_cast<const uint8_t *>(at_slab & ~(uintptr_t)3) + 4 * lane;
-                    const uint32_t dst = to + slab * kSlab + 4 * lane;
-                    uint32_t off = at_slab & 3;
+                    const uintptr_t slab_at = (slab ? at1 : at) & ~(uintptr_t)15;
+                    uint32_t off = (uint32_t)((slab ? at1 : at) & 15) + lane / 8 * (uint32_t)bytes;   // of the lane's row
+                    const uint32_t dst = to + slab * kSlab + lane / 8 * kPitch + lane % 8 * 16;
+                    const uintptr_t from = slab_at + lane % 8 * 16;
                     if (whole) {
 #pragma unroll
-                        for (int r = 0; r < 16; ++r, off += (uint32_t)bytes)
-                            copy4(dst + r * kPitch, from + (off & ~3u));
+                        for (int r = 0; r < 16; r += 4, off += 4 * (uint32_t)bytes)
+                            copy16(dst + r * kPitch, from + (off & ~15u));
                     } else {
-                        const int left = (int)(bytes - first) - (kUp ? 0 : slab * 128) - 4 * lane;
-#pragma unroll 4
-                        for (int r = 0; r < 16; ++r, off += (uint32_t)bytes) {
-                            const int some = r < n ? min(max(left + (int)(off & 3u), 0), 4) : 0;
-                            copy4(dst + r * kPitch, some ? from + (off & ~3u) : reinterpret_cast<const uint8_t *>(p.status), some);
+                        const int left = (int)(bytes - first) - (!kUp && slab ? 128 : 0) - lane % 8 * 16;
+#pragma unroll
+                        for (int r = 0; r < 16; r += 4, off += 4 * (uint32_t)bytes) {
+                            const int some = r + lane / 8 < n ? min(max(left + (int)(off & 15u), 0), 16) : 0;
+                            copy16(dst + r * kPitch, some ? from + (off & ~15u) : reinterpret_cast<uintptr_t>(p.status), some);
                         }
                     }
                 }
+                const int r = lane % 16;
+                const uintptr_t row_at = (lane < 16 ? at : at1) + r * bytes, from = (row_at & ~(uintptr_t)15) + 128;
+                const int64_t left = (int64_t)(row_at - from) - first - (!kUp && lane >= 16 ? 128 : 0) + bytes;
+                const int some = r < n ? (int)max((int64_t)0, min((int64_t)16, left)) : 0;
+                copy16(to + lane * kPitch + 128, some ? from : reinterpret_cast<uintptr_t>(p.status), some);
             }
-            word(lane, 32);
             copies_arrive(bar);
         }
         if (kMx) {   // 8 scale bytes a lane: [slab][row]
@@ -728,8 +732,8 @@ struct Layer {
         __syncwarp();
     }
 
-    // Narrow rows: by how many bits what this lane reads of the unit's slabs (rows `row` and `row` + 8, and
-    // the same of the up rows) lies past an aligned word.
+    // Narrow rows: by how many bytes what this lane reads of the unit's slabs (rows `row` and `row` + 8, and
+    // the same of the up rows) lies past an aligned piece.
     uint32_t shift[2][2];
 
     __device__ __forceinline__ void place_rows(const void *w, int row0, int K, int second)
@@ -741,7 +745,23 @@ struct Layer {
         for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-                shift[m][r] = ((base + (uint32_t)(row0 + row + 8 * r + m * second) * bytes) & 3u) * 8u;
+                shift[m][r] = (base + (uint32_t)(row0 + row + 8 * r + m * second) * bytes) & 15u;
+    }
+
+    // the 16 bytes from byte d of two pieces
+    __device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, uint32_t d) const
+    {
+        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        uint32_t x[6], y[5];
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            x[i] = d & 8u ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+            y[i] = d & 4u ? x[i + 1] : x[i];
+        const uint32_t bits = d % 4u * 8u;
+        return make_uint4(__funnelshift_r(y[0], y[1], bits), __funnelshift_r(y[1], y[2], bits),
+                          __funnelshift_r(y[2], y[3], bits), __funnelshift_r(y[3], y[4], bits));
     }
 
     // Token operands of one step (a stage, or half of one), kGroups groups of 32 k, for kCols column tiles: this lane's 8 elements
@@ -824,19 +844,20 @@ struct Layer {
                 for (int r = 0; r < 2; ++r) {   // slab rows `row` and `row` + 8
                     const uint8_t *piece = from + m * kSlab + r * 8 * kPitch;
                     if constexpr (kMx) {
-                        uint32_t w = *reinterpret_cast<const uint32_t *>(piece);
-                        if (!kWide)
-                            w = __funnelshift_r(w, *reinterpret_cast<const uint32_t *>(piece + 4), shift[m][r]);
+                        uint32_t w;
+                        if (kWide) {
+                            w = *reinterpret_cast<const uint32_t *>(piece);
+                        } else {
+                            const uint32_t *words = reinterpret_cast<const uint32_t *>(piece + (shift[m][r] & 12u));
+                            w = __funnelshift_r(words[0], words[1], shift[m][r] % 4u * 8u);
+                        }
                         codes_to_half(w, a[m][r]);
                         if (i % 4 == 0)
                             scales_to_float(i < 4 ? sc[m][r].x : sc[m][r].y, s[m][r]);
                     } else {
                         uint4 v = *reinterpret_cast<const uint4 *>(piece);
-                        if (!kWide) {
-                            const uint32_t w = *reinterpret_cast<const uint32_t *>(piece + 16);
-                            v.x = __funnelshift_r(v.x, v.y, shift[m][r]), v.y = __funnelshift_r(v.y, v.z, shift[m][r]);
-                            v.z = __funnelshift_r(v.z, v.w, shift[m][r]), v.w = __funnelshift_r(v.w, w, shift[m][r]);
-                        }
+                        if (!kWide)
+                            v = shifted(v, *reinterpret_cast<const uint4 *>(piece + 16), shift[m][r]);
                         a[m][r][0] = v.x, a[m][r][1] = v.y, a[m][r][2] = v.z, a[m][r][3] = v.w;
                     }
                 }
@@ -1452,7 +1473,7 @@ struct Layer {
 };
 
 template <int DT, int WDT, int kRegime, bool kWide>
-__global__ void __launch_bounds__(32 * warps_of(WDT == MOE_MXFP4, kWide), 1)
+__global__ void __launch_bounds__(32 * warps_of(WDT == MOE_MXFP4, kWide, kRegime), 1)
     layer_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -1470,7 +1491,7 @@ cudaError_t launch_one(const Params &p, const mrr_device::Info &info, int grid, 
         return err;
     void *args[] = {const_cast<Params *>(&p)};
     return cudaLaunchCooperativeKernel(reinterpret_cast<void *>(kernel), dim3(grid),
-                                       dim3(32 * warps_of(WDT == MOE_MXFP4, wide)), args, smem, s);
+                                       dim3(32 * warps_of(WDT == MOE_MXFP4, wide, kRegime)), args, smem, s);
 }
 
 template <int DT>

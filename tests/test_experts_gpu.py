@@ -406,6 +406,12 @@ def test_layer_most_assignments(T, E, k, H, I, mx):
     close(y, ref, bound, "bfloat16")
 
 
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T,E,k,H,I", [(64, 1024, 64, 70, 38), (8, 1024, 64, 70, 38), (64, 64, 64, 102, 42)])
+def test_layer_most_assignments_of_narrow_rows(T, E, k, H, I, mx):
+    test_layer_most_assignments(T, E, k, H, I, mx)
+
+
 def test_layer_all_tokens_choose_the_same_experts():
     """A bias that decides the choice: one pair of experts takes all 64 tokens."""
     import torch
