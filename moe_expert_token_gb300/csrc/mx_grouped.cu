@@ -774,7 +774,7 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
     //    against 45 (2).  Tiles of 64 token rows then leave room for more stages and two sets of sums,
     //    so that a tile's results are written under the next one: 82.8 us against 85.5 with 192.
     //  * Above, 128 weight rows cost some two thirds of 256.  8 experts of 7168 x 1024, gated, 1024
-    //    rows: 22 us (1 round) against 25 (1); 3072 rows: 49 (3) against 42 (2).
+    //    rows: 22 us (1 round) against 25 (1); 1536 rows: 35 (2) against 27 (1).
     const int mats = gated ? 2 : 1;
     const bool few = A <= kFewRows * E;
     const int64_t token_tiles = A <= 96 * E ? (A < E ? A : E) : A / 192 + E / 2;
