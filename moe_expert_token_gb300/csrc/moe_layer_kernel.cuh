@@ -21,7 +21,8 @@
 //  * The grid waits twice: for the logits, and for h.  Between them every block computes the
 //    routing of all tokens for itself, which costs less than a third wait.
 //  * Up product: an item is 16 gate rows and the 16 up rows that belong to them, K split over the
-//    warps, joined in shared memory; SwiGLU and the routing weight are applied there, in float32.
+//    warps, joined in shared memory, or all of K by one warp; SwiGLU and the routing weight are
+//    applied to the sums, in float32.
 //  * Down product: an item is 16 output rows for all tokens; the warps split (expert, K) pairs.
 // Measured, with x and the weights from HBM: 1 token, 64 experts of 7168 x 2048 in bfloat16, top 8 (706 MB)
 // 117.5 us, 6.0 TB/s; 48 tokens (5.64 GB) 899 us, 6.3 TB/s; 7 tokens, 60 experts of 2056 x 1400 in float16, top
@@ -461,6 +462,8 @@ struct Layer {
     uint32_t held[2];            // scale bytes on their way through registers, for stage held_slot (-1: none)
     int held_slot;
     int nact, up_items, up_units, up_tiles, down_items, down_chunks, down_parts;
+    bool solo;                   // up items are single warps', not the block's
+    int up_first, up_stride, up_begin, up_step;   // this warp's items, and its units of one
     const uint16_t *act, *start, *cols;
     const uint8_t *tokens;       // of the columns (kMany)
 
@@ -501,6 +504,20 @@ struct Layer {
         up_tiles = (p.I + 15) / 16;
         up_items = nact * up_tiles;
         up_units = (p.H + kUpK - 1) / kUpK;
+        // An up item is worked off by the block, its warps splitting K and joining their sums, or by one warp,
+        // which needs no join.  Which takes less, in units of a stage's time: the block's share of K and
+        // about one for each join, times its items; or all of K, a fifth more for the more scattered
+        // reads of the weights, times the warp's items.  48 tokens, 64 experts of 7168 x 2048 in bfloat16:
+        // the block 898 us, warps 970; 39 tokens, 248 experts of 556 x 1439 in float16: 675 and 508; 32
+        // tokens, 64 MXFP4 experts of 7168 x 2048: 412 and 370; 2 tokens, 18 experts of 5015 x 196: 47 and 88.
+        const int blocks = gridDim.x, joins = !kMany ? 1 : min(NT, (p.T * p.k + 8 * nact - 1) / (8 * nact));
+        const int joint = (up_items + blocks - 1) / blocks * ((up_units + kWarps - 1) / kWarps + joins);
+        const int alone = (up_items + kWarps * blocks - 1) / (kWarps * blocks) * up_units;
+        solo = 5 * (int64_t)joint > 6 * (int64_t)alone;
+        up_first = blockIdx.x + (solo ? warp * blocks : 0);
+        up_stride = solo ? kWarps * blocks : blocks;
+        up_begin = solo ? 0 : warp;
+        up_step = solo ? 1 : kWarps;
         down_items = (p.H + 15) / 16;
         down_chunks = (p.I + kDownK - 1) / kDownK;
         // an expert's K is cut into shares, taken by the warps in turn: single chunks, or (where a
@@ -557,9 +574,9 @@ struct Layer {
     {
         Cursor c;
         c.phase = 0;
-        c.item = blockIdx.x;
-        c.chunk = warp;
-        if (c.item >= up_items || warp >= up_units)
+        c.item = up_first;
+        c.chunk = up_begin;
+        if (c.item >= up_items || up_begin >= up_units)
             first_down(c);
         else
             c.expert = c.item / up_tiles;
@@ -576,11 +593,11 @@ struct Layer {
     __device__ __forceinline__ void advance(Cursor &c) const
     {
         if (c.phase == 0) {
-            c.chunk += kWarps;
+            c.chunk += up_step;
             if (c.chunk < up_units)
                 return;
-            c.chunk = warp;
-            c.item += gridDim.x;
+            c.chunk = up_begin;
+            c.item += up_stride;
             if (c.item >= up_items)
                 first_down(c);
             else
@@ -988,6 +1005,44 @@ struct Layer {
         return v;
     }
 
+    // h of column c of active expert ai, rows i0 + row and i0 + row + 8, from their gate and up sums: the
+    // eight lanes that share t hold a column's 16 rows
+    __device__ __forceinline__ void finish(const float *weight, int ai, int i0, int c, float g0, float g1, float u0, float u1) const
+    {
+        const int a = column_of(ai, c);
+        float h[2] = {0.f, 0.f};
+        int tok = 0;
+        if (a >= 0) {
+            tok = token_of(ai, c);
+            const float s = kMx ? p.x_scale[tok] : 1.f, w = !kMany ? weight[a] : __ldcg(p.route_weight + a);
+            const float gate[2] = {g0 * s, g1 * s}, upv[2] = {u0 * s, u1 * s};
+#pragma unroll
+            for (int b = 0; b < 2; ++b)   // rows past I: what the copy brought there is another row's
+                h[b] = i0 + row + 8 * b < p.I ? gate[b] / (1.f + expf(-gate[b])) * upv[b] * w : 0.f;
+        }
+        if (kScaled) {
+            uint32_t m = max(__float_as_uint(h[0]) & 0x7fffffffu, __float_as_uint(h[1]) & 0x7fffffffu);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1)
+                m = max(m, __shfl_xor_sync(kFull, m, o));
+            const uint32_t field = f16_scale_field(m);
+            h[0] *= field_value(field), h[1] *= field_value(field);
+            if (a >= 0 && g == 0) {
+                p.h_field[(int64_t)a * (p.Ip / 16) + i0 / 16] = (uint8_t)field;
+                atomicMax(p.h_max + tok, m);
+            }
+        }
+        if (a >= 0) {
+            const int64_t to = (int64_t)a * p.Ip + i0 + row;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                store1<MDT>(p.h, to + 8 * b, h[b]);
+                if (!kMany && p.pairs)
+                    store1<MDT>(p.h, p.h_plane + to + 8 * b, h[b] - value_of<MDT>(h[b]));
+            }
+        }
+    }
+
     // ------------------------------------------------------------ before the first wait
 
     // x's row t as the products take it: 16-bit, zeros past H, scaled (kMx); and the ends of its h rows
@@ -1282,23 +1337,32 @@ struct Layer {
         };
         Column col[kCols], next_col[kCols];
         Tokens<kUpGroups> ahead;   // the next unit's operands
-        if ((int)blockIdx.x < up_items && warp < up_units) {
-            x_columns(next_col, blockIdx.x / up_tiles);
-            load_all<true>(ahead, next_col, warp * kUpK);
+        if (up_first < up_items && up_begin < up_units) {
+            x_columns(next_col, up_first / up_tiles);
+            load_all<true>(ahead, next_col, up_begin * kUpK);
         }
-        for (int item = blockIdx.x; item < up_items; item += gridDim.x) {
+        for (int item = up_first; item < up_items; item += up_stride) {
             const int ai = item / up_tiles, i0 = (item - ai * up_tiles) * 16, nt = tiles_of(ai);
             place_rows(p.w13, act[ai] * 2 * p.I + i0, p.H, p.I);
             float acc[2][NT][4] = {};
-            for (int u = warp; u < up_units; u += kWarps) {
+            for (int u = up_begin; u < up_units; u += up_step) {
                 const int at = take();
-                int k1 = (u + kWarps) * kUpK;
-                if (u + kWarps >= up_units) {   // then comes the next item's first unit
-                    k1 = warp * kUpK;
-                    if (item + (int)gridDim.x < up_items)
-                        x_columns(next_col, (item + gridDim.x) / up_tiles);
+                int k1 = (u + up_step) * kUpK;
+                if (u + up_step >= up_units) {   // then comes the next item's first unit
+                    k1 = up_begin * kUpK;
+                    if (item + up_stride < up_items)
+                        x_columns(next_col, (item + up_stride) / up_tiles);
                 }
                 multiply_all<true>(at, 0, nt, ahead, col, next_col, u * kUpK, k1, acc, [&](int j) { return x_column(ai, j); });
+            }
+            if (solo) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    if (j < nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            finish(weight, ai, i0, 8 * j + 2 * t + c, acc[0][j][c], acc[0][j][2 + c], acc[1][j][c], acc[1][j][2 + c]);
+                continue;
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
