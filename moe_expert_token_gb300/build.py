@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("gating_f16.cu", "gating_bf16.cu", "gating_f32.cu", "mrr_v2.cu",
                                             "mrr_v2_noalloc.cu", "mrr_push.cu", "gating.cu", "mx_quantize.cu", "mx_grouped.cu",
-                                            "moe_layer.cu", "moe_layer_bf16.cu", "moe_layer_f16.cu")]
+                                            "moe_layer.cu", "moe_layer_bf16.cu", "moe_layer_f16.cu",
+                                            "moe_layer_bf16_split.cu", "moe_layer_f16_split.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "gating_kernel.cuh"),
                   os.path.join(CSRC, "ws_layout.h"), os.path.join(CSRC, "mrr_shape.h"),
                   os.path.join(CSRC, "mx.cuh"), os.path.join(CSRC, "tc.cuh"),

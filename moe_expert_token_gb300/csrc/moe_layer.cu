@@ -20,7 +20,7 @@ constexpr int kPairTokens = 4;   // up to so many tokens h is held in two parts
 constexpr int kMaxGrid = 512;    // words of the first grid-wide wait
 
 struct Layout {
-    size_t waits, part, xh, route_expert, route_weight, x_scale, h_max, h, h_field, bytes;
+    size_t waits, part, xh, route_expert, route_weight, x_scale, h_max, h, h_field, split, split_count, bytes;
     int Hp, Ip;
 };
 
@@ -44,6 +44,9 @@ Layout layout(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
     l.h_max = take(T * 4);
     l.h = take((T <= kPairTokens ? 2 : 1) * T * k * l.Ip * 2);
     l.h_field = take(T * k * (l.Ip / 16));
+    const int64_t items = (H + 15) / 16, shares = items > kMaxGrid / 2 ? 0 : items * kMaxSplits < kMaxGrid ? items * kMaxSplits : kMaxGrid;
+    l.split = take(shares * T * 16 * 4);
+    l.split_count = take(shares ? items * 4 : 0);
     l.bytes = at;
     return l;
 }
@@ -128,6 +131,8 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     p.h_plane = T * k * l.Ip;
     p.pairs = T <= kPairTokens;
     p.h_field = ws + l.h_field;
+    p.split = reinterpret_cast<float *>(ws + l.split);
+    p.split_count = reinterpret_cast<unsigned *>(ws + l.split_count);
     p.Hp = l.Hp, p.Ip = l.Ip;
     // the router's 16-expert tiles, split over H until the blocks have one each
     const int64_t tiles = (E + 15) / 16, chunks = (H + 127) / 128;
@@ -173,7 +178,11 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     p.sm_count = take(16);
     if (at > info.smem_max)
         return MRR_ERR_CUDA;
-    const cudaError_t err = dt == MOE_BF16 ? launch_bf16(p, mx, regime, info, grid, (size_t)at, s) : launch_f16(p, mx, regime, info, grid, (size_t)at, s);
+    // y's rows in items of 16: blocks share them where there are two blocks or more to each, and work for them
+    const int64_t down_items = (H + 15) / 16, down_chunks = (I + (mx ? 511 : 127)) / (mx ? 512 : 128);
+    const bool split = 2 * down_items <= grid && active * down_chunks >= 4 * warps;
+    Launch *launch = dt == MOE_BF16 ? (split ? launch_bf16_split : launch_bf16) : (split ? launch_f16_split : launch_f16);
+    const cudaError_t err = launch(p, mx, regime, info, grid, (size_t)at, s);
     if (err != cudaSuccess) {
         (void)cudaGetLastError();
         return MRR_ERR_CUDA;

@@ -1,0 +1,12 @@
+// Instances of the layer's kernel for x in f16, whose blocks share the down items (each type's and form's compile beside the others').
+#include "moe_layer_kernel.cuh"
+
+namespace moe_layer {
+
+cudaError_t launch_f16_split(const Params &p, bool mx, int regime, const mrr_device::Info &info, int grid, size_t smem,
+                       cudaStream_t s)
+{
+    return launch_dt<MOE_F16, true>(p, mx, regime, info, grid, smem, s);
+}
+
+}  // namespace moe_layer

@@ -23,7 +23,8 @@
 //  * Up product: an item is 16 gate rows and the 16 up rows that belong to them, K split over the
 //    warps, joined in shared memory, or all of K by one warp; SwiGLU and the routing weight are
 //    applied to the sums, in float32.
-//  * Down product: an item is 16 output rows for all tokens; the warps split (expert, K) pairs.
+//  * Down product: an item is 16 output rows for all tokens; the warps split (expert, K) pairs, and where
+//    there are few items, several blocks do.
 // Measured, with x and the weights from HBM: 1 token, 64 experts of 7168 x 2048 in bfloat16, top 8 (706 MB)
 // 117.5 us, 6.0 TB/s; 48 tokens (5.64 GB) 899 us, 6.3 TB/s; 7 tokens, 60 experts of 2056 x 1400 in float16, top
 // 6 (0.54 GB) 99.5 us, 5.5 TB/s; 4 tokens, 256 MXFP4 experts of 7168 x 2048, top 8 (0.72 GB) 183 us, 3.9 TB/s,
@@ -76,6 +77,7 @@ __host__ __device__ constexpr int stages_of(bool mx, bool wide, int regime) { re
 __host__ __device__ constexpr int pitch_of(bool wide) { return wide ? 128 : 144; }
 __host__ __device__ constexpr int stage_of(bool wide) { return 2 * 16 * pitch_of(wide); }
 constexpr int kMaxParts = 16;                    // most shares of H the logits are split into
+constexpr int kMaxSplits = 16;                   // most blocks that share a down item
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct Params {
@@ -103,6 +105,8 @@ struct Params {
     uint16_t *h;                  // [1 or 2][T k][Ip]
     int64_t h_plane;              // elements from the first parts to the second
     int pairs;
+    float *split;                 // [splits][H / 16, rounded up][T][16]: y's shares where blocks split its sums
+    unsigned *split_count;        // [H / 16, rounded up]: shares that are there
     uint8_t *h_field;             // [T k][Ip / 16]: exponent of the power of two each tile of h carries (float16)
     int Hp, Ip, kparts;
     int x_wide, wr_wide;              // 16-byte loads possible
@@ -439,7 +443,11 @@ struct Cursor {
     const uint8_t *scale_src;  // this lane's 8 scale bytes of chunk 0; null if there is no such row
 };
 
-template <int DT, int WDT, int kRegime, bool kWide>
+// kSplit: y has few rows (H up to half of 16 a block), and several blocks share a down item: each writes its
+// sums, and the last to come adds them up, always in the same order.  39 tokens, 248 experts of 556 x 1439 in
+// float16 (35 items): 516 -> 295 us; 13 tokens, 12 experts of 153 x 1455: 49 -> 33; where items are not shared
+// the code for it costs up to 5 %, so it is an instance of its own.
+template <int DT, int WDT, int kRegime, bool kWide, bool kSplit>
 struct Layer {
     static constexpr bool kMany = kRegime != kFew;            // more than 8 tokens
     static constexpr bool kMx = WDT == MOE_MXFP4;
@@ -463,6 +471,7 @@ struct Layer {
     int held_slot;
     int nact, up_items, up_units, up_tiles, down_items, down_chunks, down_parts;
     bool solo;                   // up items are single warps', not the block's
+    int splits_, split_, down_first_;   // kSplit: blocks of a down item; which of them this is; its first item
     int up_first, up_stride, up_begin, up_step;   // this warp's items, and its units of one
     const uint16_t *act, *start, *cols;
     const uint8_t *tokens;       // of the columns (kMany)
@@ -520,10 +529,20 @@ struct Layer {
         up_step = solo ? 1 : kWarps;
         down_items = (p.H + 15) / 16;
         down_chunks = (p.I + kDownK - 1) / kDownK;
+        if (kSplit) {
+            splits_ = max(1, min(min(blocks / down_items, kMaxSplits), nact * down_chunks / (2 * kWarps)));
+            split_ = splits_ > 1 ? blockIdx.x / down_items : 0;
+            down_first_ = splits_ == 1 ? blockIdx.x : split_ < splits_ ? blockIdx.x - split_ * down_items : down_items;
+        }
         // an expert's K is cut into shares, taken by the warps in turn: single chunks, or (where a
         // change of expert costs something) as few as give every warp four or more
-        down_parts = !kMany ? down_chunks : min(down_chunks, (4 * kWarps + nact - 1) / nact);
+        down_parts = !kMany ? down_chunks : min(down_chunks, (4 * down_stride() + nact - 1) / nact);
     }
+
+    __device__ __forceinline__ int splits() const { return kSplit ? splits_ : 1; }
+    __device__ __forceinline__ int split() const { return kSplit ? split_ : 0; }
+    __device__ __forceinline__ int down_first() const { return kSplit ? down_first_ : (int)blockIdx.x; }
+    __device__ __forceinline__ int down_stride() const { return splits() * kWarps; }
 
     // point the cursor at the rows of its item and expert
     __device__ __forceinline__ void aim(Cursor &c) const
@@ -547,13 +566,13 @@ struct Layer {
     {
         if (++c.chunk < c.last)
             return true;
-        c.part += kWarps;
+        c.part += down_stride();
         return enter_part(c);
     }
 
     __device__ __forceinline__ bool first_chunk(Cursor &c) const
     {
-        c.part = warp;
+        c.part = split() * kWarps + warp;
         c.expert = 0;
         return enter_part(c);
     }
@@ -586,7 +605,7 @@ struct Layer {
 
     __device__ __forceinline__ void first_down(Cursor &c) const
     {
-        c.item = blockIdx.x;
+        c.item = down_first();
         c.phase = c.item < down_items && first_chunk(c) ? 1 : 2;
     }
 
@@ -632,7 +651,7 @@ struct Layer {
             // Rows that begin at any byte: the nine aligned 16-byte pieces that hold 128 bytes of each, cut off
             // at the row's end.  Lanes take 8 pieces of 4 rows at a time, the ninth of all 32 rows last.  Bound by
             // the instructions of copies and shifts: 7 tokens, 60 experts of 2055 x 1399 in float16 take
-            // 152 us (2056 x 1400: 97); by 33 aligned words a row 197, by loads of single elements 655.
+            // 146 us (2056 x 1400: 98); by 33 aligned words a row 197, by loads of single elements 655.
             const int K = kUp ? p.H : p.I;
             const int64_t bytes = kMx ? K / 2 : 2 * (int64_t)K;
             const uintptr_t all = reinterpret_cast<uintptr_t>(kUp ? p.w13 : p.w2);
@@ -1043,6 +1062,39 @@ struct Layer {
         }
     }
 
+    // this block's sum for row r of down item `item`, which exists
+    __device__ __forceinline__ void give(int item, int tok, int r, float v) const
+    {
+        if (splits() == 1)
+            store1<DT>(p.y, (int64_t)tok * p.H + item * 16 + r, v * field_value(254u - field_of(tok)));
+        else
+            __stcg(p.split + (((int64_t)split() * down_items + item) * p.T + tok) * 16 + r, v);
+    }
+
+    // the last of the item's blocks adds up what all have given
+    __device__ __forceinline__ void add_shares(int item, int *last) const
+    {
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            *last = atomicAdd(p.split_count + item, 1u) == (unsigned)splits() - 1u;
+            __threadfence();
+        }
+        __syncthreads();
+        if (*last == 0)
+            return;
+        for (int i = threadIdx.x; i < 16 * p.T; i += kThreads) {
+            const int r = i % 16, tok = i / 16;
+            if (item * 16 + r >= p.H)
+                continue;
+            float v = 0.f;
+#pragma unroll 4
+            for (int q = 0; q < splits(); ++q)
+                v += __ldcg(p.split + (((int64_t)q * down_items + item) * p.T + tok) * 16 + r);
+            store1<DT>(p.y, (int64_t)tok * p.H + item * 16 + r, v * field_value(254u - field_of(tok)));
+        }
+    }
+
     // ------------------------------------------------------------ before the first wait
 
     // x's row t as the products take it: 16-bit, zeros past H, scaled (kMx); and the ends of its h rows
@@ -1279,6 +1331,9 @@ struct Layer {
             p.waits->arrived[threadIdx.x] = 0;
             p.status[threadIdx.x] = 0;
         }
+        if (kSplit && blockIdx.x == 0)
+            for (int i = threadIdx.x; i < (p.H + 15) / 16; i += kThreads)
+                p.split_count[i] = 0u;
         for (int tok = gridDim.x - 1 - blockIdx.x; tok < p.T; tok += gridDim.x)
             prepare_row(tok);
         for (int item = blockIdx.x; item < (p.E + 15) / 16 * p.kparts; item += gridDim.x)
@@ -1411,7 +1466,7 @@ struct Layer {
             const int token = p.pairs ? g % 4 : g;
             const uint32_t field = token < p.T ? field_of(token) : 127u;
             Cursor w;   // where the operands in `b` come from
-            bool some = (int)blockIdx.x < down_items && first_chunk(w);
+            bool some = down_first() < down_items && first_chunk(w);
             Column c[kCols], c1[kCols];
             Tokens<kDownGroups> b;
             // up to 4 tokens: columns 4 .. 7 are the second parts of h
@@ -1429,7 +1484,7 @@ struct Layer {
                 load_all<false>(b, c1, w.chunk * kDownK);
             }
             c[0].field = field;   // all that is still asked of the column whose operands are there
-            for (int item = blockIdx.x; item < down_items; item += gridDim.x) {
+            for (int item = down_first(); item < down_items; item += gridDim.x) {
                 float acc[2][NT][4] = {};
                 for (bool more = some; more;) {
                     const int at = take(), e = w.expert;
@@ -1456,15 +1511,17 @@ struct Layer {
                         float v = gather(red(buf), 0, r, tok);
                         if (p.pairs)
                             v += gather(red(buf), 0, r, tok + 4);
-                        store1<DT>(p.y, (int64_t)tok * p.H + n, v * field_value(254u - field_of(tok)));
+                        give(item, tok, r, v);
                     }
                 }
+                if (splits() > 1)
+                    add_shares(item, s_ok);
                 buf ^= 1;
             }
         } else {
             constexpr int kSumPitch = 17;   // [token][16 rows and a pad]
             float *mine = reinterpret_cast<float *>(smem + p.sm_red) + warp * p.T * kSumPitch;
-            for (int item = blockIdx.x; item < down_items; item += gridDim.x) {
+            for (int item = down_first(); item < down_items; item += gridDim.x) {
                 for (int i = lane; i < p.T * kSumPitch; i += 32)
                     mine[i] = 0.f;
                 __syncwarp();
@@ -1494,7 +1551,7 @@ struct Layer {
                             multiply_all<false>(at, 0, tiles, b, c, c1, k0, k0 + kDownK / 2, acc, column);
                         more = ++w.chunk < w.last;
                         if (!more) {
-                            w.part += kWarps;
+                            w.part += down_stride();
                             some = enter_part(w);
                             enter();
                         }
@@ -1526,8 +1583,10 @@ struct Layer {
 #pragma unroll
                     for (int q = 0; q < kWarps; ++q)
                         v += all[(q * p.T + tok) * kSumPitch + r];
-                    store1<DT>(p.y, (int64_t)tok * p.H + n, v * field_value(254u - field_of(tok)));
+                    give(item, tok, r, v);
                 }
+                if (splits() > 1)
+                    add_shares(item, s_ok);
                 __syncthreads();
             }
         }
@@ -1536,20 +1595,20 @@ struct Layer {
     }
 };
 
-template <int DT, int WDT, int kRegime, bool kWide>
+template <int DT, int WDT, int kRegime, bool kWide, bool kSplit>
 __global__ void __launch_bounds__(32 * warps_of(WDT == MOE_MXFP4, kWide, kRegime), 1)
     layer_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    Layer<DT, WDT, kRegime, kWide>(p, smem).run();
+    Layer<DT, WDT, kRegime, kWide, kSplit>(p, smem).run();
 }
 
-template <int DT, int WDT, int kRegime>
+template <int DT, int WDT, int kRegime, bool kSplit>
 cudaError_t launch_one(const Params &p, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s)
 {
     static std::atomic<uint64_t> allowed[2];
     const bool wide = p.w13_wide && p.w2_wide;
-    auto kernel = wide ? layer_kernel<DT, WDT, kRegime, true> : layer_kernel<DT, WDT, kRegime, false>;
+    auto kernel = wide ? layer_kernel<DT, WDT, kRegime, true, kSplit> : layer_kernel<DT, WDT, kRegime, false, kSplit>;
     const cudaError_t err = mrr_device::allow_smem(kernel, info, allowed[wide]);
     if (err != cudaSuccess)
         return err;
@@ -1558,18 +1617,22 @@ cudaError_t launch_one(const Params &p, const mrr_device::Info &info, int grid, 
                                        dim3(32 * warps_of(WDT == MOE_MXFP4, wide, kRegime)), args, smem, s);
 }
 
-template <int DT>
+template <int DT, bool kSplit>
 cudaError_t launch_dt(const Params &p, bool mx, int regime, const mrr_device::Info &info, int grid, size_t smem,
                       cudaStream_t s)
 {
     if (regime == kFew)
-        return mx ? launch_one<DT, MOE_MXFP4, kFew>(p, info, grid, smem, s) : launch_one<DT, DT, kFew>(p, info, grid, smem, s);
+        return mx ? launch_one<DT, MOE_MXFP4, kFew, kSplit>(p, info, grid, smem, s)
+                  : launch_one<DT, DT, kFew, kSplit>(p, info, grid, smem, s);
     if (regime == kSpread)
-        return mx ? launch_one<DT, MOE_MXFP4, kSpread>(p, info, grid, smem, s) : launch_one<DT, DT, kSpread>(p, info, grid, smem, s);
-    return launch_one<DT, DT, kDense>(p, info, grid, smem, s);
+        return mx ? launch_one<DT, MOE_MXFP4, kSpread, kSplit>(p, info, grid, smem, s)
+                  : launch_one<DT, DT, kSpread, kSplit>(p, info, grid, smem, s);
+    return launch_one<DT, DT, kDense, kSplit>(p, info, grid, smem, s);
 }
 
-cudaError_t launch_bf16(const Params &p, bool mx, int regime, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s);
-cudaError_t launch_f16(const Params &p, bool mx, int regime, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s);
+// moe_layer_{bf16,f16}[_split].cu
+using Launch = cudaError_t(const Params &p, bool mx, int regime, const mrr_device::Info &info, int grid, size_t smem,
+                           cudaStream_t s);
+Launch launch_bf16, launch_f16, launch_bf16_split, launch_f16_split;
 
 }  // namespace moe_layer

@@ -412,6 +412,28 @@ def test_layer_most_assignments_of_narrow_rows(T, E, k, H, I, mx):
     test_layer_most_assignments(T, E, k, H, I, mx)
 
 
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T,E,k,H,I", [(20, 40, 4, 96, 1040), (3, 24, 8, 30, 2050), (64, 9, 3, 1, 700), (8, 16, 8, 1216, 640)])
+def test_layer_few_output_rows(T, E, k, H, I, mx):
+    """Items of the down product that several blocks share: right, and bit for bit the same each time, whatever the
+    workspace held before."""
+    import torch
+
+    H += mx and H % 2
+    layer_case(T + H, T, E, k, H, I, "float16" if T == 20 else "bfloat16", mx=mx, norm_type=1)
+    bf = lambda *s_: torch.randn(*s_, device="cuda").bfloat16()  # noqa: E731
+    x, wr = bf(T, H), bf(E, H)
+    w13, w2, kw = bf(E, 2 * I, H), bf(E, H, I), {}
+    if mx:
+        (w13, s13), (w2, s2) = moe.moe_mx_quantize(w13), moe.moe_mx_quantize(w2)
+        kw = dict(w13_scales=s13, w2_scales=s2)
+    n = moe.moe_few_token_layer_workspace(T, H, E, I, k)
+    runs = [moe.moe_few_token_layer(x, wr, w13, w2, k, check_status=True, **kw,
+                                    workspace=torch.full((n,), fill, dtype=torch.uint8, device="cuda"))
+            for fill in (0, 255, 1, 77)]
+    assert all(torch.equal(runs[0], r) for r in runs[1:])
+
+
 def test_layer_all_tokens_choose_the_same_experts():
     """A bias that decides the choice: one pair of experts takes all 64 tokens."""
     import torch
