@@ -27,7 +27,7 @@
 //    there are few items, several blocks do.
 // Measured, with x and the weights from HBM: 1 token, 64 experts of 7168 x 2048 in bfloat16, top 8 (706 MB)
 // 117.5 us, 6.0 TB/s; 48 tokens (5.64 GB) 899 us, 6.3 TB/s; 7 tokens, 60 experts of 2056 x 1400 in float16, top
-// 6 (0.54 GB) 99.5 us, 5.5 TB/s; 4 tokens, 256 MXFP4 experts of 7168 x 2048, top 8 (0.72 GB) 183 us, 3.9 TB/s,
+// 6 (0.54 GB) 99.5 us, 5.5 TB/s; 4 tokens, 256 MXFP4 experts of 7168 x 2048, top 8 (0.72 GB) 181 us, 4.0 TB/s,
 // bound by the instructions that unpack; 1 token, 8 experts of 1024 x 512 (6 MB) 16 us, bound by the
 // latency of three phases that wait for one another.
 // With up to 8 tokens the columns are the tokens themselves and the down product adds up all
