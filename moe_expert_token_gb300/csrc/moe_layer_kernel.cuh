@@ -1,5 +1,5 @@
 // The kernel of the mixture-of-experts layer for a few tokens (include/moe_layer.h), for GB300
-// (sm_103a).  moe_layer_{bf16,f16}.cu instantiate it, moe_layer.cu holds the host entry.
+// (sm_103a).  moe_layer_{bf16,f16}[_split].cu instantiate it, moe_layer.cu holds the host entry.
 //
 //   logits = x w_router^T;  experts, weights = gating(logits)
 //   h[a, i] = weight[a] silu(w13[e, i] . x) (w13[e, I + i] . x)      for each assignment a = (token, expert)
@@ -14,12 +14,13 @@
 //  * Each warp streams its own share of the K axis through a private ring of kStages 4 KB stages in
 //    shared memory.  A stage is two slabs of 16 rows x 128 bytes, each one tiled bulk copy issued by
 //    one lane (thread copies of 16 bytes, with their addresses, were most of the instructions that
-//    a stage cost).  The ring runs on across items, and from the up product into the down product:
+//    a stage cost; they bring rows that are not aligned to 16 bytes).  The ring runs on across items, and from the up product into the down product:
 //    the down weights of the first items are in flight while the grid waits for h.
 //  * A lane's 16-byte piece of a row feeds two matrix instructions: the order of k inside a group of
 //    32 is free as long as both operands share it, so lane (g, t) holds elements 8t .. 8t+7.
 //  * The grid waits twice: for the logits, and for h.  Between them every block computes the
-//    routing of all tokens for itself, which costs less than a third wait.
+//    routing of all tokens for itself, which costs less than a third wait; with more than 8 tokens
+//    each token's is one block's work, and there is one.
 //  * Up product: an item is 16 gate rows and the 16 up rows that belong to them, K split over the
 //    warps, joined in shared memory, or all of K by one warp; SwiGLU and the routing weight are
 //    applied to the sums, in float32.
