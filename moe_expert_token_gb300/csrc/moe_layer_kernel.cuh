@@ -136,10 +136,10 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// an asynchronous copy of 8 bytes; with ok false the destination is zeroed and src not read
-__device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool ok)
+// an asynchronous copy of 8 bytes: the first `bytes` of them are read, the rest zeros
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, int bytes)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 // of 16 bytes
@@ -703,11 +703,13 @@ struct Layer {
             }
             copies_arrive(bar);
         }
-        if (kMx) {   // 8 scale bytes a lane: [slab][row]
-            const int64_t at = (int64_t)c.chunk * (kUp ? 8 : 16), left = scale_row_bytes(kUp ? p.H : p.I) - at - (kUp ? 0 : lane / 16 * 8);
+        if (kMx) {
+            // 8 scale bytes a lane: [slab][row].  Bytes that stand for no block, the unused one of a last pair
+            // among them, read 0: 2^-127 leaves the zeros past K what they are, where a 255 would make them NaN.
+            const int at = c.chunk * (kUp ? 8 : 16), left = ((kUp ? p.H : p.I) + kBlock - 1) / kBlock - at - (kUp ? 0 : lane / 16 * 8);
             const bool ok = c.scale_src && left > 0;
             if (kUp ? p.s13_wide : p.s2_wide) {
-                copy8(mrr::smem_addr(scales(slot)) + lane * 8, ok ? c.scale_src + at : p.w13_s, ok);
+                copy8(mrr::smem_addr(scales(slot)) + lane * 8, ok ? c.scale_src + at : p.w13_s, ok ? min(left, 8) : 0);
                 copies_arrive(bar);
             } else {   // two bytes at a time, put into the stage at the next issue: they have come by then
                 held[0] = held[1] = 0u;
@@ -716,7 +718,7 @@ struct Layer {
 #pragma unroll
                     for (int b = 0; b < 8; b += 2)
                         if (b < left)
-                            held[b / 4] |= load_pair(c.scale_src + at + b) << (8 * (b % 4));
+                            held[b / 4] |= (load_pair(c.scale_src + at + b) & (b + 1 < left ? 0xffffu : 0xffu)) << (8 * (b % 4));
             }
         }
     }

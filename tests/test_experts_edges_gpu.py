@@ -1,0 +1,92 @@
+"""Calls of the expert operators at the edges of what their headers allow, against the float64 oracle.
+
+The tolerances are those of test_experts_gpu.py: the oracle's bound on float32 sums, h's 16-bit
+roundings in the layer, and the result's own rounding.
+"""
+import numpy as np
+import pytest
+
+import moe_expert_token_gb300 as moe
+import moe_expert_token_gb300.mrr_v2 as m
+from oracle import experts as ox
+from test_experts_gpu import H_UNIT, UNIT, close, down, grouped_case, up, weights
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    import torch
+
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from moe_expert_token_gb300 import build
+
+    build.build()
+    m.load_library()
+
+
+def offset(a, n):
+    """The device tensor of a numpy array, n elements past the start of an allocation."""
+    import torch
+
+    t = torch.from_numpy(np.ascontiguousarray(a))
+    flat = torch.zeros(t.numel() + n, dtype=t.dtype, device="cuda")
+    flat[n:] = t.reshape(-1).cuda()
+    return flat[n:].view(t.shape)
+
+
+def biased_layer(x, H, E, w13, s13, w2, s2):
+    """A layer whose bias gives every token experts E - 1 and 1, with weights 3.5 / 5 and 1.5 / 5."""
+    import torch
+
+    wr = torch.zeros(E, H, dtype=torch.bfloat16, device="cuda")
+    bias = torch.zeros(E, dtype=torch.bfloat16, device="cuda")
+    bias[E - 1], bias[1] = 3.0, 1.0
+    return moe.moe_few_token_layer(x, wr, w13, w2, 2, bias=bias, w13_scales=s13, w2_scales=s2, norm_type=1,
+                                   check_status=True)
+
+
+def biased_reference(x, E, v13, v2, h_unit):
+    T = len(x)
+    return ox.layer(x, np.tile(np.array([3.5, 1.5]) / 5.0, (T, 1)), np.tile([E - 1, 1], (T, 1)), np.full(T, 1e-6), v13,
+                    v2, h_unit)
+
+
+# ----------------------------------------------------------------------------- the unused scale byte of a last pair
+
+@pytest.mark.parametrize("T", [1, 3, 7, 20])
+@pytest.mark.parametrize("H,I", [(160, 96), (224, 224), (194, 222), (992, 736), (1026, 542)])
+@pytest.mark.parametrize("off", [0, 2])
+def test_layer_ignores_the_unused_scale_byte(T, H, I, off):
+    """K mod 64 in 2, 30 and 32: the last pair's second byte stands for no block, and 255 (NaN) in it
+    changes nothing.  Scale rows of 8-byte multiples and others, aligned and not."""
+    import torch
+
+    rng = np.random.default_rng(H + I + T)
+    E = 3
+    (w13, s13, v13), (w2, s2, v2) = weights(rng, E, 2 * I, H), weights(rng, E, H, I)
+    s13[..., -1, 1] = s2[..., -1, 1] = 255
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(torch.bfloat16).cuda()
+    y = biased_layer(x, H, E, up(w13), offset(s13, off), up(w2), offset(s2, off))
+    ref, bound = biased_reference(down(x), E, v13, v2, (H_UNIT if T <= 4 else UNIT)["float16"])
+    close(y, ref, bound, "bfloat16")
+
+
+@pytest.mark.parametrize("K", [32, 96, 160, 224, 992])
+def test_grouped_ignores_the_unused_scale_byte(K):
+    def edit(s):
+        s[..., -1, 1] = 255
+
+    got, ref, bound = grouped_case(K, [3, 0, 40, 130], K, 48, out="float32", x_edit=edit, w_edit=edit)
+    assert np.isfinite(ref).all()
+    close(got, ref, bound, "float32")
+
+
+@pytest.mark.parametrize("K", [2, 30, 96, 1026])
+def test_dequantize_ignores_the_unused_scale_byte(K):
+    import torch
+
+    q, s = ox.mx_quantize(np.random.default_rng(K).standard_normal((3, K)))
+    s[:, -1, 1] = 255
+    assert np.array_equal(down(moe.moe_mx_dequantize(up(q), up(s), torch.float32)), ox.mx_values(q, s))
