@@ -709,7 +709,9 @@ struct Layer {
             const int at = c.chunk * (kUp ? 8 : 16), left = ((kUp ? p.H : p.I) + kBlock - 1) / kBlock - at - (kUp ? 0 : lane / 16 * 8);
             const bool ok = c.scale_src && left > 0;
             if (kUp ? p.s13_wide : p.s2_wide) {
-                copy8(mrr::smem_addr(scales(slot)) + lane * 8, ok ? c.scale_src + at : p.w13_s, ok ? min(left, 8) : 0);
+                // the address counts even where nothing is read: one that is aligned whatever the scales' are
+                copy8(mrr::smem_addr(scales(slot)) + lane * 8,
+                      ok ? c.scale_src + at : reinterpret_cast<const uint8_t *>(p.status), ok ? min(left, 8) : 0);
                 copies_arrive(bar);
             } else {   // two bytes at a time, put into the stage at the next issue: they have come by then
                 held[0] = held[1] = 0u;

@@ -90,3 +90,23 @@ def test_dequantize_ignores_the_unused_scale_byte(K):
     q, s = ox.mx_quantize(np.random.default_rng(K).standard_normal((3, K)))
     s[:, -1, 1] = 255
     assert np.array_equal(down(moe.moe_mx_dequantize(up(q), up(s), torch.float32)), ox.mx_values(q, s))
+
+
+# ----------------------------------------------------------------------------- scales of unlike alignment
+
+@pytest.mark.parametrize("T", [1, 4, 8, 20])
+@pytest.mark.parametrize("H,I", [(200, 256), (456, 200), (242, 480)])
+@pytest.mark.parametrize("off13,off2", [(2, 0), (1, 0), (4, 8), (0, 2), (0, 3)])
+def test_layer_scales_of_unlike_alignment(T, H, I, off13, off2):
+    """w13_scales and w2_scales aligned differently, where scale rows are 8-byte multiples (H and I of 193 to
+    256 and 449 to 512), half of a stage's lanes have no bytes to bring (I = 200, 256), and the last items have
+    fewer than 16 rows."""
+    import torch
+
+    rng = np.random.default_rng(H + I + T)
+    E = 3
+    (w13, s13, v13), (w2, s2, v2) = weights(rng, E, 2 * I, H), weights(rng, E, H, I)
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(torch.bfloat16).cuda()
+    y = biased_layer(x, H, E, up(w13), offset(s13, off13), up(w2), offset(s2, off2))
+    ref, bound = biased_reference(down(x), E, v13, v2, (H_UNIT if T <= 4 else UNIT)["float16"])
+    close(y, ref, bound, "bfloat16")
