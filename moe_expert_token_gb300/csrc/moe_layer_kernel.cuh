@@ -1281,12 +1281,12 @@ struct Layer {
             for (int a0 = 0; a0 < n; a0 += 32) {   // in order: an expert's columns are in token order
                 const int a = a0 + lane, e = a < n ? expert[a] : -1;
                 const uint32_t same = __match_any_sync(kFull, e);
-                const int rank = __popc(same & ((1u << lane) - 1u));
+                const int rank = __popc(same & ((1u << lane) - 1u)), before = a < n ? count[e] : 0;
+                __syncwarp();   // every lane has read its count before the first of its expert's changes it
                 if (a < n) {
-                    place[a] = (uint16_t)(count[e] + rank);
-                    __syncwarp(__activemask());
+                    place[a] = (uint16_t)(before + rank);
                     if (rank == 0)
-                        count[e] = (uint16_t)(count[e] + __popc(same));
+                        count[e] = (uint16_t)(before + __popc(same));
                 }
                 __syncwarp();
             }
