@@ -49,6 +49,9 @@ constexpr int kTurnPitch = 36;           // floats: 16-byte reads of rows and 4-
 constexpr int kFewRows = 24;             // so many rows an expert, on average, or fewer: weights' bytes are what counts
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
+// The barriers, for tests that let a wait run out: one of a kind expects an arrival that never comes.
+enum Barrier { kNone, kFullStage, kEmptyStage, kFullSums, kEmptySums };
+
 struct Params {
     const uint8_t *scales, *w_scales;
     int A, K, E, N, counts_i64, counts_prefix, gated, out_dt;
@@ -62,6 +65,8 @@ struct Params {
     int align, w_align;    // of scale rows: 32, 16, 8 or 2 bytes
     int out_wide;          // 16-bit and MXFP4 rows can be written so many bytes at a time: 32, 8, or 0 (less)
     int sm_stage, sm_tables, sm_scales, sm_turn;
+    uint64_t wait_ns;  // limit of each wait
+    int short_of;      // a Barrier, else kNone
 };
 
 struct Maps {
@@ -86,24 +91,25 @@ struct Shared {
     int abort, bad;
 };
 
-__device__ __forceinline__ bool wait(Shared *sh, uint64_t *bar, uint32_t parity)
+// Wait for a phase of `bar`, by a whole warp, which stays together: false for all of it where a lane has
+// given up, after p.wait_ns or because another warp has.
+__device__ __forceinline__ bool wait(const Params &p, Shared *sh, uint64_t *bar, uint32_t parity)
 {
+    bool there = true;
     uint64_t t0 = 0;   // the timer is slow to read: not before a wait has become a long one
-    for (uint32_t it = 1;; ++it) {
-        if (mrr::mbar_try_wait(mrr::smem_addr(bar), parity))
-            return true;
+    for (uint32_t it = 1; !mrr::mbar_try_wait(mrr::smem_addr(bar), parity); ++it)
         if (it % 1024 == 0) {
-            if (*reinterpret_cast<volatile int *>(&sh->abort))
-                return false;
             const uint64_t now = mrr::global_timer_ns();
             if (t0 == 0)
                 t0 = now;
-            else if (now - t0 > kWaitLimitNs) {
+            else if (now - t0 > p.wait_ns)
                 *reinterpret_cast<volatile int *>(&sh->abort) = 1;
-                return false;
+            if (*reinterpret_cast<volatile int *>(&sh->abort)) {
+                there = false;
+                break;
             }
         }
-    }
+    return __all_sync(kFull, there);
 }
 
 // Row and tile prefixes of the experts, into tables[0 .. E] and tables[E + 1 .. 2 E + 1]; flags of bad
@@ -393,12 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mrr::mbar_init(mrr::smem_addr(&sh->full[s]), 1 + 4);   // the copies' thread, four scale warps
-            mrr::mbar_init(mrr::smem_addr(&sh->empty[s]), 1);
+            mrr::mbar_init(mrr::smem_addr(&sh->full[s]), 1 + 4 + (p.short_of == kFullStage));   // the copies' thread, four scale warps
+            mrr::mbar_init(mrr::smem_addr(&sh->empty[s]), 1 + (p.short_of == kEmptyStage));
         }
         for (int b = 0; b < 2; ++b) {
-            mrr::mbar_init(mrr::smem_addr(&sh->sums_full[b]), 1);
-            mrr::mbar_init(mrr::smem_addr(&sh->sums_empty[b]), kEpilogueWarps);
+            mrr::mbar_init(mrr::smem_addr(&sh->sums_full[b]), 1 + (p.short_of == kFullSums));
+            mrr::mbar_init(mrr::smem_addr(&sh->sums_empty[b]), kEpilogueWarps + (p.short_of == kEmptySums));
         }
         mrr::mbar_init(mrr::smem_addr(&sh->drained), 1);
         sh->abort = 0;
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {   // codes
         const bool leader = tc::elect();
         int stage = 0;
-        uint32_t parity = 1u, issued = 0u;
+        uint32_t parity = 1u;
         bool ok = true;
         for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
             const Tile t = tile_at(p, tables, features, kFeatures, i);
@@ -443,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const CUtensorMap *x_map = &maps.x[box];
             const uint32_t bytes = (kTiles * kRowTile + box_rows(box)) * kStepBytes;
             for (int k = 0; k < steps; ++k) {
-                if (!(ok = wait(sh, &sh->empty[stage], parity)))
+                if (!(ok = wait(p, sh, &sh->empty[stage], parity)))
                     break;
                 const uint32_t at = stage0 + stage * stage_size, bar = mrr::smem_addr(&sh->full[stage]);
                 if (leader) {
@@ -455,15 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::load_box(at + off_x, x_map, k * kStepBytes, x_row, bar);
                 }
                 __syncwarp();
-                issued |= 1u << stage;
                 next_stage(stage, parity);
             }
-        }
-        if (!ok && lane == 0) {   // leave no copy in flight: give each stage's a moment to land
-            for (int s = 0; s < p.stages; ++s)
-                if (issued >> s & 1u)
-                    for (int b = 0; b < 2; ++b)
-                        mrr::mbar_wait_bounded(mrr::smem_addr(&sh->full[s]), b, 1000000ull);
         }
     } else if (warp == 1) {   // matrix instructions
         const bool leader = tc::elect();
@@ -473,14 +472,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t scales0 = tmem + p.sums * sums_columns;
         for (long long i = blockIdx.x; ok && i < total; i += gridDim.x) {
             const Tile t = tile_at(p, tables, features, kFeatures, i);
-            if (!(ok = wait(sh, &sh->sums_empty[set], set_parity)))
+            if (!(ok = wait(p, sh, &sh->sums_empty[set], set_parity)))
                 break;
             tc::fence_after();
             const uint32_t d = tmem + set * sums_columns;
             const uint32_t columns = tc::uniform(t.columns);
             const uint32_t instr[2] = {tc::mxf4_instr(columns, 0), tc::mxf4_instr(columns, 1)};
             for (int k = 0; k < steps; ++k) {
-                if (!(ok = wait(sh, &sh->full[stage], parity)))
+                if (!(ok = wait(p, sh, &sh->full[stage], parity)))
                     break;
                 tc::fence_after();
                 const uint32_t at = stage0 + stage * stage_size;
@@ -508,10 +507,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 set = 0;
                 set_parity ^= 1u;
             }
-        }
-        if (!ok && leader) {   // tensor memory is freed only after what was issued is done
-            tc::commit(mrr::smem_addr(&sh->drained));
-            mrr::mbar_wait_bounded(mrr::smem_addr(&sh->drained), 0, 100000000ull);
         }
     } else if (warp >= kScaleWarp) {   // scales
         const int r = threadIdx.x - 32 * kScaleWarp;
@@ -590,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         put(kTokenAtoms + 1536, now[3][2 * u + 1]);
                     }
                     // the other buffer is free again once all four warps are here
-                    if (any_of(1, 128, !wait(sh, &sh->empty[stage], parity))) {
+                    if (any_of(1, 128, !wait(p, sh, &sh->empty[stage], parity))) {
                         ok = false;
                         break;
                     }
@@ -622,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t parity = 0u;
         for (long long i = blockIdx.x; i < total; i += gridDim.x) {
             const Tile t = tile_at(p, tables, features, kFeatures, i);
-            const bool failed = !wait(sh, &sh->sums_full[set], parity);
+            const bool failed = !wait(p, sh, &sh->sums_full[set], parity);
             // kMixed: lane quarters 0 and 1 hold gate values, 2 and 3 the up values of the same features,
             // which change hands through shared memory; the two warps leave together
             const int pair = 2 + 2 * part + quarter % 2;
@@ -697,8 +692,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (threadIdx.x == 0 && sh->abort)
-        atomicOr(p.status, mrr_ws::kFlagTimeout);
+    if (sh->abort) {   // given up, by any warp: nothing may be in flight when the block leaves
+        if (threadIdx.x == 0) {
+            atomicOr(p.status, mrr_ws::kFlagTimeout);
+            // a stage's copies have a moment to land; at most one of the two phases is not over
+            for (int s = 0; s < p.stages; ++s)
+                for (int b = 0; b < 2; ++b)
+                    mrr::mbar_wait_bounded(mrr::smem_addr(&sh->full[s]), b, 1000000ull);
+        }
+        __syncwarp();
+        if (warp == 1) {   // tensor memory is freed only after what was issued, by this thread, is done
+            if (tc::elect()) {
+                tc::commit(mrr::smem_addr(&sh->drained));
+                mrr::mbar_wait_bounded(mrr::smem_addr(&sh->drained), 0, 100000000ull);
+            }
+            __syncwarp();
+        }
+    }
     if (warp == 1)
         tc::dealloc(tmem, kColumns);
 }
@@ -729,11 +739,14 @@ extern "C" {
 
 size_t moe_mx_grouped_workspace(int64_t E) { return E < 1 ? 0 : mrr_ws::kHeaderBytes; }
 
-mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64_t A, int64_t K,
-                              const void *expert_num, int expert_num_is_i64, int64_t expert_num_type, int64_t E,
-                              const uint8_t *w_codes, const uint8_t *w_scales, int64_t N, int gated,
-                              const float *row_weight, void *out, moe_dtype out_dt, uint8_t *out_scales,
-                              void *workspace, size_t workspace_bytes, mrr_stream_t stream)
+// moe_mx_grouped_run with another limit on its waits, and short of an arrival on one kind of barrier (a
+// Barrier): what a test calls to see a wait run out.  Not part of the library's interface.
+mrr_status moe_mx_grouped_run_waits(const uint8_t *codes, const uint8_t *scales, int64_t A, int64_t K,
+                                    const void *expert_num, int expert_num_is_i64, int64_t expert_num_type, int64_t E,
+                                    const uint8_t *w_codes, const uint8_t *w_scales, int64_t N, int gated,
+                                    const float *row_weight, void *out, moe_dtype out_dt, uint8_t *out_scales,
+                                    void *workspace, size_t workspace_bytes, mrr_stream_t stream, uint64_t wait_ns,
+                                    int short_of)
 {
     if (out_dt != MOE_F16 && out_dt != MOE_BF16 && out_dt != MOE_F32 && out_dt != MOE_MXFP4)
         return MRR_ERR_DTYPE;
@@ -759,6 +772,7 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
         return MRR_ERR_CUDA;
     }
     Params p{};
+    p.wait_ns = wait_ns, p.short_of = short_of;
     p.scales = scales, p.w_scales = w_scales;
     p.A = (int)A, p.K = (int)K, p.E = (int)E, p.N = (int)N;
     p.counts_i64 = expert_num_is_i64, p.counts_prefix = expert_num_type == 0, p.gated = gated, p.out_dt = (int)out_dt;
@@ -827,6 +841,17 @@ mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64
         return MRR_ERR_CUDA;
     }
     return MRR_OK;
+}
+
+mrr_status moe_mx_grouped_run(const uint8_t *codes, const uint8_t *scales, int64_t A, int64_t K,
+                              const void *expert_num, int expert_num_is_i64, int64_t expert_num_type, int64_t E,
+                              const uint8_t *w_codes, const uint8_t *w_scales, int64_t N, int gated,
+                              const float *row_weight, void *out, moe_dtype out_dt, uint8_t *out_scales,
+                              void *workspace, size_t workspace_bytes, mrr_stream_t stream)
+{
+    return moe_mx_grouped_run_waits(codes, scales, A, K, expert_num, expert_num_is_i64, expert_num_type, E, w_codes,
+                                    w_scales, N, gated, row_weight, out, out_dt, out_scales, workspace, workspace_bytes,
+                                    stream, kWaitLimitNs, kNone);
 }
 
 }  // extern "C"

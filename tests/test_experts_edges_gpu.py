@@ -3,6 +3,9 @@
 The tolerances are those of test_experts_gpu.py: the oracle's bound on float32 sums, h's 16-bit
 roundings in the layer, and the result's own rounding.
 """
+import ctypes
+import time
+
 import numpy as np
 import pytest
 
@@ -110,3 +113,52 @@ def test_layer_scales_of_unlike_alignment(T, H, I, off13, off2):
     y = biased_layer(x, H, E, up(w13), offset(s13, off13), up(w2), offset(s2, off2))
     ref, bound = biased_reference(down(x), E, v13, v2, (H_UNIT if T <= 4 else UNIT)["float16"])
     close(y, ref, bound, "bfloat16")
+
+
+# ----------------------------------------------------------------------------- waits that run out
+
+def limited(name, more):
+    """The library's internal form of a run function, whose waits have a limit of their own and may be short
+    of an arrival: `more` are the argtypes behind the public function's."""
+    lib = m.load_library()
+    f = getattr(lib, name + "_waits")
+    f.restype = ctypes.c_int
+    f.argtypes = [*getattr(lib, name).argtypes, *more]
+    return f
+
+
+LIMIT_NS = 20_000_000       # far more than a launch takes, far less than a test may
+
+
+@pytest.mark.parametrize("short_of", [1, 2, 3, 4], ids=["full_stage", "empty_stage", "full_sums", "empty_sums"])
+@pytest.mark.parametrize("A,N,gated", [(64, 5120, 0), (64, 2560, 1), (1600, 5120, 0), (1600, 2560, 1)])
+def test_grouped_wait_that_runs_out_is_reported(short_of, A, N, gated):
+    """One arrival less than a kind of barrier expects: the call ends soon, with MRR_ERR_TIMEOUT, and the next
+    one is right.  More tiles than blocks have sets of sums for, more steps than the ring has stages; tiles of one
+    weight tile and of two."""
+    import torch
+
+    E, K = 8, 2560
+    gen = torch.Generator(device="cuda").manual_seed(A + N)
+    byte = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=gen, device="cuda", dtype=torch.uint8)  # noqa: E731
+    q, s = byte(0, 256, A, K // 2), byte(120, 128, A, K // 64, 2)
+    w, ws = byte(0, 256, E, N * (1 + gated), K // 2), byte(120, 128, E, N * (1 + gated), K // 64, 2)
+    c = torch.full((E,), A // E, dtype=torch.int32, device="cuda")
+    want = moe.moe_mx_grouped_matmul(q, s, c, w, ws, gated=bool(gated), check_status=True)
+    y = torch.empty_like(want)
+    space = torch.empty(moe.moe_mx_grouped_workspace(E), dtype=torch.uint8, device="cuda")
+    run = limited("moe_mx_grouped_run", [ctypes.c_uint64, ctypes.c_int])
+
+    def call(short):
+        st = run(q.data_ptr(), s.data_ptr(), A, K, c.data_ptr(), 0, 1, E, w.data_ptr(), ws.data_ptr(), N, gated, None,
+                 y.data_ptr(), 1, None, space.data_ptr(), space.numel(), None, LIMIT_NS, short)
+        assert st == m.MRR_OK
+        return m.mrr_v2_read_status(space.data_ptr(), space.numel(), None)
+
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    assert call(short_of) == m.MRR_ERR_TIMEOUT
+    assert time.perf_counter() - t0 < 1.0
+    y.zero_()
+    assert call(0) == m.MRR_OK
+    assert torch.equal(y, want)
