@@ -17,7 +17,7 @@ bool sizes_ok(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
 
 constexpr int kDenseTokens = 12;  // more tokens an expert than that, on average: 16-bit weights go to kDense
 constexpr int kPairTokens = 4;   // up to so many tokens h is held in two parts
-constexpr int kMaxGrid = 512;    // words of the first grid-wide wait
+constexpr int kMaxGrid = 512;    // blocks; words of the first grid-wide wait, less one
 
 struct Layout {
     size_t waits, part, xh, route_expert, route_weight, x_scale, h_max, h, h_field, split, split_count, bytes;
@@ -35,7 +35,7 @@ Layout layout(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
     Layout l;
     l.Hp = (int)mrr_ws::round_up(H, 256);   // the products read whole stages, of up to 256 elements
     l.Ip = (int)mrr_ws::round_up(I, 512);   // of x and 512 of h
-    l.waits = take(sizeof(Waits) + kMaxGrid * 8);
+    l.waits = take(sizeof(Waits) + (kMaxGrid + 1) * 8);
     l.part = take(kMaxParts * T * E * 4);
     l.xh = take(T * l.Hp * 2);
     l.route_expert = take(T * k * 4);
@@ -71,12 +71,16 @@ size_t moe_few_token_layer_workspace(int64_t T, int64_t H, int64_t E, int64_t I,
     return sizes_ok(T, H, E, I, k) ? layout(T, H, E, I, k).bytes : 0;
 }
 
-mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64_t H, const void *w_router, int64_t E,
-                                   const void *bias, const void *w13, const uint8_t *w13_scales, const void *w2,
-                                   const uint8_t *w2_scales, moe_dtype w_dt, int64_t I, int64_t k, int64_t k_group,
-                                   int64_t group_count, float routed_scaling_factor, float eps,
-                                   int64_t group_select_mode, int64_t norm_type, void *y, float *topk_weight,
-                                   int32_t *expert_idx, void *workspace, size_t workspace_bytes, mrr_stream_t stream)
+// moe_few_token_layer_run with another limit on its waits; short_of, where not NULL, is a device word that is 0, or 1 +
+// the number of a grid-wide wait that is to expect a block more than there are.  What a test calls to see a wait run
+// out.  Not part of the library's interface.
+mrr_status moe_few_token_layer_run_waits(const void *x, moe_dtype dt, int64_t T, int64_t H, const void *w_router,
+                                         int64_t E, const void *bias, const void *w13, const uint8_t *w13_scales,
+                                         const void *w2, const uint8_t *w2_scales, moe_dtype w_dt, int64_t I, int64_t k,
+                                         int64_t k_group, int64_t group_count, float routed_scaling_factor, float eps,
+                                         int64_t group_select_mode, int64_t norm_type, void *y, float *topk_weight,
+                                         int32_t *expert_idx, void *workspace, size_t workspace_bytes,
+                                         mrr_stream_t stream, uint64_t wait_ns, const unsigned *short_of)
 {
     if ((dt != MOE_F16 && dt != MOE_BF16) || (w_dt != dt && w_dt != MOE_MXFP4))
         return MRR_ERR_DTYPE;
@@ -121,6 +125,7 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
     p.status = reinterpret_cast<uint32_t *>(ws);
     p.waits = reinterpret_cast<Waits *>(ws + l.waits);
     p.tag = fresh_tag();
+    p.wait_ns = wait_ns, p.short_of = short_of;
     p.part = reinterpret_cast<float *>(ws + l.part);
     p.xh = reinterpret_cast<uint16_t *>(ws + l.xh);
     p.route_expert = reinterpret_cast<int *>(ws + l.route_expert);
@@ -188,6 +193,18 @@ mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64
         return MRR_ERR_CUDA;
     }
     return MRR_OK;
+}
+
+mrr_status moe_few_token_layer_run(const void *x, moe_dtype dt, int64_t T, int64_t H, const void *w_router, int64_t E,
+                                   const void *bias, const void *w13, const uint8_t *w13_scales, const void *w2,
+                                   const uint8_t *w2_scales, moe_dtype w_dt, int64_t I, int64_t k, int64_t k_group,
+                                   int64_t group_count, float routed_scaling_factor, float eps,
+                                   int64_t group_select_mode, int64_t norm_type, void *y, float *topk_weight,
+                                   int32_t *expert_idx, void *workspace, size_t workspace_bytes, mrr_stream_t stream)
+{
+    return moe_few_token_layer_run_waits(x, dt, T, H, w_router, E, bias, w13, w13_scales, w2, w2_scales, w_dt, I, k, k_group,
+                                         group_count, routed_scaling_factor, eps, group_select_mode, norm_type, y,
+                                         topk_weight, expert_idx, workspace, workspace_bytes, stream, kWaitLimitNs, nullptr);
 }
 
 }  // extern "C"

@@ -93,6 +93,8 @@ struct Params {
     uint32_t *status;
     struct Waits *waits;          // see grid_wait
     unsigned long long tag;
+    uint64_t wait_ns;             // limit of each wait
+    const unsigned *short_of;     // null, or (tests that let a wait run out) a word: 1 + the grid-wide wait that expects a block more
     float *part;                  // [kparts][T][E]
     uint16_t *xh;                 // [T][Hp]: x's rows as the products take them
     int *route_expert;            // [T][k], with more than 8 tokens
@@ -242,16 +244,17 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, __half2 b)
 // bits, different for each call) into its own, block 0 reads them all and then writes the tag into
 // the word that the others read.  The later waits count arrivals in words that block 0 cleared before
 // the first.  One thread a block reads one word: 152 blocks that each read 152 words held one another
-// up for microseconds.  For a launch replayed from a graph, with the same tag, each block clears its
-// word, and block 0 the common one, after the last wait, when all are through the first.  A wait that
-// lasts kWaitLimitNs all the same gives up and returns false.
+// up for microseconds.  A launch replayed from a graph has the same tag each time, so a block never leaves
+// without clearing its word (block 0 the common one): after the last wait, when all are through the first,
+// or where it gives up, which can only make others give up too.  A wait that lasts p.wait_ns all the same
+// gives up and returns false.
 struct Waits {
     unsigned long long go, arrived[2];
     unsigned long long block[];
 };
 
 template <typename Done>
-__device__ __forceinline__ bool poll(const unsigned long long *word, Done done)
+__device__ __forceinline__ bool poll(const Params &p, const unsigned long long *word, Done done)
 {
     uint64_t t0 = 0;   // the timer is slow to read: not before a wait has become a long one
     for (uint32_t it = 1;; ++it) {
@@ -263,7 +266,7 @@ __device__ __forceinline__ bool poll(const unsigned long long *word, Done done)
             const uint64_t now = mrr::global_timer_ns();
             if (t0 == 0)
                 t0 = now;
-            else if (now - t0 > kWaitLimitNs)
+            else if (now - t0 > p.wait_ns)
                 return false;
         }
     }
@@ -279,6 +282,7 @@ template <int kThreads>
 __device__ __forceinline__ bool grid_wait(const Params &p, int which, int *s_ok)
 {
     Waits *w = p.waits;
+    const unsigned blocks = gridDim.x + (p.short_of && __ldcg(p.short_of) == 1u + which);
     auto is_tag = [&](unsigned long long v) { return v == p.tag; };
     bool ok = true;
     if (threadIdx.x == 0)
@@ -287,17 +291,17 @@ __device__ __forceinline__ bool grid_wait(const Params &p, int which, int *s_ok)
     if (which > 0) {
         if (threadIdx.x == 0) {
             asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(&w->arrived[which - 1]) : "memory");
-            ok = poll(&w->arrived[which - 1], [](unsigned long long v) { return v >= gridDim.x; });
+            ok = poll(p, &w->arrived[which - 1], [&](unsigned long long v) { return v >= blocks; });
         }
     } else if (blockIdx.x > 0) {
         if (threadIdx.x == 0) {
             publish(&w->block[blockIdx.x], p.tag);
-            ok = poll(&w->go, is_tag);
+            ok = poll(p, &w->go, is_tag);
         }
     } else {
-        for (int i = threadIdx.x; i < (int)gridDim.x; i += kThreads)
+        for (int i = threadIdx.x; i < (int)blocks; i += kThreads)
             if (i > 0)
-                ok = ok && poll(&w->block[i], is_tag);
+                ok = ok && poll(p, &w->block[i], is_tag);
         if (!ok)
             *s_ok = 0;
         __syncthreads();
@@ -763,7 +767,7 @@ struct Layer {
                     const uint64_t now = mrr::global_timer_ns();
                     if (t0 == 0)
                         t0 = now;
-                    else if (now - t0 > kWaitLimitNs) {
+                    else if (now - t0 > p.wait_ns) {
                         dead = true;
                         break;
                     }
@@ -1327,6 +1331,21 @@ struct Layer {
         return *s_nact;
     }
 
+    // this block's word of the first grid-wide wait, see there
+    __device__ __forceinline__ void clear_word() const
+    {
+        if (threadIdx.x == 0)
+            (blockIdx.x == 0 ? p.waits->go : p.waits->block[blockIdx.x]) = 0;
+    }
+
+    // a grid-wide wait has run out
+    __device__ __forceinline__ void give_up() const
+    {
+        clear_word();
+        if (threadIdx.x == 0)
+            atomicOr(p.status, mrr_ws::kFlagTimeout);
+    }
+
     // ------------------------------------------------------------ the two products
 
     __device__ void run()
@@ -1344,15 +1363,13 @@ struct Layer {
         for (int item = blockIdx.x; item < (p.E + 15) / 16 * p.kparts; item += gridDim.x)
             router_item(item);
         if (!grid_wait<kThreads>(p, 0, s_ok)) {
-            if (threadIdx.x == 0)
-                atomicOr(p.status, mrr_ws::kFlagTimeout);
+            give_up();
             return;
         }
         float *weight = reinterpret_cast<float *>(smem + p.sm_weight);
         uint16_t *expert = reinterpret_cast<uint16_t *>(smem);   // needed until the ring is
         if (!assign(expert, weight, s_ok)) {
-            if (threadIdx.x == 0)
-                atomicOr(p.status, mrr_ws::kFlagTimeout);
+            give_up();
             return;
         }
         sizes(columns(expert));
@@ -1460,12 +1477,10 @@ struct Layer {
         }
         if (!grid_wait<kThreads>(p, 2, s_ok)) {
             drain();
-            if (threadIdx.x == 0)
-                atomicOr(p.status, mrr_ws::kFlagTimeout);
+            give_up();
             return;
         }
-        if (threadIdx.x == 0)
-            (blockIdx.x == 0 ? p.waits->go : p.waits->block[blockIdx.x]) = 0;
+        clear_word();
 
         if (!kMany) {
             const int token = p.pairs ? g % 4 : g;

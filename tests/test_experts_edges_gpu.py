@@ -162,3 +162,51 @@ def test_grouped_wait_that_runs_out_is_reported(short_of, A, N, gated):
     y.zero_()
     assert call(0) == m.MRR_OK
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T,which", [(3, 0), (3, 2), (20, 0), (20, 1), (20, 2)])
+@pytest.mark.parametrize("H,I,mx", [(512, 256, False), (70, 38, False), (512, 256, True), (66, 166, True)])
+def test_layer_wait_that_runs_out_is_reported(T, which, H, I, mx):
+    """A grid-wide wait that expects a block more than there are: the call ends soon, with MRR_ERR_TIMEOUT, and
+    what follows on the same workspace is right: a replay of the same graph, whose first wait goes by the same
+    tag, on other inputs, and a plain call."""
+    import torch
+
+    E, k = 8, 2
+    gen = torch.Generator(device="cuda").manual_seed(T + H)
+    rnd = lambda *s: (torch.randn(*s, generator=gen, device="cuda") * s[-1] ** -0.5).bfloat16()  # noqa: E731
+    xs = [rnd(T, H) * H ** 0.5 for _ in range(4)]
+    wr, w13, w2, s13, s2 = rnd(E, H), rnd(E, 2 * I, H), rnd(E, H, I), None, None
+    if mx:
+        (w13, s13), (w2, s2) = moe.moe_mx_quantize(w13), moe.moe_mx_quantize(w2)
+    want = [moe.moe_few_token_layer(x, wr, w13, w2, k, w13_scales=s13, w2_scales=s2, check_status=True) for x in xs]
+    x, y = torch.empty_like(xs[0]), torch.empty_like(xs[0])
+    short_of = torch.zeros(1, dtype=torch.int32, device="cuda")
+    space = torch.full((moe.moe_few_token_layer_workspace(T, H, E, I, k),), 0xA5, dtype=torch.uint8, device="cuda")
+    run = limited("moe_few_token_layer_run", [ctypes.c_uint64, ctypes.c_void_p])
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st = run(ptr(x), 1, T, H, ptr(wr), E, None, ptr(w13), ptr(s13), ptr(w2), ptr(s2), 3 if mx else 1, I, k, 1, 1, 1.0,
+                 1e-20, 0, 0, ptr(y), None, None, ptr(space), space.numel(), torch.cuda.current_stream().cuda_stream,
+                 LIMIT_NS, ptr(short_of))
+    assert st == m.MRR_OK
+
+    def replay(i, short):
+        x.copy_(xs[i])
+        y.zero_()
+        short_of.fill_(short)
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        graph.replay()
+        st = m.mrr_v2_read_status(ptr(space), space.numel(), torch.cuda.current_stream().cuda_stream)
+        assert time.perf_counter() - t0 < 1.0
+        return st
+
+    assert replay(0, 0) == m.MRR_OK and torch.equal(y, want[0])
+    for i in (1, 2):
+        assert replay(i, 1 + which) == m.MRR_ERR_TIMEOUT
+        assert replay(i + 1, 0) == m.MRR_OK
+        assert torch.equal(y, want[i + 1])
+    again = moe.moe_few_token_layer(xs[1], wr, w13, w2, k, w13_scales=s13, w2_scales=s2, workspace=space, check_status=True)
+    assert torch.equal(again, want[1])
