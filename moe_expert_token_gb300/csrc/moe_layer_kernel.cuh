@@ -724,17 +724,17 @@ struct Layer {
 #pragma unroll
                     for (int b = 0; b < 8; b += 2)
                         if (b < left)
-                            held[b / 4] |= (load_pair(c.scale_src + at + b) & (b + 1 < left ? 0xffffu : 0xffu)) << (8 * (b % 4));
+                            held[b / 4] |= load_pair(c.scale_src + at + b, b + 1 < left) << (8 * (b % 4));
             }
         }
     }
 
-    // two bytes at any address
-    __device__ __forceinline__ uint32_t load_pair(const uint8_t *p_) const
+    // two bytes at any address, or one
+    __device__ __forceinline__ uint32_t load_pair(const uint8_t *p_, bool both) const
     {
-        if (reinterpret_cast<uintptr_t>(p_) % 2 == 0)
+        if (both && reinterpret_cast<uintptr_t>(p_) % 2 == 0)
             return __ldg(reinterpret_cast<const uint16_t *>(p_));
-        return (uint32_t)__ldg(p_) | (uint32_t)__ldg(p_ + 1) << 8;
+        return (uint32_t)__ldg(p_) | (both ? (uint32_t)__ldg(p_ + 1) << 8 : 0u);
     }
 
     __device__ __forceinline__ void put_held()
