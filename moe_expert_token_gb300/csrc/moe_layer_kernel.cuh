@@ -1504,8 +1504,22 @@ struct Layer {
                 load_all<false>(b, c1, w.chunk * kDownK);
             }
             c[0].field = field;   // all that is still asked of the column whose operands are there
+            // A token that did not choose an expert has zeros for it, which a NaN or an infinity in the expert's
+            // weights would still reach: sums are taken over expert by expert, by the columns that chose it.
+            const int pair_at = p.pairs ? 2 * t % 4 : 2 * t;
             for (int item = down_first(); item < down_items; item += gridDim.x) {
-                float acc[2][NT][4] = {};
+                float acc[2][NT][4] = {}, sum[4] = {};
+                auto take_over = [&](int e) {
+                    uint32_t who = 0u;   // the two columns' assignments
+                    if (p.T > 1)
+                        who = *reinterpret_cast<const uint32_t *>(cols + 8 * e + pair_at);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool chose = i % 2 ? who >> 16 != 0xffffu : (who & 0xffffu) != 0xffffu;
+                        sum[i] += chose ? acc[0][0][i] + acc[1][0][i] : 0.f;
+                        acc[0][0][i] = acc[1][0][i] = 0.f;
+                    }
+                };
                 for (bool more = some; more;) {
                     const int at = take(), e = w.expert;
                     place_rows(p.w2, act[e] * p.H + item * 16, p.I, 0);
@@ -1519,11 +1533,10 @@ struct Layer {
                         enter(c1[0]);
                     multiply_all<false>(at, kDownSteps - 1, 1, b, c, c1, 0, w.chunk * kDownK, acc,
                                         [&](int) { return Column(); });
+                    if (!more || (p.T > 1 && w.expert != e))   // one token chose all that are streamed
+                        take_over(e);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[0][0][i] += acc[1][0][i];
-                put(red(buf), 0, acc[0][0], row);
+                put(red(buf), 0, sum, row);
                 __syncthreads();
                 if (threadIdx.x < 128) {
                     const int r = threadIdx.x % 16, tok = threadIdx.x / 16, n = item * 16 + r;

@@ -210,3 +210,52 @@ def test_layer_wait_that_runs_out_is_reported(T, which, H, I, mx):
         assert torch.equal(y, want[i + 1])
     again = moe.moe_few_token_layer(xs[1], wr, w13, w2, k, w13_scales=s13, w2_scales=s2, workspace=space, check_status=True)
     assert torch.equal(again, want[1])
+
+
+# ----------------------------------------------------------------------------- NaN and infinity in weights
+
+def chosen_layer(choice, E, H, I, w13, s13, w2, s2, dt, seed=0):
+    """A layer whose tokens choose the experts of `choice` [T, 2] (in this order, by logits of 12 and 8
+    against about 0): (y, the oracle's routing of the same inputs)."""
+    import torch
+
+    rng = np.random.default_rng(seed)
+    f = lambda a: torch.from_numpy(a).to(getattr(torch, dt))  # noqa: E731
+    x = rng.standard_normal((len(choice), H))
+    x[:, :E] = 0
+    for t, (a, b) in enumerate(choice):
+        x[t, a], x[t, b] = 1.5, 1.0
+    wr = np.zeros((E, H))
+    wr[np.arange(E), np.arange(E)] = 8.0
+    x, wr = f(x), f(wr)
+    y, w, idx = moe.moe_few_token_layer(x.cuda(), wr.cuda(), w13, w2, 2, w13_scales=s13, w2_scales=s2,
+                                        return_routing=True, check_status=True)
+    rw, ridx, sure, error = ox.routing(down(x), down(wr), 2)
+    assert sure.all() and np.array_equal(idx.cpu().numpy(), ridx) and ridx.tolist() == [list(c) for c in choice]
+    return y, down(x), rw, ridx, 3 * error + 1e-5
+
+
+@pytest.mark.parametrize("T", [2, 4, 5, 8, 12])
+@pytest.mark.parametrize("H,I", [(96, 64), (2080, 320), (70, 1100)])
+@pytest.mark.parametrize("mx", [False, True])
+def test_layer_weights_of_an_expert_reach_only_its_tokens(T, H, I, mx):
+    """NaN in rows of an expert's weights is the result of the tokens that chose it, and of no other."""
+    import torch
+
+    rng = np.random.default_rng(T + H)
+    E = 8
+    choice = [(1, 6)] + [(3, 4) if t % 2 else (4, 7) for t in range(1, T)]
+    if mx:
+        (w13, s13, v13), (w2, s2, v2) = weights(rng, E, 2 * I, H), weights(rng, E, H, I)
+        s2[1, 5, 0, 0] = s2[6, H - 1, -1, 0] = 255
+        v2 = ox.mx_values(w2, s2)
+        w13, s13, w2, s2 = (up(a) for a in (w13, s13, w2, s2))
+    else:
+        w13, w2 = (torch.from_numpy(rng.standard_normal(s) * s[-1] ** -0.5).to(torch.bfloat16).cuda()
+                   for s in ((E, 2 * I, H), (E, H, I)))
+        w2[1, 5, 3] = w2[6, H - 1, I - 1] = float("nan")
+        s13, s2, v13, v2 = None, None, down(w13), down(w2)
+    y, x, rw, ridx, werr = chosen_layer(choice, E, H, I, w13, s13, w2, s2, "bfloat16")
+    ref, bound = ox.layer(x, rw, ridx, werr, v13, v2, (H_UNIT if T <= 4 else UNIT)["float16" if mx else "bfloat16"])
+    assert np.isnan(ref[0]).sum() == 2 and np.isfinite(ref[1:]).all()
+    close(y, ref, bound, "bfloat16")
