@@ -1542,7 +1542,9 @@ struct Layer {
                     const int r = threadIdx.x % 16, tok = threadIdx.x / 16, n = item * 16 + r;
                     if (tok < p.T && n < p.H) {
                         float v = gather(red(buf), 0, r, tok);
-                        if (p.pairs)
+                        // a sum that is not finite is all said: an infinite weight times a second part, which may
+                        // be 0 or of the other sign, would make it NaN
+                        if (p.pairs && fabsf(v) <= 3.4e38f)
                             v += gather(red(buf), 0, r, tok + 4);
                         give(item, tok, r, v);
                     }

@@ -259,3 +259,22 @@ def test_layer_weights_of_an_expert_reach_only_its_tokens(T, H, I, mx):
     ref, bound = ox.layer(x, rw, ridx, werr, v13, v2, (H_UNIT if T <= 4 else UNIT)["float16" if mx else "bfloat16"])
     assert np.isnan(ref[0]).sum() == 2 and np.isfinite(ref[1:]).all()
     close(y, ref, bound, "bfloat16")
+
+
+@pytest.mark.parametrize("T", [1, 3, 6, 12])
+@pytest.mark.parametrize("dt", ["bfloat16", "float16"])
+def test_layer_an_infinite_weight_gives_infinity(T, dt):
+    """An infinity in a weight of the down product makes that element of y infinite, with the sign of h: a
+    second part of h, which may be zero or of the other sign, must not make it NaN."""
+    import torch
+
+    rng = np.random.default_rng(T)
+    E, H, I = 8, 80, 48
+    w13, w2 = (torch.from_numpy(rng.standard_normal(s) * s[-1] ** -0.5).to(getattr(torch, dt)).cuda()
+               for s in ((E, 2 * I, H), (E, H, I)))
+    w2[4, :, 7] = float("inf")
+    w2[4, ::2, 7] = float("-inf")
+    y, x, rw, ridx, werr = chosen_layer([(4, 7)] * T, E, H, I, w13, None, w2, None, dt)
+    ref, bound = ox.layer(x, rw, ridx, werr, down(w13), down(w2), (H_UNIT if T <= 4 else UNIT)[dt])
+    assert np.isinf(ref).all()
+    close(y, ref, np.where(np.isfinite(bound), bound, 0), dt)
