@@ -5,7 +5,8 @@ integer device addresses) and the torch-level calls on top of it.
 ``moe_mx_quantize`` makes the packed float4_e2m1 rows and e8m0 scales that ``moe_re_routing`` moves;
 ``moe_mx_grouped_matmul`` takes what it returns, with its expert_token_num;
 ``moe_few_token_layer`` runs router, top-k, experts and the weighted sum of a decode step at once.
-A call given a ``stream`` runs and allocates there; its results are that stream's.
+A call given a ``stream`` of the tensors' device runs and allocates there; its results are that stream's.
+Results have no gradient, whatever the inputs ask for: the operators are for inference.
 Every step runs in the CUDA library; there is no other code path.
 """
 from __future__ import annotations
@@ -80,8 +81,10 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(stream, call, *args, **kw):
-    """``call`` with ``stream`` current: what it allocates belongs to that stream too."""
+def _on(stream, dev, call, *args, **kw):
+    """``call`` on tensors of ``dev`` with ``stream`` current: what it allocates belongs to that stream too."""
+    if stream.device != dev:
+        raise ValueError("stream must be one of the tensors' device")
     with torch.cuda.stream(stream):
         return call(*args, **kw)
 
@@ -125,7 +128,7 @@ def moe_mx_quantize(x, *, stream=None):
     """
     lib = _lib or _load()
     if stream is not None:
-        return _on(stream, moe_mx_quantize, x)
+        return _on(stream, x.device, moe_mx_quantize, x)
     shape = x.shape
     if not x.is_cuda or not shape:
         raise ValueError("x must be a CUDA tensor of at least one dimension")
@@ -152,7 +155,7 @@ def moe_mx_dequantize(codes, scales, dtype=None, *, stream=None):
     (float16, bfloat16, the default, or float32)."""
     lib = _lib or _load()
     if stream is not None:
-        return _on(stream, moe_mx_dequantize, codes, scales, dtype)
+        return _on(stream, codes.device, moe_mx_dequantize, codes, scales, dtype)
     dtype = torch.bfloat16 if dtype is None else dtype
     code = _CODES.get(dtype)
     if code is None:
@@ -184,7 +187,8 @@ def moe_mx_grouped_matmul(tokens, scales, expert_token_num, weight, weight_scale
     """
     lib = _lib or _load()
     if stream is not None:
-        return _on(stream, moe_mx_grouped_matmul, tokens, scales, expert_token_num, weight, weight_scales, gated=gated,
+        return _on(stream, tokens.device, moe_mx_grouped_matmul, tokens, scales, expert_token_num, weight, weight_scales,
+                   gated=gated,
                    out_dtype=out_dtype, row_weight=row_weight, expert_token_num_type=expert_token_num_type,
                    workspace=workspace, check_status=check_status)
     K = _check_mx(tokens, scales, "tokens")
@@ -243,7 +247,7 @@ def moe_few_token_layer(x, w_router, w13, w2, k: int, *, bias=None, w13_scales=N
     """
     lib = _lib or _load()
     if stream is not None:
-        return _on(stream, moe_few_token_layer, x, w_router, w13, w2, k, bias=bias, w13_scales=w13_scales,
+        return _on(stream, x.device, moe_few_token_layer, x, w_router, w13, w2, k, bias=bias, w13_scales=w13_scales,
                    w2_scales=w2_scales, k_group=k_group, group_count=group_count,
                    routed_scaling_factor=routed_scaling_factor, eps=eps, group_select_mode=group_select_mode,
                    norm_type=norm_type, return_routing=return_routing, workspace=workspace, check_status=check_status)
