@@ -89,6 +89,15 @@ def _on(stream, dev, call, *args, **kw):
         return call(*args, **kw)
 
 
+def _space(workspace, nbytes, dev):
+    """The caller's workspace, which must be memory of the tensors' device, or a new one."""
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the tensors' device")
+    return workspace
+
+
 def _run(function, name, args, dev, workspace=None, check_status=False):
     """Call ``function(*args, stream)`` on dev's current stream, with ``dev`` current."""
     handle = _raw_stream(dev.index)
@@ -188,9 +197,8 @@ def moe_mx_grouped_matmul(tokens, scales, expert_token_num, weight, weight_scale
     lib = _lib or _load()
     if stream is not None:
         return _on(stream, tokens.device, moe_mx_grouped_matmul, tokens, scales, expert_token_num, weight, weight_scales,
-                   gated=gated,
-                   out_dtype=out_dtype, row_weight=row_weight, expert_token_num_type=expert_token_num_type,
-                   workspace=workspace, check_status=check_status)
+                   gated=gated, out_dtype=out_dtype, row_weight=row_weight,
+                   expert_token_num_type=expert_token_num_type, workspace=workspace, check_status=check_status)
     K = _check_mx(tokens, scales, "tokens")
     if tokens.dim() != 2 or weight.dim() != 3:
         raise ValueError("tokens must be 2-D and weight 3-D")
@@ -222,8 +230,7 @@ def moe_mx_grouped_matmul(tokens, scales, expert_token_num, weight, weight_scale
         if code is None:
             raise TypeError("out_dtype must be float16, bfloat16, float32 or 'mxfp4'")
         out = torch.empty((A, N), dtype=out_dtype, device=dev)
-    if workspace is None:
-        workspace = torch.empty(lib.moe_mx_grouped_workspace(E), dtype=torch.uint8, device=dev)
+    workspace = _space(workspace, lib.moe_mx_grouped_workspace(E), dev)
     _run(lib.moe_mx_grouped_run, "moe_mx_grouped_run",
          (tokens.data_ptr(), scales.data_ptr(), A, K, c.data_ptr(), int(c.dtype == torch.int64), expert_token_num_type,
           E, weight.data_ptr(), weight_scales.data_ptr(), N, int(gated), _ptr(row_weight), out.data_ptr(), code,
@@ -281,8 +288,7 @@ def moe_few_token_layer(x, w_router, w13, w2, k: int, *, bias=None, w13_scales=N
     if return_routing:
         weight = torch.empty((T, k), dtype=torch.float32, device=dev)
         idx = torch.empty((T, k), dtype=torch.int32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(lib.moe_few_token_layer_workspace(T, H, E, I, k), dtype=torch.uint8, device=dev)
+    workspace = _space(workspace, lib.moe_few_token_layer_workspace(T, H, E, I, k), dev)
     _run(lib.moe_few_token_layer_run, "moe_few_token_layer_run",
          (x.data_ptr(), dt, T, H, w_router.data_ptr(), E, _ptr(bias), w13.data_ptr(), _ptr(w13_scales), w2.data_ptr(),
           _ptr(w2_scales), w_dt, I, k, k_group, group_count, routed_scaling_factor, eps, group_select_mode, norm_type,

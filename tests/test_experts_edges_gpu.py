@@ -278,3 +278,27 @@ def test_layer_an_infinite_weight_gives_infinity(T, dt):
     ref, bound = ox.layer(x, rw, ridx, werr, down(w13), down(w2), (H_UNIT if T <= 4 else UNIT)[dt])
     assert np.isinf(ref).all()
     close(y, ref, np.where(np.isfinite(bound), bound, 0), dt)
+
+
+# ----------------------------------------------------------------------------- what a caller's workspace may be
+
+def test_workspace_of_other_memory_is_refused():
+    """A workspace in host memory, or one whose bytes are not one after another, is refused, and one that
+    is too small or not aligned reported: none of them reaches the kernel."""
+    import torch
+
+    q = torch.zeros(8, 32, dtype=torch.uint8, device="cuda")
+    s = torch.full((8, 1, 2), 127, dtype=torch.uint8, device="cuda")
+    c = torch.tensor([4, 4], dtype=torch.int32, device="cuda")
+    w, ws = torch.zeros(2, 6, 32, dtype=torch.uint8, device="cuda"), torch.zeros(2, 6, 1, 2, dtype=torch.uint8, device="cuda")
+    x = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda")
+    wr, w13, w2 = (torch.zeros(*n, dtype=torch.bfloat16, device="cuda") for n in ((4, 64), (4, 64, 64), (4, 64, 32)))
+    good = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    for bad, err in ((torch.empty(1 << 20, dtype=torch.uint8), ValueError), (good[::2], ValueError),
+                     (good[:1].expand(1 << 20), ValueError), (good[:64], m.MrrError), (good[16:], m.MrrError)):
+        with pytest.raises(err):
+            moe.moe_mx_grouped_matmul(q, s, c, w, ws, workspace=bad)
+        with pytest.raises(err):
+            moe.moe_few_token_layer(x, wr, w13, w2, 2, workspace=bad)
+    moe.moe_mx_grouped_matmul(q, s, c, w, ws, workspace=good, check_status=True)
+    moe.moe_few_token_layer(x, wr, w13, w2, 2, workspace=good, check_status=True)
