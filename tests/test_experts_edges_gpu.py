@@ -302,3 +302,47 @@ def test_workspace_of_other_memory_is_refused():
             moe.moe_few_token_layer(x, wr, w13, w2, 2, workspace=bad)
     moe.moe_mx_grouped_matmul(q, s, c, w, ws, workspace=good, check_status=True)
     moe.moe_few_token_layer(x, wr, w13, w2, 2, workspace=good, check_status=True)
+
+
+# ----------------------------------------------------------------------------- the choice of experts
+
+SEPARATED = [(1, 8, 2, 256, 128, 0, 1, 1), (1, 64, 8, 512, 48, 1, 8, 4), (1, 1024, 64, 512, 32, 1, 1, 1), (1, 60, 6, 200, 72, 2, 4, 3),
+             (3, 256, 8, 512, 32, 0, 8, 2), (8, 1024, 64, 512, 32, 1, 16, 8), (9, 96, 4, 256, 40, 2, 1, 1),
+             (64, 1024, 64, 512, 32, 1, 1, 1), (64, 64, 64, 256, 40, 0, 1, 1), (40, 1024, 7, 256, 32, 0, 32, 8)]
+
+
+def separated(T, E, H, seed):
+    """x [T, H] and router weights [E, H] in bfloat16 whose logits spread over -3 .. 3, each token's in an
+    order of its own."""
+    import torch
+
+    rng = np.random.default_rng(seed)
+    x = torch.from_numpy(rng.standard_normal((T, H))).to(torch.bfloat16)
+    z = np.stack([rng.permutation(np.linspace(-3, 3, E)) for _ in range(T)])
+    return x, torch.from_numpy(np.linalg.lstsq(x.double().numpy(), z, rcond=None)[0].T.copy()).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T,E,k,H,I,norm,groups,keep", SEPARATED)
+def test_layer_experts_are_the_oracles(T, E, k, H, I, norm, groups, keep, mx):
+    """The experts, their order and weights, and y, against the oracle's own routing, with logits far enough apart
+    for it to be certain of every token's (one token of a step among them, and the largest tables)."""
+    x, wr = separated(T, E, H, T + E + H + 1)
+    kw = dict(norm_type=norm, group_count=groups, k_group=keep, group_select_mode=groups > 1, routed_scaling_factor=1.5)
+    rw, ridx, sure, error = ox.routing(x.double().numpy(), wr.double().numpy(), k, **kw)
+    assert sure.all()
+    rng = np.random.default_rng(E)
+    if mx:
+        (w13, s13, v13), (w2, s2, v2) = weights(rng, E, 2 * I, H), weights(rng, E, H, I)
+        w13, s13, w2, s2 = (up(a) for a in (w13, s13, w2, s2))
+    else:
+        w13, w2 = (up(rng.standard_normal(s) * s[-1] ** -0.5, "bfloat16") for s in ((E, 2 * I, H), (E, H, I)))
+        s13, s2, v13, v2 = None, None, down(w13), down(w2)
+    y, w, idx = moe.moe_few_token_layer(x.cuda(), wr.cuda(), w13, w2, k, w13_scales=s13, w2_scales=s2,
+                                        return_routing=True, check_status=True, **kw)
+    assert np.array_equal(idx.cpu().numpy(), ridx)
+    werr = 3 * error + 1e-5      # as in layer_case of test_experts_gpu.py
+    assert np.all(np.abs(down(w) - rw) <= werr[:, None] * np.abs(rw) + 1e-9)
+    ref, bound = ox.layer(x.double().numpy(), rw, ridx, werr, v13, v2,
+                          (H_UNIT if T <= 4 else UNIT)["float16" if mx else "bfloat16"])
+    close(y, ref, bound, "bfloat16")
