@@ -9,8 +9,9 @@
  *   y[t, n]      = sum over token t's experts of weight * sum_i h[t, e, i] w2[e, n, i]
  *
  * Sums are held in float32.  y is rounded once to x's type.  Between the two products weight * h goes
- * on in 16 bits (x's type, float16 for MXFP4 weights; float16 with a power of two for each 16
- * elements): as the sum of two such values with up to 4 tokens, rounded once with more.
+ * on as the sum of two 16-bit values (x's type, float16 for MXFP4 weights; float16 with a power of two
+ * for each 16 elements), whose error does not show in y.  With MXFP4 weights, bfloat16 x and more than 4
+ * tokens it is one float16 value: 2^-12, beside y's own rounding of 2^-9.
  *
  * Conventions are those of mrr_v2.h.
  */

@@ -16,7 +16,7 @@ bool sizes_ok(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
 }
 
 constexpr int kDenseTokens = 12;  // more tokens an expert than that, on average: 16-bit weights go to kDense
-constexpr int kPairTokens = 4;   // up to so many tokens h is held in two parts
+constexpr int kPairTokens = 4;   // up to so many tokens the second parts of h have columns of their own
 constexpr int kMaxGrid = 512;    // blocks; words of the first grid-wide wait, less one
 
 struct Layout {
@@ -42,7 +42,7 @@ Layout layout(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
     l.route_weight = take(T * k * 4);
     l.x_scale = take(T * 4);
     l.h_max = take(T * 4);
-    l.h = take((T <= kPairTokens ? 2 : 1) * T * k * l.Ip * 2);
+    l.h = take(2 * T * k * l.Ip * 2);
     l.h_field = take(T * k * (l.Ip / 16));
     const int64_t items = (H + 15) / 16, shares = items > kMaxGrid / 2 ? 0 : items * kMaxSplits < kMaxGrid ? items * kMaxSplits : kMaxGrid;
     l.split = take(shares * T * 16 * 4);
@@ -133,7 +133,6 @@ mrr_status moe_few_token_layer_run_waits(const void *x, moe_dtype dt, int64_t T,
     p.x_scale = reinterpret_cast<float *>(ws + l.x_scale);
     p.h_max = reinterpret_cast<uint32_t *>(ws + l.h_max);
     p.h = reinterpret_cast<uint16_t *>(ws + l.h);
-    p.h_plane = T * k * l.Ip;
     p.pairs = T <= kPairTokens;
     p.h_field = ws + l.h_field;
     p.split = reinterpret_cast<float *>(ws + l.split);

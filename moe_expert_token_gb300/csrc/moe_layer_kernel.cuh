@@ -58,8 +58,8 @@ constexpr uint32_t kFull = 0xffffffffu;
 //    one tile for MXFP4, whose unpacking needs the registers.  An expert with more tokens than that is
 //    streamed once for each tileful (the second time from L2: both run at about the same time).
 //  * kDense, 16-bit weights of experts with many tokens: all 4 tiles are loaded ahead, which takes all
-//    registers.  48 tokens, 16 experts of 7168 x 2048, 24 tokens an expert: 433 -> 333 us; 64 tokens, 64
-//    experts of 2048 x 1408, 6 tokens an expert: 261 -> 277; 12 tokens an expert: no difference.
+//    registers.  48 tokens, 16 experts of 7168 x 2048, 24 tokens an expert: 474 -> 402 us; 64 tokens, 16
+//    experts of 2048 x 1408, 32 an expert: 224 -> 175; 6 to 16 an expert: the same to 2 % slower.
 //    (For MXFP4, in half as long steps and with 8 warps: 16 tokens an expert 139 -> 162, 24 the same.)
 enum Regime { kFew, kSpread, kDense };
 __host__ __device__ constexpr int tiles_for(bool mx, int regime) { return regime == kFew || mx ? 1 : 4; }
@@ -101,12 +101,12 @@ struct Params {
     float *route_weight;
     float *x_scale;               // [T]: what undoes their scaling
     uint32_t *h_max;              // [T]: float bits of the largest |h| of the token
-    // h in 16 bits.  Up to 4 tokens (pairs) it is the sum of two parts: the down product has 8 columns
-    // anyway, and the four that the tokens leave take the second parts, so that y is rounded once, at
-    // its end.  With more tokens a second part would cost what it reads (8 % of a layer for 48 tokens,
-    // 17 % for 7), and h is rounded once: y's error is then 1.4 times that of its own rounding.
-    uint16_t *h;                  // [1 or 2][T k][Ip]
-    int64_t h_plane;              // elements from the first parts to the second
+    // h as the sum of two 16-bit parts, so that y is rounded once, at its end: with one part y's error was 1.4 times
+    // that.  Up to 4 tokens (pairs) the second parts take the four columns of the down product that the tokens
+    // leave; with more they are a second product with the same weights, which costs 3 % of a layer for 48 tokens,
+    // 4 % for 7, and 21 % where an expert has 24 tokens.  With MXFP4 weights and y in bfloat16 more than 4 tokens
+    // have one (float16) part, see kParts.  An element's parts lie 16 bytes apart, so that one load brings both.
+    uint16_t *h;                  // [T k][Ip / 8][parts][8]
     int pairs;
     float *split;                 // [splits][H / 16, rounded up][T][16]: y's shares where blocks split its sums
     unsigned *split_count;        // [H / 16, rounded up]: shares that are there
@@ -814,11 +814,16 @@ struct Layer {
     // that a step's time hides the loads.
     static constexpr int kCols = kRegime == kDense || NT == 1 ? NT : 2;
     static constexpr int kSlabGroups = kSlabK / 32, kUpGroups = kUpK / 32;
-    // MXFP4's down stages are 16 groups long: worked off a slab at a time, to hold half the operands
-    static constexpr int kDownSteps = kMx ? 2 : 1, kDownGroups = kDownK / 32 / kDownSteps;
-    template <int kGroups>
+    // Parts of h that more than 4 tokens' columns take one after the other.  One float16 part is enough
+    // where y is bfloat16: it adds 2^-12 to an error of 2^-9.
+    static constexpr int kParts = kMx && DT == MOE_BF16 ? 1 : 2;
+    static constexpr int kStored = kMany ? kParts : 2;   // in memory
+    // Down stages are worked off in steps, so that a step's operands fit the registers: MXFP4's are 16 groups long
+    static __host__ __device__ constexpr int down_steps(int parts) { return kMx ? 2 * parts : kRegime == kDense ? parts : 1; }
+    static __host__ __device__ constexpr int down_groups(int parts) { return kDownK / 32 / down_steps(parts); }
+    template <int kGroups, int kOf = 1>   // kOf: parts
     struct Tokens {
-        uint4 v[kCols][kGroups];
+        uint4 v[kOf][kCols][kGroups];
         uint32_t tile[kCols][kGroups];   // exponents of the tiles' powers of two (h in float16)
     };
     // Where a column's operands come from, this lane's part: null pointers for a column that is not there.
@@ -828,13 +833,22 @@ struct Layer {
         uint32_t field = 127u;           // exponent of the power of two that the token's sums carry
     };
 
-    template <bool kUp, int kGroups>
-    __device__ __forceinline__ void load(Tokens<kGroups> &b, int j, int i, const Column &c, int k0) const
+    template <bool kUp, int kGroups, int kOf>
+    __device__ __forceinline__ void load(Tokens<kGroups, kOf> &b, int j, int i, const Column &c, int k0) const
     {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c.v)
-            v = *reinterpret_cast<const uint4 *>(c.v + k0 + 32 * i);
-        b.v[j][i] = v;
+        const uint16_t *from = c.v + (kUp ? 1 : kStored) * (k0 + 32 * i);
+        uint4 v = make_uint4(0, 0, 0, 0), w = v;
+        if (c.v) {
+            if constexpr (kOf == 2)   // both parts, 32 bytes
+                asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w), "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                             : "l"(from));
+            else
+                v = *reinterpret_cast<const uint4 *>(from);
+        }
+        b.v[0][j][i] = v;
+        if constexpr (kOf == 2)
+            b.v[1][j][i] = w;
         if (!kUp && kScaled) {
             uint32_t f = 253u;
             if (c.v)
@@ -843,8 +857,8 @@ struct Layer {
         }
     }
 
-    template <bool kUp, int kGroups>
-    __device__ __forceinline__ void load_all(Tokens<kGroups> &b, const Column (&c)[kCols], int k0) const
+    template <bool kUp, int kGroups, int kOf>
+    __device__ __forceinline__ void load_all(Tokens<kGroups, kOf> &b, const Column (&c)[kCols], int k0) const
     {
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
@@ -854,14 +868,14 @@ struct Layer {
     }
 
     // The products of a step: two row tiles, one a slab (kUp), or one whose K runs on from slab to slab,
-    // from slab0, against column tiles j0 .. j0 + kN - 1.  kNext: their operands are b, which is loaded
-    // anew from `next` at k1; else they are loaded here from `now` at k1, four groups at a time.
+    // from the stage's group g0, against column tiles j0 .. j0 + kN - 1.  kNext: their operands are b, which is
+    // loaded anew from `next` at k1; else they are loaded here from `now` at k1, four groups at a time.
     // Past K both operands are zeros.
-    template <bool kUp, int kN, bool kNext, int kGroups, int kHeld>
-    __device__ __forceinline__ void multiply(int slot, int slab0, int j0, Tokens<kHeld> &b, const Column (&now)[kCols],
+    template <bool kUp, int kN, bool kNext, int kGroups, int kHeld, int kOf>
+    __device__ __forceinline__ void multiply(int slot, int g0, int j0, Tokens<kHeld, kOf> &b, const Column (&now)[kCols],
                                              const Column (&next)[kCols], int k1, float (&acc)[2][NT][4]) const
     {
-        constexpr int kTiles = kUp ? 2 : 1, kBatch = kGroups < 4 ? kGroups : 4;
+        constexpr int kTiles = kUp ? 2 : 1, kBatch = kHeld < kGroups ? kHeld : kGroups;
         const int stage_at = (warp * kStages + slot) * kStage + lane_at;   // kWide: a multiple of 1024, and lane_at
         uint2 sc[2][2];   // 8 scale bytes of rows `row` and `row` + 8
         if constexpr (kMx)
@@ -869,11 +883,11 @@ struct Layer {
             for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    sc[m][r] = *reinterpret_cast<const uint2 *>(scales(slot) + (kUp ? m : slab0) * 128 + r * 64 + row * 8);
+                    sc[m][r] = *reinterpret_cast<const uint2 *>(scales(slot) + (kUp ? m : g0 / kSlabGroups) * 128 + r * 64 + row * 8);
         float s[2][2][4];
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            const int q = i % kSlabGroups, slab = kUp ? 0 : slab0 + i / kSlabGroups;
+            const int q = (g0 + i) % kSlabGroups, slab = kUp ? 0 : (g0 + i) / kSlabGroups;
             const uint8_t *from = kWide ? smem + (stage_at ^ (kMx ? q << 4 : q << 6)) + slab * kSlab
                                         : smem + stage_at + (kMx ? q << 4 : q << 6) + slab * kSlab;
             if (!kNext && i % kBatch == 0)
@@ -898,7 +912,7 @@ struct Layer {
                         }
                         codes_to_half(w, a[m][r]);
                         if (i % 4 == 0)
-                            scales_to_float(i < 4 ? sc[m][r].x : sc[m][r].y, s[m][r]);
+                            scales_to_float(q < 4 ? sc[m][r].x : sc[m][r].y, s[m][r]);
                     } else {
                         uint4 v = *reinterpret_cast<const uint4 *>(piece);
                         if (!kWide)
@@ -909,26 +923,30 @@ struct Layer {
 #pragma unroll
             for (int j = 0; j < kN; ++j) {
                 const int at = kNext ? i : i % kBatch;
-                uint4 x = b.v[j][at];
-                if (!kUp && kScaled) {   // the token's power of two over the tile's: at most 1
-                    const __half2 f = __float2half2_rn(field_value(127u - min(b.tile[j][at] - now[j].field, 126u)));
-                    x = make_uint4(half2_mul(x.x, f), half2_mul(x.y, f), half2_mul(x.z, f), half2_mul(x.w, f));
-                }
+                __half2 f;   // the token's power of two over the tile's: at most 1
+                if (!kUp && kScaled)
+                    f = __float2half2_rn(field_value(127u - min(b.tile[j][at] - now[j].field, 126u)));
 #pragma unroll
-                for (int m = 0; m < kTiles; ++m) {
-                    // one row tile: two chains of sums, so that an instruction waits for the last but one
-                    float(&to)[4] = acc[kUp ? m : i % 2][j0 + j];
-                    if constexpr (kMx) {
-                        float d[4];
-                        mma_first<MDT>(d, a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], x.x, x.y);
-                        mma<MDT>(d, a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], x.z, x.w);
-                        to[0] = fmaf(s[m][0][i % 4], d[0], to[0]);
-                        to[1] = fmaf(s[m][0][i % 4], d[1], to[1]);
-                        to[2] = fmaf(s[m][1][i % 4], d[2], to[2]);
-                        to[3] = fmaf(s[m][1][i % 4], d[3], to[3]);
-                    } else {
-                        mma<MDT>(to, a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], x.x, x.y);
-                        mma<MDT>(to, a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], x.z, x.w);
+                for (int part = 0; part < kOf; ++part) {
+                    uint4 x = b.v[part][j][at];
+                    if (!kUp && kScaled)
+                        x = make_uint4(half2_mul(x.x, f), half2_mul(x.y, f), half2_mul(x.z, f), half2_mul(x.w, f));
+#pragma unroll
+                    for (int m = 0; m < kTiles; ++m) {
+                        // one row tile: two chains of sums, the parts' or so that an instruction waits for the last but one
+                        float(&to)[4] = acc[kUp ? m : kOf == 2 ? part : i % 2][j0 + j];
+                        if constexpr (kMx) {
+                            float d[4];
+                            mma_first<MDT>(d, a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], x.x, x.y);
+                            mma<MDT>(d, a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], x.z, x.w);
+                            to[0] = fmaf(s[m][0][i % 4], d[0], to[0]);
+                            to[1] = fmaf(s[m][0][i % 4], d[1], to[1]);
+                            to[2] = fmaf(s[m][1][i % 4], d[2], to[2]);
+                            to[3] = fmaf(s[m][1][i % 4], d[3], to[3]);
+                        } else {
+                            mma<MDT>(to, a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], x.x, x.y);
+                            mma<MDT>(to, a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], x.z, x.w);
+                        }
                     }
                 }
             }
@@ -941,17 +959,17 @@ struct Layer {
 
     // All nt column tiles of a step: the first kCols, whose operands are b, and (rarely) more, whose
     // operands are loaded here from column(tile) at k0.
-    template <bool kUp, int kGroups, typename Of>
-    __device__ __forceinline__ void multiply_all(int slot, int slab0, int nt, Tokens<kGroups> &b,
+    template <bool kUp, int kGroups, int kOf, typename Of>
+    __device__ __forceinline__ void multiply_all(int slot, int g0, int nt, Tokens<kGroups, kOf> &b,
                                                  const Column (&now)[kCols], const Column (&next)[kCols], int k0, int k1,
                                                  float (&acc)[2][NT][4], Of column) const
     {
         if (kCols == 1 || nt == 1)
-            multiply<kUp, 1, true, kGroups>(slot, slab0, 0, b, now, next, k1, acc);
+            multiply<kUp, 1, true, kGroups>(slot, g0, 0, b, now, next, k1, acc);
         else if (kCols > 2 && nt == 2)
-            multiply<kUp, 2, true, kGroups>(slot, slab0, 0, b, now, next, k1, acc);
+            multiply<kUp, 2, true, kGroups>(slot, g0, 0, b, now, next, k1, acc);
         else
-            multiply<kUp, kCols, true, kGroups>(slot, slab0, 0, b, now, next, k1, acc);
+            multiply<kUp, kCols, true, kGroups>(slot, g0, 0, b, now, next, k1, acc);
 #pragma unroll
         for (int j = kCols; j < NT; j += kCols) {
             if (j >= nt)
@@ -960,8 +978,8 @@ struct Layer {
             for (int c = 0; c < kCols; ++c)
                 if (j + c < nt)
                     more[c] = column(j + c);
-            Tokens<kGroups < 4 ? kGroups : 4> x;
-            multiply<kUp, kCols, false, kGroups>(slot, slab0, j, x, more, more, k0, acc);
+            Tokens<kGroups < 4 / kOf ? kGroups : 4 / kOf, kOf> x;
+            multiply<kUp, kCols, false, kGroups>(slot, g0, j, x, more, more, k0, acc);
         }
     }
 
@@ -998,7 +1016,7 @@ struct Layer {
         Column c;
         const int a = column_of(ai, 8 * tile + g);
         if (a >= 0) {
-            c.v = p.h + (int64_t)a * p.Ip + 8 * t;
+            c.v = p.h + kStored * ((int64_t)a * p.Ip + 8 * t);
             c.tile = p.h_field + (int64_t)a * (p.Ip / 16) + t / 2;
             c.field = field_of(token_of(ai, 8 * tile + g));
         }
@@ -1033,6 +1051,15 @@ struct Layer {
         return v;
     }
 
+    // element i of assignment a's h
+    __device__ __forceinline__ void store_h(int64_t a, int i, float v) const
+    {
+        const int64_t to = kStored * (a * p.Ip + i / 8 * 8) + i % 8;
+        store1<MDT>(p.h, to, v);
+        if (kStored == 2)
+            store1<MDT>(p.h, to + 8, v - value_of<MDT>(v));
+    }
+
     // h of column c of active expert ai, rows i0 + row and i0 + row + 8, from their gate and up sums: the
     // eight lanes that share t hold a column's 16 rows
     __device__ __forceinline__ void finish(const float *weight, int ai, int i0, int c, float g0, float g1, float u0, float u1) const
@@ -1061,14 +1088,18 @@ struct Layer {
             }
         }
         if (a >= 0) {
-            const int64_t to = (int64_t)a * p.Ip + i0 + row;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                store1<MDT>(p.h, to + 8 * b, h[b]);
-                if (!kMany && p.pairs)
-                    store1<MDT>(p.h, p.h_plane + to + 8 * b, h[b] - value_of<MDT>(h[b]));
-            }
+            for (int b = 0; b < 2; ++b)
+                store_h(a, i0 + row + 8 * b, h[b]);
         }
+    }
+
+    // The sum of two chains of one part, or of the parts'.  A first parts' sum that is not finite is all said: an
+    // infinite weight times a second part, which may be 0 or of the other sign, would make it NaN.
+    template <int kOf>
+    static __device__ __forceinline__ float joined(float a, float b)
+    {
+        return kOf == 1 || fabsf(a) <= 3.4e38f ? a + b : a;
     }
 
     // this block's sum for row r of down item `item`, which exists
@@ -1135,9 +1166,7 @@ struct Layer {
         const int end = (p.I + 15) / 16 * 16, pad = p.Ip - end;
         for (int i = threadIdx.x; i < p.k * pad; i += kThreads) {
             const int64_t a = (int64_t)tok * p.k + i / pad;
-            p.h[a * p.Ip + end + i % pad] = 0;
-            if (p.pairs)
-                p.h[p.h_plane + a * p.Ip + end + i % pad] = 0;
+            store_h(a, end + i % pad, 0.f);
             if (i % pad % 16 == 0)
                 p.h_field[a * (p.Ip / 16) + (end + i % pad) / 16] = 253;
         }
@@ -1348,6 +1377,161 @@ struct Layer {
 
     // ------------------------------------------------------------ the two products
 
+    // The down product with up to 8 tokens, whose columns are the tokens; with up to 4 (pairs) columns 4 .. 7 are
+    // the second parts of h, else kOf parts come one after the other.
+    template <int kOf, typename Take>
+    __device__ __forceinline__ void down_few(int &buf, int *s_ok, Take take)
+    {
+        constexpr int kSteps = down_steps(kOf), kGroups = down_groups(kOf);
+        const int token = p.pairs ? g % 4 : g;
+        const uint32_t field = token < p.T ? field_of(token) : 127u;
+        Cursor w;   // where the operands in `b` come from
+        bool some = down_first() < down_items && first_chunk(w);
+        Column c[kCols], c1[kCols];
+        Tokens<kGroups, kOf> b;
+        auto enter = [&](Column &to) {
+            to = Column();
+            const int a = column_of(w.expert, token);
+            if (a >= 0) {
+                to.v = p.h + kStored * ((int64_t)a * p.Ip + 8 * t) + (p.pairs && g >= 4 ? 8 : 0);
+                to.tile = p.h_field + (int64_t)a * (p.Ip / 16) + t / 2;
+            }
+            to.field = field;
+        };
+        if (some) {
+            enter(c1[0]);
+            load_all<false>(b, c1, w.chunk * kDownK);
+        }
+        c[0].field = field;   // all that is still asked of the column whose operands are there
+        // A token that did not choose an expert has zeros for it, which a NaN or an infinity in the expert's
+        // weights would still reach: sums are taken over expert by expert, by the columns that chose it.
+        const int pair_at = p.pairs ? 2 * t % 4 : 2 * t;
+        for (int item = down_first(); item < down_items; item += gridDim.x) {
+            float acc[2][NT][4] = {}, sum[4] = {};
+            auto take_over = [&](int e) {
+                uint32_t who = 0u;   // the two columns' assignments
+                if (p.T > 1)
+                    who = *reinterpret_cast<const uint32_t *>(cols + 8 * e + pair_at);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool chose = i % 2 ? who >> 16 != 0xffffu : (who & 0xffffu) != 0xffffu;
+                    sum[i] += chose ? joined<kOf>(acc[0][0][i], acc[1][0][i]) : 0.f;
+                    acc[0][0][i] = acc[1][0][i] = 0.f;
+                }
+            };
+            for (bool more = some; more;) {
+                const int at = take(), e = w.expert, k0 = w.chunk * kDownK;
+                place_rows(p.w2, act[e] * p.H + item * 16, p.I, 0);
+#pragma unroll
+                for (int u = 0; u + 1 < kSteps; ++u)
+                    multiply_all<false>(at, u * kGroups, 1, b, c, c1, 0, k0 + (u + 1) * kGroups * 32, acc,
+                                        [&](int) { return Column(); });
+                more = next_chunk(w);
+                if (!more)   // the next item starts over
+                    first_chunk(w);
+                if (w.expert != e)
+                    enter(c1[0]);
+                multiply_all<false>(at, (kSteps - 1) * kGroups, 1, b, c, c1, 0, w.chunk * kDownK, acc,
+                                    [&](int) { return Column(); });
+                if (!more || (p.T > 1 && w.expert != e))   // one token chose all that are streamed
+                    take_over(e);
+            }
+            put(red(buf), 0, sum, row);
+            __syncthreads();
+            if (threadIdx.x < 128) {
+                const int r = threadIdx.x % 16, tok = threadIdx.x / 16, n = item * 16 + r;
+                if (tok < p.T && n < p.H) {
+                    float v = gather(red(buf), 0, r, tok);
+                    if (p.pairs)
+                        v = joined<2>(v, gather(red(buf), 0, r, tok + 4));
+                    give(item, tok, r, v);
+                }
+            }
+            if (splits() > 1)
+                add_shares(item, s_ok);
+            buf ^= 1;
+        }
+    }
+
+    // The down product with more tokens: an expert's columns are the tokens that chose it.
+    template <typename Take>
+    __device__ __forceinline__ void down_many(int *s_ok, Take take)
+    {
+        constexpr int kSteps = down_steps(kParts), kGroups = down_groups(kParts);
+        constexpr int kSumPitch = 17;   // [token][16 rows and a pad]
+        float *mine = reinterpret_cast<float *>(smem + p.sm_red) + warp * p.T * kSumPitch;
+        for (int item = down_first(); item < down_items; item += gridDim.x) {
+            for (int i = lane; i < p.T * kSumPitch; i += 32)
+                mine[i] = 0.f;
+            __syncwarp();
+            Cursor w;
+            bool some = first_chunk(w);
+            Column c[kCols], c1[kCols];
+            Tokens<kGroups, kParts> b;
+            auto enter = [&]() {   // the columns of expert w.expert
+#pragma unroll
+                for (int j = 0; j < kCols; ++j)
+                    c1[j] = some && j < tiles_of(w.expert) ? h_column(w.expert, j) : Column();
+            };
+            enter();
+            if (some)
+                load_all<false>(b, c1, w.chunk * kDownK);
+            while (some) {   // one share of an expert's K
+                const int ai = w.expert, tiles = tiles_of(ai);
+                place_rows(p.w2, act[ai] * p.H + item * 16, p.I, 0);
+                float acc[2][NT][4] = {};
+#pragma unroll
+                for (int j = 0; j < kCols; ++j)
+                    c[j] = c1[j];
+                for (bool more = true; more;) {
+                    const int at = take(), k0 = w.chunk * kDownK;
+                    auto column = [&](int j) { return h_column(ai, j); };
+#pragma unroll
+                    for (int u = 0; u + 1 < kSteps; ++u)
+                        multiply_all<false>(at, u * kGroups, tiles, b, c, c1, k0 + u * kGroups * 32,
+                                            k0 + (u + 1) * kGroups * 32, acc, column);
+                    more = ++w.chunk < w.last;
+                    if (!more) {
+                        w.part += down_stride();
+                        some = enter_part(w);
+                        enter();
+                    }
+                    multiply_all<false>(at, (kSteps - 1) * kGroups, tiles, b, c, c1, k0 + (kSteps - 1) * kGroups * 32,
+                                        w.chunk * kDownK, acc, column);
+                }
+                const int first = start[ai], count = start[ai + 1] - first;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    if (j >= tiles)
+                        break;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        if (8 * j + 2 * t + c < count) {
+                            float *to = mine + tokens[first + 8 * j + 2 * t + c] * kSumPitch + row;
+                            to[0] += joined<kParts>(acc[0][j][c], acc[1][j][c]);
+                            to[8] += joined<kParts>(acc[0][j][2 + c], acc[1][j][2 + c]);
+                        }
+                }
+                __syncwarp();   // the next share's columns are other lanes'
+            }
+            __syncthreads();
+            const float *all = reinterpret_cast<const float *>(smem + p.sm_red);
+            for (int i = threadIdx.x; i < 16 * p.T; i += kThreads) {
+                const int r = i % 16, tok = i / 16, n = item * 16 + r;
+                if (n >= p.H)
+                    continue;
+                float v = 0.f;
+#pragma unroll
+                for (int q = 0; q < kWarps; ++q)
+                    v += all[(q * p.T + tok) * kSumPitch + r];
+                give(item, tok, r, v);
+            }
+            if (splits() > 1)
+                add_shares(item, s_ok);
+            __syncthreads();
+        }
+    }
+
     __device__ void run()
     {
         int *s_ok = reinterpret_cast<int *>(smem + p.sm_count) + 1;
@@ -1466,10 +1650,7 @@ struct Layer {
                                 atomicMax(p.h_max + tok, m);
                             }
                         }
-                        const int64_t to = (int64_t)a * p.Ip + i0 + r;
-                        store1<MDT>(p.h, to, h);
-                        if (!kMany && p.pairs)
-                            store1<MDT>(p.h, p.h_plane + to, h - value_of<MDT>(h));
+                        store_h(a, i0 + r, h);
                     }
                 }
                 buf ^= 1;
@@ -1483,147 +1664,12 @@ struct Layer {
         clear_word();
 
         if (!kMany) {
-            const int token = p.pairs ? g % 4 : g;
-            const uint32_t field = token < p.T ? field_of(token) : 127u;
-            Cursor w;   // where the operands in `b` come from
-            bool some = down_first() < down_items && first_chunk(w);
-            Column c[kCols], c1[kCols];
-            Tokens<kDownGroups> b;
-            // up to 4 tokens: columns 4 .. 7 are the second parts of h
-            auto enter = [&](Column &to) {
-                to = Column();
-                const int a = column_of(w.expert, p.pairs ? g % 4 : g);
-                if (a >= 0) {
-                    to.v = p.h + (p.pairs && g >= 4 ? p.h_plane : 0) + (int64_t)a * p.Ip + 8 * t;
-                    to.tile = p.h_field + (int64_t)a * (p.Ip / 16) + t / 2;
-                }
-                to.field = field;
-            };
-            if (some) {
-                enter(c1[0]);
-                load_all<false>(b, c1, w.chunk * kDownK);
-            }
-            c[0].field = field;   // all that is still asked of the column whose operands are there
-            // A token that did not choose an expert has zeros for it, which a NaN or an infinity in the expert's
-            // weights would still reach: sums are taken over expert by expert, by the columns that chose it.
-            const int pair_at = p.pairs ? 2 * t % 4 : 2 * t;
-            for (int item = down_first(); item < down_items; item += gridDim.x) {
-                float acc[2][NT][4] = {}, sum[4] = {};
-                auto take_over = [&](int e) {
-                    uint32_t who = 0u;   // the two columns' assignments
-                    if (p.T > 1)
-                        who = *reinterpret_cast<const uint32_t *>(cols + 8 * e + pair_at);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool chose = i % 2 ? who >> 16 != 0xffffu : (who & 0xffffu) != 0xffffu;
-                        sum[i] += chose ? acc[0][0][i] + acc[1][0][i] : 0.f;
-                        acc[0][0][i] = acc[1][0][i] = 0.f;
-                    }
-                };
-                for (bool more = some; more;) {
-                    const int at = take(), e = w.expert;
-                    place_rows(p.w2, act[e] * p.H + item * 16, p.I, 0);
-                    if (kDownSteps == 2)
-                        multiply_all<false>(at, 0, 1, b, c, c1, 0, w.chunk * kDownK + kDownK / 2, acc,
-                                            [&](int) { return Column(); });
-                    more = next_chunk(w);
-                    if (!more)   // the next item starts over
-                        first_chunk(w);
-                    if (w.expert != e)
-                        enter(c1[0]);
-                    multiply_all<false>(at, kDownSteps - 1, 1, b, c, c1, 0, w.chunk * kDownK, acc,
-                                        [&](int) { return Column(); });
-                    if (!more || (p.T > 1 && w.expert != e))   // one token chose all that are streamed
-                        take_over(e);
-                }
-                put(red(buf), 0, sum, row);
-                __syncthreads();
-                if (threadIdx.x < 128) {
-                    const int r = threadIdx.x % 16, tok = threadIdx.x / 16, n = item * 16 + r;
-                    if (tok < p.T && n < p.H) {
-                        float v = gather(red(buf), 0, r, tok);
-                        // a sum that is not finite is all said: an infinite weight times a second part, which may
-                        // be 0 or of the other sign, would make it NaN
-                        if (p.pairs && fabsf(v) <= 3.4e38f)
-                            v += gather(red(buf), 0, r, tok + 4);
-                        give(item, tok, r, v);
-                    }
-                }
-                if (splits() > 1)
-                    add_shares(item, s_ok);
-                buf ^= 1;
-            }
+            if (kParts == 2 && !p.pairs)
+                down_few<kParts>(buf, s_ok, take);
+            else
+                down_few<1>(buf, s_ok, take);
         } else {
-            constexpr int kSumPitch = 17;   // [token][16 rows and a pad]
-            float *mine = reinterpret_cast<float *>(smem + p.sm_red) + warp * p.T * kSumPitch;
-            for (int item = down_first(); item < down_items; item += gridDim.x) {
-                for (int i = lane; i < p.T * kSumPitch; i += 32)
-                    mine[i] = 0.f;
-                __syncwarp();
-                Cursor w;
-                bool some = first_chunk(w);
-                Column c[kCols], c1[kCols];
-                Tokens<kDownGroups> b;
-                auto enter = [&]() {   // the columns of expert w.expert
-#pragma unroll
-                    for (int j = 0; j < kCols; ++j)
-                        c1[j] = some && j < tiles_of(w.expert) ? h_column(w.expert, j) : Column();
-                };
-                enter();
-                if (some)
-                    load_all<false>(b, c1, w.chunk * kDownK);
-                while (some) {   // one share of an expert's K
-                    const int ai = w.expert, tiles = tiles_of(ai);
-                    place_rows(p.w2, act[ai] * p.H + item * 16, p.I, 0);
-                    float acc[2][NT][4] = {};
-#pragma unroll
-                    for (int j = 0; j < kCols; ++j)
-                        c[j] = c1[j];
-                    for (bool more = true; more;) {
-                        const int at = take(), k0 = w.chunk * kDownK;
-                        auto column = [&](int j) { return h_column(ai, j); };
-                        if (kDownSteps == 2)
-                            multiply_all<false>(at, 0, tiles, b, c, c1, k0, k0 + kDownK / 2, acc, column);
-                        more = ++w.chunk < w.last;
-                        if (!more) {
-                            w.part += down_stride();
-                            some = enter_part(w);
-                            enter();
-                        }
-                        multiply_all<false>(at, kDownSteps - 1, tiles, b, c, c1, k0 + (kDownSteps - 1) * (kDownK / 2),
-                                            w.chunk * kDownK, acc, column);
-                    }
-                    const int first = start[ai], count = start[ai + 1] - first;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        if (j >= tiles)
-                            break;
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            if (8 * j + 2 * t + c < count) {
-                                float *to = mine + tokens[first + 8 * j + 2 * t + c] * kSumPitch + row;
-                                to[0] += acc[0][j][c] + acc[1][j][c];
-                                to[8] += acc[0][j][2 + c] + acc[1][j][2 + c];
-                            }
-                    }
-                    __syncwarp();   // the next share's columns are other lanes'
-                }
-                __syncthreads();
-                const float *all = reinterpret_cast<const float *>(smem + p.sm_red);
-                for (int i = threadIdx.x; i < 16 * p.T; i += kThreads) {
-                    const int r = i % 16, tok = i / 16, n = item * 16 + r;
-                    if (n >= p.H)
-                        continue;
-                    float v = 0.f;
-#pragma unroll
-                    for (int q = 0; q < kWarps; ++q)
-                        v += all[(q * p.T + tok) * kSumPitch + r];
-                    give(item, tok, r, v);
-                }
-                if (splits() > 1)
-                    add_shares(item, s_ok);
-                __syncthreads();
-            }
+            down_many(s_ok, take);
         }
         if (dead && lane == 0)   // every unit was waited for, or given up
             atomicOr(p.status, mrr_ws::kFlagTimeout);

@@ -346,3 +346,31 @@ def test_layer_experts_are_the_oracles(T, E, k, H, I, norm, groups, keep, mx):
     ref, bound = ox.layer(x.double().numpy(), rw, ridx, werr, v13, v2,
                           (H_UNIT if T <= 4 else UNIT)["float16" if mx else "bfloat16"])
     close(y, ref, bound, "bfloat16")
+
+
+# ----------------------------------------------------------------------------- precision between the products
+
+@pytest.mark.parametrize("T,E,k,H,I", [(2, 8, 2, 512, 256), (5, 16, 4, 512, 256), (8, 12, 3, 1030, 90), (9, 16, 4, 512, 320),
+                                       (33, 40, 5, 454, 200), (64, 8, 4, 512, 192), (64, 8, 4, 390, 70), (20, 40, 4, 96, 1040)])
+@pytest.mark.parametrize("dt", ["bfloat16", "float16"])
+@pytest.mark.parametrize("mx", [False, True])
+def test_layer_error_is_that_of_rounding_once(T, E, k, H, I, dt, mx):
+    """y's error against 64 bits is that of rounding the exact y once, whatever h is held in between the
+    products: as two 16-bit parts its error does not show (2^-17 and less), and as one float16 part under a bfloat16 y
+    it adds in squares an eighth of y's own: a factor of (1 + 1/64)^(1/2) = 1.008.  Float32 sums add 2^-20."""
+    import torch
+
+    rng = np.random.default_rng(T + H)
+    f = lambda a: torch.from_numpy(a).to(getattr(torch, dt)).cuda()  # noqa: E731
+    x, wr = f(rng.standard_normal((T, H))), f(rng.standard_normal((E, H)) * H ** -0.5)
+    if mx:
+        (w13, s13, v13), (w2, s2, v2) = weights(rng, E, 2 * I, H), weights(rng, E, H, I)
+        w13, s13, w2, s2 = (up(a) for a in (w13, s13, w2, s2))
+    else:
+        w13, w2 = f(rng.standard_normal((E, 2 * I, H)) * H ** -0.5), f(rng.standard_normal((E, H, I)) * I ** -0.5)
+        s13, s2, v13, v2 = None, None, down(w13), down(w2)
+    y, w, idx = moe.moe_few_token_layer(x, wr, w13, w2, k, w13_scales=s13, w2_scales=s2, norm_type=1,
+                                        return_routing=True, check_status=True)
+    ref, _ = ox.layer(down(x), down(w), idx.cpu().numpy(), np.zeros(T), v13, v2, 0.0)
+    once = torch.from_numpy(ref).to(getattr(torch, dt)).double().numpy()
+    assert np.linalg.norm(down(y) - ref) <= 1.02 * np.linalg.norm(once - ref)
