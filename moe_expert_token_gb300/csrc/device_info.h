@@ -1,5 +1,8 @@
 // What a launch asks of the current device each time, asked of the driver once for each device: the
 // calls behind it cost as much as a small kernel.
+// What is remembered belongs to this copy of the library: functions that hold it in a static variable are
+// static themselves, as the loader would make an inline function's variable one for all copies in a process,
+// and a kernel's attributes are each copy's own.
 #ifndef MRR_DEVICE_INFO_H
 #define MRR_DEVICE_INFO_H
 
@@ -16,7 +19,7 @@ struct Info {
 };
 
 // the current device; false on a CUDA error
-inline bool current(Info &info)
+static inline bool current(Info &info)
 {
     static std::atomic<int64_t> known[kMaxDevices];   // SMs << 32 | bytes, 0: not asked yet
     if (cudaGetDevice(&info.device) != cudaSuccess)

@@ -1685,7 +1685,7 @@ __global__ void __launch_bounds__(32 * warps_of(WDT == MOE_MXFP4, kWide, kRegime
 }
 
 template <int DT, int WDT, int kRegime, bool kSplit>
-cudaError_t launch_one(const Params &p, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s)
+static cudaError_t launch_one(const Params &p, const mrr_device::Info &info, int grid, size_t smem, cudaStream_t s)
 {
     static std::atomic<uint64_t> allowed[2];
     const bool wide = p.w13_wide && p.w2_wide;

@@ -121,7 +121,7 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 
 // a 2-D map of `rows` rows of row_bytes bytes (base and row_bytes multiples of 16), boxes of 128 bytes
 // by box_rows, 128-byte swizzle
-inline bool make_map(CUtensorMap *map, const void *base, int64_t rows, int64_t row_bytes, int box_rows)
+static inline bool make_map(CUtensorMap *map, const void *base, int64_t rows, int64_t row_bytes, int box_rows)
 {
     typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,

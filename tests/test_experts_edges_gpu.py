@@ -374,3 +374,27 @@ def test_layer_error_is_that_of_rounding_once(T, E, k, H, I, dt, mx):
     ref, _ = ox.layer(down(x), down(w), idx.cpu().numpy(), np.zeros(T), v13, v2, 0.0)
     once = torch.from_numpy(ref).to(getattr(torch, dt)).double().numpy()
     assert np.linalg.norm(down(y) - ref) <= 1.02 * np.linalg.norm(once - ref)
+
+
+def test_a_second_copy_of_the_library_runs(tmp_path):
+    import shutil
+
+    import torch
+
+    from moe_expert_token_gb300 import build
+
+    path = str(tmp_path / "copy.so")
+    shutil.copy(build.LIB_PATH, path)
+    libs = [m.load_library(), m.load_library(path)]
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    T, E, H, I, k = 3, 4, 64, 32, 2
+    x, wr, w13, w2 = (torch.randn(*s, generator=gen, device="cuda").bfloat16() for s in ((T, H), (E, H), (E, 2 * I, H), (E, H, I)))
+    ys = []
+    for lib in libs:
+        y, space = torch.empty_like(x), torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+        assert lib.moe_few_token_layer_run(
+            x.data_ptr(), 1, T, H, wr.data_ptr(), E, None, w13.data_ptr(), None, w2.data_ptr(), None, 1, I, k, 1, 1, 1.0,
+            1e-20, 0, 0, y.data_ptr(), None, None, space.data_ptr(), space.numel(), None) == m.MRR_OK
+        torch.cuda.synchronize()
+        ys.append(y)
+    assert torch.equal(*ys)
