@@ -24,7 +24,8 @@
 extern "C" {
 #endif
 
-/* most tokens moe_few_token_layer_run takes; more go through the re-routing op and the grouped product */
+/* most tokens moe_few_token_layer_run takes; more go through the re-routing op and the grouped product where the
+ * weights are MXFP4 (there is no grouped product of 16-bit weights) */
 #define MOE_LAYER_MAX_TOKENS 64
 
 /* Workspace bytes of moe_few_token_layer_run (host only); 0 where a size is out of range. */
@@ -44,7 +45,9 @@ size_t moe_few_token_layer_workspace(int64_t T, int64_t H, int64_t E, int64_t I,
  *                not be initialised; status with mrr_v2_read_status (MRR_ERR_TIMEOUT: a bounded
  *                wait gave up, the outputs are unspecified)
  * Every expert index is in range whatever the logits hold; a token with a NaN logit gets
- * unspecified experts.  A NaN or infinity in x reaches that token's outputs only.
+ * unspecified experts.  A NaN or infinity in x reaches that token's outputs only, and one in an expert's weights
+ * those of the tokens that chose it.  The same inputs give the same bits; a token's last bits may differ with the
+ * tokens beside it, as how sums are shared out depends on how many experts all of them reach.
  * Host errors: MRR_ERR_DTYPE, MRR_ERR_ATTR, MRR_ERR_SHAPE (T outside 0 .. MOE_LAYER_MAX_TOKENS, H
  * or I outside 1 .. 65536 or, with MXFP4 weights, odd; E outside 1 .. 1024; k outside 1 .. min(E,
  * 64); grouping as in mrr_gating_topk_run), MRR_ERR_NULL, MRR_ERR_ALIGN (a pointer not aligned to

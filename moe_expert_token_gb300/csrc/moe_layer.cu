@@ -51,7 +51,8 @@ Layout layout(int64_t T, int64_t H, int64_t E, int64_t I, int64_t k)
     return l;
 }
 
-// 64 bits that no other call of this process has, and that memory holds by chance only
+// 64 bits that no other call of this process has, and that memory holds by chance only: a counter through
+// SplitMix64's steps (Steele, Lea, Flood, "Fast splittable pseudorandom number generators", 2014), less the last
 unsigned long long fresh_tag()
 {
     static std::atomic<unsigned long long> n{

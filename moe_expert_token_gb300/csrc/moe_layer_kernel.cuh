@@ -27,14 +27,15 @@
 //  * Down product: an item is 16 output rows for all tokens; the warps split (expert, K) pairs, and where
 //    there are few items, several blocks do.
 // Measured, with x and the weights from HBM: 1 token, 64 experts of 7168 x 2048 in bfloat16, top 8 (706 MB)
-// 117.5 us, 6.0 TB/s; 48 tokens (5.64 GB) 899 us, 6.3 TB/s; 7 tokens, 60 experts of 2056 x 1400 in float16, top
-// 6 (0.54 GB) 99.5 us, 5.5 TB/s; 4 tokens, 256 MXFP4 experts of 7168 x 2048, top 8 (0.72 GB) 181 us, 4.0 TB/s,
+// 118 us, 6.0 TB/s; 48 tokens (5.64 GB) 928 us, 6.1 TB/s; 7 tokens, 60 experts of 2056 x 1400 in float16, top
+// 6 (0.54 GB) 104 us, 5.2 TB/s; 4 tokens, 256 MXFP4 experts of 7168 x 2048, top 8 (0.72 GB) 182 us, 4.0 TB/s,
 // bound by the instructions that unpack; 1 token, 8 experts of 1024 x 512 (6 MB) 16 us, bound by the
 // latency of three phases that wait for one another.
 // With up to 8 tokens the columns are the tokens themselves and the down product adds up all
 // experts in registers; with more, an expert's columns are the tokens that chose it, and each
-// warp adds them to its own sums in shared memory.  No sum depends on the order of anything but
-// the sizes: results repeat bit for bit.
+// warp adds them to its own sums in shared memory.  The order of every sum goes by the sizes and by how many
+// experts the tokens reach: the same inputs give the same bits, but a token's last bits may differ with the
+// tokens beside it.
 #pragma once
 
 #include <math.h>
@@ -65,9 +66,9 @@ enum Regime { kFew, kSpread, kDense };
 __host__ __device__ constexpr int tiles_for(bool mx, int regime) { return regime == kFew || mx ? 1 : 4; }
 // Warps of a block and stages of a warp's ring.  Unpacking 4-bit weights is bound by how many
 // instructions are ready, so MXFP4 has 12 warps (as many as registers allow) with shorter rings (4 tokens,
-// 256 experts of 7168 x 2048: 181 us, with 8 warps 202); the 16-bit types stream at the memory's rate with 8.
+// 256 experts of 7168 x 2048: 182 us, with 8 warps 201); the 16-bit types stream at the memory's rate with 8.
 // Rows that tiled copies cannot take (narrow) cost instructions too, and have 12 where registers and
-// memory allow (7 tokens, 60 experts of 2055 x 1399: 152 us, with 8 warps 177).
+// memory allow (7 tokens, 60 experts of 2055 x 1399: 151 us, with 8 warps 168).
 __host__ __device__ constexpr int warps_of(bool mx, bool wide, int regime)
 {
     return wide ? (mx ? 12 : 8) : regime == kFew ? 12 : 8;
@@ -450,7 +451,7 @@ struct Cursor {
 
 // kSplit: y has few rows (H up to half of 16 a block), and several blocks share a down item: each writes its
 // sums, and the last to come adds them up, always in the same order.  39 tokens, 248 experts of 556 x 1439 in
-// float16 (35 items): 516 -> 295 us; 13 tokens, 12 experts of 153 x 1455: 49 -> 33; where items are not shared
+// float16 (35 items): 557 -> 304 us; 13 tokens, 12 experts of 153 x 1455: 50 -> 33; where items are not shared
 // the code for it costs up to 5 %, so it is an instance of its own.
 template <int DT, int WDT, int kRegime, bool kWide, bool kSplit>
 struct Layer {
@@ -522,8 +523,8 @@ struct Layer {
         // which needs no join.  Which takes less, in units of a stage's time: the block's share of K and
         // about one for each join, times its items; or all of K, a fifth more for the more scattered
         // reads of the weights, times the warp's items.  48 tokens, 64 experts of 7168 x 2048 in bfloat16:
-        // the block 898 us, warps 970; 39 tokens, 248 experts of 556 x 1439 in float16: 675 and 508; 32
-        // tokens, 64 MXFP4 experts of 7168 x 2048: 412 and 370; 2 tokens, 18 experts of 5015 x 196: 47 and 88.
+        // the block 926 us, warps 1000; 39 tokens, 248 experts of 556 x 1439 in float16: 477 and 300; 32
+        // tokens, 64 MXFP4 experts of 7168 x 2048: 413 and 350; 2 tokens, 18 experts of 5015 x 196: 46 and 88.
         const int blocks = gridDim.x, joins = !kMany ? 1 : min(NT, (p.T * p.k + 8 * nact - 1) / (8 * nact));
         const int joint = (up_items + blocks - 1) / blocks * ((up_units + kWarps - 1) / kWarps + joins);
         const int alone = (up_items + kWarps * blocks - 1) / (kWarps * blocks) * up_units;
@@ -656,7 +657,7 @@ struct Layer {
             // Rows that begin at any byte: the nine aligned 16-byte pieces that hold 128 bytes of each, cut off
             // at the row's end.  Lanes take 8 pieces of 4 rows at a time, the ninth of all 32 rows last.  Bound by
             // the instructions of copies and shifts: 7 tokens, 60 experts of 2055 x 1399 in float16 take
-            // 146 us (2056 x 1400: 98); by 33 aligned words a row 197, by loads of single elements 655.
+            // 151 us (2056 x 1400: 104); by 33 aligned words a row it was 197, by loads of single elements 655.
             const int K = kUp ? p.H : p.I;
             const int64_t bytes = kMx ? K / 2 : 2 * (int64_t)K;
             const uintptr_t all = reinterpret_cast<uintptr_t>(kUp ? p.w13 : p.w2);

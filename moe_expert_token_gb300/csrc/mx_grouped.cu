@@ -19,9 +19,9 @@
 //    it holds up the matrix instructions behind it: 8 copies a step took a third of the kernel's time.
 //  * Neighbouring blocks work on the token tiles of the same weights, which so come from HBM once.
 //
-// Measured, gated, 32 experts of 7168 x 2048: 512 rows 82.6 us, the weights' 499 MB at 6.0 TB/s, bound by HBM;
-// 16384 rows 200 us, 962 GFLOP at 4.8 PFLOP/s, bound by the copies from L2 into shared memory (57 KB a
-// step of 25 MFLOP), the tensor pipe (54 % active) and the results, which are written between tiles.
+// Measured, gated, 32 experts of 7168 x 2048: 512 rows 83 us, the weights' 499 MB at 6.0 TB/s, bound by HBM;
+// 16384 rows 201 us, 962 GFLOP at 4.8 PFLOP/s, bound by the copies from L2 into shared memory (57 KB a
+// step of 25 MFLOP), the tensor pipe (53 % active) and the results, which are written between tiles.
 //
 // Every wait is bounded: one that lasts two seconds sets a flag, all roles leave, copies in flight
 // are waited for, tensor memory is freed, and mrr_v2_read_status reports MRR_ERR_TIMEOUT.
