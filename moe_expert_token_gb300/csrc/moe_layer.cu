@@ -73,8 +73,8 @@ size_t moe_few_token_layer_workspace(int64_t T, int64_t H, int64_t E, int64_t I,
 }
 
 // moe_few_token_layer_run with another limit on its waits; short_of, where not NULL, is a device word that is 0, or 1 +
-// the number of a grid-wide wait that is to expect a block more than there are.  What a test calls to see a wait run
-// out.  Not part of the library's interface.
+// the number of a grid-wide wait that is to expect a block more than there are, or kShortStages, for copies that do
+// not count as landed.  What a test calls to see a wait run out.  Not part of the library's interface.
 mrr_status moe_few_token_layer_run_waits(const void *x, moe_dtype dt, int64_t T, int64_t H, const void *w_router,
                                          int64_t E, const void *bias, const void *w13, const uint8_t *w13_scales,
                                          const void *w2, const uint8_t *w2_scales, moe_dtype w_dt, int64_t I, int64_t k,

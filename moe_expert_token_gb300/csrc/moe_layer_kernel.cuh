@@ -81,6 +81,7 @@ __host__ __device__ constexpr int stage_of(bool wide) { return 2 * 16 * pitch_of
 constexpr int kMaxParts = 16;                    // most shares of H the logits are split into
 constexpr int kMaxSplits = 16;                   // most blocks that share a down item
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr unsigned kShortStages = 4;
 
 struct Params {
     const void *x, *wr, *bias, *w13, *w2;
@@ -95,7 +96,8 @@ struct Params {
     struct Waits *waits;          // see grid_wait
     unsigned long long tag;
     uint64_t wait_ns;             // limit of each wait
-    const unsigned *short_of;     // null, or (tests that let a wait run out) a word: 1 + the grid-wide wait that expects a block more
+    const unsigned *short_of;     // null, or (tests that let a wait run out) a word: 1 + the grid-wide wait that expects a
+                                  // block more, or kShortStages: the stages' barriers expect an arrival more
     float *part;                  // [kparts][T][E]
     uint16_t *xh;                 // [T][Hp]: x's rows as the products take them
     int *route_expert;            // [T][k], with more than 8 tokens
@@ -503,7 +505,8 @@ struct Layer {
         cols = reinterpret_cast<const uint16_t *>(sm + p.sm_cols);
         tokens = sm + p.sm_tokens;
         if (threadIdx.x < kWarps * kStages)   // the tiled copies, or every lane's, and (scales) every lane's
-            mrr::mbar_init(mrr::smem_addr(sm + p.sm_bar) + threadIdx.x * 8, (kWide ? 1 : 32) + (kMx ? 32 : 0));
+            mrr::mbar_init(mrr::smem_addr(sm + p.sm_bar) + threadIdx.x * 8,
+                           (kWide ? 1 : 32) + (kMx ? 32 : 0) + (p.short_of && __ldcg(p.short_of) == kShortStages));
         mrr::mbar_init_fence();
     }
 
@@ -758,8 +761,8 @@ struct Layer {
             advance(c);
     }
 
-    // the stage's copies have landed
-    __device__ __forceinline__ void landed(int slot, uint32_t parity)
+    // the stage's copies have landed, or the warp has given up, and brings no more: `next` is over
+    __device__ __forceinline__ void landed(int slot, uint32_t parity, Cursor &next)
     {
         if (!dead) {
             uint64_t t0 = 0;   // the timer is slow to read: not before a wait has become a long one
@@ -774,8 +777,20 @@ struct Layer {
                     }
                 }
             dead = __any_sync(kFull, dead);
+            if (dead)
+                next.phase = 2;
         }
         __syncwarp();
+    }
+
+    // A warp that has given up leaves no copy in flight: each stage's have a moment to land.  At most one of a
+    // barrier's two phases is not over.
+    __device__ __forceinline__ void settle() const
+    {
+        for (int s = 0; s < kStages; ++s)
+            for (int b = 0; b < 2; ++b)
+                mrr::mbar_wait_bounded(bars + 8 * s, b, 1000000ull);
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
 
     // Narrow rows: by how many bytes what this lane reads of the unit's slabs (rows `row` and `row` + 8, and
@@ -1571,7 +1586,7 @@ struct Layer {
         };
         // take the next stage: its copies have landed, and every lane is done with the one before
         auto take = [&]() {
-            landed(slot, parity);
+            landed(slot, parity, next);
             issue_next();
             --filled;
             const int s = slot;
@@ -1583,10 +1598,12 @@ struct Layer {
         auto drain = [&]() {
             put_held();
             for (; filled > 0; --filled) {
-                landed(slot, parity);
+                landed(slot, parity, next);
                 slot = slot + 1 == kStages ? 0 : slot + 1;
                 parity ^= slot == 0;
             }
+            if (dead)
+                settle();
         };
         for (int s = 0; s < kStages - 1; ++s)
             issue_next();
@@ -1672,8 +1689,11 @@ struct Layer {
         } else {
             down_many(s_ok, take);
         }
-        if (dead && lane == 0)   // every unit was waited for, or given up
-            atomicOr(p.status, mrr_ws::kFlagTimeout);
+        if (dead) {   // every unit was waited for, or given up
+            settle();
+            if (lane == 0)
+                atomicOr(p.status, mrr_ws::kFlagTimeout);
+        }
     }
 };
 

@@ -164,11 +164,11 @@ def test_grouped_wait_that_runs_out_is_reported(short_of, A, N, gated):
     assert torch.equal(y, want)
 
 
-@pytest.mark.parametrize("T,which", [(3, 0), (3, 2), (20, 0), (20, 1), (20, 2)])
+@pytest.mark.parametrize("T,which", [(3, 0), (3, 2), (3, 3), (7, 3), (20, 0), (20, 1), (20, 2), (20, 3)])
 @pytest.mark.parametrize("H,I,mx", [(512, 256, False), (70, 38, False), (512, 256, True), (66, 166, True)])
 def test_layer_wait_that_runs_out_is_reported(T, which, H, I, mx):
-    """A grid-wide wait that expects a block more than there are: the call ends soon, with MRR_ERR_TIMEOUT, and
-    what follows on the same workspace is right: a replay of the same graph, whose first wait goes by the same
+    """A grid-wide wait that expects a block more than there are, or (3) copies whose barriers expect an arrival
+    more: the call ends soon, with MRR_ERR_TIMEOUT, and what follows on the same workspace is right: a replay of the same graph, whose first wait goes by the same
     tag, on other inputs, and a plain call."""
     import torch
 
