@@ -12,6 +12,21 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (GB300, sm_103a)")
 
 
+# Host checks that pass stand-in addresses with arguments that are otherwise valid: without a GPU the call ends
+# in an error, with one it would launch a kernel on memory that is not there.
+NO_GPU_ONLY = {"test_run_without_scales_ignores_scale_pointers"}
+
+
+def pytest_collection_modifyitems(items):
+    chosen = [item for item in items if item.name in NO_GPU_ONLY]
+    if chosen:
+        import torch
+
+        if torch.cuda.is_available():
+            for item in chosen:
+                item.add_marker(pytest.mark.skip(reason="would launch on stand-in addresses"))
+
+
 @pytest.fixture(scope="session")
 def oracle_lib():
     import oracle
