@@ -3,7 +3,10 @@
 The op lives in the CUDA library ``lib/libmrr_v2.so`` (C ABI: include/mrr_v2.h);
 ``moe_expert_token_gb300.mrr_v2`` is its ctypes binding and ``moe_re_routing`` the torch-level
 call.  ``moe_expert_token_gb300.experts`` holds the operators on either side of it (include/moe_mx.h,
-include/moe_layer.h): MXFP4 rows, the experts' products, and a whole layer for a few tokens.  Build the library with ``python -m moe_expert_token_gb300.build``.
+include/moe_layer.h): MXFP4 rows, the experts' products, and a whole layer for a few tokens.
+``moe_expert_token_gb300.tokens`` holds what stands around the experts (include/moe_tokens.h,
+include/moe_norm.h): the norm in front of them, tokens laid out by expert and back, and gradients.
+Build the library with ``python -m moe_expert_token_gb300.build``.
 """
 from .experts import (  # noqa: F401
     moe_few_token_layer,
@@ -36,4 +39,24 @@ from .mrr_v2 import (  # noqa: F401
     mrr_v2_run_plan_multi,
     mrr_v2_unroute,
     mrr_v2_unroute_plan,
+)
+from .tokens import (  # noqa: F401
+    moe_add_rms_norm,
+    moe_add_rms_norm_grad,
+    moe_add_rms_norm_grad_run,
+    moe_add_rms_norm_grad_workspace,
+    moe_add_rms_norm_run,
+    moe_combine_grad_run,
+    moe_combine_run,
+    moe_combine_tokens,
+    moe_combine_tokens_grad,
+    moe_dequantize_rows,
+    moe_dequantize_rows_run,
+    moe_gating_top_k_grad,
+    moe_sort_run,
+    moe_sort_tokens,
+    moe_sort_tokens_grad,
+    moe_sort_workspace,
+    mrr_gating_topk_grad_run,
+    mrr_gating_topk_grad_workspace,
 )

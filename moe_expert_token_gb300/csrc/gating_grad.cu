@@ -1,0 +1,279 @@
+// The gradient of the MoE gating top-k op (include/mrr_gating.h, mrr_gating_topk_grad_run).
+//
+// A warp has a token row, each lane every 32nd expert of it.  The gradient of the scores is dense only where
+// the whole normalised output has one; else it is k numbers, added into a row of zeros in shared memory.  Every
+// element of x is read once and of grad_x written once, with one or two exponentials between: for the usual
+// sizes (16384 rows of 256 in 16 bits, 17 MB) the launch and the latency of a row count for as much as HBM.
+//
+// The gradient of the biases is a sum over rows: lanes hold their experts' sums while the block goes from row to
+// row, each block leaves one row of partial sums, and a second launch adds those in order.
+#include <string.h>
+
+#include "column_sum.cuh"
+#include "mrr_gating.h"
+
+using namespace moe_rows;
+
+static_assert((int)MRR_GATE_F16 == (int)MOE_F16 && (int)MRR_GATE_BF16 == (int)MOE_BF16 && (int)MRR_GATE_F32 == (int)MOE_F32,
+              "one set of type codes");
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kMaxBlocks = 608;
+
+struct Params {
+    const void *grad_y, *x, *bias, *extra_bias;
+    const int32_t *expert_idx;
+    const uint8_t *extra_mask;
+    const float *grad_norm;
+    void *grad_x;
+    float *partial;    // [blocks][2][e], or NULL
+    int64_t T;
+    int e, k, norm_type;
+    float scale, eps;
+};
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// softmax is x's exponential over the row's sum (top: the row's largest); softplus log(1 + exp(x))
+__device__ __forceinline__ float score_of(int norm_type, float x, float top, float sum)
+{
+    if (norm_type == 0)
+        return expf(x - top) / sum;
+    if (norm_type == 1)
+        return sigmoid(x);
+    return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
+}
+
+template <int DT, int VPL>
+__global__ void __launch_bounds__(32 * kWarps) gating_grad(Params p)
+{
+    extern __shared__ float rows[];   // [kWarps][e]
+    mrr::grid_launch_dependents();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    float *ds = rows + warp * p.e;
+    float acc[VPL], extra_acc[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        acc[i] = extra_acc[i] = 0.0f;
+    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < p.T; t += (int64_t)gridDim.x * kWarps) {
+        float x[VPL];
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int at = 32 * i + lane;
+            x[i] = at < p.e ? load1<DT>(p.x, t * p.e + at) : -INFINITY;
+            top = fmaxf(top, x[i]);
+            if (at < p.e)
+                ds[at] = p.grad_norm ? __ldg(p.grad_norm + t * p.e + at) : 0.0f;
+        }
+        float total = 1.0f;
+        if (p.norm_type == 0) {
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2)
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+            total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                total += 32 * i + lane < p.e ? expf(x[i] - top) : 0.0f;
+            total = warp_sum(total);
+        }
+        const bool extra = p.extra_mask && p.extra_bias && p.extra_mask[t] != 0;
+        const void *bias = extra ? p.extra_bias : p.bias;
+        // up to two slots a lane
+        int idx[2];
+        float g[2], s[2], sum = 0.0f, inner = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int j = 32 * h + lane;
+            idx[h] = j < p.k ? __ldg(p.expert_idx + t * p.k + j) : -1;
+            if (idx[h] >= p.e)
+                idx[h] = -1;
+            g[h] = s[h] = 0.0f;
+            if (idx[h] >= 0) {
+                g[h] = load1<DT>(p.grad_y, t * p.k + j);
+                s[h] = score_of(p.norm_type, load1<DT>(p.x, t * p.e + idx[h]), top, total);
+                if (bias)
+                    s[h] += load1<DT>(bias, idx[h]);
+            }
+            sum += s[h];
+            inner = fmaf(g[h], s[h], inner);
+        }
+        sum = warp_sum(sum) + p.eps;
+        inner = warp_sum(inner) / sum;
+        const float factor = p.scale / sum;
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (32 * h >= p.k)
+                break;
+            const float d = factor * (g[h] - inner);
+            const uint32_t same = __match_any_sync(kFull, idx[h]);
+            const bool twice = __any_sync(kFull, idx[h] >= 0 && __popc(same) > 1);
+            if (!twice) {
+                if (idx[h] >= 0)
+                    ds[idx[h]] += d;
+            } else {   // an expert twice in one row (hash routing): one lane after the other
+                for (int l = 0; l < 32; ++l) {
+                    if (l == lane && idx[h] >= 0)
+                        ds[idx[h]] += d;
+                    __syncwarp();
+                }
+            }
+            __syncwarp();
+        }
+        float dot = 0.0f;
+        if (p.norm_type == 0) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const int at = 32 * i + lane;
+                x[i] = at < p.e ? expf(x[i] - top) / total : 0.0f;
+                dot = fmaf(x[i], at < p.e ? ds[at] : 0.0f, dot);
+            }
+            dot = warp_sum(dot);
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int at = 32 * i + lane;
+            if (at >= p.e)
+                continue;
+            const float d = ds[at];
+            float out;
+            if (p.norm_type == 0)
+                out = x[i] * (d - dot);
+            else if (p.norm_type == 1)
+                out = d * (sigmoid(x[i]) * sigmoid(-x[i]));   // 1 - sigmoid(x) = sigmoid(-x), without its cancellation
+            else
+                out = d * sigmoid(x[i]);
+            store1<DT>(p.grad_x, t * p.e + at, out);
+            if (extra)
+                extra_acc[i] += d;
+            else
+                acc[i] += d;
+        }
+        __syncwarp();
+    }
+    if (!p.partial)
+        return;
+    // the warps' sums, in order
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        if (which && !p.extra_mask)
+            break;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (32 * i + lane < p.e)
+                ds[32 * i + lane] = which ? extra_acc[i] : acc[i];
+        __syncthreads();
+        for (int at = threadIdx.x; at < p.e; at += 32 * kWarps) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                s += rows[w * p.e + at];
+            p.partial[((int64_t)blockIdx.x * 2 + which) * p.e + at] = s;
+        }
+    }
+}
+
+int64_t blocks_for(int64_t T)
+{
+    const int64_t blocks = (T + kWarps - 1) / kWarps;
+    return blocks < kMaxBlocks ? blocks : kMaxBlocks;
+}
+
+template <int DT>
+void launch(const Params &p, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)blocks_for(p.T);
+    const int smem = kWarps * p.e * 4, per = (p.e + 31) / 32;
+    auto kernel = per <= 2    ? gating_grad<DT, 2>
+                  : per <= 4  ? gating_grad<DT, 4>
+                  : per <= 8  ? gating_grad<DT, 8>
+                  : per <= 16 ? gating_grad<DT, 16> : gating_grad<DT, 32>;
+    kernel<<<grid, 32 * kWarps, smem, st>>>(p);
+}
+
+bool aligned(const void *p, uintptr_t n) { return (uintptr_t)p % n == 0; }
+
+}  // namespace
+
+extern "C" {
+
+size_t mrr_gating_topk_grad_workspace(int64_t T, int64_t e)
+{
+    if (T < 0 || T > INT32_MAX || e < 1 || e > MRR_GATE_MAX_EXPERTS)
+        return 0;
+    return (size_t)((blocks_for(T) * 2 * e * 4 + 255) / 256 * 256);
+}
+
+mrr_status mrr_gating_topk_grad_run(const void *grad_y, const void *x, mrr_gate_dtype dt, int64_t T, int64_t e,
+                                    int64_t k, const int32_t *expert_idx, const void *bias,
+                                    const void *additional_bias, const uint8_t *additional_token_mask,
+                                    const float *grad_norm_out, float routed_scaling_factor, float eps,
+                                    int64_t norm_type, void *grad_x, void *grad_bias, void *grad_additional_bias,
+                                    void *workspace, size_t workspace_bytes, mrr_stream_t stream)
+{
+    if (dt != MRR_GATE_F16 && dt != MRR_GATE_BF16 && dt != MRR_GATE_F32)
+        return MRR_ERR_DTYPE;
+    if (norm_type < 0 || norm_type > 2)
+        return MRR_ERR_ATTR;
+    if (T < 0 || T > INT32_MAX || e < 1 || e > MRR_GATE_MAX_EXPERTS || k < 1 || k > 64 || k > e)
+        return MRR_ERR_SHAPE;
+    if (T > 0 && (!grad_y || !x || !expert_idx || !grad_x))
+        return MRR_ERR_NULL;
+    const uintptr_t size = dt == MRR_GATE_F32 ? 4 : 2;
+    if (!aligned(grad_y, size) || !aligned(x, size) || !aligned(expert_idx, 4) || !aligned(bias, size) ||
+        !aligned(additional_bias, size) || !aligned(grad_norm_out, 4) || !aligned(grad_x, size) ||
+        !aligned(grad_bias, size) || !aligned(grad_additional_bias, size))
+        return MRR_ERR_ALIGN;
+    const bool sums = grad_bias || grad_additional_bias;
+    if (sums && T > 0 &&
+        (!workspace || !aligned(workspace, 256) || workspace_bytes < mrr_gating_topk_grad_workspace(T, e)))
+        return MRR_ERR_WORKSPACE;
+    // without a mask or an additional bias no row uses one
+    const bool masked = additional_bias && additional_token_mask;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (T > 0) {
+        Params p;
+        memset(&p, 0, sizeof(p));
+        p.grad_y = grad_y;
+        p.x = x;
+        p.bias = bias;
+        p.extra_bias = masked ? additional_bias : nullptr;
+        p.extra_mask = masked ? additional_token_mask : nullptr;
+        p.expert_idx = expert_idx;
+        p.grad_norm = grad_norm_out;
+        p.grad_x = grad_x;
+        p.partial = sums ? static_cast<float *>(workspace) : nullptr;
+        p.T = T;
+        p.e = (int)e;
+        p.k = (int)k;
+        p.norm_type = (int)norm_type;
+        p.scale = routed_scaling_factor;
+        p.eps = eps;
+        if (dt == MRR_GATE_F32)
+            launch<MOE_F32>(p, st);
+        else if (dt == MRR_GATE_BF16)
+            launch<MOE_BF16>(p, st);
+        else
+            launch<MOE_F16>(p, st);
+        if (cudaGetLastError() != cudaSuccess)
+            return MRR_ERR_CUDA;
+    }
+    const int rows = T > 0 ? (int)blocks_for(T) : 0;
+    const float *table = static_cast<const float *>(workspace);
+    if (grad_bias && launch_column_sum(table, rows, 2 * e, (int)e, dt, grad_bias, st) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MRR_ERR_CUDA;
+    }
+    if (grad_additional_bias &&
+        launch_column_sum(table + e, masked ? rows : 0, 2 * e, (int)e, dt, grad_additional_bias, st) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MRR_ERR_CUDA;
+    }
+    return MRR_OK;
+}
+
+}  // extern "C"

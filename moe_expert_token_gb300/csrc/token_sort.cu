@@ -1,0 +1,492 @@
+// Tokens laid out by expert (include/moe_tokens.h): a stable counting sort of the slots by expert,
+// and the move of every token's row to its k places.
+//
+// A slot's row is the number of slots whose (key, slot) is smaller, slots without an expert here
+// having the key E behind all others: their rows are the rows of zeros.  So every row of the output
+// belongs to one slot and is written by the block that has the slot's token, which reads the token
+// once and writes it k times: T (1 + k) rows of traffic, the least there is.  HBM bounds it.
+//
+// Few slots (sort_few): one launch.  Each block looks at all keys and counts the smaller ones for its
+// own slots only.  Many slots: one launch counts each chunk's keys, and in the second each block adds up the
+// table of counts for its place in every expert's rows, ranks its own slots, and moves its rows.
+#include <atomic>
+#include <math.h>
+#include <string.h>
+
+#include "mx.cuh"
+#include "moe_tokens.h"
+#include "ptx.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr uint32_t kNone = 0x80000000u;   // beside a row: the slot has no expert here, the row is zeros
+constexpr int kFewSlots = 4096;
+constexpr int kFewMine = 128;             // most slots of a block of sort_few
+constexpr int kBatch = 1024;              // slots that a block of sort_rows ranks at once
+constexpr int kMaxE = MOE_SORT_MAX_EXPERTS;
+// Blocks of the move: four on each of the 152 SMs.
+constexpr int kGroups = 608;
+
+struct Params {
+    const void *idx;
+    uint64_t first;
+    const uint8_t *x, *scales;
+    const void *weight;
+    uint8_t *out, *out_scales;
+    float *out_weight;
+    int32_t *token_idx, *row_idx;
+    void *num;
+    uint32_t *table;
+    int64_t row_bytes, row_stride, scale_row_bytes;
+    int64_t T;
+    uint32_t n;        // T * k
+    int k, E;
+    int idx64, weight_dt, cumsum, scale_unit;
+    int tokens;        // a block's tokens (the last block's: fewer)
+    int groups;        // blocks along the tokens
+    int parts, chunks; // the table: chunks of `parts` blocks' slots
+};
+
+__device__ __forceinline__ uint32_t key_of(const Params &p, uint32_t slot)
+{
+    const uint64_t v = p.idx64 ? (uint64_t)__ldg(static_cast<const long long *>(p.idx) + slot)
+                               : (uint64_t)(int64_t)__ldg(static_cast<const int *>(p.idx) + slot);
+    const uint64_t d = v - p.first;   // unsigned: anything below `first` is far above E
+    return d < (uint64_t)p.E ? (uint32_t)d : (uint32_t)p.E;
+}
+
+template <int W>
+struct Vec;
+template <>
+struct Vec<16> { using T = uint4; };
+template <>
+struct Vec<8> { using T = uint2; };
+template <>
+struct Vec<4> { using T = uint32_t; };
+template <>
+struct Vec<2> { using T = uint16_t; };
+template <>
+struct Vec<1> { using T = uint8_t; };
+
+template <typename V>
+__device__ __forceinline__ V zero_of()
+{
+    V v;
+    memset(&v, 0, sizeof(v));
+    return v;
+}
+
+// Move tokens first .. first + count - 1 (their slots' rows in `rows`, k for each) : vectors v0 .. v1 - 1 of
+// W bytes of each.  A warp takes kEach vectors a lane of one token, all loaded before the first is stored.
+template <int W>
+__device__ __forceinline__ void move_rows(const Params &p, int64_t first, int count, const uint32_t *rows, int v0, int v1)
+{
+    using V = typename Vec<W>::T;
+    constexpr int kEach = 4;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int segs = (v1 - v0 + 32 * kEach - 1) / (32 * kEach);
+    for (int u = warp; u < count * segs; u += kWarps) {
+        const int t = u / segs, at = v0 + (u - t * segs) * 32 * kEach + lane;
+        const uint32_t *r = rows + t * p.k;
+        bool any = false;
+        for (int j = 0; j < p.k; ++j)
+            any |= !(r[j] & kNone);
+        V v[kEach];
+        const V *from = reinterpret_cast<const V *>(p.x + (first + t) * p.row_stride);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            v[i] = any && at + 32 * i < v1 ? __ldg(from + at + 32 * i) : zero_of<V>();
+        for (int j = 0; j < p.k; ++j) {
+            const uint32_t row = r[j];
+            V *to = reinterpret_cast<V *>(p.out + (int64_t)(row & ~kNone) * p.row_bytes);
+            if (row & kNone) {
+#pragma unroll
+                for (int i = 0; i < kEach; ++i)
+                    if (at + 32 * i < v1)
+                        to[at + 32 * i] = zero_of<V>();
+            } else {
+#pragma unroll
+                for (int i = 0; i < kEach; ++i)
+                    if (at + 32 * i < v1)
+                        to[at + 32 * i] = v[i];
+            }
+        }
+    }
+}
+
+// The slots first .. first + count - 1: their index entries, weights and scales.
+__device__ __forceinline__ void write_slots(const Params &p, uint32_t first, int count, const uint32_t *rows)
+{
+    for (int s = threadIdx.x; s < count; s += kThreads) {
+        const uint32_t slot = first + s, row = rows[s] & ~kNone;
+        const bool none = rows[s] & kNone;
+        p.row_idx[slot] = none ? -1 : (int32_t)row;
+        p.token_idx[row] = none ? -1 : (int32_t)slot;
+        if (p.out_weight) {
+            float w = 0.0f;
+            if (!none)
+                w = p.weight_dt == MOE_F32    ? moe_mx::load1<MOE_F32>(p.weight, slot)
+                    : p.weight_dt == MOE_BF16 ? moe_mx::load1<MOE_BF16>(p.weight, slot)
+                                              : moe_mx::load1<MOE_F16>(p.weight, slot);
+            p.out_weight[row] = w;
+        }
+    }
+    if (!p.out_scales)
+        return;
+    // 4-byte units where rows and both pointers allow it, else bytes
+    const int64_t units = p.scale_row_bytes / p.scale_unit;
+    for (int64_t i = threadIdx.x; i < count * units; i += kThreads) {
+        const int64_t s = i / units, at = i - s * units;
+        const uint32_t row = rows[s];
+        const int64_t from = (int64_t)((first + (uint32_t)s) / (uint32_t)p.k) * units + at;
+        const int64_t to = (int64_t)(row & ~kNone) * units + at;
+        if (p.scale_unit == 4)
+            reinterpret_cast<uint32_t *>(p.out_scales)[to] =
+                row & kNone ? 0u : __ldg(reinterpret_cast<const uint32_t *>(p.scales) + from);
+        else
+            p.out_scales[to] = row & kNone ? (uint8_t)0 : __ldg(p.scales + from);
+    }
+}
+
+__device__ __forceinline__ void store_num(const Params &p, int e, uint32_t v)
+{
+    if (p.idx64)
+        static_cast<long long *>(p.num)[e] = v;
+    else
+        static_cast<int *>(p.num)[e] = (int)v;
+}
+
+// v[0 .. count - 1] to its exclusive prefix, by the whole block
+__device__ __forceinline__ void block_prefix(uint32_t *v, int count)
+{
+    __shared__ uint32_t of_warp[kWarps];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int per = (count + kThreads - 1) / kThreads, lo = threadIdx.x * per, hi = min(count, lo + per);
+    uint32_t sum = 0;
+    for (int i = lo; i < hi; ++i)
+        sum += v[i];
+    uint32_t upto = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const uint32_t o = __shfl_up_sync(kFull, upto, d);
+        upto += lane >= d ? o : 0u;
+    }
+    if (lane == 31)
+        of_warp[warp] = upto;
+    __syncthreads();
+    uint32_t at = upto - sum;
+    for (int w = 0; w < warp; ++w)
+        at += of_warp[w];
+    for (int i = lo; i < hi; ++i) {
+        const uint32_t c = v[i];
+        v[i] = at;
+        at += c;
+    }
+    __syncthreads();
+}
+
+// The share of the row's vectors that this block's y index has.
+__device__ __forceinline__ void my_vectors(int vectors, int &v0, int &v1)
+{
+    const int per = (vectors + gridDim.y - 1) / gridDim.y;
+    v0 = min(vectors, (int)blockIdx.y * per);
+    v1 = min(vectors, v0 + per);
+}
+
+template <int W>
+__global__ void __launch_bounds__(kThreads) sort_few(Params p)
+{
+    // (key, slot) as one number: 13 bits over 12
+    __shared__ __align__(16) uint32_t order[kFewSlots];
+    __shared__ uint32_t rows[kFewMine];
+    if (blockIdx.x == (unsigned)p.groups) {   // one more block: the experts' counts
+        if (blockIdx.y != 0)
+            return;
+        for (int e = threadIdx.x; e < p.E; e += kThreads)
+            order[e] = 0u;
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < p.n; i += kThreads) {
+            const uint32_t key = key_of(p, i);
+            if (key < (uint32_t)p.E)
+                atomicAdd(&order[key], 1u);
+        }
+        __syncthreads();
+        if (!p.cumsum) {
+            for (int e = threadIdx.x; e < p.E; e += kThreads)
+                store_num(p, e, order[e]);
+        } else {
+            // an expert's inclusive prefix is its exclusive one and its count
+            uint32_t own[kMaxE / kThreads];
+            for (int e = threadIdx.x, i = 0; e < p.E; e += kThreads, ++i)
+                own[i] = order[e];
+            __syncthreads();
+            block_prefix(order, p.E);
+            for (int e = threadIdx.x, i = 0; e < p.E; e += kThreads, ++i)
+                store_num(p, e, order[e] + own[i]);
+        }
+        return;
+    }
+    const uint32_t n4 = (p.n + 3) / 4 * 4;
+    for (uint32_t i = threadIdx.x; i < n4; i += kThreads)
+        order[i] = i < p.n ? key_of(p, i) << 12 | i : 0xffffffffu;
+    __syncthreads();
+    const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+    const int tokens = (int)min((int64_t)p.tokens, p.T - t0), mine = tokens * p.k;
+    const uint32_t s0 = (uint32_t)t0 * p.k;
+    const int lane = threadIdx.x % 32;
+    for (int s = threadIdx.x / 32; s < mine; s += kWarps) {
+        const uint32_t own = order[s0 + s];
+        uint32_t smaller = 0;
+        for (uint32_t i = 4 * lane; i < n4; i += 128) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(order + i);
+            smaller += (o.x < own) + (o.y < own) + (o.z < own) + (o.w < own);
+        }
+        smaller = __reduce_add_sync(kFull, smaller);
+        if (lane == 0)
+            rows[s] = smaller | (own >> 12 == (uint32_t)p.E ? kNone : 0u);
+    }
+    __syncthreads();
+    if (blockIdx.y == 0)
+        write_slots(p, s0, mine, rows);
+    if (p.out) {
+        int v0, v1;
+        my_vectors((int)(p.row_bytes / W), v0, v1);
+        move_rows<W>(p, t0, tokens, rows, v0, v1);
+    }
+}
+
+// table[c][e] = how often key e (E: none) occurs among chunk c's slots
+__global__ void __launch_bounds__(1024) sort_count(Params p)
+{
+    mrr::grid_launch_dependents();
+    __shared__ uint32_t count[kMaxE + 1];
+    for (int e = threadIdx.x; e <= p.E; e += 1024)
+        count[e] = 0u;
+    __syncthreads();
+    const uint64_t per = (uint64_t)p.parts * p.tokens * p.k;
+    const uint64_t lo = blockIdx.x * per, hi = min((uint64_t)p.n, lo + per);
+    for (uint64_t i = lo + threadIdx.x; i < hi; i += 1024)
+        atomicAdd(&count[key_of(p, (uint32_t)i)], 1u);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= p.E; e += 1024)
+        p.table[(size_t)blockIdx.x * (p.E + 1) + e] = count[e];
+}
+
+template <int W>
+__global__ void __launch_bounds__(kThreads) sort_rows(Params p)
+{
+    __shared__ uint32_t base[kMaxE + 2];   // of each key: all its slots, then the row of this block's next one
+    __shared__ uint32_t before[kMaxE + 1]; // of each key: its slots ahead of this block's
+    __shared__ uint32_t rows[kBatch];
+    const int lane = threadIdx.x % 32;
+    const int chunk = blockIdx.x / p.parts;
+    for (int e = threadIdx.x; e <= p.E; e += kThreads)
+        before[e] = 0u;
+    __syncthreads();
+    // slots of this chunk ahead of this block's
+    const uint64_t each = (uint64_t)p.tokens * p.k;
+    for (uint64_t i = chunk * p.parts * each + threadIdx.x; i < blockIdx.x * each; i += kThreads)
+        atomicAdd(&before[key_of(p, (uint32_t)i)], 1u);
+    __syncthreads();
+    mrr::grid_dependency_wait();   // the table is the previous launch's
+    for (int e = threadIdx.x; e <= p.E; e += kThreads) {
+        uint32_t all = 0, ahead = 0;
+#pragma unroll 8
+        for (int c = 0; c < p.chunks; ++c) {
+            const uint32_t v = p.table[(size_t)c * (p.E + 1) + e];
+            all += v;
+            ahead += c < chunk ? v : 0u;
+        }
+        base[e] = all;
+        before[e] += ahead;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && !p.cumsum) {
+        for (int e = threadIdx.x; e < p.E; e += kThreads)
+            store_num(p, e, base[e]);
+        __syncthreads();
+    }
+    block_prefix(base, p.E + 1);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && p.cumsum)
+        for (int e = threadIdx.x; e < p.E; e += kThreads)
+            store_num(p, e, base[e + 1]);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= p.E; e += kThreads)
+        base[e] += before[e];
+
+    int v0 = 0, v1 = 0;
+    if (p.out)
+        my_vectors((int)(p.row_bytes / W), v0, v1);
+    const int64_t t_end = min(p.T, (int64_t)(blockIdx.x + 1) * p.tokens);
+    const int per = kBatch / p.k;   // tokens ranked at once
+    for (int64_t t0 = (int64_t)blockIdx.x * p.tokens; t0 < t_end; t0 += per) {
+        const int tokens = (int)min((int64_t)per, t_end - t0), mine = tokens * p.k;
+        const uint32_t s0 = (uint32_t)(t0 * p.k);
+        __syncthreads();   // the batch before has been moved
+        for (int s = threadIdx.x; s < mine; s += kThreads)
+            rows[s] = key_of(p, s0 + s);
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            // 32 slots at a time, in order: slots of one key follow each other in lane order
+            for (int s = lane; s < mine + lane; s += 32) {
+                const uint32_t key = s < mine ? rows[s] : (uint32_t)p.E + 1;
+                const uint32_t same = __match_any_sync(kFull, key);
+                const uint32_t at = base[key];
+                __syncwarp();
+                if (s < mine)
+                    rows[s] = (at + __popc(same & ((1u << lane) - 1))) | (key == (uint32_t)p.E ? kNone : 0u);
+                if (lane == __ffs(same) - 1)
+                    base[key] = at + __popc(same);
+                __syncwarp();
+            }
+        }
+        __syncthreads();
+        if (blockIdx.y == 0)
+            write_slots(p, s0, mine, rows);
+        if (p.out)
+            move_rows<W>(p, t0, tokens, rows, v0, v1);
+    }
+}
+
+// How the work is cut, from the sizes alone (the workspace's size follows from it).  Each block of the move
+// reads chunks * (E + 1) counts and up to parts * tokens * k keys; the two are about equal where
+// parts^2 = groups (E + 1) / (tokens k).
+void cut(int64_t T, int64_t k, int64_t E, int64_t &tokens, int64_t &groups, int64_t &parts, int64_t &chunks)
+{
+    tokens = (T + kGroups - 1) / kGroups;
+    groups = (T + tokens - 1) / tokens;
+    parts = (int64_t)sqrt((double)groups * (double)(E + 1) / (double)(tokens * k));
+    parts = parts < 1 ? 1 : parts > groups ? groups : parts;
+    chunks = (groups + parts - 1) / parts;
+}
+
+bool sizes_ok(int64_t T, int64_t k, int64_t E)
+{
+    return T >= 0 && T <= INT32_MAX && k >= 1 && k <= MOE_SORT_MAX_K && E >= 1 && E <= kMaxE && T * k <= INT32_MAX;
+}
+
+template <int W>
+cudaError_t launch(const Params &p, bool few, cudaStream_t st)
+{
+    // where tokens are few, several blocks share a token's row, 1 KB each at least
+    const int64_t most = (p.row_bytes + 1023) / 1024, want = kGroups / p.groups;
+    const unsigned splits = (unsigned)(want < 1 || !p.out ? 1 : want < most ? want : most);
+    if (few) {
+        sort_few<W><<<dim3(p.groups + 1, splits), kThreads, 0, st>>>(p);
+        return cudaGetLastError();
+    }
+    sort_count<<<p.chunks, 1024, 0, st>>>(p);
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(p.groups, splits);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, sort_rows<W>, p);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+bool aligned(const void *p, uintptr_t n) { return (uintptr_t)p % n == 0; }
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_sort_workspace(int64_t T, int64_t k, int64_t E)
+{
+    if (!sizes_ok(T, k, E) || T * k <= kFewSlots)
+        return 0;
+    int64_t tokens, groups, parts, chunks;
+    cut(T, k, E, tokens, groups, parts, chunks);
+    return (size_t)((4 * chunks * (E + 1) + 255) / 256 * 256);
+}
+
+mrr_status moe_sort_run(const void *expert_idx, int idx_is_i64, int64_t T, int64_t k, int64_t first_expert, int64_t E,
+                        const void *x, int64_t row_bytes, int64_t row_stride, const void *scales,
+                        int64_t scale_row_bytes, const void *weight, moe_dtype weight_dt, void *sorted_x,
+                        void *sorted_scales, float *sorted_weight, int32_t *token_idx, int32_t *row_idx,
+                        void *expert_num, int64_t expert_num_type, void *workspace, size_t workspace_bytes,
+                        mrr_stream_t stream)
+{
+    if (weight && weight_dt != MOE_F16 && weight_dt != MOE_BF16 && weight_dt != MOE_F32)
+        return MRR_ERR_DTYPE;
+    if (expert_num_type != 0 && expert_num_type != 1)
+        return MRR_ERR_ATTR;
+    if (!sizes_ok(T, k, E) || row_bytes < 0 || row_bytes > (1 << 24) || row_stride < row_bytes ||
+        (scales && (scale_row_bytes < 1 || scale_row_bytes > (1 << 20))))
+        return MRR_ERR_SHAPE;
+    if (!expert_num || (T > 0 && (!expert_idx || !token_idx || !row_idx || (row_bytes > 0 && (!x || !sorted_x)) ||
+                                  (scales && !sorted_scales) || (weight && !sorted_weight))))
+        return MRR_ERR_NULL;
+    const uintptr_t idx_bytes = idx_is_i64 ? 8 : 4;
+    if (!aligned(expert_idx, idx_bytes) || !aligned(expert_num, idx_bytes) || !aligned(token_idx, 4) ||
+        !aligned(row_idx, 4) || (weight && (!aligned(weight, weight_dt == MOE_F32 ? 4 : 2) || !aligned(sorted_weight, 4))))
+        return MRR_ERR_ALIGN;
+    if (moe_sort_workspace(T, k, E) > 0 &&
+        (!workspace || !aligned(workspace, 256) || workspace_bytes < moe_sort_workspace(T, k, E)))
+        return MRR_ERR_WORKSPACE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        if (cudaMemsetAsync(expert_num, 0, idx_bytes * (size_t)E, st) == cudaSuccess)
+            return MRR_OK;
+        (void)cudaGetLastError();
+        return MRR_ERR_CUDA;
+    }
+    int64_t tokens, groups, parts, chunks;
+    cut(T, k, E, tokens, groups, parts, chunks);
+    Params p;
+    memset(&p, 0, sizeof(p));
+    p.idx = expert_idx;
+    p.first = (uint64_t)first_expert;
+    p.x = static_cast<const uint8_t *>(x);
+    p.out = row_bytes > 0 ? static_cast<uint8_t *>(sorted_x) : nullptr;
+    p.row_bytes = row_bytes;
+    p.row_stride = row_stride;
+    if (scales) {
+        p.scales = static_cast<const uint8_t *>(scales);
+        p.out_scales = static_cast<uint8_t *>(sorted_scales);
+        p.scale_row_bytes = scale_row_bytes;
+        p.scale_unit = scale_row_bytes % 4 == 0 && aligned(scales, 4) && aligned(sorted_scales, 4) ? 4 : 1;
+    }
+    if (weight) {
+        p.weight = weight;
+        p.weight_dt = weight_dt;
+        p.out_weight = sorted_weight;
+    }
+    p.token_idx = token_idx;
+    p.row_idx = row_idx;
+    p.num = expert_num;
+    p.table = static_cast<uint32_t *>(workspace);
+    p.T = T;
+    p.n = (uint32_t)(T * k);
+    p.k = (int)k;
+    p.E = (int)E;
+    p.idx64 = idx_is_i64 != 0;
+    p.cumsum = expert_num_type == 0;
+    p.tokens = (int)tokens;
+    p.groups = (int)groups;
+    p.parts = (int)parts;
+    p.chunks = (int)chunks;
+    const bool few = T * k <= kFewSlots;
+    // widest vectors that rows, stride and pointers are multiples of
+    const uintptr_t all = p.out ? (uintptr_t)x | (uintptr_t)sorted_x | (uintptr_t)row_bytes | (T > 1 ? (uintptr_t)row_stride : 0)
+                                : 0;
+    const cudaError_t err = all % 16 == 0  ? launch<16>(p, few, st)
+                            : all % 8 == 0 ? launch<8>(p, few, st)
+                            : all % 4 == 0 ? launch<4>(p, few, st)
+                            : all % 2 == 0 ? launch<2>(p, few, st)
+                                           : launch<1>(p, few, st);
+    if (err == cudaSuccess)
+        return MRR_OK;
+    (void)cudaGetLastError();
+    return MRR_ERR_CUDA;
+}
+
+}  // extern "C"

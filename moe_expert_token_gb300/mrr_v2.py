@@ -154,6 +154,28 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_few_token_layer_run.argtypes = [P, I32, I64, I64, P, I64, P, P, P, P, P, I32, I64, I64, I64, I64,
                                             ctypes.c_float, ctypes.c_float, I64, I64, P, P, P, P,
                                             ctypes.c_size_t, P]
+    lib.moe_sort_workspace.restype = ctypes.c_size_t
+    lib.moe_sort_workspace.argtypes = [I64, I64, I64]
+    lib.moe_sort_run.restype = I32
+    lib.moe_sort_run.argtypes = [P, I32, I64, I64, I64, I64, P, I64, I64, P, I64, P, I32, P, P, P, P, P, P, I64, P,
+                                 ctypes.c_size_t, P]
+    lib.moe_combine_run.restype = I32
+    lib.moe_combine_run.argtypes = [P, I32, I64, I64, P, I64, I64, P, I32, P, P]
+    lib.moe_combine_grad_run.restype = I32
+    lib.moe_combine_grad_run.argtypes = [P, P, I32, I64, I64, P, P, I64, I64, P, I32, P, P, P]
+    lib.moe_add_rms_norm_run.restype = I32
+    lib.moe_add_rms_norm_run.argtypes = [P, P, I32, I64, I64, I64, I64, P, I32, ctypes.c_float, P, P, I32, P, P, P]
+    lib.moe_add_rms_norm_grad_workspace.restype = ctypes.c_size_t
+    lib.moe_add_rms_norm_grad_workspace.argtypes = [I64, I64]
+    lib.moe_add_rms_norm_grad_run.restype = I32
+    lib.moe_add_rms_norm_grad_run.argtypes = [P, P, P, I32, I64, I64, P, I32, ctypes.c_float, P, P, P, ctypes.c_size_t, P]
+    lib.moe_dequantize_rows_run.restype = I32
+    lib.moe_dequantize_rows_run.argtypes = [P, P, I32, I64, I64, I32, P, P]
+    lib.mrr_gating_topk_grad_workspace.restype = ctypes.c_size_t
+    lib.mrr_gating_topk_grad_workspace.argtypes = [I64, I64]
+    lib.mrr_gating_topk_grad_run.restype = I32
+    lib.mrr_gating_topk_grad_run.argtypes = [P, P, I32, I64, I64, I64, P, P, P, P, P, ctypes.c_float, ctypes.c_float, I64,
+                                             P, P, P, P, ctypes.c_size_t, P]
     if path == _build.LIB_PATH:
         _lib = lib
     return lib
