@@ -20,12 +20,14 @@ SOURCES = [os.path.join(CSRC, f) for f in ("gating_f16.cu", "gating_bf16.cu", "g
                                             "mrr_v2_noalloc.cu", "mrr_push.cu", "gating.cu", "mx_quantize.cu", "mx_grouped.cu",
                                             "moe_layer.cu", "moe_layer_bf16.cu", "moe_layer_f16.cu",
                                             "moe_layer_bf16_split.cu", "moe_layer_f16_split.cu", "token_sort.cu",
-                                            "token_combine.cu", "rms_norm.cu", "rms_norm_grad.cu", "gating_grad.cu")]
+                                            "token_combine.cu", "rms_norm.cu", "rms_norm_f16.cu", "rms_norm_bf16.cu",
+                                            "rms_norm_f32.cu", "gating_grad.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "gating_kernel.cuh"),
                   os.path.join(CSRC, "ws_layout.h"), os.path.join(CSRC, "mrr_shape.h"),
                   os.path.join(CSRC, "mx.cuh"), os.path.join(CSRC, "tc.cuh"),
                   os.path.join(CSRC, "device_info.h"), os.path.join(CSRC, "moe_layer_kernel.cuh"), os.path.join(INCLUDE, "moe_mx.h"),
-                  os.path.join(CSRC, "rows.cuh"), os.path.join(CSRC, "column_sum.cuh"),
+                  os.path.join(CSRC, "rows.cuh"), os.path.join(CSRC, "column_sum.cuh"), os.path.join(CSRC, "rms_norm.h"),
+                  os.path.join(CSRC, "rms_norm_kernel.cuh"), os.path.join(CSRC, "rms_norm_grad_kernel.cuh"),
                   os.path.join(INCLUDE, "moe_layer.h"), os.path.join(INCLUDE, "moe_tokens.h"), os.path.join(INCLUDE, "moe_norm.h"),
                   os.path.join(INCLUDE, "mrr_v2.h"), os.path.join(INCLUDE, "mrr_gating.h")]
 LIB_DIR = os.path.join(PKG, "lib")

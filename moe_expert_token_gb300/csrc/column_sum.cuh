@@ -7,9 +7,9 @@
 
 namespace moe_rows {
 
-constexpr int kSumColumns = 32, kSumWarps = 8;
+constexpr int kSumColumns = 32, kSumWarps = 32;
 
-// out[c] in dt = sum over rows r < rows of table[r * pitch + c], c < columns; a warp adds every eighth row.  Launched
+// out[c] in dt = sum over rows r < rows of table[r * pitch + c], c < columns; a warp adds every 32nd row.  Launched
 // as the programmatic successor of the kernel that writes the table.
 static __global__ void __launch_bounds__(kSumColumns * kSumWarps) column_sum(const float *table, int rows, int64_t pitch,
                                                                              int columns, int dt, void *out)

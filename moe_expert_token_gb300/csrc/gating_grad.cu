@@ -1,15 +1,20 @@
 // The gradient of the MoE gating top-k op (include/mrr_gating.h, mrr_gating_topk_grad_run).
 //
-// A warp has a token row, each lane every 32nd expert of it.  The gradient of the scores is dense only where
-// the whole normalised output has one; else it is k numbers, added into a row of zeros in shared memory.  Every
-// element of x is read once and of grad_x written once, with one or two exponentials between: for the usual
-// sizes (16384 rows of 256 in 16 bits, 17 MB) the launch and the latency of a row count for as much as HBM.
+// Scores that stand alone (sigmoid, softplus) without a gradient of the normalised output: grad_x is zero but for
+// the k chosen experts (gating_grad_chosen).  A group of lanes has a token, a lane a chosen expert, so several tokens share
+// a warp; x is read where it is needed, and the row of zeros is written ahead of the k values.  Else every
+// element of x has a share (gating_grad_dense): a warp has a token, each lane every 32nd expert, and the chosen
+// experts' shares are added into a row in shared memory.  Each element is read or written once with one or
+// two exponentials between: for the usual sizes (16384 rows of 256 in 16 bits, 8 to 17 MB) launches and the latency of a
+// row count for as much as HBM.
 //
-// The gradient of the biases is a sum over rows: lanes hold their experts' sums while the block goes from row to
-// row, each block leaves one row of partial sums, and a second launch adds those in order.
+// The gradient of the biases is a sum over rows: warps hold sums of their own while the block goes from row to row,
+// each block leaves one row of partial sums, and a second launch adds those in order.
+#include <atomic>
 #include <string.h>
 
 #include "column_sum.cuh"
+#include "device_info.h"
 #include "mrr_gating.h"
 
 using namespace moe_rows;
@@ -20,7 +25,7 @@ static_assert((int)MRR_GATE_F16 == (int)MOE_F16 && (int)MRR_GATE_BF16 == (int)MO
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kMaxBlocks = 608;
+constexpr int kMaxBlocks = 304;   // two on each of the 152 SMs
 
 struct Params {
     const void *grad_y, *x, *bias, *extra_bias;
@@ -36,6 +41,15 @@ struct Params {
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
+// d score / d x of a score that stands alone: s (1 - s), without the cancellation of 1 - s, or the sigmoid
+__device__ __forceinline__ float slope_of(int norm_type, float x)
+{
+    if (norm_type == 2)
+        return sigmoid(x);
+    const float z = expf(-fabsf(x)), n = 1.0f + z;
+    return z / (n * n);
+}
+
 // softmax is x's exponential over the row's sum (top: the row's largest); softplus log(1 + exp(x))
 __device__ __forceinline__ float score_of(int norm_type, float x, float top, float sum)
 {
@@ -46,8 +60,145 @@ __device__ __forceinline__ float score_of(int norm_type, float x, float top, flo
     return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
 }
 
+// grad_x [first, first + count) to zero, by one warp: 16 bytes at a time where they are aligned
+template <int DT>
+__device__ __forceinline__ void clear_rows(void *grad_x, int64_t first, int64_t count, int lane)
+{
+    constexpr int kElem = DT == MOE_F32 ? 4 : 2;
+    uint8_t *lo = static_cast<uint8_t *>(grad_x) + first * kElem, *hi = lo + count * kElem;
+    uint8_t *from = reinterpret_cast<uint8_t *>(((uintptr_t)lo + 15) / 16 * 16);
+    uint8_t *to = reinterpret_cast<uint8_t *>((uintptr_t)hi / 16 * 16);
+    if (from >= to)
+        from = to = hi;
+    for (uint8_t *q = lo + kElem * lane; q < from; q += 32 * kElem)
+        store1<DT>(q, 0, 0.0f);
+    for (uint8_t *q = from + 16 * lane; q < to; q += 32 * 16)
+        *reinterpret_cast<uint4 *>(q) = make_uint4(0u, 0u, 0u, 0u);
+    for (uint8_t *q = to + kElem * lane; q < hi; q += 32 * kElem)
+        store1<DT>(q, 0, 0.0f);
+}
+
+// LANES lanes a token (k <= LANES; 32 lanes: two slots each).  sums: [2][e] of each warp, where bias gradients are asked for.
+template <int DT, int LANES>
+__global__ void __launch_bounds__(32 * kWarps) gating_grad_chosen(Params p)
+{
+    extern __shared__ float sums[];
+    mrr::grid_launch_dependents();
+    constexpr int kSlots = LANES == 32 ? 2 : 1, kTokens = 32 / LANES;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, of_warp = lane / LANES, at = lane % LANES;
+    const int kinds = p.extra_mask ? 2 : 1;
+    float *mine = sums + warp * kinds * p.e;
+    if (p.partial) {
+        for (int i = lane; i < kinds * p.e; i += 32)
+            mine[i] = 0.0f;
+        __syncwarp();
+    }
+    for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTokens; t0 < p.T; t0 += (int64_t)gridDim.x * kWarps * kTokens) {
+        const int64_t t = t0 + of_warp;
+        const bool here = t < p.T;
+        const bool extra = here && p.extra_mask && p.extra_mask[t] != 0;
+        const void *bias = extra ? p.extra_bias : p.bias;
+        int idx[kSlots];
+        float g[kSlots], x[kSlots], d[kSlots], sum = 0.0f, inner = 0.0f;
+#pragma unroll
+        for (int h = 0; h < kSlots; ++h) {
+            const int j = LANES * h + at;
+            const bool in = here && j < p.k;
+            idx[h] = in ? __ldg(p.expert_idx + t * p.k + j) : -1;
+            g[h] = in ? load1<DT>(p.grad_y, t * p.k + j) : 0.0f;
+            if (idx[h] < 0 || idx[h] >= p.e)
+                idx[h] = -1, g[h] = 0.0f;
+        }
+#pragma unroll
+        for (int h = 0; h < kSlots; ++h) {
+            x[h] = idx[h] >= 0 ? load1<DT>(p.x, t * p.e + idx[h]) : 0.0f;
+            float s = 0.0f;
+            if (idx[h] >= 0)
+                s = score_of(p.norm_type, x[h], 0.0f, 1.0f) + (bias ? load1<DT>(bias, idx[h]) : 0.0f);
+            sum += s;
+            inner = fmaf(g[h], s, inner);
+        }
+        clear_rows<DT>(p.grad_x, t0 * p.e, min((int64_t)kTokens, p.T - t0) * p.e, lane);
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o /= 2) {
+            sum += __shfl_xor_sync(kFull, sum, o);
+            inner += __shfl_xor_sync(kFull, inner, o);
+        }
+        sum += p.eps;
+        const float factor = p.scale / sum;
+        inner /= sum;
+#pragma unroll
+        for (int h = 0; h < kSlots; ++h)
+            d[h] = factor * (g[h] - inner);
+        // an expert that a token has twice (hash routing): its first slot gets the sum, in the order of the slots
+        bool twice = false;
+#pragma unroll
+        for (int h = 0; h < kSlots; ++h) {
+            const uint32_t group = LANES == 32 ? kFull : ((1u << LANES) - 1) << (of_warp * LANES);
+            const uint32_t same = __match_any_sync(kFull, idx[h]) & group;
+            twice |= idx[h] >= 0 && __popc(same) > 1;
+            if (kSlots == 2 && h == 1)
+                twice = twice || p.k > 32;   // the two halves are not compared here
+        }
+        if (__any_sync(kFull, twice)) {
+            float all[kSlots];
+            bool first[kSlots];
+#pragma unroll
+            for (int h = 0; h < kSlots; ++h)
+                all[h] = 0.0f, first[h] = true;
+#pragma unroll
+            for (int o = 0; o < kSlots; ++o)
+                for (int l = 0; l < LANES; ++l) {
+                    const int other = __shfl_sync(kFull, idx[o], of_warp * LANES + l);
+                    const float share = __shfl_sync(kFull, d[o], of_warp * LANES + l);
+#pragma unroll
+                    for (int h = 0; h < kSlots; ++h)
+                        if (other == idx[h]) {
+                            all[h] += share;
+                            if (LANES * o + l < LANES * h + at)
+                                first[h] = false;
+                        }
+                }
+#pragma unroll
+            for (int h = 0; h < kSlots; ++h) {
+                d[h] = all[h];
+                if (!first[h])
+                    idx[h] = -1;
+            }
+        }
+        __syncwarp();   // the zeros are written
+#pragma unroll
+        for (int h = 0; h < kSlots; ++h)
+            if (idx[h] >= 0)
+                store1<DT>(p.grad_x, t * p.e + idx[h], d[h] * slope_of(p.norm_type, x[h]));
+        if (p.partial) {
+            // one token after the other: two of them may have the same expert
+#pragma unroll
+            for (int w = 0; w < kTokens; ++w) {
+                if (w == of_warp) {
+#pragma unroll
+                    for (int h = 0; h < kSlots; ++h)
+                        if (idx[h] >= 0)
+                            mine[(extra ? p.e : 0) + idx[h]] += d[h];
+                }
+                __syncwarp();
+            }
+        }
+    }
+    if (!p.partial)
+        return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kinds * p.e; i += 32 * kWarps) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            s += sums[w * kinds * p.e + i];
+        p.partial[(int64_t)blockIdx.x * 2 * p.e + i] = s;
+    }
+}
+
 template <int DT, int VPL>
-__global__ void __launch_bounds__(32 * kWarps) gating_grad(Params p)
+__global__ void __launch_bounds__(32 * kWarps) gating_grad_dense(Params p)
 {
     extern __shared__ float rows[];   // [kWarps][e]
     mrr::grid_launch_dependents();
@@ -75,8 +226,10 @@ __global__ void __launch_bounds__(32 * kWarps) gating_grad(Params p)
                 top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
             total = 0.0f;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                total += 32 * i + lane < p.e ? expf(x[i] - top) : 0.0f;
+            for (int i = 0; i < VPL; ++i) {
+                x[i] = 32 * i + lane < p.e ? expf(x[i] - top) : 0.0f;   // the scores, but for their sum
+                total += x[i];
+            }
             total = warp_sum(total);
         }
         const bool extra = p.extra_mask && p.extra_bias && p.extra_mask[t] != 0;
@@ -128,7 +281,7 @@ __global__ void __launch_bounds__(32 * kWarps) gating_grad(Params p)
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
                 const int at = 32 * i + lane;
-                x[i] = at < p.e ? expf(x[i] - top) / total : 0.0f;
+                x[i] /= total;
                 dot = fmaf(x[i], at < p.e ? ds[at] : 0.0f, dot);
             }
             dot = warp_sum(dot);
@@ -142,10 +295,8 @@ __global__ void __launch_bounds__(32 * kWarps) gating_grad(Params p)
             float out;
             if (p.norm_type == 0)
                 out = x[i] * (d - dot);
-            else if (p.norm_type == 1)
-                out = d * (sigmoid(x[i]) * sigmoid(-x[i]));   // 1 - sigmoid(x) = sigmoid(-x), without its cancellation
             else
-                out = d * sigmoid(x[i]);
+                out = d * slope_of(p.norm_type, x[i]);
             store1<DT>(p.grad_x, t * p.e + at, out);
             if (extra)
                 extra_acc[i] += d;
@@ -183,16 +334,33 @@ int64_t blocks_for(int64_t T)
     return blocks < kMaxBlocks ? blocks : kMaxBlocks;
 }
 
-template <int DT>
-void launch(const Params &p, cudaStream_t st)
+template <int DT, int LANES>
+cudaError_t launch_chosen(const Params &p, cudaStream_t st)
 {
-    const unsigned grid = (unsigned)blocks_for(p.T);
+    static std::atomic<uint64_t> done;
+    mrr_device::Info info;
+    if (!mrr_device::current(info))
+        return cudaErrorUnknown;
+    const int smem = p.partial ? kWarps * (p.extra_mask ? 2 : 1) * p.e * 4 : 0;   // up to 64 KB
+    const cudaError_t err = mrr_device::allow_smem(gating_grad_chosen<DT, LANES>, info, done);
+    if (err != cudaSuccess)
+        return err;
+    gating_grad_chosen<DT, LANES><<<(unsigned)blocks_for(p.T), 32 * kWarps, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int DT>
+cudaError_t launch(const Params &p, cudaStream_t st)
+{
+    if (p.norm_type != 0 && !p.grad_norm)
+        return p.k <= 8 ? launch_chosen<DT, 8>(p, st) : p.k <= 16 ? launch_chosen<DT, 16>(p, st) : launch_chosen<DT, 32>(p, st);
     const int smem = kWarps * p.e * 4, per = (p.e + 31) / 32;
-    auto kernel = per <= 2    ? gating_grad<DT, 2>
-                  : per <= 4  ? gating_grad<DT, 4>
-                  : per <= 8  ? gating_grad<DT, 8>
-                  : per <= 16 ? gating_grad<DT, 16> : gating_grad<DT, 32>;
-    kernel<<<grid, 32 * kWarps, smem, st>>>(p);
+    auto kernel = per <= 2    ? gating_grad_dense<DT, 2>
+                  : per <= 4  ? gating_grad_dense<DT, 4>
+                  : per <= 8  ? gating_grad_dense<DT, 8>
+                  : per <= 16 ? gating_grad_dense<DT, 16> : gating_grad_dense<DT, 32>;
+    kernel<<<(unsigned)blocks_for(p.T), 32 * kWarps, smem, st>>>(p);
+    return cudaGetLastError();
 }
 
 bool aligned(const void *p, uintptr_t n) { return (uintptr_t)p % n == 0; }
@@ -253,14 +421,13 @@ mrr_status mrr_gating_topk_grad_run(const void *grad_y, const void *x, mrr_gate_
         p.norm_type = (int)norm_type;
         p.scale = routed_scaling_factor;
         p.eps = eps;
-        if (dt == MRR_GATE_F32)
-            launch<MOE_F32>(p, st);
-        else if (dt == MRR_GATE_BF16)
-            launch<MOE_BF16>(p, st);
-        else
-            launch<MOE_F16>(p, st);
-        if (cudaGetLastError() != cudaSuccess)
+        const cudaError_t err = dt == MRR_GATE_F32    ? launch<MOE_F32>(p, st)
+                                : dt == MRR_GATE_BF16 ? launch<MOE_BF16>(p, st)
+                                                      : launch<MOE_F16>(p, st);
+        if (err != cudaSuccess) {
+            (void)cudaGetLastError();
             return MRR_ERR_CUDA;
+        }
     }
     const int rows = T > 0 ? (int)blocks_for(T) : 0;
     const float *table = static_cast<const float *>(workspace);

@@ -1,275 +1,15 @@
-// A residual's addition, the root-mean-square norm of the sum with its 8-bit and MXFP4 forms, and rows of 8 bits
-// back to values (include/moe_norm.h).
-//
-// h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight: every element is read and written once and a
-// handful of operations are made of it, so HBM bounds both.  A row stays in registers, 8 elements a
-// chunk, between the sum of its squares and the results: it belongs to one block (or, where it is short,
-// to one warp).
+// Host entry points of the norm and its gradient, and rows of 8 bits back to values (include/moe_norm.h).  The norm's
+// kernels are in rms_norm_kernel.cuh and rms_norm_grad_kernel.cuh.
 #include <string.h>
 
-#include "moe_norm.h"
+#include "column_sum.cuh"
+#include "rms_norm.h"
 #include "rows.cuh"
 
 using namespace moe_rows;
+using namespace moe_norm;
 
 namespace {
-
-constexpr int kMaxWarps = 32;
-
-struct Params {
-    const void *x, *residual, *weight;
-    void *h, *y, *q, *scales;
-    int64_t T, x_stride, residual_stride;   // in elements
-    int H, weight_f32, quant, q_wide;       // q_wide: a chunk's codes are stored at once
-    float eps;
-};
-
-// The sum or maximum of v over the row's threads: a warp's, or with kBlock all warps'; each thread gets it.
-template <bool kBlock>
-__device__ __forceinline__ float row_sum(float v, float *of_warp)
-{
-    v = warp_sum(v);
-    if (kBlock) {
-        if (threadIdx.x % 32 == 0)
-            of_warp[threadIdx.x / 32] = v;
-        __syncthreads();
-        v = 0.0f;
-        for (int w = 0; w < blockDim.x / 32; ++w)
-            v += of_warp[w];
-    }
-    return v;
-}
-
-template <bool kBlock>
-__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *of_warp)
-{
-    v = __reduce_max_sync(kFull, v);
-    if (kBlock) {
-        if (threadIdx.x % 32 == 0)
-            of_warp[threadIdx.x / 32] = v;
-        __syncthreads();
-        v = 0u;
-        for (int w = 0; w < blockDim.x / 32; ++w)
-            v = max(v, of_warp[w]);
-    }
-    return v;
-}
-
-// the float32 scale of magnitudes up to the float with bits m, for codes up to `top`, and its reciprocal
-__device__ __forceinline__ float float_scale(uint32_t m, float top, float &inverse)
-{
-    if (m >= 0x7f800000u) {
-        inverse = 0.0f;
-        return __uint_as_float(0x7fffffffu);
-    }
-    const float s = fmaxf(__uint_as_float(m) / top, 0x1p-126f);
-    inverse = 1.0f / s;
-    return s;
-}
-
-__device__ __forceinline__ uint32_t int8_of(float v) { return (uint32_t)min(127, max(-127, __float2int_rn(v))) & 0xffu; }
-
-// codes of a chunk (elements c .. c + n - 1 of row `row`), from their values over the scale
-__device__ __forceinline__ void store_bytes(const Params &p, int64_t row, int c, int n, uint32_t lo, uint32_t hi)
-{
-    uint8_t *to = static_cast<uint8_t *>(p.q) + row * p.H + c;
-    if (n >= 8 && p.q_wide) {
-        *reinterpret_cast<uint2 *>(to) = make_uint2(lo, hi);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n)
-                to[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i % 4)));
-    }
-}
-
-__device__ __forceinline__ uint32_t largest(const float (&v)[8])
-{
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    return m;
-}
-
-// y's chunks of one row to codes and scales.  A block of 32 elements is 4 lanes' chunks, one of 128 elements 16 lanes'.
-template <int NV, bool kBlock>
-__device__ __forceinline__ void quantize(const Params &p, int64_t row, int tid, int threads, const float (&y)[NV][8],
-                                         uint32_t *of_warp)
-{
-    const int kind = p.quant;
-    if (kind == MOE_Q_INT8 || kind == MOE_Q_E4M3) {
-        uint32_t m = 0u;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            m = max(m, largest(y[i]));
-        m = row_max<kBlock>(m, of_warp);
-        float inverse;
-        const float s = float_scale(m, kind == MOE_Q_INT8 ? 127.0f : 448.0f, inverse);
-        if (tid == 0)
-            static_cast<float *>(p.scales)[row] = s;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = 8 * (tid + i * threads), n = p.H - c;
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = y[i][j] * inverse;
-            if (n <= 0)
-                continue;
-            if (kind == MOE_Q_INT8)
-                store_bytes(p, row, c, n, int8_of(v[0]) | int8_of(v[1]) << 8 | int8_of(v[2]) << 16 | int8_of(v[3]) << 24,
-                            int8_of(v[4]) | int8_of(v[5]) << 8 | int8_of(v[6]) << 16 | int8_of(v[7]) << 24);
-            else
-                store_bytes(p, row, c, n, encode_e4m3(v[0], v[1], v[2], v[3]), encode_e4m3(v[4], v[5], v[6], v[7]));
-        }
-        return;
-    }
-    const int blocks = (p.H + 31) / 32;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (tid + i * threads), n = p.H - c;
-        uint32_t m = largest(y[i]);
-        m = max(m, __shfl_xor_sync(kFull, m, 1));
-        m = max(m, __shfl_xor_sync(kFull, m, 2));
-        float inverse;
-        if (kind == MOE_Q_E4M3_128) {
-            m = max(m, __shfl_xor_sync(kFull, m, 4));
-            m = max(m, __shfl_xor_sync(kFull, m, 8));
-            const float s = float_scale(m, 448.0f, inverse);
-            if (c % 128 == 0 && n > 0)
-                static_cast<float *>(p.scales)[row * ((p.H + 127) / 128) + c / 128] = s;
-        } else {
-            // the exponent field of m is floor(log2 m) + 127; 8 (e4m3) or 2 (e2m1) less is the scale's byte
-            const uint32_t less = kind == MOE_Q_MXFP8 ? 8u : 2u, field = m >> 23;
-            const uint32_t b = field == 255u ? 255u : field > less ? field - less : 0u;
-            inverse = __uint_as_float((254u - min(b, 252u)) << 23);
-            if (c % 32 == 0 && n > 0) {
-                uint8_t *to = static_cast<uint8_t *>(p.scales) + row * ((p.H + 63) / 64 * 2) + c / 32;
-                to[0] = (uint8_t)b;
-                if (c / 32 == blocks - 1 && blocks % 2)
-                    to[1] = 127u;
-            }
-        }
-        if (n <= 0)
-            continue;
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = y[i][j] * inverse;
-        if (kind == MOE_Q_MXFP4) {
-            const uint32_t w = encode8(v);
-            uint8_t *to = static_cast<uint8_t *>(p.q) + (row * p.H + c) / 2;
-            if (n >= 8 && p.q_wide) {
-                *reinterpret_cast<uint32_t *>(to) = w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (2 * j < n)
-                        to[j] = (uint8_t)(w >> (8 * j));
-            }
-        } else {
-            store_bytes(p, row, c, n, encode_e4m3(v[0], v[1], v[2], v[3]), encode_e4m3(v[4], v[5], v[6], v[7]));
-        }
-    }
-}
-
-// NV chunks a thread; kBlock: a block has a row, else each of its warps has one.
-template <int DT, int W, int NV, bool kBlock>
-__global__ void __launch_bounds__(kBlock ? 1024 : 256) add_rms_norm(Params p)
-{
-    __shared__ float sums[kMaxWarps];
-    __shared__ uint32_t tops[kMaxWarps];
-    const int threads = kBlock ? blockDim.x : 32, tid = kBlock ? threadIdx.x : threadIdx.x % 32;
-    const int64_t row = kBlock ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
-    if (row >= p.T)
-        return;
-    constexpr int kElem = DT == MOE_F32 ? 4 : 2;
-    const uint8_t *x = static_cast<const uint8_t *>(p.x) + row * p.x_stride * kElem;
-    const uint8_t *res = static_cast<const uint8_t *>(p.residual) + row * p.residual_stride * kElem;
-    float v[NV][8];
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (tid + i * threads);
-        load8<DT, W>(x, c, p.H - c, v[i]);
-    }
-    if (p.residual) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = 8 * (tid + i * threads);
-            float r[8];
-            load8<DT, W>(res, c, p.H - c, r);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[i][j] += r[j];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (tid + i * threads);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            sum = fmaf(v[i][j], v[i][j], sum);
-        if (p.h)
-            store8<DT, W>(static_cast<uint8_t *>(p.h) + row * p.H * kElem, c, p.H - c, v[i]);
-    }
-    sum = row_sum<kBlock>(sum, sums);
-    const float r = 1.0f / sqrtf(sum / (float)p.H + p.eps);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (tid + i * threads);
-        float w[8];
-        if (p.weight_f32)
-            load8<MOE_F32, W == 2 ? 4 : W>(p.weight, c, p.H - c, w);
-        else
-            load8<DT, W>(p.weight, c, p.H - c, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[i][j] = v[i][j] * r * w[j];
-        if (p.y)
-            store8<DT, W>(static_cast<uint8_t *>(p.y) + row * p.H * kElem, c, p.H - c, v[i]);
-    }
-    if (p.quant != MOE_Q_NONE)
-        quantize<NV, kBlock>(p, row, tid, threads, v, tops);
-}
-
-template <int DT, int W>
-void launch(const Params &p, cudaStream_t st)
-{
-    const int chunks = (p.H + 7) / 8;
-    // Short rows: a warp each.
-    if (chunks <= 128) {
-        const unsigned grid = (unsigned)((p.T + 7) / 8);
-        if (chunks <= 32)
-            add_rms_norm<DT, W, 1, false><<<grid, 256, 0, st>>>(p);
-        else
-            add_rms_norm<DT, W, 4, false><<<grid, 256, 0, st>>>(p);
-        return;
-    }
-    // Few rows: as many threads to a row as there are chunks.  Many: four chunks a thread.
-    auto threads = [&](int each) { return (unsigned)(((chunks + each - 1) / each + 31) / 32 * 32); };
-    const unsigned grid = (unsigned)p.T;
-    if (p.T <= 304 && chunks <= 1024)
-        add_rms_norm<DT, W, 1, true><<<grid, threads(1), 0, st>>>(p);
-    else if (chunks <= 4096)
-        add_rms_norm<DT, W, 4, true><<<grid, threads(4), 0, st>>>(p);
-    else
-        add_rms_norm<DT, W, 8, true><<<grid, threads(8), 0, st>>>(p);
-}
-
-template <int DT>
-void launch(const Params &p, uintptr_t all, cudaStream_t st)
-{
-    if (all % 16 == 0)
-        launch<DT, 16>(p, st);
-    else if (all % 8 == 0)
-        launch<DT, 8>(p, st);
-    else if (all % 4 == 0 || DT == MOE_F32)
-        launch<DT, 4>(p, st);
-    else
-        launch<DT, DT == MOE_F32 ? 4 : 2>(p, st);
-}
 
 // Rows of 8 bits back to values: a thread has 8 elements of one row.
 template <int DT>
@@ -308,18 +48,27 @@ __global__ void __launch_bounds__(256) dequantize(const uint8_t *q, const void *
     }
     constexpr int kElem = DT == MOE_F32 ? 4 : 2;
     uint8_t *to = static_cast<uint8_t *>(x) + row * H * kElem;
-    if (wide)
-        store8<DT, 16>(to, c, 8, v);
-    else
-        store8<DT, kElem>(to, c, n == 8 ? 8 : n, v);
+    if (wide) {
+        Chunk<DT, 16> out;
+        out.set(v);
+        out.store(to, c * kElem, H * kElem);
+    } else {
+        Chunk<DT, kElem> out;
+        out.set(v);
+        out.store(to, c * kElem, H * kElem);
+    }
 }
 
 bool aligned(const void *p, uintptr_t n) { return (uintptr_t)p % n == 0; }
 uintptr_t size_of(int dt) { return dt == MOE_F32 ? 4 : 2; }
 bool is_float(int dt) { return dt == MOE_F16 || dt == MOE_BF16 || dt == MOE_F32; }
-mrr_status done()
+
+mrr_status done(cudaError_t err)
 {
-    return cudaGetLastError() == cudaSuccess ? MRR_OK : MRR_ERR_CUDA;
+    if (err == cudaSuccess)
+        return MRR_OK;
+    (void)cudaGetLastError();
+    return MRR_ERR_CUDA;
 }
 
 }  // namespace
@@ -364,20 +113,14 @@ mrr_status moe_add_rms_norm_run(const void *x, const void *residual, moe_dtype d
     p.quant = quant;
     p.q_wide = quant == MOE_Q_MXFP4 ? H % 8 == 0 && aligned(q, 4) : H % 8 == 0 && aligned(q, 8);
     p.eps = eps;
-    // what every row's first element is aligned to
-    uintptr_t all = (uintptr_t)x | (uintptr_t)weight | (uintptr_t)h | (uintptr_t)y;
+    // pieces that every row begins with and consists of
+    uintptr_t all = (uintptr_t)x | (uintptr_t)weight | (uintptr_t)h | (uintptr_t)y | (uintptr_t)H * size;
     if (T > 1)
-        all |= (uintptr_t)x_stride * size | (h || y ? (uintptr_t)H * size : 0);
+        all |= (uintptr_t)x_stride * size | (residual ? (uintptr_t)residual_stride * size : 0);
     if (residual)
-        all |= (uintptr_t)residual | (T > 1 ? (uintptr_t)residual_stride * size : 0);
+        all |= (uintptr_t)residual;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (dt == MOE_F32)
-        launch<MOE_F32>(p, all, st);
-    else if (dt == MOE_BF16)
-        launch<MOE_BF16>(p, all, st);
-    else
-        launch<MOE_F16>(p, all, st);
-    return done();
+    return done(dt == MOE_F32 ? norm_f32(p, all, st) : dt == MOE_BF16 ? norm_bf16(p, all, st) : norm_f16(p, all, st));
 }
 
 mrr_status moe_dequantize_rows_run(const void *q, const void *scales, moe_quant quant, int64_t T, int64_t H,
@@ -401,7 +144,68 @@ mrr_status moe_dequantize_rows_run(const void *q, const void *scales, moe_quant 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     auto kernel = dt == MOE_F32 ? dequantize<MOE_F32> : dt == MOE_BF16 ? dequantize<MOE_BF16> : dequantize<MOE_F16>;
     kernel<<<grid, 256, 0, st>>>(static_cast<const uint8_t *>(q), scales, quant, T, (int)H, (int)chunks, wide, x);
-    return done();
+    return done(cudaGetLastError());
+}
+
+size_t moe_add_rms_norm_grad_workspace(int64_t T, int64_t H)
+{
+    if (T < 0 || T > INT32_MAX || H < 1 || H > MOE_NORM_MAX_H)
+        return 0;
+    return (size_t)((grad_blocks(T, H) * H * 4 + 255) / 256 * 256);
+}
+
+mrr_status moe_add_rms_norm_grad_run(const void *grad_y, const void *h, const void *grad_h, moe_dtype dt, int64_t T,
+                                     int64_t H, const void *weight, moe_dtype weight_dt, float eps, void *grad_x,
+                                     void *grad_weight, void *workspace, size_t workspace_bytes, mrr_stream_t stream)
+{
+    if (!is_float(dt) || (weight_dt != dt && weight_dt != MOE_F32))
+        return MRR_ERR_DTYPE;
+    if (!(eps >= 0.0f))
+        return MRR_ERR_ATTR;
+    if (T < 0 || T > INT32_MAX || H < 1 || H > MOE_NORM_MAX_H)
+        return MRR_ERR_SHAPE;
+    if (!weight || (T > 0 && (!grad_y || !h || !grad_x)))
+        return MRR_ERR_NULL;
+    const uintptr_t size = size_of(dt);
+    if (!aligned(grad_y, size) || !aligned(h, size) || !aligned(grad_h, size) || !aligned(grad_x, size) ||
+        !aligned(weight, size_of(weight_dt)) || !aligned(grad_weight, size_of(weight_dt)))
+        return MRR_ERR_ALIGN;
+    if (grad_weight && T > 0 &&
+        (!workspace || !aligned(workspace, 256) || workspace_bytes < moe_add_rms_norm_grad_workspace(T, H)))
+        return MRR_ERR_WORKSPACE;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (T > 0) {
+        GradParams p;
+        memset(&p, 0, sizeof(p));
+        p.grad_y = grad_y;
+        p.h = h;
+        p.grad_h = grad_h;
+        p.weight = weight;
+        p.grad_x = grad_x;
+        p.partial = grad_weight ? static_cast<float *>(workspace) : nullptr;
+        p.T = T;
+        p.H = (int)H;
+        p.weight_f32 = weight_dt == MOE_F32;
+        p.eps = eps;
+        const uintptr_t all = (uintptr_t)grad_y | (uintptr_t)h | (uintptr_t)grad_h | (uintptr_t)grad_x |
+                              (uintptr_t)weight | (uintptr_t)H * size;
+        mrr_device::Info info;
+        cudaError_t err = cudaErrorUnknown;
+        if (mrr_device::current(info))
+            err = dt == MOE_F32    ? norm_grad_f32(p, all, info, st)
+                  : dt == MOE_BF16 ? norm_grad_bf16(p, all, info, st)
+                                   : norm_grad_f16(p, all, info, st);
+        if (err != cudaSuccess) {
+            (void)cudaGetLastError();
+            return MRR_ERR_CUDA;
+        }
+    }
+    if (grad_weight && launch_column_sum(static_cast<const float *>(workspace), T > 0 ? (int)grad_blocks(T, H) : 0, H,
+                                         (int)H, weight_dt, grad_weight, st) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return MRR_ERR_CUDA;
+    }
+    return MRR_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,46 @@
+// The norm's kernels as its host entry points see them: one translation unit for each element type.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "device_info.h"
+#include "moe_norm.h"
+
+namespace moe_norm {
+
+struct Params {
+    const void *x, *residual, *weight;
+    void *h, *y, *q, *scales;
+    int64_t T, x_stride, residual_stride;   // in elements
+    int H, weight_f32, quant, q_wide;       // q_wide: a chunk's codes are stored at once
+    float eps;
+};
+
+struct GradParams {
+    const void *grad_y, *h, *grad_h, *weight;
+    void *grad_x;
+    float *partial;        // [blocks][H], or NULL
+    int64_t T;
+    int H, weight_f32;
+    float eps;
+};
+
+constexpr int kMaxBlocks = 304;   // of the gradient: two on each of the 152 SMs
+constexpr int kShortWarps = 8;    // its blocks' rows at once where a warp has a row
+
+inline int64_t grad_blocks(int64_t T, int64_t H)
+{
+    const int64_t rows = H <= 1024 ? kShortWarps : 1, blocks = (T + rows - 1) / rows;
+    return blocks < kMaxBlocks ? blocks : kMaxBlocks;
+}
+
+// `all`: the pieces that rows come in, in its lowest bits (every address, stride and size or-ed together)
+cudaError_t norm_f16(const Params &p, uintptr_t all, cudaStream_t st);
+cudaError_t norm_bf16(const Params &p, uintptr_t all, cudaStream_t st);
+cudaError_t norm_f32(const Params &p, uintptr_t all, cudaStream_t st);
+cudaError_t norm_grad_f16(const GradParams &p, uintptr_t all, const mrr_device::Info &info, cudaStream_t st);
+cudaError_t norm_grad_bf16(const GradParams &p, uintptr_t all, const mrr_device::Info &info, cudaStream_t st);
+cudaError_t norm_grad_f32(const GradParams &p, uintptr_t all, const mrr_device::Info &info, cudaStream_t st);
+
+}  // namespace moe_norm

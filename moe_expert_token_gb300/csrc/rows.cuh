@@ -9,37 +9,60 @@ using namespace moe_mx;
 
 constexpr uint32_t kFull = 0xffffffffu;
 
-// Elements c .. c + n - 1 of a row of DT whose elements c (a multiple of 8) lie at addresses aligned to W bytes,
-// as floats; zeros for the others of the 8 (n may be 0 or less, or above 8).
+// Eight consecutive elements of DT as they lie in a row whose bytes, from its start, come in pieces of W (the row's
+// size is a multiple of W, its address aligned to W).  Pieces past the row's end are zeros and are not stored.  A piece
+// is loaded under a predicate of its own and without a branch: several chunks' loads are under way at once.
 template <int DT, int W>
-__device__ __forceinline__ void load8(const void *row, int c, int n, float (&v)[8])
-{
-    constexpr int kElem = DT == MOE_F32 ? 4 : 2, kWords = 2 * kElem;
-    const uint8_t *p = static_cast<const uint8_t *>(row) + (int64_t)c * kElem;
-    if (n >= 8) {
-        uint32_t w[kWords];
-        if constexpr (W == 16) {
+struct Chunk {
+    static constexpr int kElem = DT == MOE_F32 ? 4 : 2, kBytes = 8 * kElem, kWords = kBytes / 4;
+    uint32_t w[kWords];
+
+    // bytes at .. at + kBytes - 1 of a row of `size` bytes
+    __device__ __forceinline__ void load(const void *row, int at, int size)
+    {
+        const uint8_t *p = static_cast<const uint8_t *>(row) + at;
 #pragma unroll
-            for (int i = 0; i < kWords; i += 4) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p + 4 * i));
-                w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
+        for (int i = 0; i < kBytes; i += W) {
+            const bool in = at + i < size;
+            if constexpr (W == 16) {
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                if (in)
+                    q = __ldg(reinterpret_cast<const uint4 *>(p + i));
+                w[i / 4] = q.x, w[i / 4 + 1] = q.y, w[i / 4 + 2] = q.z, w[i / 4 + 3] = q.w;
+            } else if constexpr (W == 8) {
+                uint2 q = make_uint2(0u, 0u);
+                if (in)
+                    q = __ldg(reinterpret_cast<const uint2 *>(p + i));
+                w[i / 4] = q.x, w[i / 4 + 1] = q.y;
+            } else if constexpr (W == 4) {
+                w[i / 4] = in ? __ldg(reinterpret_cast<const uint32_t *>(p + i)) : 0u;
+            } else {
+                const uint32_t half = in ? __ldg(reinterpret_cast<const uint16_t *>(p + i)) : 0u;
+                w[i / 4] = i % 4 == 0 ? half : w[i / 4] | half << 16;
             }
-        } else if constexpr (W == 8) {
-#pragma unroll
-            for (int i = 0; i < kWords; i += 2) {
-                const uint2 q = __ldg(reinterpret_cast<const uint2 *>(p + 4 * i));
-                w[i] = q.x, w[i + 1] = q.y;
-            }
-        } else if constexpr (W == 4) {
-#pragma unroll
-            for (int i = 0; i < kWords; ++i)
-                w[i] = __ldg(reinterpret_cast<const uint32_t *>(p + 4 * i));
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords; ++i)
-                w[i] = __ldg(reinterpret_cast<const uint16_t *>(p + 4 * i)) |
-                       (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(p + 4 * i) + 1) << 16;
         }
+    }
+
+    __device__ __forceinline__ void store(void *row, int at, int size) const
+    {
+        uint8_t *p = static_cast<uint8_t *>(row) + at;
+#pragma unroll
+        for (int i = 0; i < kBytes; i += W) {
+            if (at + i >= size)
+                continue;
+            if constexpr (W == 16)
+                *reinterpret_cast<uint4 *>(p + i) = make_uint4(w[i / 4], w[i / 4 + 1], w[i / 4 + 2], w[i / 4 + 3]);
+            else if constexpr (W == 8)
+                *reinterpret_cast<uint2 *>(p + i) = make_uint2(w[i / 4], w[i / 4 + 1]);
+            else if constexpr (W == 4)
+                *reinterpret_cast<uint32_t *>(p + i) = w[i / 4];
+            else
+                *reinterpret_cast<uint16_t *>(p + i) = (uint16_t)(w[i / 4] >> (i % 4 * 8));
+        }
+    }
+
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if constexpr (DT == MOE_F32) {
@@ -48,45 +71,31 @@ __device__ __forceinline__ void load8(const void *row, int c, int n, float (&v)[
                 const float2 f = unpack2<DT>(w[i / 2]);
                 v[i] = i % 2 ? f.y : f.x;
             }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = i < n ? load1<DT>(row, c + i) : 0.0f;
     }
-}
 
-template <int DT, int W>
-__device__ __forceinline__ void store8(void *row, int c, int n, const float (&v)[8])
-{
-    constexpr int kElem = DT == MOE_F32 ? 4 : 2, kWords = 2 * kElem;
-    uint8_t *p = static_cast<uint8_t *>(row) + (int64_t)c * kElem;
-    if (n >= 8) {
-        uint32_t w[kWords];
+    __device__ __forceinline__ void set(const float (&v)[8])
+    {
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
             if constexpr (DT == MOE_F32)
                 w[i] = __float_as_uint(v[i]);
             else
                 w[i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
-#pragma unroll
-        for (int i = 0; i < kWords; ++i)
-            if constexpr (W == 16) {
-                if (i % 4 == 0)
-                    *reinterpret_cast<uint4 *>(p + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-            } else if constexpr (W == 8) {
-                if (i % 2 == 0)
-                    *reinterpret_cast<uint2 *>(p + 4 * i) = make_uint2(w[i], w[i + 1]);
-            } else if constexpr (W == 4) {
-                *reinterpret_cast<uint32_t *>(p + 4 * i) = w[i];
-            } else {
-                reinterpret_cast<uint16_t *>(p + 4 * i)[0] = (uint16_t)w[i];
-                reinterpret_cast<uint16_t *>(p + 4 * i)[1] = (uint16_t)(w[i] >> 16);
-            }
+    }
+};
+
+// chunk c of a norm's weight, which is of DT or float32, as floats
+template <int DT, int W>
+__device__ __forceinline__ void load_weight(const void *weight, bool is_f32, int c, int H, float (&v)[8])
+{
+    if (DT == MOE_F32 || is_f32) {
+        Chunk<MOE_F32, W == 2 ? 4 : W> w;
+        w.load(weight, 32 * c, 4 * H);
+        w.get(v);
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n)
-                store1<DT>(row, c + i, v[i]);
+        Chunk<DT, W> w;
+        w.load(weight, Chunk<DT, W>::kBytes * c, Chunk<DT, W>::kElem * H);
+        w.get(v);
     }
 }
 

@@ -1,7 +1,10 @@
 // The experts' rows back to their tokens, weighted and summed, and the gradient of that
 // (include/moe_tokens.h).
 //
-// Both read or write every row once and compute two operations an element, so HBM bounds them.
+// Both read or write every row once and compute two operations an element, so HBM bounds them.  A token's row
+// belongs to one group of threads, which knows the token's rows and weights before it begins, and goes through the
+// columns with kRows rows' loads under way at once.  Blocks are small and many and take tokens in order: what is
+// read and written at a time then lies close together.
 #include <string.h>
 
 #include "mx.cuh"
@@ -11,10 +14,10 @@ using namespace moe_mx;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;   // most threads of a block
 constexpr int kWarps = kThreads / 32;
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kRows = 8;   // rows of a token loaded before the first is used
+constexpr int kRows = 8;        // rows of a token loaded before the first is used
 
 // W bytes of consecutive elements of DT, as they lie in memory
 template <int DT, int W>
@@ -96,164 +99,219 @@ __device__ __forceinline__ float load_weight(const void *weight, int dt, int64_t
     return dt == MOE_F32 ? load1<MOE_F32>(weight, i) : dt == MOE_BF16 ? load1<MOE_BF16>(weight, i) : load1<MOE_F16>(weight, i);
 }
 
+__device__ __forceinline__ void store_weight(void *weight, int dt, int64_t i, float v)
+{
+    if (dt == MOE_F32)
+        store1<MOE_F32>(weight, i, v);
+    else if (dt == MOE_BF16)
+        store1<MOE_BF16>(weight, i, v);
+    else
+        store1<MOE_F16>(weight, i, v);
+}
+
 struct Params {
     const void *rows, *weight, *grad_y;
     const int32_t *row_idx, *token_idx;
     void *y, *grad_rows, *grad_weight;
     int64_t T, R;
-    int H, k, weight_dt, segs;
+    int H, k, weight_dt;
+    int group, tokens;   // threads of a token, tokens of a block
 };
 
-// A warp has 32 pieces of one token.  The token's rows and weights are loaded by the lanes, one each, and
-// passed round; the rows' pieces are loaded kRows at a time.
-template <int DT, int W>
-__global__ void __launch_bounds__(kThreads) combine(Params p)
+// pieces of W bytes that a thread has of a row at once, `group` pieces apart: 16 bytes together
+template <int W>
+__host__ __device__ constexpr int pieces_at_once() { return 16 / W; }
+
+// Threads of a token whose row is `columns` threads' work: a power of two up to 16, else warps, at most kThreads, and as
+// few as take no more turns than kThreads would.
+int group_of(int64_t columns)
 {
-    using P = Piece<DT, W>;
-    const int lane = threadIdx.x % 32;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
-    const int64_t t = unit / p.segs;
-    if (t >= p.T)
-        return;
-    const int c = ((int)(unit - t * p.segs) * 32 + lane) * P::kEach;
-    const bool mine = c < p.H;
-    float sum[P::kEach];
-#pragma unroll
-    for (int i = 0; i < P::kEach; ++i)
-        sum[i] = 0.0f;
-    for (int j0 = 0; j0 < p.k; j0 += 32) {
-        int64_t row = -1;
-        float weight = 1.0f;
-        if (j0 + lane < p.k) {
-            row = __ldg(p.row_idx + t * p.k + j0 + lane);
-            row = row < p.R ? row : -1;
-            if (p.weight)
-                weight = load_weight(p.weight, p.weight_dt, t * p.k + j0 + lane);
-        }
-        const int count = min(32, p.k - j0);
-        for (int j1 = 0; j1 < count; j1 += kRows) {
-            P v[kRows];
-#pragma unroll
-            for (int j = 0; j < kRows; ++j) {
-                const int r = __shfl_sync(kFull, (int)row, min(j1 + j, 31));
-                if (j1 + j < count && r >= 0 && mine)
-                    v[j].load(p.rows, (int64_t)r * p.H + c);
-            }
-#pragma unroll
-            for (int j = 0; j < kRows; ++j) {
-                const int r = __shfl_sync(kFull, (int)row, min(j1 + j, 31));
-                const float w = __shfl_sync(kFull, weight, min(j1 + j, 31));
-                if (j1 + j < count && r >= 0 && mine) {
-                    float f[P::kEach];
-                    v[j].get(f);
-#pragma unroll
-                    for (int i = 0; i < P::kEach; ++i)
-                        sum[i] = fmaf(w, f[i], sum[i]);
-                }
-            }
-        }
+    if (columns <= 16) {
+        int g = 1;
+        while (g < columns)
+            g *= 2;
+        return g;
     }
-    if (mine) {
-        P out;
-        out.set(sum);
-        out.store(p.y, t * p.H + c);
+    const int64_t turns = (columns + kThreads - 1) / kThreads;
+    return (int)(((columns + turns - 1) / turns + 31) / 32 * 32);
+}
+
+// slots j0 .. j0 + kRows - 1 of a token: their rows (-1: none) and weights
+__device__ __forceinline__ void load_slots(const Params &p, int64_t t, int j0, int (&row)[kRows], float (&weight)[kRows])
+{
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+        row[j] = -1;
+        weight[j] = 1.0f;
+        if (j0 + j < p.k) {
+            row[j] = __ldg(p.row_idx + t * p.k + j0 + j);
+            row[j] = row[j] < p.R ? row[j] : -1;
+            if (p.weight)
+                weight[j] = load_weight(p.weight, p.weight_dt, t * p.k + j0 + j);
+        }
     }
 }
 
-// One block for each token, and behind them blocks that write the rows of zeros.  Each thread holds its pieces of
-// grad_y while it goes through kSlots of the token's rows, and one of the sums of each.
-constexpr int kSlots = 8;
+template <int DT, int W>
+__global__ void __launch_bounds__(kThreads, W > 2 ? 3 : 2) combine(Params p)
+{
+    using P = Piece<DT, W>;
+    constexpr int U = pieces_at_once<W>();
+    const int of_block = threadIdx.x / p.group, lane = threadIdx.x - of_block * p.group;
+    const int64_t t = (int64_t)blockIdx.x * p.tokens + of_block;
+    if (t >= p.T)
+        return;
+    const int pieces = p.H / P::kEach;
+    int row[kRows];
+    float weight[kRows];
+    load_slots(p, t, 0, row, weight);
+    for (int c = lane; c < pieces; c += U * p.group) {
+        float sum[U][P::kEach];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < P::kEach; ++i)
+                sum[u][i] = 0.0f;
+        for (int j0 = 0;;) {
+            P v[kRows][U];
+#pragma unroll
+            for (int j = 0; j < kRows; ++j)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (row[j] >= 0 && c + u * p.group < pieces)
+                        v[j][u].load(p.rows, (int64_t)row[j] * p.H + (c + u * p.group) * P::kEach);
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
+                if (row[j] < 0)
+                    continue;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float f[P::kEach];
+                    v[j][u].get(f);
+#pragma unroll
+                    for (int i = 0; i < P::kEach; ++i)
+                        sum[u][i] = fmaf(weight[j], f[i], sum[u][i]);
+                }
+            }
+            if (p.k <= kRows)
+                break;
+            j0 = j0 + kRows < p.k ? j0 + kRows : 0;   // the next slots, and after the last the first again
+            load_slots(p, t, j0, row, weight);
+            if (j0 == 0)
+                break;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c + u * p.group < pieces) {
+                P out;
+                out.set(sum[u]);
+                out.store(p.y, t * p.H + (c + u * p.group) * P::kEach);
+            }
+    }
+}
 
+// The blocks behind the tokens' write the rows of zeros.
 template <int DT, int W>
 __global__ void __launch_bounds__(kThreads) combine_grad(Params p)
 {
     using P = Piece<DT, W>;
-    __shared__ float part[kWarps][kSlots];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    constexpr int U = pieces_at_once<W>();
+    __shared__ float part[kWarps][kRows];
+    const int lane32 = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int pieces = p.H / P::kEach;
-    if (blockIdx.x >= p.T) {
-        const int64_t r0 = ((int64_t)blockIdx.x - p.T) * kThreads + threadIdx.x;
+    const int64_t token_blocks = (p.T + p.tokens - 1) / p.tokens;
+    if (blockIdx.x >= token_blocks) {
+        const int64_t r0 = ((int64_t)blockIdx.x - token_blocks) * blockDim.x + threadIdx.x;
         uint32_t none = __ballot_sync(kFull, r0 < p.R && __ldg(p.token_idx + min(r0, p.R - 1)) < 0);
         while (none) {
-            const int64_t r = r0 - lane + __ffs(none) - 1;
+            const int64_t r = r0 - lane32 + __ffs(none) - 1;
             none &= none - 1;
             P z;
             z.zero();
-            for (int c = lane; c < pieces; c += 32)
+            for (int c = lane32; c < pieces; c += 32)
                 z.store(p.grad_rows, r * p.H + (int64_t)c * P::kEach);
         }
         return;
     }
-    const int64_t t = blockIdx.x;
-    for (int j0 = 0; j0 < p.k; j0 += kSlots) {
-        int64_t row[kSlots];
-        float weight[kSlots], sum[kSlots];
+    const int of_block = threadIdx.x / p.group, lane = threadIdx.x - of_block * p.group;
+    const int64_t t = (int64_t)blockIdx.x * p.tokens + of_block;
+    const bool mine = t < p.T;   // the whole block stays for its barriers
+    for (int j0 = 0; j0 < p.k; j0 += kRows) {
+        int row[kRows];
+        float weight[kRows], sum[kRows];
+        if (mine) {
+            load_slots(p, t, j0, row, weight);
+        } else {
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
-            row[j] = -1;
-            weight[j] = 1.0f;
-            sum[j] = 0.0f;
-            if (j0 + j < p.k) {
-                row[j] = __ldg(p.row_idx + t * p.k + j0 + j);
-                row[j] = row[j] < p.R ? row[j] : -1;
-                if (p.weight)
-                    weight[j] = load_weight(p.weight, p.weight_dt, t * p.k + j0 + j);
-            }
+            for (int j = 0; j < kRows; ++j)
+                row[j] = -1;
         }
-        for (int c = threadIdx.x; c < pieces; c += kThreads) {
-            P g, v[kSlots];
-            g.load(p.grad_y, t * p.H + (int64_t)c * P::kEach);
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+            sum[j] = 0.0f;
+        for (int c = lane; mine && c < pieces; c += U * p.group) {
+            P g[U], v[kRows][U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c + u * p.group < pieces)
+                    g[u].load(p.grad_y, t * p.H + (c + u * p.group) * P::kEach);
+                else
+                    g[u].zero();
             if (p.grad_weight) {
 #pragma unroll
-                for (int j = 0; j < kSlots; ++j)
-                    if (row[j] >= 0)
-                        v[j].load(p.rows, row[j] * p.H + (int64_t)c * P::kEach);
-            }
-            float f[P::kEach];
-            g.get(f);
+                for (int j = 0; j < kRows; ++j)
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j) {
+                    for (int u = 0; u < U; ++u)
+                        if (row[j] >= 0 && c + u * p.group < pieces)
+                            v[j][u].load(p.rows, (int64_t)row[j] * p.H + (c + u * p.group) * P::kEach);
+            }
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
                 if (row[j] < 0)
                     continue;
-                float x[P::kEach];
-                if (p.grad_weight) {
-                    v[j].get(x);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (c + u * p.group >= pieces)
+                        continue;
+                    float f[P::kEach], x[P::kEach];
+                    g[u].get(f);
+                    if (p.grad_weight) {
+                        v[j][u].get(x);
+#pragma unroll
+                        for (int i = 0; i < P::kEach; ++i)
+                            sum[j] = fmaf(f[i], x[i], sum[j]);
+                    }
 #pragma unroll
                     for (int i = 0; i < P::kEach; ++i)
-                        sum[j] = fmaf(f[i], x[i], sum[j]);
+                        x[i] = weight[j] * f[i];
+                    P out;
+                    out.set(x);
+                    out.store(p.grad_rows, (int64_t)row[j] * p.H + (c + u * p.group) * P::kEach);
                 }
-#pragma unroll
-                for (int i = 0; i < P::kEach; ++i)
-                    x[i] = weight[j] * f[i];
-                P out;
-                out.set(x);
-                out.store(p.grad_rows, row[j] * p.H + (int64_t)c * P::kEach);
             }
         }
         if (!p.grad_weight)
             continue;
+        // over the token's threads: inside a warp by shuffles, warps through shared memory
+        const int width = min(p.group, 32);
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
-            float s = sum[j];
-#pragma unroll
-            for (int d = 16; d > 0; d /= 2)
-                s += __shfl_xor_sync(kFull, s, d);
-            if (lane == 0)
-                part[warp][j] = s;
+        for (int j = 0; j < kRows; ++j) {
+            for (int d = width / 2; d > 0; d /= 2)
+                sum[j] += __shfl_xor_sync(kFull, sum[j], d);
+            if (p.group >= 32 && lane32 == 0)
+                part[warp][j] = sum[j];
         }
         __syncthreads();
-        if (threadIdx.x < kSlots && j0 + (int)threadIdx.x < p.k) {
+        if (mine && lane < kRows && p.group >= 32 && j0 + lane < p.k) {
             float s = 0.0f;
+            for (int w = 0; w < p.group / 32; ++w)
+                s += part[warp + w][lane];
+            store_weight(p.grad_weight, p.weight_dt, t * p.k + j0 + lane, s);
+        } else if (mine && p.group < 32 && lane == 0) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                s += part[w][threadIdx.x];
-            const int64_t at = t * p.k + j0 + threadIdx.x;
-            if (p.weight_dt == MOE_F32)
-                store1<MOE_F32>(p.grad_weight, at, s);
-            else if (p.weight_dt == MOE_BF16)
-                store1<MOE_BF16>(p.grad_weight, at, s);
-            else
-                store1<MOE_F16>(p.grad_weight, at, s);
+            for (int j = 0; j < kRows; ++j)
+                if (j0 + j < p.k)
+                    store_weight(p.grad_weight, p.weight_dt, t * p.k + j0 + j, sum[j]);
         }
         __syncthreads();
     }
@@ -262,15 +320,17 @@ __global__ void __launch_bounds__(kThreads) combine_grad(Params p)
 template <int DT, int W>
 void launch(Params p, bool grad, cudaStream_t st)
 {
+    const int64_t columns = p.H / Piece<DT, W>::kEach, at_once = pieces_at_once<W>();
+    p.group = group_of((columns + at_once - 1) / at_once);
+    p.tokens = kThreads / p.group;
+    const int threads = p.group * p.tokens;   // whole warps
+    const int64_t blocks = (p.T + p.tokens - 1) / p.tokens;
     if (grad) {
-        const int64_t blocks = p.T + (p.token_idx ? (p.R + kThreads - 1) / kThreads : 0);
-        combine_grad<DT, W><<<(unsigned)blocks, kThreads, 0, st>>>(p);
-        return;
+        // behind the tokens' blocks, one for each `threads` rows (160 or more)
+        combine_grad<DT, W><<<(unsigned)(blocks + (p.R + threads - 1) / threads), threads, 0, st>>>(p);
+    } else if (blocks > 0) {
+        combine<DT, W><<<(unsigned)blocks, threads, 0, st>>>(p);
     }
-    constexpr int kEach = Piece<DT, W>::kEach;
-    p.segs = (p.H + 32 * kEach - 1) / (32 * kEach);
-    const int64_t units = p.T * p.segs;
-    combine<DT, W><<<(unsigned)((units + kWarps - 1) / kWarps), kThreads, 0, st>>>(p);
 }
 
 template <int DT>
@@ -307,11 +367,10 @@ mrr_status check(moe_dtype dt, int64_t R, int64_t H, int64_t T, int64_t k, const
 {
     if (!is_float(dt) || (weight && !is_float(weight_dt)))
         return MRR_ERR_DTYPE;
-    // at most 2^31 - 1 blocks: a warp has a piece of 64 elements or more, or a block a token
-    if (T < 0 || R < 0 || T > INT32_MAX || R > INT32_MAX || H < 1 || H > (1 << 20) || k < 1 ||
-        k > MOE_SORT_MAX_K || (T + 1) * ((H + 31) / 32) > 8ll * INT32_MAX || T + R / kThreads + 1 > INT32_MAX)
-        return MRR_ERR_SHAPE;
-    return MRR_OK;
+    // at most 2^31 - 1 blocks: one or more tokens each, and behind them blocks for 128 or more rows each
+    const bool ok = T >= 0 && R >= 0 && T <= INT32_MAX && R <= INT32_MAX && H >= 1 && H <= (1 << 20) && k >= 1 &&
+                    k <= MOE_SORT_MAX_K && T + R / 128 < INT32_MAX;
+    return ok ? MRR_OK : MRR_ERR_SHAPE;
 }
 
 }  // namespace

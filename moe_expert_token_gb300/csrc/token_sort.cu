@@ -7,8 +7,10 @@
 // once and writes it k times: T (1 + k) rows of traffic, the least there is.  HBM bounds it.
 //
 // Few slots (sort_few): one launch.  Each block looks at all keys and counts the smaller ones for its
-// own slots only.  Many slots: one launch counts each chunk's keys, and in the second each block adds up the
-// table of counts for its place in every expert's rows, ranks its own slots, and moves its rows.
+// own slots only.  Many slots: one launch counts each chunk's keys; in the second each block adds up the
+// table of counts for its place in every expert's rows and ranks its own slots; the third moves the rows.  It has
+// many small blocks that take the tokens in order, so that what is written at a time lies close together: with
+// blocks that stay and rank and move a share of the tokens each, 16384 x 7168 bfloat16 to 8 experts took 355 us.
 #include <atomic>
 #include <math.h>
 #include <string.h>
@@ -25,10 +27,9 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kNone = 0x80000000u;   // beside a row: the slot has no expert here, the row is zeros
 constexpr int kFewSlots = 4096;
 constexpr int kFewMine = 128;             // most slots of a block of sort_few
-constexpr int kBatch = 1024;              // slots that a block of sort_rows ranks at once
+constexpr int kBatch = 1024;              // slots that a block of sort_rank ranks at once
 constexpr int kMaxE = MOE_SORT_MAX_EXPERTS;
-// Blocks of the move: four on each of the 152 SMs.
-constexpr int kGroups = 608;
+constexpr int kGroups = 608;              // blocks of sort_rank: four on each of the 152 SMs
 
 struct Params {
     const void *idx;
@@ -48,6 +49,7 @@ struct Params {
     int tokens;        // a block's tokens (the last block's: fewer)
     int groups;        // blocks along the tokens
     int parts, chunks; // the table: chunks of `parts` blocks' slots
+    int group, move_tokens;   // the move: threads of a token, tokens of a block
 };
 
 __device__ __forceinline__ uint32_t key_of(const Params &p, uint32_t slot)
@@ -70,6 +72,10 @@ template <>
 struct Vec<2> { using T = uint16_t; };
 template <>
 struct Vec<1> { using T = uint8_t; };
+
+// vectors of a row that a thread of sort_move has under way at once
+template <int W>
+__host__ __device__ constexpr int vectors_at_once() { return W == 16 ? 4 : 8; }
 
 template <typename V>
 __device__ __forceinline__ V zero_of()
@@ -117,7 +123,7 @@ __device__ __forceinline__ void move_rows(const Params &p, int64_t first, int co
     }
 }
 
-// The slots first .. first + count - 1: their index entries, weights and scales.
+// The slots first .. first + count - 1: their index entries and weights.
 __device__ __forceinline__ void write_slots(const Params &p, uint32_t first, int count, const uint32_t *rows)
 {
     for (int s = threadIdx.x; s < count; s += kThreads) {
@@ -134,9 +140,13 @@ __device__ __forceinline__ void write_slots(const Params &p, uint32_t first, int
             p.out_weight[row] = w;
         }
     }
+}
+
+// Their scales, in 4-byte units where rows and both pointers allow it, else bytes.
+__device__ __forceinline__ void write_scales(const Params &p, uint32_t first, int count, const uint32_t *rows)
+{
     if (!p.out_scales)
         return;
-    // 4-byte units where rows and both pointers allow it, else bytes
     const int64_t units = p.scale_row_bytes / p.scale_unit;
     for (int64_t i = threadIdx.x; i < count * units; i += kThreads) {
         const int64_t s = i / units, at = i - s * units;
@@ -249,8 +259,10 @@ __global__ void __launch_bounds__(kThreads) sort_few(Params p)
             rows[s] = smaller | (own >> 12 == (uint32_t)p.E ? kNone : 0u);
     }
     __syncthreads();
-    if (blockIdx.y == 0)
+    if (blockIdx.y == 0) {
         write_slots(p, s0, mine, rows);
+        write_scales(p, s0, mine, rows);
+    }
     if (p.out) {
         int v0, v1;
         my_vectors((int)(p.row_bytes / W), v0, v1);
@@ -275,9 +287,10 @@ __global__ void __launch_bounds__(1024) sort_count(Params p)
         p.table[(size_t)blockIdx.x * (p.E + 1) + e] = count[e];
 }
 
-template <int W>
-__global__ void __launch_bounds__(kThreads) sort_rows(Params p)
+// Every slot's row, and what moves with slots.  Each block has p.tokens tokens.
+__global__ void __launch_bounds__(kThreads) sort_rank(Params p)
 {
+    mrr::grid_launch_dependents();
     __shared__ uint32_t base[kMaxE + 2];   // of each key: all its slots, then the row of this block's next one
     __shared__ uint32_t before[kMaxE + 1]; // of each key: its slots ahead of this block's
     __shared__ uint32_t rows[kBatch];
@@ -304,28 +317,23 @@ __global__ void __launch_bounds__(kThreads) sort_rows(Params p)
         before[e] += ahead;
     }
     __syncthreads();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && !p.cumsum) {
+    if (blockIdx.x == 0 && !p.cumsum) {
         for (int e = threadIdx.x; e < p.E; e += kThreads)
             store_num(p, e, base[e]);
         __syncthreads();
     }
     block_prefix(base, p.E + 1);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && p.cumsum)
+    if (blockIdx.x == 0 && p.cumsum)
         for (int e = threadIdx.x; e < p.E; e += kThreads)
             store_num(p, e, base[e + 1]);
     __syncthreads();
     for (int e = threadIdx.x; e <= p.E; e += kThreads)
         base[e] += before[e];
 
-    int v0 = 0, v1 = 0;
-    if (p.out)
-        my_vectors((int)(p.row_bytes / W), v0, v1);
-    const int64_t t_end = min(p.T, (int64_t)(blockIdx.x + 1) * p.tokens);
-    const int per = kBatch / p.k;   // tokens ranked at once
-    for (int64_t t0 = (int64_t)blockIdx.x * p.tokens; t0 < t_end; t0 += per) {
-        const int tokens = (int)min((int64_t)per, t_end - t0), mine = tokens * p.k;
-        const uint32_t s0 = (uint32_t)(t0 * p.k);
-        __syncthreads();   // the batch before has been moved
+    const uint32_t s_end = (uint32_t)min((uint64_t)p.n, (blockIdx.x + 1) * each);
+    for (uint32_t s0 = (uint32_t)(blockIdx.x * each); s0 < s_end; s0 += kBatch) {
+        const int mine = (int)min((uint32_t)kBatch, s_end - s0);
+        __syncthreads();   // the batch before has been written
         for (int s = threadIdx.x; s < mine; s += kThreads)
             rows[s] = key_of(p, s0 + s);
         __syncthreads();
@@ -344,14 +352,90 @@ __global__ void __launch_bounds__(kThreads) sort_rows(Params p)
             }
         }
         __syncthreads();
-        if (blockIdx.y == 0)
-            write_slots(p, s0, mine, rows);
-        if (p.out)
-            move_rows<W>(p, t0, tokens, rows, v0, v1);
+        write_slots(p, s0, mine, rows);
     }
 }
 
-// How the work is cut, from the sizes alone (the workspace's size follows from it).  Each block of the move
+// The rows, of p.move_tokens tokens a block and a group of p.group threads to a token, and behind them blocks that
+// write the rows of zeros.  kEach vectors of a row are loaded before the first is stored, the first ones before the
+// ranks are there (x is no output of the launches before).
+template <int W>
+__global__ void __launch_bounds__(kThreads) sort_move(Params p)
+{
+    using V = typename Vec<W>::T;
+    constexpr int kEach = vectors_at_once<W>();
+    const int64_t token_blocks = (p.T + p.move_tokens - 1) / p.move_tokens;
+    const int vectors = (int)(p.row_bytes / W);
+    if (blockIdx.x >= token_blocks) {
+        mrr::grid_dependency_wait();
+        const int lane = threadIdx.x % 32;
+        const uint64_t r0 = (blockIdx.x - token_blocks) * (uint64_t)blockDim.x + threadIdx.x;
+        uint32_t none = __ballot_sync(kFull, r0 < p.n && p.token_idx[r0 < p.n ? r0 : 0] < 0);
+        while (none) {
+            const int64_t r = (int64_t)(r0 - lane) + __ffs(none) - 1;
+            none &= none - 1;
+            for (int c = lane; c < vectors; c += 32)
+                reinterpret_cast<V *>(p.out + r * p.row_bytes)[c] = zero_of<V>();
+            for (int64_t c = lane; p.out_scales && c < p.scale_row_bytes; c += 32)
+                p.out_scales[r * p.scale_row_bytes + c] = 0u;
+        }
+        return;
+    }
+    const int of_block = threadIdx.x / p.group, lane = threadIdx.x - of_block * p.group;
+    const int64_t t = (int64_t)blockIdx.x * p.move_tokens + of_block;
+    if (t >= p.T)
+        return;
+    const V *from = reinterpret_cast<const V *>(p.x + t * p.row_stride);
+    V v[kEach];
+    auto load = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (c + i * p.group < vectors)
+                v[i] = __ldg(from + c + i * p.group);
+    };
+    load(lane);
+    mrr::grid_dependency_wait();
+    const int32_t *rows = p.row_idx + t * p.k;
+    for (int c = lane; c < vectors;) {
+        for (int j0 = 0; j0 < p.k; j0 += 8) {
+            int32_t row[8];   // all loaded before the first store, which the compiler could not tell apart from them
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                row[j] = j0 + j < p.k ? rows[j0 + j] : -1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (row[j] < 0)
+                    continue;
+                V *to = reinterpret_cast<V *>(p.out + row[j] * p.row_bytes);
+#pragma unroll
+                for (int i = 0; i < kEach; ++i)
+                    if (c + i * p.group < vectors)
+                        to[c + i * p.group] = v[i];
+            }
+        }
+        c += kEach * p.group;
+        load(c);
+    }
+    if (!p.out_scales)
+        return;
+    // 4-byte units where rows and both pointers allow it, else bytes
+    const int units = (int)(p.scale_row_bytes / p.scale_unit);
+    for (int c = lane; c < units; c += p.group) {
+        if (p.scale_unit == 4) {
+            const uint32_t s = __ldg(reinterpret_cast<const uint32_t *>(p.scales) + t * units + c);
+            for (int j = 0; j < p.k; ++j)
+                if (rows[j] >= 0)
+                    reinterpret_cast<uint32_t *>(p.out_scales)[(int64_t)rows[j] * units + c] = s;
+        } else {
+            const uint8_t s = __ldg(p.scales + t * units + c);
+            for (int j = 0; j < p.k; ++j)
+                if (rows[j] >= 0)
+                    p.out_scales[(int64_t)rows[j] * units + c] = s;
+        }
+    }
+}
+
+// How the work is cut, from the sizes alone (the workspace's size follows from it).  Each block of sort_rank
 // reads chunks * (E + 1) counts and up to parts * tokens * k keys; the two are about equal where
 // parts^2 = groups (E + 1) / (tokens k).
 void cut(int64_t T, int64_t k, int64_t E, int64_t &tokens, int64_t &groups, int64_t &parts, int64_t &chunks)
@@ -368,29 +452,51 @@ bool sizes_ok(int64_t T, int64_t k, int64_t E)
     return T >= 0 && T <= INT32_MAX && k >= 1 && k <= MOE_SORT_MAX_K && E >= 1 && E <= kMaxE && T * k <= INT32_MAX;
 }
 
-template <int W>
-cudaError_t launch(const Params &p, bool few, cudaStream_t st)
+// a launch that may begin while the one before it on the stream ends
+template <typename... Args>
+cudaError_t launch_next(void (*kernel)(Args...), unsigned grid, unsigned threads, cudaStream_t st, const Params &p)
 {
-    // where tokens are few, several blocks share a token's row, 1 KB each at least
-    const int64_t most = (p.row_bytes + 1023) / 1024, want = kGroups / p.groups;
-    const unsigned splits = (unsigned)(want < 1 || !p.out ? 1 : want < most ? want : most);
-    if (few) {
-        sort_few<W><<<dim3(p.groups + 1, splits), kThreads, 0, st>>>(p);
-        return cudaGetLastError();
-    }
-    sort_count<<<p.chunks, 1024, 0, st>>>(p);
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(p.groups, splits);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, sort_rows<W>, p);
-    return err != cudaSuccess ? err : cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int W>
+cudaError_t launch(Params p, bool few, cudaStream_t st)
+{
+    if (few) {
+        // where tokens are few, several blocks share a token's row, 1 KB each at least
+        const int64_t most = (p.row_bytes + 1023) / 1024, want = kGroups / p.groups;
+        const unsigned splits = (unsigned)(want < 1 || !p.out ? 1 : want < most ? want : most);
+        sort_few<W><<<dim3(p.groups + 1, splits), kThreads, 0, st>>>(p);
+        return cudaGetLastError();
+    }
+    sort_count<<<p.chunks, 1024, 0, st>>>(p);
+    cudaError_t err = launch_next(sort_rank, (unsigned)p.groups, kThreads, st, p);
+    if (err != cudaSuccess || (!p.out && !p.out_scales))
+        return err;
+    // threads of a token: a power of two up to 16, else warps, as few as take no more turns than kThreads would
+    const int64_t columns = (p.row_bytes / W + vectors_at_once<W>() - 1) / vectors_at_once<W>();
+    if (columns <= 16) {
+        p.group = 1;
+        while (p.group < columns)
+            p.group *= 2;
+    } else {
+        const int64_t turns = (columns + kThreads - 1) / kThreads;
+        p.group = (int)(((columns + turns - 1) / turns + 31) / 32 * 32);
+    }
+    p.move_tokens = kThreads / p.group;
+    const unsigned threads = p.group * p.move_tokens;   // whole warps
+    const int64_t blocks = (p.T + p.move_tokens - 1) / p.move_tokens + ((int64_t)p.n + threads - 1) / threads;
+    return launch_next(sort_move<W>, (unsigned)blocks, threads, st, p);
 }
 
 bool aligned(const void *p, uintptr_t n) { return (uintptr_t)p % n == 0; }
