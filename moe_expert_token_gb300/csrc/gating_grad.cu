@@ -60,24 +60,6 @@ __device__ __forceinline__ float score_of(int norm_type, float x, float top, flo
     return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
 }
 
-// grad_x [first, first + count) to zero, by one warp: 16 bytes at a time where they are aligned
-template <int DT>
-__device__ __forceinline__ void clear_rows(void *grad_x, int64_t first, int64_t count, int lane)
-{
-    constexpr int kElem = DT == MOE_F32 ? 4 : 2;
-    uint8_t *lo = static_cast<uint8_t *>(grad_x) + first * kElem, *hi = lo + count * kElem;
-    uint8_t *from = reinterpret_cast<uint8_t *>(((uintptr_t)lo + 15) / 16 * 16);
-    uint8_t *to = reinterpret_cast<uint8_t *>((uintptr_t)hi / 16 * 16);
-    if (from >= to)
-        from = to = hi;
-    for (uint8_t *q = lo + kElem * lane; q < from; q += 32 * kElem)
-        store1<DT>(q, 0, 0.0f);
-    for (uint8_t *q = from + 16 * lane; q < to; q += 32 * 16)
-        *reinterpret_cast<uint4 *>(q) = make_uint4(0u, 0u, 0u, 0u);
-    for (uint8_t *q = to + kElem * lane; q < hi; q += 32 * kElem)
-        store1<DT>(q, 0, 0.0f);
-}
-
 // LANES lanes a token (k <= LANES; 32 lanes: two slots each).  sums: [2][e] of each warp, where bias gradients are asked for.
 template <int DT, int LANES>
 __global__ void __launch_bounds__(32 * kWarps) gating_grad_chosen(Params p)
@@ -118,7 +100,7 @@ __global__ void __launch_bounds__(32 * kWarps) gating_grad_chosen(Params p)
             sum += s;
             inner = fmaf(g[h], s, inner);
         }
-        clear_rows<DT>(p.grad_x, t0 * p.e, min((int64_t)kTokens, p.T - t0) * p.e, lane);
+        clear<DT == MOE_F32 ? 4 : 2>(p.grad_x, t0 * p.e, min((int64_t)kTokens, p.T - t0) * p.e, lane, 32);
 #pragma unroll
         for (int o = LANES / 2; o > 0; o /= 2) {
             sum += __shfl_xor_sync(kFull, sum, o);

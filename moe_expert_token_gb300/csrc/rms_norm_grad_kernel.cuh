@@ -103,13 +103,14 @@ struct Ahead {
 
 // NV chunks a thread; kBlock: a block has a row at a time, else each of its warps has one.
 template <int DT, int W, int NV, bool kBlock, int kStages>
-__global__ void __launch_bounds__(kBlock ? (NV > 4 ? 1024 : 512) : 32 * kShortWarps, NV > 4 ? 1 : 2) rms_norm_grad(GradParams p)
+__global__ void __launch_bounds__(kBlock ? (NV > 4 ? 1024 : 512) : 32 * kShortWarps, NV > 4 || !kBlock ? 1 : 2) rms_norm_grad(GradParams p)
 {
     // (all of it dynamic: together with static memory it could not be allowed up to the device's limit)
     extern __shared__ __align__(16) uint8_t memory[];
     float2 (*sums)[kSumWords] = reinterpret_cast<float2 (*)[kSumWords]>(memory);
     uint8_t *space = memory + kSumBytes;
     mrr::grid_launch_dependents();
+    constexpr bool kWeightHere = NV <= 4;   // up to 64 KB
     const int warp = threadIdx.x / 32;
     const int64_t step = kBlock ? gridDim.x : gridDim.x * kShortWarps;
     Ahead<DT, W, NV, kStages> in;
@@ -121,15 +122,36 @@ __global__ void __launch_bounds__(kBlock ? (NV > 4 ? 1024 : 512) : 32 * kShortWa
     in.tid = kBlock ? threadIdx.x : threadIdx.x % 32;
     in.size = p.H * Chunk<DT, W>::kElem;
     in.slots = NV * blockDim.x;
-    in.own = space + (kBlock ? in.tid : NV * 32 * warp + in.tid) * Chunk<DT, W>::kBytes;
+    in.own = space + (kWeightHere ? 32 * in.slots : 0) + (kBlock ? in.tid : NV * 32 * warp + in.tid) * Chunk<DT, W>::kBytes;
     in.clear();
 
+    // the weight of this thread's chunks as floats, in two planes of 16 bytes a chunk
+    float4 *weight = reinterpret_cast<float4 *>(space) + (kBlock ? in.tid : NV * 32 * warp + in.tid);
     float acc[NV][8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        if (kWeightHere) {
+            float w[8];
+            load_weight<DT, W>(p.weight, p.weight_f32, in.tid + i * in.threads, p.H, w);
+            weight[i * in.threads] = make_float4(w[0], w[1], w[2], w[3]);
+            weight[in.slots + i * in.threads] = make_float4(w[4], w[5], w[6], w[7]);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             acc[i][j] = 0.0f;
+    }
+    // h, grad_y and the weight of chunk i; read twice a row, which costs less than the threads that registers would
+    auto get = [&](int stage, int64_t row, int i, float (&h)[8], float (&g)[8], float (&w)[8]) {
+        in.get(stage, row, 0, i, h);
+        in.get(stage, row, 1, i, g);
+        if (kWeightHere) {
+            const float4 lo = weight[i * in.threads], hi = weight[in.slots + i * in.threads];
+            w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+        } else {
+            load_weight<DT, W>(p.weight, p.weight_f32, in.tid + i * in.threads, p.H, w);
+        }
+    };
+    const float per_element = 1.0f / (float)p.H;
     int64_t row = kBlock ? blockIdx.x : blockIdx.x * kShortWarps + warp;
     for (int s = 0; s < kStages; ++s)
         in.fetch(s, row + s * step, p.T);
@@ -140,13 +162,11 @@ __global__ void __launch_bounds__(kBlock ? (NV > 4 ? 1024 : 512) : 32 * kShortWa
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float h[8], g[8], w[8];
-            in.get(stage, row, 0, i, h);
-            in.get(stage, row, 1, i, g);
-            load_weight<DT, W>(p.weight, p.weight_f32, in.tid + i * in.threads, p.H, w);
+            get(stage, row, i, h, g, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 squares = fmaf(h[j], h[j], squares);
-                inner = fmaf(g[j] * w[j], h[j], inner);
+                inner = fmaf(g[j] * h[j], w[j], inner);
             }
         }
         squares = warp_sum(squares);
@@ -162,14 +182,12 @@ __global__ void __launch_bounds__(kBlock ? (NV > 4 ? 1024 : 512) : 32 * kShortWa
                 inner += sums[turn][w].y;
             }
         }
-        const float r = 1.0f / sqrtf(squares / (float)p.H + p.eps);
-        const float factor = r * r * r * (inner / (float)p.H);
+        const float r = rsqrtf(fmaf(squares, per_element, p.eps));
+        const float factor = -r * r * r * (inner * per_element);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float h[8], g[8], w[8], d[8];
-            in.get(stage, row, 0, i, h);
-            in.get(stage, row, 1, i, g);
-            load_weight<DT, W>(p.weight, p.weight_f32, in.tid + i * in.threads, p.H, w);
+            get(stage, row, i, h, g, w);
             if (p.grad_h) {
                 in.get(stage, row, 2, i, d);
             } else {
@@ -179,8 +197,8 @@ __global__ void __launch_bounds__(kBlock ? (NV > 4 ? 1024 : 512) : 32 * kShortWa
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                acc[i][j] = fmaf(g[j], h[j] * r, acc[i][j]);
-                d[j] += r * (g[j] * w[j]) - h[j] * factor;
+                acc[i][j] = fmaf(g[j] * h[j], r, acc[i][j]);
+                d[j] = fmaf(g[j] * w[j], r, fmaf(h[j], factor, d[j]));
             }
             Chunk<DT, W> out;
             out.set(d);
@@ -237,16 +255,18 @@ cudaError_t launch(const GradParams &p, const mrr_device::Info &info, cudaStream
 {
     const int chunks = (p.H + 7) / 8;
     const unsigned threads = kBlock ? ((chunks + NV - 1) / NV + 31) / 32 * 32 : 32 * kShortWarps;
-    const int stage = (p.grad_h ? 3 : 2) * NV * (int)threads * Chunk<DT, W>::kBytes;
-    const int shares = kBlock ? 0 : kShortWarps * p.H * 4;
-    const int half = info.smem_max / 2 - 1024;   // of an SM's shared memory: two blocks
+    const int slots = NV * (int)threads, stage = (p.grad_h ? 3 : 2) * slots * Chunk<DT, W>::kBytes;
+    const int weight = NV <= 4 ? 32 * slots : 0;
+    const int shares = kBlock ? 0 : kShortWarps * p.H * 4;   // in the place of the rest, at the end
+    auto bytes = [&](int stages) { return weight + stages * stage > shares ? weight + stages * stage : shares; };
     if constexpr (W > 2 && NV <= 4) {
-        if (4 * stage <= half)
-            return launch<DT, W, NV, kBlock, 4>(p, threads, 4 * stage > shares ? 4 * stage : shares, info, st);
-        if (2 * stage <= info.smem_max - 1024)
-            return launch<DT, W, NV, kBlock, 2>(p, threads, 2 * stage > shares ? 2 * stage : shares, info, st);
+        const int half = info.smem_max / 2 - 1024, whole = info.smem_max - 1024;   // two blocks on an SM, or one
+        if (bytes(4) <= half)
+            return launch<DT, W, NV, kBlock, 4>(p, threads, bytes(4), info, st);
+        if (bytes(2) <= whole)
+            return launch<DT, W, NV, kBlock, 2>(p, threads, bytes(2), info, st);
     }
-    return launch<DT, W, NV, kBlock, 0>(p, threads, shares, info, st);
+    return launch<DT, W, NV, kBlock, 0>(p, threads, bytes(0), info, st);
 }
 
 template <int DT, int W>

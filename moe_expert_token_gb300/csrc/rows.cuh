@@ -120,6 +120,32 @@ __device__ __forceinline__ float2 decode_e4m3x2(uint32_t two)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// elements first .. first + count - 1 of ELEM bytes (2 or 4; 1: bytes) at `base` to zero, by threads 0 .. threads - 1:
+// 16 bytes at a time between the first and last 16-byte boundary
+template <int ELEM>
+__device__ __forceinline__ void clear(void *base, int64_t first, int64_t count, int thread, int threads)
+{
+    uint8_t *lo = static_cast<uint8_t *>(base) + first * ELEM, *hi = lo + count * ELEM;
+    uint8_t *from = reinterpret_cast<uint8_t *>(((uintptr_t)lo + 15) / 16 * 16);
+    uint8_t *to = reinterpret_cast<uint8_t *>((uintptr_t)hi / 16 * 16);
+    if (from >= to)
+        from = to = hi;
+    auto edge = [](uint8_t *q) {
+        if constexpr (ELEM == 4)
+            *reinterpret_cast<uint32_t *>(q) = 0u;
+        else if constexpr (ELEM == 2)
+            *reinterpret_cast<uint16_t *>(q) = 0u;
+        else
+            *q = 0u;
+    };
+    for (uint8_t *q = lo + (int64_t)ELEM * thread; q < from; q += ELEM * threads)
+        edge(q);
+    for (uint8_t *q = from + (int64_t)16 * thread; q < to; q += 16 * threads)
+        *reinterpret_cast<uint4 *>(q) = make_uint4(0u, 0u, 0u, 0u);
+    for (uint8_t *q = to + (int64_t)ELEM * thread; q < hi; q += ELEM * threads)
+        edge(q);
+}
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll

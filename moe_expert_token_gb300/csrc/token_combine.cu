@@ -2,13 +2,15 @@
 // (include/moe_tokens.h).
 //
 // Both read or write every row once and compute two operations an element, so HBM bounds them.  A token's row
-// belongs to one group of threads, which knows the token's rows and weights before it begins, and goes through the
-// columns with kRows rows' loads under way at once.  Blocks are small and many and take tokens in order: what is
-// read and written at a time then lies close together.
+// belongs to one group of threads, which goes through the columns with 64 or 128 bytes of loads a thread under way
+// at once: of 8 rows, or of 4, 2 or 1 rows (where k is that small) in 2, 2 or 4 places.  The rows' places and their weights
+// are read again for each turn, from L1, which the rows themselves are kept out of: held in registers they cost threads.  Blocks are small and many and take tokens in order: what is read and written at a
+// time then lies close together.
 #include <string.h>
 
-#include "mx.cuh"
+#include "rows.cuh"
 #include "moe_tokens.h"
+#include "ptx.cuh"
 
 using namespace moe_mx;
 
@@ -16,8 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;   // most threads of a block
 constexpr int kWarps = kThreads / 32;
-constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kRows = 8;        // rows of a token loaded before the first is used
+using moe_rows::kFull;
 
 // W bytes of consecutive elements of DT, as they lie in memory
 template <int DT, int W>
@@ -27,19 +28,21 @@ struct Piece {
     static constexpr int kWords = (W + 3) / 4;
     uint32_t w[kWords];
 
+    // (streamed: past L1)
     __device__ __forceinline__ void load(const void *base, int64_t i)
     {
         const uint8_t *p = static_cast<const uint8_t *>(base) + i * kElem;
         if constexpr (W == 16) {
-            const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p));
+            const uint4 q = mrr::ld_stream_v4(p);
             w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
         } else if constexpr (W == 8) {
-            const uint2 q = __ldg(reinterpret_cast<const uint2 *>(p));
-            w[0] = q.x, w[1] = q.y;
+            asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[kWords - 1]) : "l"(p));
         } else if constexpr (W == 4) {
-            w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+            asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
         } else {
-            w[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
+            uint16_t h;
+            asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(h) : "l"(p));
+            w[0] = h;
         }
     }
 
@@ -118,9 +121,13 @@ struct Params {
     int group, tokens;   // threads of a token, tokens of a block
 };
 
-// pieces of W bytes that a thread has of a row at once, `group` pieces apart: 16 bytes together
-template <int W>
-__host__ __device__ constexpr int pieces_at_once() { return 16 / W; }
+// pieces of W bytes that a thread has of each of R rows at once, `group` pieces apart (with pieces of 2 bytes, 32 in all:
+// each takes a register)
+template <int W, int R>
+__host__ __device__ constexpr int pieces_at_once()
+{
+    return (R == 8 ? 1 : R == 1 ? 4 : 2) * (W >= 4 ? 16 / W : 4);
+}
 
 // Threads of a token whose row is `columns` threads' work: a power of two up to 16, else warps, at most kThreads, and as
 // few as take no more turns than kThreads would.
@@ -136,11 +143,12 @@ int group_of(int64_t columns)
     return (int)(((columns + turns - 1) / turns + 31) / 32 * 32);
 }
 
-// slots j0 .. j0 + kRows - 1 of a token: their rows (-1: none) and weights
-__device__ __forceinline__ void load_slots(const Params &p, int64_t t, int j0, int (&row)[kRows], float (&weight)[kRows])
+// slots j0 .. j0 + R - 1 of a token: their rows (-1: none) and weights
+template <int R>
+__device__ __forceinline__ void load_slots(const Params &p, int64_t t, int j0, int (&row)[R], float (&weight)[R])
 {
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
+    for (int j = 0; j < R; ++j) {
         row[j] = -1;
         weight[j] = 1.0f;
         if (j0 + j < p.k) {
@@ -152,19 +160,17 @@ __device__ __forceinline__ void load_slots(const Params &p, int64_t t, int j0, i
     }
 }
 
-template <int DT, int W>
+// R rows at once
+template <int DT, int W, int R>
 __global__ void __launch_bounds__(kThreads, W > 2 ? 3 : 2) combine(Params p)
 {
     using P = Piece<DT, W>;
-    constexpr int U = pieces_at_once<W>();
+    constexpr int U = pieces_at_once<W, R>();
     const int of_block = threadIdx.x / p.group, lane = threadIdx.x - of_block * p.group;
     const int64_t t = (int64_t)blockIdx.x * p.tokens + of_block;
     if (t >= p.T)
         return;
     const int pieces = p.H / P::kEach;
-    int row[kRows];
-    float weight[kRows];
-    load_slots(p, t, 0, row, weight);
     for (int c = lane; c < pieces; c += U * p.group) {
         float sum[U][P::kEach];
 #pragma unroll
@@ -172,16 +178,19 @@ __global__ void __launch_bounds__(kThreads, W > 2 ? 3 : 2) combine(Params p)
 #pragma unroll
             for (int i = 0; i < P::kEach; ++i)
                 sum[u][i] = 0.0f;
-        for (int j0 = 0;;) {
-            P v[kRows][U];
+        for (int j0 = 0; j0 < p.k; j0 += R) {
+            int row[R];
+            float weight[R];
+            load_slots<R>(p, t, j0, row, weight);
+            P v[R][U];
 #pragma unroll
-            for (int j = 0; j < kRows; ++j)
+            for (int j = 0; j < R; ++j)
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (row[j] >= 0 && c + u * p.group < pieces)
                         v[j][u].load(p.rows, (int64_t)row[j] * p.H + (c + u * p.group) * P::kEach);
 #pragma unroll
-            for (int j = 0; j < kRows; ++j) {
+            for (int j = 0; j < R; ++j) {
                 if (row[j] < 0)
                     continue;
 #pragma unroll
@@ -193,12 +202,6 @@ __global__ void __launch_bounds__(kThreads, W > 2 ? 3 : 2) combine(Params p)
                         sum[u][i] = fmaf(weight[j], f[i], sum[u][i]);
                 }
             }
-            if (p.k <= kRows)
-                break;
-            j0 = j0 + kRows < p.k ? j0 + kRows : 0;   // the next slots, and after the last the first again
-            load_slots(p, t, j0, row, weight);
-            if (j0 == 0)
-                break;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -210,63 +213,55 @@ __global__ void __launch_bounds__(kThreads, W > 2 ? 3 : 2) combine(Params p)
     }
 }
 
-// The blocks behind the tokens' write the rows of zeros.
-template <int DT, int W>
-__global__ void __launch_bounds__(kThreads) combine_grad(Params p)
+// A thread's sums of R slots stay while it goes through the columns.  The blocks behind the tokens' write the rows of
+// zeros, each every `zero_blocks`th row: these rows follow one another.
+template <int DT, int W, int R>
+__global__ void __launch_bounds__(kThreads, 2) combine_grad(Params p)
 {
     using P = Piece<DT, W>;
-    constexpr int U = pieces_at_once<W>();
-    __shared__ float part[kWarps][kRows];
+    constexpr int U = pieces_at_once<W, R>();
+    __shared__ float part[kWarps][R];
     const int lane32 = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int pieces = p.H / P::kEach;
     const int64_t token_blocks = (p.T + p.tokens - 1) / p.tokens;
     if (blockIdx.x >= token_blocks) {
-        const int64_t r0 = ((int64_t)blockIdx.x - token_blocks) * blockDim.x + threadIdx.x;
-        uint32_t none = __ballot_sync(kFull, r0 < p.R && __ldg(p.token_idx + min(r0, p.R - 1)) < 0);
+        const int64_t zero_blocks = gridDim.x - token_blocks;
+        const int64_t mine = blockIdx.x - token_blocks + threadIdx.x * zero_blocks;
+        uint32_t none = __ballot_sync(kFull, mine < p.R && __ldg(p.token_idx + min(mine, p.R - 1)) < 0);
         while (none) {
-            const int64_t r = r0 - lane32 + __ffs(none) - 1;
+            const int64_t r = __shfl_sync(kFull, mine, __ffs(none) - 1);
             none &= none - 1;
-            P z;
-            z.zero();
-            for (int c = lane32; c < pieces; c += 32)
-                z.store(p.grad_rows, r * p.H + (int64_t)c * P::kEach);
+            moe_rows::clear<P::kElem>(p.grad_rows, r * p.H, p.H, lane32, 32);
         }
         return;
     }
     const int of_block = threadIdx.x / p.group, lane = threadIdx.x - of_block * p.group;
     const int64_t t = (int64_t)blockIdx.x * p.tokens + of_block;
     const bool mine = t < p.T;   // the whole block stays for its barriers
-    for (int j0 = 0; j0 < p.k; j0 += kRows) {
-        int row[kRows];
-        float weight[kRows], sum[kRows];
-        if (mine) {
-            load_slots(p, t, j0, row, weight);
-        } else {
+    for (int j0 = 0; j0 < p.k; j0 += R) {
+        float sum[R];
 #pragma unroll
-            for (int j = 0; j < kRows; ++j)
-                row[j] = -1;
-        }
-#pragma unroll
-        for (int j = 0; j < kRows; ++j)
+        for (int j = 0; j < R; ++j)
             sum[j] = 0.0f;
         for (int c = lane; mine && c < pieces; c += U * p.group) {
-            P g[U], v[kRows][U];
+            int row[R];
+            float weight[R];
+            load_slots<R>(p, t, j0, row, weight);
+            P g[U], v[R][U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (c + u * p.group < pieces)
                     g[u].load(p.grad_y, t * p.H + (c + u * p.group) * P::kEach);
-                else
-                    g[u].zero();
             if (p.grad_weight) {
 #pragma unroll
-                for (int j = 0; j < kRows; ++j)
+                for (int j = 0; j < R; ++j)
 #pragma unroll
                     for (int u = 0; u < U; ++u)
                         if (row[j] >= 0 && c + u * p.group < pieces)
                             v[j][u].load(p.rows, (int64_t)row[j] * p.H + (c + u * p.group) * P::kEach);
             }
 #pragma unroll
-            for (int j = 0; j < kRows; ++j) {
+            for (int j = 0; j < R; ++j) {
                 if (row[j] < 0)
                     continue;
 #pragma unroll
@@ -295,21 +290,21 @@ __global__ void __launch_bounds__(kThreads) combine_grad(Params p)
         // over the token's threads: inside a warp by shuffles, warps through shared memory
         const int width = min(p.group, 32);
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
+        for (int j = 0; j < R; ++j) {
             for (int d = width / 2; d > 0; d /= 2)
                 sum[j] += __shfl_xor_sync(kFull, sum[j], d);
             if (p.group >= 32 && lane32 == 0)
                 part[warp][j] = sum[j];
         }
         __syncthreads();
-        if (mine && lane < kRows && p.group >= 32 && j0 + lane < p.k) {
+        if (mine && lane < R && p.group >= 32 && j0 + lane < p.k) {
             float s = 0.0f;
             for (int w = 0; w < p.group / 32; ++w)
                 s += part[warp + w][lane];
             store_weight(p.grad_weight, p.weight_dt, t * p.k + j0 + lane, s);
         } else if (mine && p.group < 32 && lane == 0) {
 #pragma unroll
-            for (int j = 0; j < kRows; ++j)
+            for (int j = 0; j < R; ++j)
                 if (j0 + j < p.k)
                     store_weight(p.grad_weight, p.weight_dt, t * p.k + j0 + j, sum[j]);
         }
@@ -317,20 +312,33 @@ __global__ void __launch_bounds__(kThreads) combine_grad(Params p)
     }
 }
 
-template <int DT, int W>
+template <int DT, int W, int R>
 void launch(Params p, bool grad, cudaStream_t st)
 {
-    const int64_t columns = p.H / Piece<DT, W>::kEach, at_once = pieces_at_once<W>();
+    const int64_t columns = p.H / Piece<DT, W>::kEach, at_once = pieces_at_once<W, R>();
     p.group = group_of((columns + at_once - 1) / at_once);
     p.tokens = kThreads / p.group;
     const int threads = p.group * p.tokens;   // whole warps
     const int64_t blocks = (p.T + p.tokens - 1) / p.tokens;
     if (grad) {
         // behind the tokens' blocks, one for each `threads` rows (160 or more)
-        combine_grad<DT, W><<<(unsigned)(blocks + (p.R + threads - 1) / threads), threads, 0, st>>>(p);
+        combine_grad<DT, W, R><<<(unsigned)(blocks + (p.R + threads - 1) / threads), threads, 0, st>>>(p);
     } else if (blocks > 0) {
-        combine<DT, W><<<(unsigned)blocks, threads, 0, st>>>(p);
+        combine<DT, W, R><<<(unsigned)blocks, threads, 0, st>>>(p);
     }
+}
+
+template <int DT, int W>
+void launch(const Params &p, bool grad, cudaStream_t st)
+{
+    if (p.k > 4)
+        launch<DT, W, 8>(p, grad, st);
+    else if (p.k > 2)
+        launch<DT, W, 4>(p, grad, st);
+    else if (p.k > 1)
+        launch<DT, W, 2>(p, grad, st);
+    else
+        launch<DT, W, 1>(p, grad, st);
 }
 
 template <int DT>

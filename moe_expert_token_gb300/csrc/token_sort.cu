@@ -15,15 +15,15 @@
 #include <math.h>
 #include <string.h>
 
-#include "mx.cuh"
 #include "moe_tokens.h"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr uint32_t kFull = 0xffffffffu;
+using moe_rows::kFull;
 constexpr uint32_t kNone = 0x80000000u;   // beside a row: the slot has no expert here, the row is zeros
 constexpr int kFewSlots = 4096;
 constexpr int kFewMine = 128;             // most slots of a block of sort_few
@@ -270,6 +270,25 @@ __global__ void __launch_bounds__(kThreads) sort_few(Params p)
     }
 }
 
+// count[key] of slots lo .. hi - 1, by a block: eight loads a thread under way at once
+template <int THREADS>
+__device__ __forceinline__ void count_keys(const Params &p, uint64_t lo, uint64_t hi, uint32_t *count)
+{
+    for (uint64_t i = lo + threadIdx.x; i < hi; i += 8 * THREADS) {
+        uint32_t key[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            key[u] = i + u * THREADS < hi ? key_of(p, (uint32_t)(i + u * THREADS)) : 0u;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (i + u * THREADS < hi)
+                atomicAdd(&count[key[u]], 1u);
+    }
+}
+
+// behind the table: the number of rows that experts have
+__device__ __forceinline__ uint32_t *used_rows(const Params &p) { return p.table + (size_t)p.chunks * (p.E + 1); }
+
 // table[c][e] = how often key e (E: none) occurs among chunk c's slots
 __global__ void __launch_bounds__(1024) sort_count(Params p)
 {
@@ -280,8 +299,7 @@ __global__ void __launch_bounds__(1024) sort_count(Params p)
     __syncthreads();
     const uint64_t per = (uint64_t)p.parts * p.tokens * p.k;
     const uint64_t lo = blockIdx.x * per, hi = min((uint64_t)p.n, lo + per);
-    for (uint64_t i = lo + threadIdx.x; i < hi; i += 1024)
-        atomicAdd(&count[key_of(p, (uint32_t)i)], 1u);
+    count_keys<1024>(p, lo, hi, count);
     __syncthreads();
     for (int e = threadIdx.x; e <= p.E; e += 1024)
         p.table[(size_t)blockIdx.x * (p.E + 1) + e] = count[e];
@@ -301,8 +319,7 @@ __global__ void __launch_bounds__(kThreads) sort_rank(Params p)
     __syncthreads();
     // slots of this chunk ahead of this block's
     const uint64_t each = (uint64_t)p.tokens * p.k;
-    for (uint64_t i = chunk * p.parts * each + threadIdx.x; i < blockIdx.x * each; i += kThreads)
-        atomicAdd(&before[key_of(p, (uint32_t)i)], 1u);
+    count_keys<kThreads>(p, chunk * p.parts * each, blockIdx.x * each, before);
     __syncthreads();
     mrr::grid_dependency_wait();   // the table is the previous launch's
     for (int e = threadIdx.x; e <= p.E; e += kThreads) {
@@ -323,6 +340,8 @@ __global__ void __launch_bounds__(kThreads) sort_rank(Params p)
         __syncthreads();
     }
     block_prefix(base, p.E + 1);
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *used_rows(p) = base[p.E];
     if (blockIdx.x == 0 && p.cumsum)
         for (int e = threadIdx.x; e < p.E; e += kThreads)
             store_num(p, e, base[e + 1]);
@@ -368,17 +387,18 @@ __global__ void __launch_bounds__(kThreads) sort_move(Params p)
     const int vectors = (int)(p.row_bytes / W);
     if (blockIdx.x >= token_blocks) {
         mrr::grid_dependency_wait();
-        const int lane = threadIdx.x % 32;
-        const uint64_t r0 = (blockIdx.x - token_blocks) * (uint64_t)blockDim.x + threadIdx.x;
-        uint32_t none = __ballot_sync(kFull, r0 < p.n && p.token_idx[r0 < p.n ? r0 : 0] < 0);
-        while (none) {
-            const int64_t r = (int64_t)(r0 - lane) + __ffs(none) - 1;
-            none &= none - 1;
-            for (int c = lane; c < vectors; c += 32)
-                reinterpret_cast<V *>(p.out + r * p.row_bytes)[c] = zero_of<V>();
-            for (int64_t c = lane; p.out_scales && c < p.scale_row_bytes; c += 32)
-                p.out_scales[r * p.scale_row_bytes + c] = 0u;
-        }
+        // a share of the bytes behind the last expert's rows, in 16-byte units
+        const int64_t used = *used_rows(p);
+        auto share = [&](uint8_t *out, int64_t row_bytes) {
+            const int64_t lo = used * row_bytes, all = p.n * row_bytes - lo, blocks = gridDim.x - token_blocks;
+            const int64_t per = (all + 16 * blocks - 1) / (16 * blocks) * 16, at = (blockIdx.x - token_blocks) * per;
+            if (at < all)
+                moe_rows::clear<1>(out, lo + at, min(per, all - at), threadIdx.x, blockDim.x);
+        };
+        if (p.out)
+            share(p.out, p.row_bytes);
+        if (p.out_scales)
+            share(p.out_scales, p.scale_row_bytes);
         return;
     }
     const int of_block = threadIdx.x / p.group, lane = threadIdx.x - of_block * p.group;
@@ -495,7 +515,8 @@ cudaError_t launch(Params p, bool few, cudaStream_t st)
     }
     p.move_tokens = kThreads / p.group;
     const unsigned threads = p.group * p.move_tokens;   // whole warps
-    const int64_t blocks = (p.T + p.move_tokens - 1) / p.move_tokens + ((int64_t)p.n + threads - 1) / threads;
+    // behind the tokens' blocks, kGroups for the zeros
+    const int64_t blocks = (p.T + p.move_tokens - 1) / p.move_tokens + kGroups;
     return launch_next(sort_move<W>, (unsigned)blocks, threads, st, p);
 }
 
@@ -511,7 +532,7 @@ size_t moe_sort_workspace(int64_t T, int64_t k, int64_t E)
         return 0;
     int64_t tokens, groups, parts, chunks;
     cut(T, k, E, tokens, groups, parts, chunks);
-    return (size_t)((4 * chunks * (E + 1) + 255) / 256 * 256);
+    return (size_t)((4 * (chunks * (E + 1) + 1) + 255) / 256 * 256);
 }
 
 mrr_status moe_sort_run(const void *expert_idx, int idx_is_i64, int64_t T, int64_t k, int64_t first_expert, int64_t E,
