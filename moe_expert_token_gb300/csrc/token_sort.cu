@@ -7,14 +7,15 @@
 // once and writes it k times: T (1 + k) rows of traffic, the least there is.  HBM bounds it.
 //
 // Few slots (sort_few): one launch.  Each block looks at all keys and counts the smaller ones for its
-// own slots only.  Many slots: one launch counts each chunk's keys; in the second each block adds up the
-// table of counts for its place in every expert's rows and ranks its own slots; the third moves the rows.  It has
+// own slots only.  Many slots: a first launch of one cluster counts the keys of kChunks chunks, passes the counts
+// round, and leaves where each chunk's slots of each key begin; in the second each block ranks its own slots (it counts
+// those of its chunk ahead of them while the first launch runs); the third moves the rows.  It has
 // many small blocks that take the tokens in order, so that what is written at a time lies close together: with
 // blocks that stay and rank and move a share of the tokens each, 16384 x 7168 bfloat16 to 8 experts took 355 us.
 #include <atomic>
-#include <math.h>
 #include <string.h>
 
+#include "device_info.h"
 #include "moe_tokens.h"
 #include "ptx.cuh"
 #include "rows.cuh"
@@ -25,11 +26,16 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 using moe_rows::kFull;
 constexpr uint32_t kNone = 0x80000000u;   // beside a row: the slot has no expert here, the row is zeros
+constexpr int kMoveThreads = 256;         // most threads of a block of sort_move
 constexpr int kFewSlots = 4096;
 constexpr int kFewMine = 128;             // most slots of a block of sort_few
 constexpr int kBatch = 1024;              // slots that a block of sort_rank ranks at once
 constexpr int kMaxE = MOE_SORT_MAX_EXPERTS;
 constexpr int kGroups = 608;              // blocks of sort_rank: four on each of the 152 SMs
+constexpr int kCluster = 16;              // blocks of sort_count
+constexpr int kCountThreads = 1024;
+constexpr int kOfBlock = 4;               // chunks of one of them
+constexpr int kChunks = kCluster * kOfBlock;
 
 struct Params {
     const void *idx;
@@ -48,7 +54,7 @@ struct Params {
     int idx64, weight_dt, cumsum, scale_unit;
     int tokens;        // a block's tokens (the last block's: fewer)
     int groups;        // blocks along the tokens
-    int parts, chunks; // the table: chunks of `parts` blocks' slots
+    int parts;         // the table: chunks of `parts` blocks' slots, kChunks at most
     int group, move_tokens;   // the move: threads of a token, tokens of a block
 };
 
@@ -58,6 +64,22 @@ __device__ __forceinline__ uint32_t key_of(const Params &p, uint32_t slot)
                                : (uint64_t)(int64_t)__ldg(static_cast<const int *>(p.idx) + slot);
     const uint64_t d = v - p.first;   // unsigned: anything below `first` is far above E
     return d < (uint64_t)p.E ? (uint32_t)d : (uint32_t)p.E;
+}
+
+// f(slot, key) of slots lo .. hi - 1, by threads 0 .. THREADS - 1: eight loads a thread under way at once
+template <int THREADS, typename F>
+__device__ __forceinline__ void keys_of(const Params &p, uint32_t lo, uint32_t hi, uint32_t thread, F f)
+{
+    for (uint32_t i = lo + thread; i < hi; i += 8 * THREADS) {
+        uint32_t key[8];
+#pragma unroll
+        for (uint32_t u = 0; u < 8; ++u)
+            key[u] = i + u * THREADS < hi ? key_of(p, i + u * THREADS) : 0u;
+#pragma unroll
+        for (uint32_t u = 0; u < 8; ++u)
+            if (i + u * THREADS < hi)
+                f(i + u * THREADS, key[u]);
+    }
 }
 
 template <int W>
@@ -169,12 +191,13 @@ __device__ __forceinline__ void store_num(const Params &p, int e, uint32_t v)
         static_cast<int *>(p.num)[e] = (int)v;
 }
 
-// v[0 .. count - 1] to its exclusive prefix, by the whole block
+// v[0 .. count - 1] to its exclusive prefix, by a block of THREADS threads
+template <int THREADS>
 __device__ __forceinline__ void block_prefix(uint32_t *v, int count)
 {
-    __shared__ uint32_t of_warp[kWarps];
+    __shared__ uint32_t of_warp[THREADS / 32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int per = (count + kThreads - 1) / kThreads, lo = threadIdx.x * per, hi = min(count, lo + per);
+    const int per = (count + THREADS - 1) / THREADS, lo = threadIdx.x * per, hi = min(count, lo + per);
     uint32_t sum = 0;
     for (int i = lo; i < hi; ++i)
         sum += v[i];
@@ -218,11 +241,10 @@ __global__ void __launch_bounds__(kThreads) sort_few(Params p)
         for (int e = threadIdx.x; e < p.E; e += kThreads)
             order[e] = 0u;
         __syncthreads();
-        for (uint32_t i = threadIdx.x; i < p.n; i += kThreads) {
-            const uint32_t key = key_of(p, i);
+        keys_of<kThreads>(p, 0, p.n, threadIdx.x, [&](uint32_t, uint32_t key) {
             if (key < (uint32_t)p.E)
                 atomicAdd(&order[key], 1u);
-        }
+        });
         __syncthreads();
         if (!p.cumsum) {
             for (int e = threadIdx.x; e < p.E; e += kThreads)
@@ -233,15 +255,16 @@ __global__ void __launch_bounds__(kThreads) sort_few(Params p)
             for (int e = threadIdx.x, i = 0; e < p.E; e += kThreads, ++i)
                 own[i] = order[e];
             __syncthreads();
-            block_prefix(order, p.E);
+            block_prefix<kThreads>(order, p.E);
             for (int e = threadIdx.x, i = 0; e < p.E; e += kThreads, ++i)
                 store_num(p, e, order[e] + own[i]);
         }
         return;
     }
     const uint32_t n4 = (p.n + 3) / 4 * 4;
-    for (uint32_t i = threadIdx.x; i < n4; i += kThreads)
-        order[i] = i < p.n ? key_of(p, i) << 12 | i : 0xffffffffu;
+    keys_of<kThreads>(p, 0, p.n, threadIdx.x, [&](uint32_t i, uint32_t key) { order[i] = key << 12 | i; });
+    if (threadIdx.x < n4 - p.n)
+        order[p.n + threadIdx.x] = 0xffffffffu;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
     const int tokens = (int)min((int64_t)p.tokens, p.T - t0), mine = tokens * p.k;
@@ -270,46 +293,94 @@ __global__ void __launch_bounds__(kThreads) sort_few(Params p)
     }
 }
 
-// count[key] of slots lo .. hi - 1, by a block: eight loads a thread under way at once
-template <int THREADS>
-__device__ __forceinline__ void count_keys(const Params &p, uint64_t lo, uint64_t hi, uint32_t *count)
+// behind the table: the number of rows that experts have
+__device__ __forceinline__ uint32_t *used_rows(const Params &p) { return p.table + kChunks * (p.E + 1); }
+
+__device__ __forceinline__ void cluster_barrier()
 {
-    for (uint64_t i = lo + threadIdx.x; i < hi; i += 8 * THREADS) {
-        uint32_t key[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            key[u] = i + u * THREADS < hi ? key_of(p, (uint32_t)(i + u * THREADS)) : 0u;
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (i + u * THREADS < hi)
-                atomicAdd(&count[key[u]], 1u);
-    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// behind the table: the number of rows that experts have
-__device__ __forceinline__ uint32_t *used_rows(const Params &p) { return p.table + (size_t)p.chunks * (p.E + 1); }
+// the word at shared-memory address `at` of block `rank` of the cluster
+__device__ __forceinline__ uint32_t load_from_block(uint32_t at, uint32_t rank)
+{
+    uint32_t there, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(there) : "memory");
+    return v;
+}
 
-// table[c][e] = how often key e (E: none) occurs among chunk c's slots
-__global__ void __launch_bounds__(1024) sort_count(Params p)
+// table[c][e] = the row of chunk c's first slot of key e (E: none).  One cluster; a block has kOfBlock chunks.
+// Shared memory: all[E + 1], and count[kOfBlock][E + 1].
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads) sort_count(Params p)
 {
     mrr::grid_launch_dependents();
-    __shared__ uint32_t count[kMaxE + 1];
-    for (int e = threadIdx.x; e <= p.E; e += 1024)
+    extern __shared__ uint32_t all[];
+    const int keys = p.E + 1;
+    uint32_t *count = all + keys;
+    for (int e = threadIdx.x; e < kOfBlock * keys; e += kCountThreads)
         count[e] = 0u;
     __syncthreads();
-    const uint64_t per = (uint64_t)p.parts * p.tokens * p.k;
-    const uint64_t lo = blockIdx.x * per, hi = min((uint64_t)p.n, lo + per);
-    count_keys<1024>(p, lo, hi, count);
+    {
+        constexpr int kEach = kCountThreads / kOfBlock;
+        const int mine = threadIdx.x / kEach;
+        const uint64_t chunk = blockIdx.x * kOfBlock + mine, per = (uint64_t)p.parts * p.tokens * p.k;
+        keys_of<kEach>(p, (uint32_t)min((uint64_t)p.n, chunk * per), (uint32_t)min((uint64_t)p.n, (chunk + 1) * per),
+                       threadIdx.x % kEach, [&](uint32_t, uint32_t key) { atomicAdd(&count[mine * keys + key], 1u); });
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e <= p.E; e += 1024)
-        p.table[(size_t)blockIdx.x * (p.E + 1) + e] = count[e];
+    // a key's counts to what its chunks ahead, in this block, have; and the block's own
+    for (int e = threadIdx.x; e < keys; e += kCountThreads) {
+        uint32_t sum = 0;
+#pragma unroll
+        for (int c = 0; c < kOfBlock; ++c) {
+            const uint32_t v = count[c * keys + e];
+            count[c * keys + e] = sum;
+            sum += v;
+        }
+        all[e] = sum;
+    }
+    cluster_barrier();
+    uint32_t sum[(kMaxE + kCountThreads) / kCountThreads];
+    const uint32_t from = mrr::smem_addr(all);
+    int turn = 0;
+    for (int e = threadIdx.x; e < keys; e += kCountThreads, ++turn) {
+        uint32_t total = 0, ahead = 0;
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) {
+            const uint32_t v = load_from_block(from + 4 * e, r);
+            total += v;
+            ahead += r < (int)blockIdx.x ? v : 0u;
+        }
+        sum[turn] = total;
+#pragma unroll
+        for (int c = 0; c < kOfBlock; ++c)
+            count[c * keys + e] += ahead;
+    }
+    cluster_barrier();   // all[] is read no more
+    turn = 0;
+    for (int e = threadIdx.x; e < keys; e += kCountThreads, ++turn)
+        all[e] = sum[turn];
+    __syncthreads();
+    block_prefix<kCountThreads>(all, keys);
+    turn = 0;
+    for (int e = threadIdx.x; e < keys; e += kCountThreads, ++turn) {
+        const uint32_t first = all[e];
+#pragma unroll
+        for (int c = 0; c < kOfBlock; ++c)
+            p.table[(size_t)(blockIdx.x * kOfBlock + c) * keys + e] = first + count[c * keys + e];
+        if (blockIdx.x == 0 && e < p.E)
+            store_num(p, e, p.cumsum ? first + sum[turn] : sum[turn]);
+        if (blockIdx.x == 0 && e == p.E)
+            *used_rows(p) = first;
+    }
 }
 
 // Every slot's row, and what moves with slots.  Each block has p.tokens tokens.
 __global__ void __launch_bounds__(kThreads) sort_rank(Params p)
 {
     mrr::grid_launch_dependents();
-    __shared__ uint32_t base[kMaxE + 2];   // of each key: all its slots, then the row of this block's next one
+    __shared__ uint32_t base[kMaxE + 2];   // of each key: the row of this block's next slot
     __shared__ uint32_t before[kMaxE + 1]; // of each key: its slots ahead of this block's
     __shared__ uint32_t rows[kBatch];
     const int lane = threadIdx.x % 32;
@@ -319,35 +390,12 @@ __global__ void __launch_bounds__(kThreads) sort_rank(Params p)
     __syncthreads();
     // slots of this chunk ahead of this block's
     const uint64_t each = (uint64_t)p.tokens * p.k;
-    count_keys<kThreads>(p, chunk * p.parts * each, blockIdx.x * each, before);
+    keys_of<kThreads>(p, (uint32_t)(chunk * p.parts * each), (uint32_t)(blockIdx.x * each), threadIdx.x,
+                      [&](uint32_t, uint32_t key) { atomicAdd(&before[key], 1u); });
     __syncthreads();
     mrr::grid_dependency_wait();   // the table is the previous launch's
-    for (int e = threadIdx.x; e <= p.E; e += kThreads) {
-        uint32_t all = 0, ahead = 0;
-#pragma unroll 8
-        for (int c = 0; c < p.chunks; ++c) {
-            const uint32_t v = p.table[(size_t)c * (p.E + 1) + e];
-            all += v;
-            ahead += c < chunk ? v : 0u;
-        }
-        base[e] = all;
-        before[e] += ahead;
-    }
-    __syncthreads();
-    if (blockIdx.x == 0 && !p.cumsum) {
-        for (int e = threadIdx.x; e < p.E; e += kThreads)
-            store_num(p, e, base[e]);
-        __syncthreads();
-    }
-    block_prefix(base, p.E + 1);
-    if (blockIdx.x == 0 && threadIdx.x == 0)
-        *used_rows(p) = base[p.E];
-    if (blockIdx.x == 0 && p.cumsum)
-        for (int e = threadIdx.x; e < p.E; e += kThreads)
-            store_num(p, e, base[e + 1]);
-    __syncthreads();
     for (int e = threadIdx.x; e <= p.E; e += kThreads)
-        base[e] += before[e];
+        base[e] = before[e] + p.table[(size_t)chunk * (p.E + 1) + e];
 
     const uint32_t s_end = (uint32_t)min((uint64_t)p.n, (blockIdx.x + 1) * each);
     for (uint32_t s0 = (uint32_t)(blockIdx.x * each); s0 < s_end; s0 += kBatch) {
@@ -379,7 +427,7 @@ __global__ void __launch_bounds__(kThreads) sort_rank(Params p)
 // write the rows of zeros.  kEach vectors of a row are loaded before the first is stored, the first ones before the
 // ranks are there (x is no output of the launches before).
 template <int W>
-__global__ void __launch_bounds__(kThreads) sort_move(Params p)
+__global__ void __launch_bounds__(kMoveThreads) sort_move(Params p)
 {
     using V = typename Vec<W>::T;
     constexpr int kEach = vectors_at_once<W>();
@@ -455,16 +503,12 @@ __global__ void __launch_bounds__(kThreads) sort_move(Params p)
     }
 }
 
-// How the work is cut, from the sizes alone (the workspace's size follows from it).  Each block of sort_rank
-// reads chunks * (E + 1) counts and up to parts * tokens * k keys; the two are about equal where
-// parts^2 = groups (E + 1) / (tokens k).
-void cut(int64_t T, int64_t k, int64_t E, int64_t &tokens, int64_t &groups, int64_t &parts, int64_t &chunks)
+// How the work is cut, from the sizes alone.  A chunk is at most 10 of sort_rank's blocks.
+void cut(int64_t T, int64_t &tokens, int64_t &groups, int64_t &parts)
 {
     tokens = (T + kGroups - 1) / kGroups;
     groups = (T + tokens - 1) / tokens;
-    parts = (int64_t)sqrt((double)groups * (double)(E + 1) / (double)(tokens * k));
-    parts = parts < 1 ? 1 : parts > groups ? groups : parts;
-    chunks = (groups + parts - 1) / parts;
+    parts = (groups + kChunks - 1) / kChunks;
 }
 
 bool sizes_ok(int64_t T, int64_t k, int64_t E)
@@ -489,6 +533,24 @@ cudaError_t launch_next(void (*kernel)(Args...), unsigned grid, unsigned threads
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// sort_count's cluster and shared memory are beyond what a kernel may have unasked: asked for once on each device
+cudaError_t allow_count()
+{
+    static std::atomic<uint64_t> done;
+    mrr_device::Info info;
+    if (!mrr_device::current(info))
+        return cudaErrorUnknown;
+    const uint64_t bit = info.device < mrr_device::kMaxDevices ? 1ull << info.device : 0;
+    if (done.load(std::memory_order_acquire) & bit)
+        return cudaSuccess;
+    cudaError_t err = cudaFuncSetAttribute(sort_count, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(sort_count, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (kOfBlock + 1) * (kMaxE + 1));
+    if (err == cudaSuccess && bit)
+        done.fetch_or(bit, std::memory_order_release);
+    return err;
+}
+
 template <int W>
 cudaError_t launch(Params p, bool few, cudaStream_t st)
 {
@@ -499,21 +561,26 @@ cudaError_t launch(Params p, bool few, cudaStream_t st)
         sort_few<W><<<dim3(p.groups + 1, splits), kThreads, 0, st>>>(p);
         return cudaGetLastError();
     }
-    sort_count<<<p.chunks, 1024, 0, st>>>(p);
-    cudaError_t err = launch_next(sort_rank, (unsigned)p.groups, kThreads, st, p);
+    cudaError_t err = allow_count();
+    if (err != cudaSuccess)
+        return err;
+    sort_count<<<kCluster, kCountThreads, 4 * (kOfBlock + 1) * (p.E + 1), st>>>(p);
+    err = cudaGetLastError();
+    if (err == cudaSuccess)
+        err = launch_next(sort_rank, (unsigned)p.groups, kThreads, st, p);
     if (err != cudaSuccess || (!p.out && !p.out_scales))
         return err;
-    // threads of a token: a power of two up to 16, else warps, as few as take no more turns than kThreads would
+    // threads of a token: a power of two up to 16, else warps, as few as take no more turns than kMoveThreads would
     const int64_t columns = (p.row_bytes / W + vectors_at_once<W>() - 1) / vectors_at_once<W>();
     if (columns <= 16) {
         p.group = 1;
         while (p.group < columns)
             p.group *= 2;
     } else {
-        const int64_t turns = (columns + kThreads - 1) / kThreads;
+        const int64_t turns = (columns + kMoveThreads - 1) / kMoveThreads;
         p.group = (int)(((columns + turns - 1) / turns + 31) / 32 * 32);
     }
-    p.move_tokens = kThreads / p.group;
+    p.move_tokens = kMoveThreads / p.group;
     const unsigned threads = p.group * p.move_tokens;   // whole warps
     // behind the tokens' blocks, kGroups for the zeros
     const int64_t blocks = (p.T + p.move_tokens - 1) / p.move_tokens + kGroups;
@@ -530,9 +597,7 @@ size_t moe_sort_workspace(int64_t T, int64_t k, int64_t E)
 {
     if (!sizes_ok(T, k, E) || T * k <= kFewSlots)
         return 0;
-    int64_t tokens, groups, parts, chunks;
-    cut(T, k, E, tokens, groups, parts, chunks);
-    return (size_t)((4 * (chunks * (E + 1) + 1) + 255) / 256 * 256);
+    return (size_t)((4 * (kChunks * (E + 1) + 1) + 255) / 256 * 256);
 }
 
 mrr_status moe_sort_run(const void *expert_idx, int idx_is_i64, int64_t T, int64_t k, int64_t first_expert, int64_t E,
@@ -566,8 +631,8 @@ mrr_status moe_sort_run(const void *expert_idx, int idx_is_i64, int64_t T, int64
         (void)cudaGetLastError();
         return MRR_ERR_CUDA;
     }
-    int64_t tokens, groups, parts, chunks;
-    cut(T, k, E, tokens, groups, parts, chunks);
+    int64_t tokens, groups, parts;
+    cut(T, tokens, groups, parts);
     Params p;
     memset(&p, 0, sizeof(p));
     p.idx = expert_idx;
@@ -600,7 +665,6 @@ mrr_status moe_sort_run(const void *expert_idx, int idx_is_i64, int64_t T, int64
     p.tokens = (int)tokens;
     p.groups = (int)groups;
     p.parts = (int)parts;
-    p.chunks = (int)chunks;
     const bool few = T * k <= kFewSlots;
     // widest vectors that rows, stride and pointers are multiples of
     const uintptr_t all = p.out ? (uintptr_t)x | (uintptr_t)sorted_x | (uintptr_t)row_bytes | (T > 1 ? (uintptr_t)row_stride : 0)
