@@ -11,51 +11,70 @@ using namespace moe_norm;
 
 namespace {
 
-// Rows of 8 bits back to values: a thread has 8 elements of one row.
-template <int DT>
-__global__ void __launch_bounds__(256) dequantize(const uint8_t *q, const void *scales, int kind, int64_t T, int H,
-                                                  int chunks, int wide, void *x)
+// Rows of 8 bits back to values.  A row belongs to a group of threads, each with kAtOnce chunks of 8 elements under way.
+constexpr int kThreads = 128, kAtOnce = 4;
+
+struct Values {
+    const uint8_t *q;
+    const void *scales;
+    void *x;
+    int64_t T;
+    int H, quant, chunks, group, rows;   // threads of a row, rows of a block
+};
+
+// kWide: a chunk's codes come in one load of 8 bytes, its values go in stores of 16
+template <int DT, bool kWide>
+__global__ void __launch_bounds__(kThreads) dequantize(Values p)
 {
-    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = at / chunks;
-    if (row >= T)
+    const int of_block = threadIdx.x / p.group, lane = threadIdx.x - of_block * p.group;
+    const int64_t row = (int64_t)blockIdx.x * p.rows + of_block;
+    if (row >= p.T)
         return;
-    const int c = (int)(at - row * chunks) * 8, n = min(8, H - c);
-    const uint8_t *from = q + row * H + c;
-    uint32_t w[2] = {0u, 0u};
-    if (wide) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(from));
-        w[0] = v.x, w[1] = v.y;
-    } else {
+    const uint8_t *from = p.q + row * p.H;
+    using C = Chunk<DT, kWide ? 16 : DT == MOE_F32 ? 4 : 2>;
+    uint8_t *to = static_cast<uint8_t *>(p.x) + row * p.H * C::kElem;
+    const float of_row = p.quant == MOE_Q_INT8 || p.quant == MOE_Q_E4M3 ? __ldg(static_cast<const float *>(p.scales) + row) : 0.0f;
+    for (int c0 = lane; c0 < p.chunks; c0 += kAtOnce * p.group) {
+        uint32_t w[kAtOnce][2];
+        float s[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n)
-                w[i / 4] |= (uint32_t)__ldg(from + i) << (8 * (i % 4));
-    }
-    float s;
-    if (kind == MOE_Q_MXFP8)
-        s = e8m0_value(__ldg(static_cast<const uint8_t *>(scales) + row * ((H + 63) / 64 * 2) + c / 32));
-    else if (kind == MOE_Q_E4M3_128)
-        s = __ldg(static_cast<const float *>(scales) + row * ((H + 127) / 128) + c / 128);
-    else
-        s = __ldg(static_cast<const float *>(scales) + row);
-    float v[8];
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int c = c0 + u * p.group;
+            w[u][0] = w[u][1] = 0u;
+            s[u] = of_row;
+            if (c >= p.chunks)
+                continue;
+            if (kWide) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(from + 8 * c));
+                w[u][0] = v.x, w[u][1] = v.y;
+            } else {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const uint32_t two = w[i / 4] >> (8 * (i % 4)) & 0xffffu;
-        const float2 f = kind == MOE_Q_INT8 ? make_float2((float)(int8_t)two, (float)(int8_t)(two >> 8)) : decode_e4m3x2(two);
-        v[i] = f.x * s, v[i + 1] = f.y * s;
-    }
-    constexpr int kElem = DT == MOE_F32 ? 4 : 2;
-    uint8_t *to = static_cast<uint8_t *>(x) + row * H * kElem;
-    if (wide) {
-        Chunk<DT, 16> out;
-        out.set(v);
-        out.store(to, c * kElem, H * kElem);
-    } else {
-        Chunk<DT, kElem> out;
-        out.set(v);
-        out.store(to, c * kElem, H * kElem);
+                for (int i = 0; i < 8; ++i)
+                    if (8 * c + i < p.H)
+                        w[u][i / 4] |= (uint32_t)__ldg(from + 8 * c + i) << (8 * (i % 4));
+            }
+            if (p.quant == MOE_Q_MXFP8)
+                s[u] = e8m0_value(__ldg(static_cast<const uint8_t *>(p.scales) + row * ((p.H + 63) / 64 * 2) + c / 4));
+            else if (p.quant == MOE_Q_E4M3_128)
+                s[u] = __ldg(static_cast<const float *>(p.scales) + row * ((p.H + 127) / 128) + c / 16);
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int c = c0 + u * p.group;
+            if (c >= p.chunks)
+                continue;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const uint32_t two = w[u][i / 4] >> (8 * (i % 4)) & 0xffffu;
+                const float2 f = p.quant == MOE_Q_INT8 ? make_float2((float)(int8_t)two, (float)(int8_t)(two >> 8))
+                                                       : decode_e4m3x2(two);
+                v[i] = f.x * s[u], v[i + 1] = f.y * s[u];
+            }
+            C out;
+            out.set(v);
+            out.store(to, c * C::kBytes, p.H * C::kElem);
+        }
     }
 }
 
@@ -130,8 +149,7 @@ mrr_status moe_dequantize_rows_run(const void *q, const void *scales, moe_quant 
         return MRR_ERR_DTYPE;
     if (quant < MOE_Q_INT8 || quant > MOE_Q_MXFP8)
         return MRR_ERR_ATTR;
-    const int64_t chunks = (H + 7) / 8;
-    if (T < 0 || T > INT32_MAX || H < 1 || H > (1 << 20) || T * chunks > 256ll * INT32_MAX)
+    if (T < 0 || T > INT32_MAX || H < 1 || H > (1 << 20))
         return MRR_ERR_SHAPE;
     if (T > 0 && (!q || !scales || !x))
         return MRR_ERR_NULL;
@@ -139,11 +157,28 @@ mrr_status moe_dequantize_rows_run(const void *q, const void *scales, moe_quant 
         return MRR_ERR_ALIGN;
     if (T == 0)
         return MRR_OK;
-    const int wide = H % 8 == 0 && aligned(q, 8) && aligned(x, 16);
-    const unsigned grid = (unsigned)((T * chunks + 255) / 256);
+    const bool wide = H % 8 == 0 && aligned(q, 8) && aligned(x, 16);
+    Values p;
+    memset(&p, 0, sizeof(p));
+    p.q = static_cast<const uint8_t *>(q);
+    p.scales = scales;
+    p.x = x;
+    p.T = T;
+    p.H = (int)H;
+    p.quant = quant;
+    p.chunks = (int)((H + 7) / 8);
+    // many rows: as many threads as have kAtOnce chunks each; few: as have one.  A power of two up to 16, else warps.
+    const int64_t each = T < 2 * 152 ? 1 : kAtOnce, need = (p.chunks + each - 1) / each;
+    p.group = need > 16 ? (int)(need < kThreads ? (need + 31) / 32 * 32 : kThreads) : 1;
+    while (need <= 16 && p.group < need)
+        p.group *= 2;
+    p.rows = kThreads / p.group;
+    const unsigned grid = (unsigned)((T + p.rows - 1) / p.rows), threads = p.group * p.rows;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    auto kernel = dt == MOE_F32 ? dequantize<MOE_F32> : dt == MOE_BF16 ? dequantize<MOE_BF16> : dequantize<MOE_F16>;
-    kernel<<<grid, 256, 0, st>>>(static_cast<const uint8_t *>(q), scales, quant, T, (int)H, (int)chunks, wide, x);
+    auto kernel = dt == MOE_F32    ? (wide ? dequantize<MOE_F32, true> : dequantize<MOE_F32, false>)
+                  : dt == MOE_BF16 ? (wide ? dequantize<MOE_BF16, true> : dequantize<MOE_BF16, false>)
+                                   : (wide ? dequantize<MOE_F16, true> : dequantize<MOE_F16, false>);
+    kernel<<<grid, threads, 0, st>>>(p);
     return done(cudaGetLastError());
 }
 

@@ -7,8 +7,11 @@
 //
 // The blocks stay for many rows and hold their share of grad_weight in registers; each leaves one row of partial
 // sums, which a second launch adds in order.  What a row waits for (its loads, the sum over the block) is hidden by
-// copies that run kStages rows ahead into shared memory: each thread copies, and later reads, its own chunks only,
-// so the copies need no barrier.  Rows that do not fit, or that come in pieces of 2 bytes, are loaded directly.
+// copies that run kStages rows ahead into shared memory: each warp copies, and later reads, its own chunks only,
+// so the copies need no barrier of the block.  Rows that do not fit, or that come in pieces of 2 bytes, are loaded
+// directly.  Accesses to shared memory are what the kernel has least to spare of (with the weight read from there too,
+// 71 % of L1's throughput and 65 us for 8191 x 4100 bfloat16), so the weight is held in registers, and with one chunk
+// a thread so are 16-bit rows, packed as they come.  8191 x 4100: 53 us; 16384 x 7168: 142 us, 6.6 TB/s.
 #pragma once
 
 #include <atomic>
@@ -35,7 +38,7 @@ __device__ __forceinline__ void copy_async(void *to, const void *from)
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(mrr::smem_addr(to)), "l"(from), "n"(W) : "memory");
 }
 
-// The chunks of h, grad_y and grad_h that a thread has of the rows ahead.  kStages 0: none, loaded when asked for.
+// The chunks of h, grad_y and grad_h that a warp has of the rows ahead.  kStages 0: none, loaded when asked for.
 template <int DT, int W, int NV, int kStages>
 struct Ahead {
     using C = Chunk<DT, W>;
@@ -58,21 +61,26 @@ struct Ahead {
 #pragma unroll
                     for (int b = 0; b < C::kBytes; b += 16)
                         *reinterpret_cast<uint4 *>(slot(s, t, i) + b) = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
     }
 
+    // the warp's chunks, in pieces that follow each other from lane to lane
     __device__ __forceinline__ void fetch(int stage, int64_t row, int64_t T) const
     {
         if constexpr (kStages > 0) {
+            __syncwarp();   // the stage's last row has been read
             if (row < T) {
+                const int shift = tid % 32 * (W - C::kBytes);   // from this lane's chunk to its first piece
                 for (int t = 0; t < tensors; ++t) {
                     const uint8_t *src = from[t] + row * size;
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
-                        const int at = (tid + i * threads) * C::kBytes;
+                        const int at = (tid + i * threads) * C::kBytes + shift;
+                        uint8_t *to = slot(stage, t, i) + shift;
 #pragma unroll
-                        for (int b = 0; b < C::kBytes; b += W)
-                            if (at + b < size)
-                                copy_async<W>(slot(stage, t, i) + b, src + at + b);
+                        for (int b = 0; b < C::kBytes / W; ++b)
+                            if (at + 32 * W * b < size)
+                                copy_async<W>(to + 32 * W * b, src + at + 32 * W * b);
                     }
                 }
             }
@@ -82,35 +90,43 @@ struct Ahead {
 
     __device__ __forceinline__ void wait() const
     {
-        if constexpr (kStages > 0)
+        if constexpr (kStages > 0) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages > 0 ? kStages - 1 : 0) : "memory");
+            __syncwarp();
+        }
     }
 
-    __device__ __forceinline__ void get(int stage, int64_t row, int which, int i, float (&v)[8]) const
+    __device__ __forceinline__ C get(int stage, int64_t row, int which, int i) const
     {
         C c;
         if constexpr (kStages > 0) {
             const uint4 *q = reinterpret_cast<const uint4 *>(slot(stage, which, i));
 #pragma unroll
-            for (int b = 0; b < C::kBytes / 16; ++b)
-                c.w[4 * b] = q[b].x, c.w[4 * b + 1] = q[b].y, c.w[4 * b + 2] = q[b].z, c.w[4 * b + 3] = q[b].w;
+            for (int b = 0; b < C::kBytes / 16; ++b) {
+                const uint4 v = q[b];
+                c.w[4 * b] = v.x, c.w[4 * b + 1] = v.y, c.w[4 * b + 2] = v.z, c.w[4 * b + 3] = v.w;
+            }
         } else {
             c.load(from[which] + row * size, (tid + i * threads) * C::kBytes, size);
         }
-        c.get(v);
+        return c;
     }
 };
 
+// Threads of a block at most: of 2 chunks a thread 448, so that two blocks' registers (72 a thread) fit an SM.
+template <int NV, bool kBlock>
+constexpr int most_threads() { return !kBlock ? 32 * kShortWarps : NV == 2 ? 448 : NV <= 4 ? 512 : 1024; }
+
 // NV chunks a thread; kBlock: a block has a row at a time, else each of its warps has one.
 template <int DT, int W, int NV, bool kBlock, int kStages>
-__global__ void __launch_bounds__(kBlock ? (NV > 4 ? 1024 : 512) : 32 * kShortWarps, NV > 4 || !kBlock ? 1 : 2) rms_norm_grad(GradParams p)
+__global__ void __launch_bounds__(most_threads<NV, kBlock>(), NV > 2 || !kBlock ? 1 : 2) rms_norm_grad(GradParams p)
 {
     // (all of it dynamic: together with static memory it could not be allowed up to the device's limit)
     extern __shared__ __align__(16) uint8_t memory[];
     float2 (*sums)[kSumWords] = reinterpret_cast<float2 (*)[kSumWords]>(memory);
     uint8_t *space = memory + kSumBytes;
     mrr::grid_launch_dependents();
-    constexpr bool kWeightHere = NV <= 4;   // up to 64 KB
+    constexpr bool kHoldWeight = NV <= 4, kHoldRow = DT != MOE_F32 && NV == 1;
     const int warp = threadIdx.x / 32;
     const int64_t step = kBlock ? gridDim.x : gridDim.x * kShortWarps;
     Ahead<DT, W, NV, kStages> in;
@@ -122,35 +138,18 @@ __global__ void __launch_bounds__(kBlock ? (NV > 4 ? 1024 : 512) : 32 * kShortWa
     in.tid = kBlock ? threadIdx.x : threadIdx.x % 32;
     in.size = p.H * Chunk<DT, W>::kElem;
     in.slots = NV * blockDim.x;
-    in.own = space + (kWeightHere ? 32 * in.slots : 0) + (kBlock ? in.tid : NV * 32 * warp + in.tid) * Chunk<DT, W>::kBytes;
+    in.own = space + (kBlock ? in.tid : NV * 32 * warp + in.tid) * Chunk<DT, W>::kBytes;
     in.clear();
 
-    // the weight of this thread's chunks as floats, in two planes of 16 bytes a chunk
-    float4 *weight = reinterpret_cast<float4 *>(space) + (kBlock ? in.tid : NV * 32 * warp + in.tid);
-    float acc[NV][8];
+    float acc[NV][8], weight[kHoldWeight ? NV : 1][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (kWeightHere) {
-            float w[8];
-            load_weight<DT, W>(p.weight, p.weight_f32, in.tid + i * in.threads, p.H, w);
-            weight[i * in.threads] = make_float4(w[0], w[1], w[2], w[3]);
-            weight[in.slots + i * in.threads] = make_float4(w[4], w[5], w[6], w[7]);
-        }
+        if (kHoldWeight)
+            load_weight<DT, W>(p.weight, p.weight_f32, in.tid + i * in.threads, p.H, weight[kHoldWeight ? i : 0]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             acc[i][j] = 0.0f;
     }
-    // h, grad_y and the weight of chunk i; read twice a row, which costs less than the threads that registers would
-    auto get = [&](int stage, int64_t row, int i, float (&h)[8], float (&g)[8], float (&w)[8]) {
-        in.get(stage, row, 0, i, h);
-        in.get(stage, row, 1, i, g);
-        if (kWeightHere) {
-            const float4 lo = weight[i * in.threads], hi = weight[in.slots + i * in.threads];
-            w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
-        } else {
-            load_weight<DT, W>(p.weight, p.weight_f32, in.tid + i * in.threads, p.H, w);
-        }
-    };
     const float per_element = 1.0f / (float)p.H;
     int64_t row = kBlock ? blockIdx.x : blockIdx.x * kShortWarps + warp;
     for (int s = 0; s < kStages; ++s)
@@ -158,11 +157,30 @@ __global__ void __launch_bounds__(kBlock ? (NV > 4 ? 1024 : 512) : 32 * kShortWa
     int turn = 0, stage = 0;
     for (; row < p.T; row += step, turn ^= 1) {
         in.wait();
+        Chunk<DT, W> held[kHoldRow ? NV : 1][2];
+        auto get = [&](int i, bool again, float (&h)[8], float (&g)[8]) {
+            const int at = kHoldRow ? i : 0;
+            if (!kHoldRow || !again) {
+                held[at][0] = in.get(stage, row, 0, i);
+                held[at][1] = in.get(stage, row, 1, i);
+            }
+            // (unpacked anew each time: kept as floats they would take twice the registers)
+            if (kHoldRow && again) {
+#pragma unroll
+                for (int j = 0; j < Chunk<DT, W>::kWords; ++j)
+                    asm volatile("" : "+r"(held[at][0].w[j]), "+r"(held[at][1].w[j]));
+            }
+            held[at][0].get(h);
+            held[at][1].get(g);
+            if (!kHoldWeight)
+                load_weight<DT, W>(p.weight, p.weight_f32, in.tid + i * in.threads, p.H, weight[0]);
+        };
         float squares = 0.0f, inner = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float h[8], g[8], w[8];
-            get(stage, row, i, h, g, w);
+            float h[8], g[8];
+            get(i, false, h, g);
+            const float (&w)[8] = weight[kHoldWeight ? i : 0];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 squares = fmaf(h[j], h[j], squares);
@@ -186,10 +204,11 @@ __global__ void __launch_bounds__(kBlock ? (NV > 4 ? 1024 : 512) : 32 * kShortWa
         const float factor = -r * r * r * (inner * per_element);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float h[8], g[8], w[8], d[8];
-            get(stage, row, i, h, g, w);
+            float h[8], g[8], d[8];
+            get(i, true, h, g);
+            const float (&w)[8] = weight[kHoldWeight ? i : 0];
             if (p.grad_h) {
-                in.get(stage, row, 2, i, d);
+                in.get(stage, row, 2, i).get(d);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -255,14 +274,14 @@ cudaError_t launch(const GradParams &p, const mrr_device::Info &info, cudaStream
 {
     const int chunks = (p.H + 7) / 8;
     const unsigned threads = kBlock ? ((chunks + NV - 1) / NV + 31) / 32 * 32 : 32 * kShortWarps;
-    const int slots = NV * (int)threads, stage = (p.grad_h ? 3 : 2) * slots * Chunk<DT, W>::kBytes;
-    const int weight = NV <= 4 ? 32 * slots : 0;
-    const int shares = kBlock ? 0 : kShortWarps * p.H * 4;   // in the place of the rest, at the end
-    auto bytes = [&](int stages) { return weight + stages * stage > shares ? weight + stages * stage : shares; };
+    const int stage = (p.grad_h ? 3 : 2) * NV * (int)threads * Chunk<DT, W>::kBytes;
+    const int shares = kBlock ? 0 : kShortWarps * p.H * 4;   // in the stages' place, at the end
+    auto bytes = [&](int stages) { return stages * stage > shares ? stages * stage : shares; };
     if constexpr (W > 2 && NV <= 4) {
         const int half = info.smem_max / 2 - 1024, whole = info.smem_max - 1024;   // two blocks on an SM, or one
-        if (bytes(4) <= half)
-            return launch<DT, W, NV, kBlock, 4>(p, threads, bytes(4), info, st);
+        // (a fourth stage leaves L1 too little: 75 us where three take 58)
+        if (bytes(3) <= half)
+            return launch<DT, W, NV, kBlock, 3>(p, threads, bytes(3), info, st);
         if (bytes(2) <= whole)
             return launch<DT, W, NV, kBlock, 2>(p, threads, bytes(2), info, st);
     }
@@ -275,8 +294,8 @@ cudaError_t launch_grad(const GradParams &p, const mrr_device::Info &info, cudaS
     const int chunks = (p.H + 7) / 8;
     return chunks <= 32     ? launch<DT, W, 1, false>(p, info, st)
            : chunks <= 128  ? launch<DT, W, 4, false>(p, info, st)
-           : chunks <= 512  ? launch<DT, W, 1, true>(p, info, st)
-           : chunks <= 1024 ? launch<DT, W, 2, true>(p, info, st)
+           : chunks <= 256  ? launch<DT, W, 1, true>(p, info, st)
+           : chunks <= 896  ? launch<DT, W, 2, true>(p, info, st)
            : chunks <= 2048 ? launch<DT, W, 4, true>(p, info, st)
                             : launch<DT, W, 8, true>(p, info, st);
 }

@@ -84,46 +84,56 @@ def mrr_gating_topk_grad_run(grad_y, x, dt, T, e, k, expert_idx, bias, additiona
 # kernels of a few microseconds.
 torch = None
 _lib = None
+_empty = _i32 = _i64 = _f32 = _u8 = None
 _CODES = {}
 
 
 def _load():
-    global torch, _lib
+    global torch, _lib, _empty, _i32, _i64, _f32, _u8
     if _lib is None:
-        _lib = _x._load()
+        lib = _x._load()
         torch = _x.torch
         _CODES.update(_x._CODES)
+        _empty, _i32, _i64, _f32, _u8 = torch.empty, torch.int32, torch.int64, torch.float32, torch.uint8
+        _lib = lib
     return _lib
 
 
-def _rows_of(x, name):
-    """x as [T, H] rows without gaps inside a row: (dtype code, T, H, row stride in elements)."""
-    if not x.is_cuda or x.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+def _stride_of(x, name):
+    """The row stride, in elements, of x as [T, H] rows without gaps inside a row."""
+    if not x.is_cuda or x.dim() != 2 or x.shape[1] < 1:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor with rows of one element or more")
     T, H = x.shape
-    if H < 1:
-        raise ValueError(f"{name}'s rows are empty")
-    stride = H if T < 2 else x.stride(0)
+    if T < 2 or x.is_contiguous():
+        if H > 1 and T and x.stride(1) != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        return H
+    stride = x.stride(0)
     if (H > 1 and x.stride(1) != 1) or stride < H:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return T, H, stride
+    return stride
 
 
-def _index(t, shape, dev, name):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous int32 {list(shape)} on the tensors' device")
+def _slots(t, dev, name):
+    """The shape of an int32 index [T, k]."""
+    shape = t.shape
+    if t.dtype is not _i32 or len(shape) != 2 or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 [T, k] on the tensors' device")
+    return shape
 
 
 def _weight(weight, shape, dev, name):
-    """The code of a weight [T, k], or 0 for None."""
-    if weight is None:
-        return 0
+    """The code of a weight [T, k]."""
     code = _CODES.get(weight.dtype)
     if code is None:
         raise TypeError(f"{name} must be float16, bfloat16 or float32")
-    if tuple(weight.shape) != shape or weight.device != dev or not weight.is_contiguous():
+    if weight.shape != shape or weight.device != dev or not weight.is_contiguous():
         raise ValueError(f"{name} must be contiguous {list(shape)} on the tensors' device")
     return code
+
+
+def _bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def moe_sort_tokens(x, expert_idx, num_experts: int, *, first_expert: int = 0, per_token_scales=None,
@@ -147,44 +157,44 @@ def moe_sort_tokens(x, expert_idx, num_experts: int, *, first_expert: int = 0, p
         return _on(stream, x.device, moe_sort_tokens, x, expert_idx, num_experts, first_expert=first_expert,
                    per_token_scales=per_token_scales, expert_topk_weight=expert_topk_weight,
                    expert_token_num_type=expert_token_num_type, workspace=workspace)
-    T, H, stride = _rows_of(x, "x")
-    dev, kind = x.device, expert_idx.dtype
-    if kind is not torch.int32 and kind is not torch.int64:
+    stride = _stride_of(x, "x")
+    (T, H), dev, kind, slots = x.shape, x.device, expert_idx.dtype, expert_idx.shape
+    if kind is not _i32 and kind is not _i64:
         raise TypeError("expert_idx must be int32 or int64")
-    if expert_idx.dim() != 2 or expert_idx.shape[0] != T or expert_idx.device != dev or not expert_idx.is_contiguous():
+    if len(slots) != 2 or slots[0] != T or expert_idx.device != dev or not expert_idx.is_contiguous():
         raise ValueError("expert_idx must be contiguous [T, k] on x's device")
-    k = expert_idx.shape[1]
+    k = slots[1]
     if not 1 <= k <= 64 or not 1 <= num_experts <= 4096:
         raise ValueError("k must be in 1..64 and num_experts in 1..4096")
     if not -2 ** 63 <= first_expert < 2 ** 63 - 4096:
         raise ValueError("first_expert is out of range")
     scales, weight, n, size = per_token_scales, expert_topk_weight, T * k, x.element_size()
     sorted_scales = sorted_weight = None
-    scale_bytes = 0
+    scale_bytes = weight_dt = 0
     if scales is not None:
-        if scales.dim() < 1 or scales.shape[0] != T or scales.device != dev or not scales.is_contiguous():
+        scale_shape = scales.shape
+        if not scale_shape or scale_shape[0] != T or scales.device != dev or not scales.is_contiguous():
             raise ValueError("per_token_scales must be contiguous [T, ...] on x's device")
-        sorted_scales = torch.empty((n, *scales.shape[1:]), dtype=scales.dtype, device=dev)
         scale_bytes = scales.element_size()
-        for d in scales.shape[1:]:
+        for d in scale_shape[1:]:
             scale_bytes *= d
         if scale_bytes == 0:
             raise ValueError("per_token_scales' rows are empty")
-    weight_dt = _weight(weight, (T, k), dev, "expert_topk_weight")
+        sorted_scales = _empty((n, *scale_shape[1:]), dtype=scales.dtype, device=dev)
     if weight is not None:
-        sorted_weight = torch.empty((n, 1), dtype=torch.float32, device=dev)
-    sorted_x = torch.empty((n, H), dtype=x.dtype, device=dev)
-    token_idx = torch.empty(n, dtype=torch.int32, device=dev)
-    row_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
-    num = torch.empty(num_experts, dtype=kind, device=dev)
-    need = lib.moe_sort_workspace(T, k, num_experts)
-    if need or workspace is not None:
-        workspace = _space(workspace, need, dev)
+        weight_dt = _weight(weight, slots, dev, "expert_topk_weight")
+        sorted_weight = _empty((n, 1), dtype=_f32, device=dev)
+    sorted_x = _empty((n, H), dtype=x.dtype, device=dev)
+    token_idx = _empty(n, dtype=_i32, device=dev)
+    row_idx = _empty(slots, dtype=_i32, device=dev)
+    num = _empty(num_experts, dtype=kind, device=dev)
+    if n > 4096 or workspace is not None:   # (none is needed for fewer slots)
+        workspace = _space(workspace, lib.moe_sort_workspace(T, k, num_experts), dev)
     _run(lib.moe_sort_run, "moe_sort_run",
-         (expert_idx.data_ptr(), int(kind is torch.int64), T, k, first_expert, num_experts, x.data_ptr(), H * size,
+         (expert_idx.data_ptr(), int(kind is _i64), T, k, first_expert, num_experts, x.data_ptr(), H * size,
           stride * size, _ptr(scales), scale_bytes, _ptr(weight), weight_dt, sorted_x.data_ptr(), _ptr(sorted_scales),
           _ptr(sorted_weight), token_idx.data_ptr(), row_idx.data_ptr(), num.data_ptr(), expert_token_num_type,
-          _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()), dev)
+          _ptr(workspace), _bytes(workspace)), dev)
     return sorted_x, sorted_scales, token_idx, row_idx, num, sorted_weight
 
 
@@ -198,19 +208,16 @@ def moe_combine_tokens(rows, row_idx, weight=None, *, stream=None):
     lib = _lib or _load()
     if stream is not None:
         return _on(stream, rows.device, moe_combine_tokens, rows, row_idx, weight)
-    R, H, stride = _rows_of(rows, "rows")
-    dev = rows.device
+    shape, dev = rows.shape, rows.device
     code = _CODES.get(rows.dtype)
     if code is None:
         raise TypeError("rows must be float16, bfloat16 or float32")
-    if stride != H:
-        raise ValueError("rows must be contiguous")
-    if row_idx.dim() != 2:
-        raise ValueError("row_idx must be [T, k]")
-    T, k = shape = tuple(row_idx.shape)
-    _index(row_idx, shape, dev, "row_idx")
-    weight_dt = _weight(weight, shape, dev, "weight")
-    y = torch.empty((T, H), dtype=rows.dtype, device=dev)
+    if len(shape) != 2 or not shape[1] or not rows.is_cuda or not rows.is_contiguous():
+        raise ValueError("rows must be a contiguous 2-D CUDA tensor")
+    R, H = shape
+    T, k = slots = _slots(row_idx, dev, "row_idx")
+    weight_dt = 0 if weight is None else _weight(weight, slots, dev, "weight")
+    y = _empty((T, H), dtype=rows.dtype, device=dev)
     _run(lib.moe_combine_run, "moe_combine_run",
          (rows.data_ptr(), code, R, H, row_idx.data_ptr(), T, k, _ptr(weight), weight_dt, y.data_ptr()), dev)
     return y
@@ -231,34 +238,38 @@ def moe_combine_tokens_grad(grad_y, rows, row_idx, token_idx, weight=None, *, st
     lib = _lib or _load()
     if stream is not None:
         return _on(stream, grad_y.device, moe_combine_tokens_grad, grad_y, rows, row_idx, token_idx, weight)
-    T, H, stride = _rows_of(grad_y, "grad_y")
-    R, _, row_stride = _rows_of(rows, "rows")
-    dev = grad_y.device
-    code = _CODES.get(grad_y.dtype)
+    shape, dev, dtype = grad_y.shape, grad_y.device, grad_y.dtype
+    code = _CODES.get(dtype)
     if code is None:
         raise TypeError("grad_y must be float16, bfloat16 or float32")
-    if rows.dtype != grad_y.dtype:
+    if rows.dtype is not dtype:
         raise TypeError("rows must have grad_y's type")
-    if stride != H or row_stride != H or rows.shape[1] != H or rows.device != dev:
-        raise ValueError("grad_y [T, H] and rows [R, H] must be contiguous and on one device")
-    if row_idx.dim() != 2 or row_idx.shape[0] != T:
+    if len(shape) != 2 or not shape[1] or not grad_y.is_cuda or not grad_y.is_contiguous():
+        raise ValueError("grad_y must be a contiguous 2-D CUDA tensor")
+    T, H = shape
+    if rows.dim() != 2 or rows.shape[1] != H or rows.device != dev or not rows.is_contiguous():
+        raise ValueError("rows must be contiguous [R, H] on grad_y's device")
+    R = rows.shape[0]
+    slots = _slots(row_idx, dev, "row_idx")
+    if slots[0] != T:
         raise ValueError("row_idx must be [T, k]")
-    shape = tuple(row_idx.shape)
-    _index(row_idx, shape, dev, "row_idx")
-    _index(token_idx, (R,), dev, "token_idx")
-    weight_dt = _weight(weight, shape, dev, "weight")
-    grad_rows = torch.empty((R, H), dtype=grad_y.dtype, device=dev)
-    grad_weight = None if weight is None else torch.empty(shape, dtype=weight.dtype, device=dev)
+    if token_idx.dtype is not _i32 or token_idx.shape != (R,) or token_idx.device != dev or not token_idx.is_contiguous():
+        raise ValueError("token_idx must be contiguous int32 [R] on the tensors' device")
+    weight_dt, grad_weight = 0, None
+    if weight is not None:
+        weight_dt = _weight(weight, slots, dev, "weight")
+        grad_weight = _empty(slots, dtype=weight.dtype, device=dev)
+    grad_rows = _empty((R, H), dtype=dtype, device=dev)
     _run(lib.moe_combine_grad_run, "moe_combine_grad_run",
-         (grad_y.data_ptr(), rows.data_ptr(), code, R, H, row_idx.data_ptr(), token_idx.data_ptr(), T, shape[1],
+         (grad_y.data_ptr(), rows.data_ptr(), code, R, H, row_idx.data_ptr(), token_idx.data_ptr(), T, slots[1],
           _ptr(weight), weight_dt, grad_rows.data_ptr(), _ptr(grad_weight)), dev)
     return grad_rows, grad_weight
 
 
 def _norm_weight(weight, dtype, H, dev):
-    if weight.dtype is not dtype and weight.dtype is not torch.float32:
+    if weight.dtype is not dtype and weight.dtype is not _f32:
         raise TypeError("weight must be float32 or of the rows' type")
-    if tuple(weight.shape) != (H,) or weight.device != dev or not weight.is_contiguous():
+    if weight.shape != (H,) or weight.device != dev or not weight.is_contiguous():
         raise ValueError("weight must be contiguous [H] on the rows' device")
     return _CODES[weight.dtype]
 
@@ -282,8 +293,9 @@ def moe_add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, quant=None,
     lib = _lib or _load()
     if stream is not None:
         return _on(stream, x.device, moe_add_rms_norm, x, weight, residual, eps=eps, quant=quant, return_y=return_y)
-    T, H, stride = _rows_of(x, "x")
-    dtype, dev = x.dtype, x.device
+    stride = _stride_of(x, "x")
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    T, H = shape
     code = _CODES.get(dtype)
     if code is None:
         raise TypeError("x must be float16, bfloat16 or float32")
@@ -295,27 +307,28 @@ def moe_add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, quant=None,
     if not eps >= 0.0:
         raise ValueError("eps must not be negative")
     weight_dt = _norm_weight(weight, dtype, H, dev)
-    h, residual_stride = x, 0
+    h, h_out, residual_stride = x, None, 0
     if residual is not None:
-        _, _, residual_stride = _rows_of(residual, "residual")
-        if residual.dtype is not dtype or residual.shape != x.shape or residual.device != dev:
+        residual_stride = _stride_of(residual, "residual")
+        if residual.dtype is not dtype or residual.shape != shape or residual.device != dev:
             raise ValueError("residual must be like x")
-        h = torch.empty((T, H), dtype=dtype, device=dev)
-    y = torch.empty((T, H), dtype=dtype, device=dev) if return_y else None
+        h = _empty(shape, dtype=dtype, device=dev)
+        h_out = h.data_ptr()
+    y = _empty(shape, dtype=dtype, device=dev) if return_y else None
     q = scales = None
     if kind == MOE_Q_MXFP4:
         if H % 2:
             raise ValueError("mxfp4 rows need an even H")
-        q = torch.empty((T, H // 2), dtype=torch.uint8, device=dev)
+        q = _empty((T, H // 2), dtype=_u8, device=dev)
     elif kind != MOE_Q_NONE:
-        q = torch.empty((T, H), dtype=torch.int8 if kind == MOE_Q_INT8 else torch.float8_e4m3fn, device=dev)
+        q = _empty(shape, dtype=torch.int8 if kind == MOE_Q_INT8 else torch.float8_e4m3fn, device=dev)
     if kind == MOE_Q_MXFP8 or kind == MOE_Q_MXFP4:
-        scales = torch.empty((T, (H + 63) // 64, 2), dtype=torch.uint8, device=dev)
+        scales = _empty((T, (H + 63) // 64, 2), dtype=_u8, device=dev)
     elif kind != MOE_Q_NONE:
-        scales = torch.empty((T, (H + 127) // 128) if kind == MOE_Q_E4M3_128 else (T,), dtype=torch.float32, device=dev)
+        scales = _empty((T, (H + 127) // 128) if kind == MOE_Q_E4M3_128 else (T,), dtype=_f32, device=dev)
     _run(lib.moe_add_rms_norm_run, "moe_add_rms_norm_run",
-         (x.data_ptr(), _ptr(residual), code, T, H, stride, residual_stride, weight.data_ptr(), weight_dt, eps,
-          None if residual is None else h.data_ptr(), _ptr(y), kind, _ptr(q), _ptr(scales)), dev)
+         (x.data_ptr(), _ptr(residual), code, T, H, stride, residual_stride, weight.data_ptr(), weight_dt, eps, h_out,
+          _ptr(y), kind, _ptr(q), _ptr(scales)), dev)
     return y, h, q, scales
 
 
@@ -326,23 +339,25 @@ def moe_add_rms_norm_grad(grad_y, h, weight, *, grad_h=None, eps: float = 1e-6, 
     lib = _lib or _load()
     if stream is not None:
         return _on(stream, h.device, moe_add_rms_norm_grad, grad_y, h, weight, grad_h=grad_h, eps=eps, workspace=workspace)
-    T, H, _ = _rows_of(h, "h")
-    dtype, dev = h.dtype, h.device
+    shape, dtype, dev = h.shape, h.dtype, h.device
     code = _CODES.get(dtype)
     if code is None:
         raise TypeError("h must be float16, bfloat16 or float32")
+    if len(shape) != 2 or not shape[1] or not h.is_cuda:
+        raise ValueError("h must be a 2-D CUDA tensor with rows of one element or more")
     for t in (grad_y, h) if grad_h is None else (grad_y, h, grad_h):
-        if t.dtype is not dtype or tuple(t.shape) != (T, H) or t.device != dev or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
             raise ValueError("grad_y, h and grad_h must be contiguous [T, H] of one type and device")
     if not eps >= 0.0:
         raise ValueError("eps must not be negative")
+    T, H = shape
     weight_dt = _norm_weight(weight, dtype, H, dev)
-    grad_x = torch.empty((T, H), dtype=dtype, device=dev)
-    grad_weight = torch.empty(H, dtype=weight.dtype, device=dev)
+    grad_x = _empty(shape, dtype=dtype, device=dev)
+    grad_weight = _empty(H, dtype=weight.dtype, device=dev)
     workspace = _space(workspace, lib.moe_add_rms_norm_grad_workspace(T, H), dev)
     _run(lib.moe_add_rms_norm_grad_run, "moe_add_rms_norm_grad_run",
          (grad_y.data_ptr(), h.data_ptr(), _ptr(grad_h), code, T, H, weight.data_ptr(), weight_dt, eps,
-          grad_x.data_ptr(), grad_weight.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size()), dev)
+          grad_x.data_ptr(), grad_weight.data_ptr(), workspace.data_ptr(), _bytes(workspace)), dev)
     return grad_x, grad_weight
 
 
@@ -357,22 +372,25 @@ def moe_dequantize_rows(q, scales, dtype=None, *, stream=None):
     code = _CODES.get(dtype)
     if code is None:
         raise TypeError("dtype must be float16, bfloat16 or float32")
-    if q.dtype is not torch.int8 and q.dtype is not torch.float8_e4m3fn:
+    is_int8, shape, dev = q.dtype is torch.int8, q.shape, q.device
+    if not is_int8 and q.dtype is not torch.float8_e4m3fn:
         raise TypeError("q must be int8 or float8_e4m3fn")
-    T, H, stride = _rows_of(q, "q")
-    dev, shape = q.device, tuple(scales.shape)
-    if stride != H or scales.device != dev or not scales.is_contiguous():
-        raise ValueError("q and scales must be contiguous and on one device")
-    if scales.dtype is torch.float32 and shape in ((T,), (T, 1)) and (len(shape) == 1 or q.dtype is torch.int8 or H <= 128):
-        kind = MOE_Q_INT8 if q.dtype is torch.int8 else MOE_Q_E4M3
-    elif q.dtype is torch.float8_e4m3fn and scales.dtype is torch.float32 and shape == (T, (H + 127) // 128):
+    if len(shape) != 2 or not shape[1] or not q.is_cuda or not q.is_contiguous():
+        raise ValueError("q must be a contiguous 2-D CUDA tensor")
+    if scales.device != dev or not scales.is_contiguous():
+        raise ValueError("scales must be contiguous and on q's device")
+    T, H = shape
+    of, is_f32 = scales.shape, scales.dtype is _f32
+    if is_f32 and (of == (T,) or is_int8 and of == (T, 1)):
+        kind = MOE_Q_INT8 if is_int8 else MOE_Q_E4M3
+    elif is_f32 and not is_int8 and of == (T, (H + 127) // 128):
         kind = MOE_Q_E4M3_128
-    elif q.dtype is torch.float8_e4m3fn and scales.element_size() == 1 and shape == (T, (H + 63) // 64, 2):
+    elif not is_int8 and scales.element_size() == 1 and of == (T, (H + 63) // 64, 2):
         kind = MOE_Q_MXFP8
     else:
-        raise ValueError("scales must be float32 [T] (or [T, ceil(H/128)] with e4m3 rows), or e8m0 bytes "
-                         "[T, ceil(H/64), 2] with e4m3 rows")
-    x = torch.empty((T, H), dtype=dtype, device=dev)
+        raise ValueError("scales must be float32 [T] (int8 also [T, 1], e4m3 also [T, ceil(H/128)]), or with e4m3 rows "
+                         "e8m0 bytes [T, ceil(H/64), 2]")
+    x = _empty(shape, dtype=dtype, device=dev)
     _run(lib.moe_dequantize_rows_run, "moe_dequantize_rows_run",
          (q.data_ptr(), scales.data_ptr(), kind, T, H, code, x.data_ptr()), dev)
     return x
@@ -400,16 +418,17 @@ def moe_gating_top_k_grad(grad_y, x, expert_idx, *, bias=None, additional_bias=N
     code = _CODES.get(dtype)
     if code is None:
         raise TypeError("x must be float16, bfloat16 or float32")
-    *lead, e = x.shape
-    k = expert_idx.shape[-1]
-    if grad_y.dtype is not dtype or grad_y.shape != (*lead, k) or grad_y.device != dev or not grad_y.is_contiguous():
+    shape, of = x.shape, expert_idx.shape
+    e, k = shape[-1], of[-1]
+    if expert_idx.dtype is not _i32 or of[:-1] != shape[:-1] or expert_idx.device != dev or not expert_idx.is_contiguous():
+        raise ValueError("expert_idx must be contiguous int32 [..., k] on x's device")
+    if grad_y.dtype is not dtype or grad_y.shape != of or grad_y.device != dev or not grad_y.is_contiguous():
         raise ValueError("grad_y must be contiguous [..., k] in x's type on x's device")
-    _index(expert_idx, (*lead, k), dev, "expert_idx")
-    if grad_out is not None and (grad_out.dtype is not torch.float32 or grad_out.shape != x.shape
+    if grad_out is not None and (grad_out.dtype is not _f32 or grad_out.shape != shape
                                  or grad_out.device != dev or not grad_out.is_contiguous()):
         raise ValueError("grad_out must be contiguous float32 like x")
     T = 1
-    for d in lead:
+    for d in shape[:-1]:
         T *= d
     for b in (bias, additional_bias):
         if b is not None and (b.dtype is not dtype or b.numel() != e or b.device != dev or not b.is_contiguous()):
@@ -418,13 +437,13 @@ def moe_gating_top_k_grad(grad_y, x, expert_idx, *, bias=None, additional_bias=N
     if mask is not None:
         if mask.dtype is not torch.bool or mask.numel() != T or mask.device != dev or not mask.is_contiguous():
             raise ValueError("additional_token_mask must be contiguous [T] bool on x's device")
-    grad_x = torch.empty_like(x)
-    grad_bias = None if bias is None else torch.empty(e, dtype=dtype, device=dev)
-    grad_extra = None if additional_bias is None else torch.empty(e, dtype=dtype, device=dev)
+    grad_x = _empty(shape, dtype=dtype, device=dev)
+    grad_bias = None if bias is None else _empty(e, dtype=dtype, device=dev)
+    grad_extra = None if additional_bias is None else _empty(e, dtype=dtype, device=dev)
     if bias is not None or additional_bias is not None or workspace is not None:
         workspace = _space(workspace, lib.mrr_gating_topk_grad_workspace(T, e), dev)
     _run(lib.mrr_gating_topk_grad_run, "mrr_gating_topk_grad_run",
          (grad_y.data_ptr(), x.data_ptr(), code, T, e, k, expert_idx.data_ptr(), _ptr(bias), _ptr(additional_bias),
           _ptr(mask), _ptr(grad_out), routed_scaling_factor, eps, norm_type, grad_x.data_ptr(), _ptr(grad_bias),
-          _ptr(grad_extra), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()), dev)
+          _ptr(grad_extra), _ptr(workspace), _bytes(workspace)), dev)
     return grad_x, grad_bias, grad_extra
