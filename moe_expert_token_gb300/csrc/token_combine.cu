@@ -17,7 +17,6 @@ using namespace moe_mx;
 namespace {
 
 constexpr int kThreads = 64;    // most threads of a block (at 16384 x 7168 bfloat16, k = 8: 256 threads 334 us, 128 316, 64 314, 32 329)
-constexpr int kWarps = kThreads / 32;
 using moe_rows::kFull;
 
 // W bytes of consecutive elements of DT, as they lie in memory
@@ -129,9 +128,9 @@ __host__ __device__ constexpr int pieces_at_once()
     return (R == 8 ? 1 : R == 1 ? 4 : 2) * (W >= 4 ? 16 / W : 4);
 }
 
-// Threads of a token whose row is `columns` threads' work: a power of two up to 16, else warps, at most kThreads, and as
-// few as take no more turns than kThreads would.
-int group_of(int64_t columns)
+// Threads of a token whose row is `columns` threads' work: a power of two up to 16, else warps, at most `most`, and as
+// few as take no more turns than those would.
+int group_of(int64_t columns, int most)
 {
     if (columns <= 16) {
         int g = 1;
@@ -139,7 +138,7 @@ int group_of(int64_t columns)
             g *= 2;
         return g;
     }
-    const int64_t turns = (columns + kThreads - 1) / kThreads;
+    const int64_t turns = (columns + most - 1) / most;
     return (int)(((columns + turns - 1) / turns + 31) / 32 * 32);
 }
 
@@ -160,7 +159,7 @@ __device__ __forceinline__ void load_slots(const Params &p, int64_t t, int j0, i
     }
 }
 
-// R rows at once
+// R rows at once.  Where tokens are few, several blocks (the y index) share a token's columns.
 template <int DT, int W, int R>
 __global__ void __launch_bounds__(kThreads, W > 2 ? 12 : 8) combine(Params p)
 {
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, W > 2 ? 12 : 8) combine(Params p)
     int row[R];
     float weight[R];
     load_slots<R>(p, t, 0, row, weight);
-    for (int c = lane; c < pieces; c += U * p.group) {
+    for (int c = blockIdx.y * U * p.group + lane; c < pieces; c += gridDim.y * U * p.group) {
         float sum[U][P::kEach];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -217,12 +216,12 @@ __global__ void __launch_bounds__(kThreads, W > 2 ? 12 : 8) combine(Params p)
 
 // A thread's sums of R slots stay while it goes through the columns.  The blocks behind the tokens' write the rows of
 // zeros, each every `zero_blocks`th row: these rows follow one another.
-template <int DT, int W, int R>
-__global__ void __launch_bounds__(kThreads, W == 16 ? 10 : 8) combine_grad(Params p)
+template <int DT, int W, int R, int THREADS>
+__global__ void __launch_bounds__(THREADS, (W == 16 ? 640 : 512) / THREADS) combine_grad(Params p)
 {
     using P = Piece<DT, W>;
     constexpr int U = pieces_at_once<W, R>();
-    __shared__ float part[kWarps][R];
+    __shared__ float part[THREADS / 32][R];
     const int lane32 = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int pieces = p.H / P::kEach;
     const int64_t token_blocks = (p.T + p.tokens - 1) / p.tokens;
@@ -314,26 +313,48 @@ __global__ void __launch_bounds__(kThreads, W == 16 ? 10 : 8) combine_grad(Param
     }
 }
 
+constexpr int kFewTokens = 304;        // for the gradient
+constexpr int kFewBlocks = 4 * 152;    // fewer than these of one group each leave SMs idle
+
+template <int DT, int W, int R, int THREADS>
+void launch_grad(Params p, cudaStream_t st)
+{
+    const int64_t columns = p.H / Piece<DT, W>::kEach, at_once = pieces_at_once<W, R>();
+    p.group = group_of((columns + at_once - 1) / at_once, THREADS);
+    p.tokens = THREADS / p.group;
+    const int threads = p.group * p.tokens;   // whole warps
+    // behind the tokens' blocks, one for each `threads` rows (32 or more)
+    const int64_t blocks = (p.T + p.tokens - 1) / p.tokens + (p.R + threads - 1) / threads;
+    combine_grad<DT, W, R, THREADS><<<(unsigned)blocks, threads, 0, st>>>(p);
+}
+
 template <int DT, int W, int R>
 void launch(Params p, bool grad, cudaStream_t st)
 {
-    const int64_t columns = p.H / Piece<DT, W>::kEach, at_once = pieces_at_once<W, R>();
-    p.group = group_of((columns + at_once - 1) / at_once);
-    p.tokens = kThreads / p.group;
-    const int threads = p.group * p.tokens;   // whole warps
-    const int64_t blocks = (p.T + p.tokens - 1) / p.tokens;
     if (grad) {
-        // behind the tokens' blocks, one for each `threads` rows (32 or more)
-        combine_grad<DT, W, R><<<(unsigned)(blocks + (p.R + threads - 1) / threads), threads, 0, st>>>(p);
-    } else if (blocks > 0) {
-        combine<DT, W, R><<<(unsigned)blocks, threads, 0, st>>>(p);
+        // few tokens: more threads to each (1 token of 7168 from 8 experts: 8.6 us with 256 threads, 16.5 with 64; 64
+        // tokens 10.5 and 20.5; 400 tokens 22.8 and 24.8; 500 of 2048 from 2 experts 10.2 and 6.5)
+        if (R == 8 && p.T < kFewTokens)
+            launch_grad<DT, W, R, R == 8 ? 256 : kThreads>(p, st);
+        else
+            launch_grad<DT, W, R, kThreads>(p, st);
+        return;
     }
+    const int64_t pieces = p.H / Piece<DT, W>::kEach, at_once = pieces_at_once<W, R>(), columns = (pieces + at_once - 1) / at_once;
+    p.group = group_of(columns, kThreads);
+    p.tokens = kThreads / p.group;
+    const int64_t blocks = (p.T + p.tokens - 1) / p.tokens;
+    if (blocks == 0)
+        return;
+    // (3 tokens of 5120: 4.8 us, and 11.2 without sharing a row; 64 of 7168: 6.8 and 14.3)
+    const int64_t turns = (columns + p.group - 1) / p.group, want = blocks < kFewBlocks ? kFewBlocks / blocks : 1;
+    combine<DT, W, R><<<dim3((unsigned)blocks, (unsigned)(turns < want ? turns : want)), p.group * p.tokens, 0, st>>>(p);
 }
 
 template <int DT, int W>
 void launch(const Params &p, bool grad, cudaStream_t st)
 {
-    if (p.k > 4)
+    if (p.k > 4 || (grad && p.T < kFewTokens))
         launch<DT, W, 8>(p, grad, st);
     else if (p.k > 2)
         launch<DT, W, 4>(p, grad, st);
