@@ -27,6 +27,9 @@ constexpr int kWarps = kThreads / 32;
 using moe_rows::kFull;
 constexpr uint32_t kNone = 0x80000000u;   // beside a row: the slot has no expert here, the row is zeros
 constexpr int kMoveThreads = 256;         // most threads of a block of sort_move
+constexpr int kMoveAtOnce = 4;            // vectors of a row that one of them has under way
+constexpr int kAnyThreads = 128;          // of sort_move_any
+constexpr int kAnySegment = 8192;         // bytes of a row that it has in shared memory
 constexpr int kFewSlots = 4096;
 constexpr int kFewMine = 128;             // most slots of a block of sort_few
 constexpr int kBatch = 1024;              // slots that a block of sort_rank ranks at once
@@ -95,9 +98,11 @@ struct Vec<2> { using T = uint16_t; };
 template <>
 struct Vec<1> { using T = uint8_t; };
 
-// vectors of a row that a thread of sort_move has under way at once
-template <int W>
-__host__ __device__ constexpr int vectors_at_once() { return W == 16 ? 4 : 8; }
+// shared memory of a token of sort_move_any: a segment that begins anywhere in 16 bytes, and a word of 16 behind it
+__host__ __device__ __forceinline__ int any_space(int64_t row_bytes)
+{
+    return (int)((row_bytes < kAnySegment ? row_bytes : kAnySegment) + 15) / 16 * 16 + 32;
+}
 
 template <typename V>
 __device__ __forceinline__ V zero_of()
@@ -423,38 +428,63 @@ __global__ void __launch_bounds__(kThreads) sort_rank(Params p)
     }
 }
 
+// The scale rows of a token: 4-byte units where rows and both pointers allow it, else bytes.
+__device__ __forceinline__ void move_scales(const Params &p, int64_t t, int lane)
+{
+    if (!p.out_scales)
+        return;
+    const int32_t *rows = p.row_idx + t * p.k;
+    const int units = (int)(p.scale_row_bytes / p.scale_unit);
+    for (int c = lane; c < units; c += p.group) {
+        if (p.scale_unit == 4) {
+            const uint32_t s = __ldg(reinterpret_cast<const uint32_t *>(p.scales) + t * units + c);
+            for (int j = 0; j < p.k; ++j)
+                if (rows[j] >= 0)
+                    reinterpret_cast<uint32_t *>(p.out_scales)[(int64_t)rows[j] * units + c] = s;
+        } else {
+            const uint8_t s = __ldg(p.scales + t * units + c);
+            for (int j = 0; j < p.k; ++j)
+                if (rows[j] >= 0)
+                    p.out_scales[(int64_t)rows[j] * units + c] = s;
+        }
+    }
+}
+
+// A block's share of the bytes behind the last expert's rows, in 16-byte units.
+__device__ __forceinline__ void clear_rest(const Params &p, int64_t block, int64_t blocks)
+{
+    const int64_t used = *used_rows(p);
+    auto share = [&](uint8_t *out, int64_t row_bytes) {
+        const int64_t lo = used * row_bytes, all = p.n * row_bytes - lo;
+        const int64_t per = (all + 16 * blocks - 1) / (16 * blocks) * 16, at = block * per;
+        if (at < all)
+            moe_rows::clear<1>(out, lo + at, min(per, all - at), threadIdx.x, blockDim.x);
+    };
+    if (p.out)
+        share(p.out, p.row_bytes);
+    if (p.out_scales)
+        share(p.out_scales, p.scale_row_bytes);
+}
+
 // The rows, of p.move_tokens tokens a block and a group of p.group threads to a token, and behind them blocks that
 // write the rows of zeros.  kEach vectors of a row are loaded before the first is stored, the first ones before the
 // ranks are there (x is no output of the launches before).
-template <int W>
 __global__ void __launch_bounds__(kMoveThreads) sort_move(Params p)
 {
-    using V = typename Vec<W>::T;
-    constexpr int kEach = vectors_at_once<W>();
+    constexpr int kEach = kMoveAtOnce;
     const int64_t token_blocks = (p.T + p.move_tokens - 1) / p.move_tokens;
-    const int vectors = (int)(p.row_bytes / W);
+    const int vectors = (int)(p.row_bytes / 16);
     if (blockIdx.x >= token_blocks) {
         mrr::grid_dependency_wait();
-        // a share of the bytes behind the last expert's rows, in 16-byte units
-        const int64_t used = *used_rows(p);
-        auto share = [&](uint8_t *out, int64_t row_bytes) {
-            const int64_t lo = used * row_bytes, all = p.n * row_bytes - lo, blocks = gridDim.x - token_blocks;
-            const int64_t per = (all + 16 * blocks - 1) / (16 * blocks) * 16, at = (blockIdx.x - token_blocks) * per;
-            if (at < all)
-                moe_rows::clear<1>(out, lo + at, min(per, all - at), threadIdx.x, blockDim.x);
-        };
-        if (p.out)
-            share(p.out, p.row_bytes);
-        if (p.out_scales)
-            share(p.out_scales, p.scale_row_bytes);
+        clear_rest(p, blockIdx.x - token_blocks, gridDim.x - token_blocks);
         return;
     }
     const int of_block = threadIdx.x / p.group, lane = threadIdx.x - of_block * p.group;
     const int64_t t = (int64_t)blockIdx.x * p.move_tokens + of_block;
     if (t >= p.T)
         return;
-    const V *from = reinterpret_cast<const V *>(p.x + t * p.row_stride);
-    V v[kEach];
+    const uint4 *from = reinterpret_cast<const uint4 *>(p.x + t * p.row_stride);
+    uint4 v[kEach];
     auto load = [&](int c) {
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
@@ -474,7 +504,7 @@ __global__ void __launch_bounds__(kMoveThreads) sort_move(Params p)
             for (int j = 0; j < 8; ++j) {
                 if (row[j] < 0)
                     continue;
-                V *to = reinterpret_cast<V *>(p.out + row[j] * p.row_bytes);
+                uint4 *to = reinterpret_cast<uint4 *>(p.out + row[j] * p.row_bytes);
 #pragma unroll
                 for (int i = 0; i < kEach; ++i)
                     if (c + i * p.group < vectors)
@@ -484,23 +514,95 @@ __global__ void __launch_bounds__(kMoveThreads) sort_move(Params p)
         c += kEach * p.group;
         load(c);
     }
-    if (!p.out_scales)
+    move_scales(p, t, lane);
+}
+
+// `size` bytes that begin `ahead` bytes behind a 16-byte boundary, as whole words of 16 from `first` to `last` (counted from
+// the boundary) and the bytes at both ends that share their 16 with something else.
+struct Ends {
+    int first, last, bytes, head, start;
+
+    __device__ __forceinline__ Ends(int ahead, int size)
+        : first((ahead + 15) & ~15), last((ahead + size) & ~15), start(ahead)
+    {
+        head = min(first - ahead, size);
+        bytes = first > last ? size : head + ahead + size - last;
+    }
+
+    // the i-th of the bytes
+    __device__ __forceinline__ int at(int i) const { return i < head ? start + i : last + i - head; }
+};
+
+// The same for rows of any size and alignment.  A segment of a token's row is brought to shared memory, placed as it lies
+// towards 16-byte boundaries; for each place it goes to, a thread makes the aligned 16 bytes of the output out of two
+// words of shared memory, by a shift that is the same for the whole row.  Bytes at the ends of a segment, that share
+// their 16 with another's, are moved singly, a lane each.  (In pieces of the widest size that all rows are multiples of
+// instead: 8192 x 2049 bfloat16 to 6 experts 66 us, this way 50; 8192 x 4097 int8 to 4 164 and 39.)
+__global__ void __launch_bounds__(kAnyThreads) sort_move_any(Params p)
+{
+    extern __shared__ __align__(16) uint8_t space[];
+    const int64_t token_blocks = (p.T + p.move_tokens - 1) / p.move_tokens;
+    if (blockIdx.x >= token_blocks) {
+        mrr::grid_dependency_wait();
+        clear_rest(p, blockIdx.x - token_blocks, gridDim.x - token_blocks);
         return;
-    // 4-byte units where rows and both pointers allow it, else bytes
-    const int units = (int)(p.scale_row_bytes / p.scale_unit);
-    for (int c = lane; c < units; c += p.group) {
-        if (p.scale_unit == 4) {
-            const uint32_t s = __ldg(reinterpret_cast<const uint32_t *>(p.scales) + t * units + c);
-            for (int j = 0; j < p.k; ++j)
-                if (rows[j] >= 0)
-                    reinterpret_cast<uint32_t *>(p.out_scales)[(int64_t)rows[j] * units + c] = s;
-        } else {
-            const uint8_t s = __ldg(p.scales + t * units + c);
-            for (int j = 0; j < p.k; ++j)
-                if (rows[j] >= 0)
-                    p.out_scales[(int64_t)rows[j] * units + c] = s;
+    }
+    const int of_block = threadIdx.x / p.group, lane = threadIdx.x - of_block * p.group;
+    const int64_t t = (int64_t)blockIdx.x * p.move_tokens + of_block;
+    const bool mine = t < p.T;   // the whole block stays for its barriers
+    const uint8_t *src = p.x + (mine ? t : 0) * p.row_stride;
+    uint8_t *here = space + of_block * any_space(p.row_bytes);
+    const int32_t *rows = p.row_idx + (mine ? t : 0) * p.k;
+    for (int64_t at = 0; at < p.row_bytes; at += kAnySegment) {
+        const int size = (int)min((int64_t)kAnySegment, p.row_bytes - at);
+        const uint8_t *from = src + at;
+        const int shift = (int)((uintptr_t)from % 16);   // where the segment begins in shared memory
+        if (at)
+            __syncthreads();   // the segment before has been read
+        if (mine) {
+            const Ends ends(shift, size);
+            for (int c = ends.first + 16 * lane; c < ends.last; c += 16 * p.group)
+                *reinterpret_cast<uint4 *>(here + c) = __ldg(reinterpret_cast<const uint4 *>(from - shift + c));
+            for (int i = lane; i < ends.bytes; i += p.group)
+                here[ends.at(i)] = __ldg(from - shift + ends.at(i));
+        }
+        __syncthreads();
+        if (at == 0)
+            mrr::grid_dependency_wait();
+        if (!mine)
+            continue;
+        for (int j = 0; j < p.k; ++j) {
+            const int32_t row = rows[j];
+            if (row < 0)
+                continue;
+            uint8_t *to = p.out + row * p.row_bytes + at;
+            const int ahead = (int)((uintptr_t)to % 16);   // of the segment, in its first 16 bytes
+            const uint32_t m = (uint32_t)(shift - ahead) & 15u, bits = (m & 3u) * 8u;
+            const Ends ends(ahead, size);
+            for (int c = ends.first + 16 * lane; c < ends.last; c += 16 * p.group) {
+                const uint4 *q = reinterpret_cast<const uint4 *>(here + (shift - ahead + c - (int)m));
+                const uint4 a = q[0], b = q[1];
+                uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                if (m & 8u) {
+#pragma unroll
+                    for (int i = 0; i < 6; ++i)
+                        w[i] = w[i + 2];
+                }
+                if (m & 4u) {
+#pragma unroll
+                    for (int i = 0; i < 5; ++i)
+                        w[i] = w[i + 1];
+                }
+                *reinterpret_cast<uint4 *>(to - ahead + c) =
+                    make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                               __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+            }
+            for (int i = lane; i < ends.bytes; i += p.group)
+                (to - ahead)[ends.at(i)] = here[shift - ahead + ends.at(i)];
         }
     }
+    if (mine)
+        move_scales(p, t, lane);
 }
 
 // How the work is cut, from the sizes alone.  A chunk is at most 10 of sort_rank's blocks.
@@ -517,13 +619,13 @@ bool sizes_ok(int64_t T, int64_t k, int64_t E)
 }
 
 // a launch that may begin while the one before it on the stream ends
-template <typename... Args>
-cudaError_t launch_next(void (*kernel)(Args...), unsigned grid, unsigned threads, cudaStream_t st, const Params &p)
+cudaError_t launch_next(void (*kernel)(Params), unsigned grid, unsigned threads, int smem, cudaStream_t st, const Params &p)
 {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -531,6 +633,20 @@ cudaError_t launch_next(void (*kernel)(Args...), unsigned grid, unsigned threads
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// threads of a token whose row is `columns` threads' work: a power of two up to 16, else warps, at most `most` and as few
+// as take no more turns than those would
+int group_of(int64_t columns, int most)
+{
+    if (columns <= 16) {
+        int g = 1;
+        while (g < columns)
+            g *= 2;
+        return g;
+    }
+    const int64_t turns = (columns + most - 1) / most;
+    return (int)(((columns + turns - 1) / turns + 31) / 32 * 32);
 }
 
 // sort_count's cluster and shared memory are beyond what a kernel may have unasked: asked for once on each device
@@ -552,39 +668,34 @@ cudaError_t allow_count()
 }
 
 template <int W>
-cudaError_t launch(Params p, bool few, cudaStream_t st)
+cudaError_t launch_few(const Params &p, cudaStream_t st)
 {
-    if (few) {
-        // where tokens are few, several blocks share a token's row, 1 KB each at least
-        const int64_t most = (p.row_bytes + 1023) / 1024, want = kGroups / p.groups;
-        const unsigned splits = (unsigned)(want < 1 || !p.out ? 1 : want < most ? want : most);
-        sort_few<W><<<dim3(p.groups + 1, splits), kThreads, 0, st>>>(p);
-        return cudaGetLastError();
-    }
+    // where tokens are few, several blocks share a token's row, 1 KB each at least
+    const int64_t most = (p.row_bytes + 1023) / 1024, want = kGroups / p.groups;
+    const unsigned splits = (unsigned)(want < 1 || !p.out ? 1 : want < most ? want : most);
+    sort_few<W><<<dim3(p.groups + 1, splits), kThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_many(Params p, bool wide, cudaStream_t st)
+{
     cudaError_t err = allow_count();
     if (err != cudaSuccess)
         return err;
     sort_count<<<kCluster, kCountThreads, 4 * (kOfBlock + 1) * (p.E + 1), st>>>(p);
     err = cudaGetLastError();
     if (err == cudaSuccess)
-        err = launch_next(sort_rank, (unsigned)p.groups, kThreads, st, p);
+        err = launch_next(sort_rank, (unsigned)p.groups, kThreads, 0, st, p);
     if (err != cudaSuccess || (!p.out && !p.out_scales))
         return err;
-    // threads of a token: a power of two up to 16, else warps, as few as take no more turns than kMoveThreads would
-    const int64_t columns = (p.row_bytes / W + vectors_at_once<W>() - 1) / vectors_at_once<W>();
-    if (columns <= 16) {
-        p.group = 1;
-        while (p.group < columns)
-            p.group *= 2;
-    } else {
-        const int64_t turns = (columns + kMoveThreads - 1) / kMoveThreads;
-        p.group = (int)(((columns + turns - 1) / turns + 31) / 32 * 32);
-    }
-    p.move_tokens = kMoveThreads / p.group;
+    const int most = wide ? kMoveThreads : kAnyThreads;
+    p.group = group_of(wide ? (p.row_bytes / 16 + kMoveAtOnce - 1) / kMoveAtOnce : (p.row_bytes + 31) / 16, most);
+    p.move_tokens = most / p.group;
     const unsigned threads = p.group * p.move_tokens;   // whole warps
     // behind the tokens' blocks, kGroups for the zeros
     const int64_t blocks = (p.T + p.move_tokens - 1) / p.move_tokens + kGroups;
-    return launch_next(sort_move<W>, (unsigned)blocks, threads, st, p);
+    return wide ? launch_next(sort_move, (unsigned)blocks, threads, 0, st, p)
+                : launch_next(sort_move_any, (unsigned)blocks, threads, p.move_tokens * any_space(p.row_bytes), st, p);
 }
 
 bool aligned(const void *p, uintptr_t n) { return (uintptr_t)p % n == 0; }
@@ -665,15 +776,18 @@ mrr_status moe_sort_run(const void *expert_idx, int idx_is_i64, int64_t T, int64
     p.tokens = (int)tokens;
     p.groups = (int)groups;
     p.parts = (int)parts;
-    const bool few = T * k <= kFewSlots;
     // widest vectors that rows, stride and pointers are multiples of
     const uintptr_t all = p.out ? (uintptr_t)x | (uintptr_t)sorted_x | (uintptr_t)row_bytes | (T > 1 ? (uintptr_t)row_stride : 0)
                                 : 0;
-    const cudaError_t err = all % 16 == 0  ? launch<16>(p, few, st)
-                            : all % 8 == 0 ? launch<8>(p, few, st)
-                            : all % 4 == 0 ? launch<4>(p, few, st)
-                            : all % 2 == 0 ? launch<2>(p, few, st)
-                                           : launch<1>(p, few, st);
+    cudaError_t err;
+    if (T * k > kFewSlots)
+        err = launch_many(p, all % 16 == 0, st);
+    else
+        err = all % 16 == 0  ? launch_few<16>(p, st)
+              : all % 8 == 0 ? launch_few<8>(p, st)
+              : all % 4 == 0 ? launch_few<4>(p, st)
+              : all % 2 == 0 ? launch_few<2>(p, st)
+                             : launch_few<1>(p, st);
     if (err == cudaSuccess)
         return MRR_OK;
     (void)cudaGetLastError();
