@@ -1,7 +1,7 @@
 """One mixture-of-experts block, as a serving rank runs it, on MXFP4 expert weights.
 
-Prefill: the routing decision, rows quantised to MXFP4, laid out as an expert-parallel exchange
-delivers them (one segment per source rank and expert), re-routed to expert-major order, the
+Prefill: the norm with its rows in MXFP4, the routing decision, rows laid out as an expert-parallel
+exchange delivers them (one segment per source rank and expert), re-routed to expert-major order, the
 experts' two products, the inverse move, and each token's weighted sum.  Decode: the whole layer in
 one launch for a few tokens, with the same weights.
 
@@ -30,22 +30,20 @@ def weights(E, H, I, generator):
     return w
 
 
-def prefill(x, w, k, ranks):
+def prefill(x, w, k, ranks, quantised=None):
     """The block on x [T, H] bfloat16, as if `ranks` source ranks had each sent a share of the tokens.
+    `quantised`: x's MXFP4 rows and scales, where the norm in front has made them already.
     Every (rank, expert) pair needs a row, as the re-routing op asks."""
     T, H = x.shape
     E = w["router"].shape[0]
     weight, expert, _ = moe.moe_gating_top_k(x @ w["router"].t(), k, bias=w["bias"], **ROUTING)
 
     # what an exchange delivers: rank by rank, each rank's rows in expert order
-    token = torch.arange(T, device=x.device).repeat_interleave(k)
-    rank = token * ranks // T
-    expert, weight = expert.flatten().long(), weight.flatten()
-    order = torch.argsort(rank * E + expert, stable=True)
-    counts = torch.bincount(rank * E + expert, minlength=ranks * E).view(ranks, E).int()
-    codes, scales = moe.moe_mx_quantize(x)
-    rows, row_scales = codes[token[order]], scales[token[order]]
-    row_weight = weight[order].float().view(-1, 1)
+    rank = (torch.arange(T, device=x.device) * ranks // T).int()
+    codes, scales = moe.moe_mx_quantize(x) if quantised is None else quantised
+    rows, row_scales, _, row_idx, counts, row_weight = moe.moe_sort_tokens(
+        codes, expert + E * rank[:, None], ranks * E, per_token_scales=scales, expert_topk_weight=weight)
+    counts = counts.view(ranks, E)
 
     # expert-major, through the experts, and back
     rows, row_scales, _, num, row_weight = moe.moe_re_routing(
@@ -54,7 +52,13 @@ def prefill(x, w, k, ranks):
     h, h_scales = moe.moe_mx_grouped_matmul(rows, row_scales, num, w["w13"], w["s13"], gated=True, out_dtype="mxfp4")
     y = moe.moe_mx_grouped_matmul(h, h_scales, num, w["w2"], w["s2"], row_weight=row_weight, check_status=True)
     y, _, _ = moe.moe_re_routing_inverse(y, counts, check_status=True)
-    return torch.zeros(T, H, device=x.device).index_add_(0, token[order], y.float()).to(x.dtype)
+    return moe.moe_combine_tokens(y, row_idx)      # the weights are in y already
+
+
+def normed_prefill(x, residual, gain, w, k, ranks):
+    """The block with the residual's addition and the norm in front: (the block's result, the new residual)."""
+    y, h, codes, scales = moe.moe_add_rms_norm(x, gain, residual, quant="mxfp4")
+    return prefill(y, w, k, ranks, (codes, scales)), h
 
 
 def decode(x, w, k):
@@ -70,8 +74,10 @@ def main():
     generator = torch.Generator(device="cuda").manual_seed(0)
     w = weights(E=32, H=2048, I=1024, generator=generator)
     x = torch.randn(4096, 2048, generator=generator, device="cuda").bfloat16()
-    y = prefill(x, w, k=4, ranks=4)
-    z = decode(x[:8].contiguous(), w, k=4)
+    gain = torch.ones(2048, dtype=torch.bfloat16, device="cuda")
+    y, _ = normed_prefill(x, torch.zeros_like(x), gain, w, k=4, ranks=4)
+    x = moe.moe_add_rms_norm(x[:8].contiguous(), gain)[0]
+    z = decode(x, w, k=4)
     off = (y[:8].float() - z.float()).norm() / z.float().norm()
     print(f"prefill {tuple(y.shape)}, decode {tuple(z.shape)}: the first 8 tokens differ by {off:.3f} "
           "(prefill's activations are quantised to MXFP4, decode's are not)")
