@@ -83,7 +83,7 @@ mrr_status moe_add_rms_norm_grad_run(const void *grad_y, const void *h, const vo
  * moe_dequantize_rows_run -- the values [T, H] in dt of quantised rows (MOE_Q_INT8, MOE_Q_E4M3,
  *   MOE_Q_E4M3_128 or MOE_Q_MXFP8; MXFP4 rows: moe_mx_dequantize_run), code times scale in
  *   float32, rounded once.
- * Host errors: MRR_ERR_DTYPE, MRR_ERR_ATTR (quant), MRR_ERR_SHAPE (T < 0 or above 2^31 - 1, H
+ * Host errors: MRR_ERR_DTYPE, MRR_ERR_ATTR (quant), MRR_ERR_SHAPE (T < 0 or above 2^31 - 1, more than 2^41 elements, H
  * outside 1 .. 2^20), MRR_ERR_NULL, MRR_ERR_ALIGN, MRR_ERR_CUDA.
  */
 mrr_status moe_dequantize_rows_run(const void *q, const void *scales, moe_quant quant, int64_t T, int64_t H,

@@ -1,15 +1,16 @@
 // The gradient of the MoE gating top-k op (include/mrr_gating.h, mrr_gating_topk_grad_run).
 //
-// Scores that stand alone (sigmoid, softplus) without a gradient of the normalised output: grad_x is zero but for
-// the k chosen experts (gating_grad_chosen).  A group of lanes has a token, a lane a chosen expert, so several tokens share
-// a warp; x is read where it is needed, and the row of zeros is written ahead of the k values.  Else every
-// element of x has a share (gating_grad_dense): a warp has a token, each lane every 32nd expert, and the chosen
-// experts' shares are added into a row in shared memory.  Each element is read or written once with one or
-// two exponentials between: for the usual sizes (16384 rows of 256 in 16 bits, 8 to 17 MB) launches and the latency of a
-// row count for as much as HBM.
+// The gradient of the scores has k numbers of a token's own, at the chosen experts, beside grad_norm_out's, which is dense.
+// A group of lanes has a token, a lane a chosen expert (two where k is above 32), whose logit it reads where it lies.
+//   * Scores that stand alone (sigmoid, softplus) without grad_norm_out: the rest of grad_x is zero.  Several tokens
+//     share a warp, which writes their rows of zeros ahead of the k values.
+//   * Else (N > 0) a warp has a token and its row of logits in registers: softmax needs its sum, and every element gets
+//     score * (grad_norm_out - dot) or the like; the k values are written over it afterwards.
+// Each element is read or written once with an exponential between: for the usual sizes (16384 rows of 256 in 16 bits, 8 to
+// 17 MB) launches and the latency of a row count for as much as HBM.  16384 x 256 bfloat16, sigmoid: 9 us.
 //
-// The gradient of the biases is a sum over rows: warps hold sums of their own while the block goes from row to row,
-// each block leaves one row of partial sums, and a second launch adds those in order.
+// The gradient of the biases is a sum over rows: warps hold sums of their own in shared memory while the block goes from
+// row to row, each block leaves one row of partial sums, and a second launch adds those in order.
 #include <atomic>
 #include <string.h>
 
@@ -60,9 +61,37 @@ __device__ __forceinline__ float score_of(int norm_type, float x, float top, flo
     return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
 }
 
-// LANES lanes a token (k <= LANES; 32 lanes: two slots each).  sums: [2][e] of each warp, where bias gradients are asked for.
-template <int DT, int LANES>
-__global__ void __launch_bounds__(32 * kWarps) gating_grad_chosen(Params p)
+// V consecutive elements of a row, from an address aligned to them
+template <int DT, int V>
+__device__ __forceinline__ void load_group(const void *base, int64_t i, float (&v)[V])
+{
+    if constexpr (V == 1) {
+        v[0] = load1<DT>(base, i);
+    } else if constexpr (DT == MOE_F32) {
+        const float4 q = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(base) + i));
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else {
+        const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(base) + i));
+        const float2 lo = unpack2<DT>(q.x), hi = unpack2<DT>(q.y);
+        v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
+    }
+}
+
+template <int DT, int V>
+__device__ __forceinline__ void store_group(void *base, int64_t i, const float (&v)[V])
+{
+    if constexpr (V == 1)
+        store1<DT>(base, i, v[0]);
+    else if constexpr (DT == MOE_F32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(base) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(base) + i) = make_uint2(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]));
+}
+
+// LANES lanes a token (k <= LANES; 32 lanes: two slots each).  N > 0 (with 32 lanes): N groups of V elements of the row a
+// lane.  Shared memory: [1 or 2][e] sums of each warp, where bias gradients are asked for.
+template <int DT, int LANES, int N, int V>
+__global__ void __launch_bounds__(32 * kWarps) gating_grad(Params p)
 {
     extern __shared__ float sums[];
     mrr::grid_launch_dependents();
@@ -81,7 +110,7 @@ __global__ void __launch_bounds__(32 * kWarps) gating_grad_chosen(Params p)
         const bool extra = here && p.extra_mask && p.extra_mask[t] != 0;
         const void *bias = extra ? p.extra_bias : p.bias;
         int idx[kSlots];
-        float g[kSlots], x[kSlots], d[kSlots], sum = 0.0f, inner = 0.0f;
+        float g[kSlots], x[kSlots], n[kSlots], d[kSlots], sum = 0.0f, inner = 0.0f;
 #pragma unroll
         for (int h = 0; h < kSlots; ++h) {
             const int j = LANES * h + at;
@@ -92,15 +121,48 @@ __global__ void __launch_bounds__(32 * kWarps) gating_grad_chosen(Params p)
                 idx[h] = -1, g[h] = 0.0f;
         }
 #pragma unroll
-        for (int h = 0; h < kSlots; ++h) {
+        for (int h = 0; h < kSlots; ++h)
             x[h] = idx[h] >= 0 ? load1<DT>(p.x, t * p.e + idx[h]) : 0.0f;
-            float s = 0.0f;
-            if (idx[h] >= 0)
-                s = score_of(p.norm_type, x[h], 0.0f, 1.0f) + (bias ? load1<DT>(bias, idx[h]) : 0.0f);
+        // the row: its scores, for softmax without their common factor
+        float row[N > 0 ? N : 1][V];
+        float top = 0.0f, total = 1.0f;
+        if constexpr (N > 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = (32 * i + lane) * V;
+                if (c < p.e)
+                    load_group<DT, V>(p.x, t * p.e + c, row[i]);
+            }
+            if (p.norm_type == 0) {
+                top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int u = 0; u < V; ++u)
+                        top = (32 * i + lane) * V < p.e ? fmaxf(top, row[i][u]) : top;
+#pragma unroll
+                for (int o = 16; o > 0; o /= 2)
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+                total = 0.0f;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int u = 0; u < V; ++u) {
+                        row[i][u] = (32 * i + lane) * V < p.e ? expf(row[i][u] - top) : 0.0f;
+                        total += row[i][u];
+                    }
+                total = warp_sum(total);
+            }
+        } else {
+            clear<DT == MOE_F32 ? 4 : 2>(p.grad_x, t0 * p.e, min((int64_t)kTokens, p.T - t0) * p.e, lane, 32);
+        }
+#pragma unroll
+        for (int h = 0; h < kSlots; ++h) {
+            n[h] = idx[h] >= 0 ? score_of(p.norm_type, x[h], top, total) : 0.0f;
+            const float s = n[h] + (bias && idx[h] >= 0 ? load1<DT>(bias, idx[h]) : 0.0f);
             sum += s;
             inner = fmaf(g[h], s, inner);
         }
-        clear<DT == MOE_F32 ? 4 : 2>(p.grad_x, t0 * p.e, min((int64_t)kTokens, p.T - t0) * p.e, lane, 32);
 #pragma unroll
         for (int o = LANES / 2; o > 0; o /= 2) {
             sum += __shfl_xor_sync(kFull, sum, o);
@@ -111,7 +173,7 @@ __global__ void __launch_bounds__(32 * kWarps) gating_grad_chosen(Params p)
         inner /= sum;
 #pragma unroll
         for (int h = 0; h < kSlots; ++h)
-            d[h] = factor * (g[h] - inner);
+            d[h] = idx[h] >= 0 ? factor * (g[h] - inner) : 0.0f;
         // an expert that a token has twice (hash routing): its first slot gets the sum, in the order of the slots
         bool twice = false;
 #pragma unroll
@@ -119,10 +181,8 @@ __global__ void __launch_bounds__(32 * kWarps) gating_grad_chosen(Params p)
             const uint32_t group = LANES == 32 ? kFull : ((1u << LANES) - 1) << (of_warp * LANES);
             const uint32_t same = __match_any_sync(kFull, idx[h]) & group;
             twice |= idx[h] >= 0 && __popc(same) > 1;
-            if (kSlots == 2 && h == 1)
-                twice = twice || p.k > 32;   // the two halves are not compared here
         }
-        if (__any_sync(kFull, twice)) {
+        if (__any_sync(kFull, twice || p.k > 32)) {   // (slots 32 and above are not compared with the others here)
             float all[kSlots];
             bool first[kSlots];
 #pragma unroll
@@ -130,6 +190,7 @@ __global__ void __launch_bounds__(32 * kWarps) gating_grad_chosen(Params p)
                 all[h] = 0.0f, first[h] = true;
 #pragma unroll
             for (int o = 0; o < kSlots; ++o)
+#pragma unroll 1
                 for (int l = 0; l < LANES; ++l) {
                     const int other = __shfl_sync(kFull, idx[o], of_warp * LANES + l);
                     const float share = __shfl_sync(kFull, d[o], of_warp * LANES + l);
@@ -145,14 +206,60 @@ __global__ void __launch_bounds__(32 * kWarps) gating_grad_chosen(Params p)
             for (int h = 0; h < kSlots; ++h) {
                 d[h] = all[h];
                 if (!first[h])
-                    idx[h] = -1;
+                    idx[h] = -1, d[h] = 0.0f;
             }
         }
-        __syncwarp();   // the zeros are written
+        float dot = 0.0f;
+        if constexpr (N > 0) {
+            const float *norm = p.grad_norm + t * p.e;   // (not read where there is none)
+            const float per = 1.0f / total;
+            float more[V];
+            if (p.norm_type == 0) {
+#pragma unroll
+                for (int h = 0; h < kSlots; ++h)
+                    dot = fmaf(d[h], n[h], dot);
+                if (p.grad_norm) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const int c = (32 * i + lane) * V;
+                        if (c < p.e) {
+                            load_group<MOE_F32, V>(norm, c, more);
+#pragma unroll
+                            for (int u = 0; u < V; ++u)
+                                dot = fmaf(more[u], row[i][u] * per, dot);
+                        }
+                    }
+                }
+                dot = warp_sum(dot);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = (32 * i + lane) * V;
+                if (c >= p.e)
+                    continue;
+#pragma unroll
+                for (int u = 0; u < V; ++u)
+                    more[u] = 0.0f;
+                if (p.grad_norm)
+                    load_group<MOE_F32, V>(norm, c, more);
+                float out[V];
+#pragma unroll
+                for (int u = 0; u < V; ++u) {
+                    out[u] = p.norm_type == 0 ? row[i][u] * per * (more[u] - dot) : more[u] * slope_of(p.norm_type, row[i][u]);
+                    if (p.partial && p.grad_norm)
+                        mine[(extra ? p.e : 0) + c + u] += more[u];
+                }
+                store_group<DT, V>(p.grad_x, t * p.e + c, out);
+            }
+        }
+        __syncwarp();   // the rest of the rows is written
 #pragma unroll
         for (int h = 0; h < kSlots; ++h)
-            if (idx[h] >= 0)
-                store1<DT>(p.grad_x, t * p.e + idx[h], d[h] * slope_of(p.norm_type, x[h]));
+            if (idx[h] >= 0) {
+                const float ds = d[h] + (N > 0 && p.grad_norm ? __ldg(p.grad_norm + t * p.e + idx[h]) : 0.0f);
+                const float out = p.norm_type == 0 ? n[h] * (ds - dot) : ds * slope_of(p.norm_type, x[h]);
+                store1<DT>(p.grad_x, t * p.e + idx[h], out);
+            }
         if (p.partial) {
             // one token after the other: two of them may have the same expert
 #pragma unroll
@@ -179,170 +286,42 @@ __global__ void __launch_bounds__(32 * kWarps) gating_grad_chosen(Params p)
     }
 }
 
-template <int DT, int VPL>
-__global__ void __launch_bounds__(32 * kWarps) gating_grad_dense(Params p)
-{
-    extern __shared__ float rows[];   // [kWarps][e]
-    mrr::grid_launch_dependents();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    float *ds = rows + warp * p.e;
-    float acc[VPL], extra_acc[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-        acc[i] = extra_acc[i] = 0.0f;
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < p.T; t += (int64_t)gridDim.x * kWarps) {
-        float x[VPL];
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int at = 32 * i + lane;
-            x[i] = at < p.e ? load1<DT>(p.x, t * p.e + at) : -INFINITY;
-            top = fmaxf(top, x[i]);
-            if (at < p.e)
-                ds[at] = p.grad_norm ? __ldg(p.grad_norm + t * p.e + at) : 0.0f;
-        }
-        float total = 1.0f;
-        if (p.norm_type == 0) {
-#pragma unroll
-            for (int d = 16; d > 0; d /= 2)
-                top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-            total = 0.0f;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                x[i] = 32 * i + lane < p.e ? expf(x[i] - top) : 0.0f;   // the scores, but for their sum
-                total += x[i];
-            }
-            total = warp_sum(total);
-        }
-        const bool extra = p.extra_mask && p.extra_bias && p.extra_mask[t] != 0;
-        const void *bias = extra ? p.extra_bias : p.bias;
-        // up to two slots a lane
-        int idx[2];
-        float g[2], s[2], sum = 0.0f, inner = 0.0f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int j = 32 * h + lane;
-            idx[h] = j < p.k ? __ldg(p.expert_idx + t * p.k + j) : -1;
-            if (idx[h] >= p.e)
-                idx[h] = -1;
-            g[h] = s[h] = 0.0f;
-            if (idx[h] >= 0) {
-                g[h] = load1<DT>(p.grad_y, t * p.k + j);
-                s[h] = score_of(p.norm_type, load1<DT>(p.x, t * p.e + idx[h]), top, total);
-                if (bias)
-                    s[h] += load1<DT>(bias, idx[h]);
-            }
-            sum += s[h];
-            inner = fmaf(g[h], s[h], inner);
-        }
-        sum = warp_sum(sum) + p.eps;
-        inner = warp_sum(inner) / sum;
-        const float factor = p.scale / sum;
-        __syncwarp();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (32 * h >= p.k)
-                break;
-            const float d = factor * (g[h] - inner);
-            const uint32_t same = __match_any_sync(kFull, idx[h]);
-            const bool twice = __any_sync(kFull, idx[h] >= 0 && __popc(same) > 1);
-            if (!twice) {
-                if (idx[h] >= 0)
-                    ds[idx[h]] += d;
-            } else {   // an expert twice in one row (hash routing): one lane after the other
-                for (int l = 0; l < 32; ++l) {
-                    if (l == lane && idx[h] >= 0)
-                        ds[idx[h]] += d;
-                    __syncwarp();
-                }
-            }
-            __syncwarp();
-        }
-        float dot = 0.0f;
-        if (p.norm_type == 0) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const int at = 32 * i + lane;
-                x[i] /= total;
-                dot = fmaf(x[i], at < p.e ? ds[at] : 0.0f, dot);
-            }
-            dot = warp_sum(dot);
-        }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int at = 32 * i + lane;
-            if (at >= p.e)
-                continue;
-            const float d = ds[at];
-            float out;
-            if (p.norm_type == 0)
-                out = x[i] * (d - dot);
-            else
-                out = d * slope_of(p.norm_type, x[i]);
-            store1<DT>(p.grad_x, t * p.e + at, out);
-            if (extra)
-                extra_acc[i] += d;
-            else
-                acc[i] += d;
-        }
-        __syncwarp();
-    }
-    if (!p.partial)
-        return;
-    // the warps' sums, in order
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        if (which && !p.extra_mask)
-            break;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (32 * i + lane < p.e)
-                ds[32 * i + lane] = which ? extra_acc[i] : acc[i];
-        __syncthreads();
-        for (int at = threadIdx.x; at < p.e; at += 32 * kWarps) {
-            float s = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                s += rows[w * p.e + at];
-            p.partial[((int64_t)blockIdx.x * 2 + which) * p.e + at] = s;
-        }
-    }
-}
-
+// with bias gradients the blocks stay for many rows, else there are as many as rows ask for
 int64_t blocks_for(int64_t T)
 {
     const int64_t blocks = (T + kWarps - 1) / kWarps;
     return blocks < kMaxBlocks ? blocks : kMaxBlocks;
 }
 
-template <int DT, int LANES>
-cudaError_t launch_chosen(const Params &p, cudaStream_t st)
+template <int DT, int LANES, int N, int V>
+cudaError_t launch(const Params &p, cudaStream_t st)
 {
     static std::atomic<uint64_t> done;
     mrr_device::Info info;
     if (!mrr_device::current(info))
         return cudaErrorUnknown;
     const int smem = p.partial ? kWarps * (p.extra_mask ? 2 : 1) * p.e * 4 : 0;   // up to 64 KB
-    const cudaError_t err = mrr_device::allow_smem(gating_grad_chosen<DT, LANES>, info, done);
+    const cudaError_t err = mrr_device::allow_smem(gating_grad<DT, LANES, N, V>, info, done);
     if (err != cudaSuccess)
         return err;
-    gating_grad_chosen<DT, LANES><<<(unsigned)blocks_for(p.T), 32 * kWarps, smem, st>>>(p);
+    const int64_t rows = kWarps * (32 / LANES), blocks = p.partial ? blocks_for(p.T) : (p.T + rows - 1) / rows;
+    gating_grad<DT, LANES, N, V><<<(unsigned)blocks, 32 * kWarps, smem, st>>>(p);
     return cudaGetLastError();
 }
 
 template <int DT>
-cudaError_t launch(const Params &p, cudaStream_t st)
+cudaError_t launch(const Params &p, bool wide, cudaStream_t st)
 {
     if (p.norm_type != 0 && !p.grad_norm)
-        return p.k <= 8 ? launch_chosen<DT, 8>(p, st) : p.k <= 16 ? launch_chosen<DT, 16>(p, st) : launch_chosen<DT, 32>(p, st);
-    const int smem = kWarps * p.e * 4, per = (p.e + 31) / 32;
-    auto kernel = per <= 2    ? gating_grad_dense<DT, 2>
-                  : per <= 4  ? gating_grad_dense<DT, 4>
-                  : per <= 8  ? gating_grad_dense<DT, 8>
-                  : per <= 16 ? gating_grad_dense<DT, 16> : gating_grad_dense<DT, 32>;
-    kernel<<<(unsigned)blocks_for(p.T), 32 * kWarps, smem, st>>>(p);
-    return cudaGetLastError();
+        return p.k <= 8    ? launch<DT, 8, 0, 1>(p, st)
+               : p.k <= 16 ? launch<DT, 16, 0, 1>(p, st)
+                           : launch<DT, 32, 0, 1>(p, st);
+    if (wide)
+        return p.e <= 128   ? launch<DT, 32, 1, 4>(p, st)
+               : p.e <= 256 ? launch<DT, 32, 2, 4>(p, st)
+               : p.e <= 512 ? launch<DT, 32, 4, 4>(p, st)
+                            : launch<DT, 32, 8, 4>(p, st);
+    return p.e <= 128 ? launch<DT, 32, 4, 1>(p, st) : p.e <= 512 ? launch<DT, 32, 16, 1>(p, st) : launch<DT, 32, 32, 1>(p, st);
 }
 
 bool aligned(const void *p, uintptr_t n) { return (uintptr_t)p % n == 0; }
@@ -403,9 +382,11 @@ mrr_status mrr_gating_topk_grad_run(const void *grad_y, const void *x, mrr_gate_
         p.norm_type = (int)norm_type;
         p.scale = routed_scaling_factor;
         p.eps = eps;
-        const cudaError_t err = dt == MRR_GATE_F32    ? launch<MOE_F32>(p, st)
-                                : dt == MRR_GATE_BF16 ? launch<MOE_BF16>(p, st)
-                                                      : launch<MOE_F16>(p, st);
+        // groups of four elements, on addresses that are multiples of them
+        const bool wide = e % 4 == 0 && aligned(x, 4 * size) && aligned(grad_x, 4 * size) && aligned(grad_norm_out, 16);
+        const cudaError_t err = dt == MRR_GATE_F32    ? launch<MOE_F32>(p, wide, st)
+                                : dt == MRR_GATE_BF16 ? launch<MOE_BF16>(p, wide, st)
+                                                      : launch<MOE_F16>(p, wide, st);
         if (err != cudaSuccess) {
             (void)cudaGetLastError();
             return MRR_ERR_CUDA;

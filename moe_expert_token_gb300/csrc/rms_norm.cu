@@ -11,7 +11,8 @@ using namespace moe_norm;
 
 namespace {
 
-// Rows of 8 bits back to values.  A row belongs to a group of threads, each with kAtOnce chunks of 8 elements under way.
+// Rows of 8 bits back to values.  Rows that are multiples of 8 elements, on aligned addresses, are taken by groups of
+// threads, each with kAtOnce chunks of 8 elements under way.
 constexpr int kThreads = 128, kAtOnce = 4;
 
 struct Values {
@@ -22,41 +23,43 @@ struct Values {
     int H, quant, chunks, group, rows;   // threads of a row, rows of a block
 };
 
-// kWide: a chunk's codes come in one load of 8 bytes, its values go in stores of 16
-template <int DT, bool kWide>
+__device__ __forceinline__ float scale_of(const Values &p, int64_t row, int at)
+{
+    if (p.quant == MOE_Q_MXFP8)
+        return e8m0_value(__ldg(static_cast<const uint8_t *>(p.scales) + row * ((p.H + 63) / 64 * 2) + at / 32));
+    if (p.quant == MOE_Q_E4M3_128)
+        return __ldg(static_cast<const float *>(p.scales) + row * ((p.H + 127) / 128) + at / 128);
+    return __ldg(static_cast<const float *>(p.scales) + row);
+}
+
+__device__ __forceinline__ float2 values_of(const Values &p, uint2 codes, int i)
+{
+    const uint32_t two = (i < 4 ? codes.x : codes.y) >> (8 * (i % 4)) & 0xffffu;
+    return p.quant == MOE_Q_INT8 ? make_float2((float)(int8_t)two, (float)(int8_t)(two >> 8)) : decode_e4m3x2(two);
+}
+
+template <int DT>
 __global__ void __launch_bounds__(kThreads) dequantize(Values p)
 {
     const int of_block = threadIdx.x / p.group, lane = threadIdx.x - of_block * p.group;
     const int64_t row = (int64_t)blockIdx.x * p.rows + of_block;
     if (row >= p.T)
         return;
-    const uint8_t *from = p.q + row * p.H;
-    using C = Chunk<DT, kWide ? 16 : DT == MOE_F32 ? 4 : 2>;
+    const uint2 *from = reinterpret_cast<const uint2 *>(p.q + row * p.H);
+    using C = Chunk<DT, 16>;
     uint8_t *to = static_cast<uint8_t *>(p.x) + row * p.H * C::kElem;
-    const float of_row = p.quant == MOE_Q_INT8 || p.quant == MOE_Q_E4M3 ? __ldg(static_cast<const float *>(p.scales) + row) : 0.0f;
+    const bool by_row = p.quant == MOE_Q_INT8 || p.quant == MOE_Q_E4M3;
+    const float of_row = by_row ? scale_of(p, row, 0) : 0.0f;
     for (int c0 = lane; c0 < p.chunks; c0 += kAtOnce * p.group) {
-        uint32_t w[kAtOnce][2];
+        uint2 w[kAtOnce];
         float s[kAtOnce];
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
             const int c = c0 + u * p.group;
-            w[u][0] = w[u][1] = 0u;
-            s[u] = of_row;
-            if (c >= p.chunks)
-                continue;
-            if (kWide) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(from + 8 * c));
-                w[u][0] = v.x, w[u][1] = v.y;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (8 * c + i < p.H)
-                        w[u][i / 4] |= (uint32_t)__ldg(from + 8 * c + i) << (8 * (i % 4));
+            if (c < p.chunks) {
+                w[u] = __ldg(from + c);
+                s[u] = by_row ? of_row : scale_of(p, row, 8 * c);
             }
-            if (p.quant == MOE_Q_MXFP8)
-                s[u] = e8m0_value(__ldg(static_cast<const uint8_t *>(p.scales) + row * ((p.H + 63) / 64 * 2) + c / 4));
-            else if (p.quant == MOE_Q_E4M3_128)
-                s[u] = __ldg(static_cast<const float *>(p.scales) + row * ((p.H + 127) / 128) + c / 16);
         }
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
@@ -66,15 +69,77 @@ __global__ void __launch_bounds__(kThreads) dequantize(Values p)
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-                const uint32_t two = w[u][i / 4] >> (8 * (i % 4)) & 0xffffu;
-                const float2 f = p.quant == MOE_Q_INT8 ? make_float2((float)(int8_t)two, (float)(int8_t)(two >> 8))
-                                                       : decode_e4m3x2(two);
+                const float2 f = values_of(p, w[u], i);
                 v[i] = f.x * s[u], v[i + 1] = f.y * s[u];
             }
             C out;
             out.set(v);
             out.store(to, c * C::kBytes, p.H * C::kElem);
         }
+    }
+}
+
+// Rows of any size: all codes are one array without gaps and so are the values, so a thread takes 8 of them that begin
+// at a multiple of 8 wherever the rows begin (kWide: on aligned addresses).  Where they all have one scale it is
+// looked up once.
+template <int DT, bool kWide>
+__global__ void __launch_bounds__(kThreads) dequantize_flat(Values p)
+{
+    const int64_t all = p.T * p.H, first = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
+    if (first >= all)
+        return;
+    const int n = (int)min((int64_t)8, all - first);
+    uint2 w = make_uint2(0u, 0u);
+    if (kWide && n == 8) {
+        w = __ldg(reinterpret_cast<const uint2 *>(p.q + first));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                (i < 4 ? w.x : w.y) |= (uint32_t)__ldg(p.q + first + i) << (8 * (i % 4));
+    }
+    const int64_t row = first / p.H;
+    const int at = (int)(first - row * p.H);
+    const int block = p.quant == MOE_Q_MXFP8 ? 32 : p.quant == MOE_Q_E4M3_128 ? 128 : p.H;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 f = values_of(p, w, i);
+        v[i] = f.x, v[i + 1] = f.y;
+    }
+    float s = scale_of(p, row, at);
+    if (at / block == (at + 7) / block && at + 8 <= p.H) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] *= s;
+    } else {
+        int64_t r = row;
+        int c = at, left = min(p.H - at, block - at % block);   // elements with this scale
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= n)
+                break;
+            if (left == 0) {
+                c = c == p.H ? 0 : c;
+                r += c == 0;
+                left = min(p.H - c, block);
+                s = scale_of(p, r, c);
+            }
+            v[i] *= s;
+            ++c;
+            --left;
+        }
+    }
+    constexpr int kElem = DT == MOE_F32 ? 4 : 2;
+    Chunk<DT, kWide ? 16 : kElem> out;
+    out.set(v);
+    if (kWide && n < 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n)
+                store1<DT>(p.x, first + i, v[i]);
+    } else {
+        out.store(static_cast<uint8_t *>(p.x) + first * kElem, 0, n * kElem);
     }
 }
 
@@ -130,7 +195,8 @@ mrr_status moe_add_rms_norm_run(const void *x, const void *residual, moe_dtype d
     p.H = (int)H;
     p.weight_f32 = weight_dt == MOE_F32;
     p.quant = quant;
-    p.q_wide = quant == MOE_Q_MXFP4 ? H % 8 == 0 && aligned(q, 4) : H % 8 == 0 && aligned(q, 8);
+    const uintptr_t codes = (uintptr_t)q | (uintptr_t)(quant == MOE_Q_MXFP4 ? H / 2 : H);
+    p.q_align = codes % 8 == 0 ? 8 : codes % 4 == 0 ? 4 : codes % 2 == 0 ? 2 : 1;
     p.eps = eps;
     // pieces that every row begins with and consists of
     uintptr_t all = (uintptr_t)x | (uintptr_t)weight | (uintptr_t)h | (uintptr_t)y | (uintptr_t)H * size;
@@ -157,7 +223,6 @@ mrr_status moe_dequantize_rows_run(const void *q, const void *scales, moe_quant 
         return MRR_ERR_ALIGN;
     if (T == 0)
         return MRR_OK;
-    const bool wide = H % 8 == 0 && aligned(q, 8) && aligned(x, 16);
     Values p;
     memset(&p, 0, sizeof(p));
     p.q = static_cast<const uint8_t *>(q);
@@ -166,7 +231,19 @@ mrr_status moe_dequantize_rows_run(const void *q, const void *scales, moe_quant 
     p.T = T;
     p.H = (int)H;
     p.quant = quant;
-    p.chunks = (int)((H + 7) / 8);
+    const bool wide = aligned(q, 8) && aligned(x, 16);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!wide || H % 8) {
+        const int64_t blocks = (T * H + 8 * kThreads - 1) / (8 * kThreads);
+        if (blocks > INT32_MAX)
+            return MRR_ERR_SHAPE;
+        auto kernel = dt == MOE_F32    ? (wide ? dequantize_flat<MOE_F32, true> : dequantize_flat<MOE_F32, false>)
+                      : dt == MOE_BF16 ? (wide ? dequantize_flat<MOE_BF16, true> : dequantize_flat<MOE_BF16, false>)
+                                       : (wide ? dequantize_flat<MOE_F16, true> : dequantize_flat<MOE_F16, false>);
+        kernel<<<(unsigned)blocks, kThreads, 0, st>>>(p);
+        return done(cudaGetLastError());
+    }
+    p.chunks = (int)(H / 8);
     // many rows: as many threads as have kAtOnce chunks each; few: as have one.  A power of two up to 16, else warps.
     const int64_t each = T < 2 * 152 ? 1 : kAtOnce, need = (p.chunks + each - 1) / each;
     p.group = need > 16 ? (int)(need < kThreads ? (need + 31) / 32 * 32 : kThreads) : 1;
@@ -174,10 +251,7 @@ mrr_status moe_dequantize_rows_run(const void *q, const void *scales, moe_quant 
         p.group *= 2;
     p.rows = kThreads / p.group;
     const unsigned grid = (unsigned)((T + p.rows - 1) / p.rows), threads = p.group * p.rows;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    auto kernel = dt == MOE_F32    ? (wide ? dequantize<MOE_F32, true> : dequantize<MOE_F32, false>)
-                  : dt == MOE_BF16 ? (wide ? dequantize<MOE_BF16, true> : dequantize<MOE_BF16, false>)
-                                   : (wide ? dequantize<MOE_F16, true> : dequantize<MOE_F16, false>);
+    auto kernel = dt == MOE_F32 ? dequantize<MOE_F32> : dt == MOE_BF16 ? dequantize<MOE_BF16> : dequantize<MOE_F16>;
     kernel<<<grid, threads, 0, st>>>(p);
     return done(cudaGetLastError());
 }

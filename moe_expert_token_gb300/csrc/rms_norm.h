@@ -13,7 +13,7 @@ struct Params {
     const void *x, *residual, *weight;
     void *h, *y, *q, *scales;
     int64_t T, x_stride, residual_stride;   // in elements
-    int H, weight_f32, quant, q_wide;       // q_wide: a chunk's codes are stored at once
+    int H, weight_f32, quant, q_align;      // q_align: of every chunk's codes, up to their size
     float eps;
 };
 

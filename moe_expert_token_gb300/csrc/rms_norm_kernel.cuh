@@ -62,18 +62,34 @@ __device__ __forceinline__ float float_scale(uint32_t m, float top, float &inver
 
 __device__ __forceinline__ uint32_t int8_of(float v) { return (uint32_t)min(127, max(-127, __float2int_rn(v))) & 0xffu; }
 
-// codes of a chunk (elements c .. c + n - 1 of row `row`), from their values over the scale
-__device__ __forceinline__ void store_bytes(const Params &p, int64_t row, int c, int n, uint32_t lo, uint32_t hi)
+// BYTES (4 or 8) bytes of codes, of which the row has n, in stores as wide as their place allows
+template <int BYTES>
+__device__ __forceinline__ void store_codes(uint8_t *to, int n, int align, uint32_t lo, uint32_t hi)
 {
-    uint8_t *to = static_cast<uint8_t *>(p.q) + row * p.H + c;
-    if (n >= 8 && p.q_wide) {
-        *reinterpret_cast<uint2 *>(to) = make_uint2(lo, hi);
+    if (n >= BYTES && align >= 4) {
+        if (BYTES == 8 && align == 8) {
+            *reinterpret_cast<uint2 *>(to) = make_uint2(lo, hi);
+        } else {
+            *reinterpret_cast<uint32_t *>(to) = lo;
+            if (BYTES == 8)
+                *reinterpret_cast<uint32_t *>(to + 4) = hi;
+        }
+    } else if (n >= BYTES && align == 2) {
+#pragma unroll
+        for (int i = 0; i < BYTES; i += 2)
+            *reinterpret_cast<uint16_t *>(to + i) = (uint16_t)((i < 4 ? lo : hi) >> (8 * (i % 4)));
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < BYTES; ++i)
             if (i < n)
                 to[i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i % 4)));
     }
+}
+
+// codes of a chunk (elements c .. c + n - 1 of row `row`), from their values over the scale
+__device__ __forceinline__ void store_bytes(const Params &p, int64_t row, int c, int n, uint32_t lo, uint32_t hi)
+{
+    store_codes<8>(static_cast<uint8_t *>(p.q) + row * p.H + c, n, p.q_align, lo, hi);
 }
 
 __device__ __forceinline__ uint32_t largest(const float (&v)[8])
@@ -151,16 +167,7 @@ __device__ __forceinline__ void quantize(const Params &p, int64_t row, int tid, 
         for (int j = 0; j < 8; ++j)
             v[j] = y[i][j] * inverse;
         if (kind == MOE_Q_MXFP4) {
-            const uint32_t w = encode8(v);
-            uint8_t *to = static_cast<uint8_t *>(p.q) + (row * p.H + c) / 2;
-            if (n >= 8 && p.q_wide) {
-                *reinterpret_cast<uint32_t *>(to) = w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (2 * j < n)
-                        to[j] = (uint8_t)(w >> (8 * j));
-            }
+            store_codes<4>(static_cast<uint8_t *>(p.q) + (row * p.H + c) / 2, n / 2, p.q_align, encode8(v), 0u);
         } else {
             store_bytes(p, row, c, n, encode_e4m3(v[0], v[1], v[2], v[3]), encode_e4m3(v[4], v[5], v[6], v[7]));
         }
