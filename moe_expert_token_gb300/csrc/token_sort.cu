@@ -6,12 +6,17 @@
 // belongs to one slot and is written by the block that has the slot's token, which reads the token
 // once and writes it k times: T (1 + k) rows of traffic, the least there is.  HBM bounds it.
 //
-// Few slots (sort_few): one launch.  Each block looks at all keys and counts the smaller ones for its
-// own slots only.  Many slots: a first launch of one cluster counts the keys of kChunks chunks, passes the counts
-// round, and leaves where each chunk's slots of each key begin; in the second each block ranks its own slots (it counts
-// those of its chunk ahead of them while the first launch runs); the third moves the rows.  It has
-// many small blocks that take the tokens in order, so that what is written at a time lies close together: with
-// blocks that stay and rank and move a share of the tokens each, 16384 x 7168 bfloat16 to 8 experts took 355 us.
+// Few slots (sort_few, up to 4096): one launch.  Each block looks at all keys and counts the smaller ones for its own
+// slots only.  More (sort_index, up to 131072): one cluster ranks them all, each warp a share that it holds in registers, the
+// counts passed round through shared memory; a second launch moves the rows.  More slots or experts still: a first launch of
+// one cluster counts the keys of kChunks chunks and leaves where each chunk's slots of each key begin (sort_count); in the
+// second each block ranks its own slots, having counted those of its chunk ahead of them while the first ran (sort_rank);
+// the third moves the rows.  600 tokens of 2048 to 8 experts: 12.6 us with sort_index, 19 with the three launches; 16384 of
+// 7168: 333 and 332.
+//
+// The move has many small blocks that take the tokens in order, so that what is written at a time lies close together: with
+// blocks that stay and rank and move a share of the tokens each, 16384 x 7168 bfloat16 to 8 experts took 355 us.  Its rows
+// take 313 us of the 329, 6.8 TB/s.
 #include <atomic>
 #include <string.h>
 
@@ -39,6 +44,9 @@ constexpr int kCluster = 16;              // blocks of sort_count
 constexpr int kCountThreads = 1024;
 constexpr int kOfBlock = 4;               // chunks of one of them
 constexpr int kChunks = kCluster * kOfBlock;
+constexpr int kRounds = 8;                // slots of a thread of sort_index
+constexpr int kIndexSlots = kCluster * kCountThreads * kRounds;
+constexpr int kIndexE = 1023;             // its most experts: a thread has a key
 
 struct Params {
     const void *idx;
@@ -150,6 +158,13 @@ __device__ __forceinline__ void move_rows(const Params &p, int64_t first, int co
     }
 }
 
+__device__ __forceinline__ float weight_of(const Params &p, int64_t slot)
+{
+    return p.weight_dt == MOE_F32    ? moe_mx::load1<MOE_F32>(p.weight, slot)
+           : p.weight_dt == MOE_BF16 ? moe_mx::load1<MOE_BF16>(p.weight, slot)
+                                     : moe_mx::load1<MOE_F16>(p.weight, slot);
+}
+
 // The slots first .. first + count - 1: their index entries and weights.
 __device__ __forceinline__ void write_slots(const Params &p, uint32_t first, int count, const uint32_t *rows)
 {
@@ -159,12 +174,7 @@ __device__ __forceinline__ void write_slots(const Params &p, uint32_t first, int
         p.row_idx[slot] = none ? -1 : (int32_t)row;
         p.token_idx[row] = none ? -1 : (int32_t)slot;
         if (p.out_weight) {
-            float w = 0.0f;
-            if (!none)
-                w = p.weight_dt == MOE_F32    ? moe_mx::load1<MOE_F32>(p.weight, slot)
-                    : p.weight_dt == MOE_BF16 ? moe_mx::load1<MOE_BF16>(p.weight, slot)
-                                              : moe_mx::load1<MOE_F16>(p.weight, slot);
-            p.out_weight[row] = w;
+            p.out_weight[row] = none ? 0.0f : weight_of(p, slot);
         }
     }
 }
@@ -381,7 +391,88 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
     }
 }
 
-// Every slot's row, and what moves with slots.  Each block has p.tokens tokens.
+// The counts of the keys (all[e] of each block of the cluster) to where this block's slots of key e begin, in all[e] too;
+// the experts' numbers and the rows they have are written by the first block.  A thread has a key (keys <= its threads).
+__device__ __forceinline__ void begin_of_keys(const Params &p, uint32_t *all, int keys)
+{
+    cluster_barrier();
+    const uint32_t from = mrr::smem_addr(all);
+    const int e = threadIdx.x;
+    uint32_t total = 0, ahead = 0;
+    if (e < keys) {
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) {
+            const uint32_t v = load_from_block(from + 4 * e, r);
+            total += v;
+            ahead += r < (int)blockIdx.x ? v : 0u;
+        }
+    }
+    cluster_barrier();   // all[] is read no more
+    if (e < keys)
+        all[e] = total;
+    __syncthreads();
+    block_prefix<kCountThreads>(all, keys);
+    if (e < keys) {
+        const uint32_t first = all[e];
+        if (blockIdx.x == 0 && e < p.E)
+            store_num(p, e, p.cumsum ? first + total : total);
+        if (blockIdx.x == 0 && e == p.E)
+            *used_rows(p) = first;
+        all[e] = first + ahead;
+    }
+    __syncthreads();
+}
+
+// Every slot's row, for up to kIndexSlots slots.  One cluster; a warp has 32 slots at a time, p.parts times, in order.
+// Shared memory: all[E + 1], and count[warps][E + 1] of 16 bits.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads) sort_index(Params p)
+{
+    mrr::grid_launch_dependents();
+    extern __shared__ uint32_t all[];
+    const int keys = p.E + 1, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    uint16_t *counts = reinterpret_cast<uint16_t *>(all + keys), *mine = counts + warp * keys;
+    const uint32_t s0 = (blockIdx.x * (kCountThreads / 32) + warp) * 32 * p.parts + lane;
+    uint32_t slot[kRounds];   // key << 16 | the number of this warp's slots of the key ahead of it
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+        slot[r] = r < p.parts && s0 + 32 * r < p.n ? key_of(p, s0 + 32 * r) : keys;
+    for (int e = lane; e < keys; e += 32)
+        mine[e] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        if (r >= p.parts)
+            break;
+        const uint32_t key = slot[r], same = __match_any_sync(kFull, key);
+        const uint32_t at = key < (uint32_t)keys ? mine[key] : 0u;
+        __syncwarp();
+        slot[r] = key << 16 | (at + __popc(same & ((1u << lane) - 1)));
+        if (key < (uint32_t)keys && lane == __ffs(same) - 1)
+            mine[key] = (uint16_t)(at + __popc(same));
+        __syncwarp();
+    }
+    __syncthreads();
+    // each warp's counts to what the warps ahead of it, in this block, have
+    if (threadIdx.x < keys) {
+        uint32_t sum = 0;
+#pragma unroll 8
+        for (int w = 0; w < kCountThreads / 32; ++w) {
+            const uint32_t v = counts[w * keys + threadIdx.x];
+            counts[w * keys + threadIdx.x] = (uint16_t)sum;
+            sum += v;
+        }
+        all[threadIdx.x] = sum;
+    }
+    begin_of_keys(p, all, keys);
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const uint32_t key = slot[r] >> 16;
+        if (r < p.parts && key < (uint32_t)keys)
+            p.row_idx[s0 + 32 * r] = key == (uint32_t)p.E ? -1 : (int32_t)(all[key] + mine[key] + (slot[r] & 0xffffu));
+    }
+}
+
+// Every slot's row.  Each block has p.tokens tokens.
 __global__ void __launch_bounds__(kThreads) sort_rank(Params p)
 {
     mrr::grid_launch_dependents();
@@ -424,16 +515,26 @@ __global__ void __launch_bounds__(kThreads) sort_rank(Params p)
             }
         }
         __syncthreads();
-        write_slots(p, s0, mine, rows);
+        for (int s = threadIdx.x; s < mine; s += kThreads)
+            p.row_idx[s0 + s] = rows[s] & kNone ? -1 : (int32_t)rows[s];
     }
 }
 
-// The scale rows of a token: 4-byte units where rows and both pointers allow it, else bytes.
-__device__ __forceinline__ void move_scales(const Params &p, int64_t t, int lane)
+// What moves with a token's rows: their slots, weights and scale rows (in 4-byte units where rows and both pointers
+// allow it, else bytes).
+__device__ __forceinline__ void move_small(const Params &p, int64_t t, int lane)
 {
+    const int32_t *rows = p.row_idx + t * p.k;
+    for (int j = lane; j < p.k; j += p.group) {
+        const int32_t row = rows[j];
+        if (row < 0)
+            continue;
+        p.token_idx[row] = (int32_t)(t * p.k) + j;
+        if (p.out_weight)
+            p.out_weight[row] = weight_of(p, t * p.k + j);
+    }
     if (!p.out_scales)
         return;
-    const int32_t *rows = p.row_idx + t * p.k;
     const int units = (int)(p.scale_row_bytes / p.scale_unit);
     for (int c = lane; c < units; c += p.group) {
         if (p.scale_unit == 4) {
@@ -464,6 +565,11 @@ __device__ __forceinline__ void clear_rest(const Params &p, int64_t block, int64
         share(p.out, p.row_bytes);
     if (p.out_scales)
         share(p.out_scales, p.scale_row_bytes);
+    for (int64_t r = used + block * blockDim.x + threadIdx.x; r < p.n; r += blocks * blockDim.x) {
+        p.token_idx[r] = -1;
+        if (p.out_weight)
+            p.out_weight[r] = 0.0f;
+    }
 }
 
 // The rows, of p.move_tokens tokens a block and a group of p.group threads to a token, and behind them blocks that
@@ -514,7 +620,7 @@ __global__ void __launch_bounds__(kMoveThreads) sort_move(Params p)
         c += kEach * p.group;
         load(c);
     }
-    move_scales(p, t, lane);
+    move_small(p, t, lane);
 }
 
 // `size` bytes that begin `ahead` bytes behind a 16-byte boundary, as whole words of 16 from `first` to `last` (counted from
@@ -602,7 +708,7 @@ __global__ void __launch_bounds__(kAnyThreads) sort_move_any(Params p)
         }
     }
     if (mine)
-        move_scales(p, t, lane);
+        move_small(p, t, lane);
 }
 
 // How the work is cut, from the sizes alone.  A chunk is at most 10 of sort_rank's blocks.
@@ -649,8 +755,12 @@ int group_of(int64_t columns, int most)
     return (int)(((columns + turns - 1) / turns + 31) / 32 * 32);
 }
 
-// sort_count's cluster and shared memory are beyond what a kernel may have unasked: asked for once on each device
-cudaError_t allow_count()
+// The cluster and shared memory of sort_count and sort_index are beyond what a kernel may have unasked: asked for once on
+// each device.
+int index_smem(int64_t E) { return (int)((4 + 2 * (kCountThreads / 32)) * (E + 1)); }
+int count_smem(int64_t E) { return (int)(4 * (kOfBlock + 1) * (E + 1)); }
+
+cudaError_t allow_clusters()
 {
     static std::atomic<uint64_t> done;
     mrr_device::Info info;
@@ -659,9 +769,15 @@ cudaError_t allow_count()
     const uint64_t bit = info.device < mrr_device::kMaxDevices ? 1ull << info.device : 0;
     if (done.load(std::memory_order_acquire) & bit)
         return cudaSuccess;
-    cudaError_t err = cudaFuncSetAttribute(sort_count, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(sort_count, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (kOfBlock + 1) * (kMaxE + 1));
+    cudaError_t err = cudaSuccess;
+    auto allow = [&](void (*kernel)(Params), int smem) {
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    };
+    allow(sort_count, count_smem(kMaxE));
+    allow(sort_index, index_smem(kIndexE));
     if (err == cudaSuccess && bit)
         done.fetch_or(bit, std::memory_order_release);
     return err;
@@ -679,14 +795,21 @@ cudaError_t launch_few(const Params &p, cudaStream_t st)
 
 cudaError_t launch_many(Params p, bool wide, cudaStream_t st)
 {
-    cudaError_t err = allow_count();
+    cudaError_t err = allow_clusters();
     if (err != cudaSuccess)
         return err;
-    sort_count<<<kCluster, kCountThreads, 4 * (kOfBlock + 1) * (p.E + 1), st>>>(p);
-    err = cudaGetLastError();
-    if (err == cudaSuccess)
-        err = launch_next(sort_rank, (unsigned)p.groups, kThreads, 0, st, p);
-    if (err != cudaSuccess || (!p.out && !p.out_scales))
+    if (p.n <= kIndexSlots && p.E <= kIndexE) {
+        Params q = p;
+        q.parts = (int)((p.n + kCluster * kCountThreads - 1) / (kCluster * kCountThreads));
+        sort_index<<<kCluster, kCountThreads, index_smem(p.E), st>>>(q);
+        err = cudaGetLastError();
+    } else {
+        sort_count<<<kCluster, kCountThreads, count_smem(p.E), st>>>(p);
+        err = cudaGetLastError();
+        if (err == cudaSuccess)
+            err = launch_next(sort_rank, (unsigned)p.groups, kThreads, 0, st, p);
+    }
+    if (err != cudaSuccess)
         return err;
     const int most = wide ? kMoveThreads : kAnyThreads;
     p.group = group_of(wide ? (p.row_bytes / 16 + kMoveAtOnce - 1) / kMoveAtOnce : (p.row_bytes + 31) / 16, most);
