@@ -21,7 +21,9 @@
  * block that holds a NaN or an infinity gets the scale NaN (e8m0: 255), its codes are unspecified;
  * where the last e8m0 pair has no second block its byte is written as 127 and never used.
  *
- * Conventions are those of mrr_v2.h.  The same inputs give the same bits.
+ * Conventions are those of mrr_v2.h.  The same inputs give the same bits; a row's last bits may differ with the number
+ * of rows beside it, as how its sum is shared out does.  Calls that may run at the same time need workspaces of their
+ * own.  Calls may be captured in a CUDA graph.
  */
 #ifndef MOE_NORM_H
 #define MOE_NORM_H

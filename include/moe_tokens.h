@@ -15,7 +15,8 @@
  * Conventions are those of mrr_v2.h: device pointers unless stated otherwise, buffers owned by
  * the caller, nothing allocated, work only enqueued on `stream` (the current device), errors
  * found on the host returned at once with nothing enqueued; inputs and outputs do not overlap.
- * The same inputs give the same bits.
+ * The same inputs give the same bits (of grad_weight, for the same T).  Calls that may run at the same time
+ * need workspaces of their own.  Calls may be captured in a CUDA graph.
  */
 #ifndef MOE_TOKENS_H
 #define MOE_TOKENS_H

@@ -2,9 +2,9 @@
 // and the move of every token's row to its k places.
 //
 // A slot's row is the number of slots whose (key, slot) is smaller, slots without an expert here
-// having the key E behind all others: their rows are the rows of zeros.  So every row of the output
-// belongs to one slot and is written by the block that has the slot's token, which reads the token
-// once and writes it k times: T (1 + k) rows of traffic, the least there is.  HBM bounds it.
+// having the key E behind all others: their rows are the rows of zeros.  The threads that have a
+// token read it once and write it to its k places: T (1 + k) rows of traffic, the least there is.
+// HBM bounds it.
 //
 // Few slots (sort_few, up to 4096): one launch.  Each block looks at all keys and counts the smaller ones for its own
 // slots only.  More (sort_index, up to 131072): one cluster ranks them all, each warp a share that it holds in registers, the
