@@ -56,10 +56,13 @@ __global__ void __launch_bounds__(kThreads) dequantize(Values p)
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
             const int c = c0 + u * p.group;
-            if (c < p.chunks) {
-                w[u] = __ldg(from + c);
-                s[u] = by_row ? of_row : scale_of(p, row, 8 * c);
-            }
+            w[u] = c < p.chunks ? __ldg(from + c) : make_uint2(0u, 0u);
+            s[u] = of_row;
+        }
+        if (!by_row) {   // (apart: a branch between the loads keeps them from being under way together)
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u)
+                s[u] = c0 + u * p.group < p.chunks ? scale_of(p, row, 8 * (c0 + u * p.group)) : 0.0f;
         }
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
