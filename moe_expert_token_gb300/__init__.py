@@ -57,6 +57,6 @@ from .tokens import (  # noqa: F401
     moe_sort_tokens,
     moe_sort_tokens_grad,
     moe_sort_workspace,
-    mrr_gating_topk_grad_run,
-    mrr_gating_topk_grad_workspace,
+    moe_gating_topk_grad_run,
+    moe_gating_topk_grad_workspace,
 )

@@ -28,7 +28,7 @@ DEPS = SOURCES + [os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "gating_kern
                   os.path.join(CSRC, "device_info.h"), os.path.join(CSRC, "moe_layer_kernel.cuh"), os.path.join(INCLUDE, "moe_mx.h"),
                   os.path.join(CSRC, "rows.cuh"), os.path.join(CSRC, "column_sum.cuh"), os.path.join(CSRC, "rms_norm.h"),
                   os.path.join(CSRC, "rms_norm_kernel.cuh"), os.path.join(CSRC, "rms_norm_grad_kernel.cuh"),
-                  os.path.join(INCLUDE, "moe_layer.h"), os.path.join(INCLUDE, "moe_tokens.h"), os.path.join(INCLUDE, "moe_norm.h"),
+                  os.path.join(INCLUDE, "moe_layer.h"), os.path.join(INCLUDE, "moe_tokens.h"), os.path.join(INCLUDE, "moe_norm.h"), os.path.join(INCLUDE, "moe_gating_grad.h"),
                   os.path.join(INCLUDE, "mrr_v2.h"), os.path.join(INCLUDE, "mrr_gating.h")]
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmrr_v2.so")

@@ -1,4 +1,4 @@
-// The gradient of the MoE gating top-k op (include/mrr_gating.h, mrr_gating_topk_grad_run).
+// The gradient of the MoE gating top-k op (include/moe_gating_grad.h).
 //
 // The gradient of the scores has k numbers of a token's own, at the chosen experts, beside grad_norm_out's, which is dense.
 // A group of lanes has a token, a lane a chosen expert (two where k is above 32), whose logit it reads where it lies.
@@ -16,7 +16,7 @@
 
 #include "column_sum.cuh"
 #include "device_info.h"
-#include "mrr_gating.h"
+#include "moe_gating_grad.h"
 
 using namespace moe_rows;
 
@@ -330,14 +330,14 @@ bool aligned(const void *p, uintptr_t n) { return (uintptr_t)p % n == 0; }
 
 extern "C" {
 
-size_t mrr_gating_topk_grad_workspace(int64_t T, int64_t e)
+size_t moe_gating_topk_grad_workspace(int64_t T, int64_t e)
 {
     if (T < 0 || T > INT32_MAX || e < 1 || e > MRR_GATE_MAX_EXPERTS)
         return 0;
     return (size_t)((blocks_for(T) * 2 * e * 4 + 255) / 256 * 256);
 }
 
-mrr_status mrr_gating_topk_grad_run(const void *grad_y, const void *x, mrr_gate_dtype dt, int64_t T, int64_t e,
+mrr_status moe_gating_topk_grad_run(const void *grad_y, const void *x, mrr_gate_dtype dt, int64_t T, int64_t e,
                                     int64_t k, const int32_t *expert_idx, const void *bias,
                                     const void *additional_bias, const uint8_t *additional_token_mask,
                                     const float *grad_norm_out, float routed_scaling_factor, float eps,
@@ -359,7 +359,7 @@ mrr_status mrr_gating_topk_grad_run(const void *grad_y, const void *x, mrr_gate_
         return MRR_ERR_ALIGN;
     const bool sums = grad_bias || grad_additional_bias;
     if (sums && T > 0 &&
-        (!workspace || !aligned(workspace, 256) || workspace_bytes < mrr_gating_topk_grad_workspace(T, e)))
+        (!workspace || !aligned(workspace, 256) || workspace_bytes < moe_gating_topk_grad_workspace(T, e)))
         return MRR_ERR_WORKSPACE;
     // without a mask or an additional bias no row uses one
     const bool masked = additional_bias && additional_token_mask;

@@ -171,10 +171,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_add_rms_norm_grad_run.argtypes = [P, P, P, I32, I64, I64, P, I32, ctypes.c_float, P, P, P, ctypes.c_size_t, P]
     lib.moe_dequantize_rows_run.restype = I32
     lib.moe_dequantize_rows_run.argtypes = [P, P, I32, I64, I64, I32, P, P]
-    lib.mrr_gating_topk_grad_workspace.restype = ctypes.c_size_t
-    lib.mrr_gating_topk_grad_workspace.argtypes = [I64, I64]
-    lib.mrr_gating_topk_grad_run.restype = I32
-    lib.mrr_gating_topk_grad_run.argtypes = [P, P, I32, I64, I64, I64, P, P, P, P, P, ctypes.c_float, ctypes.c_float, I64,
+    lib.moe_gating_topk_grad_workspace.restype = ctypes.c_size_t
+    lib.moe_gating_topk_grad_workspace.argtypes = [I64, I64]
+    lib.moe_gating_topk_grad_run.restype = I32
+    lib.moe_gating_topk_grad_run.argtypes = [P, P, I32, I64, I64, I64, P, P, P, P, P, ctypes.c_float, ctypes.c_float, I64,
                                              P, P, P, P, ctypes.c_size_t, P]
     if path == _build.LIB_PATH:
         _lib = lib

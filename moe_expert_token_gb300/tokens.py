@@ -1,6 +1,6 @@
 """What stands around the experts on one rank: the norm in front of them, the tokens' way to expert order and
 back, and the gradients of these and of the routing.  ctypes binding of include/moe_tokens.h, include/moe_norm.h and
-the gradient in include/mrr_gating.h (the ``*_run`` functions, integer device addresses) and the torch-level
+include/moe_gating_grad.h (the ``*_run`` functions, integer device addresses) and the torch-level
 calls on top of it.
 
 ``moe_add_rms_norm`` gives the router its input and the exchange its rows in 8 bits or MXFP4;
@@ -66,14 +66,14 @@ def moe_dequantize_rows_run(q, scales, quant, T, H, dt, x, stream) -> int:
     return _m.load_library().moe_dequantize_rows_run(q, scales, quant, T, H, dt, x, stream)
 
 
-def mrr_gating_topk_grad_workspace(T, e) -> int:
-    return _m.load_library().mrr_gating_topk_grad_workspace(T, e)
+def moe_gating_topk_grad_workspace(T, e) -> int:
+    return _m.load_library().moe_gating_topk_grad_workspace(T, e)
 
 
-def mrr_gating_topk_grad_run(grad_y, x, dt, T, e, k, expert_idx, bias, additional_bias, additional_token_mask,
+def moe_gating_topk_grad_run(grad_y, x, dt, T, e, k, expert_idx, bias, additional_bias, additional_token_mask,
                              grad_norm_out, routed_scaling_factor, eps, norm_type, grad_x, grad_bias,
                              grad_additional_bias, workspace, workspace_bytes, stream) -> int:
-    return _m.load_library().mrr_gating_topk_grad_run(
+    return _m.load_library().moe_gating_topk_grad_run(
         grad_y, x, dt, T, e, k, expert_idx, bias, additional_bias, additional_token_mask, grad_norm_out,
         routed_scaling_factor, eps, norm_type, grad_x, grad_bias, grad_additional_bias, workspace, workspace_bytes, stream)
 
@@ -441,8 +441,8 @@ def moe_gating_top_k_grad(grad_y, x, expert_idx, *, bias=None, additional_bias=N
     grad_bias = None if bias is None else _empty(e, dtype=dtype, device=dev)
     grad_extra = None if additional_bias is None else _empty(e, dtype=dtype, device=dev)
     if bias is not None or additional_bias is not None or workspace is not None:
-        workspace = _space(workspace, lib.mrr_gating_topk_grad_workspace(T, e), dev)
-    _run(lib.mrr_gating_topk_grad_run, "mrr_gating_topk_grad_run",
+        workspace = _space(workspace, lib.moe_gating_topk_grad_workspace(T, e), dev)
+    _run(lib.moe_gating_topk_grad_run, "moe_gating_topk_grad_run",
          (grad_y.data_ptr(), x.data_ptr(), code, T, e, k, expert_idx.data_ptr(), _ptr(bias), _ptr(additional_bias),
           _ptr(mask), _ptr(grad_out), routed_scaling_factor, eps, norm_type, grad_x.data_ptr(), _ptr(grad_bias),
           _ptr(grad_extra), _ptr(workspace), _bytes(workspace)), dev)

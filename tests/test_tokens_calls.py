@@ -98,12 +98,12 @@ def test_gating_grad_rejects():
     base = dict(grad_y=A, x=B, dt=F32, T=10, e=16, k=4, expert_idx=C, bias=D, additional_bias=None, additional_token_mask=None,
                 grad_norm_out=None, routed_scaling_factor=1.0, eps=1e-20, norm_type=1, grad_x=E, grad_bias=F, grad_additional_bias=None,
                 workspace=W, workspace_bytes=1 << 20, stream=None)
-    check(moe.mrr_gating_topk_grad_run, base, [
+    check(moe.moe_gating_topk_grad_run, base, [
         (dict(dt=3), m.MRR_ERR_DTYPE), (dict(norm_type=3), m.MRR_ERR_ATTR), (dict(T=-1), m.MRR_ERR_SHAPE), (dict(e=1025), m.MRR_ERR_SHAPE),
         (dict(k=17), m.MRR_ERR_SHAPE), (dict(k=0), m.MRR_ERR_SHAPE), (dict(grad_y=None), m.MRR_ERR_NULL), (dict(expert_idx=None), m.MRR_ERR_NULL),
         (dict(grad_x=None), m.MRR_ERR_NULL), (dict(x=B + 2), m.MRR_ERR_ALIGN), (dict(grad_norm_out=G + 2), m.MRR_ERR_ALIGN),
-        (dict(workspace=None), m.MRR_ERR_WORKSPACE), (dict(workspace_bytes=moe.mrr_gating_topk_grad_workspace(10, 16) - 1), m.MRR_ERR_WORKSPACE)])
-    assert moe.mrr_gating_topk_grad_workspace(10, 1025) == 0
+        (dict(workspace=None), m.MRR_ERR_WORKSPACE), (dict(workspace_bytes=moe.moe_gating_topk_grad_workspace(10, 16) - 1), m.MRR_ERR_WORKSPACE)])
+    assert moe.moe_gating_topk_grad_workspace(10, 1025) == 0
 
 
 def test_a_stream_of_another_device_is_refused():
