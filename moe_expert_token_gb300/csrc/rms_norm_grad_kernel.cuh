@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(most_threads<NV, kBlock>(), NV > 2 || !kBlock 
             }
         }
         const float r = rsqrtf(fmaf(squares, per_element, p.eps));
-        const float factor = -r * r * r * (inner * per_element);
+        const float factor = -(inner * per_element * r) * r * r;   // (r^3 alone passes float32 where eps is below 2^-85)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float h[8], g[8], d[8];

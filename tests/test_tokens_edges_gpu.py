@@ -117,6 +117,23 @@ def test_norm_grad_where_forms_meet(T, H, dt):
     close(gw, rw, sw, row_ops(H) + T / 64 + 60, dt)
 
 
+@pytest.mark.parametrize("H", [64, 1000, 4096])
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+def test_norm_grad_of_rows_near_zero(H, dt):
+    """Rows of zeros and of 2^-52 under a small eps: r is 2^50, and its third power no float32."""
+    eps = 2.0 ** -100
+    rng = np.random.default_rng(H)
+    h, gy = rng.standard_normal((9, H)), up(rng.standard_normal((9, H)), dt)
+    h[3:6] *= 2.0 ** -52
+    h[6:] = 0.0
+    h, w = up(h, dt), up(1 + 0.2 * rng.standard_normal(H), dt)
+    gx, gw = moe.moe_add_rms_norm_grad(gy, h, w, eps=eps)
+    rx, sx, rw, sw = ox.add_rms_norm_grad(down(gy), down(h), down(w), None, eps)
+    assert np.isfinite(rx).all()
+    close(gx, rx, sx, row_ops(H), dt)
+    close(gw, rw, sw, row_ops(H) + 60, dt)
+
+
 @pytest.mark.parametrize("H", [7168, 7176, 16384, 16392, 32768, 32776])
 @pytest.mark.parametrize("dt", ["float16", "float32"])
 def test_norm_of_long_rows(H, dt):
