@@ -23,6 +23,7 @@ struct GradParams {
     float *partial;        // [blocks][H], or NULL
     int64_t T;
     int H, weight_f32;
+    int tensors;           // 3: grad_h comes ahead as grad_y and h do
     float eps;
 };
 

@@ -8,10 +8,11 @@
 // The blocks stay for many rows and hold their share of grad_weight in registers; each leaves one row of partial
 // sums, which a second launch adds in order.  What a row waits for (its loads, the sum over the block) is hidden by
 // copies that run kStages rows ahead into shared memory: each warp copies, and later reads, its own chunks only,
-// so the copies need no barrier of the block.  Rows that do not fit, or that come in pieces of 2 bytes, are loaded
-// directly.  Accesses to shared memory are what the kernel has least to spare of (with the weight read from there too,
-// 71 % of L1's throughput and 65 us for 8191 x 4100 bfloat16), so the weight is held in registers, and with one chunk
-// a thread so are 16-bit rows, packed as they come.  8191 x 4100: 53 us; 16384 x 7168: 142 us, 6.6 TB/s.
+// so the copies need no barrier of the block.  Rows that do not fit twice (grad_h, which is read once, then stays out),
+// or that come in pieces of 2 bytes, are loaded directly.  Accesses to shared memory are what the kernel has least to
+// spare of (with the weight read from there too, 71 % of L1's throughput and 65 us for 8191 x 4100 bfloat16), so the
+// weight is held in registers, and with one chunk a thread so are 16-bit rows, packed as they come.
+// 8191 x 4100: 54.6 us; 16384 x 7168: 146 us, 6.4 TB/s; 4000 x 12288 float32: 137 us.
 #pragma once
 
 #include <atomic>
@@ -71,7 +72,7 @@ struct Ahead {
             __syncwarp();   // the stage's last row has been read
             if (row < T) {
                 const int shift = tid % 32 * (W - C::kBytes);   // from this lane's chunk to its first piece
-                for (int t = 0; t < tensors; ++t) {
+                auto fetch_one = [&](int t) {
                     const uint8_t *src = from[t] + row * size;
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
@@ -82,7 +83,12 @@ struct Ahead {
                             if (at + 32 * W * b < size)
                                 copy_async<W>(to + 32 * W * b, src + at + 32 * W * b);
                     }
-                }
+                };
+                // (a loop would keep `from` in local memory, and L1 has little room beside the stages)
+                fetch_one(0);
+                fetch_one(1);
+                if (tensors == 3)
+                    fetch_one(2);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
@@ -113,13 +119,14 @@ struct Ahead {
     }
 };
 
-// Threads of a block at most: of 2 chunks a thread 448, so that two blocks' registers (72 a thread) fit an SM.
-template <int NV, bool kBlock>
-constexpr int most_threads() { return !kBlock ? 32 * kShortWarps : NV == 2 ? 448 : NV <= 4 ? 512 : 1024; }
+// Threads of a block at most: of 2 chunks a thread 896 on an SM, whose registers give each 72 (16384 x 7172 by one block of
+// 480 threads 167 us, by 256 threads of 4 chunks 308).
+template <int NV, bool kBlock, int kPerSm>
+constexpr int most_threads() { return !kBlock ? 32 * kShortWarps : NV == 1 ? 256 : NV == 2 ? 896 / kPerSm : NV == 4 ? 640 : 1024; }
 
 // NV chunks a thread; kBlock: a block has a row at a time, else each of its warps has one.
-template <int DT, int W, int NV, bool kBlock, int kStages>
-__global__ void __launch_bounds__(most_threads<NV, kBlock>(), NV > 2 || !kBlock ? 1 : 2) rms_norm_grad(GradParams p)
+template <int DT, int W, int NV, bool kBlock, int kPerSm, int kStages>
+__global__ void __launch_bounds__(most_threads<NV, kBlock, kPerSm>(), kPerSm) rms_norm_grad(GradParams p)
 {
     // (all of it dynamic: together with static memory it could not be allowed up to the device's limit)
     extern __shared__ __align__(16) uint8_t memory[];
@@ -133,7 +140,7 @@ __global__ void __launch_bounds__(most_threads<NV, kBlock>(), NV > 2 || !kBlock 
     in.from[0] = static_cast<const uint8_t *>(p.h);
     in.from[1] = static_cast<const uint8_t *>(p.grad_y);
     in.from[2] = static_cast<const uint8_t *>(p.grad_h);
-    in.tensors = p.grad_h ? 3 : 2;
+    in.tensors = p.tensors;
     in.threads = kBlock ? blockDim.x : 32;
     in.tid = kBlock ? threadIdx.x : threadIdx.x % 32;
     in.size = p.H * Chunk<DT, W>::kElem;
@@ -208,7 +215,13 @@ __global__ void __launch_bounds__(most_threads<NV, kBlock>(), NV > 2 || !kBlock 
             get(i, true, h, g);
             const float (&w)[8] = weight[kHoldWeight ? i : 0];
             if (p.grad_h) {
-                in.get(stage, row, 2, i).get(d);
+                if (in.tensors == 3) {
+                    in.get(stage, row, 2, i).get(d);
+                } else {
+                    Chunk<DT, W> c;
+                    c.load(in.from[2] + row * in.size, (in.tid + i * in.threads) * Chunk<DT, W>::kBytes, in.size);
+                    c.get(d);
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -257,47 +270,56 @@ __global__ void __launch_bounds__(most_threads<NV, kBlock>(), NV > 2 || !kBlock 
     }
 }
 
-template <int DT, int W, int NV, bool kBlock, int kStages>
-cudaError_t launch(const GradParams &p, unsigned threads, int smem, const mrr_device::Info &info, cudaStream_t st)
+template <int DT, int W, int NV, bool kBlock, int kPerSm, int kStages>
+cudaError_t launch(GradParams p, int tensors, unsigned threads, int smem, const mrr_device::Info &info, cudaStream_t st)
 {
     static std::atomic<uint64_t> done;
-    auto kernel = rms_norm_grad<DT, W, NV, kBlock, kStages>;
+    auto kernel = rms_norm_grad<DT, W, NV, kBlock, kPerSm, kStages>;
     const cudaError_t err = mrr_device::allow_smem(kernel, info, done);
     if (err != cudaSuccess)
         return err;
+    p.tensors = tensors;
     kernel<<<(unsigned)grad_blocks(p.T, p.H), threads, kSumBytes + smem, st>>>(p);
     return cudaGetLastError();
 }
 
-template <int DT, int W, int NV, bool kBlock>
+template <int DT, int W, int NV, bool kBlock, int kPerSm>
 cudaError_t launch(const GradParams &p, const mrr_device::Info &info, cudaStream_t st)
 {
-    const int chunks = (p.H + 7) / 8;
+    const int chunks = (p.H + 7) / 8, all = p.grad_h ? 3 : 2;
     const unsigned threads = kBlock ? ((chunks + NV - 1) / NV + 31) / 32 * 32 : 32 * kShortWarps;
-    const int stage = (p.grad_h ? 3 : 2) * NV * (int)threads * Chunk<DT, W>::kBytes;
+    const int row = NV * (int)threads * Chunk<DT, W>::kBytes;
     const int shares = kBlock ? 0 : kShortWarps * p.H * 4;   // in the stages' place, at the end
-    auto bytes = [&](int stages) { return stages * stage > shares ? stages * stage : shares; };
+    auto bytes = [&](int stages, int tensors) {
+        const int b = stages * tensors * row;
+        return b > shares ? b : shares;
+    };
     if constexpr (W > 2 && NV <= 4) {
-        const int half = info.smem_max / 2 - 1024, whole = info.smem_max - 1024;   // two blocks on an SM, or one
-        // (a fourth stage leaves L1 too little: 75 us where three take 58)
-        if (bytes(3) <= half)
-            return launch<DT, W, NV, kBlock, 3>(p, threads, bytes(3), info, st);
-        if (bytes(2) <= whole)
-            return launch<DT, W, NV, kBlock, 2>(p, threads, bytes(2), info, st);
+        // two blocks on an SM, or one; pieces of less than 16 bytes come through L1 and leave it room (8191 x 4100: three
+        // stages 55.9 us, two 54.9; 4000 x 12292: 122 and 100; 16384 x 1500: 41.5 and 45.5)
+        const int whole = info.smem_max - 1024, most = W == 16 ? whole : 96 * 1024;
+        if (bytes(3, all) <= (kPerSm == 2 ? most / 2 - 512 : most))
+            return launch<DT, W, NV, kBlock, kPerSm, 3>(p, all, threads, bytes(3, all), info, st);
+        if (bytes(2, all) <= whole)
+            return launch<DT, W, NV, kBlock, kPerSm, 2>(p, all, threads, bytes(2, all), info, st);
+        // without grad_h, which is read once
+        if (bytes(2, 2) <= whole)
+            return launch<DT, W, NV, kBlock, kPerSm, 2>(p, 2, threads, bytes(2, 2), info, st);
     }
-    return launch<DT, W, NV, kBlock, 0>(p, threads, bytes(0), info, st);
+    return launch<DT, W, NV, kBlock, kPerSm, 0>(p, all, threads, bytes(0, 0), info, st);
 }
 
 template <int DT, int W>
 cudaError_t launch_grad(const GradParams &p, const mrr_device::Info &info, cudaStream_t st)
 {
     const int chunks = (p.H + 7) / 8;
-    return chunks <= 32     ? launch<DT, W, 1, false>(p, info, st)
-           : chunks <= 128  ? launch<DT, W, 4, false>(p, info, st)
-           : chunks <= 256  ? launch<DT, W, 1, true>(p, info, st)
-           : chunks <= 896  ? launch<DT, W, 2, true>(p, info, st)
-           : chunks <= 2048 ? launch<DT, W, 4, true>(p, info, st)
-                            : launch<DT, W, 8, true>(p, info, st);
+    return chunks <= 32     ? launch<DT, W, 1, false, 1>(p, info, st)
+           : chunks <= 128  ? launch<DT, W, 4, false, 1>(p, info, st)
+           : chunks <= 256  ? launch<DT, W, 1, true, 2>(p, info, st)
+           : chunks <= 896  ? launch<DT, W, 2, true, 2>(p, info, st)
+           : chunks <= 1792 ? launch<DT, W, 2, true, 1>(p, info, st)
+           : chunks <= 2560 ? launch<DT, W, 4, true, 1>(p, info, st)
+                            : launch<DT, W, 8, true, 1>(p, info, st);
 }
 
 template <int DT>

@@ -152,6 +152,20 @@ def test_norm_of_long_rows(H, dt):
     close(gw, rw, sw, row_ops(H) + T / 64 + 60, "float32")
 
 
+@pytest.mark.parametrize("H", [7168, 7176, 9218, 12288, 12292, 14336, 14344, 20480, 20482, 20488])
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+def test_norm_grad_of_long_rows(H, dt):
+    """grad_h beside rows that fit three, two or, without it, two times into shared memory, or not at all."""
+    T = 320
+    rng = np.random.default_rng(H)
+    h, gy, gh = (up(rng.standard_normal((T, H)), dt) for _ in range(3))
+    w = up(1 + 0.2 * rng.standard_normal(H), "float32")
+    gx, gw = moe.moe_add_rms_norm_grad(gy, h, w, grad_h=gh)
+    rx, sx, rw, sw = ox.add_rms_norm_grad(down(gy), down(h), down(w), down(gh))
+    close(gx, rx, sx, row_ops(H), dt)
+    close(gw, rw, sw, row_ops(H) + T / 64 + 60, "float32")
+
+
 @pytest.mark.parametrize("quant", ["int8", "e4m3", "e4m3_128", "mxfp8"])
 @pytest.mark.parametrize("H", [1, 3, 7, 8, 9, 31, 33, 127, 129, 130, 132, 136, 1000])
 @pytest.mark.parametrize("off", [0, 1, 4])
