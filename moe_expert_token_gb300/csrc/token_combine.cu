@@ -159,6 +159,60 @@ __device__ __forceinline__ void load_slots(const Params &p, int64_t t, int j0, i
     }
 }
 
+// y[t] where R slots at most, those in `mask`, have rows
+template <int DT, int W, int R>
+__device__ __forceinline__ void combine_few(const Params &p, int64_t t, int lane, uint32_t mask)
+{
+    using P = Piece<DT, W>;
+    constexpr int U = pieces_at_once<W, R>();
+    const int pieces = p.H / P::kEach;
+    int row[R];
+    float weight[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        row[j] = -1;
+        weight[j] = 1.0f;
+        if (mask) {
+            const int64_t at = t * p.k + __ffs(mask) - 1;
+            mask &= mask - 1;
+            row[j] = __ldg(p.row_idx + at);
+            if (p.weight)
+                weight[j] = load_weight(p.weight, p.weight_dt, at);
+        }
+    }
+    for (int c = blockIdx.y * U * p.group + lane; c < pieces; c += gridDim.y * U * p.group) {
+        P v[R][U];
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (row[j] >= 0 && c + u * p.group < pieces)
+                    v[j][u].load(p.rows, (int64_t)row[j] * p.H + (c + u * p.group) * P::kEach);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (c + u * p.group >= pieces)
+                continue;
+            float sum[P::kEach];
+#pragma unroll
+            for (int i = 0; i < P::kEach; ++i)
+                sum[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                if (row[j] < 0)
+                    continue;
+                float f[P::kEach];
+                v[j][u].get(f);
+#pragma unroll
+                for (int i = 0; i < P::kEach; ++i)
+                    sum[i] = fmaf(weight[j], f[i], sum[i]);
+            }
+            P out;
+            out.set(sum);
+            out.store(p.y, t * p.H + (c + u * p.group) * P::kEach);
+        }
+    }
+}
+
 // R rows at once.  Where tokens are few, several blocks (the y index) share a token's columns.
 template <int DT, int W, int R>
 __global__ void __launch_bounds__(kThreads, W > 2 ? 12 : 8) combine(Params p)
@@ -169,6 +223,26 @@ __global__ void __launch_bounds__(kThreads, W > 2 ? 12 : 8) combine(Params p)
     const int64_t t = (int64_t)blockIdx.x * p.tokens + of_block;
     if (t >= p.T)
         return;
+    // A token that has rows in few of its slots (its other experts are held elsewhere) has more of each row under way (16384 x
+    // 7168, 8 experts each, a quarter of them held: 121 us, 159 without; an eighth: 87 and 134; 8192 x 2049 float16, a quarter:
+    // 46 and 75).  Pieces of 4 bytes stay as they are: with all forms in one kernel 8192 x 2050 with every row takes
+    // 72 us instead of 64.
+    if (W != 4 && R > 1 && p.k <= R && p.group >= 32) {
+        uint32_t mask = 0u;
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            if (j < p.k) {
+                const int at = __ldg(p.row_idx + t * p.k + j);
+                mask |= at >= 0 && at < p.R ? 1u << j : 0u;
+            }
+        const int n = __popc(mask);
+        if (n <= 1)
+            return combine_few<DT, W, 1>(p, t, lane, mask);
+        if (R > 2 && n <= 2)
+            return combine_few<DT, W, 2>(p, t, lane, mask);
+        if (R > 4 && n <= 4)
+            return combine_few<DT, W, 4>(p, t, lane, mask);
+    }
     const int pieces = p.H / P::kEach;
     int row[R];
     float weight[R];
@@ -215,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, W > 2 ? 12 : 8) combine(Params p)
 }
 
 // A thread's sums of R slots stay while it goes through the columns.  The blocks behind the tokens' write the rows of
-// zeros, each every `zero_blocks`th row: these rows follow one another.
+// zeros, each every `zero_blocks`th row: these rows follow one another.  Few rows go to as many warps as there are.
 template <int DT, int W, int R, int THREADS>
 __global__ void __launch_bounds__(THREADS, (W == 16 ? 640 : 512) / THREADS) combine_grad(Params p)
 {
@@ -227,7 +301,8 @@ __global__ void __launch_bounds__(THREADS, (W == 16 ? 640 : 512) / THREADS) comb
     const int64_t token_blocks = (p.T + p.tokens - 1) / p.tokens;
     if (blockIdx.x >= token_blocks) {
         const int64_t zero_blocks = gridDim.x - token_blocks;
-        const int64_t mine = blockIdx.x - token_blocks + threadIdx.x * zero_blocks;
+        const bool few = zero_blocks * blockDim.x >= 2 * p.R;
+        const int64_t mine = blockIdx.x - token_blocks + (few ? lane32 * (blockDim.x / 32) + warp : threadIdx.x) * zero_blocks;
         uint32_t none = __ballot_sync(kFull, mine < p.R && __ldg(p.token_idx + min(mine, p.R - 1)) < 0);
         while (none) {
             const int64_t r = __shfl_sync(kFull, mine, __ffs(none) - 1);
@@ -314,6 +389,7 @@ __global__ void __launch_bounds__(THREADS, (W == 16 ? 640 : 512) / THREADS) comb
 }
 
 constexpr int kFewTokens = 304;        // for the gradient
+constexpr int kZeroBlocks = 16 * 152;
 constexpr int kFewBlocks = 4 * 152;    // fewer than these of one group each leave SMs idle
 
 template <int DT, int W, int R, int THREADS>
@@ -323,8 +399,12 @@ void launch_grad(Params p, cudaStream_t st)
     p.group = group_of((columns + at_once - 1) / at_once, THREADS);
     p.tokens = THREADS / p.group;
     const int threads = p.group * p.tokens;   // whole warps
-    // behind the tokens' blocks, one for each `threads` rows (32 or more)
-    const int64_t blocks = (p.T + p.tokens - 1) / p.tokens + (p.R + threads - 1) / threads;
+    // behind the tokens' blocks, one for each `threads` rows (32 or more); few rows are spread over more (64 x 7168, 8
+    // experts each, an eighth of them held: 7.7 us, 35 without; 4095 x 7168: 112 and 137)
+    int64_t zero_blocks = (p.R + threads - 1) / threads;
+    if (zero_blocks < kZeroBlocks)
+        zero_blocks = p.R < kZeroBlocks ? p.R : kZeroBlocks;
+    const int64_t blocks = (p.T + p.tokens - 1) / p.tokens + zero_blocks;
     combine_grad<DT, W, R, THREADS><<<(unsigned)blocks, threads, 0, st>>>(p);
 }
 
@@ -398,9 +478,9 @@ mrr_status check(moe_dtype dt, int64_t R, int64_t H, int64_t T, int64_t k, const
 {
     if (!is_float(dt) || (weight && !is_float(weight_dt)))
         return MRR_ERR_DTYPE;
-    // at most 2^31 - 1 blocks: one or more tokens each, and behind them blocks for 32 or more rows each
+    // at most 2^31 - 1 blocks: one or more tokens each, and behind them kZeroBlocks or blocks for 32 or more rows each
     const bool ok = T >= 0 && R >= 0 && T <= INT32_MAX && R <= INT32_MAX && H >= 1 && H <= (1 << 20) && k >= 1 &&
-                    k <= MOE_SORT_MAX_K && T + R / 32 < INT32_MAX;
+                    k <= MOE_SORT_MAX_K && T + R / 32 < INT32_MAX - kZeroBlocks;
     return ok ? MRR_OK : MRR_ERR_SHAPE;
 }
 

@@ -86,6 +86,27 @@ def test_combine_many_tokens(k, H, dt):
     close(gw, ref_w, size, row_ops(H), "float32")
 
 
+@pytest.mark.parametrize("k", [2, 3, 4, 5, 8])
+@pytest.mark.parametrize("H", [2048, 1028, 2049, 1026])
+@pytest.mark.parametrize("dt", ["float16", "float32"])
+@pytest.mark.parametrize("T", [5, 640])
+def test_combine_of_tokens_with_few_rows(k, H, dt, T):
+    """Any number of a token's slots have rows; weights of the others are NaN, and rows of zeros fill the gradient."""
+    rng = np.random.default_rng(k * H + T)
+    rows, row, w = combine_case(rng, T, k, T * k, H, dt, "float32", wrong=0.0)
+    row = np.where(rng.random((T, k)) < rng.random((T, 1)), row, -1)
+    row[0], row[T // 2] = -1, np.arange(k)[::-1] % 3 - 1        # no row, and some rows more than once
+    w[ints(row, "int64") < 0] = float("nan")
+    ref, size = ox.combine(down(rows), row, down(w))
+    close(moe.moe_combine_tokens(rows, ints(row, "int32"), w), ref, size, k + 2, dt)
+    rows, row, w = combine_case(rng, T, k, T * k, H, dt, "float32", wrong=0.8)
+    gy = up(rng.standard_normal((T, H)), dt)
+    grows, gw = moe.moe_combine_tokens_grad(gy, rows, ints(row, "int32"), ints(ox_token(row, T * k), "int32"), w)
+    ref_rows, ref_w, size = ox.combine_grad(down(gy), down(rows), row, down(w))
+    close(grows, ref_rows, np.abs(ref_rows), 2, dt)
+    close(gw, ref_w, size, row_ops(H), "float32")
+
+
 @pytest.mark.parametrize("T", [303, 304, 607, 608, 609])
 def test_combine_where_forms_meet(T):
     """Fewer than 608 blocks share a token's columns, fewer than 304 tokens have more threads each."""
