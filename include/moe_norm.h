@@ -17,7 +17,7 @@
  *   MOE_Q_MXFP4     e2m1 codes [T, H/2] and e8m0 scales [T, ceil(H/64), 2], as moe_mx_quantize_run
  *                   makes them of y in float32
  * Float32 scales are held to 2^-126 from below.  An element is y / s rounded to nearest, ties to
- * even, magnitudes above the type's largest to that; y / s is y times the rounded 1 / s.  A row or
+ * even, magnitudes above the type's largest to that; y / s itself is rounded to float32.  A row or
  * block that holds a NaN or an infinity gets the scale NaN (e8m0: 255), its codes are unspecified;
  * where the last e8m0 pair has no second block its byte is written as 127 and never used.
  *

@@ -60,6 +60,13 @@ __device__ __forceinline__ float float_scale(uint32_t m, float top, float &inver
     return s;
 }
 
+// y / s, rounded once: y times the rounded reciprocal, and a step by what that leaves (two operations, 0.2 us of 154)
+__device__ __forceinline__ float over(float y, float s, float inverse)
+{
+    const float q = y * inverse;
+    return fmaf(fmaf(-q, s, y), inverse, q);
+}
+
 __device__ __forceinline__ uint32_t int8_of(float v) { return (uint32_t)min(127, max(-127, __float2int_rn(v))) & 0xffu; }
 
 // BYTES (4 or 8) bytes of codes, of which the row has n, in stores as wide as their place allows
@@ -123,7 +130,7 @@ __device__ __forceinline__ void quantize(const Params &p, int64_t row, int tid, 
             float v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[j] = y[i][j] * inverse;
+                v[j] = over(y[i][j], s, inverse);
             if (n <= 0)
                 continue;
             if (kind == MOE_Q_INT8)
@@ -141,11 +148,11 @@ __device__ __forceinline__ void quantize(const Params &p, int64_t row, int tid, 
         uint32_t m = largest(y[i]);
         m = max(m, __shfl_xor_sync(kFull, m, 1));
         m = max(m, __shfl_xor_sync(kFull, m, 2));
-        float inverse;
+        float inverse, s = 0.0f;
         if (kind == MOE_Q_E4M3_128) {
             m = max(m, __shfl_xor_sync(kFull, m, 4));
             m = max(m, __shfl_xor_sync(kFull, m, 8));
-            const float s = float_scale(m, 448.0f, inverse);
+            s = float_scale(m, 448.0f, inverse);
             if (c % 128 == 0 && n > 0)
                 static_cast<float *>(p.scales)[row * ((p.H + 127) / 128) + c / 128] = s;
         } else {
@@ -165,7 +172,7 @@ __device__ __forceinline__ void quantize(const Params &p, int64_t row, int tid, 
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            v[j] = y[i][j] * inverse;
+            v[j] = kind == MOE_Q_E4M3_128 ? over(y[i][j], s, inverse) : y[i][j] * inverse;   // (by a power of two: exact)
         if (kind == MOE_Q_MXFP4) {
             store_codes<4>(static_cast<uint8_t *>(p.q) + (row * p.H + c) / 2, n / 2, p.q_align, encode8(v), 0u);
         } else {

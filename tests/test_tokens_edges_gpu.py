@@ -173,6 +173,22 @@ def test_norm_of_long_rows(H, dt):
     close(gw, rw, sw, row_ops(H) + T / 64 + 60, "float32")
 
 
+@pytest.mark.parametrize("quant", ["int8", "e4m3", "e4m3_128"])
+@pytest.mark.parametrize("T,H", [(1, 7168), (64, 1000), (2000, 2048), (400, 513)])
+def test_codes_are_of_the_rounded_quotient(quant, T, H):
+    """y in float32 is what the codes are made of: each is that of y / s in float32, to the bit."""
+    rng = np.random.default_rng(T + H)
+    x, w = up(rng.standard_normal((T, H)), "float32"), up(1 + 0.2 * rng.standard_normal(H), "float32")
+    y, _, q, s = moe.moe_add_rms_norm(x, w, quant=quant)
+    y, s = down(y).astype(np.float32), down(s).astype(np.float32).reshape(T, -1)
+    block = 128 if quant == "e4m3_128" else H
+    top = np.maximum.reduceat(np.abs(y), np.arange(0, H, block), axis=1)
+    assert np.array_equal(s, top / np.float32(127 if quant == "int8" else 448))
+    v = y / np.repeat(s, block, axis=1)[:, :H]
+    want = np.clip(np.rint(v), -127, 127) if quant == "int8" else ox.nearest(v.astype(np.float64), ox.E4M3)
+    assert np.array_equal(down(q.float()), want)
+
+
 @pytest.mark.parametrize("H", [7168, 7176, 9218, 12288, 12292, 14336, 14344, 20480, 20482, 20488])
 @pytest.mark.parametrize("dt", ["bfloat16", "float32"])
 def test_norm_grad_of_long_rows(H, dt):
