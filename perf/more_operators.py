@@ -316,7 +316,7 @@ def run(state):
         rows, scales, slot, row, num, weight = moe.moe_sort_tokens(
             s["x"], s["experts"], s["held"], first_expert=s["first"], per_token_scales=s["scales"],
             expert_topk_weight=s["weight"])
-        return {"rows": rows, "scales": scales, "slot": slot, "row": row, "num": num, "weight": weight.view(-1)}
+        return {"rows": rows, "scales": scales, "slot": slot, "row": row, "num": num, "weight": weight}
     if s["grad"]:
         drows, dw = moe.moe_combine_tokens_grad(s["dy"], s["rows"], s["row"], s["slot"], s["weight"])
         return {"rows": drows, "weight": dw}
