@@ -294,6 +294,10 @@ def run(state):
         if op == "sort" and not s["grad"]:
             return _plain_sort(s)
         return _plain_combine_grad(s) if op == "combine" and s["grad"] else _plain_combine(s)
+    elif op == "sort" and not s["grad"] and "as_called" not in s:
+        # the package gives the sorted weights as [T k, 1], as the grouped product takes them, the plain form as [T k]
+        out = run({**s, "as_called": True})
+        return {**out, "weight": out["weight"].view(-1)}
     import moe_expert_token_gb300 as moe
 
     if op == "gate_grad":
