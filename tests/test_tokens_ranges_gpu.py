@@ -1,0 +1,48 @@
+"""The operators around the experts at the far ends of what they are given."""
+import numpy as np
+import pytest
+
+import moe_expert_token_gb300 as moe
+import moe_expert_token_gb300.mrr_v2 as m
+from oracle import tokens as ox
+from test_experts_gpu import down, up
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    import torch
+
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from moe_expert_token_gb300 import build
+
+    build.build()
+    m.load_library()
+
+
+@pytest.mark.parametrize("quant", ["int8", "e4m3", "e4m3_128"])
+@pytest.mark.parametrize("exponent", [-126, -122, -119, -116, -112, -105, -98, -65, -56, 0, 100])
+def test_codes_of_quotients_at_ties(quant, exponent):
+    """Elements as near as float32 comes to the middle between two codes, under scales from 2^-126 up: each code is that of y / s
+    in float32, to the bit.  Rows below 2^-20 under an eps of 1 have r = 1, and weights of a power of two give any y."""
+    T, H = 200, 1024
+    rng = np.random.default_rng(exponent + 200)
+    block, top = (128 if quant == "e4m3_128" else H), np.float32(127 if quant == "int8" else 448)
+    values = np.arange(128.0) if quant == "int8" else ox.E4M3
+    largest = np.ldexp((1 + rng.integers(0, 2 ** 23, (T, H // block)) * 2.0 ** -23).astype(np.float32), exponent)
+    s = np.maximum(largest / top, np.float32(2.0 ** -126))
+    each, most = np.repeat(s, block, axis=1), np.repeat(largest, block, axis=1)
+    i = rng.integers(0, len(values) - 1, (T, H))
+    tie = ((values[i] + values[i + 1]) / 2 * each.astype(np.float64)).astype(np.float32)
+    y = np.minimum(tie, most) * rng.choice([-1, 1], (T, H)).astype(np.float32)
+    y[:, ::block] = largest
+    x = np.ldexp(y, -exponent - 20)
+    w = np.full(H, 2.0 ** (exponent + 20), np.float32)
+    got, _, q, scales = moe.moe_add_rms_norm(up(x, "float32"), up(w, "float32"), eps=1.0, quant=quant)
+    assert np.array_equal(down(got), y.astype(np.float64))
+    assert np.array_equal(down(scales).reshape(s.shape), s.astype(np.float64))
+    v = y / each
+    want = np.clip(np.rint(v), -127, 127) if quant == "int8" else ox.nearest(v.astype(np.float64), ox.E4M3)
+    assert np.array_equal(down(q.float()), want)
