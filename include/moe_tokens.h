@@ -52,8 +52,8 @@ size_t moe_sort_workspace(int64_t T, int64_t k, int64_t E);
  *                   its contents need not be initialised
  * Rows, scales and weights of zeros (all bytes 0) fill what is behind the last expert's rows.
  * Host errors: MRR_ERR_DTYPE, MRR_ERR_ATTR (expert_num_type), MRR_ERR_SHAPE (T < 0, k outside 1 ..
- * 64, E outside 1 .. 4096, T * k above 2^31 - 1, row_bytes outside 0 .. 2^24, row_stride < row_bytes,
- * scale_row_bytes outside 1 .. 2^20 with scales), MRR_ERR_NULL, MRR_ERR_ALIGN (expert_idx, weight or
+ * 64, E outside 1 .. 4096, first_expert + E - 1 above 2^63 - 1, T * k above 2^31 - 1, row_bytes outside
+ * 0 .. 2^24, row_stride < row_bytes, scale_row_bytes outside 1 .. 2^20 with scales), MRR_ERR_NULL, MRR_ERR_ALIGN (expert_idx, weight or
  * a written index not aligned to its type), MRR_ERR_WORKSPACE, MRR_ERR_CUDA.
  */
 mrr_status moe_sort_run(const void *expert_idx, int idx_is_i64, int64_t T, int64_t k, int64_t first_expert, int64_t E,

@@ -847,7 +847,8 @@ mrr_status moe_sort_run(const void *expert_idx, int idx_is_i64, int64_t T, int64
         return MRR_ERR_DTYPE;
     if (expert_num_type != 0 && expert_num_type != 1)
         return MRR_ERR_ATTR;
-    if (!sizes_ok(T, k, E) || row_bytes < 0 || row_bytes > (1 << 24) || row_stride < row_bytes ||
+    // (first_expert + E - 1 past int64: a key's subtraction would wrap)
+    if (!sizes_ok(T, k, E) || first_expert > INT64_MAX - (E - 1) || row_bytes < 0 || row_bytes > (1 << 24) || row_stride < row_bytes ||
         (scales && (scale_row_bytes < 1 || scale_row_bytes > (1 << 20))))
         return MRR_ERR_SHAPE;
     if (!expert_num || (T > 0 && (!expert_idx || !token_idx || !row_idx || (row_bytes > 0 && (!x || !sorted_x)) ||

@@ -115,3 +115,15 @@ def test_a_stream_of_another_device_is_refused():
                     (moe.moe_add_rms_norm, 2), (moe.moe_add_rms_norm_grad, 3), (moe.moe_dequantize_rows, 2), (moe.moe_gating_top_k_grad, 3)):
         with pytest.raises(ValueError, match="stream"):
             call(*(x,) * n, stream=stream)
+
+
+def test_sort_rejects_experts_past_the_integers():
+    """first_expert + E - 1 has to be an int64: past it the subtraction that makes a slot's key would wrap, and -2^63 count as
+    an expert held here.  (No workspace: what the range allows goes no further.)"""
+    base = dict(expert_idx=A, idx_is_i64=1, T=1000, k=8, first_expert=0, E=16, x=B, row_bytes=256, row_stride=256, scales=None,
+                scale_row_bytes=0, weight=None, weight_dt=F32, sorted_x=E, sorted_scales=None, sorted_weight=None, token_idx=A, row_idx=B,
+                expert_num=C, expert_num_type=1, workspace=None, workspace_bytes=0, stream=None)
+    check(moe.moe_sort_run, base, [
+        (dict(first_expert=2 ** 63 - 15), m.MRR_ERR_SHAPE), (dict(first_expert=2 ** 63 - 1), m.MRR_ERR_SHAPE),
+        (dict(first_expert=2 ** 63 - 4095, E=4096), m.MRR_ERR_SHAPE), (dict(first_expert=2 ** 63 - 16), m.MRR_ERR_WORKSPACE),
+        (dict(first_expert=2 ** 63 - 1, E=1), m.MRR_ERR_WORKSPACE), (dict(first_expert=-2 ** 63), m.MRR_ERR_WORKSPACE)])
