@@ -30,6 +30,23 @@ def weights(E, H, I, generator):
     return w
 
 
+def delivered(codes, scales, expert, weight, E, ranks):
+    """What an exchange delivers: rank by rank, each rank's rows in expert order, with the row of each of their slots."""
+    T, k = expert.shape
+    rank = (torch.arange(T, device=codes.device) * ranks // T).int()
+    at_once, parts, ahead = 4096 // E, [], 0     # the experts of one sort are 4096 or fewer: a few ranks' at a time
+    for r in range(0, ranks, at_once):
+        n = min(at_once, ranks - r)
+        to = -(-(r + n) * T // ranks)            # the first token of rank r + n
+        t = slice(ahead, to)
+        rows, row_scales, _, row_idx, counts, row_weight = moe.moe_sort_tokens(
+            codes[t], expert[t] + E * (rank[t] - r)[:, None], n * E, per_token_scales=scales[t],
+            expert_topk_weight=weight[t])
+        parts.append((rows, row_scales, row_idx + k * ahead if ahead else row_idx, counts.view(n, E), row_weight))
+        ahead = to
+    return parts[0] if len(parts) == 1 else [torch.cat(p) for p in zip(*parts)]
+
+
 def prefill(x, w, k, ranks, quantised=None):
     """The block on x [T, H] bfloat16, as if `ranks` source ranks had each sent a share of the tokens.
     `quantised`: x's MXFP4 rows and scales, where the norm in front has made them already.
@@ -38,12 +55,8 @@ def prefill(x, w, k, ranks, quantised=None):
     E = w["router"].shape[0]
     weight, expert, _ = moe.moe_gating_top_k(x @ w["router"].t(), k, bias=w["bias"], **ROUTING)
 
-    # what an exchange delivers: rank by rank, each rank's rows in expert order
-    rank = (torch.arange(T, device=x.device) * ranks // T).int()
     codes, scales = moe.moe_mx_quantize(x) if quantised is None else quantised
-    rows, row_scales, _, row_idx, counts, row_weight = moe.moe_sort_tokens(
-        codes, expert + E * rank[:, None], ranks * E, per_token_scales=scales, expert_topk_weight=weight)
-    counts = counts.view(ranks, E)
+    rows, row_scales, row_idx, counts, row_weight = delivered(codes, scales, expert, weight, E, ranks)
 
     # expert-major, through the experts, and back
     rows, row_scales, _, num, row_weight = moe.moe_re_routing(

@@ -6,6 +6,7 @@ import moe_expert_token_gb300 as moe
 import moe_expert_token_gb300.mrr_v2 as m
 from oracle import tokens as ox
 from test_experts_gpu import down, up
+from test_tokens_together_gpu import example
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +47,20 @@ def test_codes_of_quotients_at_ties(quant, exponent):
     v = y / each
     want = np.clip(np.rint(v), -127, 127) if quant == "int8" else ox.nearest(v.astype(np.float64), ox.E4M3)
     assert np.array_equal(down(q.float()), want)
+
+
+def test_block_of_many_ranks():
+    """More (rank, expert) pairs than one sort takes (4096): the block's result is the one that few ranks give.  A row's products
+    do not depend on where it lies, so the results are equal to the bit.  Token t chooses experts k t .. k t + k - 1 (mod E), which
+    its logits say by themselves, so every pair has rows."""
+    import torch
+
+    block = example("moe_block")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    T, E, I, k = 16384, 128, 64, 8
+    w = block.weights(E, E, I, gen) | {"router": torch.eye(E, device="cuda").bfloat16(), "bias": torch.zeros(E, device="cuda").bfloat16()}
+    expert = (k * torch.arange(T, device="cuda")[:, None] + torch.arange(k, device="cuda")) % E
+    x = (0.125 * torch.randn(T, E, generator=gen, device="cuda")).scatter_add_(1, expert, torch.full((T, k), 6.0, device="cuda")).bfloat16()
+    few = block.prefill(x, w, k, ranks=2)
+    for ranks in (32, 33, 40):                  # 4096 pairs, and more of them in shares of equal and of different sizes
+        assert torch.equal(block.prefill(x, w, k, ranks=ranks), few)
