@@ -37,19 +37,23 @@ class AddRmsNorm(torch.autograd.Function):
 
 
 class GatingTopK(torch.autograd.Function):
+    """``routing``: moe_gating_top_k's other arguments, a mask among them; the biases, which have gradients, come by themselves."""
+
     @staticmethod
-    def forward(ctx, logits, k, routing):
-        weight, expert, _ = moe.moe_gating_top_k(logits, k, **routing)
-        ctx.save_for_backward(logits, expert)
-        ctx.kw = {n: routing[n] for n in ("routed_scaling_factor", "eps", "norm_type") if n in routing}
+    def forward(ctx, logits, k, routing, bias=None, additional_bias=None):
+        weight, expert, _ = moe.moe_gating_top_k(logits, k, bias=bias, additional_bias=additional_bias, **routing)
+        ctx.save_for_backward(logits, expert, bias, additional_bias)
+        ctx.kw = {n: routing[n] for n in ("additional_token_mask", "routed_scaling_factor", "eps", "norm_type") if n in routing}
         ctx.mark_non_differentiable(expert)
         return weight, expert
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_weight, _):
-        logits, expert = ctx.saved_tensors
-        return moe.moe_gating_top_k_grad(grad_weight.contiguous(), logits, expert, **ctx.kw)[0], None, None
+        logits, expert, bias, additional_bias = ctx.saved_tensors
+        grad, grad_bias, grad_additional = moe.moe_gating_top_k_grad(grad_weight.contiguous(), logits, expert, bias=bias,
+                                                                     additional_bias=additional_bias, **ctx.kw)
+        return grad, None, None, grad_bias, grad_additional
 
 
 class SortTokens(torch.autograd.Function):

@@ -64,3 +64,33 @@ def test_block_of_many_ranks():
     few = block.prefill(x, w, k, ranks=2)
     for ranks in (32, 33, 40):                  # 4096 pairs, and more of them in shares of equal and of different sizes
         assert torch.equal(block.prefill(x, w, k, ranks=ranks), few)
+
+
+@pytest.mark.parametrize("dt", ["float32", "bfloat16"])
+@pytest.mark.parametrize("norm_type", [0, 1, 2])
+def test_training_example_routes_with_biases(dt, norm_type):
+    """GatingTopK with a bias, and with a second one for the rows of a mask: the gradients that float64 gives the same weights,
+    within the kernel's bound for them (as tests/test_tokens_gpu.py holds it)."""
+    import torch
+
+    from test_tokens_gpu import close
+
+    block = example("moe_training")
+    T, e, k = 50, 24, 4
+    rng = np.random.default_rng(norm_type)
+    logits, bias, extra = up(2 * rng.standard_normal((T, e)), dt), up(0.3 * rng.random(e), dt), up(0.5 * rng.random(e), dt)
+    gy, mask = up(rng.standard_normal((T, k)), dt), up(rng.random(T) < 0.5)
+    routing = dict(norm_type=norm_type, routed_scaling_factor=2.5)
+    for second in (None, extra):
+        leaves = [t.clone().requires_grad_() for t in (logits, bias) + (() if second is None else (second,))]
+        more = {} if second is None else {"additional_token_mask": mask}
+        weight, expert = block.GatingTopK.apply(leaves[0], k, routing | more, *leaves[1:])
+        weight.backward(gy)
+        ref = ox.gating_grad(down(gy), down(logits), expert.cpu().numpy(), bias=down(bias), scale=2.5, norm_type=norm_type,
+                             additional_bias=None if second is None else down(second),
+                             mask=None if second is None else mask.cpu().numpy())
+        ops = 3 * (e / 32 + k / 32) + 120
+        for leaf, i in zip(leaves, (0, 2, 4)):
+            close(leaf.grad, ref[i], ref[i + 1], ops + (T / 64 + 60 if i else 0), dt)
+    with pytest.raises(TypeError):              # a bias among the plain settings would get no gradient
+        block.GatingTopK.apply(logits, k, routing | {"bias": bias}, bias)
