@@ -67,7 +67,8 @@ mrr_status moe_sort_run(const void *expert_idx, int idx_is_i64, int64_t T, int64
  * moe_combine_run -- y[t] = sum over j of weight[t, j] * rows[row_idx[t, j]], float32 sums in the
  *   order of j, rounded once; without weights each counts once (the gradient of moe_sort_run: rows
  *   then are the gradient of sorted_x).  A slot whose row_idx is outside 0 .. R - 1 adds nothing,
- *   and its weight is not used; a token without any row is zero.
+ *   and its weight is not used; a token without any row is zero.  (T k tokens of one slot each, rows of one element: the
+ *   gradient of moe_sort_run's weights, rows then being the gradient of sorted_weight.)
  *   rows [R, H] in dt (read), row_idx [T, k] int32 (read), weight [T, k] in weight_dt or NULL (read),
  *   y [T, H] in dt (written).
  * Host errors: MRR_ERR_DTYPE, MRR_ERR_SHAPE (T, R < 0 or above 2^31 - 1, H outside 1 .. 2^20, k

@@ -224,7 +224,11 @@ def moe_combine_tokens(rows, row_idx, weight=None, *, stream=None):
 
 
 def moe_sort_tokens_grad(grad_sorted_x, row_idx, *, stream=None):
-    """The gradient of moe_sort_tokens with respect to x [T, H]: each token's rows of grad_sorted_x [T k, H], summed."""
+    """The gradient of moe_sort_tokens with respect to x [T, H]: each token's rows of grad_sorted_x [T k, H], summed.
+
+    That of the weights it moves, [T, k] from grad_sorted_weight [T k, 1], is a combine with one slot a token:
+    ``moe_combine_tokens(grad_sorted_weight, row_idx.view(-1, 1)).view(row_idx.shape)``, 0 for slots without a row.
+    """
     return moe_combine_tokens(grad_sorted_x, row_idx, stream=stream)
 
 

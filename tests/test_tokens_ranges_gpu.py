@@ -94,3 +94,18 @@ def test_training_example_routes_with_biases(dt, norm_type):
             close(leaf.grad, ref[i], ref[i + 1], ops + (T / 64 + 60 if i else 0), dt)
     with pytest.raises(TypeError):              # a bias among the plain settings would get no gradient
         block.GatingTopK.apply(logits, k, routing | {"bias": bias}, bias)
+
+
+@pytest.mark.parametrize("T,k,held", [(1, 8, 16), (300, 3, 16), (300, 3, 5), (9000, 8, 2)])
+def test_gradient_of_the_sorted_weights(T, k, held):
+    """Each slot's weight has the gradient of its row's, and 0 without a row: a combine with one slot a token."""
+    import torch
+
+    rng = np.random.default_rng(T)
+    idx = torch.from_numpy(rng.integers(0, 16, (T, k))).int().cuda()
+    x, weight = torch.ones((T, 4), device="cuda"), torch.rand((T, k), device="cuda")
+    _, _, _, row_idx, _, moved = moe.moe_sort_tokens(x, idx, held, expert_topk_weight=weight)
+    grad = torch.randn(moved.shape, device="cuda")
+    got = moe.moe_combine_tokens(grad, row_idx.view(-1, 1)).view(T, k)
+    want = torch.where(row_idx >= 0, grad[row_idx.clamp(min=0).long(), 0], torch.zeros((), device="cuda"))
+    assert torch.equal(got, want)
