@@ -6,7 +6,9 @@
  *   h[t, c] = x[t, c] + residual[t, c]                              (float32)
  *   r[t]    = 1 / sqrt(sum_c h[t, c]^2 / H + eps)
  *   y[t, c] = h[t, c] r[t] weight[c]                                (float32 up to its one rounding)
- * y is made from h before h is rounded to be stored, the quantised rows from y before it is.
+ * y is made from h before h is rounded to be stored, the quantised rows from y before it is.  The sum is float32 too: of a row
+ * whose squares add up to more than that holds (elements of 2^64 / sqrt(H) or more) r is 0, of one whose squares are 0 in it under an
+ * eps of 0 r is infinite, in the gradient as well.
  *
  * Quantised rows, q with scales; m is the largest magnitude of y's row or block:
  *   MOE_Q_INT8      int8;  scales [T] float32           s = m / 127, q = y / s to nearest even

@@ -71,8 +71,8 @@ mrr_status moe_sort_run(const void *expert_idx, int idx_is_i64, int64_t T, int64
  *   gradient of moe_sort_run's weights, rows then being the gradient of sorted_weight.)
  *   rows [R, H] in dt (read), row_idx [T, k] int32 (read), weight [T, k] in weight_dt or NULL (read),
  *   y [T, H] in dt (written).
- * Host errors: MRR_ERR_DTYPE, MRR_ERR_SHAPE (T, R < 0 or above 2^31 - 1, H outside 1 .. 2^20, k
- * outside 1 .. 64), MRR_ERR_NULL, MRR_ERR_ALIGN, MRR_ERR_CUDA.
+ * Host errors: MRR_ERR_DTYPE, MRR_ERR_SHAPE (T, R < 0 or above 2^31 - 1, T + R / 32 above 2^31 - 2434, H outside
+ * 1 .. 2^20, k outside 1 .. 64), MRR_ERR_NULL, MRR_ERR_ALIGN, MRR_ERR_CUDA.
  */
 mrr_status moe_combine_run(const void *rows, moe_dtype dt, int64_t R, int64_t H, const int32_t *row_idx, int64_t T,
                            int64_t k, const void *weight, moe_dtype weight_dt, void *y, mrr_stream_t stream);

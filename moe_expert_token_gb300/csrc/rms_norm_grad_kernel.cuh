@@ -9,7 +9,8 @@
 // sums, which a second launch adds in order.  What a row waits for (its loads, the sum over the block) is hidden by
 // copies that run kStages rows ahead into shared memory: each warp copies, and later reads, its own chunks only,
 // so the copies need no barrier of the block.  Rows that do not fit twice (grad_h, which is read once, then stays out),
-// or that come in pieces of 2 bytes, are loaded directly.  Accesses to shared memory are what the kernel has least to
+// that come in pieces of 2 bytes, or that have more than 20480 elements are loaded directly; the last have 8 chunks a thread, whose
+// 64 sums are more than the 64 registers of 1024 threads hold beside the rest (2000 x 20484: 237 us, 2000 x 20480 92).  Accesses to shared memory are what the kernel has least to
 // spare of (with the weight read from there too, 71 % of L1's throughput and 65 us for 8191 x 4100 bfloat16), so the
 // weight is held in registers, and with one chunk a thread so are 16-bit rows, packed as they come.
 // 8191 x 4100: 54.6 us; 16384 x 7168: 146 us, 6.4 TB/s; 4000 x 12288 float32: 137 us.

@@ -16,7 +16,8 @@ using namespace moe_mx;
 
 namespace {
 
-constexpr int kThreads = 64;    // most threads of a block (at 16384 x 7168 bfloat16, k = 8: 256 threads 334 us, 128 316, 64 314, 32 329)
+// most threads of a block (16384 x 7168 bfloat16, k = 8, each with its better launch bound: 32 threads 334 us, 64 317, 128 320, 256 342)
+constexpr int kThreads = 64;
 using moe_rows::kFull;
 
 // W bytes of consecutive elements of DT, as they lie in memory
@@ -56,13 +57,6 @@ struct Piece {
             *reinterpret_cast<uint32_t *>(p) = w[0];
         else
             *reinterpret_cast<uint16_t *>(p) = (uint16_t)w[0];
-    }
-
-    __device__ __forceinline__ void zero()
-    {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i)
-            w[i] = 0u;
     }
 
     __device__ __forceinline__ void get(float (&v)[kEach]) const
@@ -214,7 +208,7 @@ __device__ __forceinline__ void combine_few(const Params &p, int64_t t, int lane
 }
 
 // R rows at once.  Where tokens are few, several blocks (the y index) share a token's columns.
-// (Of 8 rows in pieces of 16 bytes 11 blocks an SM: for 12 a register is spilled, 320 us for 315 at 16384 x 7168.)
+// (Of 8 rows in pieces of 16 bytes 11 blocks an SM: for 12 a register is spilled, 319 us for 317 at 16384 x 7168.)
 template <int DT, int W, int R>
 __global__ void __launch_bounds__(kThreads, W == 16 && R == 8 ? 11 : W > 2 ? 12 : 8) combine(Params p)
 {

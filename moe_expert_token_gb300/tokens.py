@@ -338,7 +338,8 @@ def moe_add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, quant=None,
 
 def moe_add_rms_norm_grad(grad_y, h, weight, *, grad_h=None, eps: float = 1e-6, workspace=None, stream=None):
     """The gradient of moe_add_rms_norm's y (and, with grad_h, of its h) with respect to x, which is the residual's too,
-    and to weight.  grad_y, h and grad_h [T, H] in one type, contiguous; h as moe_add_rms_norm returned it.
+    and to weight.  grad_y, h and grad_h [T, H] in one type, contiguous; h as moe_add_rms_norm returned it (without a residual
+    that is x itself: a contiguous copy of one with gaps between its rows).
     Returns (grad_x [T, H], grad_weight [H] in weight's type)."""
     lib = _lib or _load()
     if stream is not None:

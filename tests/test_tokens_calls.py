@@ -127,3 +127,9 @@ def test_sort_rejects_experts_past_the_integers():
         (dict(first_expert=2 ** 63 - 15), m.MRR_ERR_SHAPE), (dict(first_expert=2 ** 63 - 1), m.MRR_ERR_SHAPE),
         (dict(first_expert=2 ** 63 - 4095, E=4096), m.MRR_ERR_SHAPE), (dict(first_expert=2 ** 63 - 16), m.MRR_ERR_WORKSPACE),
         (dict(first_expert=2 ** 63 - 1, E=1), m.MRR_ERR_WORKSPACE), (dict(first_expert=-2 ** 63), m.MRR_ERR_WORKSPACE)])
+
+
+def test_sort_workspace_is_the_table():
+    """A row of E + 1 counts for each of 64 chunks and one word, in whole 256 bytes, whatever T and k."""
+    for T, k, E_ in ((513, 8, 1), (16384, 8, 256), (65, 64, 4096), (2 ** 31 - 1, 1, 4096), (2 ** 25, 63, 7)):
+        assert moe.moe_sort_workspace(T, k, E_) == -(-4 * (64 * (E_ + 1) + 1) // 256) * 256
